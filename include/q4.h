@@ -58,6 +58,7 @@ extern "C" {
  * q4_last_device_flags() the bits) */
 #define Q4_DEVERR_INDEX    0x1u  /* a topk_idx entry outside [0, E) was skipped  */
 #define Q4_DEVERR_TIMEOUT  0x2u  /* a bounded wait gave up; outputs are invalid  */
+#define Q4_DEVERR_VALUE    0x4u  /* a NaN or an infinity was given to the 8-bit cache */
 
 /* ---- element types ---- */
 #define Q4_F32   0   /* IEEE fp32                        */
@@ -490,6 +491,134 @@ Q4_API int q4_moe_block(float *out, const void *x, int x_dtype, const float *log
 
 Q4_API size_t q4_moe_block_workspace_size(int64_t T, int64_t topk, int64_t E, int64_t H,
                                    int64_t I, int64_t Is);
+
+/*
+ * ---- Serving: the operators between the projections -----------------------
+ *
+ * A paged key/value cache in 8 bits, attention over it, and sampling.  (The
+ * pages describe no such format; it is this library's own.)
+ *
+ * q4_kv_cache -- the cache's buffers, owned by the caller:
+ *   k, v               int8  [pages][heads][page_tokens][dim]  codes
+ *   k_scale, v_scale   fp32  [pages][heads][page_tokens / 16]  scales
+ * 16 consecutive tokens of one head (a block) share a scale; a cached value is
+ * code * scale.  page_tokens: a power of two from 16 to 256; dim: 64 or 128;
+ * heads <= 1024.  Buffers 16-byte aligned.  A new cache needs no
+ * initialisation: only blocks of appended tokens are read.
+ *
+ * The calls below take a batch of B sequences (B <= 4096), T <= 2^24 packed rows:
+ *   page_table  int32 [B][table_stride]: the page that holds tokens
+ *               i * page_tokens .. of a sequence.  A page outside [0, pages)
+ *               records Q4_DEVERR_INDEX; its tokens are not written, and not
+ *               seen.  Pages may be shared for reading; a page that is
+ *               appended to belongs to one sequence.
+ *   kv_len      int32 [B]: tokens each sequence has, new ones included
+ *   cu_q        int32 [B + 1], cu_q[0] = 0: sequence b's new tokens are rows
+ *               cu_q[b] .. cu_q[b + 1] - 1, at positions kv_len[b] - n .. kv_len[b] - 1.
+ *               Rows from cu_q[B] to T belong to no sequence: outputs there are zeros.
+ * Lengths and tables are read on the device, so that one captured CUDA graph
+ * serves growing sequences.
+ */
+#define Q4_KV_BLOCK 16
+typedef struct q4_kv_cache {
+  int8_t *k, *v;
+  float *k_scale, *v_scale;
+  int64_t pages, heads, dim, page_tokens;
+} q4_kv_cache;
+
+/* Position rotation by tables: element pairs (a, b) of a head's first `dim`
+ * elements become (a cos - b sin, b cos + a sin), with cos and sin of row
+ * `position`, column of the pair.  Q4_ROPE_HALVES pairs elements i and
+ * i + dim / 2; Q4_ROPE_PAIRS elements 2 i and 2 i + 1. */
+#define Q4_ROPE_HALVES 0
+#define Q4_ROPE_PAIRS  1
+typedef struct q4_rope {
+  const float *cos, *sin;   /* [rows][dim / 2], 16-byte aligned */
+  int64_t rows, dim;        /* dim: a multiple of 8, at most the head's */
+  int style;
+} q4_rope;
+
+/*
+ * q4_kv_append -- new tokens into the cache, queries rotated on the way.
+ *   q, k, v     rows of Hq, heads and heads heads of dim elements, `dtype`;
+ *               q_stride, k_stride, v_stride elements between rows (slices of
+ *               one projection's output), rows a multiple of 16 bytes apart.
+ *               q and q_out may both be NULL (Hq is then ignored).
+ *   q_out       [T][Hq][dim], q_out_dtype
+ *   q_norm, k_norm   fp32 [dim] or NULL: each head's RMS norm before the
+ *               rotation, x * (1 / sqrt(mean(x^2) + eps)) * weight
+ *   rope        or NULL (no rotation).  A position >= rope->rows records
+ *               Q4_DEVERR_INDEX; the token is not stored and its q_out is zero.
+ * A block whose new values have largest magnitude m takes the scale
+ * s = max(s0, m / 127), s0 that of its earlier tokens (0 without any; s is 0
+ * below 2^-110).  Earlier codes become rint(code * (s0 / s)), new ones
+ * rint(x * (1 / s)).  Each step is one fp32 operation, and the sum of squares
+ * adds neighbours first: the cache is the same bit for bit however the tokens
+ * of one call are spread over the GPU.  NaN is stored as 0 and an infinity as
+ * the largest finite number, with Q4_DEVERR_VALUE recorded.
+ */
+Q4_API int q4_kv_append(const q4_kv_cache *cache, void *q_out, int q_out_dtype, const void *q,
+                        int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                        int64_t v_stride, int dtype, int64_t Hq, const q4_rope *rope,
+                        const float *q_norm, const float *k_norm, float eps,
+                        const int32_t *page_table, int64_t table_stride, const int32_t *kv_len,
+                        const int32_t *cu_q, int64_t B, int64_t T, void *stream);
+
+/*
+ * q4_kv_gather -- cached keys and values as numbers: row cu[b] + i of k_out
+ * and v_out ([T][heads][dim], `dtype`) is token first[b] + i of sequence b.
+ */
+Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *cache,
+                        const int32_t *page_table, int64_t table_stride, const int32_t *first,
+                        const int32_t *cu, int64_t B, int64_t T, void *stream);
+
+/*
+ * q4_kv_attention -- out[t, h] = softmax_j(scale * q[t, h] . k_j) . v_j over
+ * the cached tokens j of the row's sequence.
+ *   q       rows of Hq heads (a multiple of cache->heads: query heads
+ *           h * Hq / heads .. share kv head h), q_dtype, q_stride elements apart
+ *   out     [T][Hq][dim], out_dtype
+ *   causal  1: a query at position p sees j <= p; 0: all kv_len tokens
+ *   window  0, or (causal) how many tokens a query sees, itself included
+ *   max_q   at least the most new tokens of a sequence
+ *   max_kv  at least the largest kv_len
+ * A query that sees nothing gets zeros.  Accuracy: the codes are exact in
+ * every product; with fp32 q and out the result is that of fp32 arithmetic,
+ * with bf16 the weights are rounded to fp16.
+ *   workspace  q4_kv_attention_workspace_size bytes, 16-byte aligned, the first 4 KB zero
+ *              before its first use; every completed call leaves them zero.
+ *              Calls that share it must not overlap.  NULL: scratch the
+ *              library owns per stream (allocated by an eager call; a call
+ *              captured into a graph needs a workspace: Q4_ERR_WORKSPACE).
+ */
+Q4_API int q4_kv_attention(void *out, int out_dtype, const void *q, int q_dtype, int64_t q_stride,
+                           int64_t Hq, const q4_kv_cache *cache, const int32_t *page_table,
+                           int64_t table_stride, const int32_t *kv_len, const int32_t *cu_q,
+                           int64_t B, int64_t T, int64_t max_q, int64_t max_kv, float scale,
+                           int causal, int64_t window, void *workspace, size_t workspace_bytes,
+                           void *stream);
+Q4_API size_t q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t Hq, int64_t B,
+                                             int64_t T, int64_t max_q, int64_t max_kv);
+
+/*
+ * q4_sample -- one token for each of T rows of V logits (V <= 327,672).
+ *   tokens       int32 [T]; -1 for a row whose logits are all -inf or NaN
+ *   probs        fp32 [T] or NULL: the token's probability among those kept
+ *   logits       rows of V, `stride` elements apart, logits_dtype (aligned to its elements)
+ *   u            fp32 [T] in [0, 1)
+ *   temperature, top_k, top_p, min_p   [T] or NULL (1, off, off, off)
+ * z = l * (1 / temperature); below 1e-5 the row is greedy (z = l, top_k = 1).
+ * A NaN counts as -inf.  Weights are w = floor(exp(z - max z) * 2^40).
+ * Ranked by z, equal z by index: the first top_k (<= 0: all), of those the
+ * shortest prefix whose weight reaches top_p of theirs (>= 1: all), of those
+ * the ones with exp(z - max z) >= min_p; the first of the ranking is always
+ * kept.  The token is the first index whose kept weight, summed in index
+ * order, exceeds floor(u * (all kept weight)).  Weights are whole numbers, so
+ * the token does not depend on the order of any sum.
+ */
+Q4_API int q4_sample(int32_t *tokens, float *probs, const void *logits, int logits_dtype,
+                     int64_t stride, int64_t T, int64_t V, const float *u, const float *temperature,
+                     const int32_t *top_k, const float *top_p, const float *min_p, void *stream);
 
 /*
  * q4_selftest_wait -- failure-detection self-test; no counterpart on the

@@ -27,11 +27,15 @@ Q4_ERR_SHAPE = -6
 Q4_ERR_DEVICE = -7
 Q4_DEVERR_INDEX = 0x1
 Q4_DEVERR_TIMEOUT = 0x2
+Q4_DEVERR_VALUE = 0x4
 Q4_F32 = 0
 Q4_BF16 = 1
 Q4_LAYOUT_BLOCKS = 0
 Q4_LAYOUT_PLANAR = 1
 Q4_LAYOUT_Q8_0 = 2
+Q4_KV_BLOCK = 16
+Q4_ROPE_HALVES = 0
+Q4_ROPE_PAIRS = 1
 
 _lock = threading.Lock()
 _lib = None
@@ -55,6 +59,19 @@ class GemvOp(ctypes.Structure):
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("a_dtype", ctypes.c_int), ("c_dtype", ctypes.c_int),
                 ("ndeps", ctypes.c_int), ("deps", ctypes.c_int * 4), ("slice_rows", ctypes.c_int)]
+
+
+class KvCacheStruct(ctypes.Structure):
+    """q4_kv_cache of include/q4.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("page_tokens", ctypes.c_int64)]
+
+
+class RopeStruct(ctypes.Structure):
+    """q4_rope of include/q4.h."""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("style", ctypes.c_int)]
 
 
 # name -> (restype, argtypes), as declared in include/q4.h
@@ -95,6 +112,13 @@ SIGNATURES = {
     "q4_gemv_seq_run": (_int, [_vp, _vp]),
     "q4_gemv_seq_destroy": (None, [_vp]),
     "q4_gemv_seq_grid": (_int, [_vp]),
+    "q4_kv_append": (_int, [_vp, _vp, _int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _i64, _vp,
+                            _vp, _vp, ctypes.c_float, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "q4_kv_gather": (_int, [_vp, _vp, _int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "q4_kv_attention": (_int, [_vp, _int, _vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                               _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _sz, _vp]),
+    "q4_kv_attention_workspace_size": (_sz, [_vp, _i64, _i64, _i64, _i64, _i64]),
+    "q4_sample": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "q4_get_device_status": (_int, [_vp]),
     "q4_last_device_flags": (ctypes.c_uint, []),
     "q4_status_str": (ctypes.c_char_p, [_int]),
@@ -354,6 +378,156 @@ def q4_moe_block(out, x, logits, W_gate, W_up, W_down, T: int, topk: int, E: int
 
 def q4_moe_block_workspace_size(T: int, topk: int, E: int, H: int, I: int, Is: int = 0) -> int:
     return lib().q4_moe_block_workspace_size(T, topk, E, H, I, Is)
+
+
+# ------------------------------------------------------------------ serving
+class KVCache:
+    """A paged 8-bit key/value cache over caller tensors (q4_kv_cache): k, v
+    int8 [pages, heads, page_tokens, dim], k_scale, v_scale fp32 [pages, heads,
+    page_tokens / 16].  KVCache.empty() allocates them.  The object keeps the
+    tensors alive."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        _require_cuda(k, v, k_scale, v_scale)
+        pages, heads, page, dim = k.shape
+        if k.dtype != torch.int8 or v.dtype != torch.int8 or v.shape != k.shape:
+            raise TypeError("k and v are int8 tensors of one shape")
+        want = (pages, heads, page // Q4_KV_BLOCK)
+        if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32
+                or k_scale.shape != want or v_scale.shape != want):
+            raise TypeError(f"k_scale and v_scale are fp32 tensors of shape {want}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), pages, heads, dim, page)
+        self.ref = ctypes.addressof(self.struct)
+        self.pages, self.heads, self.page_tokens, self.dim = pages, heads, page, dim
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, page_tokens: int = 64, device="cuda"):
+        import torch
+        codes = (pages, heads, page_tokens, dim)
+        scales = (pages, heads, page_tokens // Q4_KV_BLOCK)
+        return cls(*(torch.empty(codes, dtype=torch.int8, device=device) for _ in range(2)),
+                   *(torch.empty(scales, dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _rows(t, heads, dim):
+    """Data pointer and row stride of a [T, heads, dim] view whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1 or (
+            heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"expected a [T, {heads}, {dim}] tensor with dense rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _index(name, t, shape):
+    """Data pointer of a contiguous int32 CUDA tensor of the given shape (None: any size)."""
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} is a contiguous int32 CUDA tensor")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    return t.data_ptr()
+
+
+def _floats(name, t, n):
+    """Data pointer of a contiguous fp32 CUDA tensor of n elements, or None."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise TypeError(f"{name} is a contiguous fp32 CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+def q4_kv_append(cache: KVCache, q_out, q, k, v, page_table, kv_len, cu_q, cos=None, sin=None,
+                 rope_style: int = Q4_ROPE_HALVES, q_norm=None, k_norm=None, eps: float = 1e-6,
+                 stream=None) -> None:
+    """New tokens' keys and values into the cache, their queries rotated into
+    q_out (include/q4.h).  q [T, Hq, dim], k, v [T, heads, dim]: views whose
+    rows may be strided; q and q_out may both be None.  cos, sin: fp32
+    [positions, rotated dim / 2], or None."""
+    T, B = k.shape[0], kv_len.shape[0]
+    kp, ks = _rows(k, cache.heads, cache.dim)
+    vp, vs = _rows(v, cache.heads, cache.dim)
+    if v.shape[0] != T or v.dtype != k.dtype or (q is None) != (q_out is None):
+        raise ValueError("k and v have the same rows and type; q and q_out go together")
+    dtype = _dtype_code(k)
+    qp, qs, Hq, out, out_dtype = None, 0, 0, None, Q4_F32
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _rows(q, Hq, cache.dim)
+        _require_cuda(q_out)
+        if q.shape[0] != T or q.dtype != k.dtype or q_out.numel() != T * Hq * cache.dim:
+            raise ValueError("q has the rows and type of k, q_out its size")
+        out, out_dtype = q_out.data_ptr(), _dtype_code(q_out)
+    rope = None
+    if cos is not None:
+        if cos.dim() != 2 or sin is None or sin.shape != cos.shape:
+            raise ValueError("cos and sin are two tables of one shape [positions, rotated dim / 2]")
+        rope = RopeStruct(_floats("cos", cos, cos.numel()), _floats("sin", sin, cos.numel()),
+                          cos.shape[0], 2 * cos.shape[1], rope_style)
+    _check("q4_kv_append", lib().q4_kv_append(
+        cache.ref, out, out_dtype, qp, qs, kp, ks, vp, vs, dtype, Hq,
+        ctypes.byref(rope) if rope is not None else None,
+        _floats("q_norm", q_norm, cache.dim), _floats("k_norm", k_norm, cache.dim), eps,
+        _index("page_table", page_table, (B, None)), page_table.shape[1],
+        _index("kv_len", kv_len, (B,)), _index("cu_q", cu_q, (B + 1,)), B, T, _stream(stream)))
+
+
+def q4_kv_gather(k_out, v_out, cache: KVCache, page_table, first, cu, stream=None) -> None:
+    """Cached tokens first[b] .. of each sequence b as numbers into rows
+    cu[b] .. cu[b + 1] - 1 of k_out and v_out [T, heads, dim]."""
+    _require_cuda(k_out, v_out)
+    B, T = first.shape[0], k_out.shape[0]
+    if v_out.dtype != k_out.dtype or k_out.numel() != T * cache.heads * cache.dim or (
+            v_out.numel() != k_out.numel()):
+        raise ValueError("k_out and v_out are [T, heads, dim] tensors of one type")
+    _check("q4_kv_gather", lib().q4_kv_gather(
+        k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out), cache.ref,
+        _index("page_table", page_table, (B, None)), page_table.shape[1],
+        _index("first", first, (B,)), _index("cu", cu, (B + 1,)), B, T, _stream(stream)))
+
+
+def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int, max_kv: int,
+                    scale: float | None = None, causal: bool = True, window: int = 0,
+                    workspace=None, stream=None) -> None:
+    """Attention of the new tokens' queries q [T, Hq, dim] over the cached
+    tokens into out [T, Hq, dim] (include/q4.h).  scale: dim ** -0.5 by default."""
+    _require_cuda(out, workspace)
+    T, Hq, B = q.shape[0], q.shape[1], kv_len.shape[0]
+    qp, qs = _rows(q, Hq, cache.dim)
+    if out.numel() != T * Hq * cache.dim:
+        raise ValueError("out has the size of q")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("q4_kv_attention", lib().q4_kv_attention(
+        out.data_ptr(), _dtype_code(out), qp, _dtype_code(q), qs, Hq, cache.ref,
+        _index("page_table", page_table, (B, None)), page_table.shape[1],
+        _index("kv_len", kv_len, (B,)), _index("cu_q", cu_q, (B + 1,)), B, T, max_q, max_kv,
+        cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def q4_kv_attention_workspace_size(cache: KVCache, Hq: int, B: int, T: int, max_q: int,
+                                   max_kv: int) -> int:
+    return lib().q4_kv_attention_workspace_size(cache.ref, Hq, B, T, max_q, max_kv)
+
+
+def q4_sample(tokens, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,
+              stream=None) -> None:
+    """One token a row of logits [T, V] (fp32 or bf16, rows may be strided),
+    from the uniform numbers u [T]; settings are [T] tensors or None."""
+    if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits is a [T, V] CUDA tensor with dense rows")
+    T, V = logits.shape
+    _check("q4_sample", lib().q4_sample(
+        _index("tokens", tokens, (T,)), _floats("probs", probs, T), logits.data_ptr(),
+        _dtype_code(logits), logits.stride(0) if T > 1 else V, T, V, _floats("u", u, T),
+        _floats("temperature", temperature, T),
+        None if top_k is None else _index("top_k", top_k, (T,)), _floats("top_p", top_p, T),
+        _floats("min_p", min_p, T), _stream(stream)))
 
 
 def q4_moe_static_scratch_bytes() -> int:

@@ -13,6 +13,7 @@
 
 #include "q4.h"
 #include "q4_kernels.h"
+#include "q4_kv.h"
 
 namespace {
 
@@ -69,6 +70,9 @@ struct DeviceState {
   // while one was current may still use it, so it is kept until
   // q4_release_scratch()
   std::vector<void*> retired;
+  // per stream: scratch of the cache attention's eager calls without a
+  // workspace (zeroed when allocated)
+  std::map<unsigned long long, std::pair<void*, size_t>> kv_scratch;
   // the persistent sequence kernel's ring depth and resident CTAs per SM
   // (0 until first needed)
   int seq_stages = 0, seq_per_sm = 0;
@@ -182,6 +186,53 @@ int owned_workspace(DeviceState* s, size_t bytes, cudaStream_t st, void** ws) {
   *ws = s->ws;
   return Q4_OK;
 }
+
+}  // namespace
+
+namespace q4 {
+
+int device_info(int* sms, unsigned** status) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  const int rc = current_state(&s);
+  if (rc != Q4_OK) return rc;
+  *sms = s->sms;
+  *status = s->status;
+  return Q4_OK;
+}
+
+void* kv_stream_scratch(cudaStream_t st, size_t bytes) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  unsigned long long id = 0;
+  if (capturing(st) || current_state(&s) != Q4_OK) return nullptr;
+  if (cudaStreamGetId(st, &id) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  auto& have = s->kv_scratch[id];
+  if (have.second >= bytes) return have.first;
+  const size_t want = bytes + bytes / 4;
+  void* p = nullptr;
+  if (cudaMalloc(&p, want) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  if (cudaMemsetAsync(p, 0, want, st) != cudaSuccess) {
+    cudaGetLastError();
+    cudaFree(p);
+    return nullptr;
+  }
+  // kernels enqueued earlier (or a call of another host thread about to
+  // enqueue one) may still use the smaller buffer
+  if (have.first) s->retired.push_back(have.first);
+  have = {p, want};
+  return p;
+}
+
+}  // namespace q4
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -1413,6 +1464,8 @@ int q4_release_scratch(void) {
     cudaFree(kv.second.tickets);
   }
   s->gemm_scratch.clear();
+  for (auto& kv : s->kv_scratch) cudaFree(kv.second.first);
+  s->kv_scratch.clear();
   for (void* p : s->retired) cudaFree(p);
   s->retired.clear();
   cudaFree(s->ws);

@@ -1,0 +1,686 @@
+// Attention over the paged 8-bit cache, split over the cached tokens
+// (sm_103a): the form for few new tokens a sequence.
+//
+//   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
+// over the cached tokens j that the query sees.  With few queries this reads
+// each code once and does 4 D flops for it and each query that shares it: HBM
+// bounds it, so the work is laid out by the codes.
+//
+// * The unit of work is a block: 16 tokens of one kv head, for one tile of
+//   query rows (the queries that share the head: token-major, up to 16 rows).
+//   The units of all sequences, heads and tiles form one line, which is cut
+//   into equal ranges, one per CTA, whatever the sequences' lengths.  A CTA
+//   whose range ends inside a (sequence, head, tile) writes its share of the
+//   sum (with the maximum and the weights' sum) to the workspace; the last of
+//   the CTAs that share it adds the shares in order.
+// * Inside a CTA each warp streams blocks of its own (every eighth) through
+//   its own ring of TMA stages, so that no warp waits for another until the
+//   shares of the warps are added.
+// * Codes are integers up to 127, exact in fp16, as are bf16 queries scaled
+//   by a power of two per row; fp32 queries and the softmax weights are split
+//   into two fp16 terms (22 bits) that fill the two halves of the MMA's 16
+//   rows (SPLIT: 8 rows of queries), so fp32 calls keep fp32 accuracy at the
+//   same cost.  Products accumulate in fp32.
+// * A block's scale is one number per MMA tile: the key scale multiplies the
+//   scores, the value scale the weights, relative to the largest so far.
+#include <cfloat>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "q4_kernels.h"
+#include "q4_kv_device.cuh"
+
+namespace q4 {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;                 // rows of an MMA tile
+constexpr int kStages = 4;                // ring stages of a warp, one block each
+// Weight of the softmax reference (the largest score so far) with the value scale the sums are relative to;
+// a larger value scale counts up to kMoreScale of it before the reference moves.  As large as fp16 allows
+// (2^13 * 4 < 65504).  fp16 holds a weight to 11 bits down to 2^-27 of the reference and to within 2^-38 of
+// it below that.  With SPLIT the second term is the rest times kRestScale, so that the two hold 22 bits, and
+// within 2^-49: small weights can matter together, where the largest weight's value is near zero.
+constexpr float kUnitWeight = 8192.0f;
+constexpr float kMoreScale = 4.0f;
+constexpr float kRestScale = 2048.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnParams {
+  CUtensorMap kmap, vmap;                 // codes: u8 [pages][heads * page][dim], boxes of 16 rows
+  KvAttnCall a;
+  int group;                              // query heads of one kv head
+  int tiles;                              // row tiles a sequence may have (of max_q * group rows)
+  unsigned* tickets;                      // [grid], zero
+  float* part;                            // [grid][2][kRows][dim + 2] shares
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four codes to two pairs of fp16: u = code + 128 as the low byte of 1024 + u, minus 1152, exact.
+__device__ __forceinline__ uint32_t sub1152(uint32_t x) {
+  uint32_t y;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xE480E480u));
+  return y;
+}
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = sub1152(__byte_perm(u, 0x64646464u, 0x4140));
+  hi = sub1152(__byte_perm(u, 0x64646464u, 0x4342));
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// `scale` times the rest of (lo, hi) that its fp16 rounding `w` leaves, as fp16.
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t w, float scale) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_f16((lo - f.x) * scale, (hi - f.y) * scale);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// 4-byte asynchronous copy to shared memory, counted by the barrier's thread arrivals.
+__device__ __forceinline__ void copy4_async(void* dst, const void* src, uint64_t* bar) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// One (sequence, row tile, kv head) of the line of units, and the blocks a CTA takes of it.
+struct Segment {
+  int b, h, tile;
+  int c0, nq, len;         // packed row of the first new token, new tokens, cached tokens
+  int blk0;                // first block any query of the sequence sees
+  int lo, hi;              // this CTA's blocks (absolute)
+  long long first, last;   // units of the whole (sequence, tile, head): [first, last)
+};
+
+template <int D>
+struct Stage {
+  static constexpr int kCodes = kKvBlock * D;           // bytes of keys (values)
+  static constexpr int kBytes = 2 * kCodes;
+};
+
+template <int D>
+constexpr size_t smem_bytes(int B) {
+  return 1024 + static_cast<size_t>(kWarps) * kStages * Stage<D>::kBytes +   // rings
+         static_cast<size_t>(kWarps) * kRows * D * 4 +                        // the warps' sums
+         static_cast<size_t>(kWarps) * kRows * 2 * 4 + kRows * 2 * 4 +        // their maxima and weights
+         static_cast<size_t>(kWarps) * kStages * (8 + 8) +                    // scales, barriers
+         static_cast<size_t>(B + 1) * 8 + 64;
+}
+
+// Range of blocks [lo, hi) the queries of a sequence may see, at least one block where there are queries.
+__device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len, int& lo, int& hi) {
+  hi = max(1, (len + kKvBlock - 1) / kKvBlock);
+  lo = 0;
+  if (a.window > 0) {
+    const long long first = a.causal ? static_cast<long long>(len) - nq - a.window + 1 : 0;
+    lo = first > 0 ? min(static_cast<int>(first / kKvBlock), hi - 1) : 0;
+  }
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kTileRows = SPLIT ? 8 : 16;     // query rows of a tile
+  constexpr int KT = D / 16;                    // k steps of q . k
+  constexpr int NT = D / 8;                     // column tiles of p . v
+  constexpr int kStageBytes = Stage<D>::kBytes;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* s_o = reinterpret_cast<float*>(ring + kWarps * kStages * kStageBytes);   // [warp][row][D]
+  float* s_m = s_o + kWarps * kRows * D;                                           // [warp][row]
+  float* s_l = s_m + kWarps * kRows;
+  float* s_tot = s_l + kWarps * kRows;                                             // [row]: maximum, weights' sum
+  float* s_scale = s_tot + 2 * kRows;                                              // [warp][stage][2]
+  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_scale + kWarps * kStages * 2);
+  long long* s_cum = reinterpret_cast<long long*>(s_bar + kWarps * kStages);       // [B + 1] first unit of each sequence
+  __shared__ int s_fail;
+  __shared__ int s_last;
+  __shared__ long long s_warp[kWarps];
+
+  const KvAttnCall& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, c = lane & 3;        // MMA row (and column group), thread in group
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp * kStages + i], 3);
+  if (tid == 0) s_fail = 0;
+  fence_barrier_init();
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- the line of units ----
+  const int B = a.b.B;
+  {
+    const int per = (B + kThreads - 1) / kThreads;
+    long long sum = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < B) {
+        const int nq = a.b.cu[b + 1] - a.b.cu[b];
+        int lo, hi;
+        seq_blocks(a, nq, a.b.kv_len[b], lo, hi);
+        const long long tiles = nq > 0 ? (static_cast<long long>(nq) * p.group + kTileRows - 1) / kTileRows : 0;
+        const long long n = tiles * a.c.heads * (hi - lo);
+        s_cum[b + 1] = sum + n;
+        sum += n;
+      }
+    }
+    long long up = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += x;
+    }
+    if (lane == 31) s_warp[warp] = up;
+    __syncthreads();
+    long long before = up - sum;
+    for (int i = 0; i < warp; ++i) before += s_warp[i];
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < B) s_cum[b + 1] += before;
+    }
+    if (tid == 0) s_cum[0] = 0;
+    __syncthreads();
+  }
+  const long long units = s_cum[B];
+  // a CTA for each eight units (one for each warp), as far as there are CTAs
+  const long long ctas = max(1LL, min(static_cast<long long>(gridDim.x), (units + kWarps - 1) / kWarps));
+  auto range_of = [&](long long cta) { return units * cta / ctas; };
+  // the CTA whose range holds unit u
+  auto owner_of = [&](long long u) { return ((u + 1) * ctas - 1) / units; };
+  const long long u0 = blockIdx.x < ctas ? range_of(blockIdx.x) : units;
+  const long long u1 = blockIdx.x < ctas ? range_of(blockIdx.x + 1) : units;
+
+  auto locate = [&](long long u, Segment& s) {
+    int lo = 0, hi = B - 1;                     // the last b with s_cum[b] <= u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_cum[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    s.b = lo;
+    s.c0 = a.b.cu[lo];
+    s.nq = a.b.cu[lo + 1] - s.c0;
+    s.len = a.b.kv_len[lo];
+    int b0, b1;
+    seq_blocks(a, s.nq, s.len, b0, b1);
+    const int nb = b1 - b0;
+    const long long in = u - s_cum[lo], pair = in / nb;
+    s.blk0 = b0;
+    s.h = static_cast<int>(pair % a.c.heads);
+    s.tile = static_cast<int>(pair / a.c.heads);
+    s.first = s_cum[lo] + pair * nb;
+    s.last = s.first + nb;
+    s.lo = b0 + static_cast<int>(u - s.first);
+    s.hi = b0 + static_cast<int>(min(s.last, u1) - s.first);
+  };
+
+  // ---- the warp's stream of blocks: the producer runs kStages blocks ahead ----
+  uint8_t* my_ring = ring + warp * kStages * kStageBytes;
+  float* my_scale = s_scale + warp * kStages * 2;
+  uint64_t* my_bar = s_bar + warp * kStages;
+  Segment ps = {};                              // the producer's segment
+  long long pu = u0;                            // its first unit
+  int pblk = 0, ppage = -1;                     // its next block, that block's page
+  bool more = u0 < u1;
+  auto page_of = [&](int b, int blk) -> int {
+    const long long pi = static_cast<long long>(blk) * kKvBlock / a.c.page;
+    return pi < a.b.table_stride ? __ldg(a.b.table + b * a.b.table_stride + pi) : -1;
+  };
+  // to the warp's next block at or after pblk, through the segments
+  auto settle = [&]() {
+    while (more && pblk >= ps.hi) {
+      pu = min(ps.last, u1);
+      more = pu < u1;
+      if (more) {
+        locate(pu, ps);
+        pblk = ps.lo + warp;
+      }
+    }
+    if (more) ppage = page_of(ps.b, pblk);
+  };
+  if (more) {
+    locate(pu, ps);
+    pblk = ps.lo + warp;
+    settle();
+  }
+  unsigned issued = 0;
+  auto produce = [&]() {
+    if (!more) return;
+    const int st = issued % kStages;
+    uint64_t* bar = my_bar + st;
+    float* sc = my_scale + 2 * st;
+    const bool ok = ppage >= 0 && ppage < a.c.pages && pblk * kKvBlock < ps.len;
+    if (ok) {
+      const int off = (pblk * kKvBlock) & (a.c.page - 1);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, kStageBytes);
+        uint8_t* dst = my_ring + st * kStageBytes;
+        tma_load_3d(dst, &p.kmap, 0, ps.h * a.c.page + off, ppage, bar);
+        tma_load_3d(dst + Stage<D>::kCodes, &p.vmap, 0, ps.h * a.c.page + off, ppage, bar);
+      }
+      if (lane < 2) {
+        const long long at = ((static_cast<long long>(ppage) * a.c.heads + ps.h) * a.c.page + off) / kKvBlock;
+        copy4_async(sc + lane, (lane ? a.c.vs : a.c.ks) + at, bar);
+      }
+    } else {                                    // no such page, or a sequence without tokens: a block nobody sees
+      if (lane == 0) {
+        if (pblk * kKvBlock < ps.len) atomicOr(a.err, kDevErrIndex);
+        sc[0] = -1.0f;
+        sc[1] = 0.0f;
+        mbar_arrive(bar);
+        mbar_arrive(bar);
+        mbar_arrive(bar);
+      }
+    }
+    ++issued;
+    pblk += kWarps;
+    settle();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kStages; ++i) produce();
+
+  // ---- segments ----
+  unsigned taken = 0;
+  long long u = u0;
+  while (u < u1) {
+    Segment s;
+    locate(u, s);
+    const int row0 = s.tile * kTileRows;        // first row of the tile: row = token * group + head in group
+    const int rows = min(kTileRows, s.nq * p.group - row0);
+    // this thread's two rows (SPLIT: one, whose rest fills the second)
+    int qpos[2];                                // their positions, -1: no row
+    long long qoff[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = SPLIT ? g : g + 8 * e;
+      const int j = (row0 + r) / p.group;
+      qpos[e] = r < rows ? s.len - s.nq + j : -1;
+      qoff[e] = (static_cast<long long>(s.c0) + j) * a.q_stride + (s.h * p.group + (row0 + r) % p.group) * D;
+      if (s.c0 < 0 || s.c0 + j >= a.b.T) qpos[e] = -1;
+    }
+    // queries as fp16, scaled by a power of two per row into fp16's range: the thread's
+    // elements of a row are (D / 4) c + 0 .. D / 4 - 1, four for each k step
+    uint32_t qf[KT][4];
+    float rowf[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (SPLIT && e == 1) { rowf[1] = rowf[0]; break; }
+      float x[D / 4];
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+      if (qpos[e] >= 0) {
+        if (a.q_bf16) {
+          const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + qoff[e] + c * (D / 4));
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint2 w = __ldg(q + i);
+            x[4 * i] = __uint_as_float(w.x << 16), x[4 * i + 1] = __uint_as_float(w.x & 0xffff0000u);
+            x[4 * i + 2] = __uint_as_float(w.y << 16), x[4 * i + 3] = __uint_as_float(w.y & 0xffff0000u);
+          }
+        } else {
+          const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qoff[e] + c * (D / 4));
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const float4 w = __ldg(q + i);
+            x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
+          }
+        }
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // 2^(13 - exponent of m), within fp32's normal numbers
+      const int up = m > 0.f ? max(-126, min(126, 13 + 127 - static_cast<int>(__float_as_uint(m) >> 23))) : 0;
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+      rowf[e] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale * kLog2e;
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x0 = x[4 * t + 2 * i] * f, x1 = x[4 * t + 2 * i + 1] * f;
+          qf[t][e + 2 * i] = pack_f16(x0, x1);
+          if (SPLIT) qf[t][1 + 2 * i] = pack_rest(x0, x1, qf[t][2 * i], 1.0f);
+        }
+    }
+    // range of positions each row sees: (from, to]
+    int from[2], to[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      to[e] = qpos[e] < 0 ? -1 : a.causal ? qpos[e] : s.len - 1;
+      const long long f = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
+      from[e] = f < -1 ? -1 : static_cast<int>(f);
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float mref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+    float vref = 0.f;                           // value scale the sums are relative to
+
+    for (int blk = s.lo + warp; blk < s.hi; blk += kWarps) {
+      const int st = taken % kStages;
+      bounded_wait(my_bar + st, (taken / kStages) & 1, &s_fail, a.err);
+      ++taken;
+      const float ks = my_scale[2 * st], vs = my_scale[2 * st + 1];
+      const uint32_t kb = smem_u32(my_ring + st * kStageBytes), vb = kb + Stage<D>::kCodes;
+      if (ks >= 0.f) {
+        // scores: tile j holds tokens 8 j .. 8 j + 7 of the block
+        float sc[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * j + g;
+          uint32_t w[D / 16];
+          if (D == 128) {
+            const uint4 x = lds128(kb + r * 128 + (((2 * c) ^ g) << 4)), y = lds128(kb + r * 128 + (((2 * c + 1) ^ g) << 4));
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            w[D / 16 - 4] = y.x, w[D / 16 - 3] = y.y, w[D / 16 - 2] = y.z, w[D / 16 - 1] = y.w;
+          } else {
+            const uint4 x = lds128(kb + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+          }
+          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+          for (int t = 0; t < KT; ++t) {
+            uint32_t b0, b1;
+            widen4(w[t], b0, b1);
+            mma(sc[j], qf[t], b0, b1);
+          }
+        }
+        // scaled scores of the thread's rows, four columns each
+        float x[2][4];
+#pragma unroll
+        for (int e = 0; e < (SPLIT ? 1 : 2); ++e)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float v = SPLIT ? sc[j][i] + sc[j][2 + i] : sc[j][2 * e + i];
+              const int pos = blk * kKvBlock + 8 * j + 2 * c + i;
+              x[e][2 * j + i] = pos > from[e] && pos <= to[e] ? v * (ks * rowf[e]) : -INFINITY;
+            }
+        // the references move rarely: by a row's scores, or by the value scale
+        float m[2];
+        bool move = vs > kMoreScale * vref;
+#pragma unroll
+        for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+          m[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
+          move |= m[e] > mref[e];               // also from -inf
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          const float vnew = fmaxf(vref, vs);
+          const float vf = vnew > 0.f ? vref / vnew : 1.f;
+          vref = vnew;
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+            m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
+            m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
+            m[e] = fmaxf(m[e], mref[e]);
+            const float k = m[e] > -INFINITY ? ex2(mref[e] - m[e]) : 1.f;
+            lsum[e] *= k;
+            f[e] = k * vf;
+            mref[e] = m[e];
+          }
+          if (SPLIT) f[1] = f[0];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
+        }
+        // weights, and weights times the value scale as fp16
+        const float vk = vref > 0.f ? kUnitWeight * (vs / vref) : 0.f;
+        uint32_t pf[4];
+#pragma unroll
+        for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+          const float ref = mref[e] > -INFINITY ? mref[e] : 0.f;
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = ex2(x[e][i] - ref);
+            lsum[e] += w[i];
+            w[i] *= vk;
+          }
+          pf[e] = pack_f16(w[0], w[1]);
+          pf[2 + e] = pack_f16(w[2], w[3]);
+          if (SPLIT) {
+            pf[1] = pack_rest(w[0], w[1], pf[0], kRestScale);
+            pf[3] = pack_rest(w[2], w[3], pf[2], kRestScale);
+          }
+        }
+        // values: the thread's tokens are 2c, 2c + 1, 2c + 8, 2c + 9, its elements (D / 8) g + 0 .. D / 8 - 1
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+          if (D == 128) {
+            const uint4 y = lds128(vb + r * 128 + ((g ^ (r & 7)) << 4));
+            v[i][0] = y.x, v[i][1] = y.y, v[i][D / 32 - 2] = y.z, v[i][D / 32 - 1] = y.w;
+          } else {
+            const uint2 y = lds64(vb + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+            v[i][0] = y.x, v[i][1] = y.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7362u : 0x5140u;
+            uint32_t a0, a1, b0, b1;              // pairs of tokens at elements 4 q + 2 half and + 1
+            widen4(__byte_perm(v[0][q], v[1][q], sel), a0, a1);
+            widen4(__byte_perm(v[2][q], v[3][q], sel), b0, b1);
+            mma(o[4 * q + 2 * half], pf, a0, b0);
+            mma(o[4 * q + 2 * half + 1], pf, a1, b1);
+          }
+      }
+      __syncwarp();
+      produce();
+    }
+
+    // ---- the warps' shares ----
+#pragma unroll
+    for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+      lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], 1);
+      lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], 2);
+      if (c == 0) {
+        s_m[warp * kRows + g + 8 * e] = mref[e];
+        s_l[warp * kRows + g + 8 * e] = lsum[e];
+      }
+    }
+    __syncthreads();
+    float top[2];
+#pragma unroll
+    for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+      top[e] = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top[e] = fmaxf(top[e], s_m[w * kRows + g + 8 * e]);
+      const float f = (mref[e] > -INFINITY ? ex2(mref[e] - top[e]) : 0.f) * (vref / kUnitWeight);
+      float* to_row = s_o + (warp * kRows + g + 8 * e) * D + c * (D / 4);
+      // element of accumulator column 2c (2c + 1) of tile i: (D / 4) c + i (+ D / 8)
+#pragma unroll
+      for (int i = 0; i < NT; i += 4)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float4 y;
+          if (SPLIT)
+            y = make_float4(fmaf(o[i][2 + k], 1.0f / kRestScale, o[i][k]) * f,
+                            fmaf(o[i + 1][2 + k], 1.0f / kRestScale, o[i + 1][k]) * f,
+                            fmaf(o[i + 2][2 + k], 1.0f / kRestScale, o[i + 2][k]) * f,
+                            fmaf(o[i + 3][2 + k], 1.0f / kRestScale, o[i + 3][k]) * f);
+          else
+            y = make_float4(o[i][2 * e + k] * f, o[i + 1][2 * e + k] * f, o[i + 2][2 * e + k] * f, o[i + 3][2 * e + k] * f);
+          *reinterpret_cast<float4*>(to_row + k * (D / 8) + i) = y;
+        }
+      if (warp == 0 && c == 0) {
+        float l = 0.f;
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = s_m[w * kRows + g + 8 * e];
+          l += s_l[w * kRows + g + 8 * e] * (mw > -INFINITY ? ex2(mw - top[e]) : 0.f);
+        }
+        s_tot[g + 8 * e] = top[e];
+        s_tot[kRows + g + 8 * e] = l;
+      }
+    }
+    __syncthreads();
+    const bool whole = s.first >= u0 && s.last <= u1;
+    // partial sums: slot 0 for a (sequence, head, tile) that began in an earlier CTA, 1 for one that begins here
+    float* slot = p.part + (static_cast<long long>(blockIdx.x) * 2 + (s.first >= u0 ? 1 : 0)) * kRows * (D + 2);
+    auto store = [&](int r, int d, float v) {
+      const int j = (row0 + r) / p.group;
+      if (s.c0 < 0 || s.c0 + j >= a.b.T) return;
+      const long long at = ((static_cast<long long>(s.c0) + j) * a.Hq + s.h * p.group + (row0 + r) % p.group) * D + d;
+      if (a.out_bf16)
+        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+      else
+        static_cast<float*>(a.out)[at] = v;
+    };
+    for (int i = tid; i < rows * D; i += kThreads) {
+      const int r = i / D, d = i % D;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += s_o[(w * kRows + r) * D + d];
+      if (whole) {
+        const float l = s_tot[kRows + r];
+        store(r, d, l > 0.f ? v / l : l == 0.f ? 0.f : l);   // no key: zeros; a NaN stays
+      } else {
+        slot[r * D + d] = v;
+      }
+    }
+    if (!whole) {
+      if (tid < 2 * kRows) slot[kRows * D + tid] = s_tot[tid];
+      __syncthreads();
+      const long long o0 = owner_of(s.first), o1 = owner_of(s.last - 1);
+      if (tid == 0) {
+        const unsigned old = atom_add_acq_rel_gpu(p.tickets + o0, 1u);
+        s_last = old == static_cast<unsigned>(o1 - o0);
+        if (s_last) p.tickets[o0] = 0;
+      }
+      __syncthreads();
+      if (s_last) {
+        const int shares = static_cast<int>(o1 - o0) + 1;
+        auto share = [&](int i) {
+          return p.part + ((o0 + i) * 2 + (i == 0 ? 1 : 0)) * kRows * (D + 2);
+        };
+        for (int i = tid; i < rows * D; i += kThreads) {
+          const int r = i / D, d = i % D;
+          float m = -INFINITY, l = 0.f, v = 0.f;
+          for (int k = 0; k < shares; ++k) m = fmaxf(m, __ldcg(share(k) + kRows * D + r));
+          for (int k = 0; k < shares; ++k) {
+            const float* q = share(k);
+            const float mk = __ldcg(q + kRows * D + r);
+            const float f = mk > -INFINITY ? ex2(mk - m) : 0.f;
+            l += f * __ldcg(q + kRows * D + kRows + r);
+            v += f * __ldcg(q + r * D + d);
+          }
+          store(r, d, l > 0.f ? v / l : l == 0.f ? 0.f : l);
+        }
+      }
+    }
+    __syncthreads();   // s_o and s_m are free for the next segment
+    u = min(s.last, u1);
+  }
+
+  // rows of no sequence: zeros
+  const long long end = max(0, min(a.b.T, a.b.cu[B]));
+  const long long row_elems = static_cast<long long>(a.Hq) * D;
+  for (long long i = end * row_elems + static_cast<long long>(blockIdx.x) * kThreads + tid; i < a.b.T * row_elems;
+       i += static_cast<long long>(gridDim.x) * kThreads) {
+    if (a.out_bf16)
+      static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(0.f);
+    else
+      static_cast<float*>(a.out)[i] = 0.f;
+  }
+}
+
+// cuTensorMapEncodeTiled from the driver (null if unavailable).
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      fn = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  return encode;
+}
+
+bool encode_codes(CUtensorMap* m, const int8_t* base, const KvView& c) {
+  const auto encode = encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.heads) * c.page,
+                              static_cast<cuuint64_t>(c.pages)};
+  const cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.dim), kKvBlock, 1};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(base), dims, strides, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
+  const size_t smem = smem_bytes<D>(p.a.b.B);
+  cudaError_t e = cudaFuncSetAttribute(q4_kv_attn_split_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q4_kv_attn_split_kernel<D, SPLIT>, p);
+}
+
+}  // namespace
+
+size_t kv_attn_header_bytes() { return 4096; }   // a ticket per CTA
+
+size_t kv_attn_split_bytes(int dim, int sms) {
+  return kv_attn_header_bytes() + static_cast<size_t>(sms) * 2 * kRows * (dim + 2) * 4;
+}
+
+cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, void* ws, int sms, cudaStream_t st) {
+  AttnParams p = {};
+  if (!encode_codes(&p.kmap, a.c.k, a.c) || !encode_codes(&p.vmap, a.c.v, a.c)) return cudaErrorUnknown;
+  p.a = a;
+  p.group = a.Hq / a.c.heads;
+  p.tickets = static_cast<unsigned*>(ws);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
+  // one launch for each, a CTA per SM.  fp32 in or out needs both halves of the tile; bf16 takes them too
+  // while eight rows are enough
+  const bool split = !a.q_bf16 || !a.out_bf16 || static_cast<long long>(max_q) * p.group <= 8;
+  if (a.c.dim == 128) return split ? launch<128, true>(p, sms, st) : launch<128, false>(p, sms, st);
+  return split ? launch<64, true>(p, sms, st) : launch<64, false>(p, sms, st);
+}
+
+}  // namespace q4

@@ -1,0 +1,37 @@
+// Device helpers of the serving operators.
+#pragma once
+
+#include "q4_device.cuh"
+#include "q4_kv.h"
+
+namespace q4 {
+
+// The number of j in [1, n] with f(j) <= i, f non-decreasing: the whole warp
+// searches 32 probes at a time (one step up to n = 32, two up to 1024).
+template <typename F>
+__device__ __forceinline__ int warp_count_le(int n, int i, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int at = (lane + 1) * step;
+    const bool ok = at <= n && f(lo + at) <= i;
+    const int c = __popc(__ballot_sync(0xffffffffu, ok));
+    lo += c * step;
+    n = min(step - 1, n - c * step);
+  }
+  return lo;
+}
+
+// Row of codes (token `pos`, head h) in units of rows of `dim`, or -1 where
+// the page table has no valid page for it.
+__device__ __forceinline__ long long kv_row(const KvView& c, const int32_t* table,
+                                            long long table_stride, int b, int pos, int h) {
+  const int pi = pos / c.page;
+  if (pi >= table_stride) return -1;
+  const int pg = table[b * table_stride + pi];
+  if (pg < 0 || pg >= c.pages) return -1;
+  return (static_cast<long long>(pg) * c.heads + h) * c.page + (pos & (c.page - 1));
+}
+
+}  // namespace q4
