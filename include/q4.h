@@ -550,7 +550,7 @@ typedef struct q4_rope {
  *   rope        or NULL (no rotation).  A position >= rope->rows records
  *               Q4_DEVERR_INDEX; the token is not stored and its q_out is zero.
  * A block whose new values have largest magnitude m takes the scale
- * s = max(s0, m / 127), s0 that of its earlier tokens (0 without any; s is 0
+ * s = max(s0, m * (1 / 127)), s0 that of its earlier tokens (0 without any; s is 0
  * below 2^-110).  Earlier codes become rint(code * (s0 / s)), new ones
  * rint(x * (1 / s)).  Each step is one fp32 operation, and the sum of squares
  * adds neighbours first: the cache is the same bit for bit however the tokens
@@ -582,6 +582,11 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
  *   window  0, or (causal) how many tokens a query sees, itself included
  *   max_q   at least the most new tokens of a sequence
  *   max_kv  at least the largest kv_len
+ *   total_kv  0, or at least the sum of the kv_len: with bf16 q and out,
+ *           sequences with many new tokens are attended on the tensor cores,
+ *           from fp16 copies of their cached tokens in the workspace, which
+ *           is sized by B * max_kv, or by total_kv where that is less.  A batch
+ *           that holds more records Q4_DEVERR_INDEX and gets zeros.
  * A query that sees nothing gets zeros.  Accuracy: the codes are exact in
  * every product; with fp32 q and out the result is that of fp32 arithmetic,
  * with bf16 the weights are rounded to fp16.
@@ -594,11 +599,12 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
 Q4_API int q4_kv_attention(void *out, int out_dtype, const void *q, int q_dtype, int64_t q_stride,
                            int64_t Hq, const q4_kv_cache *cache, const int32_t *page_table,
                            int64_t table_stride, const int32_t *kv_len, const int32_t *cu_q,
-                           int64_t B, int64_t T, int64_t max_q, int64_t max_kv, float scale,
-                           int causal, int64_t window, void *workspace, size_t workspace_bytes,
-                           void *stream);
+                           int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
+                           int64_t total_kv, float scale, int causal, int64_t window,
+                           void *workspace, size_t workspace_bytes, void *stream);
 Q4_API size_t q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t Hq, int64_t B,
-                                             int64_t T, int64_t max_q, int64_t max_kv);
+                                             int64_t T, int64_t max_q, int64_t max_kv,
+                                             int64_t total_kv);
 
 /*
  * q4_sample -- one token for each of T rows of V logits (V <= 327,672).

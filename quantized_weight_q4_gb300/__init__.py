@@ -116,8 +116,8 @@ SIGNATURES = {
                             _vp, _vp, ctypes.c_float, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
     "q4_kv_gather": (_int, [_vp, _vp, _int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
     "q4_kv_attention": (_int, [_vp, _int, _vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
-                               _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _sz, _vp]),
-    "q4_kv_attention_workspace_size": (_sz, [_vp, _i64, _i64, _i64, _i64, _i64]),
+                               _i64, _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _sz, _vp]),
+    "q4_kv_attention_workspace_size": (_sz, [_vp, _i64, _i64, _i64, _i64, _i64, _i64]),
     "q4_sample": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "q4_get_device_status": (_int, [_vp]),
     "q4_last_device_flags": (ctypes.c_uint, []),
@@ -492,8 +492,8 @@ def q4_kv_gather(k_out, v_out, cache: KVCache, page_table, first, cu, stream=Non
 
 
 def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int, max_kv: int,
-                    scale: float | None = None, causal: bool = True, window: int = 0,
-                    workspace=None, stream=None) -> None:
+                    total_kv: int = 0, scale: float | None = None, causal: bool = True,
+                    window: int = 0, workspace=None, stream=None) -> None:
     """Attention of the new tokens' queries q [T, Hq, dim] over the cached
     tokens into out [T, Hq, dim] (include/q4.h).  scale: dim ** -0.5 by default."""
     _require_cuda(out, workspace)
@@ -505,14 +505,14 @@ def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int
     _check("q4_kv_attention", lib().q4_kv_attention(
         out.data_ptr(), _dtype_code(out), qp, _dtype_code(q), qs, Hq, cache.ref,
         _index("page_table", page_table, (B, None)), page_table.shape[1],
-        _index("kv_len", kv_len, (B,)), _index("cu_q", cu_q, (B + 1,)), B, T, max_q, max_kv,
+        _index("kv_len", kv_len, (B,)), _index("cu_q", cu_q, (B + 1,)), B, T, max_q, max_kv, total_kv,
         cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
         _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def q4_kv_attention_workspace_size(cache: KVCache, Hq: int, B: int, T: int, max_q: int,
-                                   max_kv: int) -> int:
-    return lib().q4_kv_attention_workspace_size(cache.ref, Hq, B, T, max_q, max_kv)
+                                   max_kv: int, total_kv: int = 0) -> int:
+    return lib().q4_kv_attention_workspace_size(cache.ref, Hq, B, T, max_q, max_kv, total_kv)
 
 
 def q4_sample(tokens, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,

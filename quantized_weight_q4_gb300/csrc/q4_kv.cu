@@ -4,7 +4,7 @@
 // A block is 16 consecutive tokens of one head; its codes are int8 and its
 // scale s fp32, value = code * s.  Appending tokens with largest magnitude m
 // to a block of scale s0 (0 for a block without earlier tokens) gives
-//   s = max(s0, m / 127)   (0 below 2^-110),
+//   s = max(s0, m * (1 / 127))   (0 below 2^-110),
 //   earlier codes  c <- rint(c * (s0 / s)),
 //   new codes      rint(x * (1 / s)), clamped to +-127,
 // every step one fp32 operation, so that the codes are a function of the
@@ -250,7 +250,7 @@ __device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k
   if (odd) atomicOr(p.err, kDevErrValue);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float s = fmaxf(s0, __fdiv_rn(m, 127.0f));
+  float s = fmaxf(s0, __fmul_rn(m, 1.0f / 127.0f));
   if (s < kTinyScale) s = 0.f;
   const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
   const float ratio = s > 0.f ? __fdiv_rn(s0, s) : 0.f;

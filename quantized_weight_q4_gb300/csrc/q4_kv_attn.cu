@@ -23,6 +23,7 @@
 //   same cost.  Products accumulate in fp32.
 // * A block's scale is one number per MMA tile: the key scale multiplies the
 //   scores, the value scale the weights, relative to the largest so far.
+#include <algorithm>
 #include <cfloat>
 
 #include <cuda.h>
@@ -52,7 +53,7 @@ struct AttnParams {
   CUtensorMap kmap, vmap;                 // codes: u8 [pages][heads * page][dim], boxes of 16 rows
   KvAttnCall a;
   int group;                              // query heads of one kv head
-  int tiles;                              // row tiles a sequence may have (of max_q * group rows)
+  int max_rows;                           // sequences with more query rows are left to the prompt form
   unsigned* tickets;                      // [grid], zero
   float* part;                            // [grid][2][kRows][dim + 2] shares
 };
@@ -183,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         const int nq = a.b.cu[b + 1] - a.b.cu[b];
         int lo, hi;
         seq_blocks(a, nq, a.b.kv_len[b], lo, hi);
-        const long long tiles = nq > 0 ? (static_cast<long long>(nq) * p.group + kTileRows - 1) / kTileRows : 0;
+        const long long rows = static_cast<long long>(nq) * p.group;
+        const long long tiles = nq > 0 && rows <= p.max_rows ? (rows + kTileRows - 1) / kTileRows : 0;
         const long long n = tiles * a.c.heads * (hi - lo);
         s_cum[b + 1] = sum + n;
         sum += n;
@@ -669,16 +671,17 @@ size_t kv_attn_split_bytes(int dim, int sms) {
   return kv_attn_header_bytes() + static_cast<size_t>(sms) * 2 * kRows * (dim + 2) * 4;
 }
 
-cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, void* ws, int sms, cudaStream_t st) {
+cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, void* ws, int sms, cudaStream_t st) {
   AttnParams p = {};
   if (!encode_codes(&p.kmap, a.c.k, a.c) || !encode_codes(&p.vmap, a.c.v, a.c)) return cudaErrorUnknown;
   p.a = a;
   p.group = a.Hq / a.c.heads;
+  p.max_rows = max_rows;
   p.tickets = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
   // one launch for each, a CTA per SM.  fp32 in or out needs both halves of the tile; bf16 takes them too
   // while eight rows are enough
-  const bool split = !a.q_bf16 || !a.out_bf16 || static_cast<long long>(max_q) * p.group <= 8;
+  const bool split = !a.q_bf16 || !a.out_bf16 || std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows) <= 8;
   if (a.c.dim == 128) return split ? launch<128, true>(p, sms, st) : launch<128, false>(p, sms, st);
   return split ? launch<64, true>(p, sms, st) : launch<64, false>(p, sms, st);
 }

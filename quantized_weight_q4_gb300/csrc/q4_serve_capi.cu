@@ -116,25 +116,55 @@ int q4_kv_gather(void* k_out, void* v_out, int dtype, const q4_kv_cache* cache, 
   return status_of(q4::launch_kv_gather(p, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// Query rows (new tokens x query heads that share a kv head) up to which a
+// sequence takes the split form.
+constexpr int kSplitRows = 64;
+
+struct AttnPlan {
+  bool prompt;          // the call may have sequences for the prompt form
+  long long rows;       // fp16 rows of it
+  size_t split_bytes, total;
+};
+
+AttnPlan attn_plan(const q4::KvView& c, int64_t Hq, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
+                   int64_t total_kv, bool bf16, int sms) {
+  AttnPlan p = {};
+  p.prompt = bf16 && (max_q < T ? max_q : T) * (Hq / c.heads) > kSplitRows;
+  p.split_bytes = (q4::kv_attn_split_bytes(c.dim, sms) + 255) / 256 * 256;
+  p.total = p.split_bytes;
+  if (p.prompt) {
+    p.rows = q4::kv_prompt_rows(static_cast<int>(B), max_kv, total_kv);
+    p.total += q4::kv_prompt_bytes(c, static_cast<int>(B), p.rows);
+  }
+  return p;
+}
+
+}  // namespace
+
 size_t q4_kv_attention_workspace_size(const q4_kv_cache* cache, int64_t Hq, int64_t B, int64_t T, int64_t max_q,
-                                      int64_t max_kv) {
+                                      int64_t max_kv, int64_t total_kv) {
   q4::KvView v;
-  if (check_cache(cache, &v) != Q4_OK || Hq <= 0 || B <= 0 || T <= 0 || max_q <= 0 || max_kv <= 0) return 0;
+  if (check_cache(cache, &v) != Q4_OK || Hq <= 0 || Hq % v.heads || B <= 0 || B > q4::kKvMaxSeqs || T <= 0 ||
+      max_q <= 0 || max_kv <= 0 || max_kv > (1LL << 30) || total_kv < 0)
+    return 0;
   int sms = 0;
   unsigned* status = nullptr;
   if (q4::device_info(&sms, &status) != Q4_OK) return 0;
-  return q4::kv_attn_split_bytes(v.dim, sms);
+  return attn_plan(v, Hq, B, T, max_q, max_kv, total_kv, true, sms).total;
 }
 
 int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_t q_stride, int64_t Hq,
                     const q4_kv_cache* cache, const int32_t* page_table, int64_t table_stride,
                     const int32_t* kv_len, const int32_t* cu_q, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
-                    float scale, int causal, int64_t window, void* workspace, size_t workspace_bytes, void* stream) {
+                    int64_t total_kv, float scale, int causal, int64_t window, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   q4::KvAttnCall a = {};
   int rc = check_cache(cache, &a.c);
   if (rc == Q4_OK) rc = check_batch(page_table, table_stride, kv_len, cu_q, B, T);
   if (rc != Q4_OK) return rc;
-  if (!out || Hq <= 0 || max_q <= 0 || max_kv <= 0 || window < 0 || (causal != 0 && causal != 1) ||
+  if (!out || Hq <= 0 || max_q <= 0 || max_kv <= 0 || total_kv < 0 || window < 0 || (causal != 0 && causal != 1) ||
       (window > 0 && !causal))
     return Q4_ERR_ARG;
   if (!known(q_dtype) || !known(out_dtype)) return Q4_ERR_DTYPE;
@@ -146,20 +176,23 @@ int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_
   rc = q4::device_info(&sms, &a.err);
   if (rc != Q4_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int most = static_cast<int>(max_q < T ? max_q : T);
-  const size_t need = q4::kv_attn_split_bytes(a.c.dim, sms);
-  void* ws = workspace;
+  const AttnPlan plan = attn_plan(a.c, Hq, B, T, max_q, max_kv, total_kv, q_dtype == Q4_BF16 && out_dtype == Q4_BF16, sms);
+  if (plan.rows > 0x7fffffffLL) return Q4_ERR_SHAPE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (ws) {
-    if (workspace_bytes < need) return Q4_ERR_WORKSPACE;
+    if (workspace_bytes < plan.total) return Q4_ERR_WORKSPACE;
   } else {
-    ws = q4::kv_stream_scratch(st, need);
+    ws = static_cast<uint8_t*>(q4::kv_stream_scratch(st, plan.total));
     if (!ws) return Q4_ERR_WORKSPACE;
   }
   a.b = {page_table, table_stride, kv_len, cu_q, static_cast<int>(B), static_cast<int>(T)};
   a.out = out, a.q = q, a.q_stride = q_stride, a.Hq = static_cast<int>(Hq);
   a.q_bf16 = q_dtype == Q4_BF16, a.out_bf16 = out_dtype == Q4_BF16;
   a.scale = scale, a.causal = causal, a.window = window;
-  return status_of(q4::launch_kv_attn_split(a, most, ws, sms, st));
+  const int most = static_cast<int>(max_q < T ? max_q : T);
+  const cudaError_t e = q4::launch_kv_attn_split(a, most, plan.prompt ? kSplitRows : 0x7fffffff, ws, sms, st);
+  if (e != cudaSuccess || !plan.prompt) return status_of(e);
+  return status_of(q4::launch_kv_prompt(a, kSplitRows, plan.rows, ws + plan.split_bytes, st));
 }
 
 int q4_sample(int32_t* tokens, float* probs, const void* logits, int logits_dtype, int64_t stride, int64_t T,

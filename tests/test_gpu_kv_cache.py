@@ -59,7 +59,7 @@ class HostCache:
                 rows = x[lo - start:hi - start, h]
                 m = np.abs(rows).max()
                 s0 = scales[pg, h, off // BLOCK] if lo > blk * BLOCK else f32(0)
-                s = max(s0, f32(m / f32(127)))
+                s = max(s0, f32(m * (f32(1) / f32(127))))
                 if s < f32(2.0 ** -110):
                     s = f32(0)
                 ratio = f32(s0 / s) if s > 0 else f32(0)
