@@ -12,6 +12,7 @@
 // over neighbours first (a binary tree over the head's elements) for the same
 // reason.
 #include <cfloat>
+#include <type_traits>
 
 #include "q4_kernels.h"
 #include "q4_kv_device.cuh"
@@ -22,6 +23,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kQRows = 4;              // query heads of one token a warp takes at once
+constexpr int kBlockWarps = 4;         // warps that share a block of keys or values
+constexpr int kBlockRows = kKvBlock / kBlockWarps;
 constexpr float kTinyScale = 7.70371977754894341e-34f;   // 2^-110
 
 // D / 32 consecutive elements of a row, as fp32.
@@ -146,21 +149,20 @@ __device__ void append_queries(const KvAppendParams& p, long long task, int lane
   const int t = static_cast<int>(task / groups);
   const int h0 = static_cast<int>(task % groups) * kQRows;
   if (t >= p.b.T) return;
+  constexpr int D = 32 * E;
+  float x[kQRows][E];   // on their way while the token's sequence and position are found
+#pragma unroll
+  for (int r = 0; r < kQRows; ++r) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[r][i] = 0.f;
+    if (h0 + r < p.Hq) load_row<E>(p.q, t * p.q_stride + (h0 + r) * D + lane * E, p.in_bf16, x[r]);
+  }
   const int b = warp_count_le(p.b.B, t, [&](int j) { return __ldg(p.b.cu + j); });
   int pos = -1;
   if (b < p.b.B && t >= __ldg(p.b.cu + b)) pos = __ldg(p.b.kv_len + b) - (__ldg(p.b.cu + b + 1) - t);
   if (p.cos && pos >= p.rope_rows) {
     if (lane == 0) atomicOr(p.err, kDevErrIndex);
     pos = -1;
-  }
-  constexpr int D = 32 * E;
-  float x[kQRows][E];
-#pragma unroll
-  for (int r = 0; r < kQRows; ++r) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[r][i] = 0.f;
-    if (pos >= 0 && h0 + r < p.Hq)
-      load_row<E>(p.q, t * p.q_stride + (h0 + r) * D + lane * E, p.in_bf16, x[r]);
   }
   if (pos >= 0) {
     Turn<E> turn;
@@ -175,6 +177,11 @@ __device__ void append_queries(const KvAppendParams& p, long long task, int lane
       if (p.q_norm) norm_row<E>(x[r], w, p.eps);
       if (p.cos) rotate_row<E>(p, lane, turn, x[r]);
     }
+  } else {
+#pragma unroll
+    for (int r = 0; r < kQRows; ++r)
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[r][i] = 0.f;
   }
 #pragma unroll
   for (int r = 0; r < kQRows; ++r)
@@ -182,115 +189,135 @@ __device__ void append_queries(const KvAppendParams& p, long long task, int lane
       store_row<E>(p.q_out, (static_cast<long long>(t) * p.Hq + h0 + r) * D + lane * E, p.out_bf16, x[r]);
 }
 
-// Keys or values: one warp takes one block of one head.  Slots of a sequence
-// start at cu[b] / 16 + 2 b: at least as many as the blocks it touches.
+// Keys or values: kBlockWarps warps take one block of one head, four tokens
+// each (s_max: their largest magnitudes).  Slots of a sequence start at
+// cu[b] / 16 + 2 b: at least as many as the blocks it touches.  Every thread of
+// the CTA calls it and meets once.
 template <int E>
-__device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k, int lane) {
-  const int b = warp_count_le(p.b.B, slot, [&](int j) { return (__ldg(p.b.cu + j) >> 4) + 2 * j; });
-  if (b >= p.b.B) return;
-  const int c0 = __ldg(p.b.cu + b), c1 = __ldg(p.b.cu + b + 1), len = __ldg(p.b.kv_len + b);
-  const int start = len - (c1 - c0);          // position of the first new token
-  const int from = max(start, 0);
-  const int at = slot - ((c0 >> 4) + 2 * b), blk = (from >> 4) + at;
-  if (c1 <= c0 || at < 0 || blk * kKvBlock >= len) return;
-  const int lo = max(from, blk * kKvBlock), hi = min(len, (blk + 1) * kKvBlock);
-  const long long row0 = kv_row(p.c, p.b.table, p.b.table_stride, b, blk * kKvBlock, h);
-  const long long tok0 = static_cast<long long>(c0) + (lo - start);   // packed row of position lo
-  if (row0 < 0 || c0 < 0 || tok0 + (hi - lo) > p.b.T || (is_k && p.cos && hi > p.rope_rows)) {
-    if (lane == 0) atomicOr(p.err, kDevErrIndex);
-    return;
-  }
+__device__ void append_block(const KvAppendParams& p, long long slot, int h, bool is_k, int part, int lane,
+                             float* s_max) {
   constexpr int D = 32 * E;
-  const void* src = is_k ? p.k : p.v;
-  const long long stride = is_k ? p.k_stride : p.v_stride;
-  float x[kKvBlock][E];
+  int blk = 0, lo = 0, hi = 0;       // of this warp's four positions, those in [lo, hi) are new
+  long long row0 = -1;
+  const int b = warp_count_le(p.b.B, static_cast<int>(slot), [&](int j) { return (__ldg(p.b.cu + j) >> 4) + 2 * j; });
+  float x[kBlockRows][E];
+  float s0 = 0.f, m = 0.f;
+  bool had = false;
+  if (b < p.b.B) {
+    const int c0 = __ldg(p.b.cu + b), c1 = __ldg(p.b.cu + b + 1), len = __ldg(p.b.kv_len + b);
+    const int start = len - (c1 - c0);          // position of the first new token
+    const int from = max(start, 0);
+    const int at = static_cast<int>(slot) - ((c0 >> 4) + 2 * b);
+    blk = (from >> 4) + at;
+    if (c1 > c0 && at >= 0 && blk * kKvBlock < len) {
+      lo = max(from, blk * kKvBlock), hi = min(len, (blk + 1) * kKvBlock);
+      const long long tok0 = static_cast<long long>(c0) + (lo - start);   // packed row of position lo
+      row0 = kv_row(p.c, p.b.table, p.b.table_stride, b, blk * kKvBlock, h);
+      if (row0 < 0 || c0 < 0 || tok0 + (hi - lo) > p.b.T || (is_k && p.cos && hi > p.rope_rows)) {
+        if (lane == 0) atomicOr(p.err, kDevErrIndex);
+        row0 = -1;
+      } else {
+        const void* src = is_k ? p.k : p.v;
+        const long long stride = is_k ? p.k_stride : p.v_stride;
 #pragma unroll
-  for (int r = 0; r < kKvBlock; ++r) {
+        for (int r = 0; r < kBlockRows; ++r) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[r][i] = 0.f;
-    const int pos = blk * kKvBlock + r;
-    if (pos >= lo && pos < hi)
-      load_row<E>(src, (tok0 + pos - lo) * stride + h * D + lane * E, p.in_bf16, x[r]);
-  }
-  float* scale = (is_k ? p.c.ks : p.c.vs) + (row0 >> 4);
-  const bool had = lo > blk * kKvBlock;
-  const float s0 = had ? *scale : 0.f;
-  if (is_k && (p.k_norm || p.cos)) {
-    float w[E];
-    if (p.k_norm) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) w[i] = __ldg(p.k_norm + lane * E + i);
-    }
-#pragma unroll
-    for (int r = 0; r < kKvBlock; ++r) {
-      const int pos = blk * kKvBlock + r;
-      if (pos < lo || pos >= hi) continue;
-      if (p.k_norm) norm_row<E>(x[r], w, p.eps);
-      if (p.cos) {
-        Turn<E> turn;
-        load_turn<E>(p, pos, lane, turn);
-        rotate_row<E>(p, lane, turn, x[r]);
+          for (int i = 0; i < E; ++i) x[r][i] = 0.f;
+          const int pos = blk * kKvBlock + part * kBlockRows + r;
+          if (pos >= lo && pos < hi)
+            load_row<E>(src, (tok0 + pos - lo) * stride + h * D + lane * E, p.in_bf16, x[r]);
+        }
+        had = lo > blk * kKvBlock;
+        if (had) s0 = (is_k ? p.c.ks : p.c.vs)[row0 >> 4];
       }
     }
   }
-  // a code cannot hold a NaN or an infinity: 0 and the largest number instead, and the status word says so
-  float m = 0.f;
-  bool odd = false;
+  if (row0 >= 0) {
+    if (is_k && (p.k_norm || p.cos)) {
+      float w[E];
+      if (p.k_norm) {
 #pragma unroll
-  for (int r = 0; r < kKvBlock; ++r)
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float a = fabsf(x[r][i]);
-      if (!(a <= FLT_MAX)) {
-        odd = true;
-        x[r][i] = x[r][i] != x[r][i] ? 0.f : copysignf(FLT_MAX, x[r][i]);
+        for (int i = 0; i < E; ++i) w[i] = __ldg(p.k_norm + lane * E + i);
       }
-      m = fmaxf(m, fabsf(x[r][i]));
-    }
-  if (odd) atomicOr(p.err, kDevErrValue);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int r = 0; r < kBlockRows; ++r) {
+        const int pos = blk * kKvBlock + part * kBlockRows + r;
+        if (pos < lo || pos >= hi) continue;
+        if (p.k_norm) norm_row<E>(x[r], w, p.eps);
+        if (p.cos) {
+          Turn<E> turn;
+          load_turn<E>(p, pos, lane, turn);
+          rotate_row<E>(p, lane, turn, x[r]);
+        }
+      }
+    }
+    // a code cannot hold a NaN or an infinity: 0 and the largest number instead, and the status word says so
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < kBlockRows; ++r)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float a = fabsf(x[r][i]);
+        if (!(a <= FLT_MAX)) {
+          odd = true;
+          x[r][i] = x[r][i] != x[r][i] ? 0.f : copysignf(FLT_MAX, x[r][i]);
+        }
+        m = fmaxf(m, fabsf(x[r][i]));
+      }
+    if (odd) atomicOr(p.err, kDevErrValue);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  if (lane == 0) s_max[part] = m;
+  __syncthreads();   // also: every warp has read the block's old scale
+  if (row0 < 0) return;
+#pragma unroll
+  for (int i = 0; i < kBlockWarps; ++i) m = fmaxf(m, s_max[i]);
   float s = fmaxf(s0, __fmul_rn(m, 1.0f / 127.0f));
   if (s < kTinyScale) s = 0.f;
   const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
   const float ratio = s > 0.f ? __fdiv_rn(s0, s) : 0.f;
-  int8_t* codes = (is_k ? p.c.k : p.c.v) + row0 * D + lane * E;
-  if (had && ratio != 1.f) {
-    for (int r = 0; r < lo - blk * kKvBlock; ++r) {
+  if (part == 0 && lane == 0) (is_k ? p.c.ks : p.c.vs)[row0 >> 4] = s;
+  int8_t* codes = (is_k ? p.c.k : p.c.v) + (row0 + part * kBlockRows) * D + lane * E;
+  using Word = typename std::conditional<E == 4, uint32_t, uint16_t>::type;   // the lane's E codes of a row
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        codes[r * D + i] = static_cast<int8_t>(__float2int_rn(__fmul_rn(static_cast<float>(codes[r * D + i]), ratio)));
-    }
-  }
-  if (lane == 0) *scale = s;
-#pragma unroll
-  for (int r = 0; r < kKvBlock; ++r) {
-    const int pos = blk * kKvBlock + r;
-    if (pos < lo || pos >= hi) continue;
+  for (int r = 0; r < kBlockRows; ++r) {
+    const int pos = blk * kKvBlock + part * kBlockRows + r;
+    Word* to = reinterpret_cast<Word*>(codes + r * D);
     uint32_t w = 0;
+    if (pos >= lo && pos < hi) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = max(-127, min(127, __float2int_rn(__fmul_rn(x[r][i], inv))));
-      w |= (static_cast<uint32_t>(c) & 0xffu) << (8 * i);
+      for (int i = 0; i < E; ++i) {
+        const int c = max(-127, min(127, __float2int_rn(__fmul_rn(x[r][i], inv))));
+        w |= (static_cast<uint32_t>(c) & 0xffu) << (8 * i);
+      }
+    } else if (pos < lo && ratio != 1.f) {
+      const uint32_t old = *to;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float c = static_cast<float>(static_cast<int8_t>(old >> (8 * i)));
+        w |= (static_cast<uint32_t>(__float2int_rn(__fmul_rn(c, ratio))) & 0xffu) << (8 * i);
+      }
+    } else {
+      continue;
     }
-    if (E == 4)
-      *reinterpret_cast<uint32_t*>(codes + r * D) = w;
-    else
-      *reinterpret_cast<uint16_t*>(codes + r * D) = static_cast<uint16_t>(w);
+    *to = static_cast<Word>(w);
   }
 }
 
 template <int E>
 __global__ void __launch_bounds__(kThreads) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
                                                                 int kv_ctas) {
+  __shared__ float s_max[kWarps];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (static_cast<int>(blockIdx.x) < kv_ctas) {   // the longer tasks first
-    const long long task = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    const int unit = warp / kBlockWarps;
+    const long long task = static_cast<long long>(blockIdx.x) * (kWarps / kBlockWarps) + unit;
     const int per = 2 * p.c.heads;
     const int i = static_cast<int>(task % per);
-    append_block<E>(p, static_cast<int>(task / per), i % p.c.heads, i < p.c.heads, lane);
+    append_block<E>(p, task / per, i % p.c.heads, i < p.c.heads, warp % kBlockWarps, lane, s_max + unit * kBlockWarps);
   } else {
     append_queries<E>(p, static_cast<long long>(blockIdx.x - kv_ctas) * kWarps + warp, lane);
   }
@@ -372,7 +399,8 @@ cudaError_t launch_pdl(void (*kernel)(Args...), unsigned grid, unsigned threads,
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t st) {
   const long long slots = p.b.T / kKvBlock + 2LL * p.b.B;
-  const long long kv_ctas = (slots * 2 * p.c.heads + kWarps - 1) / kWarps;
+  const int units = kWarps / kBlockWarps;
+  const long long kv_ctas = (slots * 2 * p.c.heads + units - 1) / units;
   const long long q_tasks = p.q_out ? static_cast<long long>(p.b.T) * ((p.Hq + kQRows - 1) / kQRows) : 0;
   const long long grid = kv_ctas + (q_tasks + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -13,11 +13,13 @@
 // Weights are whole numbers, so that no sum depends on its order.
 //
 // One thread-block cluster takes one row and keeps it in shared memory: the
-// logits are read once.  Whether a token is kept is a comparison with one
-// (z, index) cut.  The cut is found by histograms over z, coarse bins of
-// 1/36 nat first, then 1/1024 of the cut's bin, then (where the cut's bin
-// still holds different z) bins of the fp32 code itself; every CTA adds its
-// peers' bins through distributed shared memory and scans them for itself.
+// logits are read once, and HBM or, for few rows, the exchanges between the
+// CTAs bound the call.  Whether a token is kept is a comparison with one cut,
+// a z and how many tokens of that z stay (by index).  The cut is found from a
+// histogram over z (bins of 1/36 nat, added over the CTAs through distributed
+// shared memory) and, of the bins that matter, a list of their z that every
+// CTA gathers and searches for itself.  Where the list would be too long
+// (thousands of equal logits) further histograms narrow it down.
 #include <cfloat>
 
 #include "q4_kernels.h"
@@ -30,19 +32,28 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2 * kThreads;
 constexpr float kPerNat = 36.0f;             // coarse bins: 1024 / 36 = 28.4 > 40 ln 2 nats
+constexpr int kList = 2048;                  // longest list
+constexpr int kListK = 1024;                 // top-k up to which all kept tokens go on the list
 constexpr int kUnit = kWarps * 256;          // a CTA's elements are a multiple of this
 constexpr int kRowCtas = 8;
 constexpr int kMaxSlice = 40960;             // 160 KB of shared memory
 typedef unsigned long long u64;
 
 struct alignas(16) Shared {
-  unsigned hist[2][4][kBins];                // counts and three 14-bit pieces of the weights, two turns
-  float top[kRowCtas];
-  u64 sums[kWarps];
-  unsigned ties[kWarps];
-  unsigned lo, hi;                           // range of the cut bin's codes in this CTA
-  u64 scan_w[kWarps];
+  unsigned hist[3][kBins];                   // this CTA's: counts, low and high words of the weights
+  unsigned n[kBins];                         // all CTAs'
+  union {
+    u64 w[kBins];
+    unsigned all[kList];                     // the gathered list (w is not needed by then)
+  };
+  unsigned list[kList];                      // this CTA's part of it
+  unsigned list_n;
+  unsigned lo, hi;                           // range of codes
   unsigned scan_n[kWarps];
+  u64 scan_w[kWarps];
+  float top[kRowCtas];
+  u64 sums[kWarps];                          // weight before the cut, and tokens at it, of each warp's elements
+  unsigned ties[kWarps];
   float red[kWarps];
   // the bin that a search found
   int bin;
@@ -61,6 +72,12 @@ __device__ __forceinline__ u64 ld_peer_u64(uint32_t a) {
   u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void st_peer_u32(uint32_t a, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_peer_u64(uint32_t a, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
 // Code of z that grows as z falls.
@@ -82,63 +99,59 @@ __device__ __forceinline__ float clean(float l, float inv) {
   return z != z ? -INFINITY : fminf(z, FLT_MAX);
 }
 
+// z of a code of falling().
+__device__ __forceinline__ float of_code(unsigned c) {
+  return __uint_as_float((c & 0x80000000u) ? c : ~c & 0x7fffffffu);
+}
+
 struct Row {
   const float* z;        // this CTA's elements
-  int base, n;           // this warp's: base + i, i < n (n a multiple of 32)
+  int base, n;           // this warp's: base + i, i < n (n a multiple of 128)
   float top;             // the row's largest z
+  int ctas, rank;
 };
 
-__device__ __forceinline__ int coarse(float d) { return min(kBins - 1, static_cast<int>(d * kPerNat)); }
+// Every element of the warp's, four a lane at a time.
+template <typename F>
+__device__ __forceinline__ void each(const Row& r, F f) {
+#pragma unroll 2
+  for (int i = 4 * (threadIdx.x & 31); i < r.n; i += 128) {
+    const float4 z = *reinterpret_cast<const float4*>(r.z + r.base + i);
+    f(z.x), f(z.y), f(z.z), f(z.w);
+  }
+}
+
+constexpr float kZero = 27.75f;   // weights are 0 from 40 ln 2 = 27.73 nats below the largest
+__device__ __forceinline__ int coarse(float d) { return static_cast<int>(d * kPerNat); }   // d < kZero: below kBins
 __device__ __forceinline__ int fine(float d, int bin) {
   return max(0, min(kBins - 1, static_cast<int>((d * kPerNat - bin) * kBins)));
 }
 
-// Two bins a thread: counts and weights of all CTAs, and those of the bins before.
+__device__ __forceinline__ void add_bin(Shared& s, int b, u64 w, bool want_n, bool want_w) {
+  if (want_n) atomicAdd(&s.hist[0][b], 1u);
+  if (want_w) {
+    const unsigned lo = static_cast<unsigned>(w), hi = static_cast<unsigned>(w >> 32);
+    const unsigned carry = atomicAdd(&s.hist[1][b], lo) > ~lo ? 1u : 0u;
+    if (hi + carry) atomicAdd(&s.hist[2][b], hi + carry);
+  }
+}
+
+__device__ __forceinline__ void clear_bins(Shared& s) {
+  uint4* h = reinterpret_cast<uint4*>(&s.hist[0][0]);
+  for (int i = threadIdx.x; i < 3 * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Two bins a thread: counts and weights, and those of all bins before.
 struct Bins {
   unsigned n[2], before_n;
   u64 w[2], before_w;
 };
 
-// Adds bin_of(z) (negative: none) of every element into histogram `turn`, then
-// all CTAs' histograms together.
-template <typename F>
-__device__ __forceinline__ void histogram(Shared& s, int turn, int ctas, const Row& r, F bin_of, Bins& out) {
-  unsigned(*h)[kBins] = s.hist[turn];
-  for (int i = threadIdx.x; i < 4 * kBins; i += kThreads) (&h[0][0])[i] = 0;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-#pragma unroll 4
-  for (int i = lane; i < r.n; i += 32) {
-    const float z = r.z[r.base + i];
-    const u64 w = weight(expf(z - r.top));
-    if (w == 0) continue;
-    const int b = bin_of(z);
-    if (b < 0) continue;
-    atomicAdd(&h[0][b], 1u);
-    atomicAdd(&h[1][b], static_cast<unsigned>(w) & 0x3fffu);
-    atomicAdd(&h[2][b], static_cast<unsigned>(w >> 14) & 0x3fffu);
-    atomicAdd(&h[3][b], static_cast<unsigned>(w >> 28));
-  }
-  cluster_sync();
-  const int b0 = 2 * threadIdx.x;
-  out.n[0] = out.n[1] = 0;
-  out.w[0] = out.w[1] = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const uint32_t a = peer_addr(&h[0][b0], c);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const u64 two = ld_peer_u64(a + q * kBins * 4);
-      const u64 x0 = two & 0xffffffffull, x1 = two >> 32;
-      if (q == 0) {
-        out.n[0] += static_cast<unsigned>(x0), out.n[1] += static_cast<unsigned>(x1);
-      } else {
-        out.w[0] += x0 << (14 * (q - 1)), out.w[1] += x1 << (14 * (q - 1));
-      }
-    }
-  }
-  // exclusive scan over the threads' pairs
-  unsigned n = out.n[0] + out.n[1];
-  u64 w = out.w[0] + out.w[1];
+// The sums before each thread's bins; the block's totals are the sums of s.scan_*.
+__device__ __forceinline__ void scan_bins(Shared& s, Bins& b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned n = b.n[0] + b.n[1];
+  const u64 w = b.w[0] + b.w[1];
   unsigned sn = n;
   u64 sw = w;
 #pragma unroll
@@ -147,14 +160,55 @@ __device__ __forceinline__ void histogram(Shared& s, int turn, int ctas, const R
     const u64 uw = __shfl_up_sync(0xffffffffu, sw, o);
     if (lane >= o) sn += un, sw += uw;
   }
-  const int warp = threadIdx.x >> 5;
   if (lane == 31) s.scan_n[warp] = sn, s.scan_w[warp] = sw;
   __syncthreads();
   unsigned pn = 0;
   u64 pw = 0;
-  for (int i = 0; i < warp; ++i) pn += s.scan_n[i], pw += s.scan_w[i];
-  out.before_n = pn + sn - n;
-  out.before_w = pw + sw - w;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i)
+    if (i < warp) pn += s.scan_n[i], pw += s.scan_w[i];
+  b.before_n = pn + sn - n;
+  b.before_w = pw + sw - w;
+}
+
+// Adds bin_of(z, d) (negative: none) of the elements within kZero of the largest
+// into this CTA's bins, and gives every CTA the sums over all.
+template <typename F>
+__device__ __forceinline__ void histogram(Shared& s, const Row& r, bool want_n, bool want_w, F bin_of, Bins& out) {
+  clear_bins(s);
+  __syncthreads();
+  each(r, [&](float z) {
+    const float d = r.top - z;
+    if (!(d < kZero)) return;
+    const int b = bin_of(z, d);
+    if (b >= 0) add_bin(s, b, want_w ? weight(expf(-d)) : 0, want_n, want_w);
+  });
+  cluster_sync();
+  // each CTA adds its share of the bins and hands the sums to all
+  const int share = kBins / r.ctas;
+  for (int i = threadIdx.x; i < share; i += kThreads) {
+    const int b = r.rank * share + i;
+    unsigned n = 0;
+    u64 w = 0;
+    for (int c = 0; c < r.ctas; c += 4) {
+      unsigned x[4][3];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < 3; ++q) x[k][q] = c + k < r.ctas ? ld_peer_u32(peer_addr(&s.hist[q][b], c + k)) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) n += x[k][0], w += x[k][1] + (static_cast<u64>(x[k][2]) << 32);
+    }
+    for (int c = 0; c < r.ctas; ++c) {
+      st_peer_u32(peer_addr(&s.n[b], c), n);
+      st_peer_u64(peer_addr(&s.w[b], c), w);
+    }
+  }
+  cluster_sync();
+  const int b0 = 2 * threadIdx.x;
+  out.n[0] = s.n[b0], out.n[1] = s.n[b0 + 1];
+  out.w[0] = s.w[b0], out.w[1] = s.w[b0 + 1];
+  scan_bins(s, out);
 }
 
 // The bin in which the count (or weight) reaches `target` (1 or more, at most
@@ -177,75 +231,168 @@ __device__ __forceinline__ void find_bin(Shared& s, const Bins& b, bool by_weigh
   __syncthreads();
 }
 
-// The cut: z with code below `code`, and the first `ties` (by index) with that code.
+// The cut: tokens with a code below `code`, and the first `ties` (by index) with that code.
 struct Cut {
   unsigned code, ties;
   u64 weight;              // of all before the cut
 };
 
-// Finds the cut at which the count (or the weight) reaches target, given the
-// coarse histogram.  `turn` alternates the histograms' buffers.
-__device__ __forceinline__ Cut find_cut(Shared& s, int& turn, int ctas, const Row& r, const Bins& first,
-                                        bool by_weight, u64 target) {
-  find_bin(s, first, by_weight, target);
-  const int b1 = s.bin;
-  u64 done_w = s.before_w;
-  u64 left = target - (by_weight ? s.before_w : s.before_n);
-  Bins bins;
-  histogram(s, turn, ctas, r, [&](float z) {
+// Elements of one code have one weight.
+__device__ __forceinline__ Cut cut_at(unsigned code, float top, bool by_weight, u64 left, u64 done_w) {
+  const u64 w = weight(expf(of_code(code) - top));
+  Cut cut;
+  cut.code = code;
+  cut.ties = static_cast<unsigned>(by_weight ? (left + w - 1) / w : left);
+  cut.weight = done_w + cut.ties * w;
+  return cut;
+}
+
+// The range of the codes that `f` hands out, in s.lo and s.hi.
+template <typename F>
+__device__ __forceinline__ void code_range(Shared& s, F f) {
+  if (threadIdx.x == 0) s.lo = 0xffffffffu, s.hi = 0;
+  __syncthreads();
+  unsigned lo = 0xffffffffu, hi = 0;
+  f([&](unsigned c) { lo = min(lo, c), hi = max(hi, c); });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if ((threadIdx.x & 31) == 0 && lo <= hi) atomicMin(&s.lo, lo), atomicMax(&s.hi, hi);
+  __syncthreads();
+}
+
+// The cut of the list in s.all at which its count (or weight) reaches target.
+// before_w: weight of the tokens that come before the list.
+__device__ __forceinline__ Cut cut_of_list(Shared& s, int n, float top, bool by_weight, u64 target, u64 before_w) {
+  unsigned code[kList / kThreads];
+  u64 w[kList / kThreads];
+#pragma unroll
+  for (int k = 0; k < kList / kThreads; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    code[k] = i < n ? s.all[i] : 0xffffffffu;
+    w[k] = i < n ? weight(expf(of_code(code[k]) - top)) : 0;
+  }
+  code_range(s, [&](auto see) {
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k)
+      if (static_cast<int>(threadIdx.x) + k * kThreads < n) see(code[k]);
+  });
+  unsigned lo = s.lo, hi = s.hi;
+  u64 left = target, done_w = before_w;
+  while (lo < hi) {
+    const int shift = max(0, 32 - __clz(hi - lo) - 10);
+    clear_bins(s);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k)
+      if (static_cast<int>(threadIdx.x) + k * kThreads < n && code[k] >= lo && code[k] <= hi)
+        add_bin(s, static_cast<int>((code[k] - lo) >> shift), w[k], true, true);
+    __syncthreads();
+    Bins b;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = 2 * threadIdx.x + j;
+      b.n[j] = s.hist[0][i];
+      b.w[j] = s.hist[1][i] + (static_cast<u64>(s.hist[2][i]) << 32);
+    }
+    scan_bins(s, b);
+    find_bin(s, b, by_weight, left);
+    done_w += s.before_w;
+    left -= by_weight ? s.before_w : s.before_n;
+    const unsigned end = hi;
+    lo += static_cast<unsigned>(s.bin) << shift;
+    hi = min(end, lo + (1u << shift) - 1u);
+    if (s.bin_n == 1 && lo < hi) {   // one token: its code is the cut
+      const unsigned l0 = lo, h0 = hi;
+      code_range(s, [&](auto see) {
+#pragma unroll
+        for (int k = 0; k < kList / kThreads; ++k)
+          if (static_cast<int>(threadIdx.x) + k * kThreads < n && code[k] >= l0 && code[k] <= h0) see(code[k]);
+      });
+      lo = hi = s.lo;
+    }
+  }
+  return cut_at(lo, top, by_weight, left, done_w);
+}
+
+// The codes of all elements with want(d) into s.all of every CTA; returns how
+// many there are, more than kList: too many for the list.
+template <typename F>
+__device__ __forceinline__ unsigned gather_list(Shared& s, const Row& r, F want) {
+  if (threadIdx.x == 0) s.list_n = 0;
+  __syncthreads();
+  each(r, [&](float z) {
     const float d = r.top - z;
-    return coarse(d) == b1 ? fine(d, b1) : -1;
-  }, bins);
-  turn ^= 1;
+    if (d < kZero && want(d)) {
+      const unsigned at = atomicAdd(&s.list_n, 1u);
+      if (at < kList) s.list[at] = falling(z);
+    }
+  });
+  cluster_sync();
+  unsigned n = 0;
+  for (int c = 0; c < r.ctas; ++c) n += ld_peer_u32(peer_addr(&s.list_n, c));
+  if (n <= kList) {
+    unsigned at = 0;
+    for (int c = 0; c < r.ctas; ++c) {
+      const unsigned here = ld_peer_u32(peer_addr(&s.list_n, c));
+      for (unsigned i = threadIdx.x; i < here; i += kThreads) s.all[at + i] = ld_peer_u32(peer_addr(&s.list[i], c));
+      at += here;
+    }
+  }
+  __syncthreads();
+  return n;
+}
+
+// The cut inside coarse bin b1, whose list would be too long: `left` of the
+// count (or weight) is to be reached in it.  Finer bins, then bins of the code.
+__device__ __noinline__ Cut cut_by_bins(Shared& s, const Row& r, int b1, bool by_weight, u64 left, u64 done_w) {
+  Bins bins;
+  histogram(s, r, true, true, [&](float z, float d) { return coarse(d) == b1 ? fine(d, b1) : -1; }, bins);
   find_bin(s, bins, by_weight, left);
   const int b2 = s.bin;
   done_w += s.before_w;
   left -= by_weight ? s.before_w : s.before_n;
-  // range of codes in that bin
-  if (threadIdx.x == 0) s.lo = 0xffffffffu, s.hi = 0;
-  __syncthreads();
-  unsigned lo = 0xffffffffu, hi = 0;
-  for (int i = threadIdx.x & 31; i < r.n; i += 32) {
-    const float z = r.z[r.base + i], d = r.top - z;
-    if (d < 32.f && coarse(d) == b1 && fine(d, b1) == b2) {
-      const unsigned c = falling(z);
-      lo = min(lo, c), hi = max(hi, c);
-    }
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if ((threadIdx.x & 31) == 0 && lo <= hi) atomicMin(&s.lo, lo), atomicMax(&s.hi, hi);
+  code_range(s, [&](auto see) {
+    each(r, [&](float z) {
+      const float d = r.top - z;
+      if (d < kZero && coarse(d) == b1 && fine(d, b1) == b2) see(falling(z));
+    });
+  });
   cluster_sync();
-  lo = 0xffffffffu, hi = 0;
-  for (int c = 0; c < ctas; ++c) {
+  unsigned lo = 0xffffffffu, hi = 0;
+  for (int c = 0; c < r.ctas; ++c) {
     lo = min(lo, ld_peer_u32(peer_addr(&s.lo, c)));
     hi = max(hi, ld_peer_u32(peer_addr(&s.hi, c)));
   }
-  // bins of the code itself until one code is left
   while (lo < hi) {
     const int shift = max(0, 32 - __clz(hi - lo) - 10);
     const unsigned l0 = lo, h0 = hi;
-    histogram(s, turn, ctas, r, [&](float z) {
+    histogram(s, r, true, true, [&](float z, float d) {
       const unsigned c = falling(z);
-      if (c < l0 || c > h0) return -1;
-      const float d = r.top - z;
-      return coarse(d) == b1 && fine(d, b1) == b2 ? static_cast<int>((c - l0) >> shift) : -1;
+      return c >= l0 && c <= h0 && coarse(d) == b1 && fine(d, b1) == b2 ? static_cast<int>((c - l0) >> shift) : -1;
     }, bins);
-    turn ^= 1;
     find_bin(s, bins, by_weight, left);
     done_w += s.before_w;
     left -= by_weight ? s.before_w : s.before_n;
     lo = l0 + (static_cast<unsigned>(s.bin) << shift);
     hi = min(h0, lo + (1u << shift) - 1u);
   }
-  // elements of one code have one weight
-  const unsigned bits = (lo & 0x80000000u) ? lo : ~lo & 0x7fffffffu;
-  const u64 w = weight(expf(__uint_as_float(bits) - r.top));
-  Cut cut;
-  cut.code = lo;
-  cut.ties = static_cast<unsigned>(by_weight ? (left + w - 1) / w : left);
-  cut.weight = done_w + cut.ties * w;
-  return cut;
+  cluster_sync();   // peers have read s.lo and s.hi
+  return cut_at(lo, r.top, by_weight, left, done_w);
+}
+
+// The cut in coarse bin s.bin (just found).
+__device__ __forceinline__ Cut cut_in_bin(Shared& s, const Row& r, bool by_weight, u64 target) {
+  const int b = s.bin;
+  const u64 done_w = s.before_w, left = target - (by_weight ? s.before_w : s.before_n);
+  const unsigned n = gather_list(s, r, [&](float d) { return coarse(d) == b; });
+  if (n <= kList) return cut_of_list(s, static_cast<int>(n), r.top, by_weight, left, done_w);
+  return cut_by_bins(s, r, b, by_weight, left, done_w);
+}
+
+// The weight that top-p asks for, of `all` (at least 1).
+__device__ __forceinline__ u64 part_of(float top_p, u64 all) {
+  const double want = ceil(static_cast<double>(top_p) * static_cast<double>(all));
+  return want >= 1.0 ? static_cast<u64>(want) : 1ull;
 }
 
 template <bool BF16>
@@ -276,6 +423,7 @@ __global__ void __launch_bounds__(kThreads) q4_sample_kernel(const __grid_consta
   r.z = zs;
   r.n = slice / kWarps;
   r.base = warp * r.n;
+  r.ctas = ctas, r.rank = rank;
   float top = -INFINITY;
 #pragma unroll 4
   for (int i = lane * kVec; i < r.n; i += 32 * kVec) {
@@ -325,86 +473,113 @@ __global__ void __launch_bounds__(kThreads) q4_sample_kernel(const __grid_consta
   }
 
   Cut cut;
-  cut.code = 0xffffffffu;    // everything
-  cut.ties = 0xffffffffu;
-  cut.weight = 0;
+  cut.code = 0xffffffffu;    // everything: no code is as large
+  cut.ties = 0;
   const bool by_k = k > 0 && k < p.V, by_p = top_p < 1.0f;
   if (by_k || by_p) {
-    Bins first;
-    int turn = 0;
-    histogram(s, turn, ctas, r, [&](float z) { return coarse(r.top - z); }, first);
-    turn ^= 1;
+    // a short top-k: every token that may be kept goes on the list, and no weights are needed before
+    const bool short_k = by_k && k <= kListK;
+    Bins bins;
+    histogram(s, r, by_k, by_p && !short_k, [&](float, float d) { return coarse(d); }, bins);
     unsigned all_n = 0;
     u64 all_w = 0;
     for (int i = 0; i < kWarps; ++i) all_n += s.scan_n[i], all_w += s.scan_w[i];
-    __syncthreads();
-    if (by_k && static_cast<unsigned>(k) < all_n) {
-      cut = find_cut(s, turn, ctas, r, first, false, static_cast<u64>(k));
-      all_w = cut.weight;
+    const bool cut_k = by_k && static_cast<unsigned>(k) < all_n;
+    bool done = false;
+    if (short_k) {
+      // the bins down to the one that holds the k-th token (all, where there are no more than k)
+      find_bin(s, bins, false, cut_k ? static_cast<u64>(k) : static_cast<u64>(all_n));
+      const int last = s.bin;
+      if (s.before_n + s.bin_n <= kList) {
+        const int n = static_cast<int>(gather_list(s, r, [&](float d) { return coarse(d) <= last; }));
+        cut = cut_of_list(s, n, r.top, false, static_cast<u64>(min(static_cast<unsigned>(k), all_n)), 0);
+        if (by_p) {
+          const u64 want = part_of(top_p, cut.weight);
+          if (want < cut.weight) cut = cut_of_list(s, n, r.top, true, want, 0);
+        }
+        done = true;
+      } else if (by_p) {
+        // many equal logits at the k-th: from the start, with weights
+        histogram(s, r, true, true, [&](float, float d) { return coarse(d); }, bins);
+        all_w = 0;
+        for (int i = 0; i < kWarps; ++i) all_w += s.scan_w[i];
+      }
     }
-    if (by_p) {
-      const double want = ceil(static_cast<double>(top_p) * static_cast<double>(all_w));
-      const u64 target = want >= 1.0 ? static_cast<u64>(want) : 1ull;
-      if (target < all_w) cut = find_cut(s, turn, ctas, r, first, true, target);
+    if (!done) {
+      if (cut_k) {
+        find_bin(s, bins, false, static_cast<u64>(k));
+        cut = cut_in_bin(s, r, false, static_cast<u64>(k));
+        all_w = cut.weight;
+      }
+      if (by_p) {
+        const u64 want = part_of(top_p, all_w);
+        if (want < all_w) {
+          if (cut_k) cluster_sync();   // peers have read this CTA's part of the last list
+          find_bin(s, bins, true, want);
+          cut = cut_in_bin(s, r, true, want);
+        }
+      }
     }
   }
 
-  // how many tokens with the cut's code come before each warp's
-  unsigned before = 0;
-  if (cut.ties != 0xffffffffu) {
-    unsigned n = 0;
-    for (int i = lane; i < r.n; i += 32) n += falling(zs[r.base + i]) == cut.code;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) s.ties[warp] = n;
-    cluster_sync();
-    unsigned c = 0;
-    for (int i = lane; i < rank * kWarps + warp; i += 32) c += ld_peer_u32(peer_addr(&s.ties[i % kWarps], i / kWarps));
-    before = __reduce_add_sync(0xffffffffu, c);
-  }
-  // kept weight of element i of this warp's; `at`: tokens with the cut's code so far
-  auto kept = [&](int i, unsigned& at) -> u64 {
-    const float z = zs[r.base + i];
-    const unsigned c = falling(z);
-    bool ok = c < cut.code;
-    if (cut.ties == 0xffffffffu) {
-      ok = true;
-    } else {
-      const unsigned same = __ballot_sync(0xffffffffu, c == cut.code);
-      ok = ok || (c == cut.code && at + __popc(same & ((1u << lane) - 1u)) < cut.ties);
-      at += __popc(same);
-    }
-    const float e = expf(z - r.top);
-    return ok && e >= min_p ? weight(e) : 0;
-  };
+  // kept weight of each warp's elements before the cut, and tokens at it
   u64 sum = 0;
-  {
-    unsigned at = before;
-    for (int i = lane; i < r.n; i += 32) sum += kept(i, at);
-  }
+  unsigned same = 0;
+  each(r, [&](float z) {
+    const unsigned c = falling(z);
+    same += c == cut.code;
+    if (c < cut.code) {
+      const float e = expf(z - r.top);
+      if (e >= min_p) sum += weight(e);
+    }
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s.sums[warp] = sum;
+  same = __reduce_add_sync(0xffffffffu, same);
+  if (lane == 0) s.sums[warp] = sum, s.ties[warp] = same;
   cluster_sync();
   // every warp: the weight before its own elements, and all of it
-  u64 mine = 0, all = 0;
-  for (int i = lane; i < ctas * kWarps; i += 32) {
-    const u64 x = ld_peer_u64(peer_addr(&s.sums[i % kWarps], i / kWarps));
+  const float tie_e = expf(of_code(cut.code) - r.top);
+  const u64 tie_w = cut.ties > 0 && tie_e >= min_p ? weight(tie_e) : 0;
+  u64 mine = 0, all = 0, own = 0;
+  unsigned before = 0;                   // tokens at the cut before the warp's
+  for (int i0 = 0, ties = 0; i0 < ctas * kWarps; i0 += 32) {
+    const int i = i0 + lane;
+    const bool have = i < ctas * kWarps;
+    u64 x = have ? ld_peer_u64(peer_addr(&s.sums[i % kWarps], i / kWarps)) : 0;
+    const unsigned t = have ? ld_peer_u32(peer_addr(&s.ties[i % kWarps], i / kWarps)) : 0;
+    unsigned up = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned u = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += u;
+    }
+    const unsigned at = ties + up - t;   // tokens at the cut before warp i's
+    x += tie_w * (at < cut.ties ? min(t, cut.ties - at) : 0u);
     all += x;
     if (i < rank * kWarps + warp) mine += x;
+    if (i == rank * kWarps + warp) own = x, before = at;
+    ties += __shfl_sync(0xffffffffu, up, 31);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     all += __shfl_xor_sync(0xffffffffu, all, o);
     mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    own += __shfl_xor_sync(0xffffffffu, own, o);
   }
+  before = __reduce_max_sync(0xffffffffu, before);
   const double want = static_cast<double>(p.u[row]) * static_cast<double>(all);
   u64 at_w = want > 0.0 ? static_cast<u64>(want) : 0ull;
   if (all > 0 && at_w >= all) at_w = all - 1;
-  if (at_w >= mine && at_w < mine + sum) {
-    unsigned at = before;
+  if (at_w >= mine && at_w < mine + own) {
+    // the token is this warp's: through its elements in index order
     u64 done = mine;
     for (int i = lane; i < r.n; i += 32) {
-      const u64 w = kept(i, at);
+      const float z = zs[r.base + i], e = expf(z - r.top);
+      const unsigned c = falling(z), tied = __ballot_sync(0xffffffffu, c == cut.code);
+      const bool ok = c < cut.code || (c == cut.code && before + __popc(tied & ((1u << lane) - 1u)) < cut.ties);
+      before += __popc(tied);
+      const u64 w = ok && e >= min_p ? weight(e) : 0;
       u64 up = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
