@@ -15,6 +15,8 @@ import ctypes
 import os
 import threading
 
+import torch as _torch
+
 from . import _build
 
 Q4_OK = 0
@@ -139,6 +141,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """The loaded C library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB_PATH
@@ -381,22 +385,29 @@ def q4_moe_block_workspace_size(T: int, topk: int, E: int, H: int, I: int, Is: i
 
 
 # ------------------------------------------------------------------ serving
+# The serving calls are made once a token and layer, so their checks are kept
+# short: one attribute at a time, nothing looked up twice.
+_FLOAT_CODES = {_torch.float32: Q4_F32, _torch.bfloat16: Q4_BF16}
+
+
 class KVCache:
     """A paged 8-bit key/value cache over caller tensors (q4_kv_cache): k, v
     int8 [pages, heads, page_tokens, dim], k_scale, v_scale fp32 [pages, heads,
     page_tokens / 16].  KVCache.empty() allocates them.  The object keeps the
     tensors alive."""
 
+    __slots__ = ("k", "v", "k_scale", "v_scale", "struct", "ref", "pages", "heads", "page_tokens",
+                 "dim")
+
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
-        _require_cuda(k, v, k_scale, v_scale)
-        pages, heads, page, dim = k.shape
-        if k.dtype != torch.int8 or v.dtype != torch.int8 or v.shape != k.shape:
+        shape = pages, heads, page, dim = k.shape
+        if k.dtype is not _torch.int8 or v.dtype is not _torch.int8 or v.shape != shape:
             raise TypeError("k and v are int8 tensors of one shape")
         want = (pages, heads, page // Q4_KV_BLOCK)
-        if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32
+        if (k_scale.dtype is not _torch.float32 or v_scale.dtype is not _torch.float32
                 or k_scale.shape != want or v_scale.shape != want):
             raise TypeError(f"k_scale and v_scale are fp32 tensors of shape {want}")
+        _require_cuda(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                     v_scale.data_ptr(), pages, heads, dim, page)
@@ -405,7 +416,7 @@ class KVCache:
 
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, page_tokens: int = 64, device="cuda"):
-        import torch
+        torch = _torch
         codes = (pages, heads, page_tokens, dim)
         scales = (pages, heads, page_tokens // Q4_KV_BLOCK)
         return cls(*(torch.empty(codes, dtype=torch.int8, device=device) for _ in range(2)),
@@ -414,32 +425,46 @@ class KVCache:
 
 def _rows(t, heads, dim):
     """Data pointer and row stride of a [T, heads, dim] view whose rows are dense."""
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if h != heads or d != dim or s2 != 1 or (s1 != dim and heads > 1):
+        raise ValueError(f"expected a [T, {heads}, {dim}] tensor with dense rows")
     if not t.is_cuda:
         raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1 or (
-            heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"expected a [T, {heads}, {dim}] tensor with dense rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
-def _index(name, t, shape):
-    """Data pointer of a contiguous int32 CUDA tensor of the given shape (None: any size)."""
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+def _index(name, t, n, rows=False):
+    """Data pointer of a contiguous int32 CUDA tensor of n elements (rows: [n, any])."""
+    if t.dtype is not _torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} is a contiguous int32 CUDA tensor")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if (t.dim() != 2 or t.shape[0] != n) if rows else t.numel() != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(n, 'any') if rows else (n,)}")
     return t.data_ptr()
 
 
 def _floats(name, t, n):
     """Data pointer of a contiguous fp32 CUDA tensor of n elements, or None."""
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+    if t.dtype is not _torch.float32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} is a contiguous fp32 CUDA tensor of {n} elements")
     return t.data_ptr()
+
+
+def _out(name, t, n):
+    """Data pointer and dtype code of a contiguous fp32 or bf16 CUDA tensor of n elements."""
+    code = _FLOAT_CODES.get(t.dtype)
+    if code is None or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous fp32 or bf16 CUDA tensor of {n} elements")
+    return t.data_ptr(), code
+
+
+def _raw_stream(stream, t):
+    """cudaStream_t of a torch stream (default: the current stream of the tensor's device)."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(t.get_device()) or None
+    return stream.cuda_stream or None
 
 
 def q4_kv_append(cache: KVCache, q_out, q, k, v, page_table, kv_len, cu_q, cos=None, sin=None,
@@ -449,46 +474,50 @@ def q4_kv_append(cache: KVCache, q_out, q, k, v, page_table, kv_len, cu_q, cos=N
     q_out (include/q4.h).  q [T, Hq, dim], k, v [T, heads, dim]: views whose
     rows may be strided; q and q_out may both be None.  cos, sin: fp32
     [positions, rotated dim / 2], or None."""
-    T, B = k.shape[0], kv_len.shape[0]
-    kp, ks = _rows(k, cache.heads, cache.dim)
-    vp, vs = _rows(v, cache.heads, cache.dim)
-    if v.shape[0] != T or v.dtype != k.dtype or (q is None) != (q_out is None):
-        raise ValueError("k and v have the same rows and type; q and q_out go together")
-    dtype = _dtype_code(k)
+    T, B, heads, dim = k.shape[0], kv_len.shape[0], cache.heads, cache.dim
+    kp, ks = _rows(k, heads, dim)
+    vp, vs = _rows(v, heads, dim)
+    dtype = _FLOAT_CODES.get(k.dtype)
+    if v.shape[0] != T or v.dtype is not k.dtype or dtype is None or (q is None) != (q_out is None):
+        raise ValueError("k and v have the same rows and type (fp32 or bf16); q and q_out go together")
     qp, qs, Hq, out, out_dtype = None, 0, 0, None, Q4_F32
     if q is not None:
         Hq = q.shape[1]
-        qp, qs = _rows(q, Hq, cache.dim)
-        _require_cuda(q_out)
-        if q.shape[0] != T or q.dtype != k.dtype or q_out.numel() != T * Hq * cache.dim:
-            raise ValueError("q has the rows and type of k, q_out its size")
-        out, out_dtype = q_out.data_ptr(), _dtype_code(q_out)
+        qp, qs = _rows(q, Hq, dim)
+        if q.shape[0] != T or q.dtype is not k.dtype:
+            raise ValueError("q has the rows and type of k")
+        out, out_dtype = _out("q_out", q_out, T * Hq * dim)
     rope = None
     if cos is not None:
         if cos.dim() != 2 or sin is None or sin.shape != cos.shape:
             raise ValueError("cos and sin are two tables of one shape [positions, rotated dim / 2]")
-        rope = RopeStruct(_floats("cos", cos, cos.numel()), _floats("sin", sin, cos.numel()),
-                          cos.shape[0], 2 * cos.shape[1], rope_style)
-    _check("q4_kv_append", lib().q4_kv_append(
-        cache.ref, out, out_dtype, qp, qs, kp, ks, vp, vs, dtype, Hq,
-        ctypes.byref(rope) if rope is not None else None,
-        _floats("q_norm", q_norm, cache.dim), _floats("k_norm", k_norm, cache.dim), eps,
-        _index("page_table", page_table, (B, None)), page_table.shape[1],
-        _index("kv_len", kv_len, (B,)), _index("cu_q", cu_q, (B + 1,)), B, T, _stream(stream)))
+        n, half = cos.shape
+        table = RopeStruct(_floats("cos", cos, n * half), _floats("sin", sin, n * half), n, 2 * half,
+                           rope_style)
+        rope = ctypes.addressof(table)
+    rc = lib().q4_kv_append(
+        cache.ref, out, out_dtype, qp, qs, kp, ks, vp, vs, dtype, Hq, rope,
+        _floats("q_norm", q_norm, dim), _floats("k_norm", k_norm, dim), eps,
+        _index("page_table", page_table, B, True), page_table.shape[1],
+        _index("kv_len", kv_len, B), _index("cu_q", cu_q, B + 1), B, T, _raw_stream(stream, k))
+    if rc:
+        raise Q4Error("q4_kv_append", rc)
 
 
 def q4_kv_gather(k_out, v_out, cache: KVCache, page_table, first, cu, stream=None) -> None:
     """Cached tokens first[b] .. of each sequence b as numbers into rows
     cu[b] .. cu[b + 1] - 1 of k_out and v_out [T, heads, dim]."""
-    _require_cuda(k_out, v_out)
     B, T = first.shape[0], k_out.shape[0]
-    if v_out.dtype != k_out.dtype or k_out.numel() != T * cache.heads * cache.dim or (
-            v_out.numel() != k_out.numel()):
-        raise ValueError("k_out and v_out are [T, heads, dim] tensors of one type")
-    _check("q4_kv_gather", lib().q4_kv_gather(
-        k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out), cache.ref,
-        _index("page_table", page_table, (B, None)), page_table.shape[1],
-        _index("first", first, (B,)), _index("cu", cu, (B + 1,)), B, T, _stream(stream)))
+    n = T * cache.heads * cache.dim
+    kp, dtype = _out("k_out", k_out, n)
+    vp, v_dtype = _out("v_out", v_out, n)
+    if v_dtype != dtype:
+        raise ValueError("k_out and v_out have one type")
+    rc = lib().q4_kv_gather(
+        kp, vp, dtype, cache.ref, _index("page_table", page_table, B, True), page_table.shape[1],
+        _index("first", first, B), _index("cu", cu, B + 1), B, T, _raw_stream(stream, k_out))
+    if rc:
+        raise Q4Error("q4_kv_gather", rc)
 
 
 def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int, max_kv: int,
@@ -496,18 +525,25 @@ def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int
                     window: int = 0, workspace=None, stream=None) -> None:
     """Attention of the new tokens' queries q [T, Hq, dim] over the cached
     tokens into out [T, Hq, dim] (include/q4.h).  scale: dim ** -0.5 by default."""
-    _require_cuda(out, workspace)
-    T, Hq, B = q.shape[0], q.shape[1], kv_len.shape[0]
+    T, Hq, dim = q.shape
+    B = kv_len.shape[0]
     qp, qs = _rows(q, Hq, cache.dim)
-    if out.numel() != T * Hq * cache.dim:
-        raise ValueError("out has the size of q")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check("q4_kv_attention", lib().q4_kv_attention(
-        out.data_ptr(), _dtype_code(out), qp, _dtype_code(q), qs, Hq, cache.ref,
-        _index("page_table", page_table, (B, None)), page_table.shape[1],
-        _index("kv_len", kv_len, (B,)), _index("cu_q", cu_q, (B + 1,)), B, T, max_q, max_kv, total_kv,
-        cache.dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-        _ptr(workspace), ws_bytes, _stream(stream)))
+    op, out_dtype = _out("out", out, T * Hq * dim)
+    q_dtype = _FLOAT_CODES.get(q.dtype)
+    if q_dtype is None:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        _require_cuda(workspace)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = lib().q4_kv_attention(
+        op, out_dtype, qp, q_dtype, qs, Hq, cache.ref,
+        _index("page_table", page_table, B, True), page_table.shape[1],
+        _index("kv_len", kv_len, B), _index("cu_q", cu_q, B + 1), B, T, max_q, max_kv, total_kv,
+        dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, ws, ws_bytes,
+        _raw_stream(stream, q))
+    if rc:
+        raise Q4Error("q4_kv_attention", rc)
 
 
 def q4_kv_attention_workspace_size(cache: KVCache, Hq: int, B: int, T: int, max_q: int,
@@ -519,15 +555,18 @@ def q4_sample(tokens, logits, u, temperature=None, top_k=None, top_p=None, min_p
               stream=None) -> None:
     """One token a row of logits [T, V] (fp32 or bf16, rows may be strided),
     from the uniform numbers u [T]; settings are [T] tensors or None."""
-    if not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits is a [T, V] CUDA tensor with dense rows")
     T, V = logits.shape
-    _check("q4_sample", lib().q4_sample(
-        _index("tokens", tokens, (T,)), _floats("probs", probs, T), logits.data_ptr(),
-        _dtype_code(logits), logits.stride(0) if T > 1 else V, T, V, _floats("u", u, T),
-        _floats("temperature", temperature, T),
-        None if top_k is None else _index("top_k", top_k, (T,)), _floats("top_p", top_p, T),
-        _floats("min_p", min_p, T), _stream(stream)))
+    s0, s1 = logits.stride()
+    dtype = _FLOAT_CODES.get(logits.dtype)
+    if dtype is None or not logits.is_cuda or (s1 != 1 and V > 1):
+        raise ValueError("logits is a [T, V] fp32 or bf16 CUDA tensor with dense rows")
+    rc = lib().q4_sample(
+        _index("tokens", tokens, T), _floats("probs", probs, T), logits.data_ptr(), dtype,
+        s0 if T > 1 else V, T, V, _floats("u", u, T), _floats("temperature", temperature, T),
+        None if top_k is None else _index("top_k", top_k, T), _floats("top_p", top_p, T),
+        _floats("min_p", min_p, T), _raw_stream(stream, logits))
+    if rc:
+        raise Q4Error("q4_sample", rc)
 
 
 def q4_moe_static_scratch_bytes() -> int:

@@ -647,8 +647,8 @@ bool encode_codes(CUtensorMap* m, const int8_t* base, const KvView& c) {
 template <int D, bool SPLIT>
 cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   const size_t smem = smem_bytes<D>(p.a.b.B);
-  cudaError_t e = cudaFuncSetAttribute(q4_kv_attn_split_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<unsigned long long> allowed;
+  cudaError_t e = allow_smem(q4_kv_attn_split_kernel<D, SPLIT>, smem_bytes<D>(kKvMaxSeqs), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));

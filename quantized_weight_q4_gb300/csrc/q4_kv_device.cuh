@@ -1,10 +1,26 @@
 // Device helpers of the serving operators.
 #pragma once
 
+#include <atomic>
+
 #include "q4_device.cuh"
 #include "q4_kv.h"
 
 namespace q4 {
+
+// Lets `kernel` use `bytes` of dynamic shared memory; asked once for each
+// device (`done`: a bit for each, one word a kernel).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // The number of j in [1, n] with f(j) <= i, f non-decreasing: the whole warp
 // searches 32 probes at a time (one step up to n = 32, two up to 1024).

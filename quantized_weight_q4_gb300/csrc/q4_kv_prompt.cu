@@ -588,8 +588,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 
 template <typename P>
 cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const P& p) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -662,6 +660,10 @@ cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows
   const long long tiles = (static_cast<long long>(a.b.T) * p.group + kTileRows - 1) / kTileRows + a.b.B;
   if (tiles * a.c.heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(tiles * a.c.heads));
+  static std::atomic<unsigned long long> allowed[2];
+  e = a.c.dim == 128 ? allow_smem(q4_kv_prompt_kernel<128>, Cfg<128>::kSmem, allowed[0])
+                     : allow_smem(q4_kv_prompt_kernel<64>, Cfg<64>::kSmem, allowed[1]);
+  if (e != cudaSuccess) return e;
   return a.c.dim == 128 ? launch_pdl(q4_kv_prompt_kernel<128>, grid, kThreads, Cfg<128>::kSmem, st, p)
                         : launch_pdl(q4_kv_prompt_kernel<64>, grid, kThreads, Cfg<64>::kSmem, st, p);
 }

@@ -617,8 +617,9 @@ cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st) {
   const int ctas = cluster_of(p.V);
   const int slice = ((p.V + 7 + ctas - 1) / ctas + kUnit - 1) / kUnit * kUnit;
   const size_t smem = sizeof(Shared) + static_cast<size_t>(slice) * 4;
+  static std::atomic<unsigned long long> allowed[2];
   auto kernel = p.bf16 ? q4_sample_kernel<true> : q4_sample_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kernel, sizeof(Shared) + static_cast<size_t>(kMaxSlice) * 4, allowed[p.bf16 ? 1 : 0]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T) * ctas);
