@@ -28,33 +28,35 @@
 namespace q4 {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2 * kThreads;
+constexpr int kBins = 1024;
 constexpr float kPerNat = 36.0f;             // coarse bins: 1024 / 36 = 28.4 > 40 ln 2 nats
 constexpr int kList = 2048;                  // longest list
 constexpr int kListK = 1024;                 // top-k up to which all kept tokens go on the list
-constexpr int kUnit = kWarps * 256;          // a CTA's elements are a multiple of this
+constexpr int kMaxWarps = 32;
 constexpr int kRowCtas = 8;
-constexpr int kMaxSlice = 40960;             // 160 KB of shared memory
+constexpr int kSliceBytes = 160 * 1024;      // most elements a CTA holds
 typedef unsigned long long u64;
 
 struct alignas(16) Shared {
   unsigned hist[3][kBins];                   // this CTA's: counts, low and high words of the weights
-  unsigned n[kBins];                         // all CTAs'
+  union {
+    unsigned n[kBins];                       // all CTAs'
+    unsigned list[kList];                    // this CTA's part of the list (n and w are in registers by then)
+  };
   union {
     u64 w[kBins];
-    unsigned all[kList];                     // the gathered list (w is not needed by then)
+    unsigned all[kList];                     // the gathered list
   };
-  unsigned list[kList];                      // this CTA's part of it
   unsigned list_n;
   unsigned lo, hi;                           // range of codes
-  unsigned scan_n[kWarps];
-  u64 scan_w[kWarps];
+  unsigned scan_n[kMaxWarps];
+  u64 scan_w[kMaxWarps];
   float top[kRowCtas];
-  u64 sums[kWarps];                          // weight before the cut, and tokens at it, of each warp's elements
-  unsigned ties[kWarps];
-  float red[kWarps];
+  u64 sums[kMaxWarps];                          // weight before the cut, and tokens at it, of each warp's elements
+  unsigned ties[kMaxWarps];
+  float red[kMaxWarps];
+  u64 part[kMaxWarps];                       // the same of the pieces of one warp's elements
+  unsigned part_ties[kMaxWarps];
   // the bin that a search found
   int bin;
   unsigned bin_n, before_n;
@@ -99,24 +101,54 @@ __device__ __forceinline__ float clean(float l, float inv) {
   return z != z ? -INFINITY : fminf(z, FLT_MAX);
 }
 
+// Inclusive sum over the warp's lanes.
+template <typename T>
+__device__ __forceinline__ T scan_up(T x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
+}
+
 // z of a code of falling().
 __device__ __forceinline__ float of_code(unsigned c) {
   return __uint_as_float((c & 0x80000000u) ? c : ~c & 0x7fffffffu);
 }
 
+// The CTA's elements as they came (fp32 or bf16; -inf where there are none).
+template <bool BF16, int THREADS>
 struct Row {
-  const float* z;        // this CTA's elements
+  static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kPer = kBins / THREADS;
+  const void* x;
   int base, n;           // this warp's: base + i, i < n (n a multiple of 128)
+  float inv;             // 1 / temperature
   float top;             // the row's largest z
   int ctas, rank;
+
+  __device__ __forceinline__ float z(int i) const {
+    if (BF16) return clean(bf16_bits_to_f32(static_cast<const uint16_t*>(x)[base + i]), inv);
+    return clean(static_cast<const float*>(x)[base + i], inv);
+  }
+  // elements i .. i + 3, i a multiple of 4
+  __device__ __forceinline__ float4 z4(int i) const {
+    if (BF16) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + base + i);
+      return make_float4(clean(__uint_as_float(w.x << 16), inv), clean(__uint_as_float(w.x & 0xffff0000u), inv),
+                         clean(__uint_as_float(w.y << 16), inv), clean(__uint_as_float(w.y & 0xffff0000u), inv));
+    }
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + base + i);
+    return make_float4(clean(f.x, inv), clean(f.y, inv), clean(f.z, inv), clean(f.w, inv));
+  }
 };
 
 // Every element of the warp's, four a lane at a time.
-template <typename F>
-__device__ __forceinline__ void each(const Row& r, F f) {
+template <typename R, typename F>
+__device__ __forceinline__ void each(const R& r, F f) {
 #pragma unroll 2
   for (int i = 4 * (threadIdx.x & 31); i < r.n; i += 128) {
-    const float4 z = *reinterpret_cast<const float4*>(r.z + r.base + i);
+    const float4 z = r.z4(i);
     f(z.x), f(z.y), f(z.z), f(z.w);
   }
 }
@@ -136,46 +168,47 @@ __device__ __forceinline__ void add_bin(Shared& s, int b, u64 w, bool want_n, bo
   }
 }
 
+template <int kThreads>
 __device__ __forceinline__ void clear_bins(Shared& s) {
   uint4* h = reinterpret_cast<uint4*>(&s.hist[0][0]);
   for (int i = threadIdx.x; i < 3 * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Two bins a thread: counts and weights, and those of all bins before.
+// A thread's bins: counts and weights, and those of all bins before.
+template <int kPer>
 struct Bins {
-  unsigned n[2], before_n;
-  u64 w[2], before_w;
+  unsigned n[kPer], before_n;
+  u64 w[kPer], before_w;
 };
 
 // The sums before each thread's bins; the block's totals are the sums of s.scan_*.
-__device__ __forceinline__ void scan_bins(Shared& s, Bins& b) {
+template <int kPer>
+__device__ __forceinline__ void scan_bins(Shared& s, Bins<kPer>& b) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned n = b.n[0] + b.n[1];
-  const u64 w = b.w[0] + b.w[1];
-  unsigned sn = n;
-  u64 sw = w;
+  unsigned n = 0;
+  u64 w = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned un = __shfl_up_sync(0xffffffffu, sn, o);
-    const u64 uw = __shfl_up_sync(0xffffffffu, sw, o);
-    if (lane >= o) sn += un, sw += uw;
-  }
+  for (int j = 0; j < kPer; ++j) n += b.n[j], w += b.w[j];
+  const unsigned sn = scan_up(n);
+  const u64 sw = scan_up(w);
   if (lane == 31) s.scan_n[warp] = sn, s.scan_w[warp] = sw;
   __syncthreads();
-  unsigned pn = 0;
-  u64 pw = 0;
+  // a lane for each warp
+  unsigned pn = lane < warp ? s.scan_n[lane] : 0;
+  u64 pw = lane < warp ? s.scan_w[lane] : 0;
+  pn = __reduce_add_sync(0xffffffffu, pn);
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i)
-    if (i < warp) pn += s.scan_n[i], pw += s.scan_w[i];
+  for (int o = 16; o > 0; o >>= 1) pw += __shfl_xor_sync(0xffffffffu, pw, o);
   b.before_n = pn + sn - n;
   b.before_w = pw + sw - w;
 }
 
 // Adds bin_of(z, d) (negative: none) of the elements within kZero of the largest
 // into this CTA's bins, and gives every CTA the sums over all.
-template <typename F>
-__device__ __forceinline__ void histogram(Shared& s, const Row& r, bool want_n, bool want_w, F bin_of, Bins& out) {
-  clear_bins(s);
+template <typename R, typename F>
+__device__ __forceinline__ void histogram(Shared& s, const R& r, bool want_n, bool want_w, F bin_of, Bins<R::kPer>& out) {
+  constexpr int kThreads = R::kThreads, kPer = R::kPer;
+  clear_bins<kThreads>(s);
   __syncthreads();
   each(r, [&](float z) {
     const float d = r.top - z;
@@ -205,23 +238,23 @@ __device__ __forceinline__ void histogram(Shared& s, const Row& r, bool want_n, 
     }
   }
   cluster_sync();
-  const int b0 = 2 * threadIdx.x;
-  out.n[0] = s.n[b0], out.n[1] = s.n[b0 + 1];
-  out.w[0] = s.w[b0], out.w[1] = s.w[b0 + 1];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) out.n[j] = s.n[kPer * threadIdx.x + j], out.w[j] = s.w[kPer * threadIdx.x + j];
   scan_bins(s, out);
 }
 
 // The bin in which the count (or weight) reaches `target` (1 or more, at most
 // the total), into s.bin and what stands beside it.
-__device__ __forceinline__ void find_bin(Shared& s, const Bins& b, bool by_weight, u64 target) {
+template <int kPer>
+__device__ __forceinline__ void find_bin(Shared& s, const Bins<kPer>& b, bool by_weight, u64 target) {
   unsigned n = b.before_n;
   u64 w = b.before_w;
   __syncthreads();   // the last search's result has been read
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < kPer; ++j) {
     const u64 at = by_weight ? w : n, to = by_weight ? w + b.w[j] : n + b.n[j];
     if (at < target && target <= to) {
-      s.bin = 2 * threadIdx.x + j;
+      s.bin = kPer * threadIdx.x + j;
       s.before_n = n, s.bin_n = b.n[j];
       s.before_w = w, s.bin_w = b.w[j];
     }
@@ -262,7 +295,9 @@ __device__ __forceinline__ void code_range(Shared& s, F f) {
 
 // The cut of the list in s.all at which its count (or weight) reaches target.
 // before_w: weight of the tokens that come before the list.
+template <typename R>
 __device__ __forceinline__ Cut cut_of_list(Shared& s, int n, float top, bool by_weight, u64 target, u64 before_w) {
+  constexpr int kThreads = R::kThreads, kPer = R::kPer;
   unsigned code[kList / kThreads];
   u64 w[kList / kThreads];
 #pragma unroll
@@ -280,17 +315,17 @@ __device__ __forceinline__ Cut cut_of_list(Shared& s, int n, float top, bool by_
   u64 left = target, done_w = before_w;
   while (lo < hi) {
     const int shift = max(0, 32 - __clz(hi - lo) - 10);
-    clear_bins(s);
+    clear_bins<kThreads>(s);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kList / kThreads; ++k)
       if (static_cast<int>(threadIdx.x) + k * kThreads < n && code[k] >= lo && code[k] <= hi)
         add_bin(s, static_cast<int>((code[k] - lo) >> shift), w[k], true, true);
     __syncthreads();
-    Bins b;
+    Bins<kPer> b;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = 2 * threadIdx.x + j;
+    for (int j = 0; j < kPer; ++j) {
+      const int i = kPer * threadIdx.x + j;
       b.n[j] = s.hist[0][i];
       b.w[j] = s.hist[1][i] + (static_cast<u64>(s.hist[2][i]) << 32);
     }
@@ -316,8 +351,8 @@ __device__ __forceinline__ Cut cut_of_list(Shared& s, int n, float top, bool by_
 
 // The codes of all elements with want(d) into s.all of every CTA; returns how
 // many there are, more than kList: too many for the list.
-template <typename F>
-__device__ __forceinline__ unsigned gather_list(Shared& s, const Row& r, F want) {
+template <typename R, typename F>
+__device__ __forceinline__ unsigned gather_list(Shared& s, const R& r, F want) {
   if (threadIdx.x == 0) s.list_n = 0;
   __syncthreads();
   each(r, [&](float z) {
@@ -328,15 +363,21 @@ __device__ __forceinline__ unsigned gather_list(Shared& s, const Row& r, F want)
     }
   });
   cluster_sync();
-  unsigned n = 0;
-  for (int c = 0; c < r.ctas; ++c) n += ld_peer_u32(peer_addr(&s.list_n, c));
+  // each warp reads every part's length, and copies from the CTAs that fall to it
+  const int lane = threadIdx.x & 31;
+  const unsigned mine = lane < r.ctas ? ld_peer_u32(peer_addr(&s.list_n, lane)) : 0;
+  unsigned up = mine;
+#pragma unroll
+  for (int o = 1; o < kRowCtas; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += x;
+  }
+  const unsigned n = __shfl_sync(0xffffffffu, up, r.ctas - 1);
   if (n <= kList) {
-    unsigned at = 0;
-    for (int c = 0; c < r.ctas; ++c) {
-      const unsigned here = ld_peer_u32(peer_addr(&s.list_n, c));
-      for (unsigned i = threadIdx.x; i < here; i += kThreads) s.all[at + i] = ld_peer_u32(peer_addr(&s.list[i], c));
-      at += here;
-    }
+    const int warp = threadIdx.x >> 5, c = warp % r.ctas, share = R::kWarps / r.ctas;   // share: warps a part
+    const unsigned here = __shfl_sync(0xffffffffu, mine, c), at = __shfl_sync(0xffffffffu, up, c) - here;
+    for (unsigned i = (warp / r.ctas) * 32 + lane; i < here; i += 32 * share)
+      s.all[at + i] = ld_peer_u32(peer_addr(&s.list[i], c));
   }
   __syncthreads();
   return n;
@@ -344,8 +385,9 @@ __device__ __forceinline__ unsigned gather_list(Shared& s, const Row& r, F want)
 
 // The cut inside coarse bin b1, whose list would be too long: `left` of the
 // count (or weight) is to be reached in it.  Finer bins, then bins of the code.
-__device__ __noinline__ Cut cut_by_bins(Shared& s, const Row& r, int b1, bool by_weight, u64 left, u64 done_w) {
-  Bins bins;
+template <typename R>
+__device__ __noinline__ Cut cut_by_bins(Shared& s, const R& r, int b1, bool by_weight, u64 left, u64 done_w) {
+  Bins<R::kPer> bins;
   histogram(s, r, true, true, [&](float z, float d) { return coarse(d) == b1 ? fine(d, b1) : -1; }, bins);
   find_bin(s, bins, by_weight, left);
   const int b2 = s.bin;
@@ -381,11 +423,12 @@ __device__ __noinline__ Cut cut_by_bins(Shared& s, const Row& r, int b1, bool by
 }
 
 // The cut in coarse bin s.bin (just found).
-__device__ __forceinline__ Cut cut_in_bin(Shared& s, const Row& r, bool by_weight, u64 target) {
+template <typename R>
+__device__ __forceinline__ Cut cut_in_bin(Shared& s, const R& r, bool by_weight, u64 target) {
   const int b = s.bin;
   const u64 done_w = s.before_w, left = target - (by_weight ? s.before_w : s.before_n);
   const unsigned n = gather_list(s, r, [&](float d) { return coarse(d) == b; });
-  if (n <= kList) return cut_of_list(s, static_cast<int>(n), r.top, by_weight, left, done_w);
+  if (n <= kList) return cut_of_list<R>(s, static_cast<int>(n), r.top, by_weight, left, done_w);
   return cut_by_bins(s, r, b, by_weight, left, done_w);
 }
 
@@ -395,12 +438,14 @@ __device__ __forceinline__ u64 part_of(float top_p, u64 all) {
   return want >= 1.0 ? static_cast<u64>(want) : 1ull;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) q4_sample_kernel(const __grid_constant__ SampleParams p, int ctas,
+template <bool BF16, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(const __grid_constant__ SampleParams p, int ctas,
                                                              int slice) {
+  using R = Row<BF16, kThreads>;
+  constexpr int kWarps = R::kWarps;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
-  float* zs = reinterpret_cast<float*>(smem + sizeof(Shared));
+  uint8_t* xs = smem + sizeof(Shared);
   pdl_launch_dependents();
   pdl_wait();
   const int row = blockIdx.x / ctas, rank = static_cast<int>(cluster_ctarank());
@@ -419,38 +464,37 @@ __global__ void __launch_bounds__(kThreads) q4_sample_kernel(const __grid_consta
   const int head = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / kSize);
   base -= head * kSize;
   const int v0 = rank * slice;
-  Row r;
-  r.z = zs;
+  R r;
+  r.x = xs;
   r.n = slice / kWarps;
   r.base = warp * r.n;
+  r.inv = inv;
   r.ctas = ctas, r.rank = rank;
-  float top = -INFINITY;
+  // asynchronous copies, so that all of a thread's are on their way together; the row's edges by element
 #pragma unroll 4
   for (int i = lane * kVec; i < r.n; i += 32 * kVec) {
     const int v = v0 + r.base + i;
-    float x[kVec];
+    uint8_t* to = xs + static_cast<size_t>(r.base + i) * kSize;
     if (v >= head && v + kVec <= head + p.V) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(base + static_cast<long long>(v) * kSize));
-      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        x[j] = clean(BF16 ? __uint_as_float((j & 1) ? q[j / 2] & 0xffff0000u : q[j / 2] << 16) : __uint_as_float(q[j & 3]), inv);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                   "l"(base + static_cast<long long>(v) * kSize)
+                   : "memory");
     } else {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        x[j] = -INFINITY;
-        if (v + j >= head && v + j < head + p.V) {
-          const uint8_t* a = base + static_cast<long long>(v + j) * kSize;
-          x[j] = clean(BF16 ? bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(a)) : *reinterpret_cast<const float*>(a), inv);
-        }
+        const bool in = v + j >= head && v + j < head + p.V;
+        const uint8_t* a = base + static_cast<long long>(v + j) * kSize;
+        if (BF16)
+          reinterpret_cast<uint16_t*>(to)[j] = in ? *reinterpret_cast<const uint16_t*>(a) : 0xff80;   // -inf
+        else
+          reinterpret_cast<uint32_t*>(to)[j] = in ? *reinterpret_cast<const uint32_t*>(a) : 0xff800000u;
       }
     }
-#pragma unroll
-    for (int j = 0; j < kVec; j += 4) {
-      *reinterpret_cast<float4*>(zs + r.base + i + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-      top = fmaxf(top, fmaxf(fmaxf(x[j], x[j + 1]), fmaxf(x[j + 2], x[j + 3])));
-    }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();   // a warp reads its own elements only
+  float top = -INFINITY;
+  each(r, [&](float z) { top = fmaxf(top, z); });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s.red[warp] = top;
@@ -476,13 +520,17 @@ __global__ void __launch_bounds__(kThreads) q4_sample_kernel(const __grid_consta
   cut.code = 0xffffffffu;    // everything: no code is as large
   cut.ties = 0;
   const bool by_k = k > 0 && k < p.V, by_p = top_p < 1.0f;
-  if (by_k || by_p) {
+  if (k == 1) {
+    cut.code = falling(top);
+    cut.ties = 1;
+  } else if (by_k || by_p) {
     // a short top-k: every token that may be kept goes on the list, and no weights are needed before
     const bool short_k = by_k && k <= kListK;
-    Bins bins;
+    Bins<R::kPer> bins;
     histogram(s, r, by_k, by_p && !short_k, [&](float, float d) { return coarse(d); }, bins);
     unsigned all_n = 0;
     u64 all_w = 0;
+#pragma unroll
     for (int i = 0; i < kWarps; ++i) all_n += s.scan_n[i], all_w += s.scan_w[i];
     const bool cut_k = by_k && static_cast<unsigned>(k) < all_n;
     bool done = false;
@@ -492,10 +540,10 @@ __global__ void __launch_bounds__(kThreads) q4_sample_kernel(const __grid_consta
       const int last = s.bin;
       if (s.before_n + s.bin_n <= kList) {
         const int n = static_cast<int>(gather_list(s, r, [&](float d) { return coarse(d) <= last; }));
-        cut = cut_of_list(s, n, r.top, false, static_cast<u64>(min(static_cast<unsigned>(k), all_n)), 0);
+        cut = cut_of_list<R>(s, n, r.top, false, static_cast<u64>(min(static_cast<unsigned>(k), all_n)), 0);
         if (by_p) {
           const u64 want = part_of(top_p, cut.weight);
-          if (want < cut.weight) cut = cut_of_list(s, n, r.top, true, want, 0);
+          if (want < cut.weight) cut = cut_of_list<R>(s, n, r.top, true, want, 0);
         }
         done = true;
       } else if (by_p) {
@@ -541,100 +589,144 @@ __global__ void __launch_bounds__(kThreads) q4_sample_kernel(const __grid_consta
   // every warp: the weight before its own elements, and all of it
   const float tie_e = expf(of_code(cut.code) - r.top);
   const u64 tie_w = cut.ties > 0 && tie_e >= min_p ? weight(tie_e) : 0;
-  u64 mine = 0, all = 0, own = 0;
-  unsigned before = 0;                   // tokens at the cut before the warp's
-  for (int i0 = 0, ties = 0; i0 < ctas * kWarps; i0 += 32) {
-    const int i = i0 + lane;
+  // weight of warp i's kept tokens, i = 32 q + lane, and of all before; tokens at the cut before it
+  constexpr int kQ = kRowCtas * kWarps / 32;
+  u64 x[kQ], upto[kQ], all = 0;
+  unsigned at[kQ], ties = 0;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    const int i = 32 * q + lane;
     const bool have = i < ctas * kWarps;
-    u64 x = have ? ld_peer_u64(peer_addr(&s.sums[i % kWarps], i / kWarps)) : 0;
-    const unsigned t = have ? ld_peer_u32(peer_addr(&s.ties[i % kWarps], i / kWarps)) : 0;
-    unsigned up = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned u = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += u;
-    }
-    const unsigned at = ties + up - t;   // tokens at the cut before warp i's
-    x += tie_w * (at < cut.ties ? min(t, cut.ties - at) : 0u);
-    all += x;
-    if (i < rank * kWarps + warp) mine += x;
-    if (i == rank * kWarps + warp) own = x, before = at;
-    ties += __shfl_sync(0xffffffffu, up, 31);
+    x[q] = have ? ld_peer_u64(peer_addr(&s.sums[i % kWarps], i / kWarps)) : 0;
+    at[q] = have ? ld_peer_u32(peer_addr(&s.ties[i % kWarps], i / kWarps)) : 0;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    own += __shfl_xor_sync(0xffffffffu, own, o);
+  for (int q = 0; q < kQ; ++q) {
+    if (32 * q >= ctas * kWarps) break;
+    const unsigned t = at[q];
+    at[q] = ties + scan_up(t) - t;
+    ties = __shfl_sync(0xffffffffu, at[q] + t, 31);
+    x[q] += tie_w * (at[q] < cut.ties ? min(t, cut.ties - at[q]) : 0u);
+    upto[q] = all + scan_up(x[q]);
+    all = __shfl_sync(0xffffffffu, upto[q], 31);
   }
-  before = __reduce_max_sync(0xffffffffu, before);
   const double want = static_cast<double>(p.u[row]) * static_cast<double>(all);
   u64 at_w = want > 0.0 ? static_cast<u64>(want) : 0ull;
   if (all > 0 && at_w >= all) at_w = all - 1;
-  if (at_w >= mine && at_w < mine + own) {
-    // the token is this warp's: through its elements in index order
-    u64 done = mine;
-    for (int i = lane; i < r.n; i += 32) {
-      const float z = zs[r.base + i], e = expf(z - r.top);
-      const unsigned c = falling(z), tied = __ballot_sync(0xffffffffu, c == cut.code);
-      const bool ok = c < cut.code || (c == cut.code && before + __popc(tied & ((1u << lane) - 1u)) < cut.ties);
-      before += __popc(tied);
-      const u64 w = ok && e >= min_p ? weight(e) : 0;
-      u64 up = w;
+  // the warp whose elements hold it, the weight and the tokens at the cut before them
+  int owner = -1;
+  u64 done = 0;
+  unsigned before = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 x = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o) up += x;
-      }
-      up += done;
-      const unsigned over = __ballot_sync(0xffffffffu, up > at_w);
-      if (over) {
-        if (lane == __ffs(over) - 1) {
-          p.tokens[row] = v0 + r.base + i - head;
-          if (p.probs) p.probs[row] = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(all));
+  for (int q = 0; q < kQ; ++q) {
+    if (32 * q >= ctas * kWarps) break;
+    const unsigned over = __ballot_sync(0xffffffffu, upto[q] > at_w);
+    if (owner < 0 && over) {
+      const int l = __ffs(over) - 1;
+      owner = 32 * q + l;
+      done = __shfl_sync(0xffffffffu, upto[q] - x[q], l);
+      before = __shfl_sync(0xffffffffu, at[q], l);
+    }
+  }
+  if (owner >= 0 && owner / kWarps == rank) {
+    // that CTA's warps take a piece of those elements each
+    r.base = (owner % kWarps) * r.n;
+    const int piece = r.n / kWarps, from = warp * piece;   // a multiple of 4
+    u64 sum = 0;
+    unsigned same = 0;
+    for (int i = from + lane; i < from + piece; i += 32) {
+      const float z = r.z(i), e = expf(z - r.top);
+      const unsigned c = falling(z);
+      same += c == cut.code;
+      if (c < cut.code && e >= min_p) sum += weight(e);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    same = __reduce_add_sync(0xffffffffu, same);
+    if (lane == 0) s.part[warp] = sum, s.part_ties[warp] = same;
+    __syncthreads();
+    const unsigned t = lane < kWarps ? s.part_ties[lane] : 0;
+    unsigned at1 = before + scan_up(t) - t;
+    const u64 w1 = (lane < kWarps ? s.part[lane] : 0) + tie_w * (at1 < cut.ties ? min(t, cut.ties - at1) : 0u);
+    const u64 up1 = done + scan_up(w1);
+    const int l = __ffs(__ballot_sync(0xffffffffu, up1 > at_w)) - 1;
+    if (l == warp) {
+      done = __shfl_sync(0xffffffffu, up1 - w1, l);
+      before = __shfl_sync(0xffffffffu, at1, l);
+      for (int i0 = from; i0 < from + piece; i0 += 32) {
+        const int i = i0 + lane;
+        const float z = i < from + piece ? r.z(i) : -INFINITY, e = expf(z - r.top);
+        const unsigned c = falling(z), tied = __ballot_sync(0xffffffffu, c == cut.code);
+        const bool ok = c < cut.code || (c == cut.code && before + __popc(tied & ((1u << lane) - 1u)) < cut.ties);
+        before += __popc(tied);
+        const u64 w = ok && e >= min_p ? weight(e) : 0;
+        const u64 up = done + scan_up(w);
+        const unsigned over = __ballot_sync(0xffffffffu, up > at_w);
+        if (over) {
+          if (lane == __ffs(over) - 1) {
+            p.tokens[row] = v0 + r.base + i - head;
+            if (p.probs) p.probs[row] = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(all));
+          }
+          break;
         }
-        break;
+        done = __shfl_sync(0xffffffffu, up, 31);
       }
-      done = __shfl_sync(0xffffffffu, up, 31);
     }
   }
   cluster_sync();   // peers may still read this CTA's sums
 }
 
-int cluster_of(int V) {
-  // a cluster reads its row faster the more CTAs share it, and pays for each exchange
-  int c = 1;
-  while (c < kRowCtas && V > 4096 * c) c *= 2;
-  return c;
+constexpr int kMost[2] = {kSliceBytes / 4, kSliceBytes / 2};   // elements of a CTA: fp32, bf16
+
+struct Shape {
+  int ctas, threads, slice;
+};
+
+// Many rows: as few CTAs a row as hold it, of 1024 threads, since each exchange costs all of them.  Few rows:
+// up to eight, of 512 threads (two fit an SM), while each has a few thousand elements.  Measured, all limits
+// on: 200 rows of 128,007 bf16 logits 120 us with two of 1024, 191 us with eight of 512; one row of 32,000
+// 23 us and 18 us.
+Shape shape_of(const SampleParams& p, int sms) {
+  Shape h;
+  h.ctas = 1;
+  const int most = kMost[p.bf16 ? 1 : 0] / 4096 * 4096;
+  while (h.ctas < kRowCtas && p.V + 7 > most * h.ctas) h.ctas *= 2;
+  while (h.ctas < kRowCtas && p.V > 4096 * h.ctas && static_cast<long long>(p.T) * h.ctas <= sms) h.ctas *= 2;
+  h.threads = static_cast<long long>(p.T) * h.ctas <= 2 * sms ? 512 : 1024;
+  const int unit = h.threads / 32 * 128;
+  h.slice = ((p.V + 7 + h.ctas - 1) / h.ctas + unit - 1) / unit * unit;
+  return h;
 }
 
-}  // namespace
-
-int sample_max_vocab() { return kRowCtas * kMaxSlice - 8; }
-
-cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st) {
-  (void)sms;
-  const int ctas = cluster_of(p.V);
-  const int slice = ((p.V + 7 + ctas - 1) / ctas + kUnit - 1) / kUnit * kUnit;
-  const size_t smem = sizeof(Shared) + static_cast<size_t>(slice) * 4;
-  static std::atomic<unsigned long long> allowed[2];
-  auto kernel = p.bf16 ? q4_sample_kernel<true> : q4_sample_kernel<false>;
-  cudaError_t e = allow_smem(kernel, sizeof(Shared) + static_cast<size_t>(kMaxSlice) * 4, allowed[p.bf16 ? 1 : 0]);
+template <bool BF16, int THREADS>
+cudaError_t launch(const SampleParams& p, const Shape& h, cudaStream_t st) {
+  static std::atomic<unsigned long long> allowed;
+  cudaError_t e = allow_smem(q4_sample_kernel<BF16, THREADS>, sizeof(Shared) + kSliceBytes, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.T) * ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.T) * h.ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(h.slice) * (BF16 ? 2 : 4);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = h.ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, p, ctas, slice);
+  return cudaLaunchKernelEx(&cfg, q4_sample_kernel<BF16, THREADS>, p, h.ctas, h.slice);
+}
+
+}  // namespace
+
+int sample_max_vocab() { return kRowCtas * (kMost[0] / 4096 * 4096) - 8; }
+
+cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st) {
+  const Shape h = shape_of(p, sms);
+  if (p.bf16) return h.threads == 512 ? launch<true, 512>(p, h, st) : launch<true, 1024>(p, h, st);
+  return h.threads == 512 ? launch<false, 512>(p, h, st) : launch<false, 1024>(p, h, st);
 }
 
 }  // namespace q4
