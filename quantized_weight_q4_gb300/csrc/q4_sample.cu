@@ -88,17 +88,19 @@ __device__ __forceinline__ unsigned falling(float z) {
   return (b & 0x80000000u) ? b : ~(b | 0x80000000u);
 }
 
-// floor(e * 2^40) of 0 <= e <= 1.
+// floor(e * 2^40) of 0 <= e <= 1: e's 24 significant bits at the top of a 64-bit word, shifted down.
 __device__ __forceinline__ u64 weight(float e) {
-  const unsigned b = __float_as_uint(e);
-  const int down = 127 - static_cast<int>(b >> 23);       // e = 1.m * 2^-down
-  if (down > 40) return 0;
-  return (static_cast<u64>((b & 0x7fffffu) | 0x800000u) << 17) >> down;
+  const unsigned b = __float_as_uint(e), m = b << 8 | 0x80000000u, s = 150u - (b >> 23);   // m 2^32 >> s
+  unsigned lo, hi;
+  asm("shf.r.clamp.b32 %0, %1, %2, %3;" : "=r"(lo) : "r"(0u), "r"(m), "r"(s));             // s >= 32: m
+  asm("shr.u32 %0, %1, %2;" : "=r"(lo) : "r"(lo), "r"(max(s, 32u) - 32u));                 // 0 from 64 on
+  asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(m), "r"(s));
+  return static_cast<u64>(hi) << 32 | lo;
 }
 
+// z: a NaN becomes -inf (the maximum drops it), an infinity the largest number.
 __device__ __forceinline__ float clean(float l, float inv) {
-  const float z = __fmul_rn(l, inv);
-  return z != z ? -INFINITY : fminf(z, FLT_MAX);
+  return fminf(fmaxf(__fmul_rn(l, inv), -INFINITY), FLT_MAX);
 }
 
 // Inclusive sum over the warp's lanes.
@@ -203,23 +205,13 @@ __device__ __forceinline__ void scan_bins(Shared& s, Bins<kPer>& b) {
   b.before_w = pw + sw - w;
 }
 
-// Adds bin_of(z, d) (negative: none) of the elements within kZero of the largest
-// into this CTA's bins, and gives every CTA the sums over all.
-template <typename R, typename F>
-__device__ __forceinline__ void histogram(Shared& s, const R& r, bool want_n, bool want_w, F bin_of, Bins<R::kPer>& out) {
-  constexpr int kThreads = R::kThreads, kPer = R::kPer;
-  clear_bins<kThreads>(s);
-  __syncthreads();
-  each(r, [&](float z) {
-    const float d = r.top - z;
-    if (!(d < kZero)) return;
-    const int b = bin_of(z, d);
-    if (b >= 0) add_bin(s, b, want_w ? weight(expf(-d)) : 0, want_n, want_w);
-  });
+// The sums of all CTAs' bins in every CTA, after each has filled its own.
+template <typename R>
+__device__ __forceinline__ void add_up(Shared& s, const R& r, Bins<R::kPer>& out) {
   cluster_sync();
   // each CTA adds its share of the bins and hands the sums to all
   const int share = kBins / r.ctas;
-  for (int i = threadIdx.x; i < share; i += kThreads) {
+  for (int i = threadIdx.x; i < share; i += R::kThreads) {
     const int b = r.rank * share + i;
     unsigned n = 0;
     u64 w = 0;
@@ -239,8 +231,59 @@ __device__ __forceinline__ void histogram(Shared& s, const R& r, bool want_n, bo
   }
   cluster_sync();
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) out.n[j] = s.n[kPer * threadIdx.x + j], out.w[j] = s.w[kPer * threadIdx.x + j];
+  for (int j = 0; j < R::kPer; ++j)
+    out.n[j] = s.n[R::kPer * threadIdx.x + j], out.w[j] = s.w[R::kPer * threadIdx.x + j];
   scan_bins(s, out);
+}
+
+// Counts and weights of bin_of(z, d) (negative: none) over the elements within
+// kZero of the largest, over all CTAs.
+template <typename R, typename F>
+__device__ __forceinline__ void histogram(Shared& s, const R& r, bool want_n, bool want_w, F bin_of,
+                                          Bins<R::kPer>& out) {
+  clear_bins<R::kThreads>(s);
+  __syncthreads();
+  each(r, [&](float z) {
+    const float d = r.top - z;
+    if (!(d < kZero)) return;
+    const int b = bin_of(z, d);
+    if (b >= 0) add_bin(s, b, want_w ? weight(expf(-d)) : 0, want_n, want_w);
+  });
+  add_up(s, r, out);
+}
+
+// The coarse bins' weights; those further than kNear from the largest together
+// in the last bin: most tokens lie there and a cut seldom does, so their
+// weights are added in registers instead of in shared memory.
+constexpr float kNear = 14.0f;
+template <typename R>
+__device__ __forceinline__ void near_histogram(Shared& s, const R& r, Bins<R::kPer>& out) {
+  clear_bins<R::kThreads>(s);
+  __syncthreads();
+  u64 rest = 0;
+  each(r, [&](float z) {
+    const float d = r.top - z;
+    const u64 w = weight(expf(-d));
+    if (d < kNear)
+      add_bin(s, coarse(d), w, false, true);
+    else
+      rest += w;
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+  if ((threadIdx.x & 31) == 0) add_bin(s, kBins - 1, rest, false, true);
+  add_up(s, r, out);
+}
+
+// Counts of the threads' largest z (theirs: its maximum): the k-th largest of
+// those is at most the k-th largest of all, and not much below it.
+template <typename R>
+__device__ __forceinline__ void top_histogram(Shared& s, const R& r, float theirs, Bins<R::kPer>& out) {
+  clear_bins<R::kThreads>(s);
+  __syncthreads();
+  const float d = r.top - theirs;
+  if (d < kZero) add_bin(s, coarse(d), 0, true, false);
+  add_up(s, r, out);
 }
 
 // The bin in which the count (or weight) reaches `target` (1 or more, at most
@@ -495,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
   __syncwarp();   // a warp reads its own elements only
   float top = -INFINITY;
   each(r, [&](float z) { top = fmaxf(top, z); });
+  const float theirs = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s.red[warp] = top;
@@ -517,68 +561,77 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
   }
 
   Cut cut;
-  cut.code = 0xffffffffu;    // everything: no code is as large
-  cut.ties = 0;
+  cut.code = 0;
+  cut.ties = 0;              // no cut: everything is kept
   const bool by_k = k > 0 && k < p.V, by_p = top_p < 1.0f;
   if (k == 1) {
     cut.code = falling(top);
     cut.ties = 1;
   } else if (by_k || by_p) {
-    // a short top-k: every token that may be kept goes on the list, and no weights are needed before
-    const bool short_k = by_k && k <= kListK;
     Bins<R::kPer> bins;
-    histogram(s, r, by_k, by_p && !short_k, [&](float, float d) { return coarse(d); }, bins);
-    unsigned all_n = 0;
-    u64 all_w = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) all_n += s.scan_n[i], all_w += s.scan_w[i];
-    const bool cut_k = by_k && static_cast<unsigned>(k) < all_n;
     bool done = false;
-    if (short_k) {
-      // the bins down to the one that holds the k-th token (all, where there are no more than k)
-      find_bin(s, bins, false, cut_k ? static_cast<u64>(k) : static_cast<u64>(all_n));
-      const int last = s.bin;
-      if (s.before_n + s.bin_n <= kList) {
-        const int n = static_cast<int>(gather_list(s, r, [&](float d) { return coarse(d) <= last; }));
-        cut = cut_of_list<R>(s, n, r.top, false, static_cast<u64>(min(static_cast<unsigned>(k), all_n)), 0);
+    if (by_k && k <= kListK) {
+      // a short top-k: every token that may be kept goes on the list
+      top_histogram(s, r, theirs, bins);
+      unsigned tops = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) tops += s.scan_n[i];
+      int last = kBins;                     // fewer threads than k have an element: all elements
+      if (tops >= static_cast<unsigned>(k)) {
+        find_bin(s, bins, false, static_cast<u64>(k));
+        last = s.bin;
+      }
+      const int n = static_cast<int>(gather_list(s, r, [&](float d) { return coarse(d) <= last; }));
+      if (n <= kList) {
+        cut = cut_of_list<R>(s, n, r.top, false, static_cast<u64>(min(k, n)), 0);
         if (by_p) {
-          const u64 want = part_of(top_p, cut.weight);
-          if (want < cut.weight) cut = cut_of_list<R>(s, n, r.top, true, want, 0);
+          const u64 part = part_of(top_p, cut.weight);
+          if (part < cut.weight) cut = cut_of_list<R>(s, n, r.top, true, part, 0);
         }
         done = true;
-      } else if (by_p) {
-        // many equal logits at the k-th: from the start, with weights
-        histogram(s, r, true, true, [&](float, float d) { return coarse(d); }, bins);
-        all_w = 0;
-        for (int i = 0; i < kWarps; ++i) all_w += s.scan_w[i];
       }
     }
     if (!done) {
+      // by the bins of all elements; a top-k needs their counts, a top-p their weights
+      const auto bin_of = [&](float, float d) { return coarse(d); };
+      if (by_k) histogram(s, r, true, by_p, bin_of, bins);
+      else near_histogram(s, r, bins);
+      unsigned all_n = 0;
+      u64 all_w = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) all_n += s.scan_n[i], all_w += s.scan_w[i];
+      const bool cut_k = by_k && static_cast<unsigned>(k) < all_n;
       if (cut_k) {
         find_bin(s, bins, false, static_cast<u64>(k));
         cut = cut_in_bin(s, r, false, static_cast<u64>(k));
         all_w = cut.weight;
       }
       if (by_p) {
-        const u64 want = part_of(top_p, all_w);
-        if (want < all_w) {
+        const u64 part = part_of(top_p, all_w);
+        if (part < all_w) {
           if (cut_k) cluster_sync();   // peers have read this CTA's part of the last list
-          find_bin(s, bins, true, want);
-          cut = cut_in_bin(s, r, true, want);
+          find_bin(s, bins, true, part);
+          if (!by_k && s.bin == kBins - 1) {   // a flat row: its cut lies among the far ones
+            histogram(s, r, false, true, bin_of, bins);
+            find_bin(s, bins, true, part);
+          }
+          cut = cut_in_bin(s, r, true, part);
         }
       }
     }
   }
 
   // kept weight of each warp's elements before the cut, and tokens at it
+  const bool has_cut = cut.ties > 0;
+  const float cut_z = has_cut ? of_code(cut.code) : -INFINITY;
   u64 sum = 0;
   unsigned same = 0;
   each(r, [&](float z) {
-    const unsigned c = falling(z);
-    same += c == cut.code;
-    if (c < cut.code) {
+    if (z > cut_z) {
       const float e = expf(z - r.top);
       if (e >= min_p) sum += weight(e);
+    } else {
+      same += z == cut_z;
     }
   });
 #pragma unroll
@@ -587,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
   if (lane == 0) s.sums[warp] = sum, s.ties[warp] = same;
   cluster_sync();
   // every warp: the weight before its own elements, and all of it
-  const float tie_e = expf(of_code(cut.code) - r.top);
-  const u64 tie_w = cut.ties > 0 && tie_e >= min_p ? weight(tie_e) : 0;
+  const float tie_e = expf(cut_z - r.top);
+  const u64 tie_w = has_cut && tie_e >= min_p ? weight(tie_e) : 0;
   // weight of warp i's kept tokens, i = 32 q + lane, and of all before; tokens at the cut before it
   constexpr int kQ = kRowCtas * kWarps / 32;
   u64 x[kQ], upto[kQ], all = 0;
@@ -636,9 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
     unsigned same = 0;
     for (int i = from + lane; i < from + piece; i += 32) {
       const float z = r.z(i), e = expf(z - r.top);
-      const unsigned c = falling(z);
-      same += c == cut.code;
-      if (c < cut.code && e >= min_p) sum += weight(e);
+      same += z == cut_z;
+      if (z > cut_z && e >= min_p) sum += weight(e);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -656,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
       for (int i0 = from; i0 < from + piece; i0 += 32) {
         const int i = i0 + lane;
         const float z = i < from + piece ? r.z(i) : -INFINITY, e = expf(z - r.top);
-        const unsigned c = falling(z), tied = __ballot_sync(0xffffffffu, c == cut.code);
-        const bool ok = c < cut.code || (c == cut.code && before + __popc(tied & ((1u << lane) - 1u)) < cut.ties);
+        const unsigned tied = __ballot_sync(0xffffffffu, z == cut_z);
+        const bool ok = z > cut_z || (z == cut_z && before + __popc(tied & ((1u << lane) - 1u)) < cut.ties);
         before += __popc(tied);
         const u64 w = ok && e >= min_p ? weight(e) : 0;
         const u64 up = done + scan_up(w);
