@@ -104,7 +104,7 @@ struct SampleParams {
   const float* top_p;
   const float* min_p;
 };
-cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st);
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t st);
 // Longest row launch_sample takes.
 int sample_max_vocab();
 

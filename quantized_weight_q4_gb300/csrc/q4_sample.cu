@@ -28,11 +28,14 @@
 namespace q4 {
 namespace {
 
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
+constexpr int kPer = kBins / kThreads;       // bins a thread
+constexpr int kUnit = kWarps * 128;          // a CTA's elements are a multiple of this
 constexpr float kPerNat = 36.0f;             // coarse bins: 1024 / 36 = 28.4 > 40 ln 2 nats
 constexpr int kList = 2048;                  // longest list
 constexpr int kListK = 1024;                 // top-k up to which all kept tokens go on the list
-constexpr int kMaxWarps = 32;
 constexpr int kRowCtas = 8;
 constexpr int kSliceBytes = 160 * 1024;      // most elements a CTA holds
 typedef unsigned long long u64;
@@ -49,14 +52,14 @@ struct alignas(16) Shared {
   };
   unsigned list_n;
   unsigned lo, hi;                           // range of codes
-  unsigned scan_n[kMaxWarps];
-  u64 scan_w[kMaxWarps];
+  unsigned scan_n[kWarps];
+  u64 scan_w[kWarps];
   float top[kRowCtas];
-  u64 sums[kMaxWarps];                          // weight before the cut, and tokens at it, of each warp's elements
-  unsigned ties[kMaxWarps];
-  float red[kMaxWarps];
-  u64 part[kMaxWarps];                       // the same of the pieces of one warp's elements
-  unsigned part_ties[kMaxWarps];
+  u64 sums[kWarps];                          // weight before the cut, and tokens at it, of each warp's elements
+  unsigned ties[kWarps];
+  float red[kWarps];
+  u64 part[kWarps];                       // the same of the pieces of one warp's elements
+  unsigned part_ties[kWarps];
   // the bin that a search found
   int bin;
   unsigned bin_n, before_n;
@@ -120,9 +123,8 @@ __device__ __forceinline__ float of_code(unsigned c) {
 }
 
 // The CTA's elements as they came (fp32 or bf16; -inf where there are none).
-template <bool BF16, int THREADS>
+template <bool BF16>
 struct Row {
-  static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kPer = kBins / THREADS;
   const void* x;
   int base, n;           // this warp's: base + i, i < n (n a multiple of 128)
   float inv;             // 1 / temperature
@@ -170,22 +172,19 @@ __device__ __forceinline__ void add_bin(Shared& s, int b, u64 w, bool want_n, bo
   }
 }
 
-template <int kThreads>
 __device__ __forceinline__ void clear_bins(Shared& s) {
   uint4* h = reinterpret_cast<uint4*>(&s.hist[0][0]);
   for (int i = threadIdx.x; i < 3 * kBins / 4; i += kThreads) h[i] = make_uint4(0, 0, 0, 0);
 }
 
 // A thread's bins: counts and weights, and those of all bins before.
-template <int kPer>
 struct Bins {
   unsigned n[kPer], before_n;
   u64 w[kPer], before_w;
 };
 
 // The sums before each thread's bins; the block's totals are the sums of s.scan_*.
-template <int kPer>
-__device__ __forceinline__ void scan_bins(Shared& s, Bins<kPer>& b) {
+__device__ __forceinline__ void scan_bins(Shared& s, Bins& b) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned n = 0;
   u64 w = 0;
@@ -207,11 +206,11 @@ __device__ __forceinline__ void scan_bins(Shared& s, Bins<kPer>& b) {
 
 // The sums of all CTAs' bins in every CTA, after each has filled its own.
 template <typename R>
-__device__ __forceinline__ void add_up(Shared& s, const R& r, Bins<R::kPer>& out) {
+__device__ __forceinline__ void add_up(Shared& s, const R& r, Bins& out) {
   cluster_sync();
   // each CTA adds its share of the bins and hands the sums to all
   const int share = kBins / r.ctas;
-  for (int i = threadIdx.x; i < share; i += R::kThreads) {
+  for (int i = threadIdx.x; i < share; i += kThreads) {
     const int b = r.rank * share + i;
     unsigned n = 0;
     u64 w = 0;
@@ -231,8 +230,8 @@ __device__ __forceinline__ void add_up(Shared& s, const R& r, Bins<R::kPer>& out
   }
   cluster_sync();
 #pragma unroll
-  for (int j = 0; j < R::kPer; ++j)
-    out.n[j] = s.n[R::kPer * threadIdx.x + j], out.w[j] = s.w[R::kPer * threadIdx.x + j];
+  for (int j = 0; j < kPer; ++j)
+    out.n[j] = s.n[kPer * threadIdx.x + j], out.w[j] = s.w[kPer * threadIdx.x + j];
   scan_bins(s, out);
 }
 
@@ -240,8 +239,8 @@ __device__ __forceinline__ void add_up(Shared& s, const R& r, Bins<R::kPer>& out
 // kZero of the largest, over all CTAs.
 template <typename R, typename F>
 __device__ __forceinline__ void histogram(Shared& s, const R& r, bool want_n, bool want_w, F bin_of,
-                                          Bins<R::kPer>& out) {
-  clear_bins<R::kThreads>(s);
+                                          Bins& out) {
+  clear_bins(s);
   __syncthreads();
   each(r, [&](float z) {
     const float d = r.top - z;
@@ -257,8 +256,8 @@ __device__ __forceinline__ void histogram(Shared& s, const R& r, bool want_n, bo
 // weights are added in registers instead of in shared memory.
 constexpr float kNear = 14.0f;
 template <typename R>
-__device__ __forceinline__ void near_histogram(Shared& s, const R& r, Bins<R::kPer>& out) {
-  clear_bins<R::kThreads>(s);
+__device__ __forceinline__ void near_histogram(Shared& s, const R& r, Bins& out) {
+  clear_bins(s);
   __syncthreads();
   u64 rest = 0;
   each(r, [&](float z) {
@@ -278,8 +277,8 @@ __device__ __forceinline__ void near_histogram(Shared& s, const R& r, Bins<R::kP
 // Counts of the threads' largest z (theirs: its maximum): the k-th largest of
 // those is at most the k-th largest of all, and not much below it.
 template <typename R>
-__device__ __forceinline__ void top_histogram(Shared& s, const R& r, float theirs, Bins<R::kPer>& out) {
-  clear_bins<R::kThreads>(s);
+__device__ __forceinline__ void top_histogram(Shared& s, const R& r, float theirs, Bins& out) {
+  clear_bins(s);
   __syncthreads();
   const float d = r.top - theirs;
   if (d < kZero) add_bin(s, coarse(d), 0, true, false);
@@ -288,8 +287,7 @@ __device__ __forceinline__ void top_histogram(Shared& s, const R& r, float their
 
 // The bin in which the count (or weight) reaches `target` (1 or more, at most
 // the total), into s.bin and what stands beside it.
-template <int kPer>
-__device__ __forceinline__ void find_bin(Shared& s, const Bins<kPer>& b, bool by_weight, u64 target) {
+__device__ __forceinline__ void find_bin(Shared& s, const Bins& b, bool by_weight, u64 target) {
   unsigned n = b.before_n;
   u64 w = b.before_w;
   __syncthreads();   // the last search's result has been read
@@ -338,9 +336,7 @@ __device__ __forceinline__ void code_range(Shared& s, F f) {
 
 // The cut of the list in s.all at which its count (or weight) reaches target.
 // before_w: weight of the tokens that come before the list.
-template <typename R>
 __device__ __forceinline__ Cut cut_of_list(Shared& s, int n, float top, bool by_weight, u64 target, u64 before_w) {
-  constexpr int kThreads = R::kThreads, kPer = R::kPer;
   unsigned code[kList / kThreads];
   u64 w[kList / kThreads];
 #pragma unroll
@@ -358,14 +354,14 @@ __device__ __forceinline__ Cut cut_of_list(Shared& s, int n, float top, bool by_
   u64 left = target, done_w = before_w;
   while (lo < hi) {
     const int shift = max(0, 32 - __clz(hi - lo) - 10);
-    clear_bins<kThreads>(s);
+    clear_bins(s);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kList / kThreads; ++k)
       if (static_cast<int>(threadIdx.x) + k * kThreads < n && code[k] >= lo && code[k] <= hi)
         add_bin(s, static_cast<int>((code[k] - lo) >> shift), w[k], true, true);
     __syncthreads();
-    Bins<kPer> b;
+    Bins b;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = kPer * threadIdx.x + j;
@@ -417,7 +413,7 @@ __device__ __forceinline__ unsigned gather_list(Shared& s, const R& r, F want) {
   }
   const unsigned n = __shfl_sync(0xffffffffu, up, r.ctas - 1);
   if (n <= kList) {
-    const int warp = threadIdx.x >> 5, c = warp % r.ctas, share = R::kWarps / r.ctas;   // share: warps a part
+    const int warp = threadIdx.x >> 5, c = warp % r.ctas, share = kWarps / r.ctas;   // share: warps a part
     const unsigned here = __shfl_sync(0xffffffffu, mine, c), at = __shfl_sync(0xffffffffu, up, c) - here;
     for (unsigned i = (warp / r.ctas) * 32 + lane; i < here; i += 32 * share)
       s.all[at + i] = ld_peer_u32(peer_addr(&s.list[i], c));
@@ -430,7 +426,7 @@ __device__ __forceinline__ unsigned gather_list(Shared& s, const R& r, F want) {
 // count (or weight) is to be reached in it.  Finer bins, then bins of the code.
 template <typename R>
 __device__ __noinline__ Cut cut_by_bins(Shared& s, const R& r, int b1, bool by_weight, u64 left, u64 done_w) {
-  Bins<R::kPer> bins;
+  Bins bins;
   histogram(s, r, true, true, [&](float z, float d) { return coarse(d) == b1 ? fine(d, b1) : -1; }, bins);
   find_bin(s, bins, by_weight, left);
   const int b2 = s.bin;
@@ -471,7 +467,7 @@ __device__ __forceinline__ Cut cut_in_bin(Shared& s, const R& r, bool by_weight,
   const int b = s.bin;
   const u64 done_w = s.before_w, left = target - (by_weight ? s.before_w : s.before_n);
   const unsigned n = gather_list(s, r, [&](float d) { return coarse(d) == b; });
-  if (n <= kList) return cut_of_list<R>(s, static_cast<int>(n), r.top, by_weight, left, done_w);
+  if (n <= kList) return cut_of_list(s, static_cast<int>(n), r.top, by_weight, left, done_w);
   return cut_by_bins(s, r, b, by_weight, left, done_w);
 }
 
@@ -481,11 +477,9 @@ __device__ __forceinline__ u64 part_of(float top_p, u64 all) {
   return want >= 1.0 ? static_cast<u64>(want) : 1ull;
 }
 
-template <bool BF16, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(const __grid_constant__ SampleParams p, int ctas,
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_constant__ SampleParams p, int ctas,
                                                              int slice) {
-  using R = Row<BF16, kThreads>;
-  constexpr int kWarps = R::kWarps;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   uint8_t* xs = smem + sizeof(Shared);
@@ -507,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
   const int head = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / kSize);
   base -= head * kSize;
   const int v0 = rank * slice;
-  R r;
+  Row<BF16> r;
   r.x = xs;
   r.n = slice / kWarps;
   r.base = warp * r.n;
@@ -568,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
     cut.code = falling(top);
     cut.ties = 1;
   } else if (by_k || by_p) {
-    Bins<R::kPer> bins;
+    Bins bins;
     bool done = false;
     if (by_k && k <= kListK) {
       // a short top-k: every token that may be kept goes on the list
@@ -583,10 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
       }
       const int n = static_cast<int>(gather_list(s, r, [&](float d) { return coarse(d) <= last; }));
       if (n <= kList) {
-        cut = cut_of_list<R>(s, n, r.top, false, static_cast<u64>(min(k, n)), 0);
+        cut = cut_of_list(s, n, r.top, false, static_cast<u64>(min(k, n)), 0);
         if (by_p) {
           const u64 part = part_of(top_p, cut.weight);
-          if (part < cut.weight) cut = cut_of_list<R>(s, n, r.top, true, part, 0);
+          if (part < cut.weight) cut = cut_of_list(s, n, r.top, true, part, 0);
         }
         done = true;
       }
@@ -728,57 +722,47 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) q4_sample_kernel(co
   cluster_sync();   // peers may still read this CTA's sums
 }
 
-constexpr int kMost[2] = {kSliceBytes / 4, kSliceBytes / 2};   // elements of a CTA: fp32, bf16
-
-struct Shape {
-  int ctas, threads, slice;
-};
-
-// Many rows: as few CTAs a row as hold it, of 1024 threads, since each exchange costs all of them.  Few rows:
-// up to eight, of 512 threads (two fit an SM), while each has a few thousand elements.  Measured, all limits
-// on: 200 rows of 128,007 bf16 logits 120 us with two of 1024, 191 us with eight of 512; one row of 32,000
-// 23 us and 18 us.
-Shape shape_of(const SampleParams& p, int sms) {
-  Shape h;
-  h.ctas = 1;
-  const int most = kMost[p.bf16 ? 1 : 0] / 4096 * 4096;
-  while (h.ctas < kRowCtas && p.V + 7 > most * h.ctas) h.ctas *= 2;
-  while (h.ctas < kRowCtas && p.V > 4096 * h.ctas && static_cast<long long>(p.T) * h.ctas <= sms) h.ctas *= 2;
-  h.threads = static_cast<long long>(p.T) * h.ctas <= 2 * sms ? 512 : 1024;
-  const int unit = h.threads / 32 * 128;
-  h.slice = ((p.V + 7 + h.ctas - 1) / h.ctas + unit - 1) / unit * unit;
-  return h;
+// CTAs of a row: up to four while each has 4096 elements or more, and eight where four would leave room for
+// only one CTA an SM (80 KB of elements each).  Measured with 512 threads each, all limits on: 200 rows of
+// 128,007 bf16 logits 90 us with four, 154 us with eight (clusters of eight seldom fit the SMs that are
+// free); one row of 32,000 logits 23 / 18 / 16.6 / 17 us with one / two / four / eight; 64 rows of 32,000
+// 25 / 24 / 22 / 44 us.
+int ctas_of(const SampleParams& p) {
+  const int size = p.bf16 ? 2 : 4;
+  int c = 1;
+  while (c < 4 && p.V > 4096 * c) c *= 2;
+  while (c < kRowCtas && static_cast<long long>(p.V) * size > 80 * 1024 * c) c *= 2;
+  return c;
 }
 
-template <bool BF16, int THREADS>
-cudaError_t launch(const SampleParams& p, const Shape& h, cudaStream_t st) {
+template <bool BF16>
+cudaError_t launch(const SampleParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> allowed;
-  cudaError_t e = allow_smem(q4_sample_kernel<BF16, THREADS>, sizeof(Shared) + kSliceBytes, allowed);
+  cudaError_t e = allow_smem(q4_sample_kernel<BF16>, sizeof(Shared) + kSliceBytes, allowed);
   if (e != cudaSuccess) return e;
+  const int ctas = ctas_of(p), slice = ((p.V + 7 + ctas - 1) / ctas + kUnit - 1) / kUnit * kUnit;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.T) * h.ctas);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(h.slice) * (BF16 ? 2 : 4);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.T) * ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared) + static_cast<size_t>(slice) * (BF16 ? 2 : 4);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = h.ctas;
+  attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, q4_sample_kernel<BF16, THREADS>, p, h.ctas, h.slice);
+  return cudaLaunchKernelEx(&cfg, q4_sample_kernel<BF16>, p, ctas, slice);
 }
 
 }  // namespace
 
-int sample_max_vocab() { return kRowCtas * (kMost[0] / 4096 * 4096) - 8; }
+int sample_max_vocab() { return kRowCtas * (kSliceBytes / 4 / kUnit * kUnit) - 8; }
 
-cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t st) {
-  const Shape h = shape_of(p, sms);
-  if (p.bf16) return h.threads == 512 ? launch<true, 512>(p, h, st) : launch<true, 1024>(p, h, st);
-  return h.threads == 512 ? launch<false, 512>(p, h, st) : launch<false, 1024>(p, h, st);
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
+  return p.bf16 ? launch<true>(p, st) : launch<false>(p, st);
 }
 
 }  // namespace q4

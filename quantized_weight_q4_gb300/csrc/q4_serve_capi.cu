@@ -204,16 +204,12 @@ int q4_sample(int32_t* tokens, float* probs, const void* logits, int logits_dtyp
   if (!aligned(logits, size_of(logits_dtype)) || !aligned(tokens, 4) || !aligned(probs, 4) || !aligned(u, 4) ||
       !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4))
     return Q4_ERR_ALIGN;
-  int sms = 0;
-  unsigned* status = nullptr;
-  const int rc = q4::device_info(&sms, &status);
-  if (rc != Q4_OK) return rc;
   q4::SampleParams p = {};
   p.tokens = tokens, p.probs = probs;
   p.logits = logits, p.stride = stride, p.bf16 = logits_dtype == Q4_BF16;
   p.T = static_cast<int>(T), p.V = static_cast<int>(V);
   p.u = u, p.temperature = temperature, p.top_k = top_k, p.top_p = top_p, p.min_p = min_p;
-  return status_of(q4::launch_sample(p, sms, static_cast<cudaStream_t>(stream)));
+  return status_of(q4::launch_sample(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
