@@ -506,7 +506,7 @@ Q4_API size_t q4_moe_block_workspace_size(int64_t T, int64_t topk, int64_t E, in
  * heads <= 1024.  Buffers 16-byte aligned.  A new cache needs no
  * initialisation: only blocks of appended tokens are read.
  *
- * The calls below take a batch of B sequences (B <= 4096), T <= 2^24 packed rows:
+ * The calls below take a batch of B sequences (B <= 2048), T <= 2^24 packed rows:
  *   page_table  int32 [B][table_stride]: the page that holds tokens
  *               i * page_tokens .. of a sequence.  A page outside [0, pages)
  *               records Q4_DEVERR_INDEX; its tokens are not written, and not

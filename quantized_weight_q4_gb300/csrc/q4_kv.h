@@ -9,7 +9,7 @@
 namespace q4 {
 
 constexpr int kKvBlock = 16;        // tokens that share a scale
-constexpr int kKvMaxSeqs = 4096;    // sequences of one call
+constexpr int kKvMaxSeqs = 2048;    // sequences of one call
 
 // A cache: codes int8 [pages][heads][page][dim], scales fp32 [pages][heads][page / 16].
 struct KvView {

@@ -8,12 +8,13 @@
 //
 // * The unit of work is a block: 16 tokens of one kv head, for one tile of
 //   query rows (the queries that share the head: token-major, up to 16 rows).
-//   The units of all sequences, heads and tiles form one line, which is cut
-//   into equal ranges, one per CTA, whatever the sequences' lengths.  A CTA
+//   The units of all sequences, heads and tiles form one line (with some empty
+//   ones before each (sequence, tile, head), for what starting one costs), which
+//   is cut into equal ranges, one per CTA, whatever the sequences' lengths.  A CTA
 //   whose range ends inside a (sequence, head, tile) writes its share of the
 //   sum (with the maximum and the weights' sum) to the workspace; the last of
 //   the CTAs that share it adds the shares in order.
-// * Inside a CTA each warp streams blocks of its own (every eighth) through
+// * Inside a CTA each warp streams blocks of its own (every twelfth) through
 //   its own ring of TMA stages, so that no warp waits for another until the
 //   shares of the warps are added.
 // * Codes are integers up to 127, exact in fp16, as are bf16 queries scaled
@@ -35,16 +36,19 @@
 namespace q4 {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                 // rows of an MMA tile
-constexpr int kStages = 4;                // ring stages of a warp, one block each
-// Weight of the softmax reference (the largest score so far) with the value scale the sums are relative to;
-// a larger value scale counts up to kMoreScale of it before the reference moves.  As large as fp16 allows
-// (2^13 * 4 < 65504).  fp16 holds a weight to 11 bits down to 2^-27 of the reference and to within 2^-38 of
-// it below that.  With SPLIT the second term is the rest times kRestScale, so that the two hold 22 bits, and
-// within 2^-49: small weights can matter together, where the largest weight's value is near zero.
-constexpr float kUnitWeight = 8192.0f;
+constexpr int kStages = 3;                // ring stages of a warp, one block each
+constexpr int kSegCost = 16;              // what starting and ending a (sequence, head, tile) costs, in units
+// Weight of the softmax reference with the value scale the sums are relative to.  The reference moves once a
+// score exceeds it by 2^kLazy, or a value scale kMoreScale times (moving costs a multiplication of every sum);
+// the weight is as large as that leaves of fp16's range (2^9 * 2^4 * 4 < 65504).  fp16 holds a weight to 11
+// bits down to 2^-23 of the reference and to within 2^-34 of it below that.  With SPLIT the second term is
+// the rest times kRestScale, so that the two hold 22 bits, and within 2^-45: small weights can matter
+// together, where the largest weight's value is near zero.
+constexpr float kUnitWeight = 512.0f;
+constexpr float kLazy = 4.0f;
 constexpr float kMoreScale = 4.0f;
 constexpr float kRestScale = 2048.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -53,6 +57,7 @@ struct AttnParams {
   CUtensorMap kmap, vmap;                 // codes: u8 [pages][heads * page][dim], boxes of 16 rows
   KvAttnCall a;
   int group;                              // query heads of one kv head
+  int page_log2;
   int max_rows;                           // sequences with more query rows are left to the prompt form
   unsigned* tickets;                      // [grid], zero
   float* part;                            // [grid][2][kRows][dim + 2] shares
@@ -114,8 +119,7 @@ __device__ __forceinline__ void copy4_async(void* dst, const void* src, uint64_t
 struct Segment {
   int b, h, tile;
   int c0, nq, len;         // packed row of the first new token, new tokens, cached tokens
-  int blk0;                // first block any query of the sequence sees
-  int lo, hi;              // this CTA's blocks (absolute)
+  int lo, hi;              // this CTA's blocks (maybe none)
   long long first, last;   // units of the whole (sequence, tile, head): [first, last)
 };
 
@@ -128,7 +132,7 @@ struct Stage {
 template <int D>
 constexpr size_t smem_bytes(int B) {
   return 1024 + static_cast<size_t>(kWarps) * kStages * Stage<D>::kBytes +   // rings
-         static_cast<size_t>(kWarps) * kRows * D * 4 +                        // the warps' sums
+         static_cast<size_t>(kWarps / 2) * kRows * D * 4 +                    // the warps' sums, two after one another
          static_cast<size_t>(kWarps) * kRows * 2 * 4 + kRows * 2 * 4 +        // their maxima and weights
          static_cast<size_t>(kWarps) * kStages * (8 + 8) +                    // scales, barriers
          static_cast<size_t>(B + 1) * 8 + 64;
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* s_o = reinterpret_cast<float*>(ring + kWarps * kStages * kStageBytes);   // [warp][row][D]
-  float* s_m = s_o + kWarps * kRows * D;                                           // [warp][row]
+  float* s_m = s_o + kWarps / 2 * kRows * D;                                           // [warp][row]
   float* s_l = s_m + kWarps * kRows;
   float* s_tot = s_l + kWarps * kRows;                                             // [row]: maximum, weights' sum
   float* s_scale = s_tot + 2 * kRows;                                              // [warp][stage][2]
@@ -162,14 +166,16 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   __shared__ int s_fail;
   __shared__ int s_last;
   __shared__ long long s_warp[kWarps];
+  __shared__ int s_pairs;                       // (sequence, tile, head)s; more than the grid: any such number
 
   const KvAttnCall& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;        // MMA row (and column group), thread in group
   if (lane == 0)
     for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp * kStages + i], 3);
-  if (tid == 0) s_fail = 0;
+  if (tid == 0) s_fail = 0, s_pairs = 0;
   fence_barrier_init();
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
 
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   const int B = a.b.B;
   {
     const int per = (B + kThreads - 1) / kThreads;
-    long long sum = 0;
+    long long sum = 0, pairs = 0;
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b < B) {
@@ -186,9 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         seq_blocks(a, nq, a.b.kv_len[b], lo, hi);
         const long long rows = static_cast<long long>(nq) * p.group;
         const long long tiles = nq > 0 && rows <= p.max_rows ? (rows + kTileRows - 1) / kTileRows : 0;
-        const long long n = tiles * a.c.heads * (hi - lo);
+        const long long n = tiles * a.c.heads * (hi - lo + kSegCost);
         s_cum[b + 1] = sum + n;
         sum += n;
+        pairs += tiles * a.c.heads;
       }
     }
     long long up = sum;
@@ -198,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       if (lane >= o) up += x;
     }
     if (lane == 31) s_warp[warp] = up;
+    if (pairs > 0) atomicAdd(&s_pairs, static_cast<int>(min(pairs, 1LL << 18)));   // kThreads of them fit an int
     __syncthreads();
     long long before = up - sum;
     for (int i = 0; i < warp; ++i) before += s_warp[i];
@@ -209,8 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     __syncthreads();
   }
   const long long units = s_cum[B];
-  // a CTA for each eight units (one for each warp), as far as there are CTAs
-  const long long ctas = max(1LL, min(static_cast<long long>(gridDim.x), (units + kWarps - 1) / kWarps));
+  // as many CTAs as have a block for every warp; where there is one for each (sequence, tile, head), the same
+  // number for each, so that those of one length begin with a CTA's range
+  const long long pairs = max(1, s_pairs);
+  long long ctas = min(static_cast<long long>(gridDim.x), units / (kWarps + kSegCost));
+  ctas = pairs <= gridDim.x ? pairs * max(1LL, ctas / pairs) : max(1LL, ctas);
   auto range_of = [&](long long cta) { return units * cta / ctas; };
   // the CTA whose range holds unit u
   auto owner_of = [&](long long u) { return ((u + 1) * ctas - 1) / units; };
@@ -229,15 +240,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     s.len = a.b.kv_len[lo];
     int b0, b1;
     seq_blocks(a, s.nq, s.len, b0, b1);
-    const int nb = b1 - b0;
+    const int nb = b1 - b0 + kSegCost;
     const long long in = u - s_cum[lo], pair = in / nb;
-    s.blk0 = b0;
     s.h = static_cast<int>(pair % a.c.heads);
     s.tile = static_cast<int>(pair / a.c.heads);
     s.first = s_cum[lo] + pair * nb;
     s.last = s.first + nb;
-    s.lo = b0 + static_cast<int>(u - s.first);
-    s.hi = b0 + static_cast<int>(min(s.last, u1) - s.first);
+    s.lo = b0 + max(0, static_cast<int>(u - s.first) - kSegCost);
+    s.hi = b0 + max(0, static_cast<int>(min(s.last, u1) - s.first) - kSegCost);
   };
 
   // ---- the warp's stream of blocks: the producer runs kStages blocks ahead ----
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   int pblk = 0, ppage = -1;                     // its next block, that block's page
   bool more = u0 < u1;
   auto page_of = [&](int b, int blk) -> int {
-    const long long pi = static_cast<long long>(blk) * kKvBlock / a.c.page;
+    const int pi = blk >> (p.page_log2 - 4);
     return pi < a.b.table_stride ? __ldg(a.b.table + b * a.b.table_stride + pi) : -1;
   };
   // to the warp's next block at or after pblk, through the segments
@@ -431,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
 #pragma unroll
         for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
           m[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
-          move |= m[e] > mref[e];               // also from -inf
+          move |= m[e] > mref[e] + kLazy;       // also from -inf
         }
         if (__any_sync(0xffffffffu, move)) {
           const float vnew = fmaxf(vref, vs);
@@ -512,29 +522,40 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       }
     }
     __syncthreads();
-    float top[2];
+    float top[2], fo[2];
 #pragma unroll
     for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
       top[e] = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top[e] = fmaxf(top[e], s_m[w * kRows + g + 8 * e]);
-      const float f = (mref[e] > -INFINITY ? ex2(mref[e] - top[e]) : 0.f) * (vref / kUnitWeight);
-      float* to_row = s_o + (warp * kRows + g + 8 * e) * D + c * (D / 4);
-      // element of accumulator column 2c (2c + 1) of tile i: (D / 4) c + i (+ D / 8)
+      fo[e] = (mref[e] > -INFINITY ? ex2(mref[e] - top[e]) : 0.f) * (vref / kUnitWeight);
+    }
+    // half of the warps store their sums, then the others add theirs
+    auto hand_in = [&](bool add) {
 #pragma unroll
-      for (int i = 0; i < NT; i += 4)
+      for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+        float* to_row = s_o + (warp % (kWarps / 2) * kRows + g + 8 * e) * D + c * (D / 4);
+        // element of accumulator column 2c (2c + 1) of tile i: (D / 4) c + i (+ D / 8)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float4 y;
-          if (SPLIT)
-            y = make_float4(fmaf(o[i][2 + k], 1.0f / kRestScale, o[i][k]) * f,
-                            fmaf(o[i + 1][2 + k], 1.0f / kRestScale, o[i + 1][k]) * f,
-                            fmaf(o[i + 2][2 + k], 1.0f / kRestScale, o[i + 2][k]) * f,
-                            fmaf(o[i + 3][2 + k], 1.0f / kRestScale, o[i + 3][k]) * f);
-          else
-            y = make_float4(o[i][2 * e + k] * f, o[i + 1][2 * e + k] * f, o[i + 2][2 * e + k] * f, o[i + 3][2 * e + k] * f);
-          *reinterpret_cast<float4*>(to_row + k * (D / 8) + i) = y;
-        }
+        for (int i = 0; i < NT; i += 4)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float y[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              y[x] = (SPLIT ? fmaf(o[i + x][2 + k], 1.0f / kRestScale, o[i + x][k]) : o[i + x][2 * e + k]) * fo[e];
+            float4* to = reinterpret_cast<float4*>(to_row + k * (D / 8) + i);
+            float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (add) old = *to;
+            *to = make_float4(old.x + y[0], old.y + y[1], old.z + y[2], old.w + y[3]);
+          }
+      }
+    };
+    if (warp < kWarps / 2) hand_in(false);
+    __syncthreads();
+    if (warp >= kWarps / 2) hand_in(true);
+#pragma unroll
+    for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
       if (warp == 0 && c == 0) {
         float l = 0.f;
         for (int w = 0; w < kWarps; ++w) {
@@ -562,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       const int r = i / D, d = i % D;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += s_o[(w * kRows + r) * D + d];
+      for (int w = 0; w < kWarps / 2; ++w) v += s_o[(w * kRows + r) * D + d];
       if (whole) {
         const float l = s_tot[kRows + r];
         store(r, d, l > 0.f ? v / l : l == 0.f ? 0.f : l);   // no key: zeros; a NaN stays
@@ -676,6 +697,8 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   if (!encode_codes(&p.kmap, a.c.k, a.c) || !encode_codes(&p.vmap, a.c.v, a.c)) return cudaErrorUnknown;
   p.a = a;
   p.group = a.Hq / a.c.heads;
+  p.page_log2 = 4;
+  while ((1 << p.page_log2) < a.c.page) ++p.page_log2;
   p.max_rows = max_rows;
   p.tickets = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
