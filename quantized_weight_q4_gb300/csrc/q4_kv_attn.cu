@@ -103,9 +103,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+// Two 16 x 16 byte matrices, transposed: lane l gives the address of row l % 16 of matrix l / 16; register
+// 2 m + x gets rows 4 (l % 4) .. + 3 of column 8 x + l / 4 of matrix m.
+__device__ __forceinline__ uint4 ldmatrix_t8(uint32_t a) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 
@@ -132,7 +135,7 @@ struct Stage {
 template <int D>
 constexpr size_t smem_bytes(int B) {
   return 1024 + static_cast<size_t>(kWarps) * kStages * Stage<D>::kBytes +   // rings
-         static_cast<size_t>(kWarps / 2) * kRows * D * 4 +                    // the warps' sums, two after one another
+         static_cast<size_t>(kWarps / 2) * kRows * (D + 8) * 4 +                    // the warps' sums, two after one another
          static_cast<size_t>(kWarps) * kRows * 2 * 4 + kRows * 2 * 4 +        // their maxima and weights
          static_cast<size_t>(kWarps) * kStages * (8 + 8) +                    // scales, barriers
          static_cast<size_t>(B + 1) * 8 + 64;
@@ -154,10 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   constexpr int KT = D / 16;                    // k steps of q . k
   constexpr int NT = D / 8;                     // column tiles of p . v
   constexpr int kStageBytes = Stage<D>::kBytes;
+  constexpr int kORow = D + 8;                  // floats between rows of the warps' sums: other banks
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* s_o = reinterpret_cast<float*>(ring + kWarps * kStages * kStageBytes);   // [warp][row][D]
-  float* s_m = s_o + kWarps / 2 * kRows * D;                                           // [warp][row]
+  float* s_o = reinterpret_cast<float*>(ring + kWarps * kStages * kStageBytes);   // [warp][row][kORow]
+  float* s_m = s_o + kWarps / 2 * kRows * kORow;                                           // [warp][row]
   float* s_l = s_m + kWarps * kRows;
   float* s_tot = s_l + kWarps * kRows;                                             // [row]: maximum, weights' sum
   float* s_scale = s_tot + 2 * kRows;                                              // [warp][stage][2]
@@ -388,11 +392,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       const long long f = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
       from[e] = f < -1 ? -1 : static_cast<int>(f);
     }
+    // blocks that every row of the tile sees whole (rows are in the order of their positions)
+    int inner_lo, inner_hi;
+    {
+      const int p0 = s.len - s.nq + row0 / p.group, p1 = s.len - s.nq + (row0 + rows - 1) / p.group;
+      inner_hi = (p0 < 0 ? 0 : a.causal ? p0 + 1 : s.len) / kKvBlock;
+      inner_lo = a.window > 0 && p1 >= a.window ? static_cast<int>((p1 - a.window + kKvBlock) / kKvBlock) : 0;
+    }
     float o[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float mref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
-    float vref = 0.f;                           // value scale the sums are relative to
+    float vref = 0.f, vinv = 0.f;               // value scale the sums are relative to, kUnitWeight over it
 
     for (int blk = s.lo + warp; blk < s.hi; blk += kWarps) {
       const int st = taken % kStages;
@@ -401,14 +412,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       const float ks = my_scale[2 * st], vs = my_scale[2 * st + 1];
       const uint32_t kb = smem_u32(my_ring + st * kStageBytes), vb = kb + Stage<D>::kCodes;
       if (ks >= 0.f) {
-        // scores: tile j holds tokens 8 j .. 8 j + 7 of the block
+        // scores: column n of tile j is token 4 (n / 2) + 2 j + n % 2 of the block, so that the thread's four
+        // columns are the tokens 4 c .. 4 c + 3
         float sc[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int r = 8 * j + g;
+          const int r = 4 * (g >> 1) + 2 * j + (g & 1);
           uint32_t w[D / 16];
           if (D == 128) {
-            const uint4 x = lds128(kb + r * 128 + (((2 * c) ^ g) << 4)), y = lds128(kb + r * 128 + (((2 * c + 1) ^ g) << 4));
+            const uint4 x = lds128(kb + r * 128 + (((2 * c) ^ (r & 7)) << 4)), y = lds128(kb + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4));
             w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
             w[D / 16 - 4] = y.x, w[D / 16 - 3] = y.y, w[D / 16 - 2] = y.z, w[D / 16 - 1] = y.w;
           } else {
@@ -426,15 +438,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         // scaled scores of the thread's rows, four columns each
         float x[2][4];
 #pragma unroll
-        for (int e = 0; e < (SPLIT ? 1 : 2); ++e)
+        for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+          const float f = ks * rowf[e];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int i = 0; i < 4; ++i)
+            x[e][i] = (SPLIT ? sc[i >> 1][i & 1] + sc[i >> 1][2 + (i & 1)] : sc[i >> 1][2 * e + (i & 1)]) * f;
+        }
+        if (blk < inner_lo || blk >= inner_hi) {   // some row does not see all of the block
+          const int pos = blk * kKvBlock + 4 * c;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float v = SPLIT ? sc[j][i] + sc[j][2 + i] : sc[j][2 * e + i];
-              const int pos = blk * kKvBlock + 8 * j + 2 * c + i;
-              x[e][2 * j + i] = pos > from[e] && pos <= to[e] ? v * (ks * rowf[e]) : -INFINITY;
-            }
+          for (int e = 0; e < (SPLIT ? 1 : 2); ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (pos + i <= from[e] || pos + i > to[e]) x[e][i] = -INFINITY;
+        }
         // the references move rarely: by a row's scores, or by the value scale
         float m[2];
         bool move = vs > kMoreScale * vref;
@@ -447,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
           const float vnew = fmaxf(vref, vs);
           const float vf = vnew > 0.f ? vref / vnew : 1.f;
           vref = vnew;
+          vinv = vref > 0.f ? kUnitWeight / vref : 0.f;
           float f[2];
 #pragma unroll
           for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
@@ -463,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
           for (int i = 0; i < NT; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
         }
         // weights, and weights times the value scale as fp16
-        const float vk = vref > 0.f ? kUnitWeight * (vs / vref) : 0.f;
+        const float vk = vs * vinv;
         uint32_t pf[4];
 #pragma unroll
         for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
@@ -482,30 +500,19 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
             pf[3] = pack_rest(w[2], w[3], pf[2], kRestScale);
           }
         }
-        // values: the thread's tokens are 2c, 2c + 1, 2c + 8, 2c + 9, its elements (D / 8) g + 0 .. D / 8 - 1
-        uint32_t v[4][D / 32];
+        // values: column n of tile i is element 8 i + n
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-          if (D == 128) {
-            const uint4 y = lds128(vb + r * 128 + ((g ^ (r & 7)) << 4));
-            v[i][0] = y.x, v[i][1] = y.y, v[i][D / 32 - 2] = y.z, v[i][D / 32 - 1] = y.w;
-          } else {
-            const uint2 y = lds64(vb + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
-            v[i][0] = y.x, v[i][1] = y.y;
+        for (int m = 0; m < D / 32; ++m) {
+          const int r = lane & 15, chunk = 2 * m + (lane >> 4);
+          const uint4 v = ldmatrix_t8(vb + r * D + ((D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) << 4));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            widen4(w[i], b0, b1);
+            mma(o[4 * m + i], pf, b0, b1);
           }
         }
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t sel = half ? 0x7362u : 0x5140u;
-            uint32_t a0, a1, b0, b1;              // pairs of tokens at elements 4 q + 2 half and + 1
-            widen4(__byte_perm(v[0][q], v[1][q], sel), a0, a1);
-            widen4(__byte_perm(v[2][q], v[3][q], sel), b0, b1);
-            mma(o[4 * q + 2 * half], pf, a0, b0);
-            mma(o[4 * q + 2 * half + 1], pf, a1, b1);
-          }
       }
       __syncwarp();
       produce();
@@ -534,21 +541,19 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     auto hand_in = [&](bool add) {
 #pragma unroll
       for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
-        float* to_row = s_o + (warp % (kWarps / 2) * kRows + g + 8 * e) * D + c * (D / 4);
-        // element of accumulator column 2c (2c + 1) of tile i: (D / 4) c + i (+ D / 8)
+        float* to_row = s_o + (warp % (kWarps / 2) * kRows + g + 8 * e) * kORow + 2 * c;
 #pragma unroll
-        for (int i = 0; i < NT; i += 4)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float y[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              y[x] = (SPLIT ? fmaf(o[i + x][2 + k], 1.0f / kRestScale, o[i + x][k]) : o[i + x][2 * e + k]) * fo[e];
-            float4* to = reinterpret_cast<float4*>(to_row + k * (D / 8) + i);
-            float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (add) old = *to;
-            *to = make_float4(old.x + y[0], old.y + y[1], old.z + y[2], old.w + y[3]);
+        for (int i = 0; i < NT; ++i) {
+          float2 y;
+          y.x = (SPLIT ? fmaf(o[i][2], 1.0f / kRestScale, o[i][0]) : o[i][2 * e]) * fo[e];
+          y.y = (SPLIT ? fmaf(o[i][3], 1.0f / kRestScale, o[i][1]) : o[i][2 * e + 1]) * fo[e];
+          float2* to = reinterpret_cast<float2*>(to_row + 8 * i);
+          if (add) {
+            const float2 old = *to;
+            y.x += old.x, y.y += old.y;
           }
+          *to = y;
+        }
       }
     };
     if (warp < kWarps / 2) hand_in(false);
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       const int r = i / D, d = i % D;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps / 2; ++w) v += s_o[(w * kRows + r) * D + d];
+      for (int w = 0; w < kWarps / 2; ++w) v += s_o[(w * kRows + r) * kORow + d];
       if (whole) {
         const float l = s_tot[kRows + r];
         store(r, d, l > 0.f ? v / l : l == 0.f ? 0.f : l);   // no key: zeros; a NaN stays
