@@ -82,10 +82,16 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The first product of a sum.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -110,12 +116,6 @@ __device__ __forceinline__ uint4 ldmatrix_t8(uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
-}
-
-// 4-byte asynchronous copy to shared memory, counted by the barrier's thread arrivals.
-__device__ __forceinline__ void copy4_async(void* dst, const void* src, uint64_t* bar) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // One (sequence, row tile, kv head) of the line of units, and the blocks a CTA takes of it.
@@ -151,12 +151,14 @@ __device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len,
   }
 }
 
+// SPLIT: the 16 rows of an MMA tile are 8 query rows in two fp16 terms each; else 16 in one term.
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kTileRows = SPLIT ? 8 : 16;     // query rows of a tile
+  constexpr int kE = SPLIT ? 1 : 2;             // query rows of a thread
+  constexpr int kTileRows = 8 * kE;             // query rows of a tile
   constexpr int KT = D / 16;                    // k steps of q . k
   constexpr int NT = D / 8;                     // column tiles of p . v
-  constexpr int kStageBytes = Stage<D>::kBytes;
+  constexpr uint32_t kStageBytes = Stage<D>::kBytes;
   constexpr int kORow = D + 8;                  // floats between rows of the warps' sums: other banks
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;        // MMA row (and column group), thread in group
   if (lane == 0)
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp * kStages + i], 3);
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp * kStages + i], 4);   // two lanes: their bytes, their scales
   if (tid == 0) s_fail = 0, s_pairs = 0;
   fence_barrier_init();
   __syncthreads();
@@ -255,64 +257,54 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   };
 
   // ---- the warp's stream of blocks: the producer runs kStages blocks ahead ----
-  uint8_t* my_ring = ring + warp * kStages * kStageBytes;
-  float* my_scale = s_scale + warp * kStages * 2;
-  uint64_t* my_bar = s_bar + warp * kStages;
+  const uint32_t my_ring = smem_u32(ring + warp * kStages * kStageBytes);
+  const uint32_t my_bar = smem_u32(s_bar + warp * kStages), my_scale = smem_u32(s_scale + warp * kStages * 2);
+  const int sub_mask = (a.c.page >> 4) - 1, sub_log2 = p.page_log2 - 4;   // blocks of a page
   Segment ps = {};                              // the producer's segment
   long long pu = u0;                            // its first unit
   int pblk = 0, ppage = -1;                     // its next block, that block's page
   bool more = u0 < u1;
-  auto page_of = [&](int b, int blk) -> int {
-    const int pi = blk >> (p.page_log2 - 4);
-    return pi < a.b.table_stride ? __ldg(a.b.table + b * a.b.table_stride + pi) : -1;
-  };
   // to the warp's next block at or after pblk, through the segments
   auto settle = [&]() {
-    while (more && pblk >= ps.hi) {
-      pu = min(ps.last, u1);
-      more = pu < u1;
-      if (more) {
-        locate(pu, ps);
-        pblk = ps.lo + warp;
+    while (pblk >= ps.hi) {
+      if (pu >= u1) {
+        more = false;
+        return;
       }
+      locate(pu, ps);
+      pu = ps.last;
+      pblk = ps.lo + warp;
     }
-    if (more) ppage = page_of(ps.b, pblk);
+    const int pi = pblk >> sub_log2;
+    ppage = pi < a.b.table_stride ? __ldg(a.b.table + ps.b * a.b.table_stride + pi) : -1;
   };
-  if (more) {
-    locate(pu, ps);
-    pblk = ps.lo + warp;
-    settle();
-  }
-  unsigned issued = 0;
+  if (more) settle();
+  uint32_t put = 0;                             // stage to fill next, in units of 8 bytes (a barrier, two scales)
   auto produce = [&]() {
     if (!more) return;
-    const int st = issued % kStages;
-    uint64_t* bar = my_bar + st;
-    float* sc = my_scale + 2 * st;
-    const bool ok = ppage >= 0 && ppage < a.c.pages && pblk * kKvBlock < ps.len;
-    if (ok) {
-      const int off = (pblk * kKvBlock) & (a.c.page - 1);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, kStageBytes);
-        uint8_t* dst = my_ring + st * kStageBytes;
-        tma_load_3d(dst, &p.kmap, 0, ps.h * a.c.page + off, ppage, bar);
-        tma_load_3d(dst + Stage<D>::kCodes, &p.vmap, 0, ps.h * a.c.page + off, ppage, bar);
-      }
+    const uint32_t bar = my_bar + put, sc = my_scale + put;
+    if (ppage >= 0 && ppage < a.c.pages && pblk * kKvBlock < ps.len) {
+      const int row = (ps.h << p.page_log2) + ((pblk & sub_mask) << 4);
       if (lane < 2) {
-        const long long at = ((static_cast<long long>(ppage) * a.c.heads + ps.h) * a.c.page + off) / kKvBlock;
-        copy4_async(sc + lane, (lane ? a.c.vs : a.c.ks) + at, bar);
+        // lane 0 the keys, lane 1 the values, each with its scale
+        const uint32_t dst = my_ring + put * (kStageBytes / 8) + lane * Stage<D>::kCodes;
+        const float* scale = (lane ? a.c.vs : a.c.ks) + ((static_cast<long long>(ppage) * a.c.heads + ps.h) << sub_log2) + (pblk & sub_mask);
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(Stage<D>::kCodes) : "memory");
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(lane ? &p.vmap : &p.kmap)), "r"(0), "r"(row), "r"(ppage), "r"(bar)
+            : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sc + 4 * lane), "l"(scale) : "memory");
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       }
-    } else {                                    // no such page, or a sequence without tokens: a block nobody sees
-      if (lane == 0) {
-        if (pblk * kKvBlock < ps.len) atomicOr(a.err, kDevErrIndex);
-        sc[0] = -1.0f;
-        sc[1] = 0.0f;
-        mbar_arrive(bar);
-        mbar_arrive(bar);
-        mbar_arrive(bar);
-      }
+    } else if (lane < 2) {                      // no such page, or a sequence without tokens: a block nobody sees
+      if (lane == 0 && pblk * kKvBlock < ps.len) atomicOr(a.err, kDevErrIndex);
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + 4 * lane), "f"(-1.0f) : "memory");
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
     }
-    ++issued;
+    put = put == 8 * (kStages - 1) ? 0 : put + 8;
     pblk += kWarps;
     settle();
   };
@@ -320,31 +312,35 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   for (int i = 0; i < kStages; ++i) produce();
 
   // ---- segments ----
-  unsigned taken = 0;
+  uint32_t take = 0, phase = 0;                 // stage to read next, as `put`; its barrier's parity
+  // swizzled places of the thread's keys in a stage (plus 2 rows, the bit that differs, for the second tile) and
+  // of its values (the chunk's bits change with the matrices)
+  const int krow = 4 * (g >> 1) + (g & 1), vrow = lane & 15;
+  const uint32_t koff = krow * D + ((D == 128 ? (2 * c) ^ (krow & 7) : c ^ ((krow >> 1) & 3)) << 4);
+  const uint32_t voff = Stage<D>::kCodes + vrow * D + (((lane >> 4) ^ (D == 128 ? vrow & 7 : (vrow >> 1) & 3)) << 4);
+  constexpr uint32_t kTileBit = D == 128 ? 32 : 16;   // two rows on: row bits 1 and up turn this chunk bit
   long long u = u0;
   while (u < u1) {
     Segment s;
     locate(u, s);
     const int row0 = s.tile * kTileRows;        // first row of the tile: row = token * group + head in group
     const int rows = min(kTileRows, s.nq * p.group - row0);
-    // this thread's two rows (SPLIT: one, whose rest fills the second)
-    int qpos[2];                                // their positions, -1: no row
+    // this thread's rows
+    int qpos[2] = {-1, -1};                     // their positions, -1: no row
     long long qoff[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = SPLIT ? g : g + 8 * e;
+    for (int e = 0; e < kE; ++e) {
+      const int r = g + 8 * e;
       const int j = (row0 + r) / p.group;
-      qpos[e] = r < rows ? s.len - s.nq + j : -1;
+      if (r < rows && s.c0 >= 0 && s.c0 + j < a.b.T) qpos[e] = s.len - s.nq + j;
       qoff[e] = (static_cast<long long>(s.c0) + j) * a.q_stride + (s.h * p.group + (row0 + r) % p.group) * D;
-      if (s.c0 < 0 || s.c0 + j >= a.b.T) qpos[e] = -1;
     }
     // queries as fp16, scaled by a power of two per row into fp16's range: the thread's
     // elements of a row are (D / 4) c + 0 .. D / 4 - 1, four for each k step
     uint32_t qf[KT][4];
     float rowf[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (SPLIT && e == 1) { rowf[1] = rowf[0]; break; }
+    for (int e = 0; e < kE; ++e) {
       float x[D / 4];
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
@@ -387,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     // range of positions each row sees: (from, to]
     int from[2], to[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kE; ++e) {
       to[e] = qpos[e] < 0 ? -1 : a.causal ? qpos[e] : s.len - 1;
       const long long f = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
       from[e] = f < -1 ? -1 : static_cast<int>(f);
@@ -406,39 +402,47 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     float vref = 0.f, vinv = 0.f;               // value scale the sums are relative to, kUnitWeight over it
 
     for (int blk = s.lo + warp; blk < s.hi; blk += kWarps) {
-      const int st = taken % kStages;
-      bounded_wait(my_bar + st, (taken / kStages) & 1, &s_fail, a.err);
-      ++taken;
-      const float ks = my_scale[2 * st], vs = my_scale[2 * st + 1];
-      const uint32_t kb = smem_u32(my_ring + st * kStageBytes), vb = kb + Stage<D>::kCodes;
+      const uint32_t kb = my_ring + take * (kStageBytes / 8);
+      bounded_wait(s_bar + warp * kStages + (take >> 3), phase, &s_fail, a.err);
+      float ks, vs;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(my_scale + take));
+      if (take == 8 * (kStages - 1)) take = 0, phase ^= 1;
+      else take += 8;
       if (ks >= 0.f) {
         // scores: column n of tile j is token 4 (n / 2) + 2 j + n % 2 of the block, so that the thread's four
         // columns are the tokens 4 c .. 4 c + 3
-        float sc[2][4];
+        uint32_t kw[2][D / 16];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 4 * (g >> 1) + 2 * j + (g & 1);
-          uint32_t w[D / 16];
-          if (D == 128) {
-            const uint4 x = lds128(kb + r * 128 + (((2 * c) ^ (r & 7)) << 4)), y = lds128(kb + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4));
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-            w[D / 16 - 4] = y.x, w[D / 16 - 3] = y.y, w[D / 16 - 2] = y.z, w[D / 16 - 1] = y.w;
-          } else {
-            const uint4 x = lds128(kb + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            const uint4 x = lds128(kb + 2 * j * D + (koff ^ (i << 4) ^ (j * kTileBit)));
+            kw[j][4 * i] = x.x, kw[j][4 * i + 1] = x.y, kw[j][4 * i + 2] = x.z, kw[j][4 * i + 3] = x.w;
           }
-          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+        float sc[2][4], sd[2][4];   // even and odd k steps: twice as many sums that do not wait for one another
 #pragma unroll
-          for (int t = 0; t < KT; ++t) {
+        for (int t = 0; t < KT; t += 2)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
             uint32_t b0, b1;
-            widen4(w[t], b0, b1);
-            mma(sc[j], qf[t], b0, b1);
+            widen4(kw[j][t], b0, b1);
+            if (t == 0) mma_first(sc[j], qf[t], b0, b1); else mma(sc[j], qf[t], b0, b1);
+            widen4(kw[j][t + 1], b0, b1);
+            if (t == 0) mma_first(sd[j], qf[t + 1], b0, b1); else mma(sd[j], qf[t + 1], b0, b1);
           }
+        uint4 vw[D / 32];
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+          vw[m] = ldmatrix_t8(kb + (voff ^ (m << 5)));
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[j][i] += sd[j][i];
         // scaled scores of the thread's rows, four columns each
         float x[2][4];
 #pragma unroll
-        for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+        for (int e = 0; e < kE; ++e) {
           const float f = ks * rowf[e];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         if (blk < inner_lo || blk >= inner_hi) {   // some row does not see all of the block
           const int pos = blk * kKvBlock + 4 * c;
 #pragma unroll
-          for (int e = 0; e < (SPLIT ? 1 : 2); ++e)
+          for (int e = 0; e < kE; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (pos + i <= from[e] || pos + i > to[e]) x[e][i] = -INFINITY;
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         float m[2];
         bool move = vs > kMoreScale * vref;
 #pragma unroll
-        for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+        for (int e = 0; e < kE; ++e) {
           m[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
           move |= m[e] > mref[e] + kLazy;       // also from -inf
         }
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
           vinv = vref > 0.f ? kUnitWeight / vref : 0.f;
           float f[2];
 #pragma unroll
-          for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+          for (int e = 0; e < kE; ++e) {
             m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
             m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
             m[e] = fmaxf(m[e], mref[e]);
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         const float vk = vs * vinv;
         uint32_t pf[4];
 #pragma unroll
-        for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+        for (int e = 0; e < kE; ++e) {
           const float ref = mref[e] > -INFINITY ? mref[e] : 0.f;
           float w[4];
 #pragma unroll
@@ -503,9 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         // values: column n of tile i is element 8 i + n
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
-          const int r = lane & 15, chunk = 2 * m + (lane >> 4);
-          const uint4 v = ldmatrix_t8(vb + r * D + ((D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) << 4));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w[4] = {vw[m].x, vw[m].y, vw[m].z, vw[m].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t b0, b1;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
 
     // ---- the warps' shares ----
 #pragma unroll
-    for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+    for (int e = 0; e < kE; ++e) {
       lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], 1);
       lsum[e] += __shfl_xor_sync(0xffffffffu, lsum[e], 2);
       if (c == 0) {
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     __syncthreads();
     float top[2], fo[2];
 #pragma unroll
-    for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+    for (int e = 0; e < kE; ++e) {
       top[e] = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top[e] = fmaxf(top[e], s_m[w * kRows + g + 8 * e]);
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     // half of the warps store their sums, then the others add theirs
     auto hand_in = [&](bool add) {
 #pragma unroll
-      for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+      for (int e = 0; e < kE; ++e) {
         float* to_row = s_o + (warp % (kWarps / 2) * kRows + g + 8 * e) * kORow + 2 * c;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     __syncthreads();
     if (warp >= kWarps / 2) hand_in(true);
 #pragma unroll
-    for (int e = 0; e < (SPLIT ? 1 : 2); ++e) {
+    for (int e = 0; e < kE; ++e) {
       if (warp == 0 && c == 0) {
         float l = 0.f;
         for (int w = 0; w < kWarps; ++w) {
@@ -707,9 +709,10 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   p.max_rows = max_rows;
   p.tickets = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
-  // one launch for each, a CTA per SM.  fp32 in or out needs both halves of the tile; bf16 takes them too
-  // while eight rows are enough
-  const bool split = !a.q_bf16 || !a.out_bf16 || std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows) <= 8;
+  // fp32 in or out needs two terms; bf16 takes them too while eight rows are enough (a thread then has one row's
+  // softmax instead of two)
+  const bool split = !a.q_bf16 || !a.out_bf16 ||
+                     std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows) <= 8;
   if (a.c.dim == 128) return split ? launch<128, true>(p, sms, st) : launch<128, false>(p, sms, st);
   return split ? launch<64, true>(p, sms, st) : launch<64, false>(p, sms, st);
 }
