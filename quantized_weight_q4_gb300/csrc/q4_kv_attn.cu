@@ -10,13 +10,14 @@
 //   query rows (the queries that share the head: token-major, up to 16 rows).
 //   The units of all sequences, heads and tiles form one line (with some empty
 //   ones before each (sequence, tile, head), for what starting one costs), which
-//   is cut into equal ranges, one per CTA, whatever the sequences' lengths.  A CTA
+//   is cut into equal ranges, whatever the sequences' lengths.  A CTA
 //   whose range ends inside a (sequence, head, tile) writes its share of the
 //   sum (with the maximum and the weights' sum) to the workspace; the last of
 //   the CTAs that share it adds the shares in order.
-// * Inside a CTA each warp streams blocks of its own (every twelfth) through
-//   its own ring of TMA stages, so that no warp waits for another until the
-//   shares of the warps are added.
+//   A range is worked on by a team of warps, a whole CTA or a quarter of one.
+// * Each warp of a team streams blocks of its own (every fourth or sixteenth)
+//   through its own ring of TMA stages, so that no warp waits for another until
+//   the shares of the warps are added.
 // * Codes are integers up to 127, exact in fp16, as are bf16 queries scaled
 //   by a power of two per row; fp32 queries and the softmax weights are split
 //   into two fp16 terms (22 bits) that fill the two halves of the MMA's 16
@@ -36,10 +37,11 @@
 namespace q4 {
 namespace {
 
-constexpr int kWarps = 12;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                 // rows of an MMA tile
-constexpr int kStages = 3;                // ring stages of a warp, one block each
+constexpr int kTeams = 4;                 // teams of a CTA at most
+constexpr int kStages = 2;                // ring stages of a warp, one block each
 constexpr int kSegCost = 16;              // what starting and ending a (sequence, head, tile) costs, in units
 // Weight of the softmax reference with the value scale the sums are relative to.  The reference moves once a
 // score exceeds it by 2^kLazy, or a value scale kMoreScale times (moving costs a multiplication of every sum);
@@ -59,8 +61,8 @@ struct AttnParams {
   int group;                              // query heads of one kv head
   int page_log2;
   int max_rows;                           // sequences with more query rows are left to the prompt form
-  unsigned* tickets;                      // [grid], zero
-  float* part;                            // [grid][2][kRows][dim + 2] shares
+  unsigned* tickets;                      // [ranges], zero
+  float* part;                            // [ranges][2][kRows][dim + 2] shares
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -136,7 +138,7 @@ template <int D>
 constexpr size_t smem_bytes(int B) {
   return 1024 + static_cast<size_t>(kWarps) * kStages * Stage<D>::kBytes +   // rings
          static_cast<size_t>(kWarps / 2) * kRows * (D + 8) * 4 +                    // the warps' sums, two after one another
-         static_cast<size_t>(kWarps) * kRows * 2 * 4 + kRows * 2 * 4 +        // their maxima and weights
+         static_cast<size_t>(kWarps) * kRows * 2 * 4 +                        // their maxima and weights
          static_cast<size_t>(kWarps) * kStages * (8 + 8) +                    // scales, barriers
          static_cast<size_t>(B + 1) * 8 + 64;
 }
@@ -152,7 +154,8 @@ __device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len,
 }
 
 // SPLIT: the 16 rows of an MMA tile are 8 query rows in two fp16 terms each; else 16 in one term.
-template <int D, bool SPLIT>
+// TEAM: warps that take a range of units together.
+template <int D, bool SPLIT, int TEAM>
 __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = SPLIT ? 1 : 2;             // query rows of a thread
   constexpr int kTileRows = 8 * kE;             // query rows of a tile
@@ -165,18 +168,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   float* s_o = reinterpret_cast<float*>(ring + kWarps * kStages * kStageBytes);   // [warp][row][kORow]
   float* s_m = s_o + kWarps / 2 * kRows * kORow;                                           // [warp][row]
   float* s_l = s_m + kWarps * kRows;
-  float* s_tot = s_l + kWarps * kRows;                                             // [row]: maximum, weights' sum
-  float* s_scale = s_tot + 2 * kRows;                                              // [warp][stage][2]
+  float* s_scale = s_l + kWarps * kRows;                                           // [warp][stage][2]
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_scale + kWarps * kStages * 2);
   long long* s_cum = reinterpret_cast<long long*>(s_bar + kWarps * kStages);       // [B + 1] first unit of each sequence
   __shared__ int s_fail;
-  __shared__ int s_last;
+  __shared__ int s_last[kTeams];
+  __shared__ float s_rowf[kTeams][kRows];       // score of a unit product
+  __shared__ float s_tot[kTeams][2][kRows];     // maximum, weights' sum
   __shared__ long long s_warp[kWarps];
   __shared__ int s_pairs;                       // (sequence, tile, head)s; more than the grid: any such number
 
   const KvAttnCall& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;        // MMA row (and column group), thread in group
+  // the warp's team: its number, the warp's place in it, threads; its sums' slots (two warps each), which hold
+  // the queries until the sums are there
+  constexpr int crew = TEAM * 32;
+  const int team = warp / TEAM, mate = warp % TEAM, mine = mate * 32 + lane;
+  float* t_o = s_o + team * TEAM / 2 * kRows * kORow;
+  uint4* s_q = reinterpret_cast<uint4*>(t_o);   // [k step][lane] A operand
+  auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(crew) : "memory"); };
   if (lane == 0)
     for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp * kStages + i], 4);   // two lanes: their bytes, their scales
   if (tid == 0) s_fail = 0, s_pairs = 0;
@@ -223,16 +234,17 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     __syncthreads();
   }
   const long long units = s_cum[B];
-  // as many CTAs as have a block for every warp; where there is one for each (sequence, tile, head), the same
-  // number for each, so that those of one length begin with a CTA's range
-  const long long pairs = max(1, s_pairs);
-  long long ctas = min(static_cast<long long>(gridDim.x), units / (kWarps + kSegCost));
-  ctas = pairs <= gridDim.x ? pairs * max(1LL, ctas / pairs) : max(1LL, ctas);
-  auto range_of = [&](long long cta) { return units * cta / ctas; };
-  // the CTA whose range holds unit u
-  auto owner_of = [&](long long u) { return ((u + 1) * ctas - 1) / units; };
-  const long long u0 = blockIdx.x < ctas ? range_of(blockIdx.x) : units;
-  const long long u1 = blockIdx.x < ctas ? range_of(blockIdx.x + 1) : units;
+  // as many ranges as have a block for every warp of a team; where there is one for each (sequence, tile, head),
+  // the same number for each, so that those of one length begin with a range
+  const long long pairs = max(1, s_pairs), most = static_cast<long long>(gridDim.x) * (kWarps / TEAM);
+  long long ranges = min(most, units / (TEAM + kSegCost));
+  ranges = pairs <= most ? pairs * max(1LL, ranges / pairs) : max(1LL, ranges);
+  auto range_of = [&](long long i) { return units * i / ranges; };
+  // the range that holds unit u
+  auto owner_of = [&](long long u) { return ((u + 1) * ranges - 1) / units; };
+  const long long range = static_cast<long long>(team) * gridDim.x + blockIdx.x;   // few ranges: one to an SM
+  const long long u0 = range < ranges ? range_of(range) : units;
+  const long long u1 = range < ranges ? range_of(range + 1) : units;
 
   auto locate = [&](long long u, Segment& s) {
     int lo = 0, hi = B - 1;                     // the last b with s_cum[b] <= u
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       }
       locate(pu, ps);
       pu = ps.last;
-      pblk = ps.lo + warp;
+      pblk = ps.lo + mate;
     }
     const int pi = pblk >> sub_log2;
     ppage = pi < a.b.table_stride ? __ldg(a.b.table + ps.b * a.b.table_stride + pi) : -1;
@@ -305,13 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
     }
     put = put == 8 * (kStages - 1) ? 0 : put + 8;
-    pblk += kWarps;
+    pblk += TEAM;
     settle();
   };
 #pragma unroll 1
   for (int i = 0; i < kStages; ++i) produce();
 
   // ---- segments ----
+  const uint32_t qb = smem_u32(s_q + lane);
   uint32_t take = 0, phase = 0;                 // stage to read next, as `put`; its barrier's parity
   // swizzled places of the thread's keys in a stage (plus 2 rows, the bit that differs, for the second tile) and
   // of its values (the chunk's bits change with the matrices)
@@ -337,49 +350,57 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     }
     // queries as fp16, scaled by a power of two per row into fp16's range: the thread's
     // elements of a row are (D / 4) c + 0 .. D / 4 - 1, four for each k step
-    uint32_t qf[KT][4];
+    if (mate == 0) {
+      uint32_t qf[KT][4];
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        float x[D / 4];
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+        if (qpos[e] >= 0) {
+          if (a.q_bf16) {
+            const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + qoff[e] + c * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint2 w = __ldg(q + i);
+              x[4 * i] = __uint_as_float(w.x << 16), x[4 * i + 1] = __uint_as_float(w.x & 0xffff0000u);
+              x[4 * i + 2] = __uint_as_float(w.y << 16), x[4 * i + 3] = __uint_as_float(w.y & 0xffff0000u);
+            }
+          } else {
+            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qoff[e] + c * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const float4 w = __ldg(q + i);
+              x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
+            }
+          }
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // 2^(13 - exponent of m), within fp32's normal numbers
+        const int up = m > 0.f ? max(-126, min(126, 13 + 127 - static_cast<int>(__float_as_uint(m) >> 23))) : 0;
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        const float rowf = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale * kLog2e;
+        if (c == 0) s_rowf[team][g + 8 * e] = rowf;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x0 = x[4 * t + 2 * i] * f, x1 = x[4 * t + 2 * i + 1] * f;
+            qf[t][e + 2 * i] = pack_f16(x0, x1);
+            if (SPLIT) qf[t][1 + 2 * i] = pack_rest(x0, x1, qf[t][2 * i], 1.0f);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s_q[t * 32 + lane] = make_uint4(qf[t][0], qf[t][1], qf[t][2], qf[t][3]);
+    }
+    team_sync();
     float rowf[2];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      float x[D / 4];
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
-      if (qpos[e] >= 0) {
-        if (a.q_bf16) {
-          const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + qoff[e] + c * (D / 4));
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint2 w = __ldg(q + i);
-            x[4 * i] = __uint_as_float(w.x << 16), x[4 * i + 1] = __uint_as_float(w.x & 0xffff0000u);
-            x[4 * i + 2] = __uint_as_float(w.y << 16), x[4 * i + 3] = __uint_as_float(w.y & 0xffff0000u);
-          }
-        } else {
-          const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qoff[e] + c * (D / 4));
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const float4 w = __ldg(q + i);
-            x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
-          }
-        }
-      }
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      // 2^(13 - exponent of m), within fp32's normal numbers
-      const int up = m > 0.f ? max(-126, min(126, 13 + 127 - static_cast<int>(__float_as_uint(m) >> 23))) : 0;
-      const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-      rowf[e] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale * kLog2e;
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float x0 = x[4 * t + 2 * i] * f, x1 = x[4 * t + 2 * i + 1] * f;
-          qf[t][e + 2 * i] = pack_f16(x0, x1);
-          if (SPLIT) qf[t][1 + 2 * i] = pack_rest(x0, x1, qf[t][2 * i], 1.0f);
-        }
-    }
+    for (int e = 0; e < kE; ++e) rowf[e] = s_rowf[team][g + 8 * e];
     // range of positions each row sees: (from, to]
     int from[2], to[2];
 #pragma unroll
@@ -401,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     float mref[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
     float vref = 0.f, vinv = 0.f;               // value scale the sums are relative to, kUnitWeight over it
 
-    for (int blk = s.lo + warp; blk < s.hi; blk += kWarps) {
+    for (int blk = s.lo + mate; blk < s.hi; blk += TEAM) {
       const uint32_t kb = my_ring + take * (kStageBytes / 8);
       bounded_wait(s_bar + warp * kStages + (take >> 3), phase, &s_fail, a.err);
       float ks, vs;
@@ -421,15 +442,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
           }
         float sc[2][4], sd[2][4];   // even and odd k steps: twice as many sums that do not wait for one another
 #pragma unroll
-        for (int t = 0; t < KT; t += 2)
+        for (int t = 0; t < KT; t += 2) {
+          const uint4 x0 = lds128(qb + t * 512), x1 = lds128(qb + t * 512 + 512);
+          const uint32_t q0[4] = {x0.x, x0.y, x0.z, x0.w}, q1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             uint32_t b0, b1;
             widen4(kw[j][t], b0, b1);
-            if (t == 0) mma_first(sc[j], qf[t], b0, b1); else mma(sc[j], qf[t], b0, b1);
+            if (t == 0) mma_first(sc[j], q0, b0, b1); else mma(sc[j], q0, b0, b1);
             widen4(kw[j][t + 1], b0, b1);
-            if (t == 0) mma_first(sd[j], qf[t + 1], b0, b1); else mma(sd[j], qf[t + 1], b0, b1);
+            if (t == 0) mma_first(sd[j], q1, b0, b1); else mma(sd[j], q1, b0, b1);
           }
+        }
         uint4 vw[D / 32];
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
@@ -530,20 +554,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         s_l[warp * kRows + g + 8 * e] = lsum[e];
       }
     }
-    __syncthreads();
+    team_sync();
     float top[2], fo[2];
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       top[e] = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top[e] = fmaxf(top[e], s_m[w * kRows + g + 8 * e]);
+      for (int w = 0; w < TEAM; ++w) top[e] = fmaxf(top[e], s_m[(warp - mate + w) * kRows + g + 8 * e]);
       fo[e] = (mref[e] > -INFINITY ? ex2(mref[e] - top[e]) : 0.f) * (vref / kUnitWeight);
     }
     // half of the warps store their sums, then the others add theirs
     auto hand_in = [&](bool add) {
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
-        float* to_row = s_o + (warp % (kWarps / 2) * kRows + g + 8 * e) * kORow + 2 * c;
+        float* to_row = t_o + (mate % (TEAM / 2) * kRows + g + 8 * e) * kORow + 2 * c;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           float2 y;
@@ -558,25 +582,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         }
       }
     };
-    if (warp < kWarps / 2) hand_in(false);
-    __syncthreads();
-    if (warp >= kWarps / 2) hand_in(true);
+    if (mate < TEAM / 2) hand_in(false);
+    team_sync();
+    if (mate >= TEAM / 2) hand_in(true);
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      if (warp == 0 && c == 0) {
+      if (mate == 0 && c == 0) {
         float l = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = s_m[w * kRows + g + 8 * e];
-          l += s_l[w * kRows + g + 8 * e] * (mw > -INFINITY ? ex2(mw - top[e]) : 0.f);
+#pragma unroll
+        for (int w = 0; w < TEAM; ++w) {
+          const float mw = s_m[(warp + w) * kRows + g + 8 * e];
+          l += s_l[(warp + w) * kRows + g + 8 * e] * (mw > -INFINITY ? ex2(mw - top[e]) : 0.f);
         }
-        s_tot[g + 8 * e] = top[e];
-        s_tot[kRows + g + 8 * e] = l;
+        s_tot[team][0][g + 8 * e] = top[e];
+        s_tot[team][1][g + 8 * e] = l;
       }
     }
-    __syncthreads();
+    team_sync();
     const bool whole = s.first >= u0 && s.last <= u1;
     // partial sums: slot 0 for a (sequence, head, tile) that began in an earlier CTA, 1 for one that begins here
-    float* slot = p.part + (static_cast<long long>(blockIdx.x) * 2 + (s.first >= u0 ? 1 : 0)) * kRows * (D + 2);
+    float* slot = p.part + (range * 2 + (s.first >= u0 ? 1 : 0)) * kRows * (D + 2);
     auto store = [&](int r, int d, float v) {
       const int j = (row0 + r) / p.group;
       if (s.c0 < 0 || s.c0 + j >= a.b.T) return;
@@ -586,34 +611,34 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       else
         static_cast<float*>(a.out)[at] = v;
     };
-    for (int i = tid; i < rows * D; i += kThreads) {
+    for (int i = mine; i < rows * D; i += crew) {
       const int r = i / D, d = i % D;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps / 2; ++w) v += s_o[(w * kRows + r) * kORow + d];
+      for (int w = 0; w < TEAM / 2; ++w) v += t_o[(w * kRows + r) * kORow + d];
       if (whole) {
-        const float l = s_tot[kRows + r];
+        const float l = s_tot[team][1][r];
         store(r, d, l > 0.f ? v / l : l == 0.f ? 0.f : l);   // no key: zeros; a NaN stays
       } else {
         slot[r * D + d] = v;
       }
     }
     if (!whole) {
-      if (tid < 2 * kRows) slot[kRows * D + tid] = s_tot[tid];
-      __syncthreads();
+      if (mine < 2 * kRows) slot[kRows * D + mine] = (&s_tot[team][0][0])[mine];
+      team_sync();
       const long long o0 = owner_of(s.first), o1 = owner_of(s.last - 1);
-      if (tid == 0) {
+      if (mine == 0) {
         const unsigned old = atom_add_acq_rel_gpu(p.tickets + o0, 1u);
-        s_last = old == static_cast<unsigned>(o1 - o0);
-        if (s_last) p.tickets[o0] = 0;
+        s_last[team] = old == static_cast<unsigned>(o1 - o0);
+        if (s_last[team]) p.tickets[o0] = 0;
       }
-      __syncthreads();
-      if (s_last) {
+      team_sync();
+      if (s_last[team]) {
         const int shares = static_cast<int>(o1 - o0) + 1;
         auto share = [&](int i) {
           return p.part + ((o0 + i) * 2 + (i == 0 ? 1 : 0)) * kRows * (D + 2);
         };
-        for (int i = tid; i < rows * D; i += kThreads) {
+        for (int i = mine; i < rows * D; i += crew) {
           const int r = i / D, d = i % D;
           float m = -INFINITY, l = 0.f, v = 0.f;
           for (int k = 0; k < shares; ++k) m = fmaxf(m, __ldcg(share(k) + kRows * D + r));
@@ -628,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         }
       }
     }
-    __syncthreads();   // s_o and s_m are free for the next segment
+    team_sync();   // t_o and s_m are free for the next segment
     u = min(s.last, u1);
   }
 
@@ -672,11 +697,11 @@ bool encode_codes(CUtensorMap* m, const int8_t* base, const KvView& c) {
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, int TEAM>
 cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   const size_t smem = smem_bytes<D>(p.a.b.B);
   static std::atomic<unsigned long long> allowed;
-  cudaError_t e = allow_smem(q4_kv_attn_split_kernel<D, SPLIT>, smem_bytes<D>(kKvMaxSeqs), allowed);
+  cudaError_t e = allow_smem(q4_kv_attn_split_kernel<D, SPLIT, TEAM>, smem_bytes<D>(kKvMaxSeqs), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -688,18 +713,28 @@ cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q4_kv_attn_split_kernel<D, SPLIT>, p);
+  return cudaLaunchKernelEx(&cfg, q4_kv_attn_split_kernel<D, SPLIT, TEAM>, p);
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
+  // Teams of four while there are more (sequence, head)s than SMs: a team's start and end then fall into the
+  // others' streams (64 sequences of 50 to 8191 tokens, 8 heads: 138 us, 166 us with whole CTAs).  With fewer,
+  // whole CTAs, which leave a quarter of the shares to join.
+  return static_cast<long long>(p.a.b.B) * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams>(p, grid, st)
+                                                              : launch<D, SPLIT, kWarps>(p, grid, st);
 }
 
 }  // namespace
 
-size_t kv_attn_header_bytes() { return 4096; }   // a ticket per CTA
+size_t kv_attn_header_bytes() { return 4096; }   // a ticket for each range
 
 size_t kv_attn_split_bytes(int dim, int sms) {
-  return kv_attn_header_bytes() + static_cast<size_t>(sms) * 2 * kRows * (dim + 2) * 4;
+  return kv_attn_header_bytes() + static_cast<size_t>(sms) * kTeams * 2 * kRows * (dim + 2) * 4;
 }
 
 cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, void* ws, int sms, cudaStream_t st) {
+  if (static_cast<size_t>(sms) * kTeams * sizeof(unsigned) > kv_attn_header_bytes()) return cudaErrorInvalidConfiguration;
   AttnParams p = {};
   if (!encode_codes(&p.kmap, a.c.k, a.c) || !encode_codes(&p.vmap, a.c.v, a.c)) return cudaErrorUnknown;
   p.a = a;
