@@ -503,7 +503,7 @@ Q4_API size_t q4_moe_block_workspace_size(int64_t T, int64_t topk, int64_t E, in
  *   k_scale, v_scale   fp32  [pages][heads][page_tokens / 16]  scales
  * 16 consecutive tokens of one head (a block) share a scale; a cached value is
  * code * scale.  page_tokens: a power of two from 16 to 256; dim: 64 or 128;
- * heads <= 1024.  Buffers 16-byte aligned.  A new cache needs no
+ * heads <= 1024; fewer than 2^31 blocks.  Buffers 16-byte aligned.  A new cache needs no
  * initialisation: only blocks of appended tokens are read.
  *
  * The calls below take a batch of B sequences (B <= 2048), T <= 2^24 packed rows:

@@ -16,7 +16,7 @@
 //   the CTAs that share it adds the shares in order.
 //   A range is worked on by a team of warps, a whole CTA or a quarter of one.
 // * Each warp of a team streams blocks of its own (every fourth or sixteenth)
-//   through its own ring of TMA stages, so that no warp waits for another until
+//   through its own ring of asynchronous copies, so that no warp waits for another until
 //   the shares of the warps are added.
 // * Codes are integers up to 127, exact in fp16, as are bf16 queries scaled
 //   by a power of two per row; fp32 queries and the softmax weights are split
@@ -27,9 +27,6 @@
 //   scores, the value scale the weights, relative to the largest so far.
 #include <algorithm>
 #include <cfloat>
-
-#include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "q4_kernels.h"
 #include "q4_kv_device.cuh"
@@ -56,7 +53,6 @@ constexpr float kRestScale = 2048.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
-  CUtensorMap kmap, vmap;                 // codes: u8 [pages][heads * page][dim], boxes of 16 rows
   KvAttnCall a;
   int group;                              // query heads of one kv head
   int page_log2;
@@ -139,7 +135,7 @@ constexpr size_t smem_bytes(int B) {
   return 1024 + static_cast<size_t>(kWarps) * kStages * Stage<D>::kBytes +   // rings
          static_cast<size_t>(kWarps / 2) * kRows * (D + 8) * 4 +                    // the warps' sums, two after one another
          static_cast<size_t>(kWarps) * kRows * 2 * 4 +                        // their maxima and weights
-         static_cast<size_t>(kWarps) * kStages * (8 + 8) +                    // scales, barriers
+         static_cast<size_t>(kWarps) * kStages * 8 +                          // scales
          static_cast<size_t>(B + 1) * 8 + 64;
 }
 
@@ -169,9 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   float* s_m = s_o + kWarps / 2 * kRows * kORow;                                           // [warp][row]
   float* s_l = s_m + kWarps * kRows;
   float* s_scale = s_l + kWarps * kRows;                                           // [warp][stage][2]
-  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_scale + kWarps * kStages * 2);
-  long long* s_cum = reinterpret_cast<long long*>(s_bar + kWarps * kStages);       // [B + 1] first unit of each sequence
-  __shared__ int s_fail;
+  long long* s_cum = reinterpret_cast<long long*>(s_scale + kWarps * kStages * 2); // [B + 1] first unit of each sequence
   __shared__ int s_last[kTeams];
   __shared__ float s_rowf[kTeams][kRows];       // score of a unit product
   __shared__ float s_tot[kTeams][2][kRows];     // maximum, weights' sum
@@ -188,10 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   float* t_o = s_o + team * TEAM / 2 * kRows * kORow;
   uint4* s_q = reinterpret_cast<uint4*>(t_o);   // [k step][lane] A operand
   auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(crew) : "memory"); };
-  if (lane == 0)
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp * kStages + i], 4);   // two lanes: their bytes, their scales
-  if (tid == 0) s_fail = 0, s_pairs = 0;
-  fence_barrier_init();
+  if (tid == 0) s_pairs = 0;
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
@@ -268,13 +259,16 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     s.hi = b0 + max(0, static_cast<int>(min(s.last, u1) - s.first) - kSegCost);
   };
 
-  // ---- the warp's stream of blocks: the producer runs kStages blocks ahead ----
+  // ---- the warp's stream of blocks: copies run kStages - 1 blocks ahead of the one in work ----
+  // A block of keys (values) is consecutive; a lane copies every 32nd 16 bytes of it, to its swizzled place.
   const uint32_t my_ring = smem_u32(ring + warp * kStages * kStageBytes);
-  const uint32_t my_bar = smem_u32(s_bar + warp * kStages), my_scale = smem_u32(s_scale + warp * kStages * 2);
+  const uint32_t my_scale = smem_u32(s_scale + warp * kStages * 2);
   const int sub_mask = (a.c.page >> 4) - 1, sub_log2 = p.page_log2 - 4;   // blocks of a page
-  Segment ps = {};                              // the producer's segment
+  const int crow = D == 128 ? lane >> 3 : lane >> 2;
+  const uint32_t cput = crow * D + (D == 128 ? ((lane & 7) ^ crow) << 4 : ((lane & 3) ^ ((crow >> 1) & 3)) << 4);
+  Segment ps = {};                              // the copies' segment
   long long pu = u0;                            // its first unit
-  int pblk = 0, ppage = -1;                     // its next block, that block's page
+  int pblk = 0, ppage = -1;                     // the next block, that block's page
   bool more = u0 < u1;
   // to the warp's next block at or after pblk, through the segments
   auto settle = [&]() {
@@ -291,41 +285,41 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     ppage = pi < a.b.table_stride ? __ldg(a.b.table + ps.b * a.b.table_stride + pi) : -1;
   };
   if (more) settle();
-  uint32_t put = 0;                             // stage to fill next, in units of 8 bytes (a barrier, two scales)
+  uint32_t put = 0;                             // stage to fill next, in units of a stage's two scales
+  // copies one block, if there is one; always closes a group, so that groups count stages
   auto produce = [&]() {
-    if (!more) return;
-    const uint32_t bar = my_bar + put, sc = my_scale + put;
-    if (ppage >= 0 && ppage < a.c.pages && pblk * kKvBlock < ps.len) {
-      const int row = (ps.h << p.page_log2) + ((pblk & sub_mask) << 4);
-      if (lane < 2) {
-        // lane 0 the keys, lane 1 the values, each with its scale
-        const uint32_t dst = my_ring + put * (kStageBytes / 8) + lane * Stage<D>::kCodes;
-        const float* scale = (lane ? a.c.vs : a.c.ks) + ((static_cast<long long>(ppage) * a.c.heads + ps.h) << sub_log2) + (pblk & sub_mask);
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(Stage<D>::kCodes) : "memory");
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(lane ? &p.vmap : &p.kmap)), "r"(0), "r"(row), "r"(ppage), "r"(bar)
-            : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sc + 4 * lane), "l"(scale) : "memory");
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    if (more) {
+      if (ppage >= 0 && ppage < a.c.pages && pblk * kKvBlock < ps.len) {
+        // below 2^31: the call's checks
+        const uint32_t at = (static_cast<uint32_t>(ppage * a.c.heads + ps.h) << sub_log2) + (pblk & sub_mask);
+        const int8_t* k = a.c.k + static_cast<uint64_t>(at) * Stage<D>::kCodes + lane * 16;
+        const int8_t* v = a.c.v + static_cast<uint64_t>(at) * Stage<D>::kCodes + lane * 16;
+        const uint32_t dst = my_ring + put * (kStageBytes / 8);
+#pragma unroll
+        for (int i = 0; i < Stage<D>::kCodes / 512; ++i) {
+          const uint32_t to = dst + i * 512 + (D == 128 && (i & 1) ? cput ^ 64 : cput);   // four rows on: that bit
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(k + i * 512) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + Stage<D>::kCodes), "l"(v + i * 512) : "memory");
+        }
+        if (lane < 2)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(my_scale + put + 4 * lane),
+                       "l"((lane ? a.c.vs : a.c.ks) + at) : "memory");
+      } else {                                  // no such page, or a sequence without tokens: a block nobody sees
+        if (lane == 0 && pblk * kKvBlock < ps.len) atomicOr(a.err, kDevErrIndex);
+        if (lane < 2) asm volatile("st.shared.f32 [%0], %1;" ::"r"(my_scale + put + 4 * lane), "f"(-1.0f) : "memory");
       }
-    } else if (lane < 2) {                      // no such page, or a sequence without tokens: a block nobody sees
-      if (lane == 0 && pblk * kKvBlock < ps.len) atomicOr(a.err, kDevErrIndex);
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + 4 * lane), "f"(-1.0f) : "memory");
-      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+      put = put == 8 * (kStages - 1) ? 0 : put + 8;
+      pblk += TEAM;
+      settle();
     }
-    put = put == 8 * (kStages - 1) ? 0 : put + 8;
-    pblk += TEAM;
-    settle();
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll 1
   for (int i = 0; i < kStages; ++i) produce();
 
   // ---- segments ----
   const uint32_t qb = smem_u32(s_q + lane);
-  uint32_t take = 0, phase = 0;                 // stage to read next, as `put`; its barrier's parity
+  uint32_t take = 0;                            // stage to read next, as `put`
   // swizzled places of the thread's keys in a stage (plus 2 rows, the bit that differs, for the second tile) and
   // of its values (the chunk's bits change with the matrices)
   const int krow = 4 * (g >> 1) + (g & 1), vrow = lane & 15;
@@ -424,11 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
 
     for (int blk = s.lo + mate; blk < s.hi; blk += TEAM) {
       const uint32_t kb = my_ring + take * (kStageBytes / 8);
-      bounded_wait(s_bar + warp * kStages + (take >> 3), phase, &s_fail, a.err);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
       float ks, vs;
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(my_scale + take));
-      if (take == 8 * (kStages - 1)) take = 0, phase ^= 1;
-      else take += 8;
+      take = take == 8 * (kStages - 1) ? 0 : take + 8;
       if (ks >= 0.f) {
         // scores: column n of tile j is token 4 (n / 2) + 2 j + n % 2 of the block, so that the thread's four
         // columns are the tokens 4 c .. 4 c + 3
@@ -669,34 +663,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   }
 }
 
-// cuTensorMapEncodeTiled from the driver (null if unavailable).
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      fn = nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }();
-  return encode;
-}
-
-bool encode_codes(CUtensorMap* m, const int8_t* base, const KvView& c) {
-  const auto encode = encoder();
-  if (!encode) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.heads) * c.page,
-                              static_cast<cuuint64_t>(c.pages)};
-  const cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.dim), kKvBlock, 1};
-  const cuuint32_t ones[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(base), dims, strides, box, ones,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool SPLIT, int TEAM>
 cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   const size_t smem = smem_bytes<D>(p.a.b.B);
@@ -736,7 +702,6 @@ size_t kv_attn_split_bytes(int dim, int sms) {
 cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, void* ws, int sms, cudaStream_t st) {
   if (static_cast<size_t>(sms) * kTeams * sizeof(unsigned) > kv_attn_header_bytes()) return cudaErrorInvalidConfiguration;
   AttnParams p = {};
-  if (!encode_codes(&p.kmap, a.c.k, a.c) || !encode_codes(&p.vmap, a.c.v, a.c)) return cudaErrorUnknown;
   p.a = a;
   p.group = a.Hq / a.c.heads;
   p.page_log2 = 4;

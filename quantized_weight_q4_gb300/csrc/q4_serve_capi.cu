@@ -24,7 +24,8 @@ int check_cache(const q4_kv_cache* c, q4::KvView* v) {
       c->page_tokens <= 0)
     return Q4_ERR_ARG;
   if ((c->dim != 64 && c->dim != 128) || c->page_tokens < 16 || c->page_tokens > 256 ||
-      (c->page_tokens & (c->page_tokens - 1)) || c->heads > 1024 || c->pages > (1LL << 30))
+      (c->page_tokens & (c->page_tokens - 1)) || c->heads > 1024 || c->pages > (1LL << 30) ||
+      c->pages * c->heads * (c->page_tokens / 16) > 0x7fffffffLL)
     return Q4_ERR_SHAPE;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
     return Q4_ERR_ALIGN;
