@@ -12,7 +12,6 @@
 // over neighbours first (a binary tree over the head's elements) for the same
 // reason.
 #include <cfloat>
-#include <type_traits>
 
 #include "q4_kernels.h"
 #include "q4_kv_device.cuh"
@@ -22,249 +21,302 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kQRows = 4;              // query heads of one token a warp takes at once
+constexpr int kQRows = 8;              // query heads of one token a warp takes
 constexpr int kBlockWarps = 4;         // warps that share a block of keys or values
+static_assert(kWarps == 2 * kBlockWarps, "a CTA takes the keys and the values of a block");
 constexpr int kBlockRows = kKvBlock / kBlockWarps;
 constexpr float kTinyScale = 7.70371977754894341e-34f;   // 2^-110
 
-// D / 32 consecutive elements of a row, as fp32.
-template <int E>
-__device__ __forceinline__ void load_row(const void* base, long long off, int bf16, float (&x)[E]) {
-  if (bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + off;
-    if (E == 4) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
-      x[0] = __uint_as_float(w.x << 16);
-      x[1] = __uint_as_float(w.x & 0xffff0000u);
-      x[2] = __uint_as_float(w.y << 16);
-      x[E - 1] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-      x[0] = __uint_as_float(w << 16);
-      x[1] = __uint_as_float(w & 0xffff0000u);
-    }
-  } else {
-    const float* p = static_cast<const float*>(base) + off;
-    if (E == 4) {
-      const float4 w = *reinterpret_cast<const float4*>(p);
-      x[0] = w.x, x[1] = w.y, x[2] = w.z, x[E - 1] = w.w;
-    } else {
-      const float2 w = *reinterpret_cast<const float2*>(p);
-      x[0] = w.x, x[1] = w.y;
-    }
-  }
-}
+// How heads are rotated.  kHalves: all of a head, pairs half of it apart; kPart: pairs half of the rotated part
+// apart, less than the head.
+enum : int { kNone = 0, kHalves = 1, kPairs = 2, kPart = 3 };
 
-template <int E>
-__device__ __forceinline__ void store_row(void* base, long long off, int bf16, const float (&x)[E]) {
-  if (bf16) {
-    __nv_bfloat162 h[E / 2];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    uint16_t* p = static_cast<uint16_t*>(base) + off;
-    if (E == 4)
-      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
-    else
-      *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<uint32_t*>(h);
-  } else {
-    float* p = static_cast<float*>(base) + off;
-    if (E == 4)
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[E - 1]);
-    else
-      *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
-  }
-}
-
-// x <- (x * 1/sqrt(mean(x^2) + eps)) * w, one rounding a step; the sum of
-// squares neighbours first, in the lane and then over lane distances 1 to 16.
-template <int E>
-__device__ __forceinline__ void norm_row(float (&x)[E], const float (&w)[E], float eps) {
-  float s = __fadd_rn(__fmul_rn(x[0], x[0]), __fmul_rn(x[1], x[1]));
-  if (E == 4)
-    s = __fadd_rn(s, __fadd_rn(__fmul_rn(x[2], x[2]), __fmul_rn(x[E - 1], x[E - 1])));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-  const float mean = __fmul_rn(s, 1.0f / (32 * E));   // exact: a power of two
-  const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, eps)));
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
-}
-
-// This lane's cosines and sines at a position: for halves the E of its own
-// elements, for pairs E / 2 of them (one per pair).
-template <int E>
-struct Turn {
-  float c[E], s[E];
+// A head's row is held by D / 8 lanes: lane l of them has elements 4 l .. 4 l + 3 and the four that lie half a head
+// further on, so that kHalves turns pairs inside the lane.  A warp works on 32 / (D / 8) rows at a time.
+template <int D>
+struct Row {
+  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  float x[8];
 };
 
-template <int E>
-__device__ __forceinline__ void load_turn(const KvAppendParams& p, int pos, int lane, Turn<E>& t) {
-  const int d = lane * E, half = p.rope_dim >> 1;
-  if (d >= p.rope_dim) return;
-  const long long row = static_cast<long long>(pos) * half;
-  if (p.rope_pairs) {
-    const float* c = p.cos + row + (d >> 1);
-    const float* s = p.sin + row + (d >> 1);
+template <int D>
+__device__ __forceinline__ void load_row(const void* base, long long off, int bf16, int l, Row<D>& r) {
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) t.c[i] = __ldg(c + i), t.s[i] = __ldg(s + i);
-  } else {
-    const int at = d < half ? d : d - half;
-#pragma unroll
-    for (int i = 0; i < E; ++i) t.c[i] = __ldg(p.cos + row + at + i), t.s[i] = __ldg(p.sin + row + at + i);
+  for (int h = 0; h < 2; ++h) {
+    const long long at = off + h * (D / 2) + 4 * l;
+    if (bf16) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+      r.x[4 * h] = __uint_as_float(w.x << 16), r.x[4 * h + 1] = __uint_as_float(w.x & 0xffff0000u);
+      r.x[4 * h + 2] = __uint_as_float(w.y << 16), r.x[4 * h + 3] = __uint_as_float(w.y & 0xffff0000u);
+    } else {
+      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+      r.x[4 * h] = w.x, r.x[4 * h + 1] = w.y, r.x[4 * h + 2] = w.z, r.x[4 * h + 3] = w.w;
+    }
   }
 }
 
-// Rotates a row held across the warp.  Every lane takes part.
-template <int E>
-__device__ __forceinline__ void rotate_row(const KvAppendParams& p, int lane, const Turn<E>& t,
-                                           float (&x)[E]) {
-  const int d = lane * E, half = p.rope_dim >> 1;
-  if (p.rope_pairs) {
-    if (d < p.rope_dim) {
+template <int D>
+__device__ __forceinline__ void zero_row(Row<D>& r) {
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = __fsub_rn(__fmul_rn(a, t.c[i]), __fmul_rn(b, t.s[i]));
-        x[2 * i + 1] = __fadd_rn(__fmul_rn(b, t.c[i]), __fmul_rn(a, t.s[i]));
+  for (int i = 0; i < 8; ++i) r.x[i] = 0.f;
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(void* base, long long off, int bf16, int l, const Row<D>& r) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const long long at = off + h * (D / 2) + 4 * l;
+    if (bf16) {
+      __nv_bfloat162 y[2] = {__floats2bfloat162_rn(r.x[4 * h], r.x[4 * h + 1]),
+                             __floats2bfloat162_rn(r.x[4 * h + 2], r.x[4 * h + 3])};
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) = *reinterpret_cast<uint2*>(y);
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(base) + at) =
+          make_float4(r.x[4 * h], r.x[4 * h + 1], r.x[4 * h + 2], r.x[4 * h + 3]);
+    }
+  }
+}
+
+// This lane's eight weights of a norm.
+template <int D>
+__device__ __forceinline__ void load_weights(const float* w, int l, float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __ldg(w + (i >> 2) * (D / 2) + 4 * l + (i & 3));
+}
+
+// x <- (x * 1/sqrt(mean(x^2) + eps)) * w, one rounding a step; the sum of squares neighbours first: in the lane,
+// over the row's lanes (both halves of the head), then the halves.  The N rows of a lane take one square root and
+// one reciprocal together: lane i of a row's lanes has row i's.
+template <int D, int N>
+__device__ __forceinline__ void norm_rows(Row<D> (&r)[N], const float (&w)[8], float eps, int l) {
+  constexpr int kLanes = Row<D>::kLanes;
+  static_assert(N <= kLanes, "a lane for each row");
+  float mine = 0.f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float* x = r[n].x + 4 * h;
+      s[h] = __fadd_rn(__fadd_rn(__fmul_rn(x[0], x[0]), __fmul_rn(x[1], x[1])),
+                       __fadd_rn(__fmul_rn(x[2], x[2]), __fmul_rn(x[3], x[3])));
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) {
+      s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], o));
+      s[1] = __fadd_rn(s[1], __shfl_xor_sync(0xffffffffu, s[1], o));
+    }
+    const float sum = __fadd_rn(s[0], s[1]);
+    if (N == 1 || l == n) mine = sum;
+  }
+  const float mean = __fmul_rn(mine, 1.0f / D);   // exact: a power of two
+  const float k = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, eps)));
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const float f = N == 1 ? k : __shfl_sync(0xffffffffu, k, n, kLanes);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[n].x[i] = __fmul_rn(__fmul_rn(r[n].x[i], f), w[i]);
+  }
+}
+
+// The cosines and sines of a lane's elements (kHalves: of its four pairs; kPairs: two pairs for each four elements).
+struct Turn {
+  float c[8], s[8];
+};
+
+template <int D, int MODE>
+__device__ __forceinline__ void load_turn(const KvAppendParams& p, int pos, int l, Turn& t) {
+  const int half = p.rope_dim >> 1;
+  const float* c = p.cos + static_cast<long long>(pos) * half;
+  const float* s = p.sin + static_cast<long long>(pos) * half;
+  if (MODE == kHalves) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(c + 4 * l)), v = __ldg(reinterpret_cast<const float4*>(s + 4 * l));
+    t.c[0] = u.x, t.c[1] = u.y, t.c[2] = u.z, t.c[3] = u.w;
+    t.s[0] = v.x, t.s[1] = v.y, t.s[2] = v.z, t.s[3] = v.w;
+  }
+#pragma unroll
+  for (int h = 0; h < 2 && MODE != kHalves; ++h) {
+    const int d = h * (D / 2) + 4 * l;
+    if (d >= p.rope_dim) continue;
+    if (MODE == kPairs) {
+      const float2 u = __ldg(reinterpret_cast<const float2*>(c + d / 2)), v = __ldg(reinterpret_cast<const float2*>(s + d / 2));
+      t.c[4 * h] = u.x, t.c[4 * h + 1] = u.y;
+      t.s[4 * h] = v.x, t.s[4 * h + 1] = v.y;
+    } else {
+      const int at = d < half ? d : d - half;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t.c[4 * h + i] = __ldg(c + at + i), t.s[4 * h + i] = __ldg(s + at + i);
+    }
+  }
+}
+
+// (a, b) <- (a c - b s, b c + a s), one rounding a step.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float y = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = y;
+}
+
+// Rotates a row.  Every lane takes part.
+template <int D, int MODE>
+__device__ __forceinline__ void rotate_row(const KvAppendParams& p, int l, const Turn& t, Row<D>& r) {
+  if (MODE == kHalves) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn(r.x[i], r.x[4 + i], t.c[i], t.s[i]);
+  } else if (MODE == kPairs) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (h * (D / 2) + 4 * l < p.rope_dim) {
+        turn(r.x[4 * h], r.x[4 * h + 1], t.c[4 * h], t.s[4 * h]);
+        turn(r.x[4 * h + 2], r.x[4 * h + 3], t.c[4 * h + 1], t.s[4 * h + 1]);
+      }
+  } else if (MODE == kPart) {
+    // four elements' partners are four of another lane, in its first or second half
+    constexpr int kLanes = Row<D>::kLanes;
+    const int half = p.rope_dim >> 1, away = half >> 2, first = (threadIdx.x & 31) - l;
+    float y[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int chunk = h * kLanes + l, d = 4 * chunk;
+      const int from = d < half ? chunk + away : d < p.rope_dim ? chunk - away : chunk;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float u = __shfl_sync(0xffffffffu, r.x[i], first + from % kLanes);
+        const float v = __shfl_sync(0xffffffffu, r.x[4 + i], first + from % kLanes);
+        const float o = from < kLanes ? u : v, x = r.x[4 * h + i];
+        y[4 * h + i] = d < half ? __fsub_rn(__fmul_rn(x, t.c[4 * h + i]), __fmul_rn(o, t.s[4 * h + i]))
+                       : d < p.rope_dim ? __fadd_rn(__fmul_rn(x, t.c[4 * h + i]), __fmul_rn(o, t.s[4 * h + i])) : x;
       }
     }
-    return;
-  }
-  const int away = half / E;
-  const int from = d < half ? lane + away : d < p.rope_dim ? lane - away : lane;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const float o = __shfl_sync(0xffffffffu, x[i], from);
-    if (d < half)
-      x[i] = __fsub_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(o, t.s[i]));
-    else if (d < p.rope_dim)
-      x[i] = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(o, t.s[i]));
+    for (int i = 0; i < 8; ++i) r.x[i] = y[i];
   }
 }
 
 // Queries: one warp takes kQRows heads of one token.
-template <int E>
-__device__ void append_queries(const KvAppendParams& p, long long task, int lane) {
-  const int groups = (p.Hq + kQRows - 1) / kQRows;
-  const int t = static_cast<int>(task / groups);
-  const int h0 = static_cast<int>(task % groups) * kQRows;
+template <int D, int MODE>
+__device__ void append_queries(const KvAppendParams& p, unsigned task, int lane) {
+  using R = Row<D>;
+  constexpr int kSteps = kQRows / R::kRows;
+  const unsigned groups = (p.Hq + kQRows - 1) / kQRows;
+  const int t = static_cast<int>(task / groups), l = lane % R::kLanes;
+  const int h0 = static_cast<int>(task - t * groups) * kQRows + lane / R::kLanes;
   if (t >= p.b.T) return;
-  constexpr int D = 32 * E;
-  float x[kQRows][E];   // on their way while the token's sequence and position are found
+  R r[kSteps];   // on their way while the token's sequence and position are found
 #pragma unroll
-  for (int r = 0; r < kQRows; ++r) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[r][i] = 0.f;
-    if (h0 + r < p.Hq) load_row<E>(p.q, t * p.q_stride + (h0 + r) * D + lane * E, p.in_bf16, x[r]);
+  for (int i = 0; i < kSteps; ++i) {
+    zero_row(r[i]);
+    const int h = h0 + i * R::kRows;
+    if (h < p.Hq) load_row<D>(p.q, t * p.q_stride + h * D, p.in_bf16, l, r[i]);
   }
   const int b = warp_count_le(p.b.B, t, [&](int j) { return __ldg(p.b.cu + j); });
   int pos = -1;
   if (b < p.b.B && t >= __ldg(p.b.cu + b)) pos = __ldg(p.b.kv_len + b) - (__ldg(p.b.cu + b + 1) - t);
-  if (p.cos && pos >= p.rope_rows) {
+  if (MODE != kNone && pos >= p.rope_rows) {
     if (lane == 0) atomicOr(p.err, kDevErrIndex);
     pos = -1;
   }
-  if (pos >= 0) {
-    Turn<E> turn;
-    float w[E];
-    if (p.cos) load_turn<E>(p, pos, lane, turn);
-    if (p.q_norm) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) w[i] = __ldg(p.q_norm + lane * E + i);
-    }
-#pragma unroll
-    for (int r = 0; r < kQRows; ++r) {
-      if (p.q_norm) norm_row<E>(x[r], w, p.eps);
-      if (p.cos) rotate_row<E>(p, lane, turn, x[r]);
-    }
-  } else {
-#pragma unroll
-    for (int r = 0; r < kQRows; ++r)
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[r][i] = 0.f;
+  Turn tn;
+  if (MODE != kNone && pos >= 0) load_turn<D, MODE>(p, pos, l, tn);
+  if (p.q_norm && pos >= 0) {
+    float w[8];
+    load_weights<D>(p.q_norm, l, w);
+    norm_rows<D, kSteps>(r, w, p.eps, l);
   }
 #pragma unroll
-  for (int r = 0; r < kQRows; ++r)
-    if (h0 + r < p.Hq)
-      store_row<E>(p.q_out, (static_cast<long long>(t) * p.Hq + h0 + r) * D + lane * E, p.out_bf16, x[r]);
+  for (int i = 0; i < kSteps; ++i) {
+    if (pos >= 0) {
+      if (MODE != kNone) rotate_row<D, MODE>(p, l, tn, r[i]);
+    } else {
+      zero_row(r[i]);
+    }
+    const int h = h0 + i * R::kRows;
+    if (h < p.Hq) store_row<D>(p.q_out, (static_cast<long long>(t) * p.Hq + h) * D, p.out_bf16, l, r[i]);
+  }
 }
 
 // Keys or values: kBlockWarps warps take one block of one head, four tokens
 // each (s_max: their largest magnitudes).  Slots of a sequence start at
 // cu[b] / 16 + 2 b: at least as many as the blocks it touches.  Every thread of
 // the CTA calls it and meets once.
-template <int E>
-__device__ void append_block(const KvAppendParams& p, long long slot, int h, bool is_k, int part, int lane,
+template <int D, int MODE>
+__device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k, int part, int lane,
                              float* s_max) {
-  constexpr int D = 32 * E;
-  int blk = 0, lo = 0, hi = 0;       // of this warp's four positions, those in [lo, hi) are new
+  using R = Row<D>;
+  constexpr int kSteps = kBlockRows / R::kRows;
+  const int l = lane % R::kLanes;
+  int pos0 = 0, lo = 0, hi = 0;      // this lane's rows are at pos0 + i * kRows; those in [lo, hi) are new
   long long row0 = -1;
-  const int b = warp_count_le(p.b.B, static_cast<int>(slot), [&](int j) { return (__ldg(p.b.cu + j) >> 4) + 2 * j; });
-  float x[kBlockRows][E];
+  const int b = warp_count_le(p.b.B, slot, [&](int j) { return (__ldg(p.b.cu + j) >> 4) + 2 * j; });
+  R r[kSteps];
   float s0 = 0.f, m = 0.f;
-  bool had = false;
   if (b < p.b.B) {
     const int c0 = __ldg(p.b.cu + b), c1 = __ldg(p.b.cu + b + 1), len = __ldg(p.b.kv_len + b);
     const int start = len - (c1 - c0);          // position of the first new token
     const int from = max(start, 0);
-    const int at = static_cast<int>(slot) - ((c0 >> 4) + 2 * b);
-    blk = (from >> 4) + at;
+    const int at = slot - ((c0 >> 4) + 2 * b), blk = (from >> 4) + at;
     if (c1 > c0 && at >= 0 && blk * kKvBlock < len) {
       lo = max(from, blk * kKvBlock), hi = min(len, (blk + 1) * kKvBlock);
+      pos0 = blk * kKvBlock + part * kBlockRows + lane / R::kLanes;
       const long long tok0 = static_cast<long long>(c0) + (lo - start);   // packed row of position lo
       row0 = kv_row(p.c, p.b.table, p.b.table_stride, b, blk * kKvBlock, h);
-      if (row0 < 0 || c0 < 0 || tok0 + (hi - lo) > p.b.T || (is_k && p.cos && hi > p.rope_rows)) {
+      if (row0 < 0 || c0 < 0 || tok0 + (hi - lo) > p.b.T || (is_k && MODE != kNone && hi > p.rope_rows)) {
         if (lane == 0) atomicOr(p.err, kDevErrIndex);
         row0 = -1;
       } else {
         const void* src = is_k ? p.k : p.v;
         const long long stride = is_k ? p.k_stride : p.v_stride;
 #pragma unroll
-        for (int r = 0; r < kBlockRows; ++r) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) x[r][i] = 0.f;
-          const int pos = blk * kKvBlock + part * kBlockRows + r;
-          if (pos >= lo && pos < hi)
-            load_row<E>(src, (tok0 + pos - lo) * stride + h * D + lane * E, p.in_bf16, x[r]);
+        for (int i = 0; i < kSteps; ++i) {
+          zero_row(r[i]);
+          const int pos = pos0 + i * R::kRows;
+          if (pos >= lo && pos < hi) load_row<D>(src, (tok0 + pos - lo) * stride + h * D, p.in_bf16, l, r[i]);
         }
-        had = lo > blk * kKvBlock;
-        if (had) s0 = (is_k ? p.c.ks : p.c.vs)[row0 >> 4];
+        if (lo > blk * kKvBlock) s0 = (is_k ? p.c.ks : p.c.vs)[row0 >> 4];
       }
     }
   }
   if (row0 >= 0) {
-    if (is_k && (p.k_norm || p.cos)) {
-      float w[E];
+    if (is_k && (p.k_norm || MODE != kNone)) {
       if (p.k_norm) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) w[i] = __ldg(p.k_norm + lane * E + i);
+        float w[8];
+        load_weights<D>(p.k_norm, l, w);
+        norm_rows<D, kSteps>(r, w, p.eps, l);
       }
 #pragma unroll
-      for (int r = 0; r < kBlockRows; ++r) {
-        const int pos = blk * kKvBlock + part * kBlockRows + r;
-        if (pos < lo || pos >= hi) continue;
-        if (p.k_norm) norm_row<E>(x[r], w, p.eps);
-        if (p.cos) {
-          Turn<E> turn;
-          load_turn<E>(p, pos, lane, turn);
-          rotate_row<E>(p, lane, turn, x[r]);
+      for (int i = 0; i < kSteps; ++i) {   // rows that are not new stay zero
+        const int pos = pos0 + i * R::kRows;
+        if (MODE != kNone) {
+          Turn tn;
+          load_turn<D, MODE>(p, max(lo, min(pos, hi - 1)), l, tn);
+          rotate_row<D, MODE>(p, l, tn, r[i]);
         }
+        if (pos < lo || pos >= hi) zero_row(r[i]);   // also with eps 0: 0 / 0
       }
     }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(r[i].x[e]));
     // a code cannot hold a NaN or an infinity: 0 and the largest number instead, and the status word says so
-    bool odd = false;
+    // (fmaxf drops a NaN, so the sum looks for it)
+    float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < kBlockRows; ++r)
+    for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float a = fabsf(x[r][i]);
-        if (!(a <= FLT_MAX)) {
-          odd = true;
-          x[r][i] = x[r][i] != x[r][i] ? 0.f : copysignf(FLT_MAX, x[r][i]);
+      for (int e = 0; e < 8; ++e) sum = fmaf(r[i].x[e], 0.f, sum);   // 0, or a NaN
+    if (sum != 0.f) {
+      atomicOr(p.err, kDevErrValue);
+      m = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float& x = r[i].x[e];
+          x = x != x ? 0.f : fminf(fmaxf(x, -FLT_MAX), FLT_MAX);
+          m = fmaxf(m, fabsf(x));
         }
-        m = fmaxf(m, fabsf(x[r][i]));
-      }
-    if (odd) atomicOr(p.err, kDevErrValue);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
@@ -275,51 +327,47 @@ __device__ void append_block(const KvAppendParams& p, long long slot, int h, boo
   for (int i = 0; i < kBlockWarps; ++i) m = fmaxf(m, s_max[i]);
   float s = fmaxf(s0, __fmul_rn(m, 1.0f / 127.0f));
   if (s < kTinyScale) s = 0.f;
-  const float inv = s > 0.f ? __fdiv_rn(1.0f, s) : 0.f;
+  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
   const float ratio = s > 0.f ? __fdiv_rn(s0, s) : 0.f;
   if (part == 0 && lane == 0) (is_k ? p.c.ks : p.c.vs)[row0 >> 4] = s;
-  int8_t* codes = (is_k ? p.c.k : p.c.v) + (row0 + part * kBlockRows) * D + lane * E;
-  using Word = typename std::conditional<E == 4, uint32_t, uint16_t>::type;   // the lane's E codes of a row
+  int8_t* codes = (is_k ? p.c.k : p.c.v) + (row0 + (pos0 & (kKvBlock - 1))) * D + 4 * l;
 #pragma unroll
-  for (int r = 0; r < kBlockRows; ++r) {
-    const int pos = blk * kKvBlock + part * kBlockRows + r;
-    Word* to = reinterpret_cast<Word*>(codes + r * D);
-    uint32_t w = 0;
-    if (pos >= lo && pos < hi) {
+  for (int i = 0; i < kSteps; ++i) {
+    const int pos = pos0 + i * R::kRows;
+    if (pos >= hi || (pos < lo && ratio == 1.f)) continue;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = max(-127, min(127, __float2int_rn(__fmul_rn(x[r][i], inv))));
-        w |= (static_cast<uint32_t>(c) & 0xffu) << (8 * i);
+    for (int half = 0; half < 2; ++half) {
+      uint32_t* to = reinterpret_cast<uint32_t*>(codes + i * R::kRows * D + half * (D / 2));
+      float x[4];
+      if (pos < lo) {
+        const uint32_t old = *to;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(static_cast<float>(static_cast<int8_t>(old >> (8 * e))), ratio);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(r[i].x[4 * half + e], inv);   // at most 127 (1 + 2^-22)
       }
-    } else if (pos < lo && ratio != 1.f) {
-      const uint32_t old = *to;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float c = static_cast<float>(static_cast<int8_t>(old >> (8 * i)));
-        w |= (static_cast<uint32_t>(__float2int_rn(__fmul_rn(c, ratio))) & 0xffu) << (8 * i);
-      }
-    } else {
-      continue;
+      uint32_t w;
+      asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\tcvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+          : "=r"(w)
+          : "r"(__float2int_rn(x[0])), "r"(__float2int_rn(x[1])), "r"(__float2int_rn(x[2])), "r"(__float2int_rn(x[3])));
+      *to = w;
     }
-    *to = static_cast<Word>(w);
   }
 }
 
-template <int E>
-__global__ void __launch_bounds__(kThreads) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 5) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
                                                                 int kv_ctas) {
   __shared__ float s_max[kWarps];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (static_cast<int>(blockIdx.x) < kv_ctas) {   // the longer tasks first
-    const int unit = warp / kBlockWarps;
-    const long long task = static_cast<long long>(blockIdx.x) * (kWarps / kBlockWarps) + unit;
-    const int per = 2 * p.c.heads;
-    const int i = static_cast<int>(task % per);
-    append_block<E>(p, task / per, i % p.c.heads, i < p.c.heads, warp % kBlockWarps, lane, s_max + unit * kBlockWarps);
+  if (static_cast<int>(blockIdx.x) < kv_ctas) {   // the longer tasks first; a CTA takes a block's keys and values
+    const int unit = warp / kBlockWarps, slot = blockIdx.x / p.c.heads;
+    append_block<D, MODE>(p, slot, blockIdx.x - slot * p.c.heads, unit == 0, warp % kBlockWarps, lane, s_max + unit * kBlockWarps);
   } else {
-    append_queries<E>(p, static_cast<long long>(blockIdx.x - kv_ctas) * kWarps + warp, lane);
+    append_queries<D, MODE>(p, (blockIdx.x - kv_ctas) * kWarps + warp, lane);
   }
 }
 
@@ -399,13 +447,18 @@ cudaError_t launch_pdl(void (*kernel)(Args...), unsigned grid, unsigned threads,
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t st) {
   const long long slots = p.b.T / kKvBlock + 2LL * p.b.B;
-  const int units = kWarps / kBlockWarps;
-  const long long kv_ctas = (slots * 2 * p.c.heads + units - 1) / units;
+  const long long kv_ctas = slots * p.c.heads;
   const long long q_tasks = p.q_out ? static_cast<long long>(p.b.T) * ((p.Hq + kQRows - 1) / kQRows) : 0;
   const long long grid = kv_ctas + (q_tasks + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(p.c.dim == 128 ? q4_kv_append_kernel<4> : q4_kv_append_kernel<2>,
-                    static_cast<unsigned>(grid), kThreads, st, p, static_cast<int>(kv_ctas));
+  if (grid > 0x7fffffffLL || q_tasks > 0xffffffffLL) return cudaErrorInvalidConfiguration;
+  const int mode = !p.cos ? kNone : p.rope_pairs ? kPairs : p.rope_dim == p.c.dim ? kHalves : kPart;
+  static void (*const kernels[2][4])(KvAppendParams, int) = {
+      {q4_kv_append_kernel<64, kNone>, q4_kv_append_kernel<64, kHalves>, q4_kv_append_kernel<64, kPairs>,
+       q4_kv_append_kernel<64, kPart>},
+      {q4_kv_append_kernel<128, kNone>, q4_kv_append_kernel<128, kHalves>, q4_kv_append_kernel<128, kPairs>,
+       q4_kv_append_kernel<128, kPart>}};
+  return launch_pdl(kernels[p.c.dim == 128][mode], static_cast<unsigned>(grid), kThreads, st, p,
+                    static_cast<int>(kv_ctas));
 }
 
 cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t st) {

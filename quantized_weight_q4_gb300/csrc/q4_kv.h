@@ -18,6 +18,7 @@ struct KvView {
   float* ks;
   float* vs;
   int pages, heads, dim, page;   // page: tokens, a power of two in [16, 256]
+  int page_log2;
 };
 
 // The batch: sequence b holds kv_len[b] tokens, the last cu[b + 1] - cu[b] of

@@ -55,7 +55,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct AttnParams {
   KvAttnCall a;
   int group;                              // query heads of one kv head
-  int page_log2;
   int max_rows;                           // sequences with more query rows are left to the prompt form
   unsigned* tickets;                      // [ranges], zero
   float* part;                            // [ranges][2][kRows][dim + 2] shares
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   // A block of keys (values) is consecutive; a lane copies every 32nd 16 bytes of it, to its swizzled place.
   const uint32_t my_ring = smem_u32(ring + warp * kStages * kStageBytes);
   const uint32_t my_scale = smem_u32(s_scale + warp * kStages * 2);
-  const int sub_mask = (a.c.page >> 4) - 1, sub_log2 = p.page_log2 - 4;   // blocks of a page
+  const int sub_mask = (a.c.page >> 4) - 1, sub_log2 = a.c.page_log2 - 4;   // blocks of a page
   const int crow = D == 128 ? lane >> 3 : lane >> 2;
   const uint32_t cput = crow * D + (D == 128 ? ((lane & 7) ^ crow) << 4 : ((lane & 3) ^ ((crow >> 1) & 3)) << 4);
   Segment ps = {};                              // the copies' segment
@@ -704,8 +703,6 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   AttnParams p = {};
   p.a = a;
   p.group = a.Hq / a.c.heads;
-  p.page_log2 = 4;
-  while ((1 << p.page_log2) < a.c.page) ++p.page_log2;
   p.max_rows = max_rows;
   p.tickets = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());

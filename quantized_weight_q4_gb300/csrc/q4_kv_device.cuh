@@ -43,7 +43,7 @@ __device__ __forceinline__ int warp_count_le(int n, int i, F f) {
 // the page table has no valid page for it.
 __device__ __forceinline__ long long kv_row(const KvView& c, const int32_t* table,
                                             long long table_stride, int b, int pos, int h) {
-  const int pi = pos / c.page;
+  const int pi = pos >> c.page_log2;
   if (pi >= table_stride) return -1;
   const int pg = table[b * table_stride + pi];
   if (pg < 0 || pg >= c.pages) return -1;

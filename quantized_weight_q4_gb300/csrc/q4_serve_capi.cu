@@ -30,7 +30,8 @@ int check_cache(const q4_kv_cache* c, q4::KvView* v) {
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
     return Q4_ERR_ALIGN;
   *v = {c->k, c->v, c->k_scale, c->v_scale, static_cast<int>(c->pages), static_cast<int>(c->heads),
-        static_cast<int>(c->dim), static_cast<int>(c->page_tokens)};
+        static_cast<int>(c->dim), static_cast<int>(c->page_tokens), 4};
+  while ((1 << v->page_log2) < v->page) ++v->page_log2;
   return Q4_OK;
 }
 
