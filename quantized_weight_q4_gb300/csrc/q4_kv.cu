@@ -22,8 +22,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kQRows = 8;              // query heads of one token a warp takes
-constexpr int kBlockWarps = 4;         // warps that share a block of keys or values
-static_assert(kWarps == 2 * kBlockWarps, "a CTA takes the keys and the values of a block");
+constexpr int kBlockWarps = 2;         // warps that share a block of keys or values
+constexpr int kHeads = kWarps / (2 * kBlockWarps);   // kv heads of a CTA
 constexpr int kBlockRows = kKvBlock / kBlockWarps;
 constexpr float kTinyScale = 7.70371977754894341e-34f;   // 2^-110
 
@@ -235,7 +235,7 @@ __device__ void append_queries(const KvAppendParams& p, unsigned task, int lane)
   }
 }
 
-// Keys or values: kBlockWarps warps take one block of one head, four tokens
+// Keys or values: kBlockWarps warps take one block of one head, eight tokens
 // each (s_max: their largest magnitudes).  Slots of a sequence start at
 // cu[b] / 16 + 2 b: at least as many as the blocks it touches.  Every thread of
 // the CTA calls it and meets once.
@@ -250,7 +250,7 @@ __device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k
   const int b = warp_count_le(p.b.B, slot, [&](int j) { return (__ldg(p.b.cu + j) >> 4) + 2 * j; });
   R r[kSteps];
   float s0 = 0.f, m = 0.f;
-  if (b < p.b.B) {
+  if (b < p.b.B && h < p.c.heads) {
     const int c0 = __ldg(p.b.cu + b), c1 = __ldg(p.b.cu + b + 1), len = __ldg(p.b.kv_len + b);
     const int start = len - (c1 - c0);          // position of the first new token
     const int from = max(start, 0);
@@ -357,15 +357,16 @@ __device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 5) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
+__global__ void __launch_bounds__(kThreads, 4) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
                                                                 int kv_ctas) {
   __shared__ float s_max[kWarps];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (static_cast<int>(blockIdx.x) < kv_ctas) {   // the longer tasks first; a CTA takes a block's keys and values
-    const int unit = warp / kBlockWarps, slot = blockIdx.x / p.c.heads;
-    append_block<D, MODE>(p, slot, blockIdx.x - slot * p.c.heads, unit == 0, warp % kBlockWarps, lane, s_max + unit * kBlockWarps);
+  if (static_cast<int>(blockIdx.x) < kv_ctas) {   // the longer tasks first; a CTA takes keys and values of kHeads heads
+    const int unit = warp / kBlockWarps, groups = (p.c.heads + kHeads - 1) / kHeads, slot = blockIdx.x / groups;
+    const int h = (blockIdx.x - slot * groups) * kHeads + (unit >> 1);
+    append_block<D, MODE>(p, slot, h, (unit & 1) == 0, warp % kBlockWarps, lane, s_max + unit * kBlockWarps);
   } else {
     append_queries<D, MODE>(p, (blockIdx.x - kv_ctas) * kWarps + warp, lane);
   }
@@ -447,7 +448,7 @@ cudaError_t launch_pdl(void (*kernel)(Args...), unsigned grid, unsigned threads,
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t st) {
   const long long slots = p.b.T / kKvBlock + 2LL * p.b.B;
-  const long long kv_ctas = slots * p.c.heads;
+  const long long kv_ctas = slots * ((p.c.heads + kHeads - 1) / kHeads);
   const long long q_tasks = p.q_out ? static_cast<long long>(p.b.T) * ((p.Hq + kQRows - 1) / kQRows) : 0;
   const long long grid = kv_ctas + (q_tasks + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffLL || q_tasks > 0xffffffffLL) return cudaErrorInvalidConfiguration;
