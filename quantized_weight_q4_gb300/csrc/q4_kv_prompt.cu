@@ -231,14 +231,46 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] . B[smem desc]
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// One lane of the warp, the same each time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// The whole warp runs the issue loop, so that descriptors stay in uniform registers (a loop of one lane took 93
+// cycles an MMA, more than the 67 it runs); the instructions themselves are the leader's.
+// D[tmem] (+)= A[smem desc] . B[smem desc]
+__device__ __forceinline__ void lead_mma(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] . B[smem desc]
+__device__ __forceinline__ void lead_mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void lead_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 
@@ -351,59 +383,72 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       for (int g = it - 1; g >= 0 && g >= it - kStages; --g) (void)mbar_wait(&full[g % kStages], (g / kStages) & 1);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
+      const uint32_t leader = elect_one();
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = gwait(bar, parity, &s_fail, a.err);
+        const bool ok = __all_sync(0xffffffffu, gwait(bar, parity, &s_fail, a.err));
         tc_fence_after();
         return ok;
       };
-      auto qk = [&](int g, int it) {   // scores of tile g with the K tile that is copy `it`
-        const uint32_t qa = smem_u32(sq + g * C::kTileBytes), kb = smem_u32(ring + (it % kStages) * C::kTileBytes);
+      // descriptors count 16 bytes
+      const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 1024, kSwizzle128);
+      const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128);
+      const uint64_t v_desc = smem_desc(smem_u32(ring), C::kHalf, 1024, kSwizzle128);
+      auto qk = [&](int g, int st) {   // scores of tile g with the K tile in stage st
+        const uint64_t qd = q_desc + g * (C::kTileBytes >> 4), kd = k_desc + st * (C::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-          tc_mma(t_s[g], smem_desc(qa + off, 16, 1024, kSwizzle128), smem_desc(kb + off, 16, 1024, kSwizzle128),
-                 C::kIdescQk, kk > 0 ? 1u : 0u);
+          const int off = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
+          lead_mma(leader, t_s[g], qd + off, kd + off, C::kIdescQk, kk > 0 ? 1u : 0u);
         }
-        tc_commit(&s_full[g]);
+        lead_commit(leader, &s_full[g]);
       };
-      auto pv = [&](int g, int it, bool more) {
-        const uint32_t vb = smem_u32(ring + (it % kStages) * C::kTileBytes);
+      auto pv = [&](int g, int st, uint32_t more) {
+        const uint64_t vd = v_desc + st * (C::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          tc_mma_ts(t_o[g], t_s[g] + kk * 8, smem_desc(vb + kk * 2048, C::kHalf, 1024, kSwizzle128), C::kIdescPv,
-                    more || kk > 0 ? 1u : 0u);
-        tc_commit(&o_done[g]);
+          lead_mma_ts(leader, t_o[g], t_s[g] + kk * 8, vd + kk * (2048 >> 4), C::kIdescPv, kk > 0 ? 1u : more);
+        lead_commit(leader, &o_done[g]);
       };
-      auto full_of = [&](int it) { return wait(&full[it % kStages], (it / kStages) & 1); };
-      bool ok = wait(q_ready, 0) && full_of(0);
+      // copies alternate between K and V; stage and parity of the next one
+      int st = 0;
+      uint32_t phase = 0;
+      auto next_copy = [&]() {
+        if (++st == kStages) st = 0, phase ^= 1;
+      };
+      bool ok = wait(q_ready, 0) && wait(&full[0], 0);
       if (ok) {
         qk(0, 0);
         qk(1, 0);
-        tc_commit(&empty[0]);
+        lead_commit(leader, &empty[0]);
+        next_copy();
       }
       for (int i = 0; ok && i < n; ++i) {
-        const int k = 2 * (i + 1), v = 2 * i + 1;
         const bool next = i + 1 < n;
-        ok = full_of(v) && wait(&p_ready[0], i & 1);
+        const int v = st;
+        ok = wait(&full[v], phase);
+        next_copy();
+        const int k = st;
+        ok = ok && wait(&p_ready[0], i & 1);
         if (!ok) break;
         pv(0, v, i > 0);
         if (next) {
-          ok = full_of(k);
+          ok = wait(&full[k], phase);
           if (!ok) break;
           qk(0, k);
         }
         ok = wait(&p_ready[1], i & 1);
         if (!ok) break;
         pv(1, v, i > 0);
-        tc_commit(&empty[v % kStages]);
+        lead_commit(leader, &empty[v]);
         if (next) {
           qk(1, k);
-          tc_commit(&empty[k % kStages]);
+          lead_commit(leader, &empty[k]);
+          next_copy();
         }
       }
       // no MMA may still run when the tensor memory is freed
-      tc_commit(drain);
+      lead_commit(leader, drain);
       (void)mbar_wait(drain, 0);
     }
   }
@@ -458,9 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
     const int from = f < -1 ? -1 : static_cast<int>(f);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    const uint4* seen_at = p.seen + tile0 + first;
+    uint4 next_seen = n > 0 ? __ldg(seen_at) : make_uint4(0, 0, 0, 0);
     for (int i = 0; i < n; ++i) {
       const int t0 = (first + i) * kTile;
-      const uint4 seen = __ldg(p.seen + tile0 + first + i);
+      const uint4 seen = next_seen;
+      if (i + 1 < n) next_seen = __ldg(seen_at + i + 1);
       ok = gwait(&s_full[g], i & 1, &s_fail, a.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
