@@ -231,6 +231,34 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// bounded_wait by the whole warp that polls instead of sleeping in the barrier: the MMA warp's waits are on the
+// path between the softmax and the tensor cores, and waking up takes some 200 cycles.
+__device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t parity, volatile int* fail, unsigned* err) {
+  const uint32_t at = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (uint32_t turn = 0;; ++turn) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((turn & 1023) == 1023) {
+      if (*fail) return false;
+      const unsigned long long t = globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        *fail = 1;
+        atomicOr(err, kDevErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // One lane of the warp, the same each time.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
@@ -386,9 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
     if (n > 0) {
       const uint32_t leader = elect_one();
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = __all_sync(0xffffffffu, gwait(bar, parity, &s_fail, a.err));
-        tc_fence_after();
-        return ok;
+        return __all_sync(0xffffffffu, poll_wait(bar, parity, &s_fail, a.err));
       };
       // descriptors count 16 bytes
       const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 1024, kSwizzle128);
@@ -431,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
         const int k = st;
         ok = ok && wait(&p_ready[0], i & 1);
         if (!ok) break;
+        tc_fence_after();
         pv(0, v, i > 0);
         if (next) {
           ok = wait(&full[k], phase);
@@ -439,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
         }
         ok = wait(&p_ready[1], i & 1);
         if (!ok) break;
+        tc_fence_after();
         pv(1, v, i > 0);
         lead_commit(leader, &empty[v]);
         if (next) {
