@@ -86,8 +86,8 @@ size_t kv_attn_split_bytes(int dim, int sms);
 // head), and zeros for rows of no sequence.  max_q: new tokens of a sequence at most.
 cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, void* ws, int sms,
                                  cudaStream_t st);
-// Sequences with more than split_rows query rows; bf16 q and out.  rows: rows of
-// fp16 keys and values the workspace holds (kv_prompt_rows).
+// Sequences with more than split_rows query rows (0: all, and zeros for rows of no
+// sequence); bf16 q and out.  rows: rows of fp16 keys and values the workspace holds (kv_prompt_rows).
 long long kv_prompt_rows(int B, long long max_kv, long long total_kv);
 size_t kv_prompt_bytes(const KvView& c, int B, long long rows);
 cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows, void* ws,

@@ -682,12 +682,13 @@ cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
 }
 
 template <int D, bool SPLIT>
-cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
-  // Teams of four while there are more (sequence, head)s than SMs: a team's start and end then fall into the
+cudaError_t launch(const AttnParams& p, int rows, int grid, cudaStream_t st) {
+  // Teams of four while there are more (sequence, tile, head)s than SMs: a team's start and end then fall into the
   // others' streams (64 sequences of 50 to 8191 tokens, 8 heads: 138 us, 166 us with whole CTAs).  With fewer,
   // whole CTAs, which leave a quarter of the shares to join.
-  return static_cast<long long>(p.a.b.B) * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams>(p, grid, st)
-                                                              : launch<D, SPLIT, kWarps>(p, grid, st);
+  const long long tiles = (rows + (SPLIT ? 7 : 15)) / (SPLIT ? 8 : 16);
+  return p.a.b.B * tiles * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams>(p, grid, st)
+                                              : launch<D, SPLIT, kWarps>(p, grid, st);
 }
 
 }  // namespace
@@ -708,10 +709,10 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
   // fp32 in or out needs two terms; bf16 takes them too while eight rows are enough (a thread then has one row's
   // softmax instead of two)
-  const bool split = !a.q_bf16 || !a.out_bf16 ||
-                     std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows) <= 8;
-  if (a.c.dim == 128) return split ? launch<128, true>(p, sms, st) : launch<128, false>(p, sms, st);
-  return split ? launch<64, true>(p, sms, st) : launch<64, false>(p, sms, st);
+  const int rows = static_cast<int>(std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows));
+  const bool split = !a.q_bf16 || !a.out_bf16 || rows <= 8;
+  if (a.c.dim == 128) return split ? launch<128, true>(p, rows, sms, st) : launch<128, false>(p, rows, sms, st);
+  return split ? launch<64, true>(p, rows, sms, st) : launch<64, false>(p, rows, sms, st);
 }
 
 }  // namespace q4

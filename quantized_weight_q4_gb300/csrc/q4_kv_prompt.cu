@@ -52,6 +52,10 @@ struct ExpandParams {
   __half* kv;                // [2][heads][rows_cap][dim]
   float* factor;             // [B][heads][2]: what a row of K (V) was divided by
   uint4* seen;               // [rows_cap / 128] bit i: token i of the tile exists
+  int* kv_cum;               // [B + 1] first tile of each sequence's tokens, and of its query rows
+  int* q_cum;
+  uint4* zeros;              // out, when rows of no sequence are this kernel's to clear, or null
+  long long row_bytes;
   unsigned* err;
 };
 
@@ -62,6 +66,8 @@ struct PromptParams {
   int rows_cap;
   const float* factor;
   const uint4* seen;
+  const int* kv_cum;
+  const int* q_cum;
 };
 
 // Sequences in this form have more query rows than the split form takes.
@@ -116,6 +122,12 @@ __device__ __forceinline__ int kv_tiles(const KvBatch& b, int i, int group, int 
   return is_prompt(nq, group, split_rows) ? (max(b.kv_len[i], 0) + kTile - 1) / kTile : 0;
 }
 
+__device__ __forceinline__ int q_tiles(const KvBatch& b, int i, int group, int split_rows) {
+  const int nq = b.cu[i + 1] - b.cu[i];
+  return is_prompt(nq, group, split_rows)
+             ? static_cast<int>((static_cast<long long>(nq) * group + kTileRows - 1) / kTileRows) : 0;
+}
+
 // ---------------------------------------------------------------------------
 // Pages to fp16 rows
 // ---------------------------------------------------------------------------
@@ -129,8 +141,22 @@ __global__ void __launch_bounds__(kExpandThreads) q4_kv_expand_kernel(const __gr
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, h = blockIdx.y, B = p.b.B;
   prefix<kExpandThreads>(B, s_cum, [&](int b) { return kv_tiles(p.b, b, p.group, p.split_rows); });
-  const int tile = blockIdx.x;
-  if (tile >= s_cum[B]) return;
+  if (p.zeros) {
+    const long long from = max(0, min(p.b.T, p.b.cu[B])) * p.row_bytes / 16, all = p.b.T * p.row_bytes / 16;
+    const long long at = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * kExpandThreads + tid;
+    for (long long i = from + at; i < all; i += static_cast<long long>(gridDim.x) * gridDim.y * kExpandThreads)
+      p.zeros[i] = make_uint4(0, 0, 0, 0);
+  }
+  const int tile = blockIdx.x, total = s_cum[B];
+  if (tile == 0 && h == 0) {   // for the attention kernel
+    for (int i = tid; i <= B; i += kExpandThreads) p.kv_cum[i] = s_cum[i];
+    __syncthreads();
+    prefix<kExpandThreads>(B, s_cum, [&](int b) { return q_tiles(p.b, b, p.group, p.split_rows); });
+    for (int i = tid; i <= B; i += kExpandThreads) p.q_cum[i] = s_cum[i];
+    __syncthreads();
+    prefix<kExpandThreads>(B, s_cum, [&](int b) { return kv_tiles(p.b, b, p.group, p.split_rows); });
+  }
+  if (tile >= total) return;
   const int b = find_seq(s_cum, B, tile), t0 = (tile - s_cum[b]) * kTile, len = p.b.kv_len[b];
   // powers of two that bring the sequence's largest scale of this head to [2^7, 2^8)
   float km = 0.f, vm = 0.f;
@@ -344,35 +370,25 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
   pdl_wait();   // before tensor memory is taken: the kernel before may need this SM's
 
   // ---- which rows: the last tiles of each sequence see the most, and go first ----
-  {
-    int* cum = reinterpret_cast<int*>(ring);
-    prefix<kThreads>(B, cum, [&](int b) {
-      const int nq = a.b.cu[b + 1] - a.b.cu[b];
-      return is_prompt(nq, p.group, p.split_rows)
-                 ? static_cast<int>((static_cast<long long>(nq) * p.group + kTileRows - 1) / kTileRows) : 0;
-    });
-    if (tid == 0) {
-      const long long t = static_cast<long long>(cum[B]) * a.c.heads - 1 - blockIdx.x;
-      s_where[0] = -1;
-      if (t >= 0) {
-        const int qt = static_cast<int>(t / a.c.heads), b = find_seq(cum, B, qt);
-        s_where[0] = b;
-        s_where[1] = qt - cum[b];
+  if (warp == 0) {
+    const long long t = static_cast<long long>(__ldg(p.q_cum + B)) * a.c.heads - 1 - blockIdx.x;
+    const int qt = t < 0 ? 0 : static_cast<int>(t / a.c.heads);
+    const int b = t < 0 ? -1 : warp_count_le(B, qt, [&](int j) { return __ldg(p.q_cum + j); });
+    if (lane == 0) {
+      s_where[0] = b;
+      if (b >= 0) {
+        s_where[1] = qt - __ldg(p.q_cum + b);
         s_where[2] = static_cast<int>(t % a.c.heads);
+        s_where[3] = __ldg(p.kv_cum + b);   // first tile of the sequence's K and V
       }
     }
-    __syncthreads();
-    // first row of the sequence's K and V
-    prefix<kThreads>(B, cum, [&](int b) { return kv_tiles(a.b, b, p.group, p.split_rows); });
-    if (tid == 0) s_where[3] = s_where[0] >= 0 ? cum[s_where[0]] : 0;
-    __syncthreads();
   }
+  __syncthreads();
   const int b = s_where[0];
   if (b < 0) return;
   const int qt = s_where[1], h = s_where[2], tile0 = s_where[3];
   const int c0 = a.b.cu[b], nq = a.b.cu[b + 1] - c0, len = a.b.kv_len[b];
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
-  fence_async_smem();        // TMA writes where the prefix sums were
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -524,10 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       fence_async_smem();
       mbar_arrive(q_ready);
     }
-    // positions the row sees: (from, to]
+    // positions the row sees: (from, to]; one that does not exist sees all, so that no tile is on its edge
     const int qpos = len - nq + j;
-    const int to = !have ? -1 : a.causal ? qpos : len - 1;
-    const long long f = a.window > 0 ? static_cast<long long>(qpos) - a.window : -1LL;
+    const int to = !have ? 0x7fffffff : a.causal ? qpos : len - 1;
+    const long long f = have && a.window > 0 ? static_cast<long long>(qpos) - a.window : -1LL;
     const int from = f < -1 ? -1 : static_cast<int>(f);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -680,13 +696,15 @@ cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, unsigned threads, size_t sm
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t factor, seen, kv, total;
+  size_t factor, seen, kv_cum, q_cum, kv, total;
 };
 Layout layout(const KvView& c, int B, long long rows_cap) {
   Layout l;
   l.factor = 0;
   l.seen = up256(static_cast<size_t>(B) * c.heads * 2 * sizeof(float));
-  l.kv = l.seen + up256(static_cast<size_t>(rows_cap / kTile) * sizeof(uint4));
+  l.kv_cum = l.seen + up256(static_cast<size_t>(rows_cap / kTile) * sizeof(uint4));
+  l.q_cum = l.kv_cum + up256((static_cast<size_t>(B) + 1) * sizeof(int));
+  l.kv = l.q_cum + up256((static_cast<size_t>(B) + 1) * sizeof(int));
   l.total = l.kv + static_cast<size_t>(rows_cap) * c.heads * c.dim * 2 * sizeof(__half);
   return l;
 }
@@ -713,6 +731,11 @@ cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows
   x.kv = reinterpret_cast<__half*>(w + l.kv);
   x.factor = reinterpret_cast<float*>(w + l.factor);
   x.seen = reinterpret_cast<uint4*>(w + l.seen);
+  x.kv_cum = reinterpret_cast<int*>(w + l.kv_cum);
+  x.q_cum = reinterpret_cast<int*>(w + l.q_cum);
+  // without a split form beside it, rows of no sequence are this form's
+  x.zeros = split_rows == 0 ? static_cast<uint4*>(a.out) : nullptr;
+  x.row_bytes = static_cast<long long>(a.Hq) * a.c.dim * 2;
   x.err = a.err;
   PromptParams p = {};
   p.a = a;
@@ -721,6 +744,8 @@ cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows
   p.rows_cap = x.rows_cap;
   p.factor = x.factor;
   p.seen = x.seen;
+  p.kv_cum = x.kv_cum;
+  p.q_cum = x.q_cum;
   const auto encode = encoder();
   if (!encode) return cudaErrorUnknown;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(rows), 2ull * a.c.heads};

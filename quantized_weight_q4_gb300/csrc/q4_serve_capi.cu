@@ -121,19 +121,44 @@ int q4_kv_gather(void* k_out, void* v_out, int dtype, const q4_kv_cache* cache, 
 namespace {
 
 // Query rows (new tokens x query heads that share a kv head) up to which a
-// sequence takes the split form.
-constexpr int kSplitRows = 64;
+// sequence takes the split form, for B sequences of up to max_kv tokens.  The
+// split form streams the codes once for every 16 rows, 1100 blocks of 16 tokens
+// a microsecond with some 40 blocks' time to start each; the prompt form first
+// writes the tokens as fp16 and then takes 1.6 us for each 128 of them and 256
+// rows, on one SM however long they are.
+// Measured with 8 kv heads of 128 (split / prompt form, us): one sequence of
+// 16,000 tokens, 128 rows 65 / 342, 512 rows 194 / 210; 16 sequences of 8,000,
+// 16 rows 65 / 346, 128 rows 435 / 330; 64 of 1,000, 64 rows 173 / 202, 128 rows
+// 303 / 216; one of 256, 1024 rows 50 / 24.
+constexpr int kRowTile = 16, kMostSplitRows = 1024;
+int split_rows_of(const q4::KvView& c, int64_t B, int64_t max_kv, int sms) {
+  const double heads = static_cast<double>(B) * c.heads, blocks = static_cast<double>((max_kv + 15) / 16);
+  const double bytes = heads * blocks * 16 * c.dim;      // of keys, or values
+  int rows = kRowTile;
+  for (int r = 2 * kRowTile; r <= kMostSplitRows; r += kRowTile) {
+    const double split = 10 + heads * (r / kRowTile) * (blocks + 40) / 1100;
+    const double ctas = heads * ((r + 255) / 256);
+    const double walk = static_cast<double>(static_cast<int64_t>((ctas + sms - 1) / sms)) * ((max_kv + 127) / 128) * 1.6;
+    const double read = bytes * 4 / 6e6, prompt = 20 + bytes * 6 / 5.5e6 + (walk > read ? walk : read);
+    if (split > prompt) break;
+    rows = r;
+  }
+  return rows;
+}
 
 struct AttnPlan {
   bool prompt;          // the call may have sequences for the prompt form
-  long long rows;       // fp16 rows of it
+  int split_rows;       // query rows up to which a sequence takes the split form
+  long long rows;       // fp16 rows of the prompt form
   size_t split_bytes, total;
 };
 
+// sized: with room for the prompt form wherever a call of these bounds or smaller ones may take it
 AttnPlan attn_plan(const q4::KvView& c, int64_t Hq, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
-                   int64_t total_kv, bool bf16, int sms) {
+                   int64_t total_kv, bool bf16, bool sized, int sms) {
   AttnPlan p = {};
-  p.prompt = bf16 && (max_q < T ? max_q : T) * (Hq / c.heads) > kSplitRows;
+  p.split_rows = sized ? kRowTile : split_rows_of(c, B, max_kv, sms);
+  p.prompt = bf16 && (max_q < T ? max_q : T) * (Hq / c.heads) > p.split_rows;
   p.split_bytes = (q4::kv_attn_split_bytes(c.dim, sms) + 255) / 256 * 256;
   p.total = p.split_bytes;
   if (p.prompt) {
@@ -154,7 +179,7 @@ size_t q4_kv_attention_workspace_size(const q4_kv_cache* cache, int64_t Hq, int6
   int sms = 0;
   unsigned* status = nullptr;
   if (q4::device_info(&sms, &status) != Q4_OK) return 0;
-  return attn_plan(v, Hq, B, T, max_q, max_kv, total_kv, true, sms).total;
+  return attn_plan(v, Hq, B, T, max_q, max_kv, total_kv, true, true, sms).total;
 }
 
 int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_t q_stride, int64_t Hq,
@@ -178,7 +203,8 @@ int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_
   rc = q4::device_info(&sms, &a.err);
   if (rc != Q4_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const AttnPlan plan = attn_plan(a.c, Hq, B, T, max_q, max_kv, total_kv, q_dtype == Q4_BF16 && out_dtype == Q4_BF16, sms);
+  const AttnPlan plan = attn_plan(a.c, Hq, B, T, max_q, max_kv, total_kv,
+                                  q_dtype == Q4_BF16 && out_dtype == Q4_BF16, false, sms);
   if (plan.rows > 0x7fffffffLL) return Q4_ERR_SHAPE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (ws) {
@@ -192,9 +218,13 @@ int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_
   a.q_bf16 = q_dtype == Q4_BF16, a.out_bf16 = out_dtype == Q4_BF16;
   a.scale = scale, a.causal = causal, a.window = window;
   const int most = static_cast<int>(max_q < T ? max_q : T);
-  const cudaError_t e = q4::launch_kv_attn_split(a, most, plan.prompt ? kSplitRows : 0x7fffffff, ws, sms, st);
-  if (e != cudaSuccess || !plan.prompt) return status_of(e);
-  return status_of(q4::launch_kv_prompt(a, kSplitRows, plan.rows, ws + plan.split_bytes, st));
+  if (!plan.prompt) return status_of(q4::launch_kv_attn_split(a, most, 0x7fffffff, ws, sms, st));
+  // one sequence: no second form beside the prompt's
+  const int split_rows = B == 1 ? 0 : plan.split_rows;
+  cudaError_t e = cudaSuccess;
+  if (B > 1) e = q4::launch_kv_attn_split(a, most, split_rows, ws, sms, st);
+  if (e == cudaSuccess) e = q4::launch_kv_prompt(a, split_rows, plan.rows, ws + plan.split_bytes, st);
+  return status_of(e);
 }
 
 int q4_sample(int32_t* tokens, float* probs, const void* logits, int logits_dtype, int64_t stride, int64_t T,

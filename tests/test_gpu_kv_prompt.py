@@ -1,5 +1,7 @@
 """Prompt attention over the paged 8-bit cache (the tensor-core form, bf16),
-alone and in batches with single tokens, against 64-bit attention."""
+alone and in batches with single tokens, against 64-bit attention.  A sequence
+of more than 1024 query rows (new tokens x query heads that share a kv head)
+takes that form whatever its length; most cases have one."""
 
 import numpy as np
 import pytest
@@ -76,43 +78,43 @@ def check(new, ctx, Hq, heads, D, page, seed, window=0, causal=True, scale=None,
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n,ctx", [(65, 0), (128, 0), (129, 0), (200, 56), (100, 1000), (257, 127), (300, 84), (513, 0)])
 def test_lengths(n, ctx, D):
-    check([n], [ctx], 2, 1, D, 64, n + ctx)
+    check([n], [ctx], 16, 1, D, 64, n + ctx)
 
 
 @pytest.mark.parametrize("Hq,heads", [(1, 1), (4, 4), (8, 1), (6, 2), (7, 1), (12, 4)])
 def test_head_layouts(Hq, heads):
-    check([150], [33], Hq, heads, 64, 32, Hq)
+    check([1030 * heads // Hq + 1], [33], Hq, heads, 64, 32, Hq)
 
 
 def test_a_token_of_many_heads():
     """One kv head shared by more query rows than a tile holds."""
-    check([3, 1], [50, 400], 300, 1, 64, 16, 9)
+    check([3, 1], [50, 400], 400, 1, 64, 16, 9)
 
 
 @pytest.mark.parametrize("page", [16, 128, 256])
 def test_ragged_batch_with_single_tokens(page):
-    check([1, 140, 0, 33, 1, 300, 2], [700, 0, 20, 5, 0, 129, 50], 8, 2, 128, page, page)
+    check([1, 140, 0, 33, 1, 300, 2], [700, 0, 20, 5, 0, 129, 50], 32, 2, 128, page, page)
 
 
 def test_sum_of_lengths_bounds_the_workspace():
     new, ctx = [1, 140, 90], [2000, 0, 38]
-    check(new, ctx, 8, 2, 128, 64, 17, total_kv=sum(new) + sum(ctx))
+    check(new, ctx, 32, 2, 128, 64, 17, total_kv=sum(new) + sum(ctx))
 
 
 @pytest.mark.parametrize("window", [1, 16, 100, 128, 300])
 def test_windows(window):
-    check([280, 90], [300, 0], 4, 2, 64, 64, window, window=window)
+    check([280, 90], [300, 0], 16, 2, 64, 64, window, window=window)
 
 
 def test_every_query_sees_everything():
-    check([140, 70], [50, 0], 4, 2, 64, 16, 8, causal=False)
+    check([140, 70], [50, 0], 32, 2, 64, 16, 8, causal=False)
 
 
 def test_scales_and_sharpness():
-    check([130], [200], 4, 2, 128, 64, 51, q_gain=4)
-    check([130], [200], 4, 2, 64, 64, 52, spread=20.0)
-    check([130], [60], 2, 2, 64, 64, 53, scale=-0.2)
-    check([130], [60], 2, 2, 64, 64, 54, scale=0.0)
+    check([130], [200], 16, 2, 128, 64, 51, q_gain=4)
+    check([130], [200], 16, 2, 64, 64, 52, spread=20.0)
+    check([130], [60], 16, 2, 64, 64, 53, scale=-0.2)
+    check([130], [60], 16, 2, 64, 64, 54, scale=0.0)
 
 
 def test_growing_maxima_rescale_the_sums():
@@ -121,7 +123,7 @@ def test_growing_maxima_rescale_the_sums():
     c = Cache([n], 1, D, 64, 61)
     cache, table = c.to_device()
     k, _ = c.values(0, n)
-    q = np.zeros((200, 2, D), f32)
+    q = np.zeros((200, 6, D), f32)
     # a direction along which the keys grow with their position
     c.k[...] = 0
     for t in range(n):
@@ -129,7 +131,7 @@ def test_growing_maxima_rescale_the_sums():
     c.ks[...] = 0.5
     cache, table = c.to_device()
     q[..., 0] = 16.0
-    out = torch.empty((200, 2, D), dtype=torch.bfloat16, device=device())
+    out = torch.empty((200, 6, D), dtype=torch.bfloat16, device=device())
     q4.q4_kv_attention(out, dev(q, torch.bfloat16), cache, table, i32([n]), i32([0, 200]), 200, n, scale=1.0)
     ref, tol = reference(c, q, [200], [n], 1.0, 0, True)
     got = out.float().cpu().numpy()
@@ -142,8 +144,8 @@ def test_nothing_to_see_and_missing_pages():
     c = Cache([0, 30, 300], 1, 64, 16, 81)
     cache, table = c.to_device()
     new = [70, 100, 120]
-    q = bf16(rng(82).standard_normal((290, 2, 64)).astype(f32))
-    out = torch.full((290, 2, 64), float("nan"), dtype=torch.bfloat16, device=device())
+    q = bf16(rng(82).standard_normal((290, 16, 64)).astype(f32))
+    out = torch.full((290, 16, 64), float("nan"), dtype=torch.bfloat16, device=device())
     args = (i32([0, 30, 300]), i32(starts(new)), 120, 300)
     q4.q4_kv_attention(out, dev(q, torch.bfloat16), cache, table, *args)
     assert q4.q4_get_device_status() == q4.Q4_OK
@@ -160,7 +162,7 @@ def test_nothing_to_see_and_missing_pages():
     seen = np.ones(300, bool)
     seen[16:32] = seen[160:176] = False
     for j in (0, 60, 119):
-        for h in range(2):
+        for h in range(16):
             ok = seen & (np.arange(300) <= 180 + j)
             p = np.exp(k[ok, 0] @ q[170 + j, h].astype(np.float64) / 8)
             want = p @ v[ok, 0] / p.sum()
@@ -171,8 +173,8 @@ def test_longer_sequences_than_the_call_says():
     """kv_len above max_kv: zeros and an error, nothing out of range."""
     c = Cache([300, 300], 1, 64, 16, 91)
     cache, table = c.to_device()
-    q = dev(rng(92).standard_normal((200, 2, 64)).astype(f32), torch.bfloat16)
-    out = torch.full((200, 2, 64), float("nan"), dtype=torch.bfloat16, device=device())
+    q = dev(rng(92).standard_normal((200, 16, 64)).astype(f32), torch.bfloat16)
+    out = torch.full((200, 16, 64), float("nan"), dtype=torch.bfloat16, device=device())
     q4.q4_kv_attention(out, q, cache, table, i32([300, 300]), i32([0, 100, 200]), 100, 120)
     assert q4.q4_get_device_status() == q4.Q4_ERR_DEVICE and q4.q4_last_device_flags() == q4.Q4_DEVERR_INDEX
     assert np.all(out.float().cpu().numpy() == 0)
@@ -181,16 +183,16 @@ def test_longer_sequences_than_the_call_says():
 def test_a_bad_query_stays_in_its_row():
     c = Cache([150], 2, 64, 16, 95)
     cache, table = c.to_device()
-    x = rng(96).standard_normal((150, 4, 64)).astype(f32)
+    x = rng(96).standard_normal((150, 16, 64)).astype(f32)
     bad = x.copy()
     bad[50, 2, 5], bad[140, 0, 0] = np.nan, np.inf
     outs = []
     for q in (x, bad):
-        out = torch.empty((150, 4, 64), dtype=torch.bfloat16, device=device())
+        out = torch.empty((150, 16, 64), dtype=torch.bfloat16, device=device())
         q4.q4_kv_attention(out, dev(q, torch.bfloat16), cache, table, i32([150]), i32([0, 150]), 150, 150)
         outs.append(out.float().cpu().numpy())
     assert np.isnan(outs[1][50, 2]).all() and np.isnan(outs[1][140, 0]).all()
-    same = np.ones((150, 4), bool)
+    same = np.ones((150, 16), bool)
     same[50, 2] = same[140, 0] = False
     assert np.array_equal(outs[0][same], outs[1][same])
 
@@ -199,11 +201,11 @@ def test_in_a_graph():
     c = Cache([700, 300], 2, 128, 64, 101)
     cache, table = c.to_device()
     new = [130, 1]
-    q = bf16(rng(102).standard_normal((131, 8, 128)).astype(f32))
+    q = bf16(rng(102).standard_normal((131, 16, 128)).astype(f32))
     lens, cu = i32([700, 300]), i32(starts(new))
     qd = dev(q, torch.bfloat16)
-    ws = torch.zeros(q4.q4_kv_attention_workspace_size(cache, 8, 2, 131, 130, 700), dtype=torch.uint8, device=device())
-    out = torch.empty((131, 8, 128), dtype=torch.bfloat16, device=device())
+    ws = torch.zeros(q4.q4_kv_attention_workspace_size(cache, 16, 2, 131, 130, 700), dtype=torch.uint8, device=device())
+    out = torch.empty((131, 16, 128), dtype=torch.bfloat16, device=device())
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     g = torch.cuda.CUDAGraph()
