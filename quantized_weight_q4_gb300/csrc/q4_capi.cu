@@ -754,7 +754,7 @@ int moe_run(DeviceState* s, const MoeShape& m, float* out, const void* x, int x_
 
 extern "C" {
 
-int q4_version(void) { return 100; }
+int q4_version(void) { return 101; }
 
 const char* q4_status_str(int status) {
   switch (status) {

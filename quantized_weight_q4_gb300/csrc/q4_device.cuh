@@ -16,7 +16,6 @@ constexpr int kBlockCols = 32;    // weights per block
 // Device status bits (mirrors Q4_DEVERR_* of the public header).
 constexpr unsigned kDevErrIndex = 0x1u;
 constexpr unsigned kDevErrTimeout = 0x2u;
-constexpr unsigned kDevErrValue = 0x4u;
 
 // Upper bound of any spin-wait, in nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;

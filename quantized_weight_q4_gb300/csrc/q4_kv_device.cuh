@@ -8,6 +8,9 @@
 
 namespace q4 {
 
+// Device status bit: a NaN or an infinity was given to the cache (Q4_DEVERR_VALUE of the public header).
+constexpr unsigned kDevErrValue = 0x4u;
+
 // Lets `kernel` use `bytes` of dynamic shared memory; asked once for each
 // device (`done`: a bit for each, one word a kernel).
 template <typename K>
