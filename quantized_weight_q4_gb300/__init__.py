@@ -401,13 +401,18 @@ class KVCache:
 
     def __init__(self, k, v, k_scale, v_scale):
         shape = pages, heads, page, dim = k.shape
+        scales = pages * heads * (page // Q4_KV_BLOCK)
         if k.dtype is not _torch.int8 or v.dtype is not _torch.int8 or v.shape != shape:
             raise TypeError("k and v are int8 tensors of one shape")
-        want = (pages, heads, page // Q4_KV_BLOCK)
         if (k_scale.dtype is not _torch.float32 or v_scale.dtype is not _torch.float32
-                or k_scale.shape != want or v_scale.shape != want):
-            raise TypeError(f"k_scale and v_scale are fp32 tensors of shape {want}")
-        _require_cuda(k, v, k_scale, v_scale)
+                or k_scale.numel() != scales or v_scale.numel() != scales):
+            raise TypeError(f"k_scale and v_scale are fp32 tensors of shape "
+                            f"{(pages, heads, page // Q4_KV_BLOCK)}")
+        if not (k.is_cuda and v.is_cuda and k_scale.is_cuda and v_scale.is_cuda):
+            raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+        if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous()):
+            raise ValueError("all tensors must be contiguous")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                     v_scale.data_ptr(), pages, heads, dim, page)
@@ -434,13 +439,23 @@ def _rows(t, heads, dim):
     return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
-def _index(name, t, n, rows=False):
-    """Data pointer of a contiguous int32 CUDA tensor of n elements (rows: [n, any])."""
+def _index(name, t, n):
+    """Data pointer of a contiguous int32 CUDA tensor of n elements."""
     if t.dtype is not _torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} is a contiguous int32 CUDA tensor")
-    if (t.dim() != 2 or t.shape[0] != n) if rows else t.numel() != n:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(n, 'any') if rows else (n,)}")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
     return t.data_ptr()
+
+
+def _table(t, n):
+    """Data pointer and columns of a contiguous int32 CUDA tensor of n rows."""
+    if t.dtype is not _torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError("page_table is a contiguous int32 CUDA tensor")
+    rows, cols = t.shape
+    if rows != n:
+        raise ValueError(f"page_table has {rows} rows, not {n}")
+    return t.data_ptr(), cols
 
 
 def _floats(name, t, n):
@@ -495,10 +510,11 @@ def q4_kv_append(cache: KVCache, q_out, q, k, v, page_table, kv_len, cu_q, cos=N
         table = RopeStruct(_floats("cos", cos, n * half), _floats("sin", sin, n * half), n, 2 * half,
                            rope_style)
         rope = ctypes.addressof(table)
+    pages, cols = _table(page_table, B)
     rc = lib().q4_kv_append(
         cache.ref, out, out_dtype, qp, qs, kp, ks, vp, vs, dtype, Hq, rope,
         _floats("q_norm", q_norm, dim), _floats("k_norm", k_norm, dim), eps,
-        _index("page_table", page_table, B, True), page_table.shape[1],
+        pages, cols,
         _index("kv_len", kv_len, B), _index("cu_q", cu_q, B + 1), B, T, _raw_stream(stream, k))
     if rc:
         raise Q4Error("q4_kv_append", rc)
@@ -513,8 +529,9 @@ def q4_kv_gather(k_out, v_out, cache: KVCache, page_table, first, cu, stream=Non
     vp, v_dtype = _out("v_out", v_out, n)
     if v_dtype != dtype:
         raise ValueError("k_out and v_out have one type")
+    pages, cols = _table(page_table, B)
     rc = lib().q4_kv_gather(
-        kp, vp, dtype, cache.ref, _index("page_table", page_table, B, True), page_table.shape[1],
+        kp, vp, dtype, cache.ref, pages, cols,
         _index("first", first, B), _index("cu", cu, B + 1), B, T, _raw_stream(stream, k_out))
     if rc:
         raise Q4Error("q4_kv_gather", rc)
@@ -536,9 +553,10 @@ def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int
     if workspace is not None:
         _require_cuda(workspace)
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    pages, cols = _table(page_table, B)
     rc = lib().q4_kv_attention(
         op, out_dtype, qp, q_dtype, qs, Hq, cache.ref,
-        _index("page_table", page_table, B, True), page_table.shape[1],
+        pages, cols,
         _index("kv_len", kv_len, B), _index("cu_q", cu_q, B + 1), B, T, max_q, max_kv, total_kv,
         dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, ws, ws_bytes,
         _raw_stream(stream, q))

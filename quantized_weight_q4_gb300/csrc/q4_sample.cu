@@ -35,7 +35,7 @@ constexpr int kPer = kBins / kThreads;       // bins a thread
 constexpr int kUnit = kWarps * 128;          // a CTA's elements are a multiple of this
 constexpr float kPerNat = 36.0f;             // coarse bins: 1024 / 36 = 28.4 > 40 ln 2 nats
 constexpr int kList = 2048;                  // longest list
-constexpr int kListK = 1024;                 // top-k up to which all kept tokens go on the list
+constexpr int kListK = 1600;                 // top-k times CTAs up to which the list takes all that may be kept
 constexpr int kRowCtas = 8;
 constexpr int kSliceBytes = 160 * 1024;      // most elements a CTA holds
 typedef unsigned long long u64;
@@ -55,8 +55,8 @@ struct alignas(16) Shared {
   unsigned scan_n[kWarps];
   u64 scan_w[kWarps];
   float top[kRowCtas];
-  u64 sums[kWarps];                          // weight before the cut, and tokens at it, of each warp's elements
-  unsigned ties[kWarps];
+  u64 sums[kRowCtas * kWarps];               // weight before the cut, and tokens at it, of every warp's elements
+  unsigned ties[kRowCtas * kWarps];
   float red[kWarps];
   u64 part[kWarps];                       // the same of the pieces of one warp's elements
   unsigned part_ties[kWarps];
@@ -274,15 +274,18 @@ __device__ __forceinline__ void near_histogram(Shared& s, const R& r, Bins& out)
   add_up(s, r, out);
 }
 
-// Counts of the threads' largest z (theirs: its maximum): the k-th largest of
-// those is at most the k-th largest of all, and not much below it.
+// Counts of this CTA's threads' largest z (theirs: its maximum), in this CTA alone: the k-th largest of those is at
+// most the CTA's k-th largest z, and not much below it.
 template <typename R>
 __device__ __forceinline__ void top_histogram(Shared& s, const R& r, float theirs, Bins& out) {
   clear_bins(s);
   __syncthreads();
   const float d = r.top - theirs;
   if (d < kZero) add_bin(s, coarse(d), 0, true, false);
-  add_up(s, r, out);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) out.n[j] = s.hist[0][kPer * threadIdx.x + j], out.w[j] = 0;
+  scan_bins(s, out);
 }
 
 // The bin in which the count (or weight) reaches `target` (1 or more, at most
@@ -564,8 +567,9 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
   } else if (by_k || by_p) {
     Bins bins;
     bool done = false;
-    if (by_k && k <= kListK) {
-      // a short top-k: every token that may be kept goes on the list
+    if (by_k && k * ctas <= kListK) {
+      // a short top-k: every token that may be kept goes on the list.  The row's first k are among the CTAs' first
+      // k, so each CTA finds for itself how far down it has to look
       top_histogram(s, r, theirs, bins);
       unsigned tops = 0;
 #pragma unroll
@@ -631,7 +635,11 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   same = __reduce_add_sync(0xffffffffu, same);
-  if (lane == 0) s.sums[warp] = sum, s.ties[warp] = same;
+  // to every CTA: none reads another's shared memory after this, so that each may leave when it is done
+  if (lane < ctas) {
+    st_peer_u64(peer_addr(&s.sums[rank * kWarps + warp], lane), sum);
+    st_peer_u32(peer_addr(&s.ties[rank * kWarps + warp], lane), same);
+  }
   cluster_sync();
   // every warp: the weight before its own elements, and all of it
   const float tie_e = expf(cut_z - r.top);
@@ -644,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
   for (int q = 0; q < kQ; ++q) {
     const int i = 32 * q + lane;
     const bool have = i < ctas * kWarps;
-    x[q] = have ? ld_peer_u64(peer_addr(&s.sums[i % kWarps], i / kWarps)) : 0;
-    at[q] = have ? ld_peer_u32(peer_addr(&s.ties[i % kWarps], i / kWarps)) : 0;
+    x[q] = have ? s.sums[i] : 0;
+    at[q] = have ? s.ties[i] : 0;
   }
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
@@ -719,7 +727,6 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
       }
     }
   }
-  cluster_sync();   // peers may still read this CTA's sums
 }
 
 // CTAs of a row: up to four while each has 4096 elements or more, and eight where four would leave room for
