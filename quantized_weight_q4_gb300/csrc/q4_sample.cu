@@ -13,13 +13,22 @@
 // Weights are whole numbers, so that no sum depends on its order.
 //
 // One thread-block cluster takes one row and keeps it in shared memory: the
-// logits are read once, and HBM or, for few rows, the exchanges between the
-// CTAs bound the call.  Whether a token is kept is a comparison with one cut,
+// logits are read once.  Whether a token is kept is a comparison with one cut,
 // a z and how many tokens of that z stay (by index).  The cut is found from a
 // histogram over z (bins of 1/36 nat, added over the CTAs through distributed
 // shared memory) and, of the bins that matter, a list of their z that every
-// CTA gathers and searches for itself.  Where the list would be too long
-// (thousands of equal logits) further histograms narrow it down.
+// CTA gathers and searches for itself; a short top-k needs no histogram of the
+// row, its list is what a CTA finds above the k-th of its threads' maxima.
+// Where the list would be too long (thousands of equal logits) further
+// histograms narrow it down.
+//
+// What bounds it: for few rows the chain of barriers and exchanges between the
+// CTAs (one row of 32,000 logits: 8 us greedy, 13 us top-k, 15 us top-k and
+// top-p; its bytes need 0.02 us).  For many, the work on each logit whose
+// weight counts: 200 rows of 128,007 bf16 logits (51 MB, 7.5 us) take 29 us
+// greedy, 54 us without limits, 63 us with top-k, 73 us with top-k and top-p
+// and 119 us with top-p alone, which has to weigh every logit; the issue slots
+// are 55% full with the mixture that a batch of requests has (79 us).
 #include <cfloat>
 
 #include "q4_kernels.h"
@@ -71,11 +80,6 @@ static_assert(sizeof(Shared) % 16 == 0, "the elements after it are stored 16 byt
 __device__ __forceinline__ unsigned ld_peer_u32(uint32_t a) {
   unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ u64 ld_peer_u64(uint32_t a) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_peer_u32(uint32_t a, unsigned v) {
@@ -135,25 +139,46 @@ struct Row {
     if (BF16) return clean(bf16_bits_to_f32(static_cast<const uint16_t*>(x)[base + i]), inv);
     return clean(static_cast<const float*>(x)[base + i], inv);
   }
-  // elements i .. i + 3, i a multiple of 4
-  __device__ __forceinline__ float4 z4(int i) const {
+};
+
+// 16 bytes of elements, as they came.
+template <bool BF16>
+struct Group {
+  static constexpr int kN = BF16 ? 8 : 4;
+  uint4 w;
+
+  // the largest (a NaN only if there is nothing else)
+  __device__ __forceinline__ float largest() const {
     if (BF16) {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + base + i);
-      return make_float4(clean(__uint_as_float(w.x << 16), inv), clean(__uint_as_float(w.x & 0xffff0000u), inv),
-                         clean(__uint_as_float(w.y << 16), inv), clean(__uint_as_float(w.y & 0xffff0000u), inv));
+      unsigned a, b;
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+      return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
     }
-    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + base + i);
-    return make_float4(clean(f.x, inv), clean(f.y, inv), clean(f.z, inv), clean(f.w, inv));
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+  __device__ __forceinline__ float get(int j) const {
+    const unsigned v = (&w.x)[BF16 ? j >> 1 : j];
+    return __uint_as_float(!BF16 || (j & 1) ? (BF16 ? v & 0xffff0000u : v) : v << 16);
   }
 };
 
-// Every element of the warp's, four a lane at a time.
-template <typename R, typename F>
-__device__ __forceinline__ void each(const R& r, F f) {
+// The warp's elements, 16 bytes a lane at a time: f(z) of those in groups
+// whose largest z passes `want`.  z grows with the logit, so one test speaks
+// for the group; most groups hold nothing that a pass looks for.  Testing
+// every element instead: 200 rows of 128,007 bf16 logits 40 us greedy, 83 us
+// with top-k and top-p; so 29 and 73 us.
+template <bool BF16, typename W, typename F>
+__device__ __forceinline__ void each(const Row<BF16>& r, W want, F f) {
+  using G = Group<BF16>;
 #pragma unroll 2
-  for (int i = 4 * (threadIdx.x & 31); i < r.n; i += 128) {
-    const float4 z = r.z4(i);
-    f(z.x), f(z.y), f(z.z), f(z.w);
+  for (int i = G::kN * (threadIdx.x & 31); i < r.n; i += 32 * G::kN) {
+    const G g = {*reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(r.x) + (r.base + i) * (BF16 ? 2 : 4))};
+    if (want(clean(g.largest(), r.inv))) {
+#pragma unroll
+      for (int j = 0; j < G::kN; ++j) f(clean(g.get(j), r.inv));
+    }
   }
 }
 
@@ -242,7 +267,7 @@ __device__ __forceinline__ void histogram(Shared& s, const R& r, bool want_n, bo
                                           Bins& out) {
   clear_bins(s);
   __syncthreads();
-  each(r, [&](float z) {
+  each(r, [&](float z) { return r.top - z < kZero; }, [&](float z) {
     const float d = r.top - z;
     if (!(d < kZero)) return;
     const int b = bin_of(z, d);
@@ -260,7 +285,7 @@ __device__ __forceinline__ void near_histogram(Shared& s, const R& r, Bins& out)
   clear_bins(s);
   __syncthreads();
   u64 rest = 0;
-  each(r, [&](float z) {
+  each(r, [&](float z) { return r.top - z < kZero; }, [&](float z) {
     const float d = r.top - z;
     const u64 w = weight(expf(-d));
     if (d < kNear)
@@ -391,15 +416,15 @@ __device__ __forceinline__ Cut cut_of_list(Shared& s, int n, float top, bool by_
   return cut_at(lo, top, by_weight, left, done_w);
 }
 
-// The codes of all elements with want(d) into s.all of every CTA; returns how
-// many there are, more than kList: too many for the list.
-template <typename R, typename F>
-__device__ __forceinline__ unsigned gather_list(Shared& s, const R& r, F want) {
+// The codes of all elements in the coarse bins first .. last into s.all of
+// every CTA; returns how many there are, more than kList: too many for the list.
+template <typename R>
+__device__ __forceinline__ unsigned gather_list(Shared& s, const R& r, int first, int last) {
   if (threadIdx.x == 0) s.list_n = 0;
   __syncthreads();
-  each(r, [&](float z) {
-    const float d = r.top - z;
-    if (d < kZero && want(d)) {
+  const auto reach = [&](float z) { return r.top - z < kZero && coarse(r.top - z) <= last; };
+  each(r, reach, [&](float z) {
+    if (reach(z) && coarse(r.top - z) >= first) {
       const unsigned at = atomicAdd(&s.list_n, 1u);
       if (at < kList) s.list[at] = falling(z);
     }
@@ -436,7 +461,7 @@ __device__ __noinline__ Cut cut_by_bins(Shared& s, const R& r, int b1, bool by_w
   done_w += s.before_w;
   left -= by_weight ? s.before_w : s.before_n;
   code_range(s, [&](auto see) {
-    each(r, [&](float z) {
+    each(r, [&](float z) { return r.top - z < kZero; }, [&](float z) {
       const float d = r.top - z;
       if (d < kZero && coarse(d) == b1 && fine(d, b1) == b2) see(falling(z));
     });
@@ -469,7 +494,7 @@ template <typename R>
 __device__ __forceinline__ Cut cut_in_bin(Shared& s, const R& r, bool by_weight, u64 target) {
   const int b = s.bin;
   const u64 done_w = s.before_w, left = target - (by_weight ? s.before_w : s.before_n);
-  const unsigned n = gather_list(s, r, [&](float d) { return coarse(d) == b; });
+  const unsigned n = gather_list(s, r, b, b);
   if (n <= kList) return cut_of_list(s, static_cast<int>(n), r.top, by_weight, left, done_w);
   return cut_by_bins(s, r, b, by_weight, left, done_w);
 }
@@ -534,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();   // a warp reads its own elements only
   float top = -INFINITY;
-  each(r, [&](float z) { top = fmaxf(top, z); });
+  each(r, [&](float z) { top = fmaxf(top, z); return false; }, [](float) {});
   const float theirs = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -579,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
         find_bin(s, bins, false, static_cast<u64>(k));
         last = s.bin;
       }
-      const int n = static_cast<int>(gather_list(s, r, [&](float d) { return coarse(d) <= last; }));
+      const int n = static_cast<int>(gather_list(s, r, 0, last));
       if (n <= kList) {
         cut = cut_of_list(s, n, r.top, false, static_cast<u64>(min(k, n)), 0);
         if (by_p) {
@@ -622,9 +647,11 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
   // kept weight of each warp's elements before the cut, and tokens at it
   const bool has_cut = cut.ties > 0;
   const float cut_z = has_cut ? of_code(cut.code) : -INFINITY;
+  // below `low` a weight is 0 or, by min-p, not kept (the slack is far above the rounding of logf and expf)
+  const float low = r.top - fminf(kZero, min_p > 0.f ? 0.001f - 1.001f * logf(min_p) : kZero);
   u64 sum = 0;
   unsigned same = 0;
-  each(r, [&](float z) {
+  each(r, [&](float z) { return z >= cut_z && z >= low; }, [&](float z) {
     if (z > cut_z) {
       const float e = expf(z - r.top);
       if (e >= min_p) sum += weight(e);
@@ -730,10 +757,11 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
 }
 
 // CTAs of a row: up to four while each has 4096 elements or more, and eight where four would leave room for
-// only one CTA an SM (80 KB of elements each).  Measured with 512 threads each, all limits on: 200 rows of
-// 128,007 bf16 logits 90 us with four, 154 us with eight (clusters of eight seldom fit the SMs that are
-// free); one row of 32,000 logits 23 / 18 / 16.6 / 17 us with one / two / four / eight; 64 rows of 32,000
-// 25 / 24 / 22 / 44 us.
+// only one CTA an SM (80 KB of elements each).  Measured with 512 threads each, top-k and top-p on: 200 rows of
+// 128,007 bf16 logits 73 us with two, 75 us with four, 133 us with eight (clusters of eight seldom fit the SMs
+// that are free), with top-p alone 146 / 123 / 162 us; one row of 32,000 logits 20 / 16.5 / 15.3 / 15.5 us with
+// one / two / four / eight; 64 rows of 32,000 20 / 21 / 20 / 37 us.  128,007 fp32 logits, four and eight: one
+// row 16 and 14 us, 200 rows 113 and 130 us, with top-p alone 171 and 164 us.
 int ctas_of(const SampleParams& p) {
   const int size = p.bf16 ? 2 : 4;
   int c = 1;
