@@ -1,5 +1,7 @@
 /*
- * q4.h -- C ABI of the GB300 (sm_103a) Q4_0 weight-only dequant-matmul library.
+ * q4.h -- C ABI of the GB300 (sm_103a) Q4_0 weight-only dequant-matmul library,
+ * and of what a decode loop runs between the matmuls: a paged 8-bit key/value
+ * cache, attention over it, and sampling ("Serving", at the end).
  *
  * The operation (C++ DeepSeek engine page, "用两千行 C++ 重写一个 DeepSeek 推理引擎",
  * §2.2 block_q4_0 / dequantize, §2.3 layout and padding, §3.4 matmul_q4_0):
@@ -182,7 +184,8 @@ Q4_API int q4_matmul_bf16_tiles(void *C, int c_dtype, const void *A, const void 
 /*
  * q4_release_scratch -- waits for the current device to finish all work,
  * then frees every buffer the library owns on it: the per-stream scratch of
- * the small-M GEMM and the library-owned workspace of the routed-expert calls
+ * the small-M GEMM and of the cache attention, and the library-owned workspace
+ * of the routed-expert calls
  * (with the ones larger calls replaced, kept until now because CUDA graphs
  * captured earlier may use them).  A graph captured with a NULL workspace
  * must not be replayed after this call.  Returns Q4_OK or Q4_ERR_CUDA.
@@ -589,7 +592,10 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
  *           that holds more records Q4_DEVERR_INDEX and gets zeros.
  * A query that sees nothing gets zeros.  Accuracy: the codes are exact in
  * every product; with fp32 q and out the result is that of fp32 arithmetic,
- * with bf16 the weights are rounded to fp16.
+ * with bf16 the weights are rounded to fp16.  Weights are held relative to the
+ * largest value scale met, with full precision down to 2^-23 of it (bf16:
+ * 2^-23 with 11 bits): a block whose scale is smaller than that by more loses
+ * bits of its share.
  *   workspace  q4_kv_attention_workspace_size bytes, 16-byte aligned, the first 4 KB zero
  *              before its first use; every completed call leaves them zero.
  *              Calls that share it must not overlap.  NULL: scratch the

@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) Q4_0 weight-only dequant-matmul: the Python binding.
+"""GB300 (sm_103a) Q4_0 weight-only dequant-matmul and the serving operators
+beside it (paged 8-bit key/value cache, attention, sampling): the Python binding.
 
 A thin ctypes layer over the C ABI declared in ``include/q4.h``.  Every
 function marshals arguments only (device pointers, sizes, the current torch

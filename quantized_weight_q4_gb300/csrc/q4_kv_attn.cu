@@ -10,14 +10,14 @@
 //   query rows (the queries that share the head: token-major, up to 16 rows).
 //   The units of all sequences, heads and tiles form one line (with some empty
 //   ones before each (sequence, tile, head), for what starting one costs), which
-//   is cut into equal ranges, whatever the sequences' lengths.  A CTA
-//   whose range ends inside a (sequence, head, tile) writes its share of the
+//   is cut into equal ranges, whatever the sequences' lengths.  A range is
+//   worked on by a team of warps, a whole CTA or a quarter of one.  A team whose
+//   range begins or ends inside a (sequence, tile, head) writes its share of the
 //   sum (with the maximum and the weights' sum) to the workspace; the last of
-//   the CTAs that share it adds the shares in order.
-//   A range is worked on by a team of warps, a whole CTA or a quarter of one.
+//   the teams that share it adds the shares in order.
 // * Each warp of a team streams blocks of its own (every fourth or sixteenth)
-//   through its own ring of asynchronous copies, so that no warp waits for another until
-//   the shares of the warps are added.
+//   through its own ring of asynchronous copies, so that no warp waits for
+//   another until the shares of the warps are added.
 // * Codes are integers up to 127, exact in fp16, as are bf16 queries scaled
 //   by a power of two per row; fp32 queries and the softmax weights are split
 //   into two fp16 terms (22 bits) that fill the two halves of the MMA's 16
@@ -25,6 +25,17 @@
 //   same cost.  Products accumulate in fp32.
 // * A block's scale is one number per MMA tile: the key scale multiplies the
 //   scores, the value scale the weights, relative to the largest so far.
+//
+// Measured (8 kv heads of 128, 32 query heads, bf16): 64 sequences of 4096
+// tokens 110 us, 4.9 TB/s of codes and scales; 64 sequences of 50 to 8191
+// tokens 127 us, 4.1 TB/s; one of 131,071 58 us, 4.6 TB/s; one of 390 with 32
+// kv heads 10 us.  What bounds the long ones is not HBM (53% busy) but the
+// widening of codes to fp16: about 520 instructions for each block and warp,
+// of which 32 are MMAs and 190 turn codes into fp16 pairs, issued in 51% of the
+// cycles by the 16 warps that 128 registers a thread leave room for.  Short
+// ones wait for a chain of page lookup, copy, product and join.
+// Two blocks a step, under one softmax, need more registers than there are:
+// 136 us for the batch.
 #include <algorithm>
 #include <cfloat>
 
@@ -684,8 +695,9 @@ cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
 template <int D, bool SPLIT>
 cudaError_t launch(const AttnParams& p, int rows, int grid, cudaStream_t st) {
   // Teams of four while there are more (sequence, tile, head)s than SMs: a team's start and end then fall into the
-  // others' streams (64 sequences of 50 to 8191 tokens, 8 heads: 138 us, 166 us with whole CTAs).  With fewer,
-  // whole CTAs, which leave a quarter of the shares to join.
+  // others' streams (quarters / whole CTAs: 64 sequences of 50 to 8191 tokens, 8 heads, 126 / 160 us; of 4096
+  // tokens 110 / 127 us).  With fewer, whole CTAs, which leave a quarter of the shares to join (one sequence of
+  // 131,071 tokens 89 / 58 us, 8 of 1024 17 / 14 us).
   const long long tiles = (rows + (SPLIT ? 7 : 15)) / (SPLIT ? 8 : 16);
   return p.a.b.B * tiles * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams>(p, grid, st)
                                               : launch<D, SPLIT, kWarps>(p, grid, st);
@@ -707,8 +719,8 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   p.max_rows = max_rows;
   p.tickets = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
-  // fp32 in or out needs two terms; bf16 takes them too while eight rows are enough (a thread then has one row's
-  // softmax instead of two)
+  // fp32 in or out needs two terms; bf16 takes them too while eight rows are enough: a thread then has one row's
+  // softmax instead of two (64 sequences of 50 to 8191 tokens 127 us, 133 us with rows in both halves)
   const int rows = static_cast<int>(std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows));
   const bool split = !a.q_bf16 || !a.out_bf16 || rows <= 8;
   if (a.c.dim == 128) return split ? launch<128, true>(p, rows, sms, st) : launch<128, false>(p, rows, sms, st);

@@ -12,12 +12,22 @@
 // * q4_kv_prompt_kernel: a CTA takes 256 query rows of one kv head (the query
 //   heads that share it, token-major) as two MMA tiles of 128, and walks over
 //   the visible tiles of 128 tokens.  One warp copies K and V tiles with TMA
-//   into a ring, one thread issues the MMAs, and four warps a tile (a thread a
+//   into a ring, one warp issues the MMAs, and four warps a tile (a thread a
 //   row) take the scores from tensor memory, form the weights and put them
 //   back as the fp16 A operand of the second product.  While one tile's rows
 //   are in the softmax the tensor cores work on the other's.  The running
 //   maximum moves only when it has grown by 2^8, so the sums in tensor memory
 //   are seldom rescaled.
+//
+// Measured (8 kv heads of 128, 32 query heads): a prompt of 8192 tokens 406 us
+// both launches, 1354 TFLOP/s of visible products (72% of the measured bf16
+// peak of cuBLAS; tiles on the diagonal do up to twice the visible work); six
+// pieces of up to 1537 tokens on up to 9000 cached ones 515 us, 1137 TFLOP/s.
+// The tensor pipe is 62% busy by its counter: what is left is the chain of a
+// tile (scores out of tensor memory, 128 exponentials a thread, weights back)
+// where two tiles an SM do not cover one another, and for the pieces the last
+// round of CTAs and the expansion.  The MMA warp runs its loop as a whole, with
+// one lane issuing: elected before the loop, its single lane took 532 us.
 #include <cfloat>
 
 #include <cuda.h>
