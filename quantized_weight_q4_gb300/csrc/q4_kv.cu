@@ -14,10 +14,10 @@
 //
 // Both move each byte once and are bound by HBM at best.  Measured: appending
 // 21,039 tokens of 7 sequences (32 + 8 heads of 128, bf16, norms, rotation;
-// 571 MB) 127 us, 4.5 TB/s; the rest is instruction issue (62% of the cycles)
+// 475 MB) 101 us, 4.7 TB/s; the rest is instruction issue (66% of the cycles)
 // and the chain from a token's sequence to its position to its cosines.  One
-// token takes 7 us on the device.  Reading 24 sequences of 100 to 6001 tokens
-// back to bf16 (455 MB) 76 us, 6.0 TB/s.
+// token takes 3 us.  Reading 24 sequences of 100 to 6001 tokens back to bf16
+// (455 MB) 76 us, 6.0 TB/s.
 #include <cfloat>
 
 #include "q4_kernels.h"
@@ -28,6 +28,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+// Measured with the tokens above, append and gather, an earlier step (156 us): four query heads a warp 174 us, sixteen
+// 205 us; four warps a block 170 us.
 constexpr int kQRows = 8;              // query heads of one token a warp takes
 constexpr int kBlockWarps = 2;         // warps that share a block of keys or values
 constexpr int kHeads = kWarps / (2 * kBlockWarps);   // kv heads of a CTA
@@ -46,17 +48,17 @@ struct Row {
   float x[8];
 };
 
-template <int D>
-__device__ __forceinline__ void load_row(const void* base, long long off, int bf16, int l, Row<D>& r) {
+// A lane's elements of a row; `at`: the address of the first.
+template <int D, bool BF16>
+__device__ __forceinline__ void load_row(const uint8_t* at, Row<D>& r) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const long long at = off + h * (D / 2) + 4 * l;
-    if (bf16) {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+    if (BF16) {
+      const uint2 w = *reinterpret_cast<const uint2*>(at + h * D);
       r.x[4 * h] = __uint_as_float(w.x << 16), r.x[4 * h + 1] = __uint_as_float(w.x & 0xffff0000u);
       r.x[4 * h + 2] = __uint_as_float(w.y << 16), r.x[4 * h + 3] = __uint_as_float(w.y & 0xffff0000u);
     } else {
-      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+      const float4 w = *reinterpret_cast<const float4*>(at + 2 * h * D);
       r.x[4 * h] = w.x, r.x[4 * h + 1] = w.y, r.x[4 * h + 2] = w.z, r.x[4 * h + 3] = w.w;
     }
   }
@@ -84,43 +86,59 @@ __device__ __forceinline__ void store_row(void* base, long long off, int bf16, i
   }
 }
 
-// This lane's eight weights of a norm.
+// This lane's eight weights of a norm (aligned to a float only).
 template <int D>
 __device__ __forceinline__ void load_weights(const float* w, int l, float (&y)[8]) {
+  if (reinterpret_cast<uintptr_t>(w) & 15u) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __ldg(w + (i >> 2) * (D / 2) + 4 * l + (i & 3));
+    for (int i = 0; i < 8; ++i) y[i] = __ldg(w + (i >> 2) * (D / 2) + 4 * l + (i & 3));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(w + h * (D / 2) + 4 * l));
+      y[4 * h] = u.x, y[4 * h + 1] = u.y, y[4 * h + 2] = u.z, y[4 * h + 3] = u.w;
+    }
+  }
 }
 
 // x <- (x * 1/sqrt(mean(x^2) + eps)) * w, one rounding a step; the sum of squares neighbours first: in the lane,
-// over the row's lanes (both halves of the head), then the halves.  The N rows of a lane take one square root and
-// one reciprocal together: lane i of a row's lanes has row i's.
+// over the row's lanes (both halves of the head), then the halves.  The 2 N sums of a lane's N rows are added
+// together: at each step a lane hands half of them to its partner and keeps the others, so that a row's sum ends in
+// some of the lanes, which take its square root and reciprocal.
 template <int D, int N>
-__device__ __forceinline__ void norm_rows(Row<D> (&r)[N], const float (&w)[8], float eps, int l) {
+__device__ __forceinline__ void norm_rows(Row<D> (&r)[N], const float (&w)[8], float eps) {
   constexpr int kLanes = Row<D>::kLanes;
-  static_assert(N <= kLanes, "a lane for each row");
-  float mine = 0.f;
+  static_assert((N == 2 || N == 4) && 2 * N <= kLanes, "a lane for each sum");
+  const int lane = threadIdx.x & 31;
+  float s[2 * N];                                 // [half][row]
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    float s[2];
+  for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float* x = r[n].x + 4 * h;
-      s[h] = __fadd_rn(__fadd_rn(__fmul_rn(x[0], x[0]), __fmul_rn(x[1], x[1])),
-                       __fadd_rn(__fmul_rn(x[2], x[2]), __fmul_rn(x[3], x[3])));
+      s[h * N + n] = __fadd_rn(__fadd_rn(__fmul_rn(x[0], x[0]), __fmul_rn(x[1], x[1])),
+                               __fadd_rn(__fmul_rn(x[2], x[2]), __fmul_rn(x[3], x[3])));
     }
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) {
+  for (int o = 1; o < kLanes; o <<= 1) {
+    const int m = N / o;                          // sums that a lane keeps
+    if (m >= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < m; ++i) {
+        const float keep = up ? s[i + m] : s[i], give = up ? s[i] : s[i + m];
+        s[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, o));
+      }
+    } else {
       s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], o));
-      s[1] = __fadd_rn(s[1], __shfl_xor_sync(0xffffffffu, s[1], o));
     }
-    const float sum = __fadd_rn(s[0], s[1]);
-    if (N == 1 || l == n) mine = sum;
   }
-  const float mean = __fmul_rn(mine, 1.0f / D);   // exact: a power of two
+  const float sum = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], 1));   // bit 0 of the lane: the half
+  const float mean = __fmul_rn(sum, 1.0f / D);    // exact: a power of two
   const float k = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, eps)));
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const float f = N == 1 ? k : __shfl_sync(0xffffffffu, k, n, kLanes);
+  for (int n = 0; n < N; ++n) {                   // the next bits: the row, its upper bit first
+    const float f = __shfl_sync(0xffffffffu, k, N == 4 ? (n & 2) | (n & 1) << 2 : n << 1, kLanes);
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[n].x[i] = __fmul_rn(__fmul_rn(r[n].x[i], f), w[i]);
   }
@@ -201,21 +219,18 @@ __device__ __forceinline__ void rotate_row(const KvAppendParams& p, int l, const
 }
 
 // Queries: one warp takes kQRows heads of one token.
-template <int D, int MODE>
-__device__ void append_queries(const KvAppendParams& p, unsigned task, int lane) {
+template <int D, int MODE, bool BF16>
+__device__ __forceinline__ void append_queries(const KvAppendParams& p, unsigned task, int lane) {
   using R = Row<D>;
-  constexpr int kSteps = kQRows / R::kRows;
+  constexpr int kSteps = kQRows / R::kRows, kSize = BF16 ? 2 : 4;
   const unsigned groups = (p.Hq + kQRows - 1) / kQRows;
   const int t = static_cast<int>(task / groups), l = lane % R::kLanes;
   const int h0 = static_cast<int>(task - t * groups) * kQRows + lane / R::kLanes;
   if (t >= p.b.T) return;
-  R r[kSteps];   // on their way while the token's sequence and position are found
+  R r[kSteps];   // on their way while the token's sequence and position are found; past the last head, that one again
+  const uint8_t* src = static_cast<const uint8_t*>(p.q) + (t * p.q_stride + 4 * l) * kSize;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    zero_row(r[i]);
-    const int h = h0 + i * R::kRows;
-    if (h < p.Hq) load_row<D>(p.q, t * p.q_stride + h * D, p.in_bf16, l, r[i]);
-  }
+  for (int i = 0; i < kSteps; ++i) load_row<D, BF16>(src + min(h0 + i * R::kRows, p.Hq - 1) * (D * kSize), r[i]);
   const int b = warp_count_le(p.b.B, t, [&](int j) { return __ldg(p.b.cu + j); });
   int pos = -1;
   if (b < p.b.B && t >= __ldg(p.b.cu + b)) pos = __ldg(p.b.kv_len + b) - (__ldg(p.b.cu + b + 1) - t);
@@ -228,8 +243,9 @@ __device__ void append_queries(const KvAppendParams& p, unsigned task, int lane)
   if (p.q_norm && pos >= 0) {
     float w[8];
     load_weights<D>(p.q_norm, l, w);
-    norm_rows<D, kSteps>(r, w, p.eps, l);
+    norm_rows<D, kSteps>(r, w, p.eps);
   }
+  const long long to = (static_cast<long long>(t) * p.Hq + h0) * D;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     if (pos >= 0) {
@@ -237,22 +253,30 @@ __device__ void append_queries(const KvAppendParams& p, unsigned task, int lane)
     } else {
       zero_row(r[i]);
     }
-    const int h = h0 + i * R::kRows;
-    if (h < p.Hq) store_row<D>(p.q_out, (static_cast<long long>(t) * p.Hq + h) * D, p.out_bf16, l, r[i]);
+    if (h0 + i * R::kRows < p.Hq) store_row<D>(p.q_out, to + i * R::kRows * D, p.out_bf16, l, r[i]);
   }
+}
+
+// The largest of m and eight magnitudes; a NaN stays.
+__device__ __forceinline__ float largest(float m, const float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(x[i]), "f"(x[i + 1]));
+  return m;
 }
 
 // Keys or values: kBlockWarps warps take one block of one head, eight tokens
 // each (s_max: their largest magnitudes).  Slots of a sequence start at
-// cu[b] / 16 + 2 b: at least as many as the blocks it touches.  Every thread of
-// the CTA calls it and meets once.
-template <int D, int MODE>
-__device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k, int part, int lane,
-                             float* s_max) {
+// cu[b] / 16 + 2 b: at least as many as the blocks it touches.  Every warp of
+// a unit (the block's warps) calls it and meets the others once.
+template <int D, int MODE, bool BF16>
+__device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k, int unit, int part,
+                                             int lane, float* s_max, float4* s_turn) {
   using R = Row<D>;
-  constexpr int kSteps = kBlockRows / R::kRows;
+  constexpr int kSteps = kBlockRows / R::kRows, kSize = BF16 ? 2 : 4;
   const int l = lane % R::kLanes;
   int pos0 = 0, lo = 0, hi = 0;      // this lane's rows are at pos0 + i * kRows; those in [lo, hi) are new
+  bool part_new = false;             // not all of the block is
   long long row0 = -1;
   const int b = warp_count_le(p.b.B, slot, [&](int j) { return (__ldg(p.b.cu + j) >> 4) + 2 * j; });
   R r[kSteps];
@@ -264,55 +288,65 @@ __device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k
     const int at = slot - ((c0 >> 4) + 2 * b), blk = (from >> 4) + at;
     if (c1 > c0 && at >= 0 && blk * kKvBlock < len) {
       lo = max(from, blk * kKvBlock), hi = min(len, (blk + 1) * kKvBlock);
+      part_new = hi - lo < kKvBlock;
       pos0 = blk * kKvBlock + part * kBlockRows + lane / R::kLanes;
       const long long tok0 = static_cast<long long>(c0) + (lo - start);   // packed row of position lo
-      row0 = kv_row(p.c, p.b.table, p.b.table_stride, b, blk * kKvBlock, h);
-      if (row0 < 0 || c0 < 0 || tok0 + (hi - lo) > p.b.T || (is_k && MODE != kNone && hi > p.rope_rows)) {
-        if (lane == 0) atomicOr(p.err, kDevErrIndex);
-        row0 = -1;
-      } else {
-        const void* src = is_k ? p.k : p.v;
+      if (c0 >= 0 && tok0 + (hi - lo) <= p.b.T && !(is_k && MODE != kNone && hi > p.rope_rows)) {
+        // the rows, on their way while the page is looked up; for one that is not new, the nearest that is
         const long long stride = is_k ? p.k_stride : p.v_stride;
+        const uint8_t* src = static_cast<const uint8_t*>(is_k ? p.k : p.v) + (tok0 * stride + h * D + 4 * l) * kSize;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          zero_row(r[i]);
-          const int pos = pos0 + i * R::kRows;
-          if (pos >= lo && pos < hi) load_row<D>(src, (tok0 + pos - lo) * stride + h * D, p.in_bf16, l, r[i]);
+          const int pos = min(max(pos0 + i * R::kRows, lo), hi - 1);
+          load_row<D, BF16>(src + (pos - lo) * stride * kSize, r[i]);
+          if (MODE == kHalves && is_k) {        // no registers for these yet: by way of shared memory, the lane's own
+            const float* c = p.cos + static_cast<long long>(pos) * (D / 2) + 4 * l;
+            const float* s = p.sin + static_cast<long long>(pos) * (D / 2) + 4 * l;
+            const uint32_t to = smem_u32(s_turn + 2 * 32 * i + lane);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(c) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to + 32 * 16), "l"(s) : "memory");
+          }
         }
-        if (lo > blk * kKvBlock) s0 = (is_k ? p.c.ks : p.c.vs)[row0 >> 4];
+        row0 = kv_row(p.c, p.b.table, p.b.table_stride, b, blk * kKvBlock, h);
+      }
+      if (row0 < 0) {
+        if (lane == 0) atomicOr(p.err, kDevErrIndex);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      } else if (lo > blk * kKvBlock) {
+        s0 = (is_k ? p.c.ks : p.c.vs)[row0 >> 4];
       }
     }
   }
   if (row0 >= 0) {
-    if (is_k && (p.k_norm || MODE != kNone)) {
-      if (p.k_norm) {
-        float w[8];
-        load_weights<D>(p.k_norm, l, w);
-        norm_rows<D, kSteps>(r, w, p.eps, l);
-      }
+    if (is_k && p.k_norm) {
+      float w[8];
+      load_weights<D>(p.k_norm, l, w);
+      norm_rows<D, kSteps>(r, w, p.eps);
+    }
+    if (is_k && MODE != kNone) {
+      if (MODE == kHalves) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {   // rows that are not new stay zero
-        const int pos = pos0 + i * R::kRows;
-        if (MODE != kNone) {
-          Turn tn;
-          load_turn<D, MODE>(p, max(lo, min(pos, hi - 1)), l, tn);
-          rotate_row<D, MODE>(p, l, tn, r[i]);
+      for (int i = 0; i < kSteps; ++i) {
+        Turn tn;
+        if (MODE == kHalves) {
+          const float4 u = s_turn[2 * 32 * i + lane], v = s_turn[2 * 32 * i + 32 + lane];
+          tn.c[0] = u.x, tn.c[1] = u.y, tn.c[2] = u.z, tn.c[3] = u.w;
+          tn.s[0] = v.x, tn.s[1] = v.y, tn.s[2] = v.z, tn.s[3] = v.w;
+        } else {
+          load_turn<D, MODE>(p, min(max(pos0 + i * R::kRows, lo), hi - 1), l, tn);
         }
-        if (pos < lo || pos >= hi) zero_row(r[i]);   // also with eps 0: 0 / 0
+        rotate_row<D, MODE>(p, l, tn, r[i]);
       }
     }
+    if (part_new) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+      for (int i = 0; i < kSteps; ++i)
+        if (pos0 + i * R::kRows < lo || pos0 + i * R::kRows >= hi) zero_row(r[i]);
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(r[i].x[e]));
+    for (int i = 0; i < kSteps; ++i) m = largest(m, r[i].x);
     // a code cannot hold a NaN or an infinity: 0 and the largest number instead, and the status word says so
-    // (fmaxf drops a NaN, so the sum looks for it)
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(r[i].x[e], 0.f, sum);   // 0, or a NaN
-    if (sum != 0.f) {
+    if (!(m <= FLT_MAX)) {
       atomicOr(p.err, kDevErrValue);
       m = 0.f;
 #pragma unroll
@@ -324,29 +358,36 @@ __device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k
           m = fmaxf(m, fabsf(x));
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));   // not negative: in the bits' order
   }
   if (lane == 0) s_max[part] = m;
-  __syncthreads();   // also: every warp has read the block's old scale
+  // the block's warps; also: all have read its old scale
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "n"(32 * kBlockWarps) : "memory");
   if (row0 < 0) return;
 #pragma unroll
   for (int i = 0; i < kBlockWarps; ++i) m = fmaxf(m, s_max[i]);
   float s = fmaxf(s0, __fmul_rn(m, 1.0f / 127.0f));
   if (s < kTinyScale) s = 0.f;
   const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  const float ratio = s > 0.f ? __fdiv_rn(s0, s) : 0.f;
   if (part == 0 && lane == 0) (is_k ? p.c.ks : p.c.vs)[row0 >> 4] = s;
   int8_t* codes = (is_k ? p.c.k : p.c.v) + (row0 + (pos0 & (kKvBlock - 1))) * D + 4 * l;
+  const auto pack = [](const float (&x)[4]) {
+    uint32_t w;
+    asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\tcvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+        : "=r"(w)
+        : "r"(__float2int_rn(x[0])), "r"(__float2int_rn(x[1])), "r"(__float2int_rn(x[2])), "r"(__float2int_rn(x[3])));
+    return w;
+  };
+  const float ratio = part_new && s > 0.f ? __fdiv_rn(s0, s) : 0.f;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int pos = pos0 + i * R::kRows;
-    if (pos >= hi || (pos < lo && ratio == 1.f)) continue;
+    if (part_new && (pos >= hi || (pos < lo && ratio == 1.f))) continue;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t* to = reinterpret_cast<uint32_t*>(codes + i * R::kRows * D + half * (D / 2));
       float x[4];
-      if (pos < lo) {
+      if (part_new && pos < lo) {
         const uint32_t old = *to;
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(static_cast<float>(static_cast<int8_t>(old >> (8 * e))), ratio);
@@ -354,28 +395,27 @@ __device__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(r[i].x[4 * half + e], inv);   // at most 127 (1 + 2^-22)
       }
-      uint32_t w;
-      asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\tcvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
-          : "=r"(w)
-          : "r"(__float2int_rn(x[0])), "r"(__float2int_rn(x[1])), "r"(__float2int_rn(x[2])), "r"(__float2int_rn(x[3])));
-      *to = w;
+      *to = pack(x);
     }
   }
 }
 
-template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 4) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
+// Registers for four CTAs an SM, three with fp32's wider rows (five and four: 133 us for 101, fp32 the same).
+template <int D, int MODE, bool BF16>
+__global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
                                                                 int kv_ctas) {
   __shared__ float s_max[kWarps];
+  __shared__ float4 s_turn[MODE == kHalves ? kWarps / 2 : 1][kBlockRows * Row<D>::kLanes * 2];   // of the keys' warps
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (static_cast<int>(blockIdx.x) < kv_ctas) {   // the longer tasks first; a CTA takes keys and values of kHeads heads
     const int unit = warp / kBlockWarps, groups = (p.c.heads + kHeads - 1) / kHeads, slot = blockIdx.x / groups;
-    const int h = (blockIdx.x - slot * groups) * kHeads + (unit >> 1);
-    append_block<D, MODE>(p, slot, h, (unit & 1) == 0, warp % kBlockWarps, lane, s_max + unit * kBlockWarps);
+    const int h = (blockIdx.x - slot * groups) * kHeads + (unit >> 1), part = warp % kBlockWarps;
+    append_block<D, MODE, BF16>(p, slot, h, (unit & 1) == 0, unit, part, lane, s_max + unit * kBlockWarps,
+                                s_turn[MODE == kHalves ? (unit >> 1) * kBlockWarps + part : 0]);
   } else {
-    append_queries<D, MODE>(p, (blockIdx.x - kv_ctas) * kWarps + warp, lane);
+    append_queries<D, MODE, BF16>(p, (blockIdx.x - kv_ctas) * kWarps + warp, lane);
   }
 }
 
@@ -460,12 +500,16 @@ cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t st) {
   const long long grid = kv_ctas + (q_tasks + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffLL || q_tasks > 0xffffffffLL) return cudaErrorInvalidConfiguration;
   const int mode = !p.cos ? kNone : p.rope_pairs ? kPairs : p.rope_dim == p.c.dim ? kHalves : kPart;
-  static void (*const kernels[2][4])(KvAppendParams, int) = {
-      {q4_kv_append_kernel<64, kNone>, q4_kv_append_kernel<64, kHalves>, q4_kv_append_kernel<64, kPairs>,
-       q4_kv_append_kernel<64, kPart>},
-      {q4_kv_append_kernel<128, kNone>, q4_kv_append_kernel<128, kHalves>, q4_kv_append_kernel<128, kPairs>,
-       q4_kv_append_kernel<128, kPart>}};
-  return launch_pdl(kernels[p.c.dim == 128][mode], static_cast<unsigned>(grid), kThreads, st, p,
+  static void (*const kernels[2][2][4])(KvAppendParams, int) = {
+      {{q4_kv_append_kernel<64, kNone, false>, q4_kv_append_kernel<64, kHalves, false>,
+        q4_kv_append_kernel<64, kPairs, false>, q4_kv_append_kernel<64, kPart, false>},
+       {q4_kv_append_kernel<64, kNone, true>, q4_kv_append_kernel<64, kHalves, true>,
+        q4_kv_append_kernel<64, kPairs, true>, q4_kv_append_kernel<64, kPart, true>}},
+      {{q4_kv_append_kernel<128, kNone, false>, q4_kv_append_kernel<128, kHalves, false>,
+        q4_kv_append_kernel<128, kPairs, false>, q4_kv_append_kernel<128, kPart, false>},
+       {q4_kv_append_kernel<128, kNone, true>, q4_kv_append_kernel<128, kHalves, true>,
+        q4_kv_append_kernel<128, kPairs, true>, q4_kv_append_kernel<128, kPart, true>}}};
+  return launch_pdl(kernels[p.c.dim == 128][p.in_bf16 != 0][mode], static_cast<unsigned>(grid), kThreads, st, p,
                     static_cast<int>(kv_ctas));
 }
 

@@ -272,3 +272,27 @@ def test_runs_in_a_graph_and_on_another_stream():
     a = ko.cpu().numpy().reshape(2, 2, 2, D)
     assert np.array_equal(a[:, 0], a[:, 1]) and np.isfinite(a).all() and np.abs(a).max() > 0.5
     assert q4.q4_get_device_status() == q4.Q4_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_norm_weights_off_16_bytes_give_the_same(D):
+    """Norm weights are aligned to a float: the same bits wherever they start."""
+    g = rng(D, 8)
+    T, Hq, heads = 37, 5, 2
+    host = HostCache(2, heads, D, 64, 8)
+    x = dev(g.standard_normal((T, Hq + 2 * heads, D)).astype(f32), torch.float32)
+    w = dev((1 + g.standard_normal(2 * D + 3)).astype(f32), torch.float32)
+    table, n, cu = i32([[1]]), i32([T]), i32([0, T])
+    got = []
+    for off in (0, 1, 2, 3):
+        w_here = torch.empty(2 * D + off, dtype=torch.float32, device=device())[off:]
+        w_here.copy_(w[:2 * D])
+        cache = host.to_device()
+        out = torch.empty((T, Hq, D), dtype=torch.float32, device=device())
+        q4.q4_kv_append(cache, out, x[:, :Hq], x[:, Hq:Hq + heads], x[:, Hq + heads:], table, n, cu,
+                        q_norm=w_here[:D], k_norm=w_here[D:])
+        torch.cuda.synchronize()
+        got.append((out, cache.k[1], cache.k_scale[1], cache.v[1]))
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    assert q4.q4_get_device_status() == q4.Q4_OK
