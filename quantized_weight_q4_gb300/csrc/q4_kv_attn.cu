@@ -50,7 +50,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                 // rows of an MMA tile
 constexpr int kTeams = 4;                 // teams of a CTA at most
 constexpr int kStages = 2;                // ring stages of a warp, one block each
-constexpr int kSegCost = 16;              // what starting and ending a (sequence, head, tile) costs, in units
+constexpr int kSegCost = 24;              // what starting and ending a (sequence, head, tile) costs, in units
 // Weight of the softmax reference with the value scale the sums are relative to.  The reference moves once a
 // score exceeds it by 2^kLazy, or a value scale kMoreScale times (moving costs a multiplication of every sum);
 // the weight is as large as that leaves of fp16's range (2^9 * 2^4 * 4 < 65504).  fp16 holds a weight to 11
@@ -142,7 +142,7 @@ struct Stage {
 
 template <int D>
 constexpr size_t smem_bytes(int B) {
-  return 1024 + static_cast<size_t>(kWarps) * kStages * Stage<D>::kBytes +   // rings
+  return kStages * Stage<D>::kBytes + static_cast<size_t>(kWarps) * kStages * Stage<D>::kBytes +   // rings
          static_cast<size_t>(kWarps / 2) * kRows * (D + 8) * 4 +                    // the warps' sums, two after one another
          static_cast<size_t>(kWarps) * kRows * 2 * 4 +                        // their maxima and weights
          static_cast<size_t>(kWarps) * kStages * 8 +                          // scales
@@ -168,9 +168,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   constexpr int KT = D / 16;                    // k steps of q . k
   constexpr int NT = D / 8;                     // column tiles of p . v
   constexpr uint32_t kStageBytes = Stage<D>::kBytes;
+  constexpr uint32_t kRingAlign = kStages * kStageBytes;   // the other stage, and places in one, by exclusive or
+  static_assert(kStages == 2, "stages take turns");
   constexpr int kORow = D + 8;                  // floats between rows of the warps' sums: other banks
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + kRingAlign - 1) & ~uintptr_t(kRingAlign - 1));
   float* s_o = reinterpret_cast<float*>(ring + kWarps * kStages * kStageBytes);   // [warp][row][kORow]
   float* s_m = s_o + kWarps / 2 * kRows * kORow;                                           // [warp][row]
   float* s_l = s_m + kWarps * kRows;
@@ -178,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   long long* s_cum = reinterpret_cast<long long*>(s_scale + kWarps * kStages * 2); // [B + 1] first unit of each sequence
   __shared__ int s_last[kTeams];
   __shared__ float s_rowf[kTeams][kRows];       // score of a unit product
+  __shared__ int2 s_see[kTeams][kRows];         // positions a row sees: (x, y]
   __shared__ float s_tot[kTeams][2][kRows];     // maximum, weights' sum
   __shared__ long long s_warp[kWarps];
   __shared__ int s_pairs;                       // (sequence, tile, head)s; more than the grid: any such number
@@ -277,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   const int crow = D == 128 ? lane >> 3 : lane >> 2;
   const uint32_t cput = crow * D + (D == 128 ? ((lane & 7) ^ crow) << 4 : ((lane & 3) ^ ((crow >> 1) & 3)) << 4);
   Segment ps = {};                              // the copies' segment
+  const int32_t* ptable = nullptr;              // its row of the page table
+  unsigned ppages = 0;                          // pages it may have (a sequence without tokens: none)
   long long pu = u0;                            // its first unit
   int pblk = 0, ppage = -1;                     // the next block, that block's page
   bool more = u0 < u1;
@@ -288,37 +293,37 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         return;
       }
       locate(pu, ps);
+      ptable = a.b.table + ps.b * a.b.table_stride;
+      ppages = ps.len > 0 ? static_cast<unsigned>(a.c.pages) : 0u;
       pu = ps.last;
       pblk = ps.lo + mate;
     }
     const int pi = pblk >> sub_log2;
-    ppage = pi < a.b.table_stride ? __ldg(a.b.table + ps.b * a.b.table_stride + pi) : -1;
+    ppage = pi < a.b.table_stride ? __ldg(ptable + pi) : -1;
   };
   if (more) settle();
-  uint32_t put = 0;                             // stage to fill next, in units of a stage's two scales
+  uint32_t put = my_ring + cput, put_scale = my_scale + 4 * lane;   // in the stage to fill next
   // copies one block, if there is one; always closes a group, so that groups count stages
   auto produce = [&]() {
     if (more) {
-      if (ppage >= 0 && ppage < a.c.pages && pblk * kKvBlock < ps.len) {
+      if (static_cast<unsigned>(ppage) < ppages) {
         // below 2^31: the call's checks
         const uint32_t at = (static_cast<uint32_t>(ppage * a.c.heads + ps.h) << sub_log2) + (pblk & sub_mask);
         const int8_t* k = a.c.k + static_cast<uint64_t>(at) * Stage<D>::kCodes + lane * 16;
         const int8_t* v = a.c.v + static_cast<uint64_t>(at) * Stage<D>::kCodes + lane * 16;
-        const uint32_t dst = my_ring + put * (kStageBytes / 8);
 #pragma unroll
         for (int i = 0; i < Stage<D>::kCodes / 512; ++i) {
-          const uint32_t to = dst + i * 512 + (D == 128 && (i & 1) ? cput ^ 64 : cput);   // four rows on: that bit
+          const uint32_t to = (D == 128 && (i & 1) ? put ^ 64 : put) + i * 512;   // four rows on: that bit
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(k + i * 512) : "memory");
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + Stage<D>::kCodes), "l"(v + i * 512) : "memory");
         }
         if (lane < 2)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(my_scale + put + 4 * lane),
-                       "l"((lane ? a.c.vs : a.c.ks) + at) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(put_scale), "l"((lane ? a.c.vs : a.c.ks) + at) : "memory");
       } else {                                  // no such page, or a sequence without tokens: a block nobody sees
-        if (lane == 0 && pblk * kKvBlock < ps.len) atomicOr(a.err, kDevErrIndex);
-        if (lane < 2) asm volatile("st.shared.f32 [%0], %1;" ::"r"(my_scale + put + 4 * lane), "f"(-1.0f) : "memory");
+        if (lane == 0 && ps.len > 0) atomicOr(a.err, kDevErrIndex);
+        if (lane < 2) asm volatile("st.shared.f32 [%0], %1;" ::"r"(put_scale), "f"(lane ? 0.0f : -1.0f) : "memory");
       }
-      put = put == 8 * (kStages - 1) ? 0 : put + 8;
+      put ^= kStageBytes, put_scale ^= 8;
       pblk += TEAM;
       settle();
     }
@@ -329,13 +334,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
 
   // ---- segments ----
   const uint32_t qb = smem_u32(s_q + lane);
-  uint32_t take = 0;                            // stage to read next, as `put`
   // swizzled places of the thread's keys in a stage (plus 2 rows, the bit that differs, for the second tile) and
   // of its values (the chunk's bits change with the matrices)
   const int krow = 4 * (g >> 1) + (g & 1), vrow = lane & 15;
   const uint32_t koff = krow * D + ((D == 128 ? (2 * c) ^ (krow & 7) : c ^ ((krow >> 1) & 3)) << 4);
   const uint32_t voff = Stage<D>::kCodes + vrow * D + (((lane >> 4) ^ (D == 128 ? vrow & 7 : (vrow >> 1) & 3)) << 4);
   constexpr uint32_t kTileBit = D == 128 ? 32 : 16;   // two rows on: row bits 1 and up turn this chunk bit
+  uint32_t take_k = my_ring ^ koff, take_v = my_ring ^ voff, take_scale = my_scale;   // in the stage to read next
   long long u = u0;
   while (u < u1) {
     Segment s;
@@ -388,7 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         const int up = m > 0.f ? max(-126, min(126, 13 + 127 - static_cast<int>(__float_as_uint(m) >> 23))) : 0;
         const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
         const float rowf = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale * kLog2e;
-        if (c == 0) s_rowf[team][g + 8 * e] = rowf;
+        if (c == 0) {
+          const long long from = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
+          s_rowf[team][g + 8 * e] = rowf;
+          s_see[team][g + 8 * e] = make_int2(from < -1 ? -1 : static_cast<int>(from),
+                                             qpos[e] < 0 ? -1 : a.causal ? qpos[e] : s.len - 1);
+        }
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -405,14 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     float rowf[2];
 #pragma unroll
     for (int e = 0; e < kE; ++e) rowf[e] = s_rowf[team][g + 8 * e];
-    // range of positions each row sees: (from, to]
-    int from[2], to[2];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      to[e] = qpos[e] < 0 ? -1 : a.causal ? qpos[e] : s.len - 1;
-      const long long f = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
-      from[e] = f < -1 ? -1 : static_cast<int>(f);
-    }
     // blocks that every row of the tile sees whole (rows are in the order of their positions)
     int inner_lo, inner_hi;
     {
@@ -427,123 +429,116 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     float vref = 0.f, vinv = 0.f;               // value scale the sums are relative to, kUnitWeight over it
 
     for (int blk = s.lo + mate; blk < s.hi; blk += TEAM) {
-      const uint32_t kb = my_ring + take * (kStageBytes / 8);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
       float ks, vs;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(my_scale + take));
-      take = take == 8 * (kStages - 1) ? 0 : take + 8;
-      if (ks >= 0.f) {
-        // scores: column n of tile j is token 4 (n / 2) + 2 j + n % 2 of the block, so that the thread's four
-        // columns are the tokens 4 c .. 4 c + 3
-        uint32_t kw[2][D / 16];
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(take_scale));
+      // scores: column n of tile j is token 4 (n / 2) + 2 j + n % 2 of the block, so that the thread's four
+      // columns are the tokens 4 c .. 4 c + 3
+      uint32_t kw[2][D / 16];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const uint4 x = lds128(kb + 2 * j * D + (koff ^ (i << 4) ^ (j * kTileBit)));
-            kw[j][4 * i] = x.x, kw[j][4 * i + 1] = x.y, kw[j][4 * i + 2] = x.z, kw[j][4 * i + 3] = x.w;
-          }
-        float sc[2][4], sd[2][4];   // even and odd k steps: twice as many sums that do not wait for one another
-#pragma unroll
-        for (int t = 0; t < KT; t += 2) {
-          const uint4 x0 = lds128(qb + t * 512), x1 = lds128(qb + t * 512 + 512);
-          const uint32_t q0[4] = {x0.x, x0.y, x0.z, x0.w}, q1[4] = {x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t b0, b1;
-            widen4(kw[j][t], b0, b1);
-            if (t == 0) mma_first(sc[j], q0, b0, b1); else mma(sc[j], q0, b0, b1);
-            widen4(kw[j][t + 1], b0, b1);
-            if (t == 0) mma_first(sd[j], q1, b0, b1); else mma(sd[j], q1, b0, b1);
-          }
+        for (int i = 0; i < D / 64; ++i) {
+          const uint4 x = lds128(take_k ^ (2 * j * D + j * kTileBit + (i << 4)));
+          kw[j][4 * i] = x.x, kw[j][4 * i + 1] = x.y, kw[j][4 * i + 2] = x.z, kw[j][4 * i + 3] = x.w;
         }
-        uint4 vw[D / 32];
+      float sc[2][4];
 #pragma unroll
-        for (int m = 0; m < D / 32; ++m) {
-          vw[m] = ldmatrix_t8(kb + (voff ^ (m << 5)));
-        }
+      for (int t = 0; t < KT; ++t) {
+        const uint4 x = lds128(qb + t * 512);
+        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[j][i] += sd[j][i];
-        // scaled scores of the thread's rows, four columns each
-        float x[2][4];
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float f = ks * rowf[e];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[e][i] = (SPLIT ? sc[i >> 1][i & 1] + sc[i >> 1][2 + (i & 1)] : sc[i >> 1][2 * e + (i & 1)]) * f;
-        }
-        if (blk < inner_lo || blk >= inner_hi) {   // some row does not see all of the block
-          const int pos = blk * kKvBlock + 4 * c;
-#pragma unroll
-          for (int e = 0; e < kE; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (pos + i <= from[e] || pos + i > to[e]) x[e][i] = -INFINITY;
-        }
-        // the references move rarely: by a row's scores, or by the value scale
-        float m[2];
-        bool move = vs > kMoreScale * vref;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          m[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
-          move |= m[e] > mref[e] + kLazy;       // also from -inf
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          const float vnew = fmaxf(vref, vs);
-          const float vf = vnew > 0.f ? vref / vnew : 1.f;
-          vref = vnew;
-          vinv = vref > 0.f ? kUnitWeight / vref : 0.f;
-          float f[2];
-#pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
-            m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
-            m[e] = fmaxf(m[e], mref[e]);
-            const float k = m[e] > -INFINITY ? ex2(mref[e] - m[e]) : 1.f;
-            lsum[e] *= k;
-            f[e] = k * vf;
-            mref[e] = m[e];
-          }
-          if (SPLIT) f[1] = f[0];
-#pragma unroll
-          for (int i = 0; i < NT; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
-        }
-        // weights, and weights times the value scale as fp16
-        const float vk = vs * vinv;
-        uint32_t pf[4];
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float ref = mref[e] > -INFINITY ? mref[e] : 0.f;
-          float w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[i] = ex2(x[e][i] - ref);
-            lsum[e] += w[i];
-            w[i] *= vk;
-          }
-          pf[e] = pack_f16(w[0], w[1]);
-          pf[2 + e] = pack_f16(w[2], w[3]);
-          if (SPLIT) {
-            pf[1] = pack_rest(w[0], w[1], pf[0], kRestScale);
-            pf[3] = pack_rest(w[2], w[3], pf[2], kRestScale);
-          }
-        }
-        // values: column n of tile i is element 8 i + n
-#pragma unroll
-        for (int m = 0; m < D / 32; ++m) {
-          const uint32_t w[4] = {vw[m].x, vw[m].y, vw[m].z, vw[m].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            widen4(w[i], b0, b1);
-            mma(o[4 * m + i], pf, b0, b1);
-          }
+        for (int j = 0; j < 2; ++j) {
+          uint32_t b0, b1;
+          widen4(kw[j][t], b0, b1);
+          if (t == 0) mma_first(sc[j], q, b0, b1); else mma(sc[j], q, b0, b1);
         }
       }
+      uint4 vw[D / 32];
+#pragma unroll
+      for (int m = 0; m < D / 32; ++m) {
+        vw[m] = ldmatrix_t8(take_v ^ (m << 5));
+      }
+      // scaled scores of the thread's rows, four columns each
+      float x[2][4];
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const float f = ks * rowf[e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[e][i] = (SPLIT ? sc[i >> 1][i & 1] + sc[i >> 1][2 + (i & 1)] : sc[i >> 1][2 * e + (i & 1)]) * f;
+      }
+      if (blk < inner_lo || blk >= inner_hi || ks < 0.f) {   // some row does not see all of the block
+        const int pos = blk * kKvBlock + 4 * c;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const int2 see = s_see[team][g + 8 * e];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (pos + i <= see.x || pos + i > see.y || ks < 0.f) x[e][i] = -INFINITY;
+        }
+      }
+      // the references move rarely: by a row's scores, or by the value scale
+      float m[2];
+      bool move = vs > kMoreScale * vref;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        m[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
+        move |= m[e] > mref[e] + kLazy;       // also from -inf
+      }
+      if (__any_sync(0xffffffffu, move)) {
+        const float vnew = fmaxf(vref, vs);
+        const float vf = vnew > 0.f ? vref / vnew : 1.f;
+        vref = vnew;
+        vinv = vref > 0.f ? kUnitWeight / vref : 0.f;
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 1));
+          m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 2));
+          m[e] = fmaxf(m[e], mref[e]);
+          const float k = m[e] > -INFINITY ? ex2(mref[e] - m[e]) : 1.f;
+          lsum[e] *= k;
+          f[e] = k * vf;
+          mref[e] = m[e];
+        }
+        if (SPLIT) f[1] = f[0];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i][0] *= f[0], o[i][1] *= f[0], o[i][2] *= f[1], o[i][3] *= f[1];
+      }
+      // weights, and weights times the value scale as fp16
+      const float vk = vs * vinv;
+      uint32_t pf[4];
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const float ref = mref[e] > -INFINITY ? mref[e] : 0.f;
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = ex2(x[e][i] - ref);
+          lsum[e] += w[i];
+          w[i] *= vk;
+        }
+        pf[e] = pack_f16(w[0], w[1]);
+        pf[2 + e] = pack_f16(w[2], w[3]);
+        if (SPLIT) {
+          pf[1] = pack_rest(w[0], w[1], pf[0], kRestScale);
+          pf[3] = pack_rest(w[2], w[3], pf[2], kRestScale);
+        }
+      }
+      // values: column n of tile i is element 8 i + n
+#pragma unroll
+      for (int m = 0; m < D / 32; ++m) {
+        const uint32_t w[4] = {vw[m].x, vw[m].y, vw[m].z, vw[m].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b0, b1;
+          widen4(w[i], b0, b1);
+          mma(o[4 * m + i], pf, b0, b1);
+        }
+      }
+      take_k ^= kStageBytes, take_v ^= kStageBytes, take_scale ^= 8;
       __syncwarp();
       produce();
     }
