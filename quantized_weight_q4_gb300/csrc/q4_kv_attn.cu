@@ -50,7 +50,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                 // rows of an MMA tile
 constexpr int kTeams = 4;                 // teams of a CTA at most
 constexpr int kStages = 2;                // ring stages of a warp, one block each
-constexpr int kSegCost = 24;              // what starting and ending a (sequence, head, tile) costs, in units
 // Weight of the softmax reference with the value scale the sums are relative to.  The reference moves once a
 // score exceeds it by 2^kLazy, or a value scale kMoreScale times (moving costs a multiplication of every sum);
 // the weight is as large as that leaves of fp16's range (2^9 * 2^4 * 4 < 65504).  fp16 holds a weight to 11
@@ -164,6 +163,10 @@ __device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len,
 template <int D, bool SPLIT, int TEAM>
 __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = SPLIT ? 1 : 2;             // query rows of a thread
+  // what starting and ending a (sequence, tile, head) costs, in units: more where all of a CTA's warps wait for it
+  // (16 / 24 / 32 / 40: 64 sequences of 50 to 8191 tokens in quarters 109 / 103 / 104 / 107 us, 12 of 700 to 5000
+  // with a window of 2048 in whole CTAs 20.5 / 20.5 / 18.7 / 18.9 us)
+  constexpr int kSegCost = TEAM == kWarps ? 32 : 24;
   constexpr int kTileRows = 8 * kE;             // query rows of a tile
   constexpr int KT = D / 16;                    // k steps of q . k
   constexpr int NT = D / 8;                     // column tiles of p . v
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   __shared__ float s_tot[kTeams][2][kRows];     // maximum, weights' sum
   __shared__ long long s_warp[kWarps];
   __shared__ int s_pairs;                       // (sequence, tile, head)s; more than the grid: any such number
+  __shared__ int s_longest;                     // units of the longest of them
 
   const KvAttnCall& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   float* t_o = s_o + team * TEAM / 2 * kRows * kORow;
   uint4* s_q = reinterpret_cast<uint4*>(t_o);   // [k step][lane] A operand
   auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(crew) : "memory"); };
-  if (tid == 0) s_pairs = 0;
+  if (tid == 0) s_pairs = s_longest = 0;
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
@@ -205,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   {
     const int per = (B + kThreads - 1) / kThreads;
     long long sum = 0, pairs = 0;
+    int longest = 0;
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b < B) {
@@ -217,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         s_cum[b + 1] = sum + n;
         sum += n;
         pairs += tiles * a.c.heads;
+        if (tiles > 0) longest = max(longest, hi - lo + kSegCost);
       }
     }
     long long up = sum;
@@ -226,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       if (lane >= o) up += x;
     }
     if (lane == 31) s_warp[warp] = up;
+    if (longest > 0) atomicMax(&s_longest, longest);
     if (pairs > 0) atomicAdd(&s_pairs, static_cast<int>(min(pairs, 1LL << 18)));   // kThreads of them fit an int
     __syncthreads();
     long long before = up - sum;
@@ -238,11 +245,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     __syncthreads();
   }
   const long long units = s_cum[B];
-  // as many ranges as have a block for every warp of a team; where there is one for each (sequence, tile, head),
-  // the same number for each, so that those of one length begin with a range
+  // as many ranges as have a block for every warp of a team; where there is one for each (sequence, tile, head) and
+  // these are of one length or nearly, the same number for each, so that they begin with a range and few are cut (64
+  // sequences of 4096 tokens 96 us, 102 us cut anywhere; of 50 to 8191 tokens 112 us so, 103 us cut anywhere)
   const long long pairs = max(1, s_pairs), most = static_cast<long long>(gridDim.x) * (kWarps / TEAM);
   long long ranges = min(most, units / (TEAM + kSegCost));
-  ranges = pairs <= most ? pairs * max(1LL, ranges / pairs) : max(1LL, ranges);
+  const bool even = pairs <= most && s_longest * pairs <= units + units / 16;
+  ranges = even ? pairs * max(1LL, ranges / pairs) : max(1LL, ranges);
   auto range_of = [&](long long i) { return units * i / ranges; };
   // the range that holds unit u
   auto owner_of = [&](long long u) { return ((u + 1) * ranges - 1) / units; };
