@@ -158,6 +158,93 @@ __device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len,
   }
 }
 
+// Four elements (d ..) of query row `row` (token-major) of a (sequence, head), v over the weights' sum l.
+template <int D>
+__device__ __forceinline__ void store4(const AttnParams& p, const Segment& s, int row, int d, float4 v, float l) {
+  const KvAttnCall& a = p.a;
+  const int j = row / p.group;
+  if (s.c0 < 0 || s.c0 + j >= a.b.T) return;
+  const long long at = ((static_cast<long long>(s.c0) + j) * a.Hq + s.h * p.group + row % p.group) * D + d;
+  auto over = [&](float y) { return l > 0.f ? y / l : l == 0.f ? 0.f : l; };   // no key: zeros; a NaN stays
+  v = make_float4(over(v.x), over(v.y), over(v.z), over(v.w));
+  if (a.out_bf16) {
+    __nv_bfloat162 y[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = *reinterpret_cast<uint2*>(y);
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+  }
+}
+
+// Barrier of a team's threads.
+template <int CREW>
+__device__ __forceinline__ void team_sync(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(CREW) : "memory");
+}
+
+// The sum of all shares of a (sequence, tile, head), the first in range o0, by the team that arrived last.  t_o, s_m,
+// s_l: shared memory of the team and of all warps.  Every share's factor is found once, and a thread's elements of
+// several shares are on their way together (an element at a time with its factors: the ragged batch 103 us for 96,
+// one sequence of 16,000 tokens 31 us for 22).
+template <int D, int ROWS, int TEAM>
+__device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int row0, int rows, long long o0, int shares,
+                                  int team, int mine, float* t_o, float* s_m, float* s_l) {
+  constexpr int crew = TEAM * 32, kVecs = D / 4, kORow = D + 8;
+  const int lane = mine & 31, warp = team * TEAM + (mine >> 5);
+  auto share = [&](int i) {
+    return p.part + ((o0 + i) * 2 + (i == 0 ? 1 : 0)) * kRows * (D + 2);
+  };
+  // a thread for each row and some of the shares: the maximum, then every share's factor
+  const int r = mine % kRows, k0 = mine / kRows;
+  constexpr int kStep = crew / kRows, kChunk = TEAM / 2 * kORow;   // factors that t_o has room for
+  float m = -INFINITY, l = 0.f;
+  for (int k = k0; k < shares; k += kStep) m = fmaxf(m, __ldcg(share(k) + kRows * D + r));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, kRows));
+  if (lane < kRows) s_m[warp * kRows + r] = m;
+  team_sync<crew>(team);
+#pragma unroll
+  for (int w = 0; w < TEAM; ++w) m = fmaxf(m, s_m[(team * TEAM + w) * kRows + r]);
+  constexpr int kPer = ROWS * kVecs > crew ? ROWS * kVecs / crew : 1;
+  float4 v[kPer];
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) v[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < shares; base += kChunk) {
+    const int end = min(shares, base + kChunk);
+    for (int k = base + k0; k < end; k += kStep) {
+      const float* q = share(k) + kRows * D + r;
+      const float mk = __ldcg(q), f = mk > -INFINITY ? ex2(mk - m) : 0.f;
+      l += f * __ldcg(q + kRows);
+      t_o[(k - base) * kRows + r] = f;
+    }
+    team_sync<crew>(team);
+#pragma unroll 4
+    for (int k = base; k < end; ++k) {
+#pragma unroll
+      for (int n = 0; n < kPer; ++n) {
+        const int i = mine + n * crew;
+        if (i < rows * kVecs) {
+          const float f = t_o[(k - base) * kRows + i / kVecs];
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(share(k) + 4 * i));
+          v[n].x = fmaf(f, x.x, v[n].x), v[n].y = fmaf(f, x.y, v[n].y);
+          v[n].z = fmaf(f, x.z, v[n].z), v[n].w = fmaf(f, x.w, v[n].w);
+        }
+      }
+    }
+    team_sync<crew>(team);
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, kRows);
+  if (lane < kRows) s_l[warp * kRows + r] = l;
+  team_sync<crew>(team);
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    const int i = mine + n * crew;
+    if (i >= rows * kVecs) continue;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < TEAM; ++w) sum += s_l[(team * TEAM + w) * kRows + i / kVecs];
+    store4<D>(p, s, row0 + i / kVecs, i % kVecs * 4, v[n], sum);
+  }
+}
+
 // SPLIT: the 16 rows of an MMA tile are 8 query rows in two fp16 terms each; else 16 in one term.
 // TEAM: warps that take a range of units together.
 template <int D, bool SPLIT, int TEAM>
@@ -198,7 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
   const int team = warp / TEAM, mate = warp % TEAM, mine = mate * 32 + lane;
   float* t_o = s_o + team * TEAM / 2 * kRows * kORow;
   uint4* s_q = reinterpret_cast<uint4*>(t_o);   // [k step][lane] A operand
-  auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(crew) : "memory"); };
   if (tid == 0) s_pairs = s_longest = 0;
   __syncthreads();
   pdl_launch_dependents();
@@ -420,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
 #pragma unroll
       for (int t = 0; t < KT; ++t) s_q[t * 32 + lane] = make_uint4(qf[t][0], qf[t][1], qf[t][2], qf[t][3]);
     }
-    team_sync();
+    team_sync<crew>(team);
     float rowf[2];
 #pragma unroll
     for (int e = 0; e < kE; ++e) rowf[e] = s_rowf[team][g + 8 * e];
@@ -562,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         s_l[warp * kRows + g + 8 * e] = lsum[e];
       }
     }
-    team_sync();
+    team_sync<crew>(team);
     float top[2], fo[2];
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
@@ -591,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       }
     };
     if (mate < TEAM / 2) hand_in(false);
-    team_sync();
+    team_sync<crew>(team);
     if (mate >= TEAM / 2) hand_in(true);
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
@@ -606,62 +692,38 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         s_tot[team][1][g + 8 * e] = l;
       }
     }
-    team_sync();
+    team_sync<crew>(team);
     const bool whole = s.first >= u0 && s.last <= u1;
     // partial sums: slot 0 for a (sequence, head, tile) that began in an earlier CTA, 1 for one that begins here
     float* slot = p.part + (range * 2 + (s.first >= u0 ? 1 : 0)) * kRows * (D + 2);
-    auto store = [&](int r, int d, float v) {
-      const int j = (row0 + r) / p.group;
-      if (s.c0 < 0 || s.c0 + j >= a.b.T) return;
-      const long long at = ((static_cast<long long>(s.c0) + j) * a.Hq + s.h * p.group + (row0 + r) % p.group) * D + d;
-      if (a.out_bf16)
-        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-      else
-        static_cast<float*>(a.out)[at] = v;
-    };
-    for (int i = mine; i < rows * D; i += crew) {
-      const int r = i / D, d = i % D;
-      float v = 0.f;
+    constexpr int kVecs = D / 4;
+    for (int i = mine; i < rows * kVecs; i += crew) {
+      const int r = i / kVecs, d = i % kVecs * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < TEAM / 2; ++w) v += t_o[(w * kRows + r) * kORow + d];
-      if (whole) {
-        const float l = s_tot[team][1][r];
-        store(r, d, l > 0.f ? v / l : l == 0.f ? 0.f : l);   // no key: zeros; a NaN stays
-      } else {
-        slot[r * D + d] = v;
+      for (int w = 0; w < TEAM / 2; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(t_o + (w * kRows + r) * kORow + d);
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
       }
+      if (whole)
+        store4<D>(p, s, row0 + r, d, v, s_tot[team][1][r]);
+      else
+        *reinterpret_cast<float4*>(slot + r * D + d) = v;
     }
     if (!whole) {
       if (mine < 2 * kRows) slot[kRows * D + mine] = (&s_tot[team][0][0])[mine];
-      team_sync();
+      team_sync<crew>(team);
       const long long o0 = owner_of(s.first), o1 = owner_of(s.last - 1);
       if (mine == 0) {
         const unsigned old = atom_add_acq_rel_gpu(p.tickets + o0, 1u);
         s_last[team] = old == static_cast<unsigned>(o1 - o0);
         if (s_last[team]) p.tickets[o0] = 0;
       }
-      team_sync();
-      if (s_last[team]) {
-        const int shares = static_cast<int>(o1 - o0) + 1;
-        auto share = [&](int i) {
-          return p.part + ((o0 + i) * 2 + (i == 0 ? 1 : 0)) * kRows * (D + 2);
-        };
-        for (int i = mine; i < rows * D; i += crew) {
-          const int r = i / D, d = i % D;
-          float m = -INFINITY, l = 0.f, v = 0.f;
-          for (int k = 0; k < shares; ++k) m = fmaxf(m, __ldcg(share(k) + kRows * D + r));
-          for (int k = 0; k < shares; ++k) {
-            const float* q = share(k);
-            const float mk = __ldcg(q + kRows * D + r);
-            const float f = mk > -INFINITY ? ex2(mk - m) : 0.f;
-            l += f * __ldcg(q + kRows * D + kRows + r);
-            v += f * __ldcg(q + r * D + d);
-          }
-          store(r, d, l > 0.f ? v / l : l == 0.f ? 0.f : l);
-        }
-      }
+      team_sync<crew>(team);
+      if (s_last[team])
+        join<D, kTileRows, TEAM>(p, s, row0, rows, o0, static_cast<int>(o1 - o0) + 1, team, mine, t_o, s_m, s_l);
     }
-    team_sync();   // t_o and s_m are free for the next segment
+    team_sync<crew>(team);   // t_o and s_m are free for the next segment
     u = min(s.last, u1);
   }
 
