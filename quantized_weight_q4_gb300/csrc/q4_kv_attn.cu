@@ -195,7 +195,12 @@ __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int 
   };
   // a thread for each row and some of the shares: the maximum, then every share's factor
   const int r = mine % kRows, k0 = mine / kRows;
-  constexpr int kStep = crew / kRows, kChunk = TEAM / 2 * kORow;   // factors that t_o has room for
+  constexpr int kPer = ROWS * kVecs > crew ? ROWS * kVecs / crew : 1;
+  constexpr int kParts = kPer > 1 ? 0 : 3 * crew;   // t_o's last floats: sums of other threads
+  constexpr int kStep = crew / kRows, kChunk = (TEAM / 2 * kRows * kORow - kParts) / kRows;   // factors it has room for
+  // with few rows several threads take shares in turn for the same elements
+  const int elems = rows * kVecs, groups = kPer > 1 || 2 * elems > crew ? 1 : 4 * elems > crew ? 2 : 4;
+  const int span = crew / groups, group = mine / span, mine_at = mine % span;
   float m = -INFINITY, l = 0.f;
   for (int k = k0; k < shares; k += kStep) m = fmaxf(m, __ldcg(share(k) + kRows * D + r));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, kRows));
@@ -203,7 +208,6 @@ __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int 
   team_sync<crew>(team);
 #pragma unroll
   for (int w = 0; w < TEAM; ++w) m = fmaxf(m, s_m[(team * TEAM + w) * kRows + r]);
-  constexpr int kPer = ROWS * kVecs > crew ? ROWS * kVecs / crew : 1;
   float4 v[kPer];
 #pragma unroll
   for (int n = 0; n < kPer; ++n) v[n] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -217,11 +221,11 @@ __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int 
     }
     team_sync<crew>(team);
 #pragma unroll 4
-    for (int k = base; k < end; ++k) {
+    for (int k = base + group; k < end; k += groups) {
 #pragma unroll
       for (int n = 0; n < kPer; ++n) {
-        const int i = mine + n * crew;
-        if (i < rows * kVecs) {
+        const int i = mine_at + n * crew;
+        if (i < elems) {
           const float f = t_o[(k - base) * kRows + i / kVecs];
           const float4 x = __ldcg(reinterpret_cast<const float4*>(share(k) + 4 * i));
           v[n].x = fmaf(f, x.x, v[n].x), v[n].y = fmaf(f, x.y, v[n].y);
@@ -233,11 +237,18 @@ __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int 
   }
   l += __shfl_xor_sync(0xffffffffu, l, kRows);
   if (lane < kRows) s_l[warp * kRows + r] = l;
+  float4* parts = reinterpret_cast<float4*>(t_o + TEAM / 2 * kRows * kORow - kParts);
+  if (group > 0 && mine_at < elems) parts[(group - 1) * elems + mine_at] = v[0];
   team_sync<crew>(team);
+  if (group > 0) return;
+  for (int n = 1; n < groups && mine_at < elems; ++n) {
+    const float4 x = parts[(n - 1) * elems + mine_at];
+    v[0].x += x.x, v[0].y += x.y, v[0].z += x.z, v[0].w += x.w;
+  }
 #pragma unroll
   for (int n = 0; n < kPer; ++n) {
-    const int i = mine + n * crew;
-    if (i >= rows * kVecs) continue;
+    const int i = mine_at + n * crew;
+    if (i >= elems) continue;
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < TEAM; ++w) sum += s_l[(team * TEAM + w) * kRows + i / kVecs];
