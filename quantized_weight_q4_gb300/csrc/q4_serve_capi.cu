@@ -122,24 +122,25 @@ namespace {
 
 // Query rows (new tokens x query heads that share a kv head) up to which a
 // sequence takes the split form, for B sequences of up to max_kv tokens.  The
-// split form streams the codes once for every 16 rows, 1100 blocks of 16 tokens
+// split form streams the codes once for every 16 rows, 1500 blocks of 16 tokens
 // a microsecond with some 40 blocks' time to start each; the prompt form first
 // writes the tokens as fp16 and then takes 1.6 us for each 128 of them and 256
-// rows, on one SM however long they are.
+// rows, on one SM however long they are, with 8 us to start and end.
 // Measured with 8 kv heads of 128 (split / prompt form, us): one sequence of
-// 16,000 tokens, 128 rows 65 / 342, 512 rows 194 / 210; 16 sequences of 8,000,
-// 16 rows 65 / 346, 128 rows 435 / 330; 64 of 1,000, 64 rows 173 / 202, 128 rows
-// 303 / 216; one of 256, 1024 rows 50 / 24.
+// 16,000 tokens, 128 rows 58 / 206, 512 rows 203 / 212; 16 sequences of 8,000,
+// 64 rows 184 / 265, 128 rows 342 / 266; 16 of 500, 64 rows 28 / 42; 64 of 300,
+// 64 rows 100 / 96; 64 of 1,000, 64 rows 161 / 172, 128 rows 278 / 191; 64 of
+// 4,000, 64 rows 385 / 535, 96 rows 555 / 538.
 constexpr int kRowTile = 16, kMostSplitRows = 1024;
 int split_rows_of(const q4::KvView& c, int64_t B, int64_t max_kv, int sms) {
   const double heads = static_cast<double>(B) * c.heads, blocks = static_cast<double>((max_kv + 15) / 16);
   const double bytes = heads * blocks * 16 * c.dim;      // of keys, or values
   int rows = kRowTile;
   for (int r = 2 * kRowTile; r <= kMostSplitRows; r += kRowTile) {
-    const double split = 10 + heads * (r / kRowTile) * (blocks + 40) / 1100;
+    const double split = 10 + heads * (r / kRowTile) * (blocks + 40) / 1500;
     const double ctas = heads * ((r + 255) / 256);
-    const double walk = static_cast<double>(static_cast<int64_t>((ctas + sms - 1) / sms)) * ((max_kv + 127) / 128) * 1.6;
-    const double read = bytes * 4 / 6e6, prompt = 20 + bytes * 6 / 5.5e6 + (walk > read ? walk : read);
+    const double walk = static_cast<double>(static_cast<int64_t>((ctas + sms - 1) / sms)) * (((max_kv + 127) / 128) * 1.6 + 8);
+    const double read = bytes * 4 / 6e6, prompt = 12 + bytes * 6 / 5.5e6 + (walk > read ? walk : read);
     if (split > prompt) break;
     rows = r;
   }
