@@ -772,9 +772,9 @@ cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
 template <int D, bool SPLIT>
 cudaError_t launch(const AttnParams& p, int rows, int grid, cudaStream_t st) {
   // Teams of four while there are more (sequence, tile, head)s than SMs: a team's start and end then fall into the
-  // others' streams (an earlier step, quarters / whole CTAs: 64 sequences of 50 to 8191 tokens, 8 heads, 126 / 160 us;
-  // of 4096 tokens 110 / 127 us).  With fewer, whole CTAs, which leave a quarter of the shares to join (one sequence of
-  // 131,071 tokens 89 / 58 us, 8 of 1024 17 / 14 us).
+  // others' streams (quarters / whole CTAs: 64 sequences of 50 to 8191 tokens, 8 heads, 96 / 141 us; of 4096 tokens
+  // 96 / 115 us).  With fewer, whole CTAs, which leave a quarter of the shares to join (one sequence of 131,071
+  // tokens 62 / 54 us, 8 of 1024 17 / 16 us).
   const long long tiles = (rows + (SPLIT ? 7 : 15)) / (SPLIT ? 8 : 16);
   return p.a.b.B * tiles * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams>(p, grid, st)
                                               : launch<D, SPLIT, kWarps>(p, grid, st);
@@ -797,7 +797,7 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   p.tickets = static_cast<unsigned*>(ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
   // fp32 in or out needs two terms; bf16 takes them too while eight rows are enough: a thread then has one row's
-  // softmax instead of two (an earlier step: 64 sequences of 50 to 8191 tokens 127 us, 133 us with rows in both halves)
+  // softmax instead of two (64 sequences of 50 to 8191 tokens 96 us, 106 us with rows in both halves)
   const int rows = static_cast<int>(std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows));
   const bool split = !a.q_bf16 || !a.out_bf16 || rows <= 8;
   if (a.c.dim == 128) return split ? launch<128, true>(p, rows, sms, st) : launch<128, false>(p, rows, sms, st);
