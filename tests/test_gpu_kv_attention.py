@@ -226,3 +226,19 @@ def test_two_streams_do_not_share_scratch():
     torch.cuda.synchronize()
     for out, w in zip(outs, want):
         assert np.array_equal(out.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind,Hq", [("f32", 4), ("bf16", 3), ("bf16", 16)])
+def test_one_long_among_many_short(kind, Hq, D):
+    """More sequences than SMs, and one cut into hundreds of shares."""
+    ctx = [i % 40 for i in range(181)]
+    ctx[77] = 100_000
+    check([1] * 181, ctx, Hq, 1, D, 64, kind, 300 + D + Hq)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq", [1, 3, 4, 5, 8, 9, 16])
+def test_few_rows_joined_from_many_shares(Hq, kind, D):
+    check([1], [30_000], Hq, 1, D, 128, kind, 400 + D + Hq)
