@@ -587,15 +587,16 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
  *   max_kv  at least the largest kv_len
  *   total_kv  0, or at least the sum of the kv_len: with bf16 q and out,
  *           sequences with many new tokens are attended on the tensor cores,
- *           from fp16 copies of their cached tokens in the workspace, which
+ *           from copies of their cached codes as fp16 in the workspace, which
  *           is sized by B * max_kv, or by total_kv where that is less.  A batch
  *           that holds more records Q4_DEVERR_INDEX and gets zeros.
  * A query that sees nothing gets zeros.  Accuracy: the codes are exact in
- * every product; with fp32 q and out the result is that of fp32 arithmetic,
- * with bf16 the weights are rounded to fp16.  Weights are held relative to the
- * largest value scale met, with full precision down to 2^-23 of it (bf16:
- * 2^-23 with 11 bits): a block whose scale is smaller than that by more loses
- * bits of its share.
+ * every product, scales, sums and maxima are fp32.  With fp32 q or out the
+ * result is that of fp32 arithmetic, with bf16 both the weights (times their
+ * value scale) may be rounded to fp16, 11 bits.  Weights are held relative to
+ * the largest value scale met, with all their bits down to 2^-23 of it (on
+ * the tensor cores: 2^-20 of the largest that the query sees): a block whose
+ * scale is smaller than that by more loses bits of its share.
  *   workspace  q4_kv_attention_workspace_size bytes, 16-byte aligned, the first 4 KB zero
  *              before its first use; every completed call leaves them zero.
  *              Calls that share it must not overlap.  NULL: scratch the

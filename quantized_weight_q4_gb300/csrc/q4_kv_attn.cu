@@ -76,18 +76,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Four codes to two pairs of fp16: u = code + 128 as the low byte of 1024 + u, minus 1152, exact.
-__device__ __forceinline__ uint32_t sub1152(uint32_t x) {
-  uint32_t y;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xE480E480u));
-  return y;
-}
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  lo = sub1152(__byte_perm(u, 0x64646464u, 0x4140));
-  hi = sub1152(__byte_perm(u, 0x64646464u, 0x4342));
-}
-
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])

@@ -25,6 +25,18 @@ cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<unsigned long long>& 
   return e;
 }
 
+// Four codes to two pairs of fp16: u = code + 128 as the low byte of 1024 + u, minus 1152, exact.
+__device__ __forceinline__ uint32_t sub1152(uint32_t x) {
+  uint32_t y;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xE480E480u));
+  return y;
+}
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = sub1152(__byte_perm(u, 0x64646464u, 0x4140));
+  hi = sub1152(__byte_perm(u, 0x64646464u, 0x4342));
+}
+
 // The number of j in [1, n] with f(j) <= i, f non-decreasing: the whole warp
 // searches 32 probes at a time (one step up to n = 32, two up to 1024).
 template <typename F>

@@ -5,10 +5,10 @@
 // the exponentials beside them.  Two launches:
 //
 // * q4_kv_expand_kernel turns the pages of each sequence into consecutive
-//   fp16 rows (code * scale, both scaled by a power of two per sequence and
-//   head so that the largest fits fp16), once for all the queries that will
-//   read them: 2 bytes written for each code, against 4 D flops for each query.
-//   It also writes which tokens of a 128-token tile exist.
+//   rows of codes as fp16 (exact), once for all the queries that will read
+//   them: 2 bytes written for each code, against 4 D flops for each query.
+//   Beside them it writes a record of each 128-token tile: the scales of its
+//   eight blocks of 16 tokens, and which tokens exist.
 // * q4_kv_prompt_kernel: a CTA takes 256 query rows of one kv head (the query
 //   heads that share it, token-major) as two MMA tiles of 128, and walks over
 //   the visible tiles of 128 tokens.  One warp copies K and V tiles with TMA
@@ -18,12 +18,20 @@
 //   are in the softmax the tensor cores work on the other's.  The running
 //   maximum moves only when it has grown by 2^8, so the sums in tensor memory
 //   are seldom rescaled.
+// * Scales are applied in fp32.  A block's key scale is part of the row's
+//   constant that multiplies its scores; its value scale is an addend of the
+//   exponent, so that the weight that is rounded to fp16 is p_j * scale
+//   (relative to a power of two above the scales that the row has seen), and
+//   the sum of p_j takes it out again.  Codes times scales as fp16 rows
+//   instead would round keys and values to 11 bits: a key channel that stands
+//   out then moves scores by 2^-12 of its share of them (that form: 410 us for
+//   the prompt below, and 471 for the pieces).
 //
-// Measured (8 kv heads of 128, 32 query heads): a prompt of 8192 tokens 406 us
-// both launches, 1354 TFLOP/s of visible products (72% of the measured bf16
+// Measured (8 kv heads of 128, 32 query heads): a prompt of 8192 tokens 424 us
+// both launches, 1296 TFLOP/s of visible products (69% of the measured bf16
 // peak of cuBLAS; tiles on the diagonal do up to twice the visible work); six
-// pieces of up to 1537 tokens on up to 9000 cached ones 470 us, 1246 TFLOP/s.
-// The tensor pipe is 62% busy by its counter: what is left is the chain of a
+// pieces of up to 1537 tokens on up to 9000 cached ones 490 us, 1195 TFLOP/s.
+// What is left is the chain of a
 // tile (scores out of tensor memory, 128 exponentials a thread, weights back)
 // where two tiles an SM do not cover one another, and for the pieces the last
 // round of CTAs and the expansion.  The MMA warp runs its loop as a whole, with
@@ -54,14 +62,33 @@ constexpr float kLazy = 8.0f;
 constexpr float kUnit = 7.0f;             // weights are 2^7 at the reference: up to 2^15 with kLazy, below fp16's 65504
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kBlocks = kTile / kKvBlock;   // blocks of a tile
+constexpr int kNoScale = -1024;             // exponent of a tile whose values are all zero
+// A block's value scale counts as at least 2^kLeast of its tile's largest, one of 0 as 2^kZero (its codes are written as
+// 0), and a tile's as at least 2^kZero of the row's reference: in fp16 its weights are 0 from 2^-32 on, while in their
+// sum they count in full down to 2^-39.
+constexpr float kLeast = -60.0f, kZero = -40.0f;
+
+// What the softmax needs of 128 tokens of a head: a word for each lane of a warp.
+struct alignas(128) TileInfo {
+  float ks[kBlocks];         // key scales
+  float lv[kBlocks];         // log2(value scale) - e
+  float iv[kBlocks];         // 2^-lv
+  unsigned seen[4];          // bit i: token i exists
+  int e;                     // value scales are in (0, 2^e), the largest in the upper half; kNoScale: all are 0
+  int full;                  // 1: all tokens exist
+  int pad[2];
+};
+static_assert(sizeof(TileInfo) == 128 && kBlocks == 8, "a word for each lane");
+constexpr int kLaneLv = 8, kLaneSeen = 24, kLaneE = 28, kLaneFull = 29;   // lanes of the words
+
 struct ExpandParams {
   KvView c;
   KvBatch b;
   int group, split_rows;
   int rows_cap;              // rows of kv
-  __half* kv;                // [2][heads][rows_cap][dim]
-  float* factor;             // [B][heads][2]: what a row of K (V) was divided by
-  uint4* seen;               // [rows_cap / 128] bit i: token i of the tile exists
+  __half* kv;                // [2][heads][rows_cap][dim] codes
+  TileInfo* info;            // [heads][rows_cap / 128]
   int* kv_cum;               // [B + 1] first tile of each sequence's tokens
   int* order;                // [B] sequences, the longest last
   int* q_cum;                // [B + 1] first tile of the query rows of each of those
@@ -75,12 +102,26 @@ struct PromptParams {
   KvAttnCall a;
   int group, split_rows;
   int rows_cap;
-  const float* factor;
-  const uint4* seen;
+  const TileInfo* info;
   const int* kv_cum;
   const int* order;
   const int* q_cum;
 };
+
+// 2^e, -126 <= e <= 127 (beyond: the nearest of those).
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 + max(-126, min(127, e))) << 23);
+}
+// The e in [-126, 126] with x < 2^e, x >= 2^(e - 1) within that range; x > 0.
+__device__ __forceinline__ int exponent_above(float x) {
+  return max(-126, min(126, static_cast<int>(__float_as_uint(x) >> 23) - 126));
+}
+// The larger; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 
 // Sequences in this form have more query rows than the split form takes.
 __device__ __forceinline__ bool is_prompt(int nq, int group, int split_rows) {
@@ -168,8 +209,6 @@ __device__ __forceinline__ void order_by_length(int B, const int* cum, int* orde
 
 __global__ void __launch_bounds__(kExpandThreads) q4_kv_expand_kernel(const __grid_constant__ ExpandParams p) {
   extern __shared__ int s_cum[];
-  __shared__ float s_max[2][kExpandThreads / 32];
-  __shared__ unsigned s_seen[4];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, h = blockIdx.y, B = p.b.B;
@@ -191,67 +230,48 @@ __global__ void __launch_bounds__(kExpandThreads) q4_kv_expand_kernel(const __gr
   }
   if (tile >= total) return;
   const int b = find_seq(s_cum, B, tile), t0 = (tile - s_cum[b]) * kTile, len = p.b.kv_len[b];
-  // powers of two that bring the sequence's largest scale of this head to [2^7, 2^8)
-  float km = 0.f, vm = 0.f;
-  for (int i = tid; i < (len + kKvBlock - 1) / kKvBlock; i += kExpandThreads) {
-    const long long row = kv_row(p.c, p.b.table, p.b.table_stride, b, i * kKvBlock, h);
-    if (row >= 0) km = fmaxf(km, p.c.ks[row >> 4]), vm = fmaxf(vm, p.c.vs[row >> 4]);
+  // the record: a lane for each block of 16 tokens
+  if (tid < 32) {
+    const int pos = t0 + lane * kKvBlock;
+    long long row = -1;
+    unsigned have = 0;
+    if (lane < kBlocks && pos < len) {
+      row = kv_row(p.c, p.b.table, p.b.table_stride, b, pos, h);
+      if (row >= 0) have = 0xffffu >> (kKvBlock - min(kKvBlock, len - pos));
+      else if (h == 0) atomicOr(p.err, kDevErrIndex);
+    }
+    const float ks = row >= 0 ? p.c.ks[row >> 4] : 0.f, vs = row >= 0 ? p.c.vs[row >> 4] : 0.f;
+    const int e = __reduce_max_sync(0xffffffffu, vs > 0.f ? exponent_above(vs) : kNoScale);
+    const unsigned next = __shfl_down_sync(0xffffffffu, have, 1);
+    const int full = __all_sync(0xffffffffu, lane >= kBlocks || have == 0xffffu);
+    TileInfo* info = p.info + static_cast<long long>(h) * (p.rows_cap / kTile) + tile;
+    if (lane < kBlocks) {
+      const float lv = vs != 0.f ? fmaxf(log2f(vs * power_of_two(-e)), kLeast) : kZero;
+      info->ks[lane] = ks;
+      info->lv[lane] = lv;
+      info->iv[lane] = exp2f(-lv);
+      if ((lane & 1) == 0) info->seen[lane >> 1] = have | next << 16;
+      if (lane == 0) info->e = e, info->full = full;
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
-    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-  }
-  if (lane == 0) s_max[0][tid >> 5] = km, s_max[1][tid >> 5] = vm;
-  if (tid < 4) s_seen[tid] = 0;
-  __syncthreads();
-  float up[2], down[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    float m = 0.f;
-    for (int i = 0; i < kExpandThreads / 32; ++i) m = fmaxf(m, s_max[x][i]);
-    const int e = m > 0.f ? max(-126, min(126, 7 + 127 - static_cast<int>(__float_as_uint(m) >> 23))) : 0;
-    up[x] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    down[x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  }
-  if (t0 == 0 && tid < 2) p.factor[(static_cast<long long>(b) * p.c.heads + h) * 2 + tid] = down[tid];
   // 16 codes a thread
   const int D = p.c.dim, chunks = D / 16;
   for (int i = tid; i < kTile * chunks; i += kExpandThreads) {
     const int t = i / chunks, c = i % chunks, pos = t0 + t;
-    long long row = -1;
-    if (pos < len) {
-      row = kv_row(p.c, p.b.table, p.b.table_stride, b, pos, h);
-      if (c == 0 && h == 0) {
-        if (row >= 0) atomicOr(&s_seen[t >> 5], 1u << (t & 31));
-        else atomicOr(p.err, kDevErrIndex);
-      }
-    }
+    const long long row = pos < len ? kv_row(p.c, p.b.table, p.b.table_stride, b, pos, h) : -1;
+    const bool value = row >= 0 && p.c.vs[row >> 4] != 0.f;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       uint4 w = make_uint4(0, 0, 0, 0);
-      float s = 0.f;
-      if (row >= 0) {
-        w = *reinterpret_cast<const uint4*>((x ? p.c.v : p.c.k) + row * D + c * 16);
-        s = (x ? p.c.vs : p.c.ks)[row >> 4] * up[x];
-      }
-      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-      __half2 f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t two = q[j >> 1] >> (16 * (j & 1));
-        f[j] = __floats2half2_rn(static_cast<float>(static_cast<int8_t>(two)) * s,
-                                 static_cast<float>(static_cast<int8_t>(two >> 8)) * s);
-      }
+      if (x ? value : row >= 0) w = *reinterpret_cast<const uint4*>((x ? p.c.v : p.c.k) + row * D + c * 16);
+      uint4 f[2];
+      widen4(w.x, f[0].x, f[0].y), widen4(w.y, f[0].z, f[0].w);
+      widen4(w.z, f[1].x, f[1].y), widen4(w.w, f[1].z, f[1].w);
       uint4* to = reinterpret_cast<uint4*>(
           p.kv + ((static_cast<long long>(x) * p.c.heads + h) * p.rows_cap + static_cast<long long>(tile) * kTile + t) * D + c * 16);
-      to[0] = *reinterpret_cast<uint4*>(&f[0]);
-      to[1] = *reinterpret_cast<uint4*>(&f[4]);
+      to[0] = f[0];
+      to[1] = f[1];
     }
-  }
-  if (h == 0) {
-    __syncthreads();
-    if (tid == 0) p.seen[tile] = make_uint4(s_seen[0], s_seen[1], s_seen[2], s_seen[3]);
   }
 }
 
@@ -262,6 +282,21 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two pairs of floats from shared memory.
+__device__ __forceinline__ void lds_pairs(uint32_t at, f32x2& a, f32x2& b) {
+  asm("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(at));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 y;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
+}
+__device__ __forceinline__ float low2(f32x2 a) {
+  float x, y;
+  unpack2(a, x, y);
+  return x;
 }
 
 // 32 lanes x 32 columns of tensor memory to registers, without the wait.
@@ -361,11 +396,13 @@ __device__ __forceinline__ void lead_commit(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
+constexpr int kScaleWords = 6 * kBlocks;   // of a softmax warp
+
 template <int D>
 struct Cfg {
   static constexpr int kHalf = kTile * 128;             // 128 rows of 64 fp16: one swizzled box
   static constexpr int kTileBytes = kHalf * (D / 64);   // a Q, K or V tile
-  static constexpr int kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes + 256;
+  static constexpr int kSmem = 1024 + 2 * kTileBytes + kStages * kTileBytes + 256 + 8 * kScaleWords * 4;
   static constexpr uint32_t kTmemCols = 512;
   // instruction descriptors: fp16 operands, fp32 sums, 128 rows; q . k: both K-major, 128 columns;
   // p . v: V MN-major, D columns
@@ -387,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
   uint64_t* o_done = p_ready + 2;       // [2] its sums include the latest weights
   uint64_t* drain = o_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  float* s_scales = reinterpret_cast<float*>(ring + kStages * C::kTileBytes + 256);   // of the softmax warps
   __shared__ int s_fail;
   __shared__ int s_where[4];
 
@@ -559,9 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       }
       const int e = m ? max(-126, min(126, 13 + 127 - static_cast<int>(m >> 23))) : 0;
       const float f = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), a.scale);
-      rowc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(a.scale) * kLog2e *
-             (n > 0 ? p.factor[(static_cast<long long>(b) * a.c.heads + h) * 2] : 0.f);
-      rowc = fmaxf(rowc, 1e-30f);   // a scale of 0: scores of 0, while those of masked tokens stay -inf
+      rowc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(a.scale) * kLog2e;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -581,13 +617,27 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
     const long long f = have && a.window > 0 ? static_cast<long long>(qpos) - a.window : -1LL;
     const int from = f < -1 ? -1 : static_cast<int>(f);
     float m = -INFINITY, l = 0.f;
+    int e = kNoScale;             // the sums are relative to 2^e, above the value scales that the row has seen
     bool ok = true;
-    const uint4* seen_at = p.seen + tile0 + first;
-    uint4 next_seen = n > 0 ? __ldg(seen_at) : make_uint4(0, 0, 0, 0);
+    // a word of the tile's record for each lane, read a tile ahead, and by way of shared memory every scale for all
+    const int* info = reinterpret_cast<const int*>(p.info + static_cast<long long>(h) * (p.rows_cap / kTile) + tile0 + first) + lane;
+    int next_rec = n > 0 ? __ldg(info) : 0;
+    const uint32_t my_scales = smem_u32(s_scales + warp * kScaleWords);   // key scales, lv and iv, each twice
+    const uint32_t put = my_scales + 8 * lane;
+    const f32x2 rowc2 = dup2(rowc);
     for (int i = 0; i < n; ++i) {
-      const int t0 = (first + i) * kTile;
-      const uint4 seen = next_seen;
-      if (i + 1 < n) next_seen = __ldg(seen_at + i + 1);
+      const int t0 = (first + i) * kTile, rec = next_rec;
+      if (i + 1 < n) next_rec = __ldg(info + 32 * (i + 1));
+      __syncwarp();               // the last tile's scales have been read
+      if (lane < 24) asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(put), "r"(rec) : "memory");
+      __syncwarp();
+      uint32_t scales;            // the loads from it stay behind the stores
+      asm volatile("mov.u32 %0, %1;" : "=r"(scales) : "r"(my_scales) : "memory");
+      const int tile_e = __shfl_sync(0xffffffffu, rec, kLaneE);
+      const int full = __shfl_sync(0xffffffffu, rec, kLaneFull);
+      // tiles on the edge of what a row sees, or with tokens that do not exist (the same for the whole warp)
+      const bool mine = t0 + kTile - 1 > to || t0 <= from || full == 0;
+      const bool edge = __any_sync(0xffffffffu, mine);
       ok = gwait(&s_full[g], i & 1, &s_fail, a.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -595,28 +645,48 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       uint32_t s[kTile];
 #pragma unroll
       for (int x = 0; x < 4; ++x) tmem_ld32_async(t_s[g] + lanes + 32 * x, s + 32 * x);
+      f32x2 mul[kBlocks];         // a block's scores to powers of two
+#pragma unroll
+      for (int k = 0; k < kBlocks; k += 2) {
+        lds_pairs(scales + 8 * k, mul[k], mul[k + 1]);
+        mul[k] = mul2(mul[k], rowc2), mul[k + 1] = mul2(mul[k + 1], rowc2);
+      }
       tmem_wait_ld();
-      // tiles on the edge of what a row sees, or with tokens that do not exist
-      const bool edge = t0 + kTile - 1 > to || t0 <= from || (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu;
-      if (__any_sync(0xffffffffu, edge)) {
-        const uint32_t bits[4] = {seen.x, seen.y, seen.z, seen.w};
+      if (edge) {
+        uint32_t bits[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) bits[x] = __shfl_sync(0xffffffffu, rec, kLaneSeen + x);
         const int lo = from - t0, hi = to - t0;
 #pragma unroll
         for (int c = 0; c < kTile; ++c)
           if (c <= lo || c > hi || !((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) mul[k] = dup2(max_nan(low2(mul[k]), 1e-30f));   // masked scores stay -inf
       }
-      float mx[4];
+      float now = -INFINITY, top[kBlocks];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
+      for (int k = 0; k < kBlocks; ++k) {
+        top[k] = __uint_as_float(s[kKvBlock * k]);
 #pragma unroll
-      for (int c = 4; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const float now = top > -INFINITY ? top * rowc : -INFINITY;
-      if (__any_sync(0xffffffffu, now > m + kLazy)) {   // also from -inf
+        for (int c = 1; c < kKvBlock; ++c) top[k] = fmaxf(top[k], __uint_as_float(s[kKvBlock * k + c]));
+        now = fmaxf(now, top[k] * low2(mul[k]));
+      }
+      int te = tile_e;
+      if (edge) {                 // only scales of blocks that the row sees something of
+        te = kNoScale;
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+          const int up = tile_e + __float2int_ru(__int_as_float(__shfl_sync(0xffffffffu, rec, kLaneLv + k)));
+          te = top[k] > -INFINITY ? max(te, up) : te;
+        }
+      }
+      if (__any_sync(0xffffffffu, now > m + kLazy || te > e)) {   // also from -inf
         const float next = fmaxf(m, now);
         const float k = next > -INFINITY ? ex2(m - next) : 1.f;
         m = next;
         l *= k;
+        const float ko = k * power_of_two(e - max(e, te));
+        e = max(e, te);
         if (i > 0) {
           ok = gwait(&o_done[g], (i - 1) & 1, &s_fail, a.err);
           ok = __all_sync(0xffffffffu, ok);
@@ -628,23 +698,32 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
             tmem_ld32_async(t_o[g] + lanes + 32 * x, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * k);
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * ko);
             tmem_st32(t_o[g] + lanes + 32 * x, o);
           }
         }
       }
-      const float off = m > -INFINITY ? kUnit - m : 0.f;
-      const f32x2 c2 = dup2(rowc), off2 = dup2(off);
-      f32x2 sum2[2] = {0ull, 0ull};
+      // the tile's scales against the row's reference
+      const int down = tile_e == kNoScale ? 0 : max(tile_e - e, static_cast<int>(kZero));
+      const float off = (m > -INFINITY ? kUnit - m : 0.f) + static_cast<float>(down);
       uint32_t w[kTile / 2];
+      f32x2 sum2[2] = {0ull, 0ull};
+      const f32x2 off2 = dup2(off);
 #pragma unroll
-      for (int c = 0; c < kTile / 2; ++c) {
-        float x, y;
-        unpack2(fma2(pack2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), c2, off2), x, y);
-        x = ex2(x), y = ex2(y);
-        sum2[c & 1] = add2(sum2[c & 1], pack2(x, y));
-        const __half2 two = __floats2half2_rn(x, y);
-        w[c] = *reinterpret_cast<const uint32_t*>(&two);
+      for (int k = 0; k < kBlocks; ++k) {
+        f32x2 lv[2], iv[2];
+        lds_pairs(scales + 64 + 8 * (k & ~1), lv[0], lv[1]);
+        lds_pairs(scales + 128 + 8 * (k & ~1), iv[0], iv[1]);
+        const f32x2 add = add2(off2, lv[k & 1]);
+#pragma unroll
+        for (int c = k * kKvBlock / 2; c < (k + 1) * kKvBlock / 2; ++c) {
+          float x, y;
+          unpack2(fma2(pack2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), mul[k], add), x, y);
+          x = ex2(x), y = ex2(y);
+          sum2[c & 1] = fma2(pack2(x, y), iv[k & 1], sum2[c & 1]);
+          const __half2 two = __floats2half2_rn(x, y);
+          w[c] = *reinterpret_cast<const uint32_t*>(&two);
+        }
       }
       tmem_st32(t_s[g] + lanes, w);
       tmem_st32(t_s[g] + lanes + 32, w + 32);
@@ -653,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       mbar_arrive(&p_ready[g]);
       float x, y;
       unpack2(add2(sum2[0], sum2[1]), x, y);
-      l += x + y;
+      l = fmaf(x + y, power_of_two(-down), l);
     }
     // the rows' results
     if (n > 0 && ok) {
@@ -662,9 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       tc_fence_after();
     }
     if (ok) {
-      const float vf = n > 0 ? p.factor[(static_cast<long long>(b) * a.c.heads + h) * 2 + 1] : 0.f;
       // a row that sees nothing: zeros; a NaN stays
-      const float k = l > 0.f ? vf / l : l == 0.f ? 0.f : l;
+      const float k = l > 0.f ? power_of_two(e) / l : l == 0.f ? 0.f : l;
       const long long at = ((static_cast<long long>(c0) + j) * a.Hq + h * p.group + row % p.group) * D;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
@@ -731,13 +809,12 @@ cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, unsigned threads, size_t sm
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t factor, seen, kv_cum, order, q_cum, kv, total;
+  size_t info, kv_cum, order, q_cum, kv, total;
 };
 Layout layout(const KvView& c, int B, long long rows_cap) {
   Layout l;
-  l.factor = 0;
-  l.seen = up256(static_cast<size_t>(B) * c.heads * 2 * sizeof(float));
-  l.kv_cum = l.seen + up256(static_cast<size_t>(rows_cap / kTile) * sizeof(uint4));
+  l.info = 0;
+  l.kv_cum = up256(static_cast<size_t>(rows_cap / kTile) * c.heads * sizeof(TileInfo));
   l.order = l.kv_cum + up256((static_cast<size_t>(B) + 1) * sizeof(int));
   l.q_cum = l.order + up256(static_cast<size_t>(B) * sizeof(int));
   l.kv = l.q_cum + up256((static_cast<size_t>(B) + 1) * sizeof(int));
@@ -765,8 +842,7 @@ cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows
   x.split_rows = split_rows;
   x.rows_cap = static_cast<int>(rows);
   x.kv = reinterpret_cast<__half*>(w + l.kv);
-  x.factor = reinterpret_cast<float*>(w + l.factor);
-  x.seen = reinterpret_cast<uint4*>(w + l.seen);
+  x.info = reinterpret_cast<TileInfo*>(w + l.info);
   x.kv_cum = reinterpret_cast<int*>(w + l.kv_cum);
   x.order = reinterpret_cast<int*>(w + l.order);
   x.q_cum = reinterpret_cast<int*>(w + l.q_cum);
@@ -779,8 +855,7 @@ cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows
   p.group = x.group;
   p.split_rows = split_rows;
   p.rows_cap = x.rows_cap;
-  p.factor = x.factor;
-  p.seen = x.seen;
+  p.info = x.info;
   p.kv_cum = x.kv_cum;
   p.order = x.order;
   p.q_cum = x.q_cum;
