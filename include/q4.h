@@ -551,7 +551,8 @@ typedef struct q4_rope {
  *   q_norm, k_norm   fp32 [dim] or NULL: each head's RMS norm before the
  *               rotation, x * (1 / sqrt(mean(x^2) + eps)) * weight
  *   rope        or NULL (no rotation).  A position >= rope->rows records
- *               Q4_DEVERR_INDEX; the token is not stored and its q_out is zero.
+ *               Q4_DEVERR_INDEX; the token is not stored (what the cache holds
+ *               in its place is undefined) and its q_out is zero.
  * A block whose new values have largest magnitude m takes the scale
  * s = max(s0, m * (1 / 127)), s0 that of its earlier tokens (0 without any; s is 0
  * below 2^-110).  Earlier codes become rint(code * (s0 / s)), new ones

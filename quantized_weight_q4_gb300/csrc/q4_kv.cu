@@ -287,11 +287,14 @@ __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, 
     const int from = max(start, 0);
     const int at = slot - ((c0 >> 4) + 2 * b), blk = (from >> 4) + at;
     if (c1 > c0 && at >= 0 && blk * kKvBlock < len) {
-      lo = max(from, blk * kKvBlock), hi = min(len, (blk + 1) * kKvBlock);
+      // tokens past the rotation tables are not stored, neither their keys nor their values
+      const int end = MODE != kNone ? min(len, p.rope_rows) : len;
+      lo = max(from, blk * kKvBlock), hi = min(end, (blk + 1) * kKvBlock);
+      const bool beyond = end < min(len, (blk + 1) * kKvBlock);
       part_new = hi - lo < kKvBlock;
       pos0 = blk * kKvBlock + part * kBlockRows + lane / R::kLanes;
       const long long tok0 = static_cast<long long>(c0) + (lo - start);   // packed row of position lo
-      if (c0 >= 0 && tok0 + (hi - lo) <= p.b.T && !(is_k && MODE != kNone && hi > p.rope_rows)) {
+      if (c0 >= 0 && lo < hi && tok0 + (hi - lo) <= p.b.T) {
         // the rows, on their way while the page is looked up; for one that is not new, the nearest that is
         const long long stride = is_k ? p.k_stride : p.v_stride;
         const uint8_t* src = static_cast<const uint8_t*>(is_k ? p.k : p.v) + (tok0 * stride + h * D + 4 * l) * kSize;
@@ -309,8 +312,8 @@ __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, 
         }
         row0 = kv_row(p.c, p.b.table, p.b.table_stride, b, blk * kKvBlock, h);
       }
+      if ((row0 < 0 || beyond) && lane == 0) atomicOr(p.err, kDevErrIndex);
       if (row0 < 0) {
-        if (lane == 0) atomicOr(p.err, kDevErrIndex);
         asm volatile("cp.async.wait_all;" ::: "memory");
       } else if (lo > blk * kKvBlock) {
         s0 = (is_k ? p.c.ks : p.c.vs)[row0 >> 4];
