@@ -172,6 +172,15 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.arrive.release.aligned;\n\t"
       "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves, for work between them.  A peer's shared memory may be
+// touched only once its CTA is known to have started: a kernel arrives at its
+// start and waits before its first access to a peer.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Address, in the cluster's shared window, of `local` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(const void* local, uint32_t rank) {
   uint32_t r;
