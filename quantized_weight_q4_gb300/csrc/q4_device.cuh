@@ -172,13 +172,13 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.arrive.release.aligned;\n\t"
       "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same in two halves, for work between them.  A peer's shared memory may be
-// touched only once its CTA is known to have started: a kernel arrives at its
-// start and waits before its first access to a peer.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+// A peer's shared memory may be touched only once its CTA is known to have
+// started: a kernel says that it has at its start, and waits for its peers
+// before its first access to one.  Nothing written before is ordered by it.
+__device__ __forceinline__ void cluster_started() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() {
+__device__ __forceinline__ void cluster_wait_started() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Address, in the cluster's shared window, of `local` in CTA `rank` of the cluster.

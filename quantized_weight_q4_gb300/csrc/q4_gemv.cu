@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(Crew<MR>::kThreads, 1)
     fence_barrier_init();
   }
   __syncthreads();
+  cluster_started();   // waited for before the first store to a peer
   pdl_launch_dependents();
 
   if (warp == Crew<MR>::kWarps) {
@@ -404,6 +405,7 @@ __global__ void __launch_bounds__(Crew<MR>::kThreads, 1)
         produce_stage<BPT, BIG, FMT>(sd, s, ring + slot * T::kStageBytes, &full[slot], lane);
       }
       // the cluster barriers of this pass's combine (see the consumers)
+      if (pass == 0) cluster_wait_started();
       cluster_sync();
       if (pass + 1 < passes) cluster_sync();
     }
@@ -503,6 +505,7 @@ __global__ void __launch_bounds__(Crew<MR>::kThreads, 1)
       const int rank = static_cast<int>(cluster_ctarank());
       const int ns = p.nsplit;
       const int csize = (MODE == kModeGateUp) ? 2 * ns : ns;
+      if (pass == 0) cluster_wait_started();
       if (tid < 256) {
 #pragma unroll
         for (int m = 0; m < MR; ++m)

@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   uint8_t* xs = smem + sizeof(Shared);
-  cluster_arrive();          // waited for before the first store to a peer
+  cluster_started();         // waited for before the first store to a peer
   pdl_launch_dependents();
   pdl_wait();
   const int row = blockIdx.x / ctas, rank = static_cast<int>(cluster_ctarank());
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s.red[warp] = top;
   __syncthreads();
-  cluster_wait();            // every CTA of the row has started
+  cluster_wait_started();
   if (tid < ctas) {
     float m = s.red[0];
     for (int i = 1; i < kWarps; ++i) m = fmaxf(m, s.red[i]);
