@@ -582,7 +582,8 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
  *   q       rows of Hq heads (a multiple of cache->heads: query heads
  *           h * Hq / heads .. share kv head h), q_dtype, q_stride elements apart
  *   out     [T][Hq][dim], out_dtype
- *   causal  1: a query at position p sees j <= p; 0: all kv_len tokens
+ *   causal  1: a query at position p sees j <= p; 0: all kv_len tokens, which
+ *           may be fewer than the queries
  *   window  0, or (causal) how many tokens a query sees, itself included
  *   max_q   at least the most new tokens of a sequence
  *   max_kv  at least the largest kv_len

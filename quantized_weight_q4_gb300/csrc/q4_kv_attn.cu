@@ -442,13 +442,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     const int row0 = s.tile * kTileRows;        // first row of the tile: row = token * group + head in group
     const int rows = min(kTileRows, s.nq * p.group - row0);
     // this thread's rows
-    int qpos[2] = {-1, -1};                     // their positions, -1: no row
+    int qpos[2];                                // their positions
+    bool have[2] = {false, false};
     long long qoff[2];
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       const int r = g + 8 * e;
       const int j = (row0 + r) / p.group;
-      if (r < rows && s.c0 >= 0 && s.c0 + j < a.b.T) qpos[e] = s.len - s.nq + j;
+      qpos[e] = s.len - s.nq + j;               // below 0 (causal): it sees nothing
+      have[e] = r < rows && s.c0 >= 0 && s.c0 + j < a.b.T;
       qoff[e] = (static_cast<long long>(s.c0) + j) * a.q_stride + (s.h * p.group + (row0 + r) % p.group) * D;
     }
     // queries as fp16, scaled by a power of two per row into fp16's range: the thread's
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         float x[D / 4];
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
-        if (qpos[e] >= 0) {
+        if (have[e]) {
           if (a.q_bf16) {
             const uint2* q = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + qoff[e] + c * (D / 4));
 #pragma unroll
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
           const long long from = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
           s_rowf[team][g + 8 * e] = rowf;
           s_see[team][g + 8 * e] = make_int2(from < -1 ? -1 : static_cast<int>(from),
-                                             qpos[e] < 0 ? -1 : a.causal ? qpos[e] : s.len - 1);
+                                             !have[e] ? -1 : a.causal ? qpos[e] : s.len - 1);
         }
 #pragma unroll
         for (int t = 0; t < KT; ++t)
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     int inner_lo, inner_hi;
     {
       const int p0 = s.len - s.nq + row0 / p.group, p1 = s.len - s.nq + (row0 + rows - 1) / p.group;
-      inner_hi = (p0 < 0 ? 0 : a.causal ? p0 + 1 : s.len) / kKvBlock;
+      inner_hi = max(0, a.causal ? p0 + 1 : s.len) / kKvBlock;
       inner_lo = a.window > 0 && p1 >= a.window ? static_cast<int>((p1 - a.window + kKvBlock) / kKvBlock) : 0;
     }
     float o[NT][4];
