@@ -602,7 +602,8 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
  *   workspace  q4_kv_attention_workspace_size bytes, 16-byte aligned, the first 4 KB zero
  *              before its first use; every completed call leaves them zero.
  *              Calls that share it must not overlap.  NULL: scratch the
- *              library owns per stream (allocated by an eager call; a call
+ *              library owns per stream (allocated by an eager call; one
+ *              that needs more waits for the stream and replaces it; a call
  *              captured into a graph needs a workspace: Q4_ERR_WORKSPACE).
  */
 Q4_API int q4_kv_attention(void *out, int out_dtype, const void *q, int q_dtype, int64_t q_stride,

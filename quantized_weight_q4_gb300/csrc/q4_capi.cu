@@ -70,8 +70,8 @@ struct DeviceState {
   // while one was current may still use it, so it is kept until
   // q4_release_scratch()
   std::vector<void*> retired;
-  // per stream: scratch of the cache attention's eager calls without a
-  // workspace (zeroed when allocated)
+  // per stream, as the GEMM's: scratch of the cache attention's eager calls
+  // without a workspace (its header zeroed when allocated)
   std::map<unsigned long long, std::pair<void*, size_t>> kv_scratch;
   // the persistent sequence kernel's ring depth and resident CTAs per SM
   // (0 until first needed)
@@ -201,8 +201,8 @@ int device_info(int* sms, unsigned** status) {
   return Q4_OK;
 }
 
-void* kv_stream_scratch(cudaStream_t st, size_t bytes) {
-  std::lock_guard<std::mutex> lock(g_mu);
+void* kv_stream_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex>& hold) {
+  hold = std::unique_lock<std::mutex>(g_mu);
   DeviceState* s = nullptr;
   unsigned long long id = 0;
   if (capturing(st) || current_state(&s) != Q4_OK) return nullptr;
@@ -212,20 +212,22 @@ void* kv_stream_scratch(cudaStream_t st, size_t bytes) {
   }
   auto& have = s->kv_scratch[id];
   if (have.second >= bytes) return have.first;
+  if (have.first) {   // kernels on this stream may still use the smaller buffer; no graph does
+    if (cudaStreamSynchronize(st) != cudaSuccess) return nullptr;
+    cudaFree(have.first);
+    have = {nullptr, 0};
+  }
   const size_t want = bytes + bytes / 4;
   void* p = nullptr;
   if (cudaMalloc(&p, want) != cudaSuccess) {
     cudaGetLastError();
     return nullptr;
   }
-  if (cudaMemsetAsync(p, 0, want, st) != cudaSuccess) {
+  if (cudaMemsetAsync(p, 0, kv_attn_header_bytes(), st) != cudaSuccess) {
     cudaGetLastError();
     cudaFree(p);
     return nullptr;
   }
-  // kernels enqueued earlier (or a call of another host thread about to
-  // enqueue one) may still use the smaller buffer
-  if (have.first) s->retired.push_back(have.first);
   have = {p, want};
   return p;
 }

@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <mutex>
 
 namespace q4 {
 
@@ -112,9 +113,11 @@ int sample_max_vocab();
 // Rows of the table of entry points that need the device: SM count and status
 // word of the current device (a Q4_* status).
 int device_info(int* sms, unsigned** status);
-// Scratch of `st` for the attention calls without a workspace: zeroed when it
-// is allocated; eager calls only (nullptr while the stream is captured or
-// when it cannot be allocated).
-void* kv_stream_scratch(cudaStream_t st, size_t bytes);
+// Scratch of `st` for the attention calls without a workspace, its header
+// zeroed when it is allocated; eager calls only (nullptr while the stream is
+// captured or when it cannot be allocated).  A larger one replaces it once the
+// stream has drained, so the caller enqueues its kernels before it lets go of
+// `hold`: another host thread's call on the stream may need a larger one.
+void* kv_stream_scratch(cudaStream_t st, size_t bytes, std::unique_lock<std::mutex>& hold);
 
 }  // namespace q4

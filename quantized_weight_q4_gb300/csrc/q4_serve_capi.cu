@@ -208,10 +208,11 @@ int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_
                                   q_dtype == Q4_BF16 && out_dtype == Q4_BF16, false, sms);
   if (plan.rows > 0x7fffffffLL) return Q4_ERR_SHAPE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  std::unique_lock<std::mutex> hold;
   if (ws) {
     if (workspace_bytes < plan.total) return Q4_ERR_WORKSPACE;
   } else {
-    ws = static_cast<uint8_t*>(q4::kv_stream_scratch(st, plan.total));
+    ws = static_cast<uint8_t*>(q4::kv_stream_scratch(st, plan.total, hold));
     if (!ws) return Q4_ERR_WORKSPACE;
   }
   a.b = {page_table, table_stride, kv_len, cu_q, static_cast<int>(B), static_cast<int>(T)};
