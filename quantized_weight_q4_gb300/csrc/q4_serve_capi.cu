@@ -122,26 +122,35 @@ namespace {
 
 // Query rows (new tokens x query heads that share a kv head) up to which a
 // sequence takes the split form, for B sequences of up to max_kv tokens.  The
-// split form streams the codes once for every 16 rows, 1500 blocks of 16 tokens
-// a microsecond with some 40 blocks' time to start each; the prompt form first
-// writes the tokens as fp16 and then takes 1.6 us for each 128 of them and 256
-// rows, on one SM however long they are, with 8 us to start and end.
+// split form streams the codes once for every 16 rows, 1650 blocks of 16 tokens
+// a microsecond (heads of 64: 2800) with 30 blocks' time to start each; the
+// prompt form first writes the codes as fp16 and then takes 1.55 us for each
+// 128 tokens and 256 rows, on one SM however long they are, with 8 us to start
+// and end.
 // Measured with 8 kv heads of 128 (split / prompt form, us): one sequence of
-// 16,000 tokens, 128 rows 58 / 206, 512 rows 203 / 212; 16 sequences of 8,000,
-// 64 rows 184 / 265, 128 rows 342 / 266; 16 of 500, 64 rows 28 / 42; 64 of 300,
-// 64 rows 100 / 96; 64 of 1,000, 64 rows 161 / 172, 128 rows 278 / 191; 64 of
-// 4,000, 64 rows 385 / 535, 96 rows 555 / 538.
+// 16,000 tokens, 128 rows 59 / 212, 512 rows 187 / 220; 16 sequences of 8,000,
+// 64 rows 183 / 265, 128 rows 323 / 266; 16 of 500, 64 rows 25 / 42, 128 rows
+// 54 / 44; 64 of 300, 64 rows 73 / 97, 128 rows 131 / 102; 64 of 1,000, 64 rows
+// 133 / 174, 128 rows 245 / 194; 64 of 4,000, 64 rows 366 / 533, 96 rows
+// 537 / 535.  Heads of 64: 16 of 500, 64 rows 17 / 32; 16 of 8,000, 64 rows
+// 111 / 191, 128 rows 194 / 191; 64 of 300, 96 rows 63 / 68; 64 of 4,000, 64
+// rows 207 / 372, 128 rows 396 / 374.
 constexpr int kRowTile = 16, kMostSplitRows = 1024;
+constexpr double kStartBlocks = 30;
+double split_rate(int dim) { return dim == 128 ? 1650 : 2800; }
+// of one block of a head: writing its codes as fp16, and reading them again
+double expand_us(int dim) { return 16.0 * dim * 6 / 5.5e6; }
+double read_us(int dim) { return 16.0 * dim * 4 / 6e6; }
+
 int split_rows_of(const q4::KvView& c, int64_t B, int64_t max_kv, int sms) {
   const double heads = static_cast<double>(B) * c.heads, blocks = static_cast<double>((max_kv + 15) / 16);
-  const double bytes = heads * blocks * 16 * c.dim;      // of keys, or values
+  const double expand = heads * blocks * expand_us(c.dim), read = heads * blocks * read_us(c.dim);
   int rows = kRowTile;
   for (int r = 2 * kRowTile; r <= kMostSplitRows; r += kRowTile) {
-    const double split = 10 + heads * (r / kRowTile) * (blocks + 40) / 1500;
+    const double split = 10 + heads * (r / kRowTile) * (blocks + kStartBlocks) / split_rate(c.dim);
     const double ctas = heads * ((r + 255) / 256);
-    const double walk = static_cast<double>(static_cast<int64_t>((ctas + sms - 1) / sms)) * (((max_kv + 127) / 128) * 1.6 + 8);
-    const double read = bytes * 4 / 6e6, prompt = 12 + bytes * 6 / 5.5e6 + (walk > read ? walk : read);
-    if (split > prompt) break;
+    const double walk = static_cast<double>(static_cast<int64_t>((ctas + sms - 1) / sms)) * (((max_kv + 127) / 128) * 1.55 + 8);
+    if (split > 10 + expand + (walk > read ? walk : read)) break;
     rows = r;
   }
   return rows;
