@@ -156,6 +156,17 @@ int split_rows_of(const q4::KvView& c, int64_t B, int64_t max_kv, int sms) {
   return rows;
 }
 
+// Tokens of a sequence above which sequences of up to `rows` query rows take
+// the split form in every batch: by the costs above the prompt form takes at
+// least expand_us + read_us for a block, so that it can be the faster one only
+// while starting the split form's tiles weighs more than what each block saves.
+int64_t most_prompt_tokens(int dim, int64_t rows) {
+  if (rows > kMostSplitRows) return INT64_MAX;
+  const double tiles = static_cast<double>((rows + kRowTile - 1) / kRowTile), block = tiles / split_rate(dim);
+  const double saved = expand_us(dim) + read_us(dim) - block;
+  return saved > 1e-9 ? 16 * (static_cast<int64_t>(kStartBlocks * block / saved) + 1) : INT64_MAX;
+}
+
 struct AttnPlan {
   bool prompt;          // the call may have sequences for the prompt form
   int split_rows;       // query rows up to which a sequence takes the split form
@@ -163,16 +174,18 @@ struct AttnPlan {
   size_t split_bytes, total;
 };
 
-// sized: with room for the prompt form wherever a call of these bounds or smaller ones may take it
+// sized: with room for the prompt form wherever a call of these bounds, or of smaller ones, takes it
 AttnPlan attn_plan(const q4::KvView& c, int64_t Hq, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
                    int64_t total_kv, bool bf16, bool sized, int sms) {
   AttnPlan p = {};
+  const int64_t most_rows = (max_q < T ? max_q : T) * (Hq / c.heads);
   p.split_rows = sized ? kRowTile : split_rows_of(c, B, max_kv, sms);
-  p.prompt = bf16 && (max_q < T ? max_q : T) * (Hq / c.heads) > p.split_rows;
+  p.prompt = bf16 && most_rows > p.split_rows;
   p.split_bytes = (q4::kv_attn_split_bytes(c.dim, sms) + 255) / 256 * 256;
   p.total = p.split_bytes;
   if (p.prompt) {
-    p.rows = q4::kv_prompt_rows(static_cast<int>(B), max_kv, total_kv);
+    const int64_t longest = sized ? most_prompt_tokens(c.dim, most_rows) : max_kv;
+    p.rows = q4::kv_prompt_rows(static_cast<int>(B), longest < max_kv ? longest : max_kv, total_kv);
     p.total += q4::kv_prompt_bytes(c, static_cast<int>(B), p.rows);
   }
   return p;

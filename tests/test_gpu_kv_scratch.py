@@ -37,3 +37,46 @@ def test_growing_scratch_is_not_kept():
     q4.q4_release_scratch()
     assert before - torch.cuda.mem_get_info()[0] <= 64 * MB
     assert q4.q4_get_device_status() == q4.Q4_OK
+
+
+def test_workspace_of_few_new_tokens_on_long_sequences():
+    """Calls that take the form without copies of the cache need no room for them: 64 sequences of up to 131,072
+    tokens with 5 new ones and 8 query heads a kv head."""
+    cache = q4.KVCache.empty(4, 8, 128, 64, device=device())
+    assert q4.q4_kv_attention_workspace_size(cache, 64, 64, 320, 5, 131072) <= 512 * MB
+    # prompts have the room for all their tokens: 8 heads of 128 as fp16, keys and values
+    assert q4.q4_kv_attention_workspace_size(cache, 64, 4, 4096, 1024, 65536) >= 4 * 65536 * 8 * 128 * 4
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_workspace_serves_smaller_calls(D):
+    """A workspace of the size for some bounds takes every call within them."""
+    g = rng(D, 31)
+    heads, group = 2, 8
+    cache = q4.KVCache.empty(64, heads, D, 64, device=device())
+    for t in (cache.k, cache.v):
+        t.fill_(3)
+    for t in (cache.k_scale, cache.v_scale):
+        t.fill_(0.01)
+    calls = 0
+    for B, max_q, max_kv in [(1, 40, 100000), (8, 12, 50000), (40, 5, 20000), (64, 9, 30000), (64, 16, 3000), (6, 200, 5000)]:
+        T = B * max_q
+        size = q4.q4_kv_attention_workspace_size(cache, heads * group, B, T, max_q, max_kv)
+        assert size <= 3000 * MB
+        ws = torch.zeros(size, dtype=torch.uint8, device=device())
+        tries = [(B, max_q, max_kv), (B, max_q, 300), (B, max_q, 800), (B, max_q, 2000), (1, max_q, max_kv)]
+        tries += [(int(g.integers(1, B + 1)), int(g.integers(1, max_q + 1)), int(np.exp(g.uniform(0, np.log(max_kv)))) + 1)
+                  for _ in range(40)]
+        for b, n, kv in tries:
+            kv = min(kv, max_kv)
+            q = torch.zeros((b * n, heads * group, D), dtype=torch.bfloat16, device=device())
+            out = torch.full_like(q, float("nan"))
+            have = min(kv, 64)
+            q4.q4_kv_attention(out, q, cache, i32(np.arange(b)[:, None]), i32([have] * b), i32(starts([n] * b)), n, kv,
+                               workspace=ws)
+            # queries before the first token see nothing; the others an average of equal values
+            want = (np.arange(n) >= n - have).astype(f32) * bf16(f32(0.03))
+            got = out.float().cpu().numpy().reshape(b, n, -1)
+            assert np.all(np.abs(got - want[None, :, None]) <= 2.0 ** -8 * 0.03)
+            calls += 1
+    assert calls == 6 * 45 and q4.q4_get_device_status() == q4.Q4_OK
