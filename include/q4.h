@@ -599,7 +599,8 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
  * the largest value scale met, with all their bits down to 2^-23 of it (on
  * the tensor cores: 2^-20 of the largest that the query sees): a block whose
  * scale is smaller than that by more loses bits of its share.
- *   workspace  q4_kv_attention_workspace_size bytes, 16-byte aligned, the first 4 KB zero
+ *   workspace  q4_kv_attention_workspace_size bytes (for these bounds or
+ *              larger ones), 16-byte aligned, the first 4 KB zero
  *              before its first use; every completed call leaves them zero.
  *              Calls that share it must not overlap.  NULL: scratch the
  *              library owns per stream (allocated by an eager call; one

@@ -128,7 +128,12 @@ __device__ __forceinline__ bool is_prompt(int nq, int group, int split_rows) {
   return static_cast<long long>(nq) * group > split_rows;
 }
 
-// Exclusive prefix sums of n_of(b) into cum[0 .. B]; every thread of the block calls it.
+// Tiles counted at most: lengths on the device may be anything, and a sum past this (of more tiles than any workspace
+// holds) stays at it.
+constexpr int kMostTiles = 1 << 29;
+__device__ __forceinline__ int add_tiles(int a, int b) { return min(a + b, kMostTiles); }
+
+// Exclusive prefix sums of n_of(b), each in [0, kMostTiles], into cum[0 .. B]; every thread of the block calls it.
 template <int THREADS, typename F>
 __device__ __forceinline__ void prefix(int B, int* cum, F n_of) {
   __shared__ int s_warp[THREADS / 32];
@@ -138,7 +143,7 @@ __device__ __forceinline__ void prefix(int B, int* cum, F n_of) {
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b < B) {
-      sum += n_of(b);
+      sum = add_tiles(sum, n_of(b));
       cum[b + 1] = sum;
     }
   }
@@ -146,15 +151,16 @@ __device__ __forceinline__ void prefix(int B, int* cum, F n_of) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, up, o);
-    if (lane >= o) up += x;
+    if (lane >= o) up = add_tiles(up, x);
   }
   if (lane == 31) s_warp[warp] = up;
+  int before = __shfl_up_sync(0xffffffffu, up, 1);
+  if (lane == 0) before = 0;
   __syncthreads();
-  int before = up - sum;
-  for (int i = 0; i < warp; ++i) before += s_warp[i];
+  for (int i = 0; i < warp; ++i) before = add_tiles(before, s_warp[i]);
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < B) cum[b + 1] += before;
+    if (b < B) cum[b + 1] = add_tiles(cum[b + 1], before);
   }
   if (tid == 0) cum[0] = 0;
   __syncthreads();
@@ -170,15 +176,19 @@ __device__ __forceinline__ int find_seq(const int* cum, int B, int i) {
   return lo;
 }
 
+// Tiles of n tokens or rows.
+__device__ __forceinline__ int tiles_of(long long n, int each) {
+  return static_cast<int>(min((max(n, 0LL) + each - 1) / each, static_cast<long long>(kMostTiles)));
+}
+
 __device__ __forceinline__ int kv_tiles(const KvBatch& b, int i, int group, int split_rows) {
   const int nq = b.cu[i + 1] - b.cu[i];
-  return is_prompt(nq, group, split_rows) ? (max(b.kv_len[i], 0) + kTile - 1) / kTile : 0;
+  return is_prompt(nq, group, split_rows) ? tiles_of(b.kv_len[i], kTile) : 0;
 }
 
 __device__ __forceinline__ int q_tiles(const KvBatch& b, int i, int group, int split_rows) {
   const int nq = b.cu[i + 1] - b.cu[i];
-  return is_prompt(nq, group, split_rows)
-             ? static_cast<int>((static_cast<long long>(nq) * group + kTileRows - 1) / kTileRows) : 0;
+  return is_prompt(nq, group, split_rows) ? tiles_of(static_cast<long long>(nq) * group, kTileRows) : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -479,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
     const long long f = static_cast<long long>(len) - nq + j0 - a.window + 1;
     first = f > 0 ? static_cast<int>(f / kTile) : 0;
   }
-  const bool fits = (static_cast<long long>(tile0) + (max(len, 0) + kTile - 1) / kTile) * kTile <= p.rows_cap;
+  const bool fits = (static_cast<long long>(tile0) + tiles_of(len, kTile)) * kTile <= p.rows_cap;
   if (!fits && tid == 0) atomicOr(a.err, kDevErrIndex);   // longer sequences than the call said
   const int n = fits && last >= 0 ? max(0, last / kTile + 1 - first) : 0;
 
