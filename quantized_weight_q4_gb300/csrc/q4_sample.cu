@@ -559,6 +559,18 @@ __global__ void __launch_bounds__(kThreads, 2) q4_sample_kernel(const __grid_con
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();   // a warp reads its own elements only
+  if (inv == 0.f) {   // an infinite temperature: z of +inf is a NaN, below those beside it; as -inf it is passed over alike
+    for (int i = r.base + lane; i < r.base + r.n; i += 32) {
+      if (BF16) {
+        uint16_t& x = reinterpret_cast<uint16_t*>(xs)[i];
+        if (x == 0x7f80) x = 0xff80;
+      } else {
+        uint32_t& x = reinterpret_cast<uint32_t*>(xs)[i];
+        if (x == 0x7f800000u) x = 0xff800000u;
+      }
+    }
+    __syncwarp();
+  }
   float top = -INFINITY;
   each(r, [&](float z) { top = fmaxf(top, z); return false; }, [](float) {});
   const float theirs = top;
