@@ -628,8 +628,8 @@ Q4_API size_t q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t H
  * A NaN counts as -inf.  Weights are w = floor(exp(z - max z) * 2^40).
  * Ranked by z, equal z by index: the first top_k (<= 0: all), of those the
  * shortest prefix whose weight reaches top_p of theirs (>= 1: all), of those
- * the ones with exp(z - max z) >= min_p; the first of the ranking is always
- * kept.  The token is the first index whose kept weight, summed in index
+ * the ones with exp(z - max z) >= min_p (above 1: 1); the first of the ranking
+ * is always kept.  The token is the first index whose kept weight, summed in index
  * order, exceeds floor(u * (all kept weight)).  Weights are whole numbers, so
  * the token does not depend on the order of any sum.
  */

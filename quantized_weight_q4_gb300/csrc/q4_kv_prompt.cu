@@ -70,7 +70,7 @@ constexpr int kNoScale = -1024;             // exponent of a tile whose values a
 constexpr float kLeast = -60.0f, kZero = -40.0f;
 
 // What the softmax needs of 128 tokens of a head: a word for each lane of a warp.
-struct alignas(128) TileInfo {
+struct TileInfo {
   float ks[kBlocks];         // key scales
   float lv[kBlocks];         // log2(value scale) - e
   float iv[kBlocks];         // 2^-lv

@@ -80,3 +80,23 @@ def test_workspace_serves_smaller_calls(D):
             assert np.all(np.abs(got - want[None, :, None]) <= 2.0 ** -8 * 0.03)
             calls += 1
     assert calls == 6 * 45 and q4.q4_get_device_status() == q4.Q4_OK
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_workspace_at_any_16_bytes(kind):
+    """A workspace starts at a multiple of 16 bytes, no more: the same bits wherever that is."""
+    td = torch.float32 if kind == "f32" else torch.bfloat16
+    new, lens = [150, 1], [400, 77]
+    c = Cache(lens, 2, 128, 64, 5)
+    cache, table = c.to_device()
+    q = dev(bf16(rng(6).standard_normal((151, 16, 128)).astype(f32)), td)
+    size = q4.q4_kv_attention_workspace_size(cache, 16, 2, 151, 150, 400)
+    outs = []
+    for off in (0, 16, 48, 240):
+        ws = torch.zeros(size + off, dtype=torch.uint8, device=device())[off:]
+        out = torch.full_like(q, float("nan"))
+        for _ in range(2):
+            q4.q4_kv_attention(out, q, cache, table, i32(lens), i32(starts(new)), 150, 400, workspace=ws)
+        outs.append(out)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    assert q4.q4_get_device_status() == q4.Q4_OK
