@@ -26,6 +26,9 @@
 //   instead would round keys and values to 11 bits: a key channel that stands
 //   out then moves scores by 2^-12 of its share of them (that form: 410 us for
 //   the prompt below, and 471 for the pieces).
+// * Weights times scales are rounded to fp16, the type of the second product:
+//   2^-11 of each, below the 2^-8 of the bf16 result.  Two terms, as the split
+//   form has, would add half of all products again.
 //
 // Measured (8 kv heads of 128, 32 query heads): a prompt of 8192 tokens 424 us
 // both launches, 1296 TFLOP/s of visible products (69% of the measured bf16
@@ -743,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       float x, y;
       unpack2(add2(sum2[0], sum2[1]), x, y);
       l = fmaf(x + y, power_of_two(-down), l);
+      asm volatile("" : "+f"(l));   // what was loaded is used before the next tile's stores
     }
     // the rows' results
     if (n > 0 && ok) {
