@@ -569,6 +569,22 @@ Q4_API int q4_kv_append(const q4_kv_cache *cache, void *q_out, int q_out_dtype, 
                         const int32_t *cu_q, int64_t B, int64_t T, void *stream);
 
 /*
+ * q4_kv_append_at -- q4_kv_append with rotations of their own: row t takes row
+ * positions[t] of the tables (int32 [T]; NULL: the token's slot).  A token's
+ * slot is not its position where it is one of several drafted for the same
+ * place, or where earlier tokens have left the cache.  positions needs rope.
+ * A row outside the tables records Q4_DEVERR_INDEX; the token is not stored
+ * (zeros are, in its place) and its q_out is zero.
+ */
+Q4_API int q4_kv_append_at(const q4_kv_cache *cache, void *q_out, int q_out_dtype, const void *q,
+                           int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, int dtype, int64_t Hq, const q4_rope *rope,
+                           const int32_t *positions, const float *q_norm, const float *k_norm,
+                           float eps, const int32_t *page_table, int64_t table_stride,
+                           const int32_t *kv_len, const int32_t *cu_q, int64_t B, int64_t T,
+                           void *stream);
+
+/*
  * q4_kv_gather -- cached keys and values as numbers: row cu[b] + i of k_out
  * and v_out ([T][heads][dim], `dtype`) is token first[b] + i of sequence b.
  */
@@ -616,6 +632,133 @@ Q4_API int q4_kv_attention(void *out, int out_dtype, const void *q, int q_dtype,
 Q4_API size_t q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t Hq, int64_t B,
                                              int64_t T, int64_t max_q, int64_t max_kv,
                                              int64_t total_kv);
+
+/*
+ * q4_kv_attention_ex -- q4_kv_attention with more to say about what a query
+ * sees, and with the sums of its exponentials.
+ *   sinks   first tokens that stay visible whatever the window (a causal query
+ *           never sees past its own position).  Without a window: no effect.
+ *   tree    int32 [T][tree_words] or NULL: the new tokens are a draft in which
+ *           several may stand at one position.  Row t sees new token i of its
+ *           sequence (at slot kv_len - n + i) if and only if bit i % 32 of word
+ *           i / 32 is set (bits from n on, and words that are not there, count
+ *           as 0); its own bit is one of them.  It sees the tokens before the
+ *           new ones as a query at position kv_len - n - 1 + c does, c the number
+ *           of its bits: with a window the last window - c of them, and the
+ *           sinks.  tree needs causal.
+ *   lse     fp32 [T][Hq] or NULL: log sum_j exp(scale * q[t, h] . k_j) over the
+ *           visible j; -inf for a query that sees nothing and for rows of no
+ *           sequence
+ * Pages before the window of a sequence's first query (of a draft: of the token
+ * before it) and behind the sinks are not read: their entries in the page table
+ * may be anything.  Workspaces are those of q4_kv_attention.
+ */
+Q4_API int q4_kv_attention_ex(void *out, int out_dtype, const void *q, int q_dtype,
+                              int64_t q_stride, int64_t Hq, const q4_kv_cache *cache,
+                              const int32_t *page_table, int64_t table_stride,
+                              const int32_t *kv_len, const int32_t *cu_q, int64_t B, int64_t T,
+                              int64_t max_q, int64_t max_kv, int64_t total_kv, float scale,
+                              int causal, int64_t window, int64_t sinks, const int32_t *tree,
+                              int64_t tree_words, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * q4_kv_weigh -- how much attention cached tokens get: for every token j of a
+ * sequence and every kv head h
+ *   weight[h, j] = (j < held[b] ? weight[h, j] : 0)
+ *                  + sum over new tokens t that see j and query heads g of h:
+ *                    exp(scale * q[t, g] . k_j - lse[t, g])
+ *   weight  fp32 [pages][heads][page_tokens], the cache's slots; needs no
+ *           initialisation: tokens from held[b] on start at 0
+ *   held    int32 [B] or NULL (the tokens before the new ones)
+ *   lse     fp32 [T][Hq], as q4_kv_attention_ex gives it for the same queries;
+ *           a row whose lse is not finite adds nothing
+ * q, cache, page_table, kv_len, cu_q, max_q, max_kv, scale, causal, window and
+ * sinks as for q4_kv_attention_ex (max_q only helps to choose a form).  Each
+ * weight is one sum in fp32, in an order that the call's shape alone decides:
+ * the same call gives the same bits.  With fp32 queries scores are those of
+ * fp32 arithmetic; bf16 queries and all codes are exact.  Slots of no token
+ * keep what they hold.  A page outside the cache records Q4_DEVERR_INDEX.
+ */
+Q4_API int q4_kv_weigh(float *weight, const void *q, int q_dtype, int64_t q_stride, int64_t Hq,
+                       const float *lse, const q4_kv_cache *cache, const int32_t *page_table,
+                       int64_t table_stride, const int32_t *kv_len, const int32_t *cu_q,
+                       const int32_t *held, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
+                       float scale, int causal, int64_t window, int64_t sinks, void *stream);
+
+/*
+ * q4_kv_select -- which tokens of a sequence to keep, for each kv head.
+ *   kept    int32 [B][heads][width] (out): positions, ascending; entries past
+ *           count[b] are not written
+ *   count   int32 [B] (out): min(kv_len[b], budget[b], width), at least 0
+ *   weight  as for q4_kv_weigh; max_kv: at least the largest kv_len
+ * Kept are the first `sinks` tokens, the last `recent` ones (where these are
+ * more than count allows: first the sinks, in order, then the newest), and of
+ * the others those of the largest weight, of equal ones the lower position
+ * (-0 equals 0; NaN is below every number).  A token whose page is outside the
+ * cache counts as NaN and records Q4_DEVERR_INDEX.
+ */
+Q4_API int q4_kv_select(int32_t *kept, int64_t width, int32_t *count, const float *weight,
+                        const q4_kv_cache *cache, const int32_t *page_table, int64_t table_stride,
+                        const int32_t *kv_len, const int32_t *budget, int64_t B, int64_t max_kv,
+                        int64_t sinks, int64_t recent, void *stream);
+
+/*
+ * q4_kv_compact -- moves tokens of the cache together: token first[b] + i of
+ * head h becomes what token kept[b, h, i] is, for i < count[b].  Drops what
+ * q4_kv_select left out, or keeps the accepted path of a draft.
+ *   kept    int32 [B][kept_heads][width], kept_heads 1 (all heads alike) or the
+ *           cache's heads; ascending, kept[i] >= first + i, below kv_len[b]
+ *   count   int32 [B], at most width counts
+ *   first   int32 [B] or NULL (0)
+ *   weight  as for q4_kv_weigh, moved along, or NULL
+ *   to_table, to_stride   the page table of the tokens' new places; NULL: they
+ *           move within page_table.  Pages that to_table lists from token first
+ *           on belong to one sequence and hold no token that the call reads.
+ * A block of 16 tokens takes the largest scale s of those that its tokens come
+ * with (tokens before first, in a block that they share: their block's), and
+ * codes become rint(code * (s0 / s)), each step one fp32 operation.  kv_len is
+ * not written: afterwards a sequence has first + count tokens, and what the
+ * cache holds behind them is undefined.  An entry of kept out of its bounds,
+ * or a page outside the cache, records Q4_DEVERR_INDEX, and the token becomes
+ * zeros; a list that does not ascend gives undefined tokens.
+ */
+Q4_API int q4_kv_compact(const q4_kv_cache *cache, float *weight, const int32_t *page_table,
+                         int64_t table_stride, const int32_t *to_table, int64_t to_stride,
+                         const int32_t *kv_len, const int32_t *first, const int32_t *kept,
+                         int64_t kept_heads, int64_t width, const int32_t *count, int64_t B,
+                         void *stream);
+
+/*
+ * q4_adjust_logits -- logits before sampling: penalties, biases, grammar masks.
+ * For row t and token v, x = logits[t, v] and then, one fp32 operation a step,
+ *   repetition   if v is in the row's history: x > 0 ? x / r : x * r
+ *   frequency    x - f * n, n times that v is in the history from prompt_len on
+ *   presence     if n > 0: x - p
+ *   bias         x + bias (of entries with the same token the last one)
+ *   mask         -inf where the token's bit is 0
+ * rounded once to out_dtype.  out may be logits (same type and stride).
+ *   history      int32 [requests][history_width] or NULL; history_len int32 [T]:
+ *                tokens of it that row t counts; prompt_len int32 [T] or NULL (0)
+ *   repetition, frequency, presence   fp32 [T] or NULL (off); they need a history
+ *   bias_index, bias   int32 and fp32 [requests][bias_width], or both NULL
+ *   mask         int32 [masks][ceil(V / 32)] or NULL: bit v % 32 of word v / 32
+ *                allows token v; mask_row int32 [T] or NULL (t): its row, below 0: all
+ *                tokens are allowed
+ *   request      int32 [T] or NULL (t): row t's row of history and biases, below 0: none
+ * Tokens outside [0, V), as padding, are passed over in history and biases.  A
+ * row of requests or masks that is not there records Q4_DEVERR_INDEX and counts as none.
+ * V <= 327,672, history_width < 2^19, bias_width < 2^12.
+ */
+Q4_API int q4_adjust_logits(void *out, int out_dtype, int64_t out_stride, const void *logits,
+                            int logits_dtype, int64_t stride, int64_t T, int64_t V,
+                            const int32_t *request, int64_t requests, const int32_t *history,
+                            int64_t history_width, const int32_t *history_len,
+                            const int32_t *prompt_len, const float *repetition,
+                            const float *frequency, const float *presence,
+                            const int32_t *bias_index, const float *bias, int64_t bias_width,
+                            const int32_t *mask, int64_t masks, const int32_t *mask_row,
+                            void *stream);
 
 /*
  * q4_sample -- one token for each of T rows of V logits (V <= 327,672).

@@ -1,5 +1,6 @@
 """GB300 (sm_103a) Q4_0 weight-only dequant-matmul and the serving operators
-beside it (paged 8-bit key/value cache, attention, sampling): the Python binding.
+beside it (paged 8-bit key/value cache, attention, eviction, logits, sampling):
+the Python binding.
 
 A thin ctypes layer over the C ABI declared in ``include/q4.h``.  Every
 function marshals arguments only (device pointers, sizes, the current torch
@@ -115,10 +116,21 @@ SIGNATURES = {
     "q4_gemv_seq_grid": (_int, [_vp]),
     "q4_kv_append": (_int, [_vp, _vp, _int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _i64, _vp,
                             _vp, _vp, ctypes.c_float, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "q4_kv_append_at": (_int, [_vp, _vp, _int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _i64, _vp, _vp,
+                               _vp, _vp, ctypes.c_float, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
     "q4_kv_gather": (_int, [_vp, _vp, _int, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
     "q4_kv_attention": (_int, [_vp, _int, _vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
                                _i64, _i64, _i64, _i64, ctypes.c_float, _int, _i64, _vp, _sz, _vp]),
+    "q4_kv_attention_ex": (_int, [_vp, _int, _vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                                  _i64, _i64, _i64, _i64, ctypes.c_float, _int, _i64, _i64, _vp, _i64,
+                                  _vp, _vp, _sz, _vp]),
     "q4_kv_attention_workspace_size": (_sz, [_vp, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "q4_kv_weigh": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
+                           _i64, _i64, ctypes.c_float, _int, _i64, _i64, _vp]),
+    "q4_kv_select": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp]),
+    "q4_kv_compact": (_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "q4_adjust_logits": (_int, [_vp, _int, _i64, _vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp]),
     "q4_sample": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "q4_get_device_status": (_int, [_vp]),
     "q4_last_device_flags": (ctypes.c_uint, []),
@@ -387,7 +399,8 @@ def q4_moe_block_workspace_size(T: int, topk: int, E: int, H: int, I: int, Is: i
 # The serving calls (serving.py) test their tensors' types at every call, so that module imports torch at its top.  It is
 # imported when one of its names is first used: the rest of this package loads without torch.
 _SERVING = ("KVCache", "q4_kv_append", "q4_kv_gather", "q4_kv_attention",
-            "q4_kv_attention_workspace_size", "q4_sample")
+            "q4_kv_attention_workspace_size", "q4_kv_weigh", "q4_kv_select", "q4_kv_compact",
+            "q4_adjust_logits", "q4_sample")
 
 
 def __getattr__(name):

@@ -756,7 +756,7 @@ int moe_run(DeviceState* s, const MoeShape& m, float* out, const void* x, int x_
 
 extern "C" {
 
-int q4_version(void) { return 101; }
+int q4_version(void) { return 102; }
 
 const char* q4_status_str(int status) {
   switch (status) {

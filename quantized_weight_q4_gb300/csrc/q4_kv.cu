@@ -218,8 +218,8 @@ __device__ __forceinline__ void rotate_row(const KvAppendParams& p, int l, const
   }
 }
 
-// Queries: one warp takes kQRows heads of one token.
-template <int D, int MODE, bool BF16>
+// Queries: one warp takes kQRows heads of one token.  AT: rotated by positions of their own instead of the slots'.
+template <int D, int MODE, bool BF16, bool AT>
 __device__ __forceinline__ void append_queries(const KvAppendParams& p, unsigned task, int lane) {
   using R = Row<D>;
   constexpr int kSteps = kQRows / R::kRows, kSize = BF16 ? 2 : 4;
@@ -234,12 +234,13 @@ __device__ __forceinline__ void append_queries(const KvAppendParams& p, unsigned
   const int b = warp_count_le(p.b.B, t, [&](int j) { return __ldg(p.b.cu + j); });
   int pos = -1;
   if (b < p.b.B && t >= __ldg(p.b.cu + b)) pos = __ldg(p.b.kv_len + b) - (__ldg(p.b.cu + b + 1) - t);
-  if (MODE != kNone && pos >= p.rope_rows) {
+  const int turn_at = AT && pos >= 0 ? __ldg(p.positions + t) : pos;
+  if (MODE != kNone && pos >= 0 && static_cast<unsigned>(turn_at) >= static_cast<unsigned>(p.rope_rows)) {
     if (lane == 0) atomicOr(p.err, kDevErrIndex);
     pos = -1;
   }
   Turn tn;
-  if (MODE != kNone && pos >= 0) load_turn<D, MODE>(p, pos, l, tn);
+  if (MODE != kNone && pos >= 0) load_turn<D, MODE>(p, turn_at, l, tn);
   if (p.q_norm && pos >= 0) {
     float w[8];
     load_weights<D>(p.q_norm, l, w);
@@ -268,8 +269,9 @@ __device__ __forceinline__ float largest(float m, const float (&x)[8]) {
 // Keys or values: kBlockWarps warps take one block of one head, eight tokens
 // each (s_max: their largest magnitudes).  Slots of a sequence start at
 // cu[b] / 16 + 2 b: at least as many as the blocks it touches.  Every warp of
-// a unit (the block's warps) calls it and meets the others once.
-template <int D, int MODE, bool BF16>
+// a unit (the block's warps) calls it and meets the others once.  AT: as for the queries; a token whose position is
+// outside the tables is stored as zeros.
+template <int D, int MODE, bool BF16, bool AT>
 __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, int h, bool is_k, int unit, int part,
                                              int lane, float* s_max, float4* s_turn) {
   using R = Row<D>;
@@ -280,6 +282,7 @@ __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, 
   long long row0 = -1;
   const int b = warp_count_le(p.b.B, slot, [&](int j) { return (__ldg(p.b.cu + j) >> 4) + 2 * j; });
   R r[kSteps];
+  int turn_at[kSteps];               // AT: the tables' rows of this lane's tokens, -1 outside
   float s0 = 0.f, m = 0.f;
   if (b < p.b.B && h < p.c.heads) {
     const int c0 = __ldg(p.b.cu + b), c1 = __ldg(p.b.cu + b + 1), len = __ldg(p.b.kv_len + b);
@@ -288,7 +291,7 @@ __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, 
     const int at = slot - ((c0 >> 4) + 2 * b), blk = (from >> 4) + at;
     if (c1 > c0 && at >= 0 && blk * kKvBlock < len) {
       // tokens past the rotation tables are not stored, neither their keys nor their values
-      const int end = MODE != kNone ? min(len, p.rope_rows) : len;
+      const int end = MODE != kNone && !AT ? min(len, p.rope_rows) : len;
       lo = max(from, blk * kKvBlock), hi = min(end, (blk + 1) * kKvBlock);
       const bool beyond = end < min(len, (blk + 1) * kKvBlock);
       part_new = hi - lo < kKvBlock;
@@ -302,9 +305,17 @@ __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, 
         for (int i = 0; i < kSteps; ++i) {
           const int pos = min(max(pos0 + i * R::kRows, lo), hi - 1);
           load_row<D, BF16>(src + (pos - lo) * stride * kSize, r[i]);
+          if (AT) {
+            turn_at[i] = __ldg(p.positions + tok0 + (pos - lo));
+            if (static_cast<unsigned>(turn_at[i]) >= static_cast<unsigned>(p.rope_rows)) {
+              turn_at[i] = -1;
+              atomicOr(p.err, kDevErrIndex);
+            }
+          }
           if (MODE == kHalves && is_k) {        // no registers for these yet: by way of shared memory, the lane's own
-            const float* c = p.cos + static_cast<long long>(pos) * (D / 2) + 4 * l;
-            const float* s = p.sin + static_cast<long long>(pos) * (D / 2) + 4 * l;
+            const int row = AT ? max(turn_at[i], 0) : pos;
+            const float* c = p.cos + static_cast<long long>(row) * (D / 2) + 4 * l;
+            const float* s = p.sin + static_cast<long long>(row) * (D / 2) + 4 * l;
             const uint32_t to = smem_u32(s_turn + 2 * 32 * i + lane);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(c) : "memory");
             asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to + 32 * 16), "l"(s) : "memory");
@@ -336,10 +347,15 @@ __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, 
           tn.c[0] = u.x, tn.c[1] = u.y, tn.c[2] = u.z, tn.c[3] = u.w;
           tn.s[0] = v.x, tn.s[1] = v.y, tn.s[2] = v.z, tn.s[3] = v.w;
         } else {
-          load_turn<D, MODE>(p, min(max(pos0 + i * R::kRows, lo), hi - 1), l, tn);
+          load_turn<D, MODE>(p, AT ? max(turn_at[i], 0) : min(max(pos0 + i * R::kRows, lo), hi - 1), l, tn);
         }
         rotate_row<D, MODE>(p, l, tn, r[i]);
       }
+    }
+    if (AT) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (turn_at[i] < 0) zero_row(r[i]);
     }
     if (part_new) {
 #pragma unroll
@@ -404,7 +420,7 @@ __device__ __forceinline__ void append_block(const KvAppendParams& p, int slot, 
 }
 
 // Registers for four CTAs an SM, three with fp32's wider rows (five and four: 133 us for 101, fp32 the same).
-template <int D, int MODE, bool BF16>
+template <int D, int MODE, bool BF16, bool AT>
 __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) q4_kv_append_kernel(const __grid_constant__ KvAppendParams p,
                                                                 int kv_ctas) {
   __shared__ float s_max[kWarps];
@@ -415,10 +431,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) q4_kv_append_kernel(co
   if (static_cast<int>(blockIdx.x) < kv_ctas) {   // the longer tasks first; a CTA takes keys and values of kHeads heads
     const int unit = warp / kBlockWarps, groups = (p.c.heads + kHeads - 1) / kHeads, slot = blockIdx.x / groups;
     const int h = (blockIdx.x - slot * groups) * kHeads + (unit >> 1), part = warp % kBlockWarps;
-    append_block<D, MODE, BF16>(p, slot, h, (unit & 1) == 0, unit, part, lane, s_max + unit * kBlockWarps,
+    append_block<D, MODE, BF16, AT>(p, slot, h, (unit & 1) == 0, unit, part, lane, s_max + unit * kBlockWarps,
                                 s_turn[MODE == kHalves ? (unit >> 1) * kBlockWarps + part : 0]);
   } else {
-    append_queries<D, MODE, BF16>(p, (blockIdx.x - kv_ctas) * kWarps + warp, lane);
+    append_queries<D, MODE, BF16, AT>(p, (blockIdx.x - kv_ctas) * kWarps + warp, lane);
   }
 }
 
@@ -504,16 +520,27 @@ cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t st) {
   if (grid > 0x7fffffffLL || q_tasks > 0xffffffffLL) return cudaErrorInvalidConfiguration;
   const int mode = !p.cos ? kNone : p.rope_pairs ? kPairs : p.rope_dim == p.c.dim ? kHalves : kPart;
   static void (*const kernels[2][2][4])(KvAppendParams, int) = {
-      {{q4_kv_append_kernel<64, kNone, false>, q4_kv_append_kernel<64, kHalves, false>,
-        q4_kv_append_kernel<64, kPairs, false>, q4_kv_append_kernel<64, kPart, false>},
-       {q4_kv_append_kernel<64, kNone, true>, q4_kv_append_kernel<64, kHalves, true>,
-        q4_kv_append_kernel<64, kPairs, true>, q4_kv_append_kernel<64, kPart, true>}},
-      {{q4_kv_append_kernel<128, kNone, false>, q4_kv_append_kernel<128, kHalves, false>,
-        q4_kv_append_kernel<128, kPairs, false>, q4_kv_append_kernel<128, kPart, false>},
-       {q4_kv_append_kernel<128, kNone, true>, q4_kv_append_kernel<128, kHalves, true>,
-        q4_kv_append_kernel<128, kPairs, true>, q4_kv_append_kernel<128, kPart, true>}}};
-  return launch_pdl(kernels[p.c.dim == 128][p.in_bf16 != 0][mode], static_cast<unsigned>(grid), kThreads, st, p,
-                    static_cast<int>(kv_ctas));
+      {{q4_kv_append_kernel<64, kNone, false, false>, q4_kv_append_kernel<64, kHalves, false, false>,
+        q4_kv_append_kernel<64, kPairs, false, false>, q4_kv_append_kernel<64, kPart, false, false>},
+       {q4_kv_append_kernel<64, kNone, true, false>, q4_kv_append_kernel<64, kHalves, true, false>,
+        q4_kv_append_kernel<64, kPairs, true, false>, q4_kv_append_kernel<64, kPart, true, false>}},
+      {{q4_kv_append_kernel<128, kNone, false, false>, q4_kv_append_kernel<128, kHalves, false, false>,
+        q4_kv_append_kernel<128, kPairs, false, false>, q4_kv_append_kernel<128, kPart, false, false>},
+       {q4_kv_append_kernel<128, kNone, true, false>, q4_kv_append_kernel<128, kHalves, true, false>,
+        q4_kv_append_kernel<128, kPairs, true, false>, q4_kv_append_kernel<128, kPart, true, false>}}};
+  // by positions of their own: the rotations only
+  static void (*const kernels_at[2][2][3])(KvAppendParams, int) = {
+      {{q4_kv_append_kernel<64, kHalves, false, true>, q4_kv_append_kernel<64, kPairs, false, true>,
+        q4_kv_append_kernel<64, kPart, false, true>},
+       {q4_kv_append_kernel<64, kHalves, true, true>, q4_kv_append_kernel<64, kPairs, true, true>,
+        q4_kv_append_kernel<64, kPart, true, true>}},
+      {{q4_kv_append_kernel<128, kHalves, false, true>, q4_kv_append_kernel<128, kPairs, false, true>,
+        q4_kv_append_kernel<128, kPart, false, true>},
+       {q4_kv_append_kernel<128, kHalves, true, true>, q4_kv_append_kernel<128, kPairs, true, true>,
+        q4_kv_append_kernel<128, kPart, true, true>}}};
+  const int wide = p.c.dim == 128, bf16 = p.in_bf16 != 0;
+  const auto kernel = p.positions && mode != kNone ? kernels_at[wide][bf16][mode - kHalves] : kernels[wide][bf16][mode];
+  return launch_pdl(kernel, static_cast<unsigned>(grid), kThreads, st, p, static_cast<int>(kv_ctas));
 }
 
 cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t st) {

@@ -45,6 +45,7 @@ struct KvAppendParams {
   const float* cos;          // [rope_rows][rope_dim / 2], or null (no rotation)
   const float* sin;
   int rope_rows, rope_dim, rope_pairs;
+  const int32_t* positions;  // [T] rows of the tables, or null: the tokens' slots
   const float* q_norm;       // [dim] or null
   const float* k_norm;
   float eps;
@@ -77,8 +78,14 @@ struct KvAttnCall {
   float scale;
   int causal;
   long long window;          // keys seen by a query, itself included; 0: all
+  long long sinks;           // first tokens that stay visible whatever the window
+  const int32_t* tree;       // [T][tree_words] bits: new tokens of its sequence that each one sees, or null
+  int tree_words;
+  float* lse;                // [T][Hq] log of each row's sum of exponentials, or null
   unsigned* err;
 };
+// Whether a call has sinks, a tree or sums to give: kernels have forms of their own for it.
+inline bool kv_attn_more(const KvAttnCall& a) { return (a.sinks > 0 && a.window > 0) || a.tree || a.lse; }
 // Workspace bytes, the first kv_attn_header_bytes() of them zero before the
 // first use and left zero.
 size_t kv_attn_header_bytes();
@@ -93,6 +100,84 @@ long long kv_prompt_rows(int B, long long max_kv, long long total_kv);
 size_t kv_prompt_bytes(const KvView& c, int B, long long rows);
 cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows, void* ws,
                              cudaStream_t st);
+
+// Attention weights of cached tokens.
+struct KvWeighCall {
+  KvView c;
+  KvBatch b;
+  float* weight;             // [pages][heads][page]
+  const void* q;
+  long long q_stride;
+  int Hq, q_bf16;
+  const float* lse;          // [T][Hq]
+  const int32_t* held;       // [B] tokens that have a weight already, or null (those before the new ones)
+  float scale;
+  int causal;
+  long long window, sinks;
+  unsigned* err;
+};
+cudaError_t launch_kv_weigh(const KvWeighCall& a, int sms, cudaStream_t st);
+
+// The tokens of a sequence and head that a budget leaves.
+struct KvSelectParams {
+  KvView c;
+  const int32_t* table;
+  long long table_stride;
+  const int32_t* kv_len;
+  const int32_t* budget;
+  const float* weight;
+  int32_t* kept;             // [B][heads][width]
+  long long width;
+  int32_t* count;            // [B]
+  int B;
+  long long sinks, recent;
+  unsigned* err;
+};
+cudaError_t launch_kv_select(const KvSelectParams& p, long long max_kv, int sms, cudaStream_t st);
+
+// Moves tokens to consecutive places.
+struct KvCompactParams {
+  KvView c;
+  float* weight;             // or null
+  const int32_t* table;
+  long long table_stride;
+  const int32_t* to_table;   // or null: within `table`
+  long long to_stride;
+  const int32_t* kv_len;
+  const int32_t* first;      // or null
+  const int32_t* kept;       // [B][kept_heads][width]
+  int kept_heads;
+  long long width;
+  const int32_t* count;
+  int B;
+  unsigned* err;
+};
+cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t st);
+
+// Penalties, biases and masks of rows of logits.
+struct AdjustParams {
+  void* out;
+  const void* logits;
+  long long out_stride, stride;   // elements between rows
+  int out_bf16, bf16, T, V;
+  const int32_t* request;    // [T] or null
+  long long requests;
+  const int32_t* history;    // [requests][history_width] or null
+  int history_width;
+  const int32_t* history_len;   // [T]
+  const int32_t* prompt_len;    // [T] or null
+  const float* repetition;   // each [T] or null
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_index;    // [requests][bias_width] or null
+  const float* bias;
+  int bias_width;
+  const int32_t* mask;       // [masks][ceil(V / 32)] or null
+  long long masks;
+  const int32_t* mask_row;   // [T] or null
+  unsigned* err;
+};
+cudaError_t launch_adjust(const AdjustParams& p, int sms, cudaStream_t st);
 
 struct SampleParams {
   int32_t* tokens;

@@ -38,6 +38,7 @@
 // (an earlier step: 136 us for 127).
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "q4_kernels.h"
 #include "q4_kv_device.cuh"
@@ -60,7 +61,7 @@ constexpr float kUnitWeight = 512.0f;
 constexpr float kLazy = 4.0f;
 constexpr float kMoreScale = 4.0f;
 constexpr float kRestScale = 2048.0f;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
   KvAttnCall a;
@@ -118,6 +119,7 @@ struct Segment {
   int b, h, tile;
   int c0, nq, len;         // packed row of the first new token, new tokens, cached tokens
   int lo, hi;              // this CTA's blocks (maybe none)
+  int front, shift;        // MORE: blocks before `front` stand for those of the sinks, `shift` earlier
   long long first, last;   // units of the whole (sequence, tile, head): [first, last)
 };
 
@@ -136,14 +138,37 @@ constexpr size_t smem_bytes(int B) {
          static_cast<size_t>(B + 1) * 8 + 64;
 }
 
-// Range of blocks [lo, hi) the queries of a sequence may see, at least one block where there are queries.
-__device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len, int& lo, int& hi) {
+// Range of blocks [lo, hi) the queries of a sequence may see, at least one block where there are queries.  MORE: the
+// blocks of the sinks that lie before the window's (from `front` on) are counted right before these, from lo on.
+template <bool MORE>
+__device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len, int& lo, int& hi, int& front) {
   hi = max(1, (len + kKvBlock - 1) / kKvBlock);
   lo = 0;
   if (a.window > 0) {
-    const long long first = a.causal ? static_cast<long long>(len) - nq - a.window + 1 : 0;
+    // a drafted token that sees no new one has the position before the first
+    const long long first = a.causal ? static_cast<long long>(len) - nq - a.window + (MORE && a.tree ? 0 : 1) : 0;
     lo = first > 0 ? min(static_cast<int>(first / kKvBlock), hi - 1) : 0;
   }
+  front = lo;
+  if (MORE) lo -= static_cast<int>(min(static_cast<long long>(lo), (a.sinks + kKvBlock - 1) / kKvBlock));
+}
+// The block that a counted one stands for.
+template <bool MORE>
+__device__ __forceinline__ int real_block(const Segment& s, int blk) {
+  return MORE && blk < s.front ? blk - s.shift : blk;
+}
+
+// Word i of a drafted token's bits (row `row` of the packed tokens): 0 past the last.
+__device__ __forceinline__ uint32_t tree_word(const KvAttnCall& a, long long row, int i) {
+  return i < a.tree_words ? static_cast<uint32_t>(__ldg(a.tree + row * a.tree_words + i)) : 0u;
+}
+
+// log of a row's sum of exponentials, l relative to 2^m; -inf for a row that sees nothing, a NaN stays.
+__device__ __forceinline__ void store_lse(const KvAttnCall& a, int group, const Segment& s, int row, float m, float l) {
+  const int j = row / group;
+  if (s.c0 < 0 || s.c0 + j >= a.b.T) return;
+  a.lse[(static_cast<long long>(s.c0) + j) * a.Hq + s.h * group + row % group] =
+      l > 0.f ? (m + log2f(l)) * kLn2 : l == 0.f ? -INFINITY : l;
 }
 
 // Four elements (d ..) of query row `row` (token-major) of a (sequence, head), v over the weights' sum l.
@@ -173,7 +198,7 @@ __device__ __forceinline__ void team_sync(int team) {
 // s_l: shared memory of the team and of all warps.  Every share's factor is found once, and a thread's elements of
 // several shares are on their way together (an element at a time with its factors: the ragged batch 103 us for 96,
 // one sequence of 16,000 tokens 31 us for 22).
-template <int D, int ROWS, int TEAM>
+template <int D, int ROWS, int TEAM, bool MORE>
 __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int row0, int rows, long long o0, int shares,
                                   int team, int mine, float* t_o, float* s_m, float* s_l) {
   constexpr int crew = TEAM * 32, kVecs = D / 4, kORow = D + 8;
@@ -241,12 +266,19 @@ __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int 
 #pragma unroll
     for (int w = 0; w < TEAM; ++w) sum += s_l[(team * TEAM + w) * kRows + i / kVecs];
     store4<D>(p, s, row0 + i / kVecs, i % kVecs * 4, v[n], sum);
+    if (MORE && p.a.lse && i % kVecs == 0) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < TEAM; ++w) top = fmaxf(top, s_m[(team * TEAM + w) * kRows + i / kVecs]);
+      store_lse(p.a, p.group, s, row0 + i / kVecs, top, sum);
+    }
   }
 }
 
 // SPLIT: the 16 rows of an MMA tile are 8 query rows in two fp16 terms each; else 16 in one term.
-// TEAM: warps that take a range of units together.
-template <int D, bool SPLIT, int TEAM>
+// TEAM: warps that take a range of units together.  MORE: with sinks, drafted tokens' bits or sums of exponentials
+// (each may be absent); a form of its own, so that calls without them keep their code.
+template <int D, bool SPLIT, int TEAM, bool MORE>
 __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = SPLIT ? 1 : 2;             // query rows of a thread
   // what starting and ending a (sequence, tile, head) costs, in units: more where all of a CTA's warps wait for it
@@ -299,8 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       const int b = tid * per + i;
       if (b < B) {
         const int nq = a.b.cu[b + 1] - a.b.cu[b];
-        int lo, hi;
-        seq_blocks(a, nq, a.b.kv_len[b], lo, hi);
+        int lo, hi, front;
+        seq_blocks<MORE>(a, nq, a.b.kv_len[b], lo, hi, front);
         const long long rows = static_cast<long long>(nq) * p.group;
         const long long tiles = nq > 0 && rows <= p.max_rows ? (rows + kTileRows - 1) / kTileRows : 0;
         const long long n = tiles * a.c.heads * (hi - lo + kSegCost);
@@ -355,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     s.nq = a.b.cu[lo + 1] - s.c0;
     s.len = a.b.kv_len[lo];
     int b0, b1;
-    seq_blocks(a, s.nq, s.len, b0, b1);
+    seq_blocks<MORE>(a, s.nq, s.len, b0, b1, s.front);
+    s.shift = b0;
     const int nb = b1 - b0 + kSegCost;
     const long long in = u - s_cum[lo], pair = in / nb;
     s.h = static_cast<int>(pair % a.c.heads);
@@ -392,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       pu = ps.last;
       pblk = ps.lo + mate;
     }
-    const int pi = pblk >> sub_log2;
+    const int pi = real_block<MORE>(ps, pblk) >> sub_log2;
     ppage = pi < a.b.table_stride ? __ldg(ptable + pi) : -1;
   };
   if (more) settle();
@@ -402,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     if (more) {
       if (static_cast<unsigned>(ppage) < ppages) {
         // below 2^31: the call's checks
-        const uint32_t at = (static_cast<uint32_t>(ppage * a.c.heads + ps.h) << sub_log2) + (pblk & sub_mask);
+        const uint32_t at = (static_cast<uint32_t>(ppage * a.c.heads + ps.h) << sub_log2) + (real_block<MORE>(ps, pblk) & sub_mask);
         const int8_t* k = a.c.k + static_cast<uint64_t>(at) * Stage<D>::kCodes + lane * 16;
         const int8_t* v = a.c.v + static_cast<uint64_t>(at) * Stage<D>::kCodes + lane * 16;
 #pragma unroll
@@ -490,10 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
         const float rowf = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale * kLog2e;
         if (c == 0) {
+          if (MORE && a.tree) {                 // as many new tokens as its path has; they are seen by their bits alone
+            int path = 0;
+            if (have[e]) {
+              const long long at = static_cast<long long>(s.c0) + (row0 + g + 8 * e) / p.group;
+              for (int i = 0; i < s.nq; i += 32) {
+                const uint32_t w = tree_word(a, at, i >> 5);
+                path += __popc(s.nq - i < 32 ? w & ((1u << (s.nq - i)) - 1u) : w);
+              }
+            }
+            qpos[e] = s.len - s.nq + path - 1;
+          }
           const long long from = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
           s_rowf[team][g + 8 * e] = rowf;
           s_see[team][g + 8 * e] = make_int2(from < -1 ? -1 : static_cast<int>(from),
-                                             !have[e] ? -1 : a.causal ? qpos[e] : s.len - 1);
+                                             !have[e] ? -1 : MORE && a.tree ? s.len - s.nq - 1 : a.causal ? qpos[e] : s.len - 1);
         }
 #pragma unroll
         for (int t = 0; t < KT; ++t)
@@ -514,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     // blocks that every row of the tile sees whole (rows are in the order of their positions)
     int inner_lo, inner_hi;
     {
-      const int p0 = s.len - s.nq + row0 / p.group, p1 = s.len - s.nq + (row0 + rows - 1) / p.group;
+      int p0 = s.len - s.nq + row0 / p.group, p1 = s.len - s.nq + (row0 + rows - 1) / p.group;
+      if (MORE && a.tree) p0 = s.len - s.nq - 1, p1 = s.len - 1;   // the shortest and the longest path there may be
       inner_hi = max(0, a.causal ? p0 + 1 : s.len) / kKvBlock;
       inner_lo = a.window > 0 && p1 >= a.window ? static_cast<int>((p1 - a.window + kKvBlock) / kKvBlock) : 0;
     }
@@ -565,14 +610,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         for (int i = 0; i < 4; ++i)
           x[e][i] = (SPLIT ? sc[i >> 1][i & 1] + sc[i >> 1][2 + (i & 1)] : sc[i >> 1][2 * e + (i & 1)]) * f;
       }
-      if (blk < inner_lo || blk >= inner_hi || ks < 0.f) {   // some row does not see all of the block
-        const int pos = blk * kKvBlock + 4 * c;
+      const int real = real_block<MORE>(s, blk);
+      const bool stays = MORE && (real + 1LL) * kKvBlock <= a.sinks;   // in every window
+      if ((real < inner_lo && !stays) || real >= inner_hi || ks < 0.f) {   // some row does not see all of the block
+        const int pos = real * kKvBlock + 4 * c;
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
           const int2 see = s_see[team][g + 8 * e];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (pos + i <= see.x || pos + i > see.y || ks < 0.f) x[e][i] = -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            bool seen = pos + i > see.x && pos + i <= see.y;
+            if (MORE) {
+              seen |= pos + i < a.sinks && pos + i <= see.y;
+              const int k = pos + i - (s.len - s.nq);   // place among the new tokens
+              if (a.tree && have[e] && k >= 0 && k < s.nq) {
+                const long long at = static_cast<long long>(s.c0) + (row0 + g + 8 * e) / p.group;
+                seen = tree_word(a, at, k >> 5) >> (k & 31) & 1u;
+              }
+            }
+            if (!seen || ks < 0.f) x[e][i] = -INFINITY;
+          }
         }
       }
       // the references move rarely: by a row's scores, or by the value scale
@@ -706,9 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         const float4 x = *reinterpret_cast<const float4*>(t_o + (w * kRows + r) * kORow + d);
         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
       }
-      if (whole)
+      if (whole) {
         store4<D>(p, s, row0 + r, d, v, s_tot[team][1][r]);
-      else
+        if (MORE && a.lse && d == 0) store_lse(a, p.group, s, row0 + r, s_tot[team][0][r], s_tot[team][1][r]);
+      } else
         *reinterpret_cast<float4*>(slot + r * D + d) = v;
     }
     if (!whole) {
@@ -722,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       }
       team_sync<crew>(team);
       if (s_last[team])
-        join<D, kTileRows, TEAM>(p, s, row0, rows, o0, static_cast<int>(o1 - o0) + 1, team, mine, t_o, s_m, s_l);
+        join<D, kTileRows, TEAM, MORE>(p, s, row0, rows, o0, static_cast<int>(o1 - o0) + 1, team, mine, t_o, s_m, s_l);
     }
     team_sync<crew>(team);   // t_o and s_m are free for the next segment
     u = min(s.last, u1);
@@ -738,13 +796,17 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     else
       static_cast<float*>(a.out)[i] = 0.f;
   }
+  if (MORE && a.lse)
+    for (long long i = end * a.Hq + static_cast<long long>(blockIdx.x) * kThreads + tid; i < static_cast<long long>(a.b.T) * a.Hq;
+         i += static_cast<long long>(gridDim.x) * kThreads)
+      a.lse[i] = -INFINITY;
 }
 
-template <int D, bool SPLIT, int TEAM>
+template <int D, bool SPLIT, int TEAM, bool MORE>
 cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   const size_t smem = smem_bytes<D>(p.a.b.B);
   static std::atomic<unsigned long long> allowed;
-  cudaError_t e = allow_smem(q4_kv_attn_split_kernel<D, SPLIT, TEAM>, smem_bytes<D>(kKvMaxSeqs), allowed);
+  cudaError_t e = allow_smem(q4_kv_attn_split_kernel<D, SPLIT, TEAM, MORE>, smem_bytes<D>(kKvMaxSeqs), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -756,18 +818,18 @@ cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q4_kv_attn_split_kernel<D, SPLIT, TEAM>, p);
+  return cudaLaunchKernelEx(&cfg, q4_kv_attn_split_kernel<D, SPLIT, TEAM, MORE>, p);
 }
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, bool MORE>
 cudaError_t launch(const AttnParams& p, int rows, int grid, cudaStream_t st) {
   // Teams of four while there are more (sequence, tile, head)s than SMs: a team's start and end then fall into the
   // others' streams (quarters / whole CTAs: 64 sequences of 50 to 8191 tokens, 8 heads, 96 / 141 us; of 4096 tokens
   // 96 / 115 us).  With fewer, whole CTAs, which leave a quarter of the shares to join (one sequence of 131,071
   // tokens 62 / 54 us, 8 of 1024 17 / 16 us).
   const long long tiles = (rows + (SPLIT ? 7 : 15)) / (SPLIT ? 8 : 16);
-  return p.a.b.B * tiles * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams>(p, grid, st)
-                                              : launch<D, SPLIT, kWarps>(p, grid, st);
+  return p.a.b.B * tiles * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams, MORE>(p, grid, st)
+                                              : launch<D, SPLIT, kWarps, MORE>(p, grid, st);
 }
 
 }  // namespace
@@ -790,8 +852,12 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   // softmax instead of two (64 sequences of 50 to 8191 tokens 96 us, 106 us with rows in both halves)
   const int rows = static_cast<int>(std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows));
   const bool split = !a.q_bf16 || !a.out_bf16 || rows <= 8;
-  if (a.c.dim == 128) return split ? launch<128, true>(p, rows, sms, st) : launch<128, false>(p, rows, sms, st);
-  return split ? launch<64, true>(p, rows, sms, st) : launch<64, false>(p, rows, sms, st);
+  const auto by_form = [&](auto more) {
+    constexpr bool kMore = decltype(more)::value;
+    if (a.c.dim == 128) return split ? launch<128, true, kMore>(p, rows, sms, st) : launch<128, false, kMore>(p, rows, sms, st);
+    return split ? launch<64, true, kMore>(p, rows, sms, st) : launch<64, false, kMore>(p, rows, sms, st);
+  };
+  return kv_attn_more(a) ? by_form(std::true_type{}) : by_form(std::false_type{});
 }
 
 }  // namespace q4

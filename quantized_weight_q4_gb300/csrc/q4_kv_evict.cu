@@ -1,0 +1,335 @@
+// Leaving tokens out of the paged 8-bit cache (sm_103a): choosing those to keep
+// by their weight, and moving kept tokens together.
+#include <algorithm>
+#include <cfloat>
+
+#include "q4_kernels.h"
+#include "q4_kv_device.cuh"
+
+namespace q4 {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Choice
+// ---------------------------------------------------------------------------
+// A cluster of CTAs takes one (sequence, head); each a run of its tokens, whose
+// weights it holds in shared memory as whole numbers in the weights' order.
+// The weight down to which tokens are kept is found digit by digit (11, 11 and
+// 10 bits): each CTA counts its tokens by digit among those that agree in the
+// digits before, and every CTA adds the counts of all.  The list is then
+// written in the tokens' order: warps count what they keep in runs of their
+// own, and write it behind the counts of those before.
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMostCluster = 8;
+constexpr int kBins = 2048;
+constexpr int kSelTokens = 40960;      // of a CTA in shared memory; more are read again from their pages
+
+// A weight as a number in its order; NaN is the least.
+__device__ __forceinline__ unsigned order_of(float w) {
+  const unsigned u = __float_as_uint(w + 0.f);   // -0 becomes 0
+  return w != w ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ uint4 ld_peer4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ unsigned ld_peer(uint32_t addr) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+__global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_constant__ KvSelectParams p, int cluster, int cap) {
+  extern __shared__ __align__(16) unsigned s_mem[];
+  unsigned* s_hist = s_mem;                       // [3][kBins]
+  unsigned* s_key = s_mem + 3 * kBins;            // [cap]
+  __shared__ unsigned s_scan[kSelWarps], s_above[kSelWarps], s_equal[kSelWarps];
+  __shared__ unsigned s_digit, s_rest;            // the digit of the cut, tokens to take among those that have it
+  __shared__ uint2 s_count;                       // of this CTA: tokens above the cut, at it
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int pair = blockIdx.x / cluster, b = pair / p.c.heads, h = pair - b * p.c.heads;
+  const int len = max(0, p.kv_len[b]);
+  const int count = static_cast<int>(min(static_cast<long long>(max(0, min(len, p.budget[b]))), p.width));
+  const int head = static_cast<int>(min(static_cast<long long>(count), p.sinks));
+  const int tail = static_cast<int>(min(static_cast<long long>(count - head), p.recent));
+  const int most = len - head - tail;             // tokens to choose from, behind the sinks
+  unsigned want = count - head - tail;            // and how many of them
+  int32_t* kept = p.kept + (static_cast<long long>(b) * p.c.heads + h) * p.width;
+  if (rank == 0 && h == 0 && tid == 0) p.count[b] = count;
+  for (int i = rank * kSelThreads + tid; i < head; i += cluster * kSelThreads) kept[i] = i;
+  for (int i = rank * kSelThreads + tid; i < tail; i += cluster * kSelThreads) kept[count - tail + i] = len - tail + i;
+  // runs of whole warps' steps, alike for all warps of the cluster
+  const int run = (most + cluster * kSelThreads - 1) / (cluster * kSelThreads) * 32;   // of a warp
+  const int from = min(static_cast<long long>(most), static_cast<long long>(rank) * run * kSelWarps);
+  const int mine = min(static_cast<long long>(most) - from, static_cast<long long>(run) * kSelWarps);
+  const bool all = want == static_cast<unsigned>(most);   // the same for the whole cluster
+  if (all || want == 0) {
+    if (all)
+      for (int i = tid; i < mine; i += kSelThreads) kept[head + from + i] = head + from + i;
+    return;
+  }
+  const int32_t* table = p.table + b * p.table_stride;
+  auto weight_of = [&](int i) {                   // of this CTA's token i
+    const int pos = head + from + i, pi = pos >> p.c.page_log2;
+    const int page = pi < p.table_stride ? __ldg(table + pi) : -1;
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.pages)) {
+      if (h == 0) atomicOr(p.err, kDevErrIndex);
+      return 0u;
+    }
+    return order_of(__ldg(p.weight + (((static_cast<long long>(page) * p.c.heads + h) << p.c.page_log2) + (pos & (p.c.page - 1)))));
+  };
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) s_hist[i] = 0;
+  for (int i = tid; i < min(mine, cap); i += kSelThreads) s_key[i] = weight_of(i);
+  auto key_of = [&](int i) { return i < cap ? s_key[i] : weight_of(i); };
+  if (cluster > 1) cluster_started();
+  __syncthreads();
+
+  // ---- the cut, digit by digit from the top ----
+  unsigned cut = 0, known = 0;                    // known: bits of the cut that are found
+#pragma unroll 1
+  for (int d = 0; d < 3; ++d) {
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? kBins / 2 : kBins;
+    unsigned* hist = s_hist + d * kBins;
+    for (int i = tid; i - tid < mine; i += kSelThreads) {
+      const unsigned key = i < mine ? key_of(i) : 0u;
+      const bool in = i < mine && (key & known) == cut;
+      const unsigned digit = key >> shift & (bins - 1), who = __ballot_sync(0xffffffffu, in);
+      if (who == 0) continue;
+      // equal weights would all wait for one counter
+      const int lead = __ffs(who) - 1;
+      const unsigned first = __shfl_sync(0xffffffffu, digit, lead);
+      if (__all_sync(0xffffffffu, !in || digit == first)) {
+        if (lane == lead) atomicAdd(hist + first, __popc(who));
+      } else if (in) {
+        atomicAdd(hist + digit, 1u);
+      }
+    }
+    if (cluster > 1) {
+      if (d == 0) cluster_wait_started();
+      cluster_sync();
+    } else {
+      __syncthreads();
+    }
+    // thread t has bins 4 t .. of all CTAs, counted from the largest digit down
+    uint4 n = make_uint4(0, 0, 0, 0);
+    const int at = kBins - 4 - 4 * tid;
+    if (at < bins)
+      for (int r = 0; r < cluster; ++r) {
+        const uint4 x = cluster > 1 ? ld_peer4(peer_addr(hist + at, r)) : *reinterpret_cast<const uint4*>(hist + at);
+        n.x += x.x, n.y += x.y, n.z += x.z, n.w += x.w;
+      }
+    const unsigned sum = n.x + n.y + n.z + n.w;
+    unsigned up = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += x;
+    }
+    if (lane == 31) s_scan[warp] = up;
+    __syncthreads();
+    unsigned before = up - sum;                   // tokens of larger digits than the thread's
+    for (int i = 0; i < warp; ++i) before += s_scan[i];
+    if (before < want && want <= before + sum) {  // one thread's
+      const unsigned c[4] = {n.w, n.z, n.y, n.x};
+      unsigned left = want - before;
+      int k = 0;
+      while (k < 3 && left > c[k]) left -= c[k++];
+      s_digit = at + 3 - k;
+      s_rest = left;
+    }
+    __syncthreads();
+    cut |= s_digit << shift;
+    known |= static_cast<unsigned>(bins - 1) << shift;
+    want = s_rest;
+  }
+
+  // ---- the list: tokens above the cut, and the first `want` of those at it ----
+  unsigned above = 0, equal = 0;                  // of this warp's run
+  const int w0 = warp * run, w1 = min(mine, w0 + run);
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const unsigned key = i < w1 ? key_of(i) : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, i < w1 && key > cut));
+    equal += __popc(__ballot_sync(0xffffffffu, i < w1 && key == cut));
+  }
+  if (lane == 0) s_above[warp] = above, s_equal[warp] = equal;
+  __syncthreads();
+  if (tid == 0) {
+    uint2 n = make_uint2(0, 0);
+    for (int i = 0; i < kSelWarps; ++i) n.x += s_above[i], n.y += s_equal[i];
+    s_count = n;
+  }
+  unsigned taken = 0, passed = 0;                 // tokens above and at the cut before this warp's
+  if (cluster > 1) {
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      taken += ld_peer(peer_addr(&s_count.x, r));
+      passed += ld_peer(peer_addr(&s_count.y, r));
+    }
+  }
+  for (int i = 0; i < warp; ++i) taken += s_above[i], passed += s_equal[i];
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const unsigned key = i < w1 ? key_of(i) : 0u;
+    const unsigned up = __ballot_sync(0xffffffffu, i < w1 && key > cut), at = __ballot_sync(0xffffffffu, i < w1 && key == cut);
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned equals = passed + __popc(at & below);   // before this token
+    if ((up >> lane & 1u) || ((at >> lane & 1u) && equals < want))
+      kept[head + taken + __popc(up & below) + min(equals, want)] = head + from + i;
+    taken += __popc(up);
+    passed += __popc(at);
+  }
+  if (cluster > 1) cluster_sync();                // the counts are read by the peers
+}
+
+// ---------------------------------------------------------------------------
+// Moving
+// ---------------------------------------------------------------------------
+// A CTA takes kMoveTokens consecutive places of a head at a time, of its keys or
+// of its values.  Within one page table a place may be the source of an earlier
+// one (never of a later one: kept[i] >= first + i), so there a CTA takes all the
+// places of a (sequence, head), in order, and writes some after all of their
+// sources are in registers; into other pages every run of places has a CTA.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveTokens = 128;
+
+// 16 codes times `ratio`, each rounded: rint(code * ratio), one fp32 operation a step.
+__device__ __forceinline__ uint32_t scale4(uint32_t w, float ratio) {
+  uint32_t y = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = __float2int_rn(__fmul_rn(static_cast<float>(static_cast<int8_t>(w >> (8 * i))), ratio));
+    y |= (static_cast<uint32_t>(c) & 0xffu) << (8 * i);
+  }
+  return y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) q4_kv_compact_kernel(const __grid_constant__ KvCompactParams p) {
+  constexpr int kParts = D / 16, kEach = kMoveTokens * kParts / kMoveThreads;
+  __shared__ long long s_src[kMoveTokens], s_dst[kMoveTokens];   // rows of codes; -1: zeros, nothing to write
+  __shared__ float s_ratio[kMoveTokens];
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / p.c.heads, h = blockIdx.x - b * p.c.heads;
+  const bool values = blockIdx.z != 0;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int len = max(0, p.kv_len[b]), first = p.first ? max(0, p.first[b]) : 0;
+  const int count = static_cast<int>(min(static_cast<long long>(max(0, p.count[b])), p.width));
+  const int end = static_cast<int>(min(static_cast<long long>(first) + count, 0x7fffffffLL));
+  const int32_t* kept = p.kept + (static_cast<long long>(b) * p.kept_heads + (p.kept_heads > 1 ? h : 0)) * p.width;
+  const int32_t* to_table = p.to_table ? p.to_table : p.table;
+  const long long to_stride = p.to_table ? p.to_stride : p.table_stride;
+  float* scales = values ? p.c.vs : p.c.ks;
+  int8_t* codes = values ? p.c.v : p.c.k;
+  // places in runs that begin with a block
+  const long long step = p.to_table ? static_cast<long long>(gridDim.y) * kMoveTokens : kMoveTokens;
+  for (long long t0 = first / kKvBlock * kKvBlock + static_cast<long long>(p.to_table ? blockIdx.y : 0) * kMoveTokens;
+       count > 0 && t0 < end; t0 += step) {
+    uint4 w[kEach];
+    if (tid < kMoveTokens) {
+      const int pos = static_cast<int>(min(t0 + tid, static_cast<long long>(end)));   // `end`: no place
+      long long dst = -1, src = -1;
+      float had = 0.f;                            // the scale that the token comes with
+      if (pos < end) {
+        dst = kv_row(p.c, to_table, to_stride, b, pos, h);
+        if (pos < first) {                        // stays where it is
+          src = dst;
+        } else {
+          const int from = __ldg(kept + (pos - first));
+          if (from >= pos && from < len) src = kv_row(p.c, p.table, p.table_stride, b, from, h);
+          if (src < 0 && !values) atomicOr(p.err, kDevErrIndex);
+        }
+        if (dst < 0 && !values) atomicOr(p.err, kDevErrIndex);
+        if (src >= 0) had = scales[src >> 4];
+      }
+      float s = had;
+#pragma unroll
+      for (int o = 1; o < kKvBlock; o <<= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+      const float ratio = s > 0.f ? __fdiv_rn(had, s) : 0.f;
+      s_src[tid] = src;
+      s_dst[tid] = pos < end && !(src == dst && ratio == 1.f) ? dst : -1;
+      s_ratio[tid] = ratio;
+      const bool lead = (tid & (kKvBlock - 1)) == 0 && dst >= 0;
+      const float weight = !values && p.weight && pos >= first && pos < end && src >= 0 ? p.weight[src] : 0.f;
+      // all sources of these places have been read before the first is written
+      asm volatile("bar.sync 1, %0;" ::"n"(kMoveTokens) : "memory");
+      if (lead) scales[dst >> 4] = s;
+      if (!values && p.weight && pos >= first && pos < end && dst >= 0) p.weight[dst] = weight;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = (i * kMoveThreads + tid) / kParts, part = (i * kMoveThreads + tid) % kParts;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (s_dst[t] >= 0 && s_src[t] >= 0) w[i] = *reinterpret_cast<const uint4*>(codes + s_src[t] * D + part * 16);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = (i * kMoveThreads + tid) / kParts, part = (i * kMoveThreads + tid) % kParts;
+      if (s_dst[t] < 0) continue;
+      const float ratio = s_ratio[t];
+      if (ratio != 1.f) {
+        w[i].x = scale4(w[i].x, ratio), w[i].y = scale4(w[i].y, ratio);
+        w[i].z = scale4(w[i].z, ratio), w[i].w = scale4(w[i].w, ratio);
+      }
+      *reinterpret_cast<uint4*>(codes + s_dst[t] * D + part * 16) = w[i];
+    }
+    __syncthreads();
+  }
+}
+
+template <typename P, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(P, Args...), dim3 grid, unsigned threads, size_t smem, int cluster, cudaStream_t st,
+                       const P& p, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_select(const KvSelectParams& p, long long max_kv, int sms, cudaStream_t st) {
+  const long long pairs = static_cast<long long>(p.B) * p.c.heads;
+  // as many CTAs for a (sequence, head) as fill the GPU, or hold its tokens in shared memory, up to eight
+  int cluster = 1;
+  while (cluster < kMostCluster && (pairs * cluster < sms || max_kv > static_cast<long long>(cluster) * kSelTokens) &&
+         max_kv > cluster * 1024LL)
+    cluster *= 2;
+  const long long each = ((max_kv + cluster * kSelThreads - 1) / (cluster * kSelThreads)) * kSelThreads;
+  const int cap = static_cast<int>(std::min<long long>(each, kSelTokens));
+  const size_t smem = (3 * kBins + static_cast<size_t>(cap)) * 4;
+  static std::atomic<unsigned long long> allowed;
+  cudaError_t e = allow_smem(q4_kv_select_kernel, (3 * kBins + static_cast<size_t>(kSelTokens)) * 4, allowed);
+  if (e != cudaSuccess) return e;
+  if (pairs * cluster > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_pdl(q4_kv_select_kernel, dim3(static_cast<unsigned>(pairs * cluster)), kSelThreads, smem, cluster, st, p,
+                    cluster, cap);
+}
+
+cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t st) {
+  const long long pairs = static_cast<long long>(p.B) * p.c.heads;
+  // into other pages: a CTA for each run of places, which may begin inside a block
+  const long long runs = p.to_table ? std::min((p.width + kKvBlock + kMoveTokens - 1) / kMoveTokens, 65535LL) : 1;
+  const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(runs), 2);
+  return p.c.dim == 128 ? launch_pdl(q4_kv_compact_kernel<128>, grid, kMoveThreads, 0, 1, st, p)
+                        : launch_pdl(q4_kv_compact_kernel<64>, grid, kMoveThreads, 0, 1, st, p);
+}
+
+}  // namespace q4

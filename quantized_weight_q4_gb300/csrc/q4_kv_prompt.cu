@@ -40,6 +40,7 @@
 // round of CTAs and the expansion.  The MMA warp runs its loop as a whole, with
 // one lane issuing: elected before the loop, its single lane took 532 us.
 #include <cfloat>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -63,7 +64,7 @@ static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "the 
 constexpr int kStages = 5;                // K and V tiles in flight
 constexpr float kLazy = 8.0f;
 constexpr float kUnit = 7.0f;             // weights are 2^7 at the reference: up to 2^15 with kLazy, below fp16's 65504
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 constexpr int kBlocks = kTile / kKvBlock;   // blocks of a tile
 constexpr int kNoScale = -1024;             // exponent of a tile whose values are all zero
@@ -97,6 +98,10 @@ struct ExpandParams {
   int* q_cum;                // [B + 1] first tile of the query rows of each of those
   uint4* zeros;              // out, when rows of no sequence are this kernel's to clear, or null
   long long row_bytes;
+  float* lse;                // with zeros: their sums of exponentials, or null
+  int Hq;
+  long long window, sinks;
+  int tree;
   unsigned* err;
 };
 
@@ -194,6 +199,16 @@ __device__ __forceinline__ int q_tiles(const KvBatch& b, int i, int group, int s
   return is_prompt(nq, group, split_rows) ? tiles_of(static_cast<long long>(nq) * group, kTileRows) : 0;
 }
 
+// First token that a window leaves to the queries from number j of a sequence on, and the tiles of the sinks before its
+// tile.  A drafted token that sees no new one has the position before the first, whatever its number.
+__device__ __forceinline__ int window_start(long long window, int tree, int len, int nq, int j) {
+  const long long f = static_cast<long long>(len) - nq - window + (tree ? 0 : j + 1);
+  return window > 0 && f > 0 ? static_cast<int>(f) : 0;
+}
+__device__ __forceinline__ int sink_tiles(long long sinks, int first) {
+  return static_cast<int>(min(static_cast<long long>(first), (sinks + kTile - 1) / kTile));
+}
+
 // ---------------------------------------------------------------------------
 // Pages to fp16 rows
 // ---------------------------------------------------------------------------
@@ -231,6 +246,10 @@ __global__ void __launch_bounds__(kExpandThreads) q4_kv_expand_kernel(const __gr
     const long long at = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * kExpandThreads + tid;
     for (long long i = from + at; i < all; i += static_cast<long long>(gridDim.x) * gridDim.y * kExpandThreads)
       p.zeros[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (long long i = static_cast<long long>(max(0, min(p.b.T, p.b.cu[B]))) * p.Hq + at; i < static_cast<long long>(p.b.T) * p.Hq;
+           i += static_cast<long long>(gridDim.x) * gridDim.y * kExpandThreads)
+        p.lse[i] = -INFINITY;
   }
   const int tile = blockIdx.x, total = s_cum[B];
   if (tile == 0 && h == 0) {   // for the attention kernel
@@ -243,15 +262,22 @@ __global__ void __launch_bounds__(kExpandThreads) q4_kv_expand_kernel(const __gr
   }
   if (tile >= total) return;
   const int b = find_seq(s_cum, B, tile), t0 = (tile - s_cum[b]) * kTile, len = p.b.kv_len[b];
+  // tiles, and blocks of others, that no query sees are not read: their pages may have left the table
+  const int start = window_start(p.window, p.tree, len, p.b.cu[b + 1] - p.b.cu[b], 0);
+  if (t0 + kTile <= start && t0 >= p.sinks) return;
+  auto row_of = [&](int pos) {
+    return pos >= len || ((pos | (kKvBlock - 1)) < start && (pos & ~(kKvBlock - 1)) >= p.sinks)
+               ? -1LL : kv_row(p.c, p.b.table, p.b.table_stride, b, pos, h);
+  };
   // the record: a lane for each block of 16 tokens
   if (tid < 32) {
     const int pos = t0 + lane * kKvBlock;
     long long row = -1;
     unsigned have = 0;
     if (lane < kBlocks && pos < len) {
-      row = kv_row(p.c, p.b.table, p.b.table_stride, b, pos, h);
+      row = row_of(pos);
       if (row >= 0) have = 0xffffu >> (kKvBlock - min(kKvBlock, len - pos));
-      else if (h == 0) atomicOr(p.err, kDevErrIndex);
+      else if (h == 0 && (pos + kKvBlock > start || pos < p.sinks)) atomicOr(p.err, kDevErrIndex);
     }
     const float ks = row >= 0 ? p.c.ks[row >> 4] : 0.f, vs = row >= 0 ? p.c.vs[row >> 4] : 0.f;
     const int e = __reduce_max_sync(0xffffffffu, vs > 0.f ? exponent_above(vs) : kNoScale);
@@ -271,7 +297,7 @@ __global__ void __launch_bounds__(kExpandThreads) q4_kv_expand_kernel(const __gr
   const int D = p.c.dim, chunks = D / 16;
   for (int i = tid; i < kTile * chunks; i += kExpandThreads) {
     const int t = i / chunks, c = i % chunks, pos = t0 + t;
-    const long long row = pos < len ? kv_row(p.c, p.b.table, p.b.table_stride, b, pos, h) : -1;
+    const long long row = row_of(pos);
     const bool value = row >= 0 && p.c.vs[row >> 4] != 0.f;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -423,7 +449,17 @@ struct Cfg {
   static constexpr uint32_t kIdescPv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
 };
 
-template <int D>
+// Columns 0 .. n of 32: all from 31 on, none below 0.
+__device__ __forceinline__ uint32_t columns_to(int n) { return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1u; }
+
+// Word i of a drafted token's bits (row `row` of the packed tokens): 0 outside.
+__device__ __forceinline__ uint32_t tree_word(const KvAttnCall& a, long long row, int i) {
+  return i >= 0 && i < a.tree_words ? static_cast<uint32_t>(__ldg(a.tree + row * a.tree_words + i)) : 0u;
+}
+
+// MORE: with sinks, drafted tokens' bits or sums of exponentials (each may be absent); a form of its own, so that
+// calls without them keep their code.
+template <int D, bool MORE>
 __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_constant__ PromptParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -486,15 +522,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
   // tiles of tokens that any row sees
   const int row0 = qt * kTileRows;
   const int j0 = row0 / p.group, j1 = min(nq - 1, (row0 + kTileRows - 1) / p.group);
-  const int last = a.causal ? min(len - 1, len - nq + j1) : len - 1;
-  int first = 0;
-  if (a.window > 0) {
-    const long long f = static_cast<long long>(len) - nq + j0 - a.window + 1;
-    first = f > 0 ? static_cast<int>(f / kTile) : 0;
-  }
+  const int last = a.causal && !(MORE && a.tree) ? min(len - 1, len - nq + j1) : len - 1;
+  const int first = window_start(a.window, MORE && a.tree, len, nq, j0) / kTile;
+  const int stay = MORE ? sink_tiles(a.sinks, first) : 0;   // the sinks' tiles come first
+  auto tile_of = [&](int i) { return MORE && i < stay ? i : i + first - stay; };
   const bool fits = (static_cast<long long>(tile0) + tiles_of(len, kTile)) * kTile <= p.rows_cap;
   if (!fits && tid == 0) atomicOr(a.err, kDevErrIndex);   // longer sequences than the call said
-  const int n = fits && last >= 0 ? max(0, last / kTile + 1 - first) : 0;
+  const int n = fits && last >= 0 ? max(0, last / kTile + 1 - first + stay) : 0;
 
   if (warp >= kTmaWarp) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -505,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
         const int st = it % kStages;
         if (it >= kStages && !gwait(&empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err)) break;
         mbar_arrive_expect_tx(&full[st], C::kTileBytes);
-        const int row = (tile0 + first + (it >> 1)) * kTile, z = (it & 1) * a.c.heads + h;
+        const int row = (tile0 + tile_of(it >> 1)) * kTile, z = (it & 1) * a.c.heads + h;
 #pragma unroll
         for (int x = 0; x < D / 64; ++x)
           tma_load_3d(ring + st * C::kTileBytes + x * C::kHalf, &p.kv, x * 64, row, z, &full[st]);
@@ -625,22 +659,28 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       mbar_arrive(q_ready);
     }
     // positions the row sees: (from, to]; one that does not exist sees all, so that no tile is on its edge
-    const int qpos = len - nq + j;
-    const int to = !have ? 0x7fffffff : a.causal ? qpos : len - 1;
+    int qpos = len - nq + j;
+    const int to = !have ? 0x7fffffff : MORE && a.tree ? len - nq - 1 : a.causal ? qpos : len - 1;
+    if (MORE && a.tree && have) {   // as many new tokens as its path has; they are seen by their bits alone
+      int path = 0;
+      for (int i = 0; i < nq; i += 32)
+        path += __popc(tree_word(a, static_cast<long long>(c0) + j, i >> 5) & columns_to(nq - 1 - i));
+      qpos = len - nq + path - 1;
+    }
     const long long f = have && a.window > 0 ? static_cast<long long>(qpos) - a.window : -1LL;
     const int from = f < -1 ? -1 : static_cast<int>(f);
     float m = -INFINITY, l = 0.f;
     int e = kNoScale;             // the sums are relative to 2^e, above the value scales that the row has seen
     bool ok = true;
     // a word of the tile's record for each lane, read a tile ahead, and by way of shared memory every scale for all
-    const int* info = reinterpret_cast<const int*>(p.info + static_cast<long long>(h) * (p.rows_cap / kTile) + tile0 + first) + lane;
-    int next_rec = n > 0 ? __ldg(info) : 0;
+    const int* info = reinterpret_cast<const int*>(p.info + static_cast<long long>(h) * (p.rows_cap / kTile) + tile0) + lane;
+    int next_rec = n > 0 ? __ldg(info + 32 * tile_of(0)) : 0;
     const uint32_t my_scales = smem_u32(s_scales + warp * kScaleWords);   // key scales, lv and iv, each twice
     const uint32_t put = my_scales + 8 * lane;
     const f32x2 rowc2 = dup2(rowc);
     for (int i = 0; i < n; ++i) {
-      const int t0 = (first + i) * kTile, rec = next_rec;
-      if (i + 1 < n) next_rec = __ldg(info + 32 * (i + 1));
+      const int t0 = tile_of(i) * kTile, rec = next_rec;
+      if (i + 1 < n) next_rec = __ldg(info + 32 * tile_of(i + 1));
       __syncwarp();               // the last tile's scales have been read
       if (lane < 24) asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(put), "r"(rec) : "memory");
       __syncwarp();
@@ -649,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       const int tile_e = __shfl_sync(0xffffffffu, rec, kLaneE);
       const int full = __shfl_sync(0xffffffffu, rec, kLaneFull);
       // tiles on the edge of what a row sees, or with tokens that do not exist (the same for the whole warp)
-      const bool mine = t0 + kTile - 1 > to || t0 <= from || full == 0;
+      const bool mine = t0 + kTile - 1 > to || (t0 <= from && !(MORE && t0 + kTile <= a.sinks)) || full == 0;
       const bool edge = __any_sync(0xffffffffu, mine);
       ok = gwait(&s_full[g], i & 1, &s_fail, a.err);
       ok = __all_sync(0xffffffffu, ok);
@@ -670,9 +710,27 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
 #pragma unroll
         for (int x = 0; x < 4; ++x) bits[x] = __shfl_sync(0xffffffffu, rec, kLaneSeen + x);
         const int lo = from - t0, hi = to - t0;
+        if (MORE) {
 #pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c <= lo || c > hi || !((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+          for (int x = 0; x < 4; ++x) {
+            const int at = t0 + 32 * x;
+            uint32_t see = columns_to(to - at) & ~columns_to(from - at);
+            if (at < a.sinks) see |= columns_to(to - at) & columns_to(static_cast<int>(min(a.sinks - at, 32LL)) - 1);
+            if (a.tree && have) {
+              const int k = at - (len - nq);   // place among the new tokens
+              const long long row = static_cast<long long>(c0) + j;
+              see |= __funnelshift_r(tree_word(a, row, k >> 5), tree_word(a, row, (k >> 5) + 1), k & 31);
+            }
+            bits[x] &= see;
+          }
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (!((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+        } else {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c <= lo || c > hi || !((bits[c >> 5] >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+        }
 #pragma unroll
         for (int k = 0; k < kBlocks; ++k) mul[k] = dup2(max_nan(low2(mul[k]), 1e-30f));   // masked scores stay -inf
       }
@@ -758,6 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_prompt_kernel(const __grid_
       // a row that sees nothing: zeros; a NaN stays
       const float k = l > 0.f ? power_of_two(e) / l : l == 0.f ? 0.f : l;
       const long long at = ((static_cast<long long>(c0) + j) * a.Hq + h * p.group + row % p.group) * D;
+      if (MORE && a.lse && have) a.lse[at / D] = l > 0.f ? (m + log2f(l) - kUnit) * kLn2 : l == 0.f ? -INFINITY : l;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
@@ -863,6 +922,11 @@ cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows
   // without a split form beside it, rows of no sequence are this form's
   x.zeros = split_rows == 0 ? static_cast<uint4*>(a.out) : nullptr;
   x.row_bytes = static_cast<long long>(a.Hq) * a.c.dim * 2;
+  x.lse = a.lse;
+  x.Hq = a.Hq;
+  x.window = a.window;
+  x.sinks = a.sinks;
+  x.tree = a.tree != nullptr;
   x.err = a.err;
   PromptParams p = {};
   p.a = a;
@@ -888,12 +952,17 @@ cudaError_t launch_kv_prompt(const KvAttnCall& a, int split_rows, long long rows
   const long long tiles = (static_cast<long long>(a.b.T) * p.group + kTileRows - 1) / kTileRows + a.b.B;
   if (tiles * a.c.heads > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(tiles * a.c.heads));
-  static std::atomic<unsigned long long> allowed[2];
-  e = a.c.dim == 128 ? allow_smem(q4_kv_prompt_kernel<128>, Cfg<128>::kSmem, allowed[0])
-                     : allow_smem(q4_kv_prompt_kernel<64>, Cfg<64>::kSmem, allowed[1]);
-  if (e != cudaSuccess) return e;
-  return a.c.dim == 128 ? launch_pdl(q4_kv_prompt_kernel<128>, grid, kThreads, Cfg<128>::kSmem, st, p)
-                        : launch_pdl(q4_kv_prompt_kernel<64>, grid, kThreads, Cfg<64>::kSmem, st, p);
+  const auto run = [&](auto dim, auto more) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool kMore = decltype(more)::value;
+    static std::atomic<unsigned long long> allowed;
+    const cudaError_t x = allow_smem(q4_kv_prompt_kernel<D, kMore>, Cfg<D>::kSmem, allowed);
+    return x != cudaSuccess ? x : launch_pdl(q4_kv_prompt_kernel<D, kMore>, grid, kThreads, Cfg<D>::kSmem, st, p);
+  };
+  const auto by_dim = [&](auto more) {
+    return a.c.dim == 128 ? run(std::integral_constant<int, 128>{}, more) : run(std::integral_constant<int, 64>{}, more);
+  };
+  return kv_attn_more(a) ? by_dim(std::true_type{}) : by_dim(std::false_type{});
 }
 
 }  // namespace q4

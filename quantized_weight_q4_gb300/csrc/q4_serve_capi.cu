@@ -60,18 +60,27 @@ int q4_kv_append(const q4_kv_cache* cache, void* q_out, int q_out_dtype, const v
                  const q4_rope* rope, const float* q_norm, const float* k_norm, float eps,
                  const int32_t* page_table, int64_t table_stride, const int32_t* kv_len, const int32_t* cu_q,
                  int64_t B, int64_t T, void* stream) {
+  return q4_kv_append_at(cache, q_out, q_out_dtype, q, q_stride, k, k_stride, v, v_stride, dtype, Hq, rope, nullptr,
+                         q_norm, k_norm, eps, page_table, table_stride, kv_len, cu_q, B, T, stream);
+}
+
+int q4_kv_append_at(const q4_kv_cache* cache, void* q_out, int q_out_dtype, const void* q, int64_t q_stride,
+                    const void* k, int64_t k_stride, const void* v, int64_t v_stride, int dtype, int64_t Hq,
+                    const q4_rope* rope, const int32_t* positions, const float* q_norm, const float* k_norm, float eps,
+                    const int32_t* page_table, int64_t table_stride, const int32_t* kv_len, const int32_t* cu_q,
+                    int64_t B, int64_t T, void* stream) {
   q4::KvAppendParams p = {};
   int rc = check_cache(cache, &p.c);
   if (rc == Q4_OK) rc = check_batch(page_table, table_stride, kv_len, cu_q, B, T);
   if (rc != Q4_OK) return rc;
   if (!known(dtype) || (q && !known(q_out_dtype))) return Q4_ERR_DTYPE;
-  if (!q != !q_out || (q && Hq <= 0) || (q_norm && !q) || !(eps >= 0.f)) return Q4_ERR_ARG;
+  if (!q != !q_out || (q && Hq <= 0) || (q_norm && !q) || !(eps >= 0.f) || (positions && !rope)) return Q4_ERR_ARG;
   if (q && Hq > 4096) return Q4_ERR_SHAPE;
   rc = check_rows(k, k_stride, cache->heads, cache->dim, dtype);
   if (rc == Q4_OK) rc = check_rows(v, v_stride, cache->heads, cache->dim, dtype);
   if (rc == Q4_OK && q) rc = check_rows(q, q_stride, Hq, cache->dim, dtype);
   if (rc != Q4_OK) return rc;
-  if (!aligned(q_out, 16) || !aligned(q_norm, 4) || !aligned(k_norm, 4)) return Q4_ERR_ALIGN;
+  if (!aligned(q_out, 16) || !aligned(q_norm, 4) || !aligned(k_norm, 4) || !aligned(positions, 4)) return Q4_ERR_ALIGN;
   if (rope) {
     if (!rope->cos || !rope->sin || rope->rows <= 0 || rope->dim <= 0 || rope->dim > cache->dim ||
         (rope->style != Q4_ROPE_HALVES && rope->style != Q4_ROPE_PAIRS))
@@ -83,6 +92,7 @@ int q4_kv_append(const q4_kv_cache* cache, void* q_out, int q_out_dtype, const v
     p.rope_rows = static_cast<int>(rope->rows);
     p.rope_dim = static_cast<int>(rope->dim);
     p.rope_pairs = rope->style == Q4_ROPE_PAIRS;
+    p.positions = positions;
   }
   int sms = 0;
   rc = q4::device_info(&sms, &p.err);
@@ -210,18 +220,31 @@ int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_
                     const int32_t* kv_len, const int32_t* cu_q, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
                     int64_t total_kv, float scale, int causal, int64_t window, void* workspace,
                     size_t workspace_bytes, void* stream) {
+  return q4_kv_attention_ex(out, out_dtype, q, q_dtype, q_stride, Hq, cache, page_table, table_stride, kv_len, cu_q, B,
+                            T, max_q, max_kv, total_kv, scale, causal, window, 0, nullptr, 0, nullptr, workspace,
+                            workspace_bytes, stream);
+}
+
+int q4_kv_attention_ex(void* out, int out_dtype, const void* q, int q_dtype, int64_t q_stride, int64_t Hq,
+                       const q4_kv_cache* cache, const int32_t* page_table, int64_t table_stride,
+                       const int32_t* kv_len, const int32_t* cu_q, int64_t B, int64_t T, int64_t max_q,
+                       int64_t max_kv, int64_t total_kv, float scale, int causal, int64_t window, int64_t sinks,
+                       const int32_t* tree, int64_t tree_words, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream) {
   q4::KvAttnCall a = {};
   int rc = check_cache(cache, &a.c);
   if (rc == Q4_OK) rc = check_batch(page_table, table_stride, kv_len, cu_q, B, T);
   if (rc != Q4_OK) return rc;
   if (!out || Hq <= 0 || max_q <= 0 || max_kv <= 0 || total_kv < 0 || window < 0 || (causal != 0 && causal != 1) ||
-      (window > 0 && !causal))
+      (window > 0 && !causal) || sinks < 0 || (tree && (!causal || tree_words <= 0)))
     return Q4_ERR_ARG;
   if (!known(q_dtype) || !known(out_dtype)) return Q4_ERR_DTYPE;
-  if (Hq % cache->heads || Hq > 4096 || max_kv > (1LL << 30)) return Q4_ERR_SHAPE;
+  if (Hq % cache->heads || Hq > 4096 || max_kv > (1LL << 30) || sinks > (1LL << 30) ||
+      (tree && tree_words > (1LL << 19)))
+    return Q4_ERR_SHAPE;
   rc = check_rows(q, q_stride, Hq, cache->dim, q_dtype);
   if (rc != Q4_OK) return rc;
-  if (!aligned(out, 16) || !aligned(workspace, 16)) return Q4_ERR_ALIGN;
+  if (!aligned(out, 16) || !aligned(workspace, 16) || !aligned(tree, 4) || !aligned(lse, 4)) return Q4_ERR_ALIGN;
   int sms = 0;
   rc = q4::device_info(&sms, &a.err);
   if (rc != Q4_OK) return rc;
@@ -241,6 +264,7 @@ int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_
   a.out = out, a.q = q, a.q_stride = q_stride, a.Hq = static_cast<int>(Hq);
   a.q_bf16 = q_dtype == Q4_BF16, a.out_bf16 = out_dtype == Q4_BF16;
   a.scale = scale, a.causal = causal, a.window = window;
+  a.sinks = sinks, a.tree = tree, a.tree_words = static_cast<int>(tree_words), a.lse = lse;
   const int most = static_cast<int>(max_q < T ? max_q : T);
   if (!plan.prompt) return status_of(q4::launch_kv_attn_split(a, most, 0x7fffffff, ws, sms, st));
   // one sequence: no second form beside the prompt's
@@ -249,6 +273,113 @@ int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_
   if (B > 1) e = q4::launch_kv_attn_split(a, most, split_rows, ws, sms, st);
   if (e == cudaSuccess) e = q4::launch_kv_prompt(a, split_rows, plan.rows, ws + plan.split_bytes, st);
   return status_of(e);
+}
+
+int q4_kv_weigh(float* weight, const void* q, int q_dtype, int64_t q_stride, int64_t Hq, const float* lse,
+                const q4_kv_cache* cache, const int32_t* page_table, int64_t table_stride, const int32_t* kv_len,
+                const int32_t* cu_q, const int32_t* held, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
+                float scale, int causal, int64_t window, int64_t sinks, void* stream) {
+  q4::KvWeighCall a = {};
+  int rc = check_cache(cache, &a.c);
+  if (rc == Q4_OK) rc = check_batch(page_table, table_stride, kv_len, cu_q, B, T);
+  if (rc != Q4_OK) return rc;
+  if (!weight || !lse || Hq <= 0 || max_q <= 0 || max_kv <= 0 || window < 0 || sinks < 0 ||
+      (causal != 0 && causal != 1) || (window > 0 && !causal))
+    return Q4_ERR_ARG;
+  if (!known(q_dtype)) return Q4_ERR_DTYPE;
+  if (Hq % cache->heads || Hq > 4096 || max_kv > (1LL << 30) || sinks > (1LL << 30)) return Q4_ERR_SHAPE;
+  rc = check_rows(q, q_stride, Hq, cache->dim, q_dtype);
+  if (rc != Q4_OK) return rc;
+  if (!aligned(weight, 16) || !aligned(lse, 4) || !aligned(held, 4)) return Q4_ERR_ALIGN;
+  int sms = 0;
+  rc = q4::device_info(&sms, &a.err);
+  if (rc != Q4_OK) return rc;
+  a.b = {page_table, table_stride, kv_len, cu_q, static_cast<int>(B), static_cast<int>(T)};
+  a.weight = weight, a.q = q, a.q_stride = q_stride, a.Hq = static_cast<int>(Hq), a.q_bf16 = q_dtype == Q4_BF16;
+  a.lse = lse, a.held = held, a.scale = scale, a.causal = causal, a.window = window, a.sinks = sinks;
+  return status_of(q4::launch_kv_weigh(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int q4_kv_select(int32_t* kept, int64_t width, int32_t* count, const float* weight, const q4_kv_cache* cache,
+                 const int32_t* page_table, int64_t table_stride, const int32_t* kv_len, const int32_t* budget,
+                 int64_t B, int64_t max_kv, int64_t sinks, int64_t recent, void* stream) {
+  q4::KvSelectParams p = {};
+  int rc = check_cache(cache, &p.c);
+  if (rc == Q4_OK) rc = check_batch(page_table, table_stride, kv_len, budget, B, 1);
+  if (rc != Q4_OK) return rc;
+  if (!kept || !count || !weight || width <= 0 || max_kv <= 0 || sinks < 0 || recent < 0) return Q4_ERR_ARG;
+  if (max_kv > (1LL << 30) || width > (1LL << 30)) return Q4_ERR_SHAPE;
+  if (!aligned(kept, 4) || !aligned(count, 4) || !aligned(weight, 16)) return Q4_ERR_ALIGN;
+  int sms = 0;
+  rc = q4::device_info(&sms, &p.err);
+  if (rc != Q4_OK) return rc;
+  p.table = page_table, p.table_stride = table_stride, p.kv_len = kv_len, p.budget = budget;
+  p.weight = weight, p.kept = kept, p.width = width, p.count = count, p.B = static_cast<int>(B);
+  p.sinks = sinks, p.recent = recent;
+  return status_of(q4::launch_kv_select(p, max_kv, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int q4_kv_compact(const q4_kv_cache* cache, float* weight, const int32_t* page_table, int64_t table_stride,
+                  const int32_t* to_table, int64_t to_stride, const int32_t* kv_len, const int32_t* first,
+                  const int32_t* kept, int64_t kept_heads, int64_t width, const int32_t* count, int64_t B,
+                  void* stream) {
+  q4::KvCompactParams p = {};
+  int rc = check_cache(cache, &p.c);
+  if (rc == Q4_OK) rc = check_batch(page_table, table_stride, kv_len, count, B, 1);
+  if (rc != Q4_OK) return rc;
+  if (!kept || width <= 0 || (kept_heads != 1 && kept_heads != cache->heads) || (to_table && to_stride <= 0))
+    return Q4_ERR_ARG;
+  if (width > (1LL << 30) || (to_table && to_stride > (1LL << 27))) return Q4_ERR_SHAPE;
+  if (!aligned(weight, 16) || !aligned(to_table, 4) || !aligned(first, 4) || !aligned(kept, 4)) return Q4_ERR_ALIGN;
+  int sms = 0;
+  rc = q4::device_info(&sms, &p.err);
+  if (rc != Q4_OK) return rc;
+  p.weight = weight, p.table = page_table, p.table_stride = table_stride;
+  p.to_table = to_table, p.to_stride = to_stride;
+  p.kv_len = kv_len, p.first = first, p.kept = kept, p.kept_heads = static_cast<int>(kept_heads), p.width = width;
+  p.count = count, p.B = static_cast<int>(B);
+  return status_of(q4::launch_kv_compact(p, static_cast<cudaStream_t>(stream)));
+}
+
+int q4_adjust_logits(void* out, int out_dtype, int64_t out_stride, const void* logits, int logits_dtype,
+                     int64_t stride, int64_t T, int64_t V, const int32_t* request, int64_t requests,
+                     const int32_t* history, int64_t history_width, const int32_t* history_len,
+                     const int32_t* prompt_len, const float* repetition, const float* frequency,
+                     const float* presence, const int32_t* bias_index, const float* bias, int64_t bias_width,
+                     const int32_t* mask, int64_t masks, const int32_t* mask_row, void* stream) {
+  if (!out || !logits || T <= 0 || V <= 0 || stride < V || out_stride < V) return Q4_ERR_ARG;
+  if (!known(logits_dtype) || !known(out_dtype)) return Q4_ERR_DTYPE;
+  const bool rows = history || bias_index;
+  if ((history && (history_width <= 0 || !history_len)) ||
+      (!history && (history_len || prompt_len || repetition || frequency || presence)) || !bias_index != !bias ||
+      (bias && bias_width <= 0) || (mask && masks <= 0) || (mask_row && !mask) || (request && !rows) ||
+      (rows && requests <= 0))
+    return Q4_ERR_ARG;
+  // a row of its own for each row of logits, or a row named
+  if ((rows && !request && requests < T) || (mask && !mask_row && masks < T)) return Q4_ERR_ARG;
+  if (out == logits && (out_dtype != logits_dtype || (out_stride != stride && T > 1))) return Q4_ERR_ARG;
+  if (V > q4::sample_max_vocab() || T > 65535 || stride > (1LL << 40) || out_stride > (1LL << 40) ||
+      (history && history_width >= (1 << 19)) || (bias && bias_width >= (1 << 12)))
+    return Q4_ERR_SHAPE;
+  if (!aligned(logits, size_of(logits_dtype)) || !aligned(out, size_of(out_dtype)) || !aligned(request, 4) ||
+      !aligned(history, 4) || !aligned(history_len, 4) || !aligned(prompt_len, 4) || !aligned(repetition, 4) ||
+      !aligned(frequency, 4) || !aligned(presence, 4) || !aligned(bias_index, 4) || !aligned(bias, 4) ||
+      !aligned(mask, 4) || !aligned(mask_row, 4))
+    return Q4_ERR_ALIGN;
+  q4::AdjustParams p = {};
+  int sms = 0;
+  const int rc = q4::device_info(&sms, &p.err);
+  if (rc != Q4_OK) return rc;
+  p.out = out, p.logits = logits, p.out_stride = out_stride, p.stride = stride;
+  p.out_bf16 = out_dtype == Q4_BF16, p.bf16 = logits_dtype == Q4_BF16;
+  p.T = static_cast<int>(T), p.V = static_cast<int>(V);
+  p.request = request, p.requests = requests;
+  p.history = history, p.history_width = static_cast<int>(history_width);
+  p.history_len = history_len, p.prompt_len = prompt_len;
+  p.repetition = repetition, p.frequency = frequency, p.presence = presence;
+  p.bias_index = bias_index, p.bias = bias, p.bias_width = static_cast<int>(bias_width);
+  p.mask = mask, p.masks = masks, p.mask_row = mask_row;
+  return status_of(q4::launch_adjust(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int q4_sample(int32_t* tokens, float* probs, const void* logits, int logits_dtype, int64_t stride, int64_t T,

@@ -1,5 +1,5 @@
 """The serving operators beside the matmuls: the paged 8-bit key/value cache,
-attention over it, and sampling (include/q4.h, "Serving").  Reached through the
+attention over it, leaving tokens out of it, and logits to tokens (include/q4.h, "Serving").  Reached through the
 package's names.
 
 These calls are made once a token and layer, so their checks are kept short:
@@ -85,6 +85,16 @@ def _table(t, n):
     return t.data_ptr(), cols
 
 
+def _words(name, t, n=None):
+    """Data pointer and columns of a contiguous int32 CUDA tensor of two dimensions, of n rows."""
+    if t.dtype is not torch.int32 or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} is a contiguous int32 CUDA tensor of two dimensions")
+    rows, cols = t.shape
+    if n is not None and rows != n:
+        raise ValueError(f"{name} has {rows} rows, not {n}")
+    return t.data_ptr(), cols
+
+
 def _floats(name, t, n):
     """Data pointer of a contiguous fp32 CUDA tensor of n elements, or None."""
     if t is None:
@@ -111,11 +121,12 @@ def _raw_stream(stream, t):
 
 def q4_kv_append(cache: KVCache, q_out, q, k, v, page_table, kv_len, cu_q, cos=None, sin=None,
                  rope_style: int = Q4_ROPE_HALVES, q_norm=None, k_norm=None, eps: float = 1e-6,
-                 stream=None) -> None:
+                 stream=None, positions=None) -> None:
     """New tokens' keys and values into the cache, their queries rotated into
     q_out (include/q4.h).  q [T, Hq, dim], k, v [T, heads, dim]: views whose
     rows may be strided; q and q_out may both be None.  cos, sin: fp32
-    [positions, rotated dim / 2], or None."""
+    [positions, rotated dim / 2], or None.  positions: int32 [T], each token's row
+    of the tables where that is not its slot (drafted tokens; after an eviction)."""
     T, B, heads, dim = k.shape[0], kv_len.shape[0], cache.heads, cache.dim
     kp, ks = _rows(k, heads, dim)
     vp, vs = _rows(v, heads, dim)
@@ -138,8 +149,12 @@ def q4_kv_append(cache: KVCache, q_out, q, k, v, page_table, kv_len, cu_q, cos=N
                            rope_style)
         rope = ctypes.addressof(table)
     pages, cols = _table(page_table, B)
-    rc = lib().q4_kv_append(
-        cache.ref, out, out_dtype, qp, qs, kp, ks, vp, vs, dtype, Hq, rope,
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions need cos and sin")
+        positions = _index("positions", positions, T)
+    rc = lib().q4_kv_append_at(
+        cache.ref, out, out_dtype, qp, qs, kp, ks, vp, vs, dtype, Hq, rope, positions,
         _floats("q_norm", q_norm, dim), _floats("k_norm", k_norm, dim), eps,
         pages, cols,
         _index("kv_len", kv_len, B), _index("cu_q", cu_q, B + 1), B, T, _raw_stream(stream, k))
@@ -166,9 +181,13 @@ def q4_kv_gather(k_out, v_out, cache: KVCache, page_table, first, cu, stream=Non
 
 def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int, max_kv: int,
                     total_kv: int = 0, scale: float | None = None, causal: bool = True,
-                    window: int = 0, workspace=None, stream=None) -> None:
+                    window: int = 0, workspace=None, stream=None, sinks: int = 0, tree=None,
+                    lse=None) -> None:
     """Attention of the new tokens' queries q [T, Hq, dim] over the cached
-    tokens into out [T, Hq, dim] (include/q4.h).  scale: dim ** -0.5 by default."""
+    tokens into out [T, Hq, dim] (include/q4.h).  scale: dim ** -0.5 by default.
+    sinks: first tokens that a window leaves visible.  tree: int32 [T, words],
+    the bits of the new tokens that each one sees.  lse: fp32 [T, Hq] (out), the
+    logarithm of each row's sum of exponentials."""
     T, Hq, dim = q.shape
     B = kv_len.shape[0]
     qp, qs = _rows(q, Hq, cache.dim)
@@ -181,12 +200,15 @@ def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int
         _require_cuda(workspace)
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     pages, cols = _table(page_table, B)
-    rc = lib().q4_kv_attention(
+    tree_ptr, words = None, 0
+    if tree is not None:
+        tree_ptr, words = _words("tree", tree, T)
+    rc = lib().q4_kv_attention_ex(
         op, out_dtype, qp, q_dtype, qs, Hq, cache.ref,
         pages, cols,
         _index("kv_len", kv_len, B), _index("cu_q", cu_q, B + 1), B, T, max_q, max_kv, total_kv,
-        dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, ws, ws_bytes,
-        _raw_stream(stream, q))
+        dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, sinks, tree_ptr, words,
+        _floats("lse", lse, T * Hq), ws, ws_bytes, _raw_stream(stream, q))
     if rc:
         raise Q4Error("q4_kv_attention", rc)
 
@@ -194,6 +216,120 @@ def q4_kv_attention(out, q, cache: KVCache, page_table, kv_len, cu_q, max_q: int
 def q4_kv_attention_workspace_size(cache: KVCache, Hq: int, B: int, T: int, max_q: int,
                                    max_kv: int, total_kv: int = 0) -> int:
     return lib().q4_kv_attention_workspace_size(cache.ref, Hq, B, T, max_q, max_kv, total_kv)
+
+
+def q4_kv_weigh(weight, q, lse, cache: KVCache, page_table, kv_len, cu_q, max_q: int, max_kv: int,
+                held=None, scale: float | None = None, causal: bool = True, window: int = 0,
+                sinks: int = 0, stream=None) -> None:
+    """Adds to weight (fp32 [pages, heads, page_tokens], the cache's slots) the
+    attention weight that each cached token gets from the queries q [T, Hq, dim],
+    with lse [T, Hq] of q4_kv_attention over the same queries.  held: int32 [B],
+    tokens whose weight is kept; the others begin at 0 (default: the new ones)."""
+    T, Hq, dim = q.shape
+    B = kv_len.shape[0]
+    qp, qs = _rows(q, Hq, cache.dim)
+    q_dtype = _FLOAT_CODES.get(q.dtype)
+    if q_dtype is None:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    pages, cols = _table(page_table, B)
+    rc = lib().q4_kv_weigh(
+        _weights(weight, cache), qp, q_dtype, qs, Hq, _floats("lse", lse, T * Hq), cache.ref, pages, cols,
+        _index("kv_len", kv_len, B), _index("cu_q", cu_q, B + 1),
+        None if held is None else _index("held", held, B), B, T, max_q, max_kv,
+        dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, sinks, _raw_stream(stream, q))
+    if rc:
+        raise Q4Error("q4_kv_weigh", rc)
+
+
+def _weights(weight, cache):
+    """Data pointer of a fp32 tensor of the cache's slots, or None."""
+    return _floats("weight", weight, cache.pages * cache.heads * cache.page_tokens)
+
+
+def q4_kv_select(kept, count, weight, cache: KVCache, page_table, kv_len, budget, max_kv: int,
+                 sinks: int = 0, recent: int = 0, stream=None) -> None:
+    """The tokens that each head keeps of a budget (int32 [B]): the first `sinks`,
+    the last `recent` and the heaviest others, ascending, into kept (int32
+    [B, heads, width]); how many, into count (int32 [B])."""
+    B, heads, width = kept.shape
+    if heads != cache.heads:
+        raise ValueError(f"kept has {heads} heads, not {cache.heads}")
+    pages, cols = _table(page_table, B)
+    rc = lib().q4_kv_select(
+        _index("kept", kept, B * heads * width), width, _index("count", count, B), _weights(weight, cache),
+        cache.ref, pages, cols, _index("kv_len", kv_len, B), _index("budget", budget, B), B, max_kv, sinks,
+        recent, _raw_stream(stream, kept))
+    if rc:
+        raise Q4Error("q4_kv_select", rc)
+
+
+def q4_kv_compact(cache: KVCache, page_table, kv_len, kept, count, weight=None, first=None, to_table=None,
+                  stream=None) -> None:
+    """Moves the tokens kept (int32 [B, 1 or heads, width], ascending; count [B] of
+    them) to places first[b] .. (default 0) of their sequences, with their weights,
+    within page_table or into the pages of to_table.  Each sequence then has
+    first + count tokens: kv_len is the caller's to set."""
+    B, heads, width = kept.shape
+    if heads not in (1, cache.heads):
+        raise ValueError(f"kept has {heads} heads, neither 1 nor {cache.heads}")
+    pages, cols = _table(page_table, B)
+    to, to_cols = (None, 0) if to_table is None else _table(to_table, B)
+    rc = lib().q4_kv_compact(
+        cache.ref, _weights(weight, cache), pages, cols, to, to_cols, _index("kv_len", kv_len, B),
+        None if first is None else _index("first", first, B), _index("kept", kept, B * heads * width), heads,
+        width, _index("count", count, B), B, _raw_stream(stream, kept))
+    if rc:
+        raise Q4Error("q4_kv_compact", rc)
+
+
+def _logit_rows(name, t):
+    """Data pointer, dtype code and row stride of a [T, V] view whose rows are dense."""
+    n, width = t.shape
+    s0, s1 = t.stride()
+    dtype = _FLOAT_CODES.get(t.dtype)
+    if dtype is None or not t.is_cuda or (s1 != 1 and width > 1):
+        raise ValueError(f"{name} is a [T, V] fp32 or bf16 CUDA tensor with dense rows")
+    return t.data_ptr(), dtype, s0 if n > 1 else width
+
+
+def q4_adjust_logits(out, logits, history=None, history_len=None, prompt_len=None, repetition=None,
+                     presence=None, frequency=None, bias_index=None, bias=None, request=None, mask=None,
+                     mask_row=None, stream=None) -> None:
+    """Penalties for the tokens of a history (int32 [requests, width]; history_len
+    of them, the first prompt_len a prompt), biases (bias_index int32 and bias fp32
+    [requests, n]) and a grammar's bits (mask int32 [masks, words]) on logits
+    [T, V], into out (which may be logits).  request, mask_row: int32 [T], each
+    row's row of these (include/q4.h)."""
+    T, V = logits.shape
+    op, out_dtype, out_stride = _logit_rows("out", out)
+    lp, dtype, stride = _logit_rows("logits", logits)
+    if out.shape != logits.shape:
+        raise ValueError("out has the shape of logits")
+    hp, hw, bp, bw, requests, mp, masks = None, 0, None, 0, 0, None, 0
+    if history is not None:
+        hp, hw = _words("history", history)
+        requests = history.shape[0]
+    if bias_index is not None:
+        bp, bw = _words("bias_index", bias_index)
+        if history is not None and bias_index.shape[0] != requests:
+            raise ValueError("history and bias_index have the same rows")
+        requests = bias_index.shape[0]
+    if mask is not None:
+        mp, words = _words("mask", mask)
+        masks = mask.shape[0]
+        if words != (V + 31) // 32:
+            raise ValueError(f"mask has {words} words a row, not {(V + 31) // 32}")
+    rc = lib().q4_adjust_logits(
+        op, out_dtype, out_stride, lp, dtype, stride, T, V,
+        None if request is None else _index("request", request, T), requests, hp, hw,
+        None if history_len is None else _index("history_len", history_len, T),
+        None if prompt_len is None else _index("prompt_len", prompt_len, T),
+        _floats("repetition", repetition, T), _floats("frequency", frequency, T),
+        _floats("presence", presence, T), bp,
+        None if bias is None else _floats("bias", bias, requests * bw), bw, mp, masks,
+        None if mask_row is None else _index("mask_row", mask_row, T), _raw_stream(stream, logits))
+    if rc:
+        raise Q4Error("q4_adjust_logits", rc)
 
 
 def q4_sample(tokens, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, probs=None,
