@@ -8,7 +8,8 @@
 // while it looks through the row's history and biases for tokens of the slice
 // and notes them in shared memory, a word a token: the last bias entry, whether
 // the prompt has it, how often the answer has it.  Notes are whole numbers, so
-// their order does not matter.
+// their order does not matter.  Most groups of eight logits have no note: they
+// are stored as they came, or as -inf.
 #include <algorithm>
 
 #include "q4_kernels.h"
@@ -18,26 +19,26 @@ namespace q4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostSlice = 16384;         // logits of a CTA
+constexpr int kUnit = 8;                  // logits that a thread has side by side
+constexpr int kUnits = 4;                 // of them
+constexpr int kMostSlice = kThreads * kUnit * kUnits;
 constexpr unsigned kSeen = 1u << 19;      // a note: bits 0-18 how often, bit 19 in the prompt, bits 20-31 bias entry + 1
 constexpr unsigned kTimes = kSeen - 1;
 constexpr int kBiasShift = 20;
 
 struct Row {
-  bool notes, penalties;
+  bool penalties;
   const float* bias;                      // of the row, or null
-  const uint32_t* mask;                   // or null
   float repetition, frequency, presence;
 };
 
-__device__ __forceinline__ float adjust(float x, const Row& r, unsigned note, int v) {
+__device__ __forceinline__ float adjust(float x, const Row& r, unsigned note) {
   if (r.penalties) {
     const unsigned n = note & kTimes;
     if (note & (kSeen | kTimes)) x = x > 0.f ? __fdiv_rn(x, r.repetition) : __fmul_rn(x, r.repetition);
     if (n) x = __fsub_rn(__fsub_rn(x, __fmul_rn(r.frequency, static_cast<float>(n))), r.presence);
   }
   if (note >> kBiasShift) x = __fadd_rn(x, __ldg(r.bias + ((note >> kBiasShift) - 1)));
-  if (r.mask && !(__ldg(r.mask + (v >> 5)) >> (v & 31) & 1u)) x = -INFINITY;
   return x;
 }
 
@@ -53,73 +54,166 @@ __device__ __forceinline__ void store1(void* p, long long i, float x) {
     static_cast<float*>(p)[i] = x;
 }
 
-// IN, OUT: bf16 or fp32.  slice: logits of a CTA.
+// Eight logits side by side, as they lie in memory.
+template <bool BF16>
+struct Unit {
+  uint4 w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, long long i) {
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 1 : 2); ++k) w[k] = at[k];
+  }
+  __device__ __forceinline__ void store(void* p, long long i) const {
+    uint4* at = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p) + i * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 1 : 2); ++k) at[k] = w[k];
+  }
+  __device__ __forceinline__ void get(float (&x)[kUnit]) const {
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+    for (int k = 0; k < kUnit; ++k)
+      x[k] = __uint_as_float(BF16 ? (k & 1 ? v[k >> 1] & 0xffff0000u : v[k >> 1] << 16) : v[k]);
+  }
+  __device__ __forceinline__ void set(const float (&x)[kUnit]) {
+    uint32_t* v = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+    for (int k = 0; k < kUnit; k += BF16 ? 2 : 1) {
+      if (BF16) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(x[k], x[k + 1]);
+        v[k >> 1] = *reinterpret_cast<const uint32_t*>(&y);
+      } else {
+        v[k] = __float_as_uint(x[k]);
+      }
+    }
+  }
+};
+
+// IN, OUT: bf16 or fp32.  slice: logits of a CTA, a multiple of eight.
 template <bool IN, bool OUT>
 __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_constant__ AdjustParams p, int slice) {
-  extern __shared__ unsigned s_note[];    // [slice]
+  extern __shared__ __align__(16) unsigned s_mem[];     // [slice + kUnit]
   const int tid = threadIdx.x, t = blockIdx.y;
   const int v0 = blockIdx.x * slice, n = min(slice, p.V - v0);
   pdl_launch_dependents();
   pdl_wait();
   const long long in = t * p.stride + v0, to = t * p.out_stride + v0;
-  Row r = {};
+  // eights that begin at 16 bytes in both rows, if there are such: from logit `lead` of the slice on
+  constexpr int kInEach = IN ? 8 : 4, kOutEach = OUT ? 8 : 4;   // logits of 16 bytes
+  const int in_at = static_cast<int>(((reinterpret_cast<uintptr_t>(p.logits) >> (IN ? 1 : 2)) + in) & (kInEach - 1));
+  const int out_at = static_cast<int>(((reinterpret_cast<uintptr_t>(p.out) >> (OUT ? 1 : 2)) + to) & (kOutEach - 1));
+  const int lead = IN ? (kInEach - in_at) & (kInEach - 1) : (kOutEach - out_at) & (kOutEach - 1);
+  const bool wide = ((in_at + lead) & (kInEach - 1)) == 0 && ((out_at + lead) & (kOutEach - 1)) == 0;
+  const int units = wide && n > lead ? (n - lead) / kUnit : 0;
+  unsigned* s_note = s_mem + kUnit - lead;              // of the slice's logits: an eight's begin at 32 bytes
+  Unit<IN> x[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+    if (i * kThreads + tid < units) x[i].load(p.logits, in + lead + (i * kThreads + tid) * kUnit);
   const int req = p.request ? __ldg(p.request + t) : t;
   const bool known = req >= 0 && req < p.requests;
-  if (p.request && req >= p.requests && (p.history || p.bias_index) && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
+  const uint32_t* mask = nullptr;
   if (p.mask) {
     const int row = p.mask_row ? __ldg(p.mask_row + t) : t;
-    if (row >= p.masks) {
-      if (blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
-    } else if (row >= 0) {
-      r.mask = reinterpret_cast<const uint32_t*>(p.mask) + row * ((p.V + 31LL) / 32);
-    }
+    if (row >= 0 && row < p.masks) mask = reinterpret_cast<const uint32_t*>(p.mask) + row * ((p.V + 31LL) / 32);
+    if (row >= p.masks && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
   }
+  if (p.request && req >= p.requests && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
+  Row r;
   r.penalties = p.history && known;
   r.repetition = p.repetition ? __ldg(p.repetition + t) : 1.f;
   r.frequency = p.frequency ? __ldg(p.frequency + t) : 0.f;
   r.presence = p.presence ? __ldg(p.presence + t) : 0.f;
-  const bool biased = p.bias_index && known;
-  r.bias = biased ? p.bias + static_cast<long long>(req) * p.bias_width : nullptr;
-  r.notes = r.penalties || biased;
-  if (r.notes) {
-    for (int i = tid; i < n; i += kThreads) s_note[i] = 0;
+  r.bias = p.bias_index && known ? p.bias + static_cast<long long>(req) * p.bias_width : nullptr;
+  const bool notes = r.penalties || r.bias;
+  if (notes) {
+    for (int i = tid; i < (slice + kUnit) / 4; i += kThreads) reinterpret_cast<uint4*>(s_mem)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    if (biased) {
+    if (r.bias) {
       const int32_t* index = p.bias_index + static_cast<long long>(req) * p.bias_width;
       for (int i = tid; i < p.bias_width; i += kThreads) {
         const int at = __ldg(index + i) - v0;
         if (at >= 0 && at < n) atomicMax(s_note + at, static_cast<unsigned>(i + 1) << kBiasShift);
       }
-      __syncthreads();
+      if (r.penalties) __syncthreads();
     }
     if (r.penalties) {
       const int32_t* history = p.history + static_cast<long long>(req) * p.history_width;
       const int len = min(__ldg(p.history_len + t), p.history_width), prompt = p.prompt_len ? __ldg(p.prompt_len + t) : 0;
-      for (int i = tid; i < len; i += kThreads) {
-        const int at = __ldg(history + i) - v0;
-        if (at >= 0 && at < n) {
-          if (i < prompt)
-            atomicOr(s_note + at, kSeen);
-          else
-            atomicAdd(s_note + at, 1u);
-        }
+      auto note = [&](int token, int i) {
+        const int at = token - v0;
+        if (static_cast<unsigned>(at) >= static_cast<unsigned>(n)) return;
+        if (i < prompt)
+          atomicOr(s_note + at, kSeen);
+        else
+          atomicAdd(s_note + at, 1u);
+      };
+      // four tokens at a time from where the list begins at 16 bytes, two such a step
+      const int skip = min(max(len, 0), static_cast<int>((16 - (reinterpret_cast<uintptr_t>(history) & 15)) & 15) / 4);
+      const int fours = (max(len, 0) - skip) / 4;
+      if (tid < skip) note(__ldg(history + tid), tid);
+      const int rest = skip + 4 * fours + tid;
+      if (rest < len) note(__ldg(history + rest), rest);   // three at most
+#pragma unroll 2
+      for (int i = tid; i < fours; i += kThreads) {
+        const int4 four = __ldg(reinterpret_cast<const int4*>(history + skip) + i);
+        const int at = skip + 4 * i;
+        note(four.x, at), note(four.y, at + 1), note(four.z, at + 2), note(four.w, at + 3);
       }
     }
     __syncthreads();
   }
-  for (int i = tid; i < n; i += kThreads)
-    store1<OUT>(p.out, to + i, adjust(load1<IN>(p.logits, in + i), r, r.notes ? s_note[i] : 0u, v0 + i));
+  auto bits_from = [&](int v) {             // the mask's bits of tokens v .. v + 7, and more above them
+    const int w = v >> 5, s = v & 31;
+    const uint32_t lo = __ldg(mask + w), hi = s > 24 && v + 32 - s < p.V ? __ldg(mask + w + 1) : 0u;
+    return __funnelshift_r(lo, hi, s);
+  };
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int u = i * kThreads + tid;
+    if (u >= units) break;
+    const int at = lead + u * kUnit;
+    const uint32_t allowed = mask ? bits_from(v0 + at) & 0xffu : 0xffu;
+    unsigned any = 0;
+    if (notes) {                            // four lanes read an eight's other half first: no bank twice
+      const uint4* four = reinterpret_cast<const uint4*>(s_note + at);
+      const uint4 a = four[tid >> 2 & 1], b = four[~tid >> 2 & 1];
+      any = a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w;
+    }
+    if (any == 0 && allowed == 0xffu && IN == OUT) {
+      reinterpret_cast<Unit<OUT>&>(x[i]).store(p.out, to + at);
+      continue;
+    }
+    float y[kUnit];
+    x[i].get(y);
+    if (any) {
+#pragma unroll
+      for (int k = 0; k < kUnit; ++k)
+        if (s_note[at + k]) y[k] = adjust(y[k], r, s_note[at + k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnit; ++k)
+      if (!(allowed >> k & 1u)) y[k] = -INFINITY;
+    Unit<OUT> z;
+    z.set(y);
+    z.store(p.out, to + at);
+  }
+  // what is outside the eights
+  const int head = units > 0 ? lead : n;
+  for (int i = tid; i < n - units * kUnit; i += kThreads) {
+    const int at = i < head ? i : i + units * kUnit;
+    float y = load1<IN>(p.logits, in + at);
+    if (notes && s_note[at]) y = adjust(y, r, s_note[at]);
+    if (mask && !(bits_from(v0 + at) & 1u)) y = -INFINITY;
+    store1<OUT>(p.out, to + at, y);
+  }
 }
 
 template <bool IN, bool OUT>
 cudaError_t launch(const AdjustParams& p, int slice, cudaStream_t st) {
-  static std::atomic<unsigned long long> allowed;
-  cudaError_t e = allow_smem(q4_adjust_kernel<IN, OUT>, kMostSlice * 4, allowed);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.V + slice - 1) / slice), static_cast<unsigned>(p.T));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(slice) * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(slice + kUnit) * 4;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
