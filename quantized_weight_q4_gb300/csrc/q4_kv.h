@@ -116,7 +116,11 @@ struct KvWeighCall {
   long long window, sinks;
   unsigned* err;
 };
-cudaError_t launch_kv_weigh(const KvWeighCall& a, int sms, cudaStream_t st);
+// max_q: new tokens of a sequence at most, as far as the caller knows.
+cudaError_t launch_kv_weigh(const KvWeighCall& a, long long max_q, int sms, cudaStream_t st);
+// On the tensor cores, bf16 queries: sequences with more than split_rows query rows of a head (0: all of them).
+cudaError_t launch_kv_weigh_prompt(const KvWeighCall& a, int split_rows, int sms, cudaStream_t st);
+int kv_weigh_prompt_group();
 
 // The tokens of a sequence and head that a budget leaves.
 struct KvSelectParams {

@@ -40,6 +40,7 @@ constexpr int kChunkTiles = 8;            // of them in shared memory at a time
 constexpr int kChunkRows = kTileRows * kChunkTiles;
 constexpr int kSegCost = 2 * kWarps;      // what starting a (sequence, head) costs, in blocks of one tile of rows
 constexpr long long kMostCost = 4096;     // of a block, so that no line, whatever the lengths, is too long for 64 bits
+constexpr int kSplitRows = 64;            // query rows of a head up to which a sequence of bf16 queries takes this form
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -77,7 +78,8 @@ struct Seq {
   long long rows, cost;    // query rows of a head; what a block of tokens costs, in tiles of rows
 };
 
-__device__ __forceinline__ Seq sequence(const KvWeighCall& a, int group, int b) {
+// max_rows: sequences with more query rows are left to the tensor cores.
+__device__ __forceinline__ Seq sequence(const KvWeighCall& a, int group, int max_rows, int b) {
   Seq s;
   s.c0 = a.b.cu[b];
   s.nq = max(0, a.b.cu[b + 1] - s.c0);
@@ -95,6 +97,7 @@ __device__ __forceinline__ Seq sequence(const KvWeighCall& a, int group, int b) 
   const int sinks = a.window > 0 && s.nq > 0
                         ? static_cast<int>(min(static_cast<long long>(lo), (a.sinks + kKvBlock - 1) / kKvBlock)) : 0;
   s.blocks = {sinks, lo, hi};
+  if (s.rows > max_rows) s.blocks = {0, 0, 0};
   return s;
 }
 
@@ -105,7 +108,8 @@ constexpr size_t smem_bytes(int B) {
 
 // SPLIT: queries in two fp16 terms.
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __grid_constant__ KvWeighCall a, int group) {
+__global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __grid_constant__ KvWeighCall a, int group,
+                                                                        int max_rows) {
   constexpr int KT = D / 16, kParts = D / 64;   // k steps; 16-byte parts of a key that a lane has
   constexpr int kWords = SPLIT ? 4 : 2;         // of a lane's operand of a step and tile of rows
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b < B) {
-        const Seq s = sequence(a, group, b);
+        const Seq s = sequence(a, group, max_rows, b);
         const int n = s.blocks.count();
         sum += n > 0 ? static_cast<long long>(n + kSegCost) * s.cost * a.c.heads : 0;
         s_cum[b + 1] = sum;
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
       const int mid = (lo + hi) >> 1;
       if (s_cum[mid] <= u) b = mid, lo = mid + 1; else hi = mid - 1;
     }
-    const Seq s = sequence(a, group, b);
+    const Seq s = sequence(a, group, max_rows, b);
     const int nb = s.blocks.count();
     const long long pair_cost = static_cast<long long>(nb + kSegCost) * s.cost;
     const int h = static_cast<int>((u - s_cum[b]) / pair_cost);
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
 }
 
 template <int D, bool SPLIT>
-cudaError_t launch(const KvWeighCall& a, int group, int sms, cudaStream_t st) {
+cudaError_t launch(const KvWeighCall& a, int group, int max_rows, int sms, cudaStream_t st) {
   static std::atomic<unsigned long long> allowed;
   cudaError_t e = allow_smem(q4_kv_weigh_kernel<D, SPLIT>, smem_bytes<D, SPLIT>(kKvMaxSeqs), allowed);
   if (e != cudaSuccess) return e;
@@ -344,15 +348,23 @@ cudaError_t launch(const KvWeighCall& a, int group, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q4_kv_weigh_kernel<D, SPLIT>, a, group);
+  return cudaLaunchKernelEx(&cfg, q4_kv_weigh_kernel<D, SPLIT>, a, group, max_rows);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_weigh(const KvWeighCall& a, int sms, cudaStream_t st) {
+cudaError_t launch_kv_weigh(const KvWeighCall& a, long long max_q, int sms, cudaStream_t st) {
   const int group = a.Hq / a.c.heads;
-  if (a.c.dim == 128) return a.q_bf16 ? launch<128, false>(a, group, sms, st) : launch<128, true>(a, group, sms, st);
-  return a.q_bf16 ? launch<64, false>(a, group, sms, st) : launch<64, true>(a, group, sms, st);
+  const long long most = std::min<long long>(max_q, a.b.T) * group;
+  const bool prompt = a.q_bf16 && most > kSplitRows && group <= kv_weigh_prompt_group();
+  if (prompt && a.b.B == 1) return launch_kv_weigh_prompt(a, 0, sms, st);
+  const int max_rows = prompt ? kSplitRows : 0x7fffffff;
+  cudaError_t e;
+  if (a.c.dim == 128)
+    e = a.q_bf16 ? launch<128, false>(a, group, max_rows, sms, st) : launch<128, true>(a, group, max_rows, sms, st);
+  else
+    e = a.q_bf16 ? launch<64, false>(a, group, max_rows, sms, st) : launch<64, true>(a, group, max_rows, sms, st);
+  return e == cudaSuccess && prompt ? launch_kv_weigh_prompt(a, kSplitRows, sms, st) : e;
 }
 
 }  // namespace q4

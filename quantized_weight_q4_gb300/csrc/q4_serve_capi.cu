@@ -297,7 +297,7 @@ int q4_kv_weigh(float* weight, const void* q, int q_dtype, int64_t q_stride, int
   a.b = {page_table, table_stride, kv_len, cu_q, static_cast<int>(B), static_cast<int>(T)};
   a.weight = weight, a.q = q, a.q_stride = q_stride, a.Hq = static_cast<int>(Hq), a.q_bf16 = q_dtype == Q4_BF16;
   a.lse = lse, a.held = held, a.scale = scale, a.causal = causal, a.window = window, a.sinks = sinks;
-  return status_of(q4::launch_kv_weigh(a, sms, static_cast<cudaStream_t>(stream)));
+  return status_of(q4::launch_kv_weigh(a, max_q, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int q4_kv_select(int32_t* kept, int64_t width, int32_t* count, const float* weight, const q4_kv_cache* cache,

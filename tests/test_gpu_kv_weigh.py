@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 
 def check(new, ctx, Hq, heads, D, page, kind, seed, window=0, sinks=0, causal=True, scale=None, held=None, q_gain=1.5,
-          spread=1.0, break_rows=(), max_q=None):
+          spread=1.0, break_rows=(), max_q=None, pad=2):
     lens = [a + b for a, b in zip(new, ctx)]
     c = Cache(lens, heads, D, page, seed, spread=spread)
     g = rng(seed, 5)
@@ -32,10 +32,10 @@ def check(new, ctx, Hq, heads, D, page, kind, seed, window=0, sinks=0, causal=Tr
     cache, table = c.to_device()
     before = (g.random((c.pages, heads, page)) * 3).astype(f32)
     weight = dev(before)
-    wide = torch.full((T + 2, Hq * D + 16), float("nan"), dtype=td, device=device())
-    wide[:T, 8:8 + Hq * D] = dev(sent.reshape(T, -1), td)
+    wide = torch.full((T + pad, Hq * D + 16), float("nan"), dtype=td, device=device())
+    wide[:T, 8:8 + Hq * D] = dev(sent.reshape(T, Hq * D), td)
     qd = wide[:, 8:8 + Hq * D].unflatten(1, (Hq, D))
-    lse_d = torch.cat([dev(lse), torch.zeros(2, Hq, device=device())])
+    lse_d = torch.cat([dev(lse), torch.zeros(pad, Hq, device=device())])
     had = [max(0, t - n) for n, t in zip(new, lens)] if held is None else [max(0, min(h, t)) for h, t in zip(held, lens)]
     q4.q4_kv_weigh(weight, qd, lse_d, cache, table, i32(lens), i32(starts(new)), max_q or max(max(new), 1), max(max(lens), 1),
                    held=None if held is None else i32(held), scale=scale, causal=causal, window=window, sinks=sinks)
@@ -123,6 +123,29 @@ def test_sharp_scores_and_uneven_scales(kind):
 def test_rows_without_a_sum_add_nothing(kind):
     check([4, 30], [50, 20], 4, 2, 64, 16, kind, 6, break_rows=[(1, -np.inf), (3, np.nan), (10, np.inf)])
     check([150], [20], 8, 1, 128, 16, kind, 7, break_rows=[(0, -np.inf), (77, np.nan), (149, np.inf)])
+
+
+@pytest.mark.parametrize("Hq,heads", [(3, 1), (14, 2), (9, 1), (16, 1), (64, 1), (5, 5), (130, 1), (300, 1)])
+def test_prompts_of_any_group(Hq, heads):
+    """Tiles of queries that whole tokens do not fill, and groups as large as a tile or larger."""
+    check([90, 1, 70], [300, 40, 0], Hq, heads, 64, 32, "bf16", Hq)
+    check([130], [7], Hq, heads, 128, 64, "bf16", Hq + 1, window=50, sinks=3, held=[0])
+
+
+def test_more_prompts_than_clusters():
+    """Several turns of work for each cluster, of unlike sizes, some without a query that sees the tokens."""
+    new = [70 + 13 * i for i in range(24)]
+    check(new, [(97 * i) % 700 for i in range(24)], 8, 4, 64, 64, "bf16", 81)
+    check(new, [(97 * i) % 700 for i in range(24)], 8, 4, 64, 64, "bf16", 82, window=30, held=[(61 * i) % 900 for i in range(24)])
+
+
+def test_prompts_of_other_masks_and_lengths():
+    check([200], [333], 8, 2, 128, 64, "bf16", 83, causal=False)
+    check([300], [-40], 8, 2, 64, 64, "bf16", 84)        # fewer tokens than queries
+    check([150, 100], [1000, 600], 8, 1, 64, 16, "bf16", 85, window=40, sinks=300, held=[1100, 0])
+    check([0], [300], 8, 1, 64, 16, "bf16", 86, held=[100], max_q=500, pad=200)   # no query at all
+    check([1], [300], 8, 1, 64, 16, "bf16", 87, max_q=500, pad=200)
+    check([2, 0, 1], [300, 50, 700], 8, 1, 64, 16, "bf16", 88, max_q=500, held=[3, 4, 5], pad=200)
 
 
 def test_weights_of_a_prompt_add_up():
