@@ -21,6 +21,7 @@
 //   first, so that their sums of work are nearly alike.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "q4_kernels.h"
 #include "q4_kv_device.cuh"
@@ -212,37 +213,40 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_weigh_prompt_kernel(const _
         }
         const uint32_t nl = smem_u32(s_lse + st * kCols);
         f32x2 part[2] = {0ull, 0ull};
-        uint32_t s[2][32];
-        tmem_ld32_async(t_d, s[0]);
-        tmem_wait_ld();
+        auto add_up = [&](auto on_edge) {
+          uint32_t s[2][32];
+          tmem_ld32_async(t_d, s[0]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < kCols / 32; ++x) {
-          const uint32_t* v = s[x & 1];
-          if (x + 1 < kCols / 32) tmem_ld32_async(t_d + 32 * (x + 1), s[(x + 1) & 1]);
+          for (int x = 0; x < kCols / 32; ++x) {
+            const uint32_t* v = s[x & 1];
+            if (x + 1 < kCols / 32) tmem_ld32_async(t_d + 32 * (x + 1), s[(x + 1) & 1]);
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            f32x2 l[2];
-            lds_pairs(nl + (32 * x + c) * 4, l[0], l[1]);
+            for (int c = 0; c < 32; c += 4) {
+              f32x2 l[2];
+              lds_pairs(nl + (32 * x + c) * 4, l[0], l[1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float y, z;
-              unpack2(fma2(pack2(__uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1])), f2, l[k]), y, z);
-              if (edge) {         // a row that adds nothing may hold anything
-                float ly, lz;
-                unpack2(l[k], ly, lz);
-                const int col = 32 * x + c + 2 * k;
-                if (col < c_lo || col >= c_hi || ly == -INFINITY) y = -INFINITY;
-                if (col + 1 < c_lo || col + 1 >= c_hi || lz == -INFINITY) z = -INFINITY;
+              for (int k = 0; k < 2; ++k) {
+                float y, z;
+                unpack2(fma2(pack2(__uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1])), f2, l[k]), y, z);
+                if (decltype(on_edge)::value) {   // a row that adds nothing may hold anything
+                  float ly, lz;
+                  unpack2(l[k], ly, lz);
+                  const int col = 32 * x + c + 2 * k;
+                  if (col < c_lo || col >= c_hi || ly == -INFINITY) y = -INFINITY;
+                  if (col + 1 < c_lo || col + 1 >= c_hi || lz == -INFINITY) z = -INFINITY;
+                }
+                part[k] = add2(part[k], pack2(ex2(y), ex2(z)));
               }
-              part[k] = add2(part[k], pack2(ex2(y), ex2(z)));
+            }
+            if (x + 1 < kCols / 32) tmem_wait_ld();
+            if (x + 2 == kCols / 32) {   // all columns are in registers
+              tc_fence_before();
+              mbar_arrive(&d_empty[g]);
             }
           }
-          if (x + 1 < kCols / 32) tmem_wait_ld();
-          if (x + 2 == kCols / 32) {   // all columns are in registers
-            tc_fence_before();
-            mbar_arrive(&d_empty[g]);
-          }
-        }
+        };
+        if (edge) add_up(std::true_type{}); else add_up(std::false_type{});
         mbar_arrive(&l_empty[st]);
         float y, z;
         unpack2(add2(part[0], part[1]), y, z);
@@ -286,23 +290,33 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_weigh_prompt_kernel(const _
         }
       }
     } else if (warp == kLseWarp) {
+      // a lane's columns, and a tile's values, on their way while the tile before is in use
+      float v[kCols / 32];
+      auto load = [&](int i) {
+        const int j0 = (t_lo + rank + 2 * i) * p.tokens;
+#pragma unroll
+        for (int k = 0; k < kCols / 32; ++k) {
+          const int c = lane + 32 * k, j = j0 + c / p.group;
+          v[k] = INFINITY;
+          if (i < n && c < p.tokens * p.group && j < nq && c0 + j < a.b.T)
+            v[k] = __ldg(a.lse + (static_cast<long long>(c0) + j) * a.Hq + h * p.group + c % p.group);
+        }
+      };
+      load(0);
       for (int i = 0; i < n; ++i) {
-        const int it = taken + i, st = it % kStages, j0 = (t_lo + rank + 2 * i) * p.tokens;
+        const int it = taken + i, st = it % kStages;
         if (it >= kStages && !__all_sync(0xffffffffu, gwait(&l_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err))) break;
         bool odd = false;
-        for (int c = lane; c < kCols; c += 32) {
-          const int j = j0 + c / p.group;
-          float l = -INFINITY;
-          if (c < p.tokens * p.group && j < nq && c0 + j < a.b.T) {
-            const float v = __ldg(a.lse + (static_cast<long long>(c0) + j) * a.Hq + h * p.group + c % p.group);
-            if (fabsf(v) <= FLT_MAX) l = -v * kLog2e;   // a row that sees nothing, or is no number, adds nothing
-          }
-          odd |= l == -INFINITY;
-          s_lse[st * kCols + c] = l;
+#pragma unroll
+        for (int k = 0; k < kCols / 32; ++k) {
+          const bool adds = fabsf(v[k]) <= FLT_MAX;   // a row that sees nothing, or is no number, adds nothing
+          odd |= !adds;
+          s_lse[st * kCols + lane + 32 * k] = adds ? -v[k] * kLog2e : -INFINITY;
         }
         odd = __any_sync(0xffffffffu, odd);
         if (lane == 0) s_odd[st] = odd;
         mbar_arrive(&l_full[st]);
+        load(i + 1);
       }
     }
     __syncwarp();
