@@ -8,8 +8,10 @@
 // while it looks through the row's history and biases for tokens of the slice
 // and notes them in shared memory, a word a token: the last bias entry, whether
 // the prompt has it, how often the answer has it.  Notes are whole numbers, so
-// their order does not matter.  Most groups of eight logits have no note: they
-// are stored as they came, or as -inf.
+// their order does not matter; who makes a token's first note puts the token on
+// a list.  The slice is stored as it came, with the mask's -inf, and then the
+// listed tokens again, a thread each: beside their neighbours they would hold
+// up whole warps, one after another.
 #include <algorithm>
 
 #include "q4_kernels.h"
@@ -25,22 +27,6 @@ constexpr int kMostSlice = kThreads * kUnit * kUnits;
 constexpr unsigned kSeen = 1u << 19;      // a note: bits 0-18 how often, bit 19 in the prompt, bits 20-31 bias entry + 1
 constexpr unsigned kTimes = kSeen - 1;
 constexpr int kBiasShift = 20;
-
-struct Row {
-  bool penalties;
-  const float* bias;                      // of the row, or null
-  float repetition, frequency, presence;
-};
-
-__device__ __forceinline__ float adjust(float x, const Row& r, unsigned note) {
-  if (r.penalties) {
-    const unsigned n = note & kTimes;
-    if (note & (kSeen | kTimes)) x = x > 0.f ? __fdiv_rn(x, r.repetition) : __fmul_rn(x, r.repetition);
-    if (n) x = __fsub_rn(__fsub_rn(x, __fmul_rn(r.frequency, static_cast<float>(n))), r.presence);
-  }
-  if (note >> kBiasShift) x = __fadd_rn(x, __ldg(r.bias + ((note >> kBiasShift) - 1)));
-  return x;
-}
 
 template <bool BF16>
 __device__ __forceinline__ float load1(const void* p, long long i) {
@@ -74,6 +60,19 @@ struct Unit {
     for (int k = 0; k < kUnit; ++k)
       x[k] = __uint_as_float(BF16 ? (k & 1 ? v[k >> 1] & 0xffff0000u : v[k >> 1] << 16) : v[k]);
   }
+  // -inf where `allowed` has a 0.
+  __device__ __forceinline__ void mask(uint32_t allowed) {
+    uint32_t* v = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 4 : 8); ++k) {
+      if (BF16) {
+        const uint32_t two = allowed >> 2 * k, keep = (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u);
+        v[k] = (v[k] & keep) | (0xff80ff80u & ~keep);
+      } else if (!(allowed >> k & 1u)) {
+        v[k] = 0xff800000u;
+      }
+    }
+  }
   __device__ __forceinline__ void set(const float (&x)[kUnit]) {
     uint32_t* v = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
@@ -91,7 +90,7 @@ struct Unit {
 // IN, OUT: bf16 or fp32.  slice: logits of a CTA, a multiple of eight.
 template <bool IN, bool OUT>
 __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_constant__ AdjustParams p, int slice) {
-  extern __shared__ __align__(16) unsigned s_mem[];     // [slice + kUnit]
+  extern __shared__ __align__(16) unsigned s_mem[];     // [slice] words, [slice] halves
   const int tid = threadIdx.x, t = blockIdx.y;
   const int v0 = blockIdx.x * slice, n = min(slice, p.V - v0);
   pdl_launch_dependents();
@@ -104,7 +103,9 @@ __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_consta
   const int lead = IN ? (kInEach - in_at) & (kInEach - 1) : (kOutEach - out_at) & (kOutEach - 1);
   const bool wide = ((in_at + lead) & (kInEach - 1)) == 0 && ((out_at + lead) & (kOutEach - 1)) == 0;
   const int units = wide && n > lead ? (n - lead) / kUnit : 0;
-  unsigned* s_note = s_mem + kUnit - lead;              // of the slice's logits: an eight's begin at 32 bytes
+  unsigned* s_note = s_mem;                             // of the slice's logits
+  uint16_t* s_list = reinterpret_cast<uint16_t*>(s_note + slice);   // those with a note
+  __shared__ int s_listed;
   Unit<IN> x[kUnits];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
@@ -118,34 +119,31 @@ __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_consta
     if (row >= p.masks && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
   }
   if (p.request && req >= p.requests && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
-  Row r;
-  r.penalties = p.history && known;
-  r.repetition = p.repetition ? __ldg(p.repetition + t) : 1.f;
-  r.frequency = p.frequency ? __ldg(p.frequency + t) : 0.f;
-  r.presence = p.presence ? __ldg(p.presence + t) : 0.f;
-  r.bias = p.bias_index && known ? p.bias + static_cast<long long>(req) * p.bias_width : nullptr;
-  const bool notes = r.penalties || r.bias;
+  const bool penalties = p.history && known;
+  const float* bias = p.bias_index && known ? p.bias + static_cast<long long>(req) * p.bias_width : nullptr;
+  const bool notes = penalties || bias;
   if (notes) {
-    for (int i = tid; i < (slice + kUnit) / 4; i += kThreads) reinterpret_cast<uint4*>(s_mem)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < slice / 4; i += kThreads) reinterpret_cast<uint4*>(s_note)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) s_listed = 0;
     __syncthreads();
-    if (r.bias) {
+    if (bias) {
       const int32_t* index = p.bias_index + static_cast<long long>(req) * p.bias_width;
       for (int i = tid; i < p.bias_width; i += kThreads) {
         const int at = __ldg(index + i) - v0;
-        if (at >= 0 && at < n) atomicMax(s_note + at, static_cast<unsigned>(i + 1) << kBiasShift);
+        if (static_cast<unsigned>(at) < static_cast<unsigned>(n) &&
+            atomicMax(s_note + at, static_cast<unsigned>(i + 1) << kBiasShift) == 0)
+          s_list[atomicAdd(&s_listed, 1)] = static_cast<uint16_t>(at);
       }
-      if (r.penalties) __syncthreads();
+      if (penalties) __syncthreads();
     }
-    if (r.penalties) {
+    if (penalties) {
       const int32_t* history = p.history + static_cast<long long>(req) * p.history_width;
       const int len = min(__ldg(p.history_len + t), p.history_width), prompt = p.prompt_len ? __ldg(p.prompt_len + t) : 0;
       auto note = [&](int token, int i) {
         const int at = token - v0;
         if (static_cast<unsigned>(at) >= static_cast<unsigned>(n)) return;
-        if (i < prompt)
-          atomicOr(s_note + at, kSeen);
-        else
-          atomicAdd(s_note + at, 1u);
+        const unsigned old = i < prompt ? atomicOr(s_note + at, kSeen) : atomicAdd(s_note + at, 1u);
+        if (old == 0) s_list[atomicAdd(&s_listed, 1)] = static_cast<uint16_t>(at);
       };
       // four tokens at a time from where the list begins at 16 bytes, two such a step
       const int skip = min(max(len, 0), static_cast<int>((16 - (reinterpret_cast<uintptr_t>(history) & 15)) & 15) / 4);
@@ -160,7 +158,6 @@ __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_consta
         note(four.x, at), note(four.y, at + 1), note(four.z, at + 2), note(four.w, at + 3);
       }
     }
-    __syncthreads();
   }
   auto bits_from = [&](int v) {             // the mask's bits of tokens v .. v + 7, and more above them
     const int w = v >> 5, s = v & 31;
@@ -173,47 +170,49 @@ __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_consta
     if (u >= units) break;
     const int at = lead + u * kUnit;
     const uint32_t allowed = mask ? bits_from(v0 + at) & 0xffu : 0xffu;
-    unsigned any = 0;
-    if (notes) {                            // four lanes read an eight's other half first: no bank twice
-      const uint4* four = reinterpret_cast<const uint4*>(s_note + at);
-      const uint4 a = four[tid >> 2 & 1], b = four[~tid >> 2 & 1];
-      any = a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w;
-    }
-    if (any == 0 && allowed == 0xffu && IN == OUT) {
-      reinterpret_cast<Unit<OUT>&>(x[i]).store(p.out, to + at);
-      continue;
-    }
-    float y[kUnit];
-    x[i].get(y);
-    if (any) {
-#pragma unroll
-      for (int k = 0; k < kUnit; ++k)
-        if (s_note[at + k]) y[k] = adjust(y[k], r, s_note[at + k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kUnit; ++k)
-      if (!(allowed >> k & 1u)) y[k] = -INFINITY;
     Unit<OUT> z;
-    z.set(y);
+    if (IN == OUT) {
+      z = reinterpret_cast<const Unit<OUT>&>(x[i]);
+    } else {
+      float y[kUnit];
+      x[i].get(y);
+      z.set(y);
+    }
+    if (allowed != 0xffu) z.mask(allowed);
     z.store(p.out, to + at);
   }
   // what is outside the eights
   const int head = units > 0 ? lead : n;
   for (int i = tid; i < n - units * kUnit; i += kThreads) {
     const int at = i < head ? i : i + units * kUnit;
+    store1<OUT>(p.out, to + at, mask && !(bits_from(v0 + at) & 1u) ? -INFINITY : load1<IN>(p.logits, in + at));
+  }
+  if (!notes) return;
+  // what has a note; within one tensor these logits are still there, or -inf by the mask as they will be
+  const float repetition = p.repetition ? __ldg(p.repetition + t) : 1.f, frequency = p.frequency ? __ldg(p.frequency + t) : 0.f;
+  const float presence = p.presence ? __ldg(p.presence + t) : 0.f;
+  __syncthreads();
+  for (int i = tid; i < s_listed; i += kThreads) {
+    const int at = s_list[i];
+    if (mask && !(bits_from(v0 + at) & 1u)) continue;
+    const unsigned note = s_note[at], times = note & kTimes;
     float y = load1<IN>(p.logits, in + at);
-    if (notes && s_note[at]) y = adjust(y, r, s_note[at]);
-    if (mask && !(bits_from(v0 + at) & 1u)) y = -INFINITY;
+    if (note & (kSeen | kTimes)) y = y > 0.f ? __fdiv_rn(y, repetition) : __fmul_rn(y, repetition);
+    if (times) y = __fsub_rn(__fsub_rn(y, __fmul_rn(frequency, static_cast<float>(times))), presence);
+    if (note >> kBiasShift) y = __fadd_rn(y, __ldg(bias + ((note >> kBiasShift) - 1)));
     store1<OUT>(p.out, to + at, y);
   }
 }
 
 template <bool IN, bool OUT>
 cudaError_t launch(const AdjustParams& p, int slice, cudaStream_t st) {
+  static std::atomic<unsigned long long> allowed;
+  const cudaError_t e = allow_smem(q4_adjust_kernel<IN, OUT>, kMostSlice * 6, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.V + slice - 1) / slice), static_cast<unsigned>(p.T));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(slice + kUnit) * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(slice) * 6;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

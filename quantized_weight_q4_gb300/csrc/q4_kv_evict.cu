@@ -189,33 +189,46 @@ __global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // Moving
 // ---------------------------------------------------------------------------
-// A CTA takes kMoveTokens consecutive places of a head at a time, of its keys or
-// of its values.  Within one page table a place may be the source of an earlier
-// one (never of a later one: kept[i] >= first + i), so there a CTA takes all the
-// places of a (sequence, head), in order, and writes some after all of their
-// sources are in registers; into other pages every run of places has a CTA.
+// A CTA takes kMoveTokens consecutive places of a head at a time, keys and
+// values: a thread a place finds its source and factor, then all threads move
+// 16 codes at a time.  Within one page table a place may be the source of an
+// earlier one (never of a later one: kept[i] >= first + i), so there a CTA takes
+// all the places of a (sequence, head), in order, and writes some after all of
+// their sources are in registers; into other pages every run of places has a
+// CTA.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTokens = 128;
 
-// 16 codes times `ratio`, each rounded: rint(code * ratio), one fp32 operation a step.
-__device__ __forceinline__ uint32_t scale4(uint32_t w, float ratio) {
-  uint32_t y = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = __float2int_rn(__fmul_rn(static_cast<float>(static_cast<int8_t>(w >> (8 * i))), ratio));
-    y |= (static_cast<uint32_t>(c) & 0xffu) << (8 * i);
-  }
+// Four codes times `ratio` (at most 1), each rounded: rint(code * ratio), one fp32 operation a step.  Codes become
+// floats, and floats codes, by an addition that leaves the whole number in the low bits.
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 y;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
   return y;
+}
+__device__ __forceinline__ uint32_t scale4(uint32_t w, f32x2 ratio) {
+  const uint32_t u = w ^ 0x80808080u;             // code + 128: the low byte of 2^23 + code + 128
+  const f32x2 less = dup2(-8388736.f), whole = dup2(12582912.f);   // -(2^23 + 128); 2^23 + 2^22: no fraction is left
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f32x2 x = pack2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + 2 * i)),
+                          __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 + 2 * i)));
+    float a, b;
+    unpack2(add2(mul2(add2(x, less), ratio), whole), a, b);
+    y[2 * i] = __float_as_uint(a), y[2 * i + 1] = __float_as_uint(b);
+  }
+  return __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) q4_kv_compact_kernel(const __grid_constant__ KvCompactParams p) {
   constexpr int kParts = D / 16, kEach = kMoveTokens * kParts / kMoveThreads;
-  __shared__ long long s_src[kMoveTokens], s_dst[kMoveTokens];   // rows of codes; -1: zeros, nothing to write
-  __shared__ float s_ratio[kMoveTokens];
+  constexpr unsigned kNone = ~0u;
+  __shared__ unsigned s_src[kMoveTokens], s_dst[kMoveTokens];   // rows of codes: fewer than 2^32 fit any GPU
+  __shared__ float s_ratio[2][kMoveTokens];                // of keys and values; -1: they stay as they are
   const int tid = threadIdx.x;
   const int b = blockIdx.x / p.c.heads, h = blockIdx.x - b * p.c.heads;
-  const bool values = blockIdx.z != 0;
   pdl_launch_dependents();
   pdl_wait();
   const int len = max(0, p.kv_len[b]), first = p.first ? max(0, p.first[b]) : 0;
@@ -224,17 +237,15 @@ __global__ void __launch_bounds__(kMoveThreads) q4_kv_compact_kernel(const __gri
   const int32_t* kept = p.kept + (static_cast<long long>(b) * p.kept_heads + (p.kept_heads > 1 ? h : 0)) * p.width;
   const int32_t* to_table = p.to_table ? p.to_table : p.table;
   const long long to_stride = p.to_table ? p.to_stride : p.table_stride;
-  float* scales = values ? p.c.vs : p.c.ks;
-  int8_t* codes = values ? p.c.v : p.c.k;
   // places in runs that begin with a block
   const long long step = p.to_table ? static_cast<long long>(gridDim.y) * kMoveTokens : kMoveTokens;
   for (long long t0 = first / kKvBlock * kKvBlock + static_cast<long long>(p.to_table ? blockIdx.y : 0) * kMoveTokens;
        count > 0 && t0 < end; t0 += step) {
-    uint4 w[kEach];
     if (tid < kMoveTokens) {
       const int pos = static_cast<int>(min(t0 + tid, static_cast<long long>(end)));   // `end`: no place
       long long dst = -1, src = -1;
-      float had = 0.f;                            // the scale that the token comes with
+      float had[2] = {0.f, 0.f}, weight = 0.f;    // the scales that the token comes with, its weight
+      const bool moves = pos >= first && pos < end;
       if (pos < end) {
         dst = kv_row(p.c, to_table, to_stride, b, pos, h);
         if (pos < first) {                        // stays where it is
@@ -242,43 +253,59 @@ __global__ void __launch_bounds__(kMoveThreads) q4_kv_compact_kernel(const __gri
         } else {
           const int from = __ldg(kept + (pos - first));
           if (from >= pos && from < len) src = kv_row(p.c, p.table, p.table_stride, b, from, h);
-          if (src < 0 && !values) atomicOr(p.err, kDevErrIndex);
         }
-        if (dst < 0 && !values) atomicOr(p.err, kDevErrIndex);
-        if (src >= 0) had = scales[src >> 4];
+        if (src < 0 || dst < 0) atomicOr(p.err, kDevErrIndex);
+        if (src >= 0) {
+          had[0] = p.c.ks[src >> 4], had[1] = p.c.vs[src >> 4];
+          if (p.weight && moves) weight = p.weight[src];
+        }
       }
-      float s = had;
+      float s[2] = {had[0], had[1]};
 #pragma unroll
-      for (int o = 1; o < kKvBlock; o <<= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-      const float ratio = s > 0.f ? __fdiv_rn(had, s) : 0.f;
-      s_src[tid] = src;
-      s_dst[tid] = pos < end && !(src == dst && ratio == 1.f) ? dst : -1;
-      s_ratio[tid] = ratio;
-      const bool lead = (tid & (kKvBlock - 1)) == 0 && dst >= 0;
-      const float weight = !values && p.weight && pos >= first && pos < end && src >= 0 ? p.weight[src] : 0.f;
-      // all sources of these places have been read before the first is written
+      for (int o = 1; o < kKvBlock; o <<= 1) {
+        s[0] = fmaxf(s[0], __shfl_xor_sync(0xffffffffu, s[0], o));
+        s[1] = fmaxf(s[1], __shfl_xor_sync(0xffffffffu, s[1], o));
+      }
+      s_src[tid] = src < 0 ? kNone : static_cast<unsigned>(src);
+      s_dst[tid] = dst < 0 ? kNone : static_cast<unsigned>(dst);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float ratio = s[x] > 0.f ? __fdiv_rn(had[x], s[x]) : 0.f;
+        s_ratio[x][tid] = src == dst && ratio == 1.f ? -1.f : ratio;
+      }
+      // all scales and weights of these places' sources have been read before the first is written
       asm volatile("bar.sync 1, %0;" ::"n"(kMoveTokens) : "memory");
-      if (lead) scales[dst >> 4] = s;
-      if (!values && p.weight && pos >= first && pos < end && dst >= 0) p.weight[dst] = weight;
+      if ((tid & (kKvBlock - 1)) == 0 && dst >= 0) p.c.ks[dst >> 4] = s[0], p.c.vs[dst >> 4] = s[1];
+      if (p.weight && moves && dst >= 0) p.weight[dst] = weight;
     }
     __syncthreads();
+    uint4 w[2][kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int t = (i * kMoveThreads + tid) / kParts, part = (i * kMoveThreads + tid) % kParts;
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (s_dst[t] >= 0 && s_src[t] >= 0) w[i] = *reinterpret_cast<const uint4*>(codes + s_src[t] * D + part * 16);
+      const unsigned src = s_src[t];
+      const long long at = static_cast<long long>(src) * D + part * 16;
+      w[0][i] = w[1][i] = make_uint4(0, 0, 0, 0);
+      if (src != kNone && s_ratio[0][t] >= 0.f) w[0][i] = *reinterpret_cast<const uint4*>(p.c.k + at);
+      if (src != kNone && s_ratio[1][t] >= 0.f) w[1][i] = *reinterpret_cast<const uint4*>(p.c.v + at);
     }
-    __syncthreads();
+    if (!p.to_table) __syncthreads();
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int t = (i * kMoveThreads + tid) / kParts, part = (i * kMoveThreads + tid) % kParts;
-      if (s_dst[t] < 0) continue;
-      const float ratio = s_ratio[t];
-      if (ratio != 1.f) {
-        w[i].x = scale4(w[i].x, ratio), w[i].y = scale4(w[i].y, ratio);
-        w[i].z = scale4(w[i].z, ratio), w[i].w = scale4(w[i].w, ratio);
+      const unsigned dst = s_dst[t];
+      const long long at = static_cast<long long>(dst) * D + part * 16;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float ratio = s_ratio[x][t];
+        if (dst == kNone || ratio < 0.f) continue;
+        uint4 y = w[x][i];
+        if (ratio != 1.f) {
+          const f32x2 two = dup2(ratio);
+          y.x = scale4(y.x, two), y.y = scale4(y.y, two), y.z = scale4(y.z, two), y.w = scale4(y.w, two);
+        }
+        *reinterpret_cast<uint4*>((x ? p.c.v : p.c.k) + at) = y;
       }
-      *reinterpret_cast<uint4*>(codes + s_dst[t] * D + part * 16) = w[i];
     }
     __syncthreads();
   }
@@ -309,7 +336,7 @@ cudaError_t launch_kv_select(const KvSelectParams& p, long long max_kv, int sms,
   const long long pairs = static_cast<long long>(p.B) * p.c.heads;
   // as many CTAs for a (sequence, head) as fill the GPU, or hold its tokens in shared memory, up to eight
   int cluster = 1;
-  while (cluster < kMostCluster && (pairs * cluster < sms || max_kv > static_cast<long long>(cluster) * kSelTokens) &&
+  while (cluster < kMostCluster && (pairs * cluster < 4LL * sms || max_kv > static_cast<long long>(cluster) * kSelTokens) &&
          max_kv > cluster * 1024LL)
     cluster *= 2;
   const long long each = ((max_kv + cluster * kSelThreads - 1) / (cluster * kSelThreads)) * kSelThreads;
@@ -327,7 +354,7 @@ cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t st) {
   const long long pairs = static_cast<long long>(p.B) * p.c.heads;
   // into other pages: a CTA for each run of places, which may begin inside a block
   const long long runs = p.to_table ? std::min((p.width + kKvBlock + kMoveTokens - 1) / kMoveTokens, 65535LL) : 1;
-  const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(runs), 2);
+  const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(runs));
   return p.c.dim == 128 ? launch_pdl(q4_kv_compact_kernel<128>, grid, kMoveThreads, 0, 1, st, p)
                         : launch_pdl(q4_kv_compact_kernel<64>, grid, kMoveThreads, 0, 1, st, p);
 }

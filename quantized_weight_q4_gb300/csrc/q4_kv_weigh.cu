@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtas = 3;                  // of an SM
+constexpr int kCtas = 2;                  // of an SM
 constexpr int kTileRows = 8;              // query rows of an MMA's columns
 constexpr int kChunkTiles = 8;            // of them in shared memory at a time
 constexpr int kChunkRows = kTileRows * kChunkTiles;
@@ -179,11 +179,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
     u = first + pair_cost;
     if (from >= end) continue;
     const int32_t* table = a.b.table + b * a.b.table_stride;
-    auto page_of = [&](int i) {   // of counted block i
-      if (i >= end) return -1;
-      const int pi = (s.blocks.real(i) * kKvBlock) >> a.c.page_log2;
-      return pi < a.b.table_stride ? __ldg(table + pi) : -1;
-    };
 
     for (long long row0 = 0; row0 == 0 || row0 < s.rows; row0 += kChunkRows) {
       const int rows = static_cast<int>(min(static_cast<long long>(kChunkRows), s.rows - row0));
@@ -242,92 +237,104 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
       auto is_seen = [&](int blk) {
         return rows > 0 && blk * kKvBlock <= seen_hi && (blk * kKvBlock + kKvBlock > seen_lo || blk * kKvBlock < a.sinks);
       };
-      auto load = [&](int i, int page, uint4 (&k)[2][kParts], float& ks) {
-        ks = 0.f;
-        if (i >= end || static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) return;
-        const int blk = s.blocks.real(i);
-        if (!is_seen(blk)) return;
-        const long long at = ((static_cast<long long>(page) * a.c.heads + h) << (a.c.page_log2 - 4)) + (blk & ((a.c.page >> 4) - 1));
-        const int8_t* p = a.c.k + at * (kKvBlock * D) + g * D + c * 16;
-#pragma unroll
-        for (int x = 0; x < kParts; ++x) {
-          k[0][x] = __ldg(reinterpret_cast<const uint4*>(p + x * 64));
-          k[1][x] = __ldg(reinterpret_cast<const uint4*>(p + 8 * D + x * 64));
-        }
-        ks = __ldg(a.c.ks + at);
-      };
-      uint4 k[2][kParts], k_next[2][kParts];
-      float ks, ks_next;
-      int page = page_of(from + warp), page_next = page_of(from + warp + kWarps);
-#pragma unroll
-      for (int x = 0; x < kParts; ++x) k_next[0][x] = k_next[1][x] = make_uint4(0, 0, 0, 0);
-      load(from + warp, page, k_next, ks_next);
-      for (int i = from + warp; i < end; i += kWarps) {
-#pragma unroll
-        for (int x = 0; x < kParts; ++x) k[0][x] = k_next[0][x], k[1][x] = k_next[1][x];
-        ks = ks_next;
-        const int cur = page;
-        page = page_next;
-        page_next = page_of(i + 2 * kWarps);
-        load(i + kWarps, page, k_next, ks_next);
-        if (static_cast<unsigned>(cur) >= static_cast<unsigned>(a.c.pages)) {
-          if (lane == 0) atomicOr(a.err, kDevErrIndex);
-          continue;
-        }
-        const int blk = s.blocks.real(i);
-        // this lane's token (c = 0: g, c = 1: g + 8) and what it has already
-        const int pos = blk * kKvBlock + g + 8 * c;
-        float* w = a.weight + (((static_cast<long long>(cur) * a.c.heads + h) << a.c.page_log2) + (pos & (a.c.page - 1)));
-        const bool mine = c < 2 && pos < s.len;
-        const bool seen = is_seen(blk);
-        if (!seen && row0 > 0) continue;
-        const float had = mine && (row0 > 0 || pos < s.held) ? *w : 0.f;
-        float sum[2] = {0.f, 0.f};
-        if (seen) {
-          const bool edge = blk >= whole_hi || (blk < whole_lo && (blk + 1LL) * kKvBlock > a.sinks);
-          for (int n = 0; n < tiles; ++n) {
-            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const uint32_t* q = s_q + (n * KT * 32 + lane) * kWords;
-#pragma unroll
-            for (int t = 0; t < KT; ++t) {
-              const uint4 x = k[0][t >> 2], y = k[1][t >> 2];
-              const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-              uint32_t f[4];
-              widen4(xw[t & 3], f[0], f[2]);
-              widen4(yw[t & 3], f[1], f[3]);
-              if (SPLIT) {
-                const uint4 z = *reinterpret_cast<const uint4*>(q + t * 32 * kWords);
-                mma(acc[0], f, z.x, z.y);
-                mma(acc[1], f, z.z, z.w);
-              } else {
-                const uint2 z = *reinterpret_cast<const uint2*>(q + t * 32 * kWords);
-                mma(acc[t & 1], f, z.x, z.y);
-              }
-            }
-            // the thread's queries 2 c and 2 c + 1 of the tile
-            const float4 r = *reinterpret_cast<const float4*>(s_row + n * kTileRows + 2 * c);
-            const float f0 = ks * r.x, f1 = ks * r.z;
-            float e[4];
-            e[0] = fmaf(acc[0][0] + acc[1][0], f0, r.y), e[1] = fmaf(acc[0][1] + acc[1][1], f1, r.w);
-            e[2] = fmaf(acc[0][2] + acc[1][2], f0, r.y), e[3] = fmaf(acc[0][3] + acc[1][3], f1, r.w);
-            if (edge) {
-              const int4 see = *reinterpret_cast<const int4*>(s_see + n * kTileRows + 2 * c);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                const int p = blk * kKvBlock + g + (v >> 1) * 8, lo = v & 1 ? see.z : see.x, hi = v & 1 ? see.w : see.y;
-                if (p > hi || (p <= lo && p >= a.sinks)) e[v] = -INFINITY;
-              }
-            }
-            sum[0] += ex2(e[0]) + ex2(e[1]);
-            sum[1] += ex2(e[2]) + ex2(e[3]);
-          }
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            sum[v] += __shfl_xor_sync(0xffffffffu, sum[v], 1);
-            sum[v] += __shfl_xor_sync(0xffffffffu, sum[v], 2);
+      // ---- the warp's blocks, 32 of them at a time: a lane looks one up ----
+      for (int i0 = from + warp; i0 < end; i0 += 32 * kWarps) {
+        const int count = min(32, (end - i0 + kWarps - 1) / kWarps);
+        int my_at = -1, my_blk = 0;               // block of the cache (-1: nothing to do), block of the sequence
+        unsigned my_kind = 0;                     // bit 0: some row sees of it, bit 1: not every row sees all of it
+        float my_scale = 0.f;
+        if (lane < count) {
+          my_blk = s.blocks.real(i0 + lane * kWarps);
+          const int pi = (my_blk * kKvBlock) >> a.c.page_log2;
+          const int page = pi < a.b.table_stride ? __ldg(table + pi) : -1;
+          const bool seen = is_seen(my_blk);
+          if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
+            atomicOr(a.err, kDevErrIndex);
+          } else if (seen || row0 == 0) {
+            my_at = ((page * a.c.heads + h) << (a.c.page_log2 - 4)) + (my_blk & ((a.c.page >> 4) - 1));
+            const bool edge = my_blk >= whole_hi || (my_blk < whole_lo && (my_blk + 1LL) * kKvBlock > a.sinks);
+            my_kind = (seen ? 1u : 0u) | (edge ? 2u : 0u);
+            if (seen) my_scale = __ldg(a.c.ks + my_at);
           }
         }
-        if (mine && (seen || pos >= s.held)) *w = had + (c ? sum[1] : sum[0]);
+        // keys of the block that lane n looked up
+        auto load = [&](int n, uint4 (&k)[2][kParts]) {
+          const int at = __shfl_sync(0xffffffffu, my_at, n);
+          if (n >= count || at < 0 || !(__shfl_sync(0xffffffffu, my_kind, n) & 1u)) return;
+          const int8_t* from_k = a.c.k + static_cast<long long>(at) * (kKvBlock * D) + g * D + c * 16;
+#pragma unroll
+          for (int x = 0; x < kParts; ++x) {
+            k[0][x] = __ldg(reinterpret_cast<const uint4*>(from_k + x * 64));
+            k[1][x] = __ldg(reinterpret_cast<const uint4*>(from_k + 8 * D + x * 64));
+          }
+        };
+        auto work = [&](int n, const uint4 (&k)[2][kParts]) {
+          const int at = __shfl_sync(0xffffffffu, my_at, n);
+          const unsigned kind = __shfl_sync(0xffffffffu, my_kind, n);
+          if (at < 0) return;
+          const int blk = __shfl_sync(0xffffffffu, my_blk, n);
+          // this lane's token (c = 0: g, c = 1: g + 8) and what it has already
+          const int pos = blk * kKvBlock + g + 8 * c;
+          float* w = a.weight + static_cast<long long>(at) * kKvBlock + g + 8 * c;
+          const bool mine = c < 2 && pos < s.len;
+          const float had = mine && (row0 > 0 || pos < s.held) ? *w : 0.f;
+          float sum[2] = {0.f, 0.f};
+          if (kind & 1u) {
+            const float ks = __shfl_sync(0xffffffffu, my_scale, n);
+            for (int t8 = 0; t8 < tiles; ++t8) {
+              float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+              const uint32_t* q = s_q + (t8 * KT * 32 + lane) * kWords;
+#pragma unroll
+              for (int t = 0; t < KT; ++t) {
+                const uint4 x = k[0][t >> 2], y = k[1][t >> 2];
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+                uint32_t f[4];
+                widen4(xw[t & 3], f[0], f[2]);
+                widen4(yw[t & 3], f[1], f[3]);
+                if (SPLIT) {
+                  const uint4 z = *reinterpret_cast<const uint4*>(q + t * 32 * kWords);
+                  mma(acc[0], f, z.x, z.y);
+                  mma(acc[1], f, z.z, z.w);
+                } else {
+                  const uint2 z = *reinterpret_cast<const uint2*>(q + t * 32 * kWords);
+                  mma(acc[t & 1], f, z.x, z.y);
+                }
+              }
+              // the thread's queries 2 c and 2 c + 1 of the tile
+              const float4 r = *reinterpret_cast<const float4*>(s_row + t8 * kTileRows + 2 * c);
+              const float f0 = ks * r.x, f1 = ks * r.z;
+              float e[4];
+              e[0] = fmaf(acc[0][0] + acc[1][0], f0, r.y), e[1] = fmaf(acc[0][1] + acc[1][1], f1, r.w);
+              e[2] = fmaf(acc[0][2] + acc[1][2], f0, r.y), e[3] = fmaf(acc[0][3] + acc[1][3], f1, r.w);
+              if (kind & 2u) {
+                const int4 see = *reinterpret_cast<const int4*>(s_see + t8 * kTileRows + 2 * c);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  const int p = blk * kKvBlock + g + (v >> 1) * 8, lo = v & 1 ? see.z : see.x, hi = v & 1 ? see.w : see.y;
+                  if (p > hi || (p <= lo && p >= a.sinks)) e[v] = -INFINITY;
+                }
+              }
+              sum[0] += ex2(e[0]) + ex2(e[1]);
+              sum[1] += ex2(e[2]) + ex2(e[3]);
+            }
+            // the lanes of c = 0, 2 end the first token's sum, those of c = 1, 3 the second's
+            const float keep = c & 1 ? sum[1] : sum[0], give = c & 1 ? sum[0] : sum[1];
+            sum[0] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+          }
+          if (mine && (kind & 1u || pos >= s.held)) *w = had + sum[0];
+        };
+        // two sets of registers take turns: a block is on its way while the other is in work
+        uint4 k[2][2][kParts];
+#pragma unroll
+        for (int x = 0; x < 2 * 2 * kParts; ++x) (&k[0][0][0])[x] = make_uint4(0, 0, 0, 0);
+        load(0, k[0]);
+        for (int n = 0; n < count; n += 2) {
+          load(n + 1, k[1]);
+          work(n, k[0]);
+          load(n + 2, k[0]);
+          if (n + 1 < count) work(n + 1, k[1]);
+        }
       }
     }
   }

@@ -134,6 +134,8 @@ def test_rows_that_share_requests(kind):
 
 
 def test_long_histories_and_many_biases():
+    check(60, 128007, "bf16", 4, width=2000, nbias=50, masks=20, hot=4.0)
+    check(60, 128007, "f32", 5, width=2000, nbias=50, masks=20, hot=4.0, out_kind="bf16")
     check(2, 40000, "f32", 1, width=100_000, hot=3.0)
     check(1, 300, "f32", 2, width=524287, nbias=4095)
     check(2, 327672, "bf16", 3, width=3000, nbias=300, masks=1)
