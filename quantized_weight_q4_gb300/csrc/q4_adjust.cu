@@ -8,10 +8,11 @@
 // while it looks through the row's history and biases for tokens of the slice
 // and notes them in shared memory, a word a token: the last bias entry, whether
 // the prompt has it, how often the answer has it.  Notes are whole numbers, so
-// their order does not matter; who makes a token's first note puts the token on
-// a list.  The slice is stored as it came, with the mask's -inf, and then the
-// listed tokens again, a thread each: beside their neighbours they would hold
-// up whole warps, one after another.
+// their order does not matter.  The slice is stored as it came, with the mask's
+// -inf, and then the tokens with a note again, a thread each, from a list:
+// beside their neighbours they would hold up whole warps, one after another.
+// A CTA is bound by the latency of what it looks up; so all that can be is on
+// its way at once, and the first part of the history before its length is known.
 #include <algorithm>
 
 #include "q4_kernels.h"
@@ -20,9 +21,10 @@
 namespace q4 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kUnit = 8;                  // logits that a thread has side by side
 constexpr int kUnits = 4;                 // of them
+constexpr int kAhead = 4;                 // fours of the history that a thread asks for at once
 constexpr int kMostSlice = kThreads * kUnit * kUnits;
 constexpr unsigned kSeen = 1u << 19;      // a note: bits 0-18 how often, bit 19 in the prompt, bits 20-31 bias entry + 1
 constexpr unsigned kTimes = kSeen - 1;
@@ -38,6 +40,16 @@ __device__ __forceinline__ void store1(void* p, long long i, float x) {
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
   else
     static_cast<float*>(p)[i] = x;
+}
+
+// Notes of a token, `at` in the slice of n: without a branch, as most tokens are of other slices.
+__device__ __forceinline__ void note_said(uint32_t notes, unsigned at, unsigned n) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t}" ::"r"(at), "r"(n),
+               "r"(notes + 4 * at) : "memory");
+}
+__device__ __forceinline__ void note_seen(uint32_t notes, unsigned at, unsigned n) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.or.b32 [%2], %3;\n\t}" ::"r"(at), "r"(n),
+               "r"(notes + 4 * at), "r"(kSeen) : "memory");
 }
 
 // Eight logits side by side, as they lie in memory.
@@ -111,65 +123,96 @@ __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_consta
   for (int i = 0; i < kUnits; ++i)
     if (i * kThreads + tid < units) x[i].load(p.logits, in + lead + (i * kThreads + tid) * kUnit);
   const int req = p.request ? __ldg(p.request + t) : t;
+  const int mask_row = !p.mask ? -1 : p.mask_row ? __ldg(p.mask_row + t) : t;
   const bool known = req >= 0 && req < p.requests;
   const uint32_t* mask = nullptr;
-  if (p.mask) {
-    const int row = p.mask_row ? __ldg(p.mask_row + t) : t;
-    if (row >= 0 && row < p.masks) mask = reinterpret_cast<const uint32_t*>(p.mask) + row * ((p.V + 31LL) / 32);
-    if (row >= p.masks && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
-  }
-  if (p.request && req >= p.requests && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kDevErrIndex);
+  if (mask_row >= 0 && mask_row < p.masks) mask = reinterpret_cast<const uint32_t*>(p.mask) + mask_row * ((p.V + 31LL) / 32);
+  if (blockIdx.x == 0 && tid == 0 && ((p.mask && mask_row >= p.masks) || (p.request && req >= p.requests))) atomicOr(p.err, kDevErrIndex);
   const bool penalties = p.history && known;
   const float* bias = p.bias_index && known ? p.bias + static_cast<long long>(req) * p.bias_width : nullptr;
   const bool notes = penalties || bias;
-  if (notes) {
-    for (int i = tid; i < slice / 4; i += kThreads) reinterpret_cast<uint4*>(s_note)[i] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) s_listed = 0;
-    __syncthreads();
-    if (bias) {
-      const int32_t* index = p.bias_index + static_cast<long long>(req) * p.bias_width;
-      for (int i = tid; i < p.bias_width; i += kThreads) {
-        const int at = __ldg(index + i) - v0;
-        if (static_cast<unsigned>(at) < static_cast<unsigned>(n) &&
-            atomicMax(s_note + at, static_cast<unsigned>(i + 1) << kBiasShift) == 0)
-          s_list[atomicAdd(&s_listed, 1)] = static_cast<uint16_t>(at);
-      }
-      if (penalties) __syncthreads();
-    }
-    if (penalties) {
-      const int32_t* history = p.history + static_cast<long long>(req) * p.history_width;
-      const int len = min(__ldg(p.history_len + t), p.history_width), prompt = p.prompt_len ? __ldg(p.prompt_len + t) : 0;
-      auto note = [&](int token, int i) {
-        const int at = token - v0;
-        if (static_cast<unsigned>(at) >= static_cast<unsigned>(n)) return;
-        const unsigned old = i < prompt ? atomicOr(s_note + at, kSeen) : atomicAdd(s_note + at, 1u);
-        if (old == 0) s_list[atomicAdd(&s_listed, 1)] = static_cast<uint16_t>(at);
-      };
-      // four tokens at a time from where the list begins at 16 bytes, two such a step
-      const int skip = min(max(len, 0), static_cast<int>((16 - (reinterpret_cast<uintptr_t>(history) & 15)) & 15) / 4);
-      const int fours = (max(len, 0) - skip) / 4;
-      if (tid < skip) note(__ldg(history + tid), tid);
-      const int rest = skip + 4 * fours + tid;
-      if (rest < len) note(__ldg(history + rest), rest);   // three at most
-#pragma unroll 2
-      for (int i = tid; i < fours; i += kThreads) {
-        const int4 four = __ldg(reinterpret_cast<const int4*>(history + skip) + i);
-        const int at = skip + 4 * i;
-        note(four.x, at), note(four.y, at + 1), note(four.z, at + 2), note(four.w, at + 3);
-      }
-    }
-  }
   auto bits_from = [&](int v) {             // the mask's bits of tokens v .. v + 7, and more above them
     const int w = v >> 5, s = v & 31;
     const uint32_t lo = __ldg(mask + w), hi = s > 24 && v + 32 - s < p.V ? __ldg(mask + w + 1) : 0u;
     return __funnelshift_r(lo, hi, s);
   };
+  uint32_t allowed[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+    allowed[i] = mask && i * kThreads + tid < units ? bits_from(v0 + lead + (i * kThreads + tid) * kUnit) & 0xffu : 0xffu;
+  if (notes) {
+    for (int i = tid; i < slice / 4; i += kThreads) reinterpret_cast<uint4*>(s_note)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) s_listed = 0;
+    const int32_t* history = p.history + static_cast<long long>(penalties ? req : 0) * p.history_width;
+    // four tokens at a time from where the list begins at 16 bytes
+    const int skip = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(history) & 15)) & 15) / 4;
+    const int fours = penalties ? max(0, p.history_width - skip) / 4 : 0;
+    const uint32_t notes_at = smem_u32(s_note);
+    const int4* four = reinterpret_cast<const int4*>(history + skip);
+    int4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      ahead[k] = k * kThreads + tid < fours ? __ldg(four + k * kThreads + tid) : make_int4(-1, -1, -1, -1);
+    const int32_t* index = bias ? p.bias_index + static_cast<long long>(req) * p.bias_width : nullptr;
+    const int biased = bias && tid < p.bias_width ? __ldg(index + tid) : -1;
+    const int len = penalties ? min(__ldg(p.history_len + t), p.history_width) : 0;
+    const int prompt = penalties && p.prompt_len ? __ldg(p.prompt_len + t) : 0;
+    __syncthreads();
+    if (bias) {
+      auto note = [&](int token, int i) {
+        const int at = token - v0;
+        if (static_cast<unsigned>(at) < static_cast<unsigned>(n)) atomicMax(s_note + at, static_cast<unsigned>(i + 1) << kBiasShift);
+      };
+      note(biased, tid);
+      for (int i = kThreads + tid; i < p.bias_width; i += kThreads) note(__ldg(index + i), i);
+      if (penalties) __syncthreads();
+    }
+    if (penalties) {
+      const int from_prompt = min(max(prompt, 0), max(len, 0));
+      auto note = [&](int token, int i) {
+        if (i >= len) return;
+        const unsigned at = static_cast<unsigned>(token - v0);
+        if (i < from_prompt) note_seen(notes_at, at, n); else note_said(notes_at, at, n);
+      };
+      auto note4 = [&](const int4& x, int i) {
+        const int at = skip + 4 * i;
+        const unsigned a[4] = {static_cast<unsigned>(x.x - v0), static_cast<unsigned>(x.y - v0),
+                               static_cast<unsigned>(x.z - v0), static_cast<unsigned>(x.w - v0)};
+        if (at >= from_prompt && at + 4 <= len) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) note_said(notes_at, a[k], n);
+        } else if (at + 4 <= from_prompt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) note_seen(notes_at, a[k], n);
+        } else {
+          note(x.x, at), note(x.y, at + 1), note(x.z, at + 2), note(x.w, at + 3);
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (skip + 4 * (k * kThreads + tid) < len) note4(ahead[k], k * kThreads + tid);
+#pragma unroll 4
+      for (int i = kAhead * kThreads + tid; i < fours && skip + 4 * i < len; i += kThreads) note4(__ldg(four + i), i);
+      if (tid < min(skip, p.history_width)) note(__ldg(history + tid), tid);
+      const int rest = skip + 4 * fours + tid;
+      if (rest < p.history_width) note(__ldg(history + rest), rest);   // three at most
+    }
+    __syncthreads();
+    for (int i = tid; i < slice / 4; i += kThreads) {
+      const uint4 x = reinterpret_cast<const uint4*>(s_note)[i];
+      if ((x.x | x.y | x.z | x.w) == 0) continue;
+      int to_list = atomicAdd(&s_listed, (x.x != 0) + (x.y != 0) + (x.z != 0) + (x.w != 0));
+      if (x.x) s_list[to_list++] = static_cast<uint16_t>(4 * i);
+      if (x.y) s_list[to_list++] = static_cast<uint16_t>(4 * i + 1);
+      if (x.z) s_list[to_list++] = static_cast<uint16_t>(4 * i + 2);
+      if (x.w) s_list[to_list] = static_cast<uint16_t>(4 * i + 3);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const int u = i * kThreads + tid;
     if (u >= units) break;
     const int at = lead + u * kUnit;
-    const uint32_t allowed = mask ? bits_from(v0 + at) & 0xffu : 0xffu;
     Unit<OUT> z;
     if (IN == OUT) {
       z = reinterpret_cast<const Unit<OUT>&>(x[i]);
@@ -178,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_consta
       x[i].get(y);
       z.set(y);
     }
-    if (allowed != 0xffu) z.mask(allowed);
+    if (allowed[i] != 0xffu) z.mask(allowed[i]);
     z.store(p.out, to + at);
   }
   // what is outside the eights
@@ -212,7 +255,7 @@ cudaError_t launch(const AdjustParams& p, int slice, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.V + slice - 1) / slice), static_cast<unsigned>(p.T));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(slice) * 6;
+  cfg.dynamicSmemBytes = p.history || p.bias_index ? static_cast<size_t>(slice) * 6 : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -21,9 +21,10 @@ namespace {
 // own, and write it behind the counts of those before.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMostCluster = 8;
+constexpr int kMostCluster = 8;        // one sequence of 100,003 tokens, 8 heads, four / eight / sixteen: 35 / 37 / 64 us
 constexpr int kBins = 2048;
 constexpr int kSelTokens = 40960;      // of a CTA in shared memory; more are read again from their pages
+constexpr int kQuad = 4;               // tokens that a thread takes side by side: of one page
 
 // A weight as a number in its order; NaN is the least.
 __device__ __forceinline__ unsigned order_of(float w) {
@@ -42,7 +43,7 @@ __device__ __forceinline__ unsigned ld_peer(uint32_t addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_constant__ KvSelectParams p, int cluster, int cap) {
+__global__ void __launch_bounds__(kSelThreads, 3) q4_kv_select_kernel(const __grid_constant__ KvSelectParams p, int cluster, int cap) {
   extern __shared__ __align__(16) unsigned s_mem[];
   unsigned* s_hist = s_mem;                       // [3][kBins]
   unsigned* s_key = s_mem + 3 * kBins;            // [cap]
@@ -64,29 +65,46 @@ __global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_
   if (rank == 0 && h == 0 && tid == 0) p.count[b] = count;
   for (int i = rank * kSelThreads + tid; i < head; i += cluster * kSelThreads) kept[i] = i;
   for (int i = rank * kSelThreads + tid; i < tail; i += cluster * kSelThreads) kept[count - tail + i] = len - tail + i;
-  // runs of whole warps' steps, alike for all warps of the cluster
-  const int run = (most + cluster * kSelThreads - 1) / (cluster * kSelThreads) * 32;   // of a warp
-  const int from = min(static_cast<long long>(most), static_cast<long long>(rank) * run * kSelWarps);
-  const int mine = min(static_cast<long long>(most) - from, static_cast<long long>(run) * kSelWarps);
   const bool all = want == static_cast<unsigned>(most);   // the same for the whole cluster
   if (all || want == 0) {
     if (all)
-      for (int i = tid; i < mine; i += kSelThreads) kept[head + from + i] = head + from + i;
+      for (int i = rank * kSelThreads + tid; i < most; i += cluster * kSelThreads) kept[head + i] = head + i;
     return;
   }
+  // tokens from a multiple of four on, the first `skip` of which are sinks; a warp's run is a number of whole steps
+  constexpr int kStep = 32 * kQuad;
+  const int base = head & ~(kQuad - 1), total = len - tail - base;
+  const int run = static_cast<int>((total + static_cast<long long>(cluster) * kSelWarps * kStep - 1) /
+                                   (static_cast<long long>(cluster) * kSelWarps * kStep)) * kStep;
+  const int from = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(rank) * run * kSelWarps));
+  const int mine = static_cast<int>(min(static_cast<long long>(total) - from, static_cast<long long>(run) * kSelWarps));
+  const int skip = from == 0 ? head - base : 0;
+  const int quads = (mine + kQuad - 1) / kQuad;
   const int32_t* table = p.table + b * p.table_stride;
-  auto weight_of = [&](int i) {                   // of this CTA's token i
-    const int pos = head + from + i, pi = pos >> p.c.page_log2;
+  auto quad_of = [&](int q) {                     // weights of tokens 4 q .. 4 q + 3 of this CTA, in their order
+    const int pos = base + from + q * kQuad, pi = pos >> p.c.page_log2;
     const int page = pi < p.table_stride ? __ldg(table + pi) : -1;
     if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.pages)) {
       if (h == 0) atomicOr(p.err, kDevErrIndex);
-      return 0u;
+      return make_uint4(0, 0, 0, 0);
     }
-    return order_of(__ldg(p.weight + (((static_cast<long long>(page) * p.c.heads + h) << p.c.page_log2) + (pos & (p.c.page - 1)))));
+    const float4 w = __ldg(reinterpret_cast<const float4*>(
+        p.weight + (((static_cast<long long>(page) * p.c.heads + h) << p.c.page_log2) + (pos & (p.c.page - 1)))));
+    return make_uint4(order_of(w.x), order_of(w.y), order_of(w.z), order_of(w.w));
   };
   for (int i = tid; i < 3 * kBins; i += kSelThreads) s_hist[i] = 0;
-  for (int i = tid; i < min(mine, cap); i += kSelThreads) s_key[i] = weight_of(i);
-  auto key_of = [&](int i) { return i < cap ? s_key[i] : weight_of(i); };
+  uint4* s_quad = reinterpret_cast<uint4*>(s_key);
+  const int held = min(quads, cap / kQuad);
+#pragma unroll 4
+  for (int q = tid; q < held; q += kSelThreads) s_quad[q] = quad_of(q);
+  // the four weights, and which of them count
+  auto keys = [&](int q, unsigned (&key)[kQuad], bool (&have)[kQuad]) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (q < quads) x = q < held ? s_quad[q] : quad_of(q);
+    key[0] = x.x, key[1] = x.y, key[2] = x.z, key[3] = x.w;
+#pragma unroll
+    for (int k = 0; k < kQuad; ++k) have[k] = q * kQuad + k >= skip && q * kQuad + k < mine;
+  };
   if (cluster > 1) cluster_started();
   __syncthreads();
 
@@ -96,18 +114,25 @@ __global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? kBins / 2 : kBins;
     unsigned* hist = s_hist + d * kBins;
-    for (int i = tid; i - tid < mine; i += kSelThreads) {
-      const unsigned key = i < mine ? key_of(i) : 0u;
-      const bool in = i < mine && (key & known) == cut;
-      const unsigned digit = key >> shift & (bins - 1), who = __ballot_sync(0xffffffffu, in);
-      if (who == 0) continue;
-      // equal weights would all wait for one counter
-      const int lead = __ffs(who) - 1;
-      const unsigned first = __shfl_sync(0xffffffffu, digit, lead);
-      if (__all_sync(0xffffffffu, !in || digit == first)) {
-        if (lane == lead) atomicAdd(hist + first, __popc(who));
-      } else if (in) {
-        atomicAdd(hist + digit, 1u);
+    for (int q = tid; q - tid < quads; q += kSelThreads) {
+      unsigned key[kQuad];
+      bool in[kQuad];
+      keys(q, key, in);
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < kQuad; ++k) any |= in[k] = in[k] && (key[k] & known) == cut;
+      if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+      for (int k = 0; k < kQuad; ++k) {
+        // equal weights would all wait for one counter
+        const unsigned who = __ballot_sync(0xffffffffu, in[k]), digit = key[k] >> shift & (bins - 1);
+        const int lead = __ffs(who) - 1;
+        const unsigned one = __shfl_sync(0xffffffffu, digit, max(lead, 0));
+        if (__all_sync(0xffffffffu, !in[k] || digit == one)) {
+          if (lane == lead) atomicAdd(hist + one, __popc(who));
+        } else if (in[k]) {
+          atomicAdd(hist + digit, 1u);
+        }
       }
     }
     if (cluster > 1) {
@@ -119,11 +144,13 @@ __global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_
     // thread t has bins 4 t .. of all CTAs, counted from the largest digit down
     uint4 n = make_uint4(0, 0, 0, 0);
     const int at = kBins - 4 - 4 * tid;
-    if (at < bins)
+    if (at < bins) {
+#pragma unroll 4
       for (int r = 0; r < cluster; ++r) {
         const uint4 x = cluster > 1 ? ld_peer4(peer_addr(hist + at, r)) : *reinterpret_cast<const uint4*>(hist + at);
         n.x += x.x, n.y += x.y, n.z += x.z, n.w += x.w;
       }
+    }
     const unsigned sum = n.x + n.y + n.z + n.w;
     unsigned up = sum;
 #pragma unroll
@@ -150,13 +177,16 @@ __global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_
   }
 
   // ---- the list: tokens above the cut, and the first `want` of those at it ----
+  const int q0 = warp * (run / kQuad), q1 = min(quads, q0 + run / kQuad);
   unsigned above = 0, equal = 0;                  // of this warp's run
-  const int w0 = warp * run, w1 = min(mine, w0 + run);
-  for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const unsigned key = i < w1 ? key_of(i) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i < w1 && key > cut));
-    equal += __popc(__ballot_sync(0xffffffffu, i < w1 && key == cut));
+  for (int q = q0 + lane; q < q1; q += 32) {
+    unsigned key[kQuad];
+    bool have[kQuad];
+    keys(q, key, have);
+#pragma unroll
+    for (int k = 0; k < kQuad; ++k) above += have[k] && key[k] > cut, equal += have[k] && key[k] == cut;
   }
+  above = __reduce_add_sync(0xffffffffu, above), equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) s_above[warp] = above, s_equal[warp] = equal;
   __syncthreads();
   if (tid == 0) {
@@ -167,21 +197,35 @@ __global__ void __launch_bounds__(kSelThreads) q4_kv_select_kernel(const __grid_
   unsigned taken = 0, passed = 0;                 // tokens above and at the cut before this warp's
   if (cluster > 1) {
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      taken += ld_peer(peer_addr(&s_count.x, r));
-      passed += ld_peer(peer_addr(&s_count.y, r));
-    }
+    const bool earlier = lane < rank;             // a lane for each of them
+    taken = __reduce_add_sync(0xffffffffu, earlier ? ld_peer(peer_addr(&s_count.x, lane)) : 0u);
+    passed = __reduce_add_sync(0xffffffffu, earlier ? ld_peer(peer_addr(&s_count.y, lane)) : 0u);
   }
   for (int i = 0; i < warp; ++i) taken += s_above[i], passed += s_equal[i];
-  for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const unsigned key = i < w1 ? key_of(i) : 0u;
-    const unsigned up = __ballot_sync(0xffffffffu, i < w1 && key > cut), at = __ballot_sync(0xffffffffu, i < w1 && key == cut);
-    const unsigned below = (1u << lane) - 1u;
-    const unsigned equals = passed + __popc(at & below);   // before this token
-    if ((up >> lane & 1u) || ((at >> lane & 1u) && equals < want))
-      kept[head + taken + __popc(up & below) + min(equals, want)] = head + from + i;
-    taken += __popc(up);
-    passed += __popc(at);
+  for (int q = q0 + lane; q - lane < q1; q += 32) {
+    unsigned key[kQuad];
+    bool have[kQuad];
+    keys(q, key, have);
+    if (q >= q1) have[0] = have[1] = have[2] = have[3] = false;
+    unsigned mine_up = 0;                         // tokens above and, in the upper half, at the cut: of this lane's four
+#pragma unroll
+    for (int k = 0; k < kQuad; ++k) mine_up += (have[k] && key[k] > cut ? 1u : 0u) + (have[k] && key[k] == cut ? 0x10000u : 0u);
+    unsigned up = mine_up;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += x;
+    }
+    unsigned a = taken + ((up - mine_up) & 0xffffu), e = passed + ((up - mine_up) >> 16);
+#pragma unroll
+    for (int k = 0; k < kQuad; ++k) {
+      const bool over = have[k] && key[k] > cut, at = have[k] && key[k] == cut;
+      if (over || (at && e < want)) kept[head + a + min(e, want)] = base + from + q * kQuad + k;
+      a += over, e += at;
+    }
+    const unsigned whole = __shfl_sync(0xffffffffu, up, 31);
+    taken += whole & 0xffffu;
+    passed += whole >> 16;
   }
   if (cluster > 1) cluster_sync();                // the counts are read by the peers
 }
@@ -336,10 +380,11 @@ cudaError_t launch_kv_select(const KvSelectParams& p, long long max_kv, int sms,
   const long long pairs = static_cast<long long>(p.B) * p.c.heads;
   // as many CTAs for a (sequence, head) as fill the GPU, or hold its tokens in shared memory, up to eight
   int cluster = 1;
-  while (cluster < kMostCluster && (pairs * cluster < 4LL * sms || max_kv > static_cast<long long>(cluster) * kSelTokens) &&
+  while (cluster < kMostCluster && (pairs * cluster < sms || max_kv > static_cast<long long>(cluster) * kSelTokens) &&
          max_kv > cluster * 1024LL)
     cluster *= 2;
-  const long long each = ((max_kv + cluster * kSelThreads - 1) / (cluster * kSelThreads)) * kSelThreads;
+  const long long step = static_cast<long long>(cluster) * kSelThreads * kQuad;
+  const long long each = (max_kv + kQuad + step - 1) / step * kSelThreads * kQuad;
   const int cap = static_cast<int>(std::min<long long>(each, kSelTokens));
   const size_t smem = (3 * kBins + static_cast<size_t>(cap)) * 4;
   static std::atomic<unsigned long long> allowed;
