@@ -94,6 +94,10 @@ size_t kv_attn_split_bytes(int dim, int sms);
 // head), and zeros for rows of no sequence.  max_q: new tokens of a sequence at most.
 cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, void* ws, int sms,
                                  cudaStream_t st);
+// On the tensor cores, split over the cached tokens: sequences with at most max_rows query rows, and zeros for rows of
+// no sequence; bf16 q and out.  Workspace as for the split form, of kv_draft_bytes.
+size_t kv_draft_bytes(int dim, int sms);
+cudaError_t launch_kv_draft(const KvAttnCall& a, int max_rows, void* ws, int sms, cudaStream_t st);
 // Sequences with more than split_rows query rows (0: all, and zeros for rows of no
 // sequence); bf16 q and out.  rows: rows of fp16 keys and values the workspace holds (kv_prompt_rows).
 long long kv_prompt_rows(int B, long long max_kv, long long total_kv);

@@ -1,0 +1,656 @@
+// Attention over the paged 8-bit cache on the tensor cores, split over the
+// cached tokens (sm_103a): the form for some tens to hundreds of query rows a
+// sequence, as drafts of several tokens have, with bf16 queries and results.
+//
+//   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
+//
+// 128 rows against each code: too many to widen the codes for every 16 of them
+// (the split form), too few to write the codes out as fp16 first (the prompt
+// form), and too few CTAs if each walks over all of a sequence.  So:
+//
+// * The unit of work is a tile of 128 tokens of a kv head for up to 128 query
+//   rows (token-major).  The units of all sequences form one line, with some
+//   empty ones before each (sequence, rows, head) for what starting one costs,
+//   that is cut evenly over the CTAs; shares of what was cut are joined by the
+//   last CTA to have one.
+// * In a CTA four warps take codes from the pages to registers, a tile ahead,
+//   and put them as exact fp16 into shared memory in the order of the MMA's
+//   operands; one warp issues the MMAs; four warps (a thread a row) turn
+//   scores into weights.  Two tiles of scores take turns in tensor memory, so
+//   that the next one's products run beside a tile's softmax.
+// * Scales are applied in fp32: a block's key scale is part of the factor of
+//   its scores, its value scale multiplies the weight before that is rounded
+//   to fp16, relative to a power of two above the scales that the row has seen.
+#include <algorithm>
+#include <cfloat>
+
+#include "q4_kernels.h"
+#include "q4_kv_device.cuh"
+#include "q4_kv_tc.cuh"
+
+namespace q4 {
+namespace {
+
+using namespace gemm;
+
+constexpr int kTile = 128;                // tokens and query rows of a tile
+constexpr int kThreads = 384;             // 4 softmax warps, 4 that widen codes, one that issues MMAs and three idle ones
+constexpr int kWidenWarp = 4, kMmaWarp = 8;
+// registers a thread: 384 x 168 at launch
+constexpr int kSoftmaxRegs = 216, kWidenRegs = 144, kOtherRegs = 56;
+static_assert(128 * (kSoftmaxRegs + kWidenRegs + kOtherRegs) <= kThreads * 168, "the shares must fit the launch's registers");
+constexpr int kStages = 2;                // of keys, and of values
+constexpr int kRecs = 4;                  // records of tiles: a tile's is in use until its weights are
+constexpr int kBlocks = kTile / kKvBlock;
+constexpr int kSegCost = 3;               // what starting a (sequence, rows, head) costs, in tiles
+constexpr float kLazy = 8.0f;             // the reference moves once a score exceeds it by 2^kLazy
+constexpr float kUnit = 7.0f;             // weights are 2^7 at the reference: up to 2^15, below fp16's 65504
+constexpr int kNoScale = -1024;           // exponent of blocks whose values are all zero
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct DraftParams {
+  KvAttnCall a;
+  int group, max_rows;       // sequences with more query rows are left to the prompt form
+  unsigned* tickets;         // [ranges], zero
+  float* part;               // [ranges][2][kTile][D + 4] shares: sums, their maximum, weights' sum and exponent
+};
+
+// What the softmax needs of a tile of tokens.
+struct Rec {
+  float ks[kBlocks], vs[kBlocks];
+  uint16_t seen[kBlocks];    // tokens of each block that exist
+};
+
+// One (sequence, rows, head) of the line, and the tiles a CTA takes of it.
+struct Segment {
+  int b, h, rows0;
+  int c0, nq, len;
+  int first, stay;           // tiles of the sinks, [0, stay), come before those from `first` on
+  int start;                 // first token that a window leaves
+  int lo, hi;                // this CTA's tiles of these (maybe none)
+  long long from, to;        // units of the whole: [from, to)
+  __device__ __forceinline__ int tile(int i) const { return i < stay ? i : i - stay + first; }
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalf = kTile * 128;             // 128 rows of 64 fp16: a swizzled box
+  static constexpr int kTileBytes = kHalf * (D / 64);
+  static constexpr size_t smem(int B) { return 1024 + (1 + 2 * kStages) * kTileBytes + 256 + static_cast<size_t>(B + 1) * 8; }
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kIdescQk = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t kIdescPv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
+};
+
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 + max(-126, min(127, e))) << 23);
+}
+__device__ __forceinline__ uint32_t columns_to(int n) { return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1u; }
+__device__ __forceinline__ uint32_t tree_word(const KvAttnCall& a, long long row, int i) {
+  return i >= 0 && i < a.tree_words ? static_cast<uint32_t>(__ldg(a.tree + row * a.tree_words + i)) : 0u;
+}
+// Barrier of the softmax warps.
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTile) : "memory"); }
+
+// The tiles that the queries of a sequence see something of, at least one.
+__device__ __forceinline__ void seq_tiles(const KvAttnCall& a, int nq, int len, int& start, int& first, int& stay, int& n) {
+  const long long f = a.window > 0 ? static_cast<long long>(len) - nq - a.window + (a.tree ? 0 : 1) : 0;
+  start = f > 0 ? static_cast<int>(f) : 0;
+  const int hi = max(1, (max(len, 0) + kTile - 1) / kTile);
+  first = min(start / kTile, hi - 1);
+  stay = static_cast<int>(min(static_cast<long long>(first), (a.sinks + kTile - 1) / kTile));
+  n = stay + hi - first;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_constant__ DraftParams p) {
+  using C = Cfg<D>;
+  constexpr int kParts = D / 16, kEach = kTile * kParts / 128;   // 16-byte parts of a row; of a tile, that a thread widens
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sk = sq + C::kTileBytes;
+  uint8_t* sv = sk + kStages * C::kTileBytes;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sv + kStages * C::kTileBytes);
+  uint64_t* k_empty = k_full + kStages;
+  uint64_t* v_full = k_empty + kStages;
+  uint64_t* v_empty = v_full + kStages;
+  uint64_t* s_full = v_empty + kStages;  // [2] scores of a tile are in tensor memory
+  uint64_t* p_ready = s_full + 2;        // [2] its weights are, and the sums rescaled
+  uint64_t* o_done = p_ready + 2;        // the sums include the latest weights
+  uint64_t* q_ready = o_done + 1;
+  uint64_t* drain = q_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  long long* s_cum = reinterpret_cast<long long*>(sv + kStages * C::kTileBytes + 256);   // [B + 1] first unit of each sequence
+  __shared__ __align__(16) Rec s_rec[kRecs];
+  __shared__ long long s_warp[kThreads / 32];
+  __shared__ int s_fail, s_last;
+
+  const KvAttnCall& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i)
+      mbar_init(&k_full[i], 128), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], 128), mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kTile);
+    mbar_init(o_done, 1), mbar_init(q_ready, kTile), mbar_init(drain, 1);
+    s_fail = 0;
+  }
+  fence_barrier_init();
+  pdl_wait();   // before tensor memory is taken: the kernel before may need this SM's
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
+
+  // ---- the line of units ----
+  {
+    const int per = (B + kThreads - 1) / kThreads;
+    long long sum = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < B) {
+        const int nq = a.b.cu[b + 1] - a.b.cu[b];
+        const long long rows = static_cast<long long>(nq) * p.group;
+        int start, first, stay, n;
+        seq_tiles(a, nq, a.b.kv_len[b], start, first, stay, n);
+        if (nq > 0 && rows <= p.max_rows) sum += (rows + kTile - 1) / kTile * a.c.heads * (n + kSegCost);
+        s_cum[b + 1] = sum;
+      }
+    }
+    long long up = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += x;
+    }
+    if (lane == 31) s_warp[warp] = up;
+    __syncthreads();
+    long long before = up - sum;
+    for (int i = 0; i < warp; ++i) before += s_warp[i];
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < B) s_cum[b + 1] += before;
+    }
+    if (tid == 0) s_cum[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_s[2] = {tmem, tmem + kTile}, t_o = tmem + 2 * kTile;
+  const long long units = s_cum[B];
+  const long long ranges = max(1LL, min(static_cast<long long>(gridDim.x), units / (kSegCost + 1)));
+  auto range_of = [&](long long i) { return units / ranges * i + min(i, units % ranges); };
+  // the range that holds unit u
+  auto owner_of = [&](long long u) {
+    const long long q = units / ranges, r = units % ranges;
+    return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
+  };
+  const long long range = blockIdx.x;
+  const long long u0 = range < ranges ? range_of(range) : units, u1 = range < ranges ? range_of(range + 1) : units;
+
+  auto locate = [&](long long u, Segment& s) {
+    int lo = 0, hi = B - 1;                     // the last b with s_cum[b] <= u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_cum[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    s.b = lo;
+    s.c0 = a.b.cu[lo];
+    s.nq = a.b.cu[lo + 1] - s.c0;
+    s.len = a.b.kv_len[lo];
+    int n;
+    seq_tiles(a, s.nq, s.len, s.start, s.first, s.stay, n);
+    const int each = n + kSegCost;
+    const long long pair = (u - s_cum[lo]) / each;
+    s.h = static_cast<int>(pair % a.c.heads);
+    s.rows0 = static_cast<int>(pair / a.c.heads) * kTile;
+    s.from = s_cum[lo] + pair * each;
+    s.to = s.from + each;
+    s.lo = max(0, static_cast<int>(u - s.from) - kSegCost);
+    s.hi = max(0, static_cast<int>(min(s.to, u1) - s.from) - kSegCost);
+  };
+
+  if (warp >= kWidenWarp && warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
+    // ================= codes to fp16 tiles =================
+    const int w = tid - kWidenWarp * 32;
+    Segment s = {};
+    long long u = u0;
+    int i = 0;
+    bool more = u0 < u1;
+    auto settle = [&]() {                       // to the next tile there is
+      while (i >= s.hi) {
+        if (u >= u1) {
+          more = false;
+          return;
+        }
+        locate(u, s);
+        u = s.to;
+        i = s.lo;
+      }
+    };
+    // A lane looks up one of the next tile's eight blocks; its tokens; and has their scales on their way.
+    int at = -1;
+    float ks = 0.f, vs = 0.f;
+    unsigned seen = 0;
+    auto look_up = [&]() {
+      at = -1, seen = 0, ks = 0.f, vs = 0.f;
+      if (!more || lane >= kBlocks) return;
+      const int pos = s.tile(i) * kTile + lane * kKvBlock;
+      if (pos >= s.len || (pos + kKvBlock <= s.start && pos >= a.sinks)) return;
+      const long long row = kv_row(a.c, a.b.table, a.b.table_stride, s.b, pos, s.h);
+      if (row < 0) {
+        if (w < 32) atomicOr(a.err, kDevErrIndex);
+        return;
+      }
+      at = static_cast<int>(row >> 4);
+      seen = 0xffffu >> (kKvBlock - min(kKvBlock, s.len - pos));
+      ks = __ldg(a.c.ks + at), vs = __ldg(a.c.vs + at);
+    };
+    // this thread's parts of the tile: part w % kParts of every (128 / kParts)th token from w / kParts on
+    auto load = [&](const int8_t* codes, uint4 (&x)[kEach]) {
+#pragma unroll
+      for (int n = 0; n < kEach; ++n) {
+        const int token = n * (128 / kParts) + w / kParts;
+        const int blk = __shfl_sync(0xffffffffu, at, token >> 4);
+        x[n] = blk >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + static_cast<long long>(blk) * (kKvBlock * D) +
+                                                               (token & (kKvBlock - 1)) * D + w % kParts * 16))
+                        : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto put = [&](uint8_t* to, const uint4 (&x)[kEach]) {
+      const int part = w % kParts, half = part >> 2;
+#pragma unroll
+      for (int n = 0; n < kEach; ++n) {
+        const int token = n * (128 / kParts) + w / kParts;
+        uint4 f[2];
+        widen4(x[n].x, f[0].x, f[0].y), widen4(x[n].y, f[0].z, f[0].w);
+        widen4(x[n].z, f[1].x, f[1].y), widen4(x[n].w, f[1].z, f[1].w);
+        uint8_t* row = to + half * C::kHalf + token * 128;
+        const int c = (2 * part & 7) ^ (token & 7);
+        // the halves' lanes begin with different ones: no bank twice
+        *reinterpret_cast<uint4*>(row + ((c ^ half) << 4)) = half ? f[1] : f[0];
+        *reinterpret_cast<uint4*>(row + ((c ^ 1 ^ half) << 4)) = half ? f[0] : f[1];
+      }
+      fence_async_smem();
+    };
+    uint4 kc[kEach], vc[kEach];
+    if (more) settle();
+    look_up();
+    load(a.c.k, kc);
+    load(a.c.v, vc);
+    bool ok = true;
+    for (int it = 0; more; ++it) {
+      const int st = it % kStages;
+      const float my_ks = ks, my_vs = vs;
+      const unsigned my_seen = seen;
+      ++i;
+      settle();
+      look_up();                                // of the next tile
+      if (it >= kStages) ok = __all_sync(0xffffffffu, gwait(&k_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err));
+      if (!ok) break;
+      if (w < kBlocks) {
+        Rec& r = s_rec[it % kRecs];
+        r.ks[w] = my_ks, r.vs[w] = my_vs, r.seen[w] = static_cast<uint16_t>(my_seen);
+      }
+      put(sk + st * C::kTileBytes, kc);
+      mbar_arrive(&k_full[st]);
+      load(a.c.k, kc);
+      if (it >= kStages) ok = __all_sync(0xffffffffu, gwait(&v_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err));
+      if (!ok) break;
+      put(sv + st * C::kTileBytes, vc);
+      mbar_arrive(&v_full[st]);
+      load(a.c.v, vc);
+    }
+  } else if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp) {
+      const uint32_t leader = elect_one();
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return poll_wait(bar, parity, &s_fail, a.err); };
+      const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 1024, kSwizzle128);
+      const uint64_t k_desc = smem_desc(smem_u32(sk), 16, 1024, kSwizzle128);
+      const uint64_t v_desc = smem_desc(smem_u32(sv), C::kHalf, 1024, kSwizzle128);
+      auto qk = [&](int it) {
+        const int st = it % kStages;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int off = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
+          lead_mma(leader, t_s[it & 1], q_desc + off, k_desc + (st * C::kTileBytes >> 4) + off, C::kIdescQk, kk > 0 ? 1u : 0u);
+        }
+        lead_commit(leader, &s_full[it & 1]);
+        lead_commit(leader, &k_empty[st]);
+      };
+      int it = 0, segs = 0;                     // tiles and (sequence, rows, head)s so far
+      bool ok = true;
+      Segment s;
+      for (long long u = u0; ok && u < u1; u = s.to) {
+        locate(u, s);
+        const int n = s.hi - s.lo;
+        if (n <= 0) continue;
+        ok = wait(q_ready, segs++ & 1) && wait(&k_full[it % kStages], (it / kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        qk(it);
+        for (int i = 0; i < n; ++i, ++it) {
+          if (i + 1 < n) {
+            ok = wait(&k_full[(it + 1) % kStages], ((it + 1) / kStages) & 1);
+            if (!ok) break;
+            qk(it + 1);
+          }
+          ok = wait(&p_ready[it & 1], (it >> 1) & 1) && wait(&v_full[it % kStages], (it / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            lead_mma_ts(leader, t_o, t_s[it & 1] + kk * 8, v_desc + ((it % kStages) * C::kTileBytes >> 4) + kk * (2048 >> 4),
+                        C::kIdescPv, kk > 0 || i > 0 ? 1u : 0u);
+          lead_commit(leader, o_done);
+          lead_commit(leader, &v_empty[it % kStages]);
+        }
+      }
+      // no MMA may still run when the tensor memory is freed
+      lead_commit(leader, drain);
+      (void)mbar_wait(drain, 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ================= softmax: a thread a row =================
+    const int r = tid;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    int it = 0;
+    bool ok = true;
+    Segment s;
+    for (long long u = u0; ok && u < u1; u = s.to) {
+      locate(u, s);
+      const int n = s.hi - s.lo, row = s.rows0 + r, j = row / p.group, head = s.h * p.group + row % p.group;
+      const long long t = static_cast<long long>(s.c0) + j;
+      const bool have = j < s.nq && s.c0 >= 0 && t < a.b.T;
+      const int base = s.len - s.nq;
+      float rowc = 0.f;
+      int qpos = base + j;
+      if (n > 0) {
+        // the row as fp16, scaled by a power of two; the sign of `scale` goes with it
+        uint4 w[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        if (have) {
+          const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.q_stride + head * D);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) w[i] = __ldg(q + i);
+          if (a.tree) {   // as many new tokens as its path has; they are seen by their bits alone
+            int path = 0;
+            for (int i = 0; i < s.nq; i += 32) path += __popc(tree_word(a, t, i >> 5) & columns_to(s.nq - 1 - i));
+            qpos = base + path - 1;
+          }
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = max(m, max(x[k] << 16 & 0x7fffffffu, x[k] & 0x7fff0000u));
+        }
+        const int e = m ? max(-126, min(126, 13 + 127 - static_cast<int>(m >> 23))) : 0;
+        const float f = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), a.scale);
+        rowc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(a.scale) * kLog2e;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          __half2 y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = __floats2half2_rn(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
+          *reinterpret_cast<uint4*>(sq + (i >> 3) * C::kHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = *reinterpret_cast<uint4*>(y);
+        }
+        fence_async_smem();
+        mbar_arrive(q_ready);
+      }
+      // positions the row sees: (from, to]; one that does not exist sees all, so that no tile is on its edge
+      const int to = !have ? 0x7fffffff : a.tree ? base - 1 : a.causal ? qpos : s.len - 1;
+      const long long lowest = have && a.window > 0 ? static_cast<long long>(qpos) - a.window : -1LL;
+      const int from = lowest < -1 ? -1 : static_cast<int>(lowest);
+      float m = -INFINITY, l = 0.f;
+      int e = kNoScale;             // the sums are relative to 2^e, above the value scales that the row has seen
+      for (int i = 0; i < n; ++i, ++it) {
+        const int t0 = s.tile(s.lo + i) * kTile;
+        ok = __all_sync(0xffffffffu, gwait(&s_full[it & 1], (it >> 1) & 1, &s_fail, a.err));
+        if (!ok) break;
+        tc_fence_after();
+        const Rec& rec = s_rec[it % kRecs];
+        const uint4 exist = *reinterpret_cast<const uint4*>(rec.seen);
+        uint32_t bits[4] = {exist.x, exist.y, exist.z, exist.w};
+        const bool mine = t0 + kTile - 1 > to || (t0 <= from && t0 + kTile > a.sinks) || (bits[0] & bits[1] & bits[2] & bits[3]) != ~0u;
+        const bool edge = __any_sync(0xffffffffu, mine);
+        uint32_t v[kTile];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld32_async(t_s[it & 1] + lanes + 32 * x, v + 32 * x);
+        float mul[kBlocks];         // a block's scores to powers of two
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) mul[k] = rec.ks[k] * rowc;
+        tmem_wait_ld();
+        if (edge) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int at = t0 + 32 * x;
+            uint32_t see = columns_to(to - at) & ~columns_to(from - at);
+            if (at < a.sinks) see |= columns_to(to - at) & columns_to(static_cast<int>(min(a.sinks - at, 32LL)) - 1);
+            if (a.tree && have) {
+              const int k = at - base;   // place among the new tokens
+              see |= __funnelshift_r(tree_word(a, t, k >> 5), tree_word(a, t, (k >> 5) + 1), k & 31);
+            }
+            bits[x] &= see;
+          }
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (!((bits[c >> 5] >> (c & 31)) & 1u)) v[c] = 0xff800000u;
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k) mul[k] = fmaxf(mul[k], 1e-30f);   // masked scores stay -inf
+        }
+        float now = -INFINITY;
+        int te = kNoScale;          // of the blocks that the row sees something of
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+          float top = __uint_as_float(v[kKvBlock * k]);
+#pragma unroll
+          for (int c = 1; c < kKvBlock; ++c) top = fmaxf(top, __uint_as_float(v[kKvBlock * k + c]));
+          now = fmaxf(now, top * mul[k]);
+          const float scale = rec.vs[k];
+          if (top > -INFINITY && scale > 0.f) te = max(te, max(-126, min(126, static_cast<int>(__float_as_uint(scale) >> 23) - 126)));
+        }
+        if (__any_sync(0xffffffffu, now > m + kLazy || te > e)) {   // also from -inf
+          const float next = fmaxf(m, now);
+          const float k = next > -INFINITY ? ex2(m - next) : 1.f;
+          m = next;
+          l *= k;
+          const float ko = k * power_of_two(e - max(e, te));
+          e = max(e, te);
+          if (i > 0) {
+            ok = __all_sync(0xffffffffu, gwait(o_done, (it - 1) & 1, &s_fail, a.err));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32_async(t_o + lanes + 32 * x, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * ko);
+              tmem_st32(t_o + lanes + 32 * x, o);
+            }
+          }
+        }
+        const f32x2 off2 = dup2(m > -INFINITY ? kUnit - m : 0.f);
+        const float unit = power_of_two(-e);   // 2^e is above the scales: a weight stays below 2^15
+        f32x2 sum2[2] = {0ull, 0ull};
+        uint32_t w[kTile / 2];
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+          const f32x2 f = dup2(mul[k]), vk = dup2(fminf(rec.vs[k] * unit, 1.f));   // larger: a block that the row does not see
+#pragma unroll
+          for (int c = k * kKvBlock / 2; c < (k + 1) * kKvBlock / 2; ++c) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), f, off2), x, y);
+            const f32x2 two = pack2(ex2(x), ex2(y));
+            sum2[c & 1] = add2(sum2[c & 1], two);
+            unpack2(mul2(two, vk), x, y);
+            const __half2 z = __floats2half2_rn(x, y);
+            w[c] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+        }
+        tmem_st32(t_s[it & 1] + lanes, w);
+        tmem_st32(t_s[it & 1] + lanes + 32, w + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_ready[it & 1]);
+        float x, y;
+        unpack2(add2(sum2[0], sum2[1]), x, y);
+        l += x + y;
+      }
+      if (ok && n > 0) ok = __all_sync(0xffffffffu, gwait(o_done, (it - 1) & 1, &s_fail, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = s.from >= u0 && s.to <= u1;
+      constexpr int kShare = kTile * (D + 4);
+      if (whole) {
+        const float k = l > 0.f ? power_of_two(e) / l : l == 0.f ? 0.f : l;   // a row that sees nothing: zeros; a NaN stays
+        if (a.lse && have) a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l) - kUnit) * kLn2 : l == 0.f ? -INFINITY : l;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t o[32];
+          tmem_ld32_async(t_o + lanes + 32 * x, o);
+          tmem_wait_ld();
+          if (have) {
+            uint4* to4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (t * a.Hq + head) * D + 32 * x);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              __nv_bfloat162 y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * i]) * k, __uint_as_float(o[8 * c + 2 * i + 1]) * k);
+              to4[c] = *reinterpret_cast<uint4*>(y);
+            }
+          }
+        }
+        tc_fence_before();
+        continue;
+      }
+      // partial sums: slot 0 for what began in an earlier CTA, 1 for what begins here
+      float* slot = p.part + (range * 2 + (s.from >= u0 ? 1 : 0)) * kShare + r * (D + 4);
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32_async(t_o + lanes + 32 * x, o);
+          tmem_wait_ld();
+        }
+        if (have) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            *reinterpret_cast<uint4*>(slot + 32 * x + c) = n > 0 ? make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      tc_fence_before();
+      if (have) *reinterpret_cast<float4*>(slot + D) = make_float4(m, l, __int_as_float(e), 0.f);
+      rows_sync();
+      const long long o0 = owner_of(s.from), o1 = owner_of(s.to - 1);
+      if (tid == 0) {
+        const unsigned old = atom_add_acq_rel_gpu(p.tickets + o0, 1u);
+        s_last = old == static_cast<unsigned>(o1 - o0);
+        if (s_last) p.tickets[o0] = 0;
+      }
+      rows_sync();
+      if (s_last && have) {
+        const int shares = static_cast<int>(o1 - o0) + 1;
+        auto share = [&](int i) { return p.part + ((o0 + i) * 2 + (i == 0 ? 1 : 0)) * kShare + r * (D + 4); };
+        float mm = -INFINITY;
+        int ee = kNoScale;
+        for (int i = 0; i < shares; ++i) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(share(i) + D));
+          mm = fmaxf(mm, x.x), ee = max(ee, __float_as_int(x.z));
+        }
+        float ll = 0.f;
+        for (int i = 0; i < shares; ++i) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(share(i) + D));
+          ll += x.x > -INFINITY ? x.y * ex2(x.x - mm) : x.y;   // without a key: 0
+        }
+        const float k = ll > 0.f ? power_of_two(ee) / ll : ll == 0.f ? 0.f : ll;
+        if (a.lse) a.lse[t * a.Hq + head] = ll > 0.f ? (mm + log2f(ll) - kUnit) * kLn2 : ll == 0.f ? -INFINITY : ll;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float4 y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+          for (int i = 0; i < shares; ++i) {
+            const float* from_share = share(i);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(from_share + D));
+            const float f = x.x > -INFINITY ? ex2(x.x - mm) * power_of_two(__float_as_int(x.z) - ee) : 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 z = __ldcg(reinterpret_cast<const float4*>(from_share + c + 4 * q));
+              y[q].x = fmaf(f, z.x, y[q].x), y[q].y = fmaf(f, z.y, y[q].y);
+              y[q].z = fmaf(f, z.z, y[q].z), y[q].w = fmaf(f, z.w, y[q].w);
+            }
+          }
+          uint4* to4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (t * a.Hq + head) * D + c);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            __nv_bfloat162 z[4] = {__floats2bfloat162_rn(y[2 * q].x * k, y[2 * q].y * k), __floats2bfloat162_rn(y[2 * q].z * k, y[2 * q].w * k),
+                                   __floats2bfloat162_rn(y[2 * q + 1].x * k, y[2 * q + 1].y * k),
+                                   __floats2bfloat162_rn(y[2 * q + 1].z * k, y[2 * q + 1].w * k)};
+            to4[q] = *reinterpret_cast<uint4*>(z);
+          }
+        }
+      }
+    }
+  }
+  // rows of no sequence: zeros
+  const long long end = max(0, min(a.b.T, a.b.cu[B])), row_elems = static_cast<long long>(a.Hq) * D;
+  const long long mine = static_cast<long long>(blockIdx.x) * kThreads + tid, step = static_cast<long long>(gridDim.x) * kThreads;
+  for (long long i = end * row_elems / 8 + mine; i < a.b.T * row_elems / 8; i += step)
+    static_cast<uint4*>(a.out)[i] = make_uint4(0, 0, 0, 0);
+  if (a.lse)
+    for (long long i = end * a.Hq + mine; i < static_cast<long long>(a.b.T) * a.Hq; i += step) a.lse[i] = -INFINITY;
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch(const DraftParams& p, int sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> allowed;
+  cudaError_t e = allow_smem(q4_kv_draft_kernel<D>, Cfg<D>::smem(kKvMaxSeqs), allowed);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<D>::smem(p.a.b.B);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q4_kv_draft_kernel<D>, p);
+}
+
+}  // namespace
+
+size_t kv_draft_bytes(int dim, int sms) {
+  return kv_attn_header_bytes() + static_cast<size_t>(sms) * 2 * kTile * (dim + 4) * 4;
+}
+
+cudaError_t launch_kv_draft(const KvAttnCall& a, int max_rows, void* ws, int sms, cudaStream_t st) {
+  if (static_cast<size_t>(sms) * sizeof(unsigned) > kv_attn_header_bytes()) return cudaErrorInvalidConfiguration;
+  DraftParams p = {};
+  p.a = a;
+  p.group = a.Hq / a.c.heads;
+  p.max_rows = max_rows;
+  p.tickets = static_cast<unsigned*>(ws);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
+  return a.c.dim == 128 ? launch<128>(p, sms, st) : launch<64>(p, sms, st);
+}
+
+}  // namespace q4

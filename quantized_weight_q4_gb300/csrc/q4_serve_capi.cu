@@ -1,5 +1,6 @@
 // C ABI of the serving operators (include/q4.h): the paged 8-bit cache,
 // attention over it, and sampling.  Argument checks and workspaces.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -178,20 +179,29 @@ int64_t most_prompt_tokens(int dim, int64_t rows) {
 }
 
 struct AttnPlan {
+  bool draft;           // the draft form takes the split form's place
   bool prompt;          // the call may have sequences for the prompt form
-  int split_rows;       // query rows up to which a sequence takes the split form
+  int split_rows;       // query rows up to which a sequence takes the split form, or the draft form
   long long rows;       // fp16 rows of the prompt form
   size_t split_bytes, total;
 };
 
-// sized: with room for the prompt form wherever a call of these bounds, or of smaller ones, takes it
+// Query rows up to which a sequence of a call with sinks, drafts or sums to give takes the draft form, where more than
+// kRowTile may come.
+constexpr int kMostDraftRows = 1024;
+
+// more: with sinks, a tree or sums to give.  sized: with room for every form that a call of these bounds, or of smaller
+// ones, takes, whatever it has of these.
 AttnPlan attn_plan(const q4::KvView& c, int64_t Hq, int64_t B, int64_t T, int64_t max_q, int64_t max_kv,
-                   int64_t total_kv, bool bf16, bool sized, int sms) {
+                   int64_t total_kv, bool bf16, bool more, bool sized, int sms) {
   AttnPlan p = {};
   const int64_t most_rows = (max_q < T ? max_q : T) * (Hq / c.heads);
-  p.split_rows = sized ? kRowTile : split_rows_of(c, B, max_kv, sms);
+  p.draft = bf16 && more && most_rows > kRowTile;
+  p.split_rows = sized ? kRowTile : p.draft ? kMostDraftRows : split_rows_of(c, B, max_kv, sms);
   p.prompt = bf16 && most_rows > p.split_rows;
-  p.split_bytes = (q4::kv_attn_split_bytes(c.dim, sms) + 255) / 256 * 256;
+  p.split_bytes = q4::kv_attn_split_bytes(c.dim, sms);
+  if (most_rows > kRowTile && (sized || p.draft)) p.split_bytes = std::max(p.split_bytes, q4::kv_draft_bytes(c.dim, sms));
+  p.split_bytes = (p.split_bytes + 255) / 256 * 256;
   p.total = p.split_bytes;
   if (p.prompt) {
     const int64_t longest = sized ? most_prompt_tokens(c.dim, most_rows) : max_kv;
@@ -212,7 +222,7 @@ size_t q4_kv_attention_workspace_size(const q4_kv_cache* cache, int64_t Hq, int6
   int sms = 0;
   unsigned* status = nullptr;
   if (q4::device_info(&sms, &status) != Q4_OK) return 0;
-  return attn_plan(v, Hq, B, T, max_q, max_kv, total_kv, true, true, sms).total;
+  return attn_plan(v, Hq, B, T, max_q, max_kv, total_kv, true, true, true, sms).total;
 }
 
 int q4_kv_attention(void* out, int out_dtype, const void* q, int q_dtype, int64_t q_stride, int64_t Hq,
@@ -248,9 +258,14 @@ int q4_kv_attention_ex(void* out, int out_dtype, const void* q, int q_dtype, int
   int sms = 0;
   rc = q4::device_info(&sms, &a.err);
   if (rc != Q4_OK) return rc;
+  a.b = {page_table, table_stride, kv_len, cu_q, static_cast<int>(B), static_cast<int>(T)};
+  a.out = out, a.q = q, a.q_stride = q_stride, a.Hq = static_cast<int>(Hq);
+  a.q_bf16 = q_dtype == Q4_BF16, a.out_bf16 = out_dtype == Q4_BF16;
+  a.scale = scale, a.causal = causal, a.window = window;
+  a.sinks = sinks, a.tree = tree, a.tree_words = static_cast<int>(tree_words), a.lse = lse;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const AttnPlan plan = attn_plan(a.c, Hq, B, T, max_q, max_kv, total_kv,
-                                  q_dtype == Q4_BF16 && out_dtype == Q4_BF16, false, sms);
+                                  q_dtype == Q4_BF16 && out_dtype == Q4_BF16, q4::kv_attn_more(a), false, sms);
   if (plan.rows > 0x7fffffffLL) return Q4_ERR_SHAPE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   std::unique_lock<std::mutex> hold;
@@ -260,17 +275,15 @@ int q4_kv_attention_ex(void* out, int out_dtype, const void* q, int q_dtype, int
     ws = static_cast<uint8_t*>(q4::kv_stream_scratch(st, plan.total, hold));
     if (!ws) return Q4_ERR_WORKSPACE;
   }
-  a.b = {page_table, table_stride, kv_len, cu_q, static_cast<int>(B), static_cast<int>(T)};
-  a.out = out, a.q = q, a.q_stride = q_stride, a.Hq = static_cast<int>(Hq);
-  a.q_bf16 = q_dtype == Q4_BF16, a.out_bf16 = out_dtype == Q4_BF16;
-  a.scale = scale, a.causal = causal, a.window = window;
-  a.sinks = sinks, a.tree = tree, a.tree_words = static_cast<int>(tree_words), a.lse = lse;
   const int most = static_cast<int>(max_q < T ? max_q : T);
-  if (!plan.prompt) return status_of(q4::launch_kv_attn_split(a, most, 0x7fffffff, ws, sms, st));
+  const auto few = [&](int rows) {
+    return plan.draft ? q4::launch_kv_draft(a, rows, ws, sms, st) : q4::launch_kv_attn_split(a, most, rows, ws, sms, st);
+  };
+  if (!plan.prompt) return status_of(few(0x7fffffff));
   // one sequence: no second form beside the prompt's
   const int split_rows = B == 1 ? 0 : plan.split_rows;
   cudaError_t e = cudaSuccess;
-  if (B > 1) e = q4::launch_kv_attn_split(a, most, split_rows, ws, sms, st);
+  if (B > 1) e = few(split_rows);
   if (e == cudaSuccess) e = q4::launch_kv_prompt(a, split_rows, plan.rows, ws + plan.split_bytes, st);
   return status_of(e);
 }
