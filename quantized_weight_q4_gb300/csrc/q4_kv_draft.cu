@@ -13,8 +13,8 @@
 //   empty ones before each (sequence, rows, head) for what starting one costs,
 //   that is cut evenly over the CTAs; shares of what was cut are joined by the
 //   last CTA to have one.
-// * In a CTA four warps take codes from the pages to registers, a tile ahead,
-//   and put them as exact fp16 into shared memory in the order of the MMA's
+// * In a CTA eight warps take codes from the pages to registers, a tile ahead
+//   (and look up its blocks two tiles ahead), and put them as exact fp16 into shared memory in the order of the MMA's
 //   operands; one warp issues the MMAs; four warps (a thread a row) turn
 //   scores into weights.  Two tiles of scores take turns in tensor memory, so
 //   that the next one's products run beside a tile's softmax.
@@ -34,11 +34,11 @@ namespace {
 using namespace gemm;
 
 constexpr int kTile = 128;                // tokens and query rows of a tile
-constexpr int kThreads = 384;             // 4 softmax warps, 4 that widen codes, one that issues MMAs and three idle ones
-constexpr int kWidenWarp = 4, kMmaWarp = 8;
-// registers a thread: 384 x 168 at launch
-constexpr int kSoftmaxRegs = 216, kWidenRegs = 144, kOtherRegs = 56;
-static_assert(128 * (kSoftmaxRegs + kWidenRegs + kOtherRegs) <= kThreads * 168, "the shares must fit the launch's registers");
+constexpr int kThreads = 512;             // 4 softmax warps, 8 that widen codes, one that issues MMAs and three idle ones
+constexpr int kWidenWarp = 4, kWidenWarps = 8, kMmaWarp = 12, kWiden = kWidenWarps * 32;
+// registers a thread: 512 x 128 at launch
+constexpr int kSoftmaxRegs = 216, kWidenRegs = 104, kOtherRegs = 56;
+static_assert(128 * (kSoftmaxRegs + 2 * kWidenRegs + kOtherRegs) <= kThreads * 128, "the shares must fit the launch's registers");
 constexpr int kStages = 2;                // of keys, and of values
 constexpr int kRecs = 4;                  // records of tiles: a tile's is in use until its weights are
 constexpr int kBlocks = kTile / kKvBlock;
@@ -105,7 +105,7 @@ __device__ __forceinline__ void seq_tiles(const KvAttnCall& a, int nq, int len, 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_constant__ DraftParams p) {
   using C = Cfg<D>;
-  constexpr int kParts = D / 16, kEach = kTile * kParts / 128;   // 16-byte parts of a row; of a tile, that a thread widens
+  constexpr int kParts = D / 16, kEach = kTile * kParts / kWiden;   // 16-byte parts of a row; of a tile, that a thread widens
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sk = sq + C::kTileBytes;
@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   uint64_t* v_empty = v_full + kStages;
   uint64_t* s_full = v_empty + kStages;  // [2] scores of a tile are in tensor memory
   uint64_t* p_ready = s_full + 2;        // [2] its weights are, and the sums rescaled
-  uint64_t* o_done = p_ready + 2;        // the sums include the latest weights
-  uint64_t* q_ready = o_done + 1;
+  uint64_t* o_done = p_ready + 2;        // [2] the sums include its weights: two, as a row may wait for a tile while the
+  uint64_t* q_ready = o_done + 2;        //     one before it is not done
   uint64_t* drain = q_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   long long* s_cum = reinterpret_cast<long long*>(sv + kStages * C::kTileBytes + 256);   // [B + 1] first unit of each sequence
@@ -129,9 +129,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i)
-      mbar_init(&k_full[i], 128), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], 128), mbar_init(&v_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kTile);
-    mbar_init(o_done, 1), mbar_init(q_ready, kTile), mbar_init(drain, 1);
+      mbar_init(&k_full[i], kWiden), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], kWiden), mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kTile), mbar_init(&o_done[i], 1);
+    mbar_init(q_ready, kTile), mbar_init(drain, 1);
     s_fail = 0;
   }
   fence_barrier_init();
@@ -227,29 +227,41 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         i = s.lo;
       }
     };
-    // A lane looks up one of the next tile's eight blocks; its tokens; and has their scales on their way.
-    int at = -1;
+    // A lane looks up one of a tile's eight blocks: the page first, and a tile later, when it has come, the block's
+    // place, its tokens and its scales.
+    struct Block {
+      int page, sub;             // page of the table (-1: none), block in it
+      unsigned seen;
+    };
+    auto look_up = [&]() {       // of tile i
+      Block x = {-1, 0, 0};
+      if (!more || lane >= kBlocks) return x;
+      const int pos = s.tile(i) * kTile + lane * kKvBlock, pi = pos >> a.c.page_log2;
+      if (pos >= s.len || (pos + kKvBlock <= s.start && pos >= a.sinks)) return x;
+      x.seen = 0xffffu >> (kKvBlock - min(kKvBlock, s.len - pos));
+      x.sub = (s.h << (a.c.page_log2 - 4)) + ((pos & (a.c.page - 1)) >> 4);
+      x.page = pi < a.b.table_stride ? __ldg(a.b.table + s.b * a.b.table_stride + pi) : -1;
+      return x;
+    };
+    int at = -1;                 // of the tile whose codes are asked for next
     float ks = 0.f, vs = 0.f;
     unsigned seen = 0;
-    auto look_up = [&]() {
+    auto find = [&](const Block& x) {
       at = -1, seen = 0, ks = 0.f, vs = 0.f;
-      if (!more || lane >= kBlocks) return;
-      const int pos = s.tile(i) * kTile + lane * kKvBlock;
-      if (pos >= s.len || (pos + kKvBlock <= s.start && pos >= a.sinks)) return;
-      const long long row = kv_row(a.c, a.b.table, a.b.table_stride, s.b, pos, s.h);
-      if (row < 0) {
+      if (x.seen == 0) return;
+      if (static_cast<unsigned>(x.page) >= static_cast<unsigned>(a.c.pages)) {
         if (w < 32) atomicOr(a.err, kDevErrIndex);
         return;
       }
-      at = static_cast<int>(row >> 4);
-      seen = 0xffffu >> (kKvBlock - min(kKvBlock, s.len - pos));
+      at = ((x.page * a.c.heads) << (a.c.page_log2 - 4)) + x.sub;
+      seen = x.seen;
       ks = __ldg(a.c.ks + at), vs = __ldg(a.c.vs + at);
     };
-    // this thread's parts of the tile: part w % kParts of every (128 / kParts)th token from w / kParts on
+    // this thread's parts of the tile: part w % kParts of every (kWiden / kParts)th token from w / kParts on
     auto load = [&](const int8_t* codes, uint4 (&x)[kEach]) {
 #pragma unroll
       for (int n = 0; n < kEach; ++n) {
-        const int token = n * (128 / kParts) + w / kParts;
+        const int token = n * (kWiden / kParts) + w / kParts;
         const int blk = __shfl_sync(0xffffffffu, at, token >> 4);
         x[n] = blk >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + static_cast<long long>(blk) * (kKvBlock * D) +
                                                                (token & (kKvBlock - 1)) * D + w % kParts * 16))
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       const int part = w % kParts, half = part >> 2;
 #pragma unroll
       for (int n = 0; n < kEach; ++n) {
-        const int token = n * (128 / kParts) + w / kParts;
+        const int token = n * (kWiden / kParts) + w / kParts;
         uint4 f[2];
         widen4(x[n].x, f[0].x, f[0].y), widen4(x[n].y, f[0].z, f[0].w);
         widen4(x[n].z, f[1].x, f[1].y), widen4(x[n].w, f[1].z, f[1].w);
@@ -274,17 +286,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     };
     uint4 kc[kEach], vc[kEach];
     if (more) settle();
-    look_up();
+    find(look_up());
     load(a.c.k, kc);
     load(a.c.v, vc);
-    bool ok = true;
-    for (int it = 0; more; ++it) {
-      const int st = it % kStages;
-      const float my_ks = ks, my_vs = vs;
-      const unsigned my_seen = seen;
+    float my_ks = ks, my_vs = vs;               // of the tile in work
+    unsigned my_seen = seen;
+    bool now = more, next = false;              // there is a tile in work, and one after it
+    Block ahead = {-1, 0, 0};
+    auto step = [&]() {
+      if (!more) return;
       ++i;
       settle();
-      look_up();                                // of the next tile
+      ahead = look_up();
+    };
+    step();
+    next = more;
+    find(ahead);
+    bool ok = true;
+    for (int it = 0; now; ++it) {
+      const int st = it % kStages;
+      step();                                   // the tile after the next
       if (it >= kStages) ok = __all_sync(0xffffffffu, gwait(&k_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err));
       if (!ok) break;
       if (w < kBlocks) {
@@ -299,6 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       put(sv + st * C::kTileBytes, vc);
       mbar_arrive(&v_full[st]);
       load(a.c.v, vc);
+      my_ks = ks, my_vs = vs, my_seen = seen;
+      now = next, next = more;
+      if (next)
+        find(ahead);
+      else
+        at = -1;
     }
   } else if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -342,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
           for (int kk = 0; kk < kTile / 16; ++kk)
             lead_mma_ts(leader, t_o, t_s[it & 1] + kk * 8, v_desc + ((it % kStages) * C::kTileBytes >> 4) + kk * (2048 >> 4),
                         C::kIdescPv, kk > 0 || i > 0 ? 1u : 0u);
-          lead_commit(leader, o_done);
+          lead_commit(leader, &o_done[it & 1]);
           lead_commit(leader, &v_empty[it % kStages]);
         }
       }
@@ -463,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
           const float ko = k * power_of_two(e - max(e, te));
           e = max(e, te);
           if (i > 0) {
-            ok = __all_sync(0xffffffffu, gwait(o_done, (it - 1) & 1, &s_fail, a.err));
+            ok = __all_sync(0xffffffffu, gwait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -504,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         unpack2(add2(sum2[0], sum2[1]), x, y);
         l += x + y;
       }
-      if (ok && n > 0) ok = __all_sync(0xffffffffu, gwait(o_done, (it - 1) & 1, &s_fail, a.err));
+      if (ok && n > 0) ok = __all_sync(0xffffffffu, gwait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
       if (!ok) break;
       tc_fence_after();
       const bool whole = s.from >= u0 && s.to <= u1;
