@@ -13,9 +13,10 @@
 //   empty ones before each (sequence, rows, head) for what starting one costs,
 //   that is cut evenly over the CTAs; shares of what was cut are joined by the
 //   last CTA to have one.
-// * In a CTA eight warps take codes from the pages to registers, a tile ahead
-//   (and look up its blocks two tiles ahead), and put them as exact fp16 into shared memory in the order of the MMA's
-//   operands; one warp issues the MMAs; four warps (a thread a row) turn
+// * In a CTA one warp looks blocks up and copies their codes into a ring (in
+//   registers of the warps that widen them they would not be far enough ahead);
+//   eight warps put them as exact fp16 into shared memory in the order of the
+//   MMA's operands; one warp issues the MMAs; four warps (a thread a row) turn
 //   scores into weights.  Two tiles of scores take turns in tensor memory, so
 //   that the next one's products run beside a tile's softmax.
 // * Scales are applied in fp32: a block's key scale is part of the factor of
@@ -34,15 +35,17 @@ namespace {
 using namespace gemm;
 
 constexpr int kTile = 128;                // tokens and query rows of a tile
-constexpr int kThreads = 512;             // 4 softmax warps, 8 that widen codes, one that issues MMAs and three idle ones
-constexpr int kWidenWarp = 4, kWidenWarps = 8, kMmaWarp = 12, kWiden = kWidenWarps * 32;
+constexpr int kThreads = 512;             // 4 softmax warps, 8 that widen codes, one each for MMAs and copies, two idle ones
+constexpr int kWidenWarp = 4, kWidenWarps = 8, kMmaWarp = 12, kCopyWarp = 13, kWiden = kWidenWarps * 32;
 // registers a thread: 512 x 128 at launch
 constexpr int kSoftmaxRegs = 216, kWidenRegs = 104, kOtherRegs = 56;
 static_assert(128 * (kSoftmaxRegs + 2 * kWidenRegs + kOtherRegs) <= kThreads * 128, "the shares must fit the launch's registers");
-constexpr int kStages = 2;                // of keys, and of values
-constexpr int kRecs = 4;                  // records of tiles: a tile's is in use until its weights are
+constexpr int kStages = 2;                // of keys as fp16; of values one
+constexpr int kRaw = 5;                   // of codes: keys and values of a tile in turn
+constexpr int kRecs = 8;                  // records of tiles: copies are six tiles at most before the softmax
 constexpr int kBlocks = kTile / kKvBlock;
 constexpr int kSegCost = 3;               // what starting a (sequence, rows, head) costs, in tiles
+constexpr int kLeastTiles = 4;            // of a CTA, about: fewer make more shares than they save
 constexpr float kLazy = 8.0f;             // the reference moves once a score exceeds it by 2^kLazy
 constexpr float kUnit = 7.0f;             // weights are 2^7 at the reference: up to 2^15, below fp16's 65504
 constexpr int kNoScale = -1024;           // exponent of blocks whose values are all zero
@@ -52,7 +55,7 @@ struct DraftParams {
   KvAttnCall a;
   int group, max_rows;       // sequences with more query rows are left to the prompt form
   unsigned* tickets;         // [ranges], zero
-  float* part;               // [ranges][2][kTile][D + 4] shares: sums, their maximum, weights' sum and exponent
+  float4* part;              // [ranges][2][D / 4 + 1][kTile] shares: sums; their maximum, weights' sum and exponent
 };
 
 // What the softmax needs of a tile of tokens.
@@ -76,7 +79,10 @@ template <int D>
 struct Cfg {
   static constexpr int kHalf = kTile * 128;             // 128 rows of 64 fp16: a swizzled box
   static constexpr int kTileBytes = kHalf * (D / 64);
-  static constexpr size_t smem(int B) { return 1024 + (1 + 2 * kStages) * kTileBytes + 256 + static_cast<size_t>(B + 1) * 8; }
+  static constexpr int kRawBytes = kTile * D;
+  static constexpr size_t smem(int B) {
+    return 1024 + (2 + kStages) * kTileBytes + kRaw * kRawBytes + 256 + static_cast<size_t>(B + 1) * 8;
+  }
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescQk = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
   static constexpr uint32_t kIdescPv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
@@ -110,17 +116,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sk = sq + C::kTileBytes;
   uint8_t* sv = sk + kStages * C::kTileBytes;
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(sv + kStages * C::kTileBytes);
+  uint8_t* raw = sv + C::kTileBytes;
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(raw + kRaw * C::kRawBytes);
+  uint64_t* raw_empty = raw_full + kRaw;
+  uint64_t* k_full = raw_empty + kRaw;
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
-  uint64_t* v_empty = v_full + kStages;
-  uint64_t* s_full = v_empty + kStages;  // [2] scores of a tile are in tensor memory
+  uint64_t* v_empty = v_full + 1;
+  uint64_t* s_full = v_empty + 1;        // [2] scores of a tile are in tensor memory
   uint64_t* p_ready = s_full + 2;        // [2] its weights are, and the sums rescaled
   uint64_t* o_done = p_ready + 2;        // [2] the sums include its weights: two, as a row may wait for a tile while the
   uint64_t* q_ready = o_done + 2;        //     one before it is not done
   uint64_t* drain = q_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  long long* s_cum = reinterpret_cast<long long*>(sv + kStages * C::kTileBytes + 256);   // [B + 1] first unit of each sequence
+  long long* s_cum = reinterpret_cast<long long*>(raw + kRaw * C::kRawBytes + 256);   // [B + 1] first unit of each sequence
   __shared__ __align__(16) Rec s_rec[kRecs];
   __shared__ long long s_warp[kThreads / 32];
   __shared__ int s_fail, s_last;
@@ -128,8 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   const KvAttnCall& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i)
-      mbar_init(&k_full[i], kWiden), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], kWiden), mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kWiden);
+    for (int i = 0; i < kStages; ++i) mbar_init(&k_full[i], kWiden), mbar_init(&k_empty[i], 1);
+    mbar_init(v_full, kWiden), mbar_init(v_empty, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kTile), mbar_init(&o_done[i], 1);
     mbar_init(q_ready, kTile), mbar_init(drain, 1);
     s_fail = 0;
@@ -176,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_s[2] = {tmem, tmem + kTile}, t_o = tmem + 2 * kTile;
   const long long units = s_cum[B];
-  const long long ranges = max(1LL, min(static_cast<long long>(gridDim.x), units / (kSegCost + 1)));
+  const long long ranges = max(1LL, min(static_cast<long long>(gridDim.x), units / (kSegCost + kLeastTiles)));
   auto range_of = [&](long long i) { return units / ranges * i + min(i, units % ranges); };
   // the range that holds unit u
   auto owner_of = [&](long long u) {
@@ -211,65 +221,24 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   if (warp >= kWidenWarp && warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
     // ================= codes to fp16 tiles =================
-    const int w = tid - kWidenWarp * 32;
-    Segment s = {};
-    long long u = u0;
-    int i = 0;
-    bool more = u0 < u1;
-    auto settle = [&]() {                       // to the next tile there is
-      while (i >= s.hi) {
-        if (u >= u1) {
-          more = false;
-          return;
-        }
-        locate(u, s);
-        u = s.to;
-        i = s.lo;
-      }
-    };
-    // A lane looks up one of a tile's eight blocks: the page first, and a tile later, when it has come, the block's
-    // place, its tokens and its scales.
-    struct Block {
-      int page, sub;             // page of the table (-1: none), block in it
-      unsigned seen;
-    };
-    auto look_up = [&]() {       // of tile i
-      Block x = {-1, 0, 0};
-      if (!more || lane >= kBlocks) return x;
-      const int pos = s.tile(i) * kTile + lane * kKvBlock, pi = pos >> a.c.page_log2;
-      if (pos >= s.len || (pos + kKvBlock <= s.start && pos >= a.sinks)) return x;
-      x.seen = 0xffffu >> (kKvBlock - min(kKvBlock, s.len - pos));
-      x.sub = (s.h << (a.c.page_log2 - 4)) + ((pos & (a.c.page - 1)) >> 4);
-      x.page = pi < a.b.table_stride ? __ldg(a.b.table + s.b * a.b.table_stride + pi) : -1;
-      return x;
-    };
-    int at = -1;                 // of the tile whose codes are asked for next
-    float ks = 0.f, vs = 0.f;
-    unsigned seen = 0;
-    auto find = [&](const Block& x) {
-      at = -1, seen = 0, ks = 0.f, vs = 0.f;
-      if (x.seen == 0) return;
-      if (static_cast<unsigned>(x.page) >= static_cast<unsigned>(a.c.pages)) {
-        if (w < 32) atomicOr(a.err, kDevErrIndex);
-        return;
-      }
-      at = ((x.page * a.c.heads) << (a.c.page_log2 - 4)) + x.sub;
-      seen = x.seen;
-      ks = __ldg(a.c.ks + at), vs = __ldg(a.c.vs + at);
-    };
-    // this thread's parts of the tile: part w % kParts of every (kWiden / kParts)th token from w / kParts on
-    auto load = [&](const int8_t* codes, uint4 (&x)[kEach]) {
+    const int w = tid - kWidenWarp * 32, part = w % kParts, half = part >> 2;
+    int it = 0, stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // this thread's parts of a tile: part w % kParts of every (kWiden / kParts)th token from w / kParts on
+    auto widen = [&](uint8_t* to, uint64_t* done, uint64_t* empty, uint32_t parity, bool wait) {
+      ok = __all_sync(0xffffffffu, gwait(&raw_full[stage], phase, &s_fail, a.err));
+      if (!ok) return;
+      const uint8_t* from = raw + stage * C::kRawBytes + part * 16;
+      uint4 x[kEach];
 #pragma unroll
       for (int n = 0; n < kEach; ++n) {
         const int token = n * (kWiden / kParts) + w / kParts;
-        const int blk = __shfl_sync(0xffffffffu, at, token >> 4);
-        x[n] = blk >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + static_cast<long long>(blk) * (kKvBlock * D) +
-                                                               (token & (kKvBlock - 1)) * D + w % kParts * 16))
-                        : make_uint4(0, 0, 0, 0);
+        x[n] = *reinterpret_cast<const uint4*>(from + token * D);
+        if (s_rec[it % kRecs].seen[token >> 4] == 0) x[n] = make_uint4(0, 0, 0, 0);   // nothing was copied
       }
-    };
-    auto put = [&](uint8_t* to, const uint4 (&x)[kEach]) {
-      const int part = w % kParts, half = part >> 2;
+      if (wait) ok = __all_sync(0xffffffffu, gwait(empty, parity, &s_fail, a.err));
+      if (!ok) return;
 #pragma unroll
       for (int n = 0; n < kEach; ++n) {
         const int token = n * (kWiden / kParts) + w / kParts;
@@ -283,49 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         *reinterpret_cast<uint4*>(row + ((c ^ 1 ^ half) << 4)) = half ? f[0] : f[1];
       }
       fence_async_smem();
+      mbar_arrive(done);
+      mbar_arrive(&raw_empty[stage]);
+      if (++stage == kRaw) stage = 0, phase ^= 1;
     };
-    uint4 kc[kEach], vc[kEach];
-    if (more) settle();
-    find(look_up());
-    load(a.c.k, kc);
-    load(a.c.v, vc);
-    float my_ks = ks, my_vs = vs;               // of the tile in work
-    unsigned my_seen = seen;
-    bool now = more, next = false;              // there is a tile in work, and one after it
-    Block ahead = {-1, 0, 0};
-    auto step = [&]() {
-      if (!more) return;
-      ++i;
-      settle();
-      ahead = look_up();
-    };
-    step();
-    next = more;
-    find(ahead);
-    bool ok = true;
-    for (int it = 0; now; ++it) {
-      const int st = it % kStages;
-      step();                                   // the tile after the next
-      if (it >= kStages) ok = __all_sync(0xffffffffu, gwait(&k_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err));
-      if (!ok) break;
-      if (w < kBlocks) {
-        Rec& r = s_rec[it % kRecs];
-        r.ks[w] = my_ks, r.vs[w] = my_vs, r.seen[w] = static_cast<uint16_t>(my_seen);
+    Segment s;
+    for (long long u = u0; ok && u < u1; u = s.to) {
+      locate(u, s);
+      for (int i = s.lo; ok && i < s.hi; ++i, ++it) {
+        const int st = it % kStages;
+        widen(sk + st * C::kTileBytes, &k_full[st], &k_empty[st], ((it / kStages) - 1) & 1, it >= kStages);
+        if (ok) widen(sv, v_full, v_empty, (it - 1) & 1, it > 0);
       }
-      put(sk + st * C::kTileBytes, kc);
-      mbar_arrive(&k_full[st]);
-      load(a.c.k, kc);
-      if (it >= kStages) ok = __all_sync(0xffffffffu, gwait(&v_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err));
-      if (!ok) break;
-      put(sv + st * C::kTileBytes, vc);
-      mbar_arrive(&v_full[st]);
-      load(a.c.v, vc);
-      my_ks = ks, my_vs = vs, my_seen = seen;
-      now = next, next = more;
-      if (next)
-        find(ahead);
-      else
-        at = -1;
     }
   } else if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -362,20 +300,108 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
             if (!ok) break;
             qk(it + 1);
           }
-          ok = wait(&p_ready[it & 1], (it >> 1) & 1) && wait(&v_full[it % kStages], (it / kStages) & 1);
+          ok = wait(&p_ready[it & 1], (it >> 1) & 1) && wait(v_full, it & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            lead_mma_ts(leader, t_o, t_s[it & 1] + kk * 8, v_desc + ((it % kStages) * C::kTileBytes >> 4) + kk * (2048 >> 4),
+            lead_mma_ts(leader, t_o, t_s[it & 1] + kk * 8, v_desc + kk * (2048 >> 4),
                         C::kIdescPv, kk > 0 || i > 0 ? 1u : 0u);
           lead_commit(leader, &o_done[it & 1]);
-          lead_commit(leader, &v_empty[it % kStages]);
+          lead_commit(leader, v_empty);
         }
       }
       // no MMA may still run when the tensor memory is freed
       lead_commit(leader, drain);
       (void)mbar_wait(drain, 0);
+    } else if (warp == kCopyWarp) {
+      // ================= pages to the ring: a lane for each block of a tile =================
+      Segment s = {};
+      long long u = u0;
+      int i = 0;
+      bool more = u0 < u1;
+      auto settle = [&]() {                     // to the next tile there is
+        while (i >= s.hi) {
+          if (u >= u1) {
+            more = false;
+            return;
+          }
+          locate(u, s);
+          u = s.to;
+          i = s.lo;
+        }
+      };
+      struct Block {
+        int at;                  // of the cache; -1: none
+        unsigned seen;           // its tokens
+        float ks, vs;
+      };
+      // The next tile's block of this lane.  The page is known a tile before it is used, and so are the scales.
+      int page = -1, sub = 0;
+      unsigned seen = 0;
+      auto look_up = [&]() {
+        seen = 0, page = -1;
+        if (!more || lane >= kBlocks) return;
+        const int pos = s.tile(i) * kTile + lane * kKvBlock, pi = pos >> a.c.page_log2;
+        if (pos >= s.len || (pos + kKvBlock <= s.start && pos >= a.sinks)) return;
+        seen = 0xffffu >> (kKvBlock - min(kKvBlock, s.len - pos));
+        sub = (s.h << (a.c.page_log2 - 4)) + ((pos & (a.c.page - 1)) >> 4);
+        page = pi < a.b.table_stride ? __ldg(a.b.table + s.b * a.b.table_stride + pi) : -1;
+      };
+      auto find = [&]() {
+        Block x = {-1, 0, 0.f, 0.f};
+        if (seen == 0) return x;
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
+          atomicOr(a.err, kDevErrIndex);
+          return x;
+        }
+        x.at = ((page * a.c.heads) << (a.c.page_log2 - 4)) + sub;
+        x.seen = seen;
+        x.ks = __ldg(a.c.ks + x.at), x.vs = __ldg(a.c.vs + x.at);
+        return x;
+      };
+      auto next = [&]() {
+        if (more) ++i, settle();
+        look_up();
+      };
+      if (more) settle();
+      look_up();
+      bool now = more;
+      Block x = find();
+      next();
+      int copied = 0, stage = 0;                // halves of tiles so far
+      uint32_t phase = 1;
+      bool ok = true;
+      for (int it = 0; now && ok; ++it) {
+        const bool then = more;
+        const Block y = find();                 // of the tile after this one
+        next();
+        const unsigned bytes = __popc(__ballot_sync(0xffffffffu, x.at >= 0)) * (kKvBlock * D);
+        for (int v = 0; v < 2; ++v) {
+          if (copied >= kRaw) ok = __all_sync(0xffffffffu, gwait(&raw_empty[stage], phase, &s_fail, a.err));
+          if (!ok) break;
+          if (v == 0 && lane < kBlocks) {
+            Rec& r = s_rec[it % kRecs];
+            r.ks[lane] = x.ks, r.vs[lane] = x.vs, r.seen[lane] = static_cast<uint16_t>(x.seen);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], bytes);
+          __syncwarp();
+          if (x.at >= 0)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(raw + stage * C::kRawBytes + lane * (kKvBlock * D))),
+                         "l"((v ? a.c.v : a.c.k) + static_cast<long long>(x.at) * (kKvBlock * D)), "n"(kKvBlock * D),
+                         "r"(smem_u32(&raw_full[stage]))
+                         : "memory");
+          ++copied;
+          if (++stage == kRaw) stage = 0, phase ^= 1;
+        }
+        x = y;
+        now = then;
+      }
+      // after a failure nobody else waits for the copies in flight
+      if (s_fail)
+        for (int n = max(0, copied - kRaw); n < copied; ++n) (void)mbar_wait(&raw_full[n % kRaw], (n / kRaw) & 1);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -535,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       if (!ok) break;
       tc_fence_after();
       const bool whole = s.from >= u0 && s.to <= u1;
-      constexpr int kShare = kTile * (D + 4);
+      constexpr int kShare = kTile * (D / 4 + 1);
       if (whole) {
         const float k = l > 0.f ? power_of_two(e) / l : l == 0.f ? 0.f : l;   // a row that sees nothing: zeros; a NaN stays
         if (a.lse && have) a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l) - kUnit) * kLn2 : l == 0.f ? -INFINITY : l;
@@ -560,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         continue;
       }
       // partial sums: slot 0 for what began in an earlier CTA, 1 for what begins here
-      float* slot = p.part + (range * 2 + (s.from >= u0 ? 1 : 0)) * kShare + r * (D + 4);
+      float4* slot = p.part + (range * 2 + (s.from >= u0 ? 1 : 0)) * kShare + r;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
@@ -571,11 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         if (have) {
 #pragma unroll
           for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<uint4*>(slot + 32 * x + c) = n > 0 ? make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]) : make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(slot)[(8 * x + c / 4) * kTile] = n > 0 ? make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]) : make_uint4(0, 0, 0, 0);
         }
       }
       tc_fence_before();
-      if (have) *reinterpret_cast<float4*>(slot + D) = make_float4(m, l, __int_as_float(e), 0.f);
+      if (have) slot[D / 4 * kTile] = make_float4(m, l, __int_as_float(e), 0.f);
       rows_sync();
       const long long o0 = owner_of(s.from), o1 = owner_of(s.to - 1);
       if (tid == 0) {
@@ -586,40 +612,42 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       rows_sync();
       if (s_last && have) {
         const int shares = static_cast<int>(o1 - o0) + 1;
-        auto share = [&](int i) { return p.part + ((o0 + i) * 2 + (i == 0 ? 1 : 0)) * kShare + r * (D + 4); };
+        auto share = [&](int i) { return p.part + ((o0 + i) * 2 + (i == 0 ? 1 : 0)) * kShare + r; };
         float mm = -INFINITY;
         int ee = kNoScale;
+#pragma unroll 4
         for (int i = 0; i < shares; ++i) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(share(i) + D));
+          const float4 x = __ldcg(share(i) + D / 4 * kTile);
           mm = fmaxf(mm, x.x), ee = max(ee, __float_as_int(x.z));
         }
         float ll = 0.f;
+#pragma unroll 4
         for (int i = 0; i < shares; ++i) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(share(i) + D));
+          const float4 x = __ldcg(share(i) + D / 4 * kTile);
           ll += x.x > -INFINITY ? x.y * ex2(x.x - mm) : x.y;   // without a key: 0
         }
         const float k = ll > 0.f ? power_of_two(ee) / ll : ll == 0.f ? 0.f : ll;
         if (a.lse) a.lse[t * a.Hq + head] = ll > 0.f ? (mm + log2f(ll) - kUnit) * kLn2 : ll == 0.f ? -INFINITY : ll;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float4 y[4];
+        for (int c = 0; c < D; c += 32) {
+          float4 y[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int q = 0; q < 8; ++q) y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
           for (int i = 0; i < shares; ++i) {
-            const float* from_share = share(i);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(from_share + D));
+            const float4* from_share = share(i);
+            const float4 x = __ldcg(from_share + D / 4 * kTile);
             const float f = x.x > -INFINITY ? ex2(x.x - mm) * power_of_two(__float_as_int(x.z) - ee) : 0.f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 z = __ldcg(reinterpret_cast<const float4*>(from_share + c + 4 * q));
+            for (int q = 0; q < 8; ++q) {
+              const float4 z = __ldcg(from_share + (c / 4 + q) * kTile);
               y[q].x = fmaf(f, z.x, y[q].x), y[q].y = fmaf(f, z.y, y[q].y);
               y[q].z = fmaf(f, z.z, y[q].z), y[q].w = fmaf(f, z.w, y[q].w);
             }
           }
           uint4* to4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (t * a.Hq + head) * D + c);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             __nv_bfloat162 z[4] = {__floats2bfloat162_rn(y[2 * q].x * k, y[2 * q].y * k), __floats2bfloat162_rn(y[2 * q].z * k, y[2 * q].w * k),
                                    __floats2bfloat162_rn(y[2 * q + 1].x * k, y[2 * q + 1].y * k),
                                    __floats2bfloat162_rn(y[2 * q + 1].z * k, y[2 * q + 1].w * k)};
@@ -676,7 +704,7 @@ cudaError_t launch_kv_draft(const KvAttnCall& a, int max_rows, void* ws, int sms
   p.group = a.Hq / a.c.heads;
   p.max_rows = max_rows;
   p.tickets = static_cast<unsigned*>(ws);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
+  p.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + kv_attn_header_bytes());
   return a.c.dim == 128 ? launch<128>(p, sms, st) : launch<64>(p, sms, st);
 }
 
