@@ -40,7 +40,7 @@ constexpr int kWidenWarp = 4, kWidenWarps = 8, kMmaWarp = 12, kCopyWarp = 13, kW
 // registers a thread: 512 x 128 at launch
 constexpr int kSoftmaxRegs = 216, kWidenRegs = 104, kOtherRegs = 56;
 static_assert(128 * (kSoftmaxRegs + 2 * kWidenRegs + kOtherRegs) <= kThreads * 128, "the shares must fit the launch's registers");
-constexpr int kStages = 2;                // of keys as fp16; of values one
+constexpr int kStages = 2;                // of keys, and of values, as fp16
 constexpr int kRaw = 5;                   // of codes: keys and values of a tile in turn
 constexpr int kRecs = 8;                  // records of tiles: copies are six tiles at most before the softmax
 constexpr int kBlocks = kTile / kKvBlock;
@@ -81,7 +81,7 @@ struct Cfg {
   static constexpr int kTileBytes = kHalf * (D / 64);
   static constexpr int kRawBytes = kTile * D;
   static constexpr size_t smem(int B) {
-    return 1024 + (2 + kStages) * kTileBytes + kRaw * kRawBytes + 256 + static_cast<size_t>(B + 1) * 8;
+    return 1024 + 2 * kStages * kTileBytes + kRaw * kRawBytes + 256 + static_cast<size_t>(B + 1) * 8;
   }
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescQk = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
@@ -113,17 +113,16 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   using C = Cfg<D>;
   constexpr int kParts = D / 16, kEach = kTile * kParts / kWiden;   // 16-byte parts of a row; of a tile, that a thread widens
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sq = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sk = sq + C::kTileBytes;
+  uint8_t* sk = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sv = sk + kStages * C::kTileBytes;
-  uint8_t* raw = sv + C::kTileBytes;
+  uint8_t* raw = sv + kStages * C::kTileBytes;
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(raw + kRaw * C::kRawBytes);
   uint64_t* raw_empty = raw_full + kRaw;
   uint64_t* k_full = raw_empty + kRaw;
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
-  uint64_t* v_empty = v_full + 1;
-  uint64_t* s_full = v_empty + 1;        // [2] scores of a tile are in tensor memory
+  uint64_t* v_empty = v_full + kStages;
+  uint64_t* s_full = v_empty + kStages;  // [2] scores of a tile are in tensor memory
   uint64_t* p_ready = s_full + 2;        // [2] its weights are, and the sums rescaled
   uint64_t* o_done = p_ready + 2;        // [2] the sums include its weights: two, as a row may wait for a tile while the
   uint64_t* q_ready = o_done + 2;        //     one before it is not done
@@ -138,8 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
   if (tid == 0) {
     for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kWiden);
-    for (int i = 0; i < kStages; ++i) mbar_init(&k_full[i], kWiden), mbar_init(&k_empty[i], 1);
-    mbar_init(v_full, kWiden), mbar_init(v_empty, 1);
+    for (int i = 0; i < kStages; ++i)
+      mbar_init(&k_full[i], kWiden), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], kWiden), mbar_init(&v_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kTile), mbar_init(&o_done[i], 1);
     mbar_init(q_ready, kTile), mbar_init(drain, 1);
     s_fail = 0;
@@ -184,14 +183,30 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t t_s[2] = {tmem, tmem + kTile}, t_o = tmem + 2 * kTile;
+  // scores (and weights) of two tiles, sums, and the queries: from there they take nothing of shared memory's bandwidth,
+  // which the codes' way through it all but fills
+  const uint32_t t_s[2] = {tmem, tmem + kTile}, t_o = tmem + 2 * kTile, t_q = tmem + 3 * kTile;
   const long long units = s_cum[B];
   const long long ranges = max(1LL, min(static_cast<long long>(gridDim.x), units / (kSegCost + kLeastTiles)));
-  auto range_of = [&](long long i) { return units / ranges * i + min(i, units % ranges); };
-  // the range that holds unit u
+  auto even_cut = [&](long long i) { return units / ranges * i + min(i, units % ranges); };
+  // the even range that holds unit u
   auto owner_of = [&](long long u) {
     const long long q = units / ranges, r = units % ranges;
     return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
+  };
+  // a cut before the first tile of a (sequence, rows, head) is one before its start
+  auto range_of = [&](long long i) {
+    const long long u = even_cut(i);
+    if (u >= units) return units;
+    int lo = 0, hi = B - 1;                     // the last b with s_cum[b] <= u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_cum[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    int start, first, stay, n;
+    seq_tiles(a, a.b.cu[lo + 1] - a.b.cu[lo], a.b.kv_len[lo], start, first, stay, n);
+    const long long into = (u - s_cum[lo]) % (n + kSegCost);
+    return into <= kSegCost ? u - into : u;
   };
   const long long range = blockIdx.x;
   const long long u0 = range < ranges ? range_of(range) : units, u1 = range < ranges ? range_of(range + 1) : units;
@@ -227,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     bool ok = true;
     // this thread's parts of a tile: part w % kParts of every (kWiden / kParts)th token from w / kParts on
     auto widen = [&](uint8_t* to, uint64_t* done, uint64_t* empty, uint32_t parity, bool wait) {
-      ok = __all_sync(0xffffffffu, gwait(&raw_full[stage], phase, &s_fail, a.err));
+      ok = __all_sync(0xffffffffu, quick_wait(&raw_full[stage], phase, &s_fail, a.err));
       if (!ok) return;
       const uint8_t* from = raw + stage * C::kRawBytes + part * 16;
       uint4 x[kEach];
@@ -237,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         x[n] = *reinterpret_cast<const uint4*>(from + token * D);
         if (s_rec[it % kRecs].seen[token >> 4] == 0) x[n] = make_uint4(0, 0, 0, 0);   // nothing was copied
       }
-      if (wait) ok = __all_sync(0xffffffffu, gwait(empty, parity, &s_fail, a.err));
+      if (wait) ok = __all_sync(0xffffffffu, quick_wait(empty, parity, &s_fail, a.err));
       if (!ok) return;
 #pragma unroll
       for (int n = 0; n < kEach; ++n) {
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       for (int i = s.lo; ok && i < s.hi; ++i, ++it) {
         const int st = it % kStages;
         widen(sk + st * C::kTileBytes, &k_full[st], &k_empty[st], ((it / kStages) - 1) & 1, it >= kStages);
-        if (ok) widen(sv, v_full, v_empty, (it - 1) & 1, it > 0);
+        if (ok) widen(sv + st * C::kTileBytes, &v_full[st], &v_empty[st], ((it / kStages) - 1) & 1, it >= kStages);
       }
     }
   } else if (warp >= kMmaWarp) {
@@ -270,7 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     if (warp == kMmaWarp) {
       const uint32_t leader = elect_one();
       auto wait = [&](uint64_t* bar, uint32_t parity) { return poll_wait(bar, parity, &s_fail, a.err); };
-      const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 1024, kSwizzle128);
       const uint64_t k_desc = smem_desc(smem_u32(sk), 16, 1024, kSwizzle128);
       const uint64_t v_desc = smem_desc(smem_u32(sv), C::kHalf, 1024, kSwizzle128);
       auto qk = [&](int it) {
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int off = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
-          lead_mma(leader, t_s[it & 1], q_desc + off, k_desc + (st * C::kTileBytes >> 4) + off, C::kIdescQk, kk > 0 ? 1u : 0u);
+          lead_mma_ts(leader, t_s[it & 1], t_q + kk * 8, k_desc + (st * C::kTileBytes >> 4) + off, C::kIdescQk, kk > 0 ? 1u : 0u);
         }
         lead_commit(leader, &s_full[it & 1]);
         lead_commit(leader, &k_empty[st]);
@@ -300,15 +314,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
             if (!ok) break;
             qk(it + 1);
           }
-          ok = wait(&p_ready[it & 1], (it >> 1) & 1) && wait(v_full, it & 1);
+          ok = wait(&p_ready[it & 1], (it >> 1) & 1) && wait(&v_full[it % kStages], (it / kStages) & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            lead_mma_ts(leader, t_o, t_s[it & 1] + kk * 8, v_desc + kk * (2048 >> 4),
+            lead_mma_ts(leader, t_o, t_s[it & 1] + kk * 8, v_desc + ((it % kStages) * C::kTileBytes >> 4) + kk * (2048 >> 4),
                         C::kIdescPv, kk > 0 || i > 0 ? 1u : 0u);
           lead_commit(leader, &o_done[it & 1]);
-          lead_commit(leader, v_empty);
+          lead_commit(leader, &v_empty[it % kStages]);
         }
       }
       // no MMA may still run when the tensor memory is freed
@@ -378,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         next();
         const unsigned bytes = __popc(__ballot_sync(0xffffffffu, x.at >= 0)) * (kKvBlock * D);
         for (int v = 0; v < 2; ++v) {
-          if (copied >= kRaw) ok = __all_sync(0xffffffffu, gwait(&raw_empty[stage], phase, &s_fail, a.err));
+          if (copied >= kRaw) ok = __all_sync(0xffffffffu, quick_wait(&raw_empty[stage], phase, &s_fail, a.err));
           if (!ok) break;
           if (v == 0 && lane < kBlocks) {
             Rec& r = s_rec[it % kRecs];
@@ -451,9 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             y[k] = __floats2half2_rn(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
-          *reinterpret_cast<uint4*>(sq + (i >> 3) * C::kHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = *reinterpret_cast<uint4*>(y);
+          w[i] = *reinterpret_cast<uint4*>(y);
         }
-        fence_async_smem();
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) tmem_st32(t_q + lanes + 32 * x, reinterpret_cast<const uint32_t*>(w) + 32 * x);
+        tmem_wait_st();
+        tc_fence_before();
         mbar_arrive(q_ready);
       }
       // positions the row sees: (from, to]; one that does not exist sees all, so that no tile is on its edge
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       int e = kNoScale;             // the sums are relative to 2^e, above the value scales that the row has seen
       for (int i = 0; i < n; ++i, ++it) {
         const int t0 = s.tile(s.lo + i) * kTile;
-        ok = __all_sync(0xffffffffu, gwait(&s_full[it & 1], (it >> 1) & 1, &s_fail, a.err));
+        ok = __all_sync(0xffffffffu, quick_wait(&s_full[it & 1], (it >> 1) & 1, &s_fail, a.err));
         if (!ok) break;
         tc_fence_after();
         const Rec& rec = s_rec[it % kRecs];
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
           const float ko = k * power_of_two(e - max(e, te));
           e = max(e, te);
           if (i > 0) {
-            ok = __all_sync(0xffffffffu, gwait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
+            ok = __all_sync(0xffffffffu, quick_wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -557,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         unpack2(add2(sum2[0], sum2[1]), x, y);
         l += x + y;
       }
-      if (ok && n > 0) ok = __all_sync(0xffffffffu, gwait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
+      if (ok && n > 0) ok = __all_sync(0xffffffffu, quick_wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
       if (!ok) break;
       tc_fence_after();
       const bool whole = s.from >= u0 && s.to <= u1;
@@ -603,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       tc_fence_before();
       if (have) slot[D / 4 * kTile] = make_float4(m, l, __int_as_float(e), 0.f);
       rows_sync();
-      const long long o0 = owner_of(s.from), o1 = owner_of(s.to - 1);
+      const long long o0 = owner_of(s.from + kSegCost), o1 = owner_of(s.to - 1);   // with the cuts before its tiles at its start
       if (tid == 0) {
         const unsigned old = atom_add_acq_rel_gpu(p.tickets + o0, 1u);
         s_last = old == static_cast<unsigned>(o1 - o0);

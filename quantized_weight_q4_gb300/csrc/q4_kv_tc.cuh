@@ -80,6 +80,25 @@ __device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// bounded_wait without a look at the timer before the second try: that look takes longer than most of a pipeline's
+// waits.  The tries suspend the thread in the barrier.
+__device__ __forceinline__ bool quick_wait(uint64_t* bar, uint32_t parity, volatile int* fail, unsigned* err) {
+  unsigned long long t0 = 0;
+  for (uint32_t turn = 1;; ++turn) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((turn & 63) == 0) {
+      if (*fail) return false;
+      const unsigned long long t = globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        *fail = 1;
+        atomicOr(err, kDevErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // One lane of the warp, the same each time.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;

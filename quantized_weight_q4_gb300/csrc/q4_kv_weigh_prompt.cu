@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_weigh_prompt_kernel(const _
       bool ok = true;
       for (int i = 0; ok && i < n; ++i) {
         const int it = taken + i, st = it % kStages, j0 = (t_lo + rank + 2 * i) * p.tokens;
-        ok = gwait(&l_full[st], (it / kStages) & 1, &s_fail, a.err) && gwait(&d_full[g], it & 1, &s_fail, a.err);
+        ok = quick_wait(&l_full[st], (it / kStages) & 1, &s_fail, a.err) && quick_wait(&d_full[g], it & 1, &s_fail, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_weigh_prompt_kernel(const _
         const uint32_t bytes = static_cast<uint32_t>(p.tokens) * p.group * D * 2;
         for (int i = 0; i < n && !s_fail; ++i) {
           const int it = taken + i, st = it % kStages;
-          if (it >= kStages && !gwait(&empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err)) break;
+          if (it >= kStages && !quick_wait(&empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err)) break;
           mbar_arrive_expect_tx(&full[st], bytes);
           const int t = c0 + (t_lo + rank + 2 * i) * p.tokens;
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_weigh_prompt_kernel(const _
       load(0);
       for (int i = 0; i < n; ++i) {
         const int it = taken + i, st = it % kStages;
-        if (it >= kStages && !__all_sync(0xffffffffu, gwait(&l_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err))) break;
+        if (it >= kStages && !__all_sync(0xffffffffu, quick_wait(&l_empty[st], ((it / kStages) - 1) & 1, &s_fail, a.err))) break;
         bool odd = false;
 #pragma unroll
         for (int k = 0; k < kCols / 32; ++k) {
