@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   const KvAttnCall& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
   if (tid == 0) {
-    for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], kWiden);
+    for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1 + kBlocks), mbar_init(&raw_empty[i], kWiden);
     for (int i = 0; i < kStages; ++i)
       mbar_init(&k_full[i], kWiden), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], kWiden), mbar_init(&v_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kTile), mbar_init(&o_done[i], 1);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       lead_commit(leader, drain);
       (void)mbar_wait(drain, 0);
     } else if (warp == kCopyWarp) {
-      // ================= pages to the ring: a lane for each block of a tile =================
+      // ================= pages to the ring =================
       Segment s = {};
       long long u = u0;
       int i = 0;
@@ -345,73 +345,71 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
           i = s.lo;
         }
       };
-      struct Block {
-        int at;                  // of the cache; -1: none
-        unsigned seen;           // its tokens
-        float ks, vs;
-      };
-      // The next tile's block of this lane.  The page is known a tile before it is used, and so are the scales.
-      int page = -1, sub = 0;
+      // The next four tiles, a lane for each of their blocks: its page, asked for four tiles before it is used, its place
+      // in the page, its tokens.
+      int tiles = 0, page = -1, sub = 0;
       unsigned seen = 0;
       auto look_up = [&]() {
-        seen = 0, page = -1;
-        if (!more || lane >= kBlocks) return;
-        const int pos = s.tile(i) * kTile + lane * kKvBlock, pi = pos >> a.c.page_log2;
-        if (pos >= s.len || (pos + kKvBlock <= s.start && pos >= a.sinks)) return;
-        seen = 0xffffu >> (kKvBlock - min(kKvBlock, s.len - pos));
-        sub = (s.h << (a.c.page_log2 - 4)) + ((pos & (a.c.page - 1)) >> 4);
-        page = pi < a.b.table_stride ? __ldg(a.b.table + s.b * a.b.table_stride + pi) : -1;
-      };
-      auto find = [&]() {
-        Block x = {-1, 0, 0.f, 0.f};
-        if (seen == 0) return x;
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
-          atomicOr(a.err, kDevErrIndex);
-          return x;
+        tiles = 0, seen = 0, page = -1;
+        for (; tiles < 32 / kBlocks && more; ++tiles) {
+          const int pos = s.tile(i) * kTile + lane % kBlocks * kKvBlock, pi = pos >> a.c.page_log2;
+          if (lane / kBlocks == tiles && pos < s.len && (pos + kKvBlock > s.start || pos < a.sinks)) {
+            seen = 0xffffu >> (kKvBlock - min(kKvBlock, s.len - pos));
+            sub = (s.h << (a.c.page_log2 - 4)) + ((pos & (a.c.page - 1)) >> 4);
+            page = pi < a.b.table_stride ? __ldg(a.b.table + s.b * a.b.table_stride + pi) : -1;
+          }
+          ++i;
+          settle();
         }
-        x.at = ((page * a.c.heads) << (a.c.page_log2 - 4)) + sub;
-        x.seen = seen;
-        x.ks = __ldg(a.c.ks + x.at), x.vs = __ldg(a.c.vs + x.at);
-        return x;
-      };
-      auto next = [&]() {
-        if (more) ++i, settle();
-        look_up();
       };
       if (more) settle();
       look_up();
-      bool now = more;
-      Block x = find();
-      next();
-      int copied = 0, stage = 0;                // halves of tiles so far
+      int it = 0, copied = 0, stage = 0;        // tiles and halves of tiles so far
       uint32_t phase = 1;
       bool ok = true;
-      for (int it = 0; now && ok; ++it) {
-        const bool then = more;
-        const Block y = find();                 // of the tile after this one
-        next();
-        const unsigned bytes = __popc(__ballot_sync(0xffffffffu, x.at >= 0)) * (kKvBlock * D);
-        for (int v = 0; v < 2; ++v) {
-          if (copied >= kRaw) ok = __all_sync(0xffffffffu, quick_wait(&raw_empty[stage], phase, &s_fail, a.err));
-          if (!ok) break;
-          if (v == 0 && lane < kBlocks) {
-            Rec& r = s_rec[it % kRecs];
-            r.ks[lane] = x.ks, r.vs[lane] = x.vs, r.seen[lane] = static_cast<uint16_t>(x.seen);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&raw_full[stage], bytes);
-          __syncwarp();
-          if (x.at >= 0)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             smem_u32(raw + stage * C::kRawBytes + lane * (kKvBlock * D))),
-                         "l"((v ? a.c.v : a.c.k) + static_cast<long long>(x.at) * (kKvBlock * D)), "n"(kKvBlock * D),
-                         "r"(smem_u32(&raw_full[stage]))
-                         : "memory");
-          ++copied;
-          if (++stage == kRaw) stage = 0, phase ^= 1;
+      while (tiles > 0 && ok) {
+        int at = -1;                            // this lane's block of the cache
+        if (seen != 0) {
+          if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages))
+            at = ((page * a.c.heads) << (a.c.page_log2 - 4)) + sub;
+          else
+            atomicOr(a.err, kDevErrIndex);
         }
-        x = y;
-        now = then;
+        const unsigned tokens = at >= 0 ? seen : 0u;
+        const int n = tiles;
+        look_up();
+        for (int g = 0; g < n && ok; ++g, ++it) {
+          const int blk = __shfl_sync(0xffffffffu, at, g * kBlocks + lane % kBlocks);
+          const unsigned have = __shfl_sync(0xffffffffu, tokens, g * kBlocks + lane % kBlocks);
+          const bool mine = lane < kBlocks, copies = mine && blk >= 0;
+          const unsigned bytes = __popc(__ballot_sync(0xffffffffu, copies)) * (kKvBlock * D);
+          for (int v = 0; v < 2; ++v) {
+            uint64_t* bar = &raw_full[stage];
+            if (copied >= kRaw) ok = __all_sync(0xffffffffu, quick_wait(&raw_empty[stage], phase, &s_fail, a.err));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            Rec& r = s_rec[it % kRecs];
+            if (v == 0 && mine) {
+              r.seen[lane] = static_cast<uint16_t>(have);
+              if (blk < 0) r.ks[lane] = r.vs[lane] = 0.f;
+            }
+            __syncwarp();
+            if (copies) {
+              if (v == 0) {                     // the scales come with the keys
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&r.ks[lane])), "l"(a.c.ks + blk) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&r.vs[lane])), "l"(a.c.vs + blk) : "memory");
+              }
+              asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                               smem_u32(raw + stage * C::kRawBytes + lane * (kKvBlock * D))),
+                           "l"((v ? a.c.v : a.c.k) + static_cast<long long>(blk) * (kKvBlock * D)), "n"(kKvBlock * D), "r"(smem_u32(bar))
+                           : "memory");
+            }
+            // an arrival of each of eight lanes, after its asynchronous copies
+            if (mine) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+            ++copied;
+            if (++stage == kRaw) stage = 0, phase ^= 1;
+          }
+        }
       }
       // after a failure nobody else waits for the copies in flight
       if (s_fail)
