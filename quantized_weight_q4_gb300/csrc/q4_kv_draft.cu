@@ -16,8 +16,8 @@
 // * In a CTA one warp looks blocks up and copies their codes into a ring (in
 //   registers of the warps that widen them they would not be far enough ahead);
 //   eight warps put them as exact fp16 into shared memory in the order of the
-//   MMA's operands; one warp issues the MMAs; four warps (a thread a row) turn
-//   scores into weights.  Two tiles of scores take turns in tensor memory, so
+//   MMA's operands; one warp issues the MMAs; eight warps (two threads a row,
+//   each half of a tile's tokens) turn scores into weights.  Two tiles of scores take turns in tensor memory, so
 //   that the next one's products run beside a tile's softmax.
 // * Scales are applied in fp32: a block's key scale is part of the factor of
 //   its scores, its value scale multiplies the weight before that is rounded
@@ -35,13 +35,13 @@ namespace {
 using namespace gemm;
 
 constexpr int kTile = 128;                // tokens and query rows of a tile
-constexpr int kThreads = 512;             // 4 softmax warps, 8 that widen codes, one each for MMAs and copies, two idle ones
-constexpr int kWidenWarp = 4, kWidenWarps = 8, kMmaWarp = 12, kCopyWarp = 13, kWiden = kWidenWarps * 32;
-// registers a thread: 512 x 128 at launch
-constexpr int kSoftmaxRegs = 216, kWidenRegs = 104, kOtherRegs = 56;
-static_assert(128 * (kSoftmaxRegs + 2 * kWidenRegs + kOtherRegs) <= kThreads * 128, "the shares must fit the launch's registers");
+constexpr int kThreads = 640;             // 8 softmax warps, 8 that widen codes, one each for MMAs and copies, two idle ones
+constexpr int kSoftmax = 2 * kTile, kWidenWarp = 8, kWidenWarps = 8, kMmaWarp = 16, kCopyWarp = 17, kWiden = kWidenWarps * 32;
+// registers a thread: 640 x 96 at launch
+constexpr int kSoftmaxRegs = 152, kWidenRegs = 56, kOtherRegs = 56;
+static_assert(128 * (2 * kSoftmaxRegs + 2 * kWidenRegs + kOtherRegs) <= kThreads * 96, "the shares must fit the launch's registers");
 constexpr int kStages = 2;                // of keys, and of values, as fp16
-constexpr int kRaw = 5;                   // of codes: keys and values of a tile in turn
+constexpr int kRaw = 4;                   // of codes: keys and values of a tile in turn
 constexpr int kRecs = 8;                  // records of tiles: copies are six tiles at most before the softmax
 constexpr int kBlocks = kTile / kKvBlock;
 constexpr int kSegCost = 3;               // what starting a (sequence, rows, head) costs, in tiles
@@ -95,8 +95,16 @@ __device__ __forceinline__ uint32_t columns_to(int n) { return n < 0 ? 0u : n >=
 __device__ __forceinline__ uint32_t tree_word(const KvAttnCall& a, long long row, int i) {
   return i >= 0 && i < a.tree_words ? static_cast<uint32_t>(__ldg(a.tree + row * a.tree_words + i)) : 0u;
 }
-// Barrier of the softmax warps.
-__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTile) : "memory"); }
+// Barriers of the softmax warps: of all, and of the two that share 32 rows (`pair`), with or without a vote.
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory"); }
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y) : "r"(static_cast<uint32_t>(x)), "r"(2 + pair) : "memory");
+  return y != 0;
+}
 
 // The tiles that the queries of a sequence see something of, at least one.
 __device__ __forceinline__ void seq_tiles(const KvAttnCall& a, int nq, int len, int& start, int& first, int& stay, int& n) {
@@ -131,7 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   long long* s_cum = reinterpret_cast<long long*>(raw + kRaw * C::kRawBytes + 256);   // [B + 1] first unit of each sequence
   __shared__ __align__(16) Rec s_rec[kRecs];
   __shared__ long long s_warp[kThreads / 32];
-  __shared__ int s_fail, s_last;
+  __shared__ float s_far[2][kTile];      // what the two threads of a row tell each other
+  __shared__ int s_scale[2][kTile];
+  __shared__ int s_fail, s_last, s_go;
 
   const KvAttnCall& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
@@ -139,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1 + kBlocks), mbar_init(&raw_empty[i], kWiden);
     for (int i = 0; i < kStages; ++i)
       mbar_init(&k_full[i], kWiden), mbar_init(&k_empty[i], 1), mbar_init(&v_full[i], kWiden), mbar_init(&v_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kTile), mbar_init(&o_done[i], 1);
-    mbar_init(q_ready, kTile), mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], kSoftmax), mbar_init(&o_done[i], 1);
+    mbar_init(q_ready, kSoftmax), mbar_init(drain, 1);
     s_fail = 0;
   }
   fence_barrier_init();
@@ -364,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       };
       if (more) settle();
       look_up();
+      const int run = min(a.c.page, kTile) / kKvBlock;   // blocks side by side
       int it = 0, copied = 0, stage = 0;        // tiles and halves of tiles so far
       uint32_t phase = 1;
       bool ok = true;
@@ -381,8 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         for (int g = 0; g < n && ok; ++g, ++it) {
           const int blk = __shfl_sync(0xffffffffu, at, g * kBlocks + lane % kBlocks);
           const unsigned have = __shfl_sync(0xffffffffu, tokens, g * kBlocks + lane % kBlocks);
-          const bool mine = lane < kBlocks, copies = mine && blk >= 0;
-          const unsigned bytes = __popc(__ballot_sync(0xffffffffu, copies)) * (kKvBlock * D);
+          const bool mine = lane < kBlocks;
+          // blocks of one page lie side by side: the first one's lane copies all of them if there is any
+          const unsigned any = __ballot_sync(0xffffffffu, mine && blk >= 0) >> (lane & ~(run - 1)) & ((1u << run) - 1u);
+          const int from = __ffs(any) - 1, first = __shfl_sync(0xffffffffu, blk, ((lane & ~(run - 1)) + max(from, 0)) & 31) - from;
+          const bool copies = mine && (lane & (run - 1)) == 0 && any != 0;
+          const unsigned bytes = __popc(__ballot_sync(0xffffffffu, copies)) * run * (kKvBlock * D);
           for (int v = 0; v < 2; ++v) {
             uint64_t* bar = &raw_full[stage];
             if (copied >= kRaw) ok = __all_sync(0xffffffffu, quick_wait(&raw_empty[stage], phase, &s_fail, a.err));
@@ -394,15 +409,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
               if (blk < 0) r.ks[lane] = r.vs[lane] = 0.f;
             }
             __syncwarp();
-            if (copies) {
-              if (v == 0) {                     // the scales come with the keys
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&r.ks[lane])), "l"(a.c.ks + blk) : "memory");
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&r.vs[lane])), "l"(a.c.vs + blk) : "memory");
-              }
+            if (copies)
               asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                smem_u32(raw + stage * C::kRawBytes + lane * (kKvBlock * D))),
-                           "l"((v ? a.c.v : a.c.k) + static_cast<long long>(blk) * (kKvBlock * D)), "n"(kKvBlock * D), "r"(smem_u32(bar))
+                           "l"((v ? a.c.v : a.c.k) + static_cast<long long>(first) * (kKvBlock * D)), "r"(run * (kKvBlock * D)),
+                           "r"(smem_u32(bar))
                            : "memory");
+            if (v == 0 && mine && blk >= 0) {   // the scales come with the keys
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&r.ks[lane])), "l"(a.c.ks + blk) : "memory");
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&r.vs[lane])), "l"(a.c.vs + blk) : "memory");
             }
             // an arrival of each of eight lanes, after its asynchronous copies
             if (mine) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -417,13 +432,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    // ================= softmax: a thread a row =================
-    const int r = tid;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // ================= softmax: two threads a row, half of a tile's tokens and of the sums each =================
+    constexpr int kCols = kTile / 2, kMine = kBlocks / 2;
+    const int half = warp >> 2, pair = warp & 3, r = pair * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(pair * 32) << 16;
+    const uint32_t t_mine = t_o + lanes + half * (D / 2);
     int it = 0;
-    bool ok = true;
     Segment s;
-    for (long long u = u0; ok && u < u1; u = s.to) {
+    // after a failed wait, of whichever warp, these go on without results: they meet in barriers
+    for (long long u = u0; u < u1; u = s.to) {
       locate(u, s);
       const int n = s.hi - s.lo, row = s.rows0 + r, j = row / p.group, head = s.h * p.group + row % p.group;
       const long long t = static_cast<long long>(s.c0) + j;
@@ -456,18 +473,22 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         const int e = m ? max(-126, min(126, 13 + 127 - static_cast<int>(m >> 23))) : 0;
         const float f = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), a.scale);
         rowc = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(a.scale) * kLog2e;
+        // 64 elements of it: of D = 128 half each, of D = 64 all by the first
+        if (D == 128 || half == 0) {
+          uint32_t packed[32];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          __half2 y[4];
+          for (int i = 0; i < 8; ++i) {
+            const uint4 mine = D == 128 && half ? w[(D / 8 - 8) + i] : w[i];
+            const uint32_t x[4] = {mine.x, mine.y, mine.z, mine.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[k] = __floats2half2_rn(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
-          w[i] = *reinterpret_cast<uint4*>(y);
+            for (int k = 0; k < 4; ++k) {
+              const __half2 y = __floats2half2_rn(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
+              packed[4 * i + k] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
+          tmem_st32(t_q + lanes + 32 * half, packed);
+          tmem_wait_st();
         }
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) tmem_st32(t_q + lanes + 32 * x, reinterpret_cast<const uint32_t*>(w) + 32 * x);
-        tmem_wait_st();
         tc_fence_before();
         mbar_arrive(q_ready);
       }
@@ -475,28 +496,28 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       const int to = !have ? 0x7fffffff : a.tree ? base - 1 : a.causal ? qpos : s.len - 1;
       const long long lowest = have && a.window > 0 ? static_cast<long long>(qpos) - a.window : -1LL;
       const int from = lowest < -1 ? -1 : static_cast<int>(lowest);
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f; // the same maximum for both threads; the sum of this one's tokens
       int e = kNoScale;             // the sums are relative to 2^e, above the value scales that the row has seen
       for (int i = 0; i < n; ++i, ++it) {
-        const int t0 = s.tile(s.lo + i) * kTile;
-        ok = __all_sync(0xffffffffu, quick_wait(&s_full[it & 1], (it >> 1) & 1, &s_fail, a.err));
-        if (!ok) break;
+        const int t0 = s.tile(s.lo + i) * kTile + half * kCols;
+        (void)quick_wait(&s_full[it & 1], (it >> 1) & 1, &s_fail, a.err);
+        __syncwarp();
         tc_fence_after();
         const Rec& rec = s_rec[it % kRecs];
-        const uint4 exist = *reinterpret_cast<const uint4*>(rec.seen);
-        uint32_t bits[4] = {exist.x, exist.y, exist.z, exist.w};
-        const bool mine = t0 + kTile - 1 > to || (t0 <= from && t0 + kTile > a.sinks) || (bits[0] & bits[1] & bits[2] & bits[3]) != ~0u;
+        const uint2 exist = *reinterpret_cast<const uint2*>(rec.seen + half * kMine);
+        uint32_t bits[2] = {exist.x, exist.y};
+        const bool mine = t0 + kCols - 1 > to || (t0 <= from && t0 + kCols > a.sinks) || (bits[0] & bits[1]) != ~0u;
         const bool edge = __any_sync(0xffffffffu, mine);
-        uint32_t v[kTile];
+        uint32_t v[kCols];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32_async(t_s[it & 1] + lanes + 32 * x, v + 32 * x);
-        float mul[kBlocks];         // a block's scores to powers of two
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) mul[k] = rec.ks[k] * rowc;
+        for (int x = 0; x < 2; ++x) tmem_ld32_async(t_s[it & 1] + lanes + half * kCols + 32 * x, v + 32 * x);
+        const float4 ks4 = *reinterpret_cast<const float4*>(rec.ks + half * kMine), vs4 = *reinterpret_cast<const float4*>(rec.vs + half * kMine);
+        const float vs[kMine] = {vs4.x, vs4.y, vs4.z, vs4.w};
+        float mul[kMine] = {ks4.x * rowc, ks4.y * rowc, ks4.z * rowc, ks4.w * rowc};   // a block's scores to powers of two
         tmem_wait_ld();
         if (edge) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 2; ++x) {
             const int at = t0 + 32 * x;
             uint32_t see = columns_to(to - at) & ~columns_to(from - at);
             if (at < a.sinks) see |= columns_to(to - at) & columns_to(static_cast<int>(min(a.sinks - at, 32LL)) - 1);
@@ -507,23 +528,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
             bits[x] &= see;
           }
 #pragma unroll
-          for (int c = 0; c < kTile; ++c)
+          for (int c = 0; c < kCols; ++c)
             if (!((bits[c >> 5] >> (c & 31)) & 1u)) v[c] = 0xff800000u;
 #pragma unroll
-          for (int k = 0; k < kBlocks; ++k) mul[k] = fmaxf(mul[k], 1e-30f);   // masked scores stay -inf
+          for (int k = 0; k < kMine; ++k) mul[k] = fmaxf(mul[k], 1e-30f);   // masked scores stay -inf
         }
         float now = -INFINITY;
         int te = kNoScale;          // of the blocks that the row sees something of
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
+        for (int k = 0; k < kMine; ++k) {
           float top = __uint_as_float(v[kKvBlock * k]);
 #pragma unroll
           for (int c = 1; c < kKvBlock; ++c) top = fmaxf(top, __uint_as_float(v[kKvBlock * k + c]));
           now = fmaxf(now, top * mul[k]);
-          const float scale = rec.vs[k];
-          if (top > -INFINITY && scale > 0.f) te = max(te, max(-126, min(126, static_cast<int>(__float_as_uint(scale) >> 23) - 126)));
+          if (top > -INFINITY && vs[k] > 0.f) te = max(te, max(-126, min(126, static_cast<int>(__float_as_uint(vs[k]) >> 23) - 126)));
         }
-        if (__any_sync(0xffffffffu, now > m + kLazy || te > e)) {   // also from -inf
+        // the vote: also, both have read their scores, whose place the weights take
+        if (pair_any(pair, now > m + kLazy || te > e)) {   // also from -inf
+          s_far[half][r] = now, s_scale[half][r] = te;
+          pair_sync(pair);
+          now = fmaxf(now, s_far[half ^ 1][r]), te = max(te, s_scale[half ^ 1][r]);
           const float next = fmaxf(m, now);
           const float k = next > -INFINITY ? ex2(m - next) : 1.f;
           m = next;
@@ -531,27 +555,27 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
           const float ko = k * power_of_two(e - max(e, te));
           e = max(e, te);
           if (i > 0) {
-            ok = __all_sync(0xffffffffu, quick_wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
-            if (!ok) break;
+            (void)quick_wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err);
+            __syncwarp();
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
+            for (int x = 0; x < D / 64; ++x) {
               uint32_t o[32];
-              tmem_ld32_async(t_o + lanes + 32 * x, o);
+              tmem_ld32_async(t_mine + 32 * x, o);
               tmem_wait_ld();
 #pragma unroll
               for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * ko);
-              tmem_st32(t_o + lanes + 32 * x, o);
+              tmem_st32(t_mine + 32 * x, o);
             }
           }
         }
         const f32x2 off2 = dup2(m > -INFINITY ? kUnit - m : 0.f);
         const float unit = power_of_two(-e);   // 2^e is above the scales: a weight stays below 2^15
         f32x2 sum2[2] = {0ull, 0ull};
-        uint32_t w[kTile / 2];
+        uint32_t w[kCols / 2];
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
-          const f32x2 f = dup2(mul[k]), vk = dup2(fminf(rec.vs[k] * unit, 1.f));   // larger: a block that the row does not see
+        for (int k = 0; k < kMine; ++k) {
+          const f32x2 f = dup2(mul[k]), vk = dup2(fminf(vs[k] * unit, 1.f));   // larger: a block that the row does not see
 #pragma unroll
           for (int c = k * kKvBlock / 2; c < (k + 1) * kKvBlock / 2; ++c) {
             float x, y;
@@ -563,8 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
             w[c] = *reinterpret_cast<const uint32_t*>(&z);
           }
         }
-        tmem_st32(t_s[it & 1] + lanes, w);
-        tmem_st32(t_s[it & 1] + lanes + 32, w + 32);
+        tmem_st32(t_s[it & 1] + lanes + half * (kCols / 2), w);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_ready[it & 1]);
@@ -572,21 +595,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
         unpack2(add2(sum2[0], sum2[1]), x, y);
         l += x + y;
       }
-      if (ok && n > 0) ok = __all_sync(0xffffffffu, quick_wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err));
-      if (!ok) break;
+      if (n > 0) (void)quick_wait(&o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &s_fail, a.err);
+      s_far[half][r] = l;
+      rows_sync();
+      if (tid == 0) s_go = !s_fail;
+      l = s_far[0][r] + s_far[1][r];
+      rows_sync();
+      if (!s_go) continue;        // the same for all of them
       tc_fence_after();
       const bool whole = s.from >= u0 && s.to <= u1;
       constexpr int kShare = kTile * (D / 4 + 1);
       if (whole) {
         const float k = l > 0.f ? power_of_two(e) / l : l == 0.f ? 0.f : l;   // a row that sees nothing: zeros; a NaN stays
-        if (a.lse && have) a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l) - kUnit) * kLn2 : l == 0.f ? -INFINITY : l;
+        if (a.lse && have && half == 0) a.lse[t * a.Hq + head] = l > 0.f ? (m + log2f(l) - kUnit) * kLn2 : l == 0.f ? -INFINITY : l;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
+        for (int x = 0; x < D / 64; ++x) {
           uint32_t o[32];
-          tmem_ld32_async(t_o + lanes + 32 * x, o);
+          tmem_ld32_async(t_mine + 32 * x, o);
           tmem_wait_ld();
           if (have) {
-            uint4* to4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (t * a.Hq + head) * D + 32 * x);
+            uint4* to4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (t * a.Hq + head) * D + half * (D / 2) + 32 * x);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               __nv_bfloat162 y[4];
@@ -602,21 +630,22 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       }
       // partial sums: slot 0 for what began in an earlier CTA, 1 for what begins here
       float4* slot = p.part + (range * 2 + (s.from >= u0 ? 1 : 0)) * kShare + r;
+      const int q0 = half * (D / 8);   // this thread's first four sums
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
+      for (int x = 0; x < D / 64; ++x) {
         uint32_t o[32];
         if (n > 0) {
-          tmem_ld32_async(t_o + lanes + 32 * x, o);
+          tmem_ld32_async(t_mine + 32 * x, o);
           tmem_wait_ld();
         }
         if (have) {
 #pragma unroll
           for (int c = 0; c < 32; c += 4)
-            reinterpret_cast<uint4*>(slot)[(8 * x + c / 4) * kTile] = n > 0 ? make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]) : make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(slot)[(q0 + 8 * x + c / 4) * kTile] = n > 0 ? make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]) : make_uint4(0, 0, 0, 0);
         }
       }
       tc_fence_before();
-      if (have) slot[D / 4 * kTile] = make_float4(m, l, __int_as_float(e), 0.f);
+      if (have && half == 0) slot[D / 4 * kTile] = make_float4(m, l, __int_as_float(e), 0.f);
       rows_sync();
       const long long o0 = owner_of(s.from + kSegCost), o1 = owner_of(s.to - 1);   // with the cuts before its tiles at its start
       if (tid == 0) {
@@ -642,9 +671,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
           ll += x.x > -INFINITY ? x.y * ex2(x.x - mm) : x.y;   // without a key: 0
         }
         const float k = ll > 0.f ? power_of_two(ee) / ll : ll == 0.f ? 0.f : ll;
-        if (a.lse) a.lse[t * a.Hq + head] = ll > 0.f ? (mm + log2f(ll) - kUnit) * kLn2 : ll == 0.f ? -INFINITY : ll;
+        if (a.lse && half == 0) a.lse[t * a.Hq + head] = ll > 0.f ? (mm + log2f(ll) - kUnit) * kLn2 : ll == 0.f ? -INFINITY : ll;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
           float4 y[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -655,12 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
             const float f = x.x > -INFINITY ? ex2(x.x - mm) * power_of_two(__float_as_int(x.z) - ee) : 0.f;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const float4 z = __ldcg(from_share + (c / 4 + q) * kTile);
+              const float4 z = __ldcg(from_share + (q0 + c / 4 + q) * kTile);
               y[q].x = fmaf(f, z.x, y[q].x), y[q].y = fmaf(f, z.y, y[q].y);
               y[q].z = fmaf(f, z.z, y[q].z), y[q].w = fmaf(f, z.w, y[q].w);
             }
           }
-          uint4* to4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (t * a.Hq + head) * D + c);
+          uint4* to4 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (t * a.Hq + head) * D + half * (D / 2) + c);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             __nv_bfloat162 z[4] = {__floats2bfloat162_rn(y[2 * q].x * k, y[2 * q].y * k), __floats2bfloat162_rn(y[2 * q].z * k, y[2 * q].w * k),
