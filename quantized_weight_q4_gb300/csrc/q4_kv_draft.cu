@@ -44,8 +44,8 @@ constexpr int kStages = 2;                // of keys, and of values, as fp16
 constexpr int kRaw = 4;                   // of codes: keys and values of a tile in turn
 constexpr int kRecs = 8;                  // records of tiles: copies are six tiles at most before the softmax
 constexpr int kBlocks = kTile / kKvBlock;
-constexpr int kSegCost = 3;               // what starting a (sequence, rows, head) costs, in tiles
-constexpr int kLeastTiles = 4;            // of a CTA, about: fewer make more shares than they save
+constexpr int kSegCost = 6;               // what starting a (sequence, rows, head) costs, in tiles (3 / 4 / 6 / 8: 92 / 85 / 85 / 86 us)
+constexpr int kLeastTiles = 6;            // of a CTA, about: a share to join costs as much as several
 constexpr float kLazy = 8.0f;             // the reference moves once a score exceeds it by 2^kLazy
 constexpr float kUnit = 7.0f;             // weights are 2^7 at the reference: up to 2^15, below fp16's 65504
 constexpr int kNoScale = -1024;           // exponent of blocks whose values are all zero
