@@ -15,8 +15,9 @@
 //   it loads; the products take the elements of queries in the same order.
 // * Codes are integers up to 127, exact in fp16, as are bf16 queries scaled by
 //   a power of two a row; fp32 queries are two fp16 terms (22 bits).
-// * Keys are read once, straight into registers, a block ahead; the queries of
-//   a (sequence, head) lie in shared memory in the order of the MMA's operand.
+// * Keys are read once, through a ring of asynchronous copies of each warp; the
+//   queries of a (sequence, head) lie in shared memory in the order of the
+//   MMA's operand.
 // * The blocks of all sequences and heads form one line, with some empty ones
 //   before each (sequence, head) for what starting it costs, cut evenly over
 //   the CTAs whatever the lengths.
@@ -34,7 +35,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtas = 2;                  // of an SM
+constexpr int kCtas = 3;                  // of an SM; with 2 / 3 blocks of a ring, 64 sequences of 50 to 8191 tokens: 71 / 77 us (two CTAs, 4: 72)
+constexpr int kStages = 2;                // blocks of a warp's ring
 constexpr int kTileRows = 8;              // query rows of an MMA's columns
 constexpr int kChunkTiles = 8;            // of them in shared memory at a time
 constexpr int kChunkRows = kTileRows * kChunkTiles;
@@ -103,7 +105,8 @@ __device__ __forceinline__ Seq sequence(const KvWeighCall& a, int group, int max
 
 template <int D, bool SPLIT>
 constexpr size_t smem_bytes(int B) {
-  return static_cast<size_t>(kChunkRows) * D * 2 * (SPLIT ? 2 : 1) + kChunkRows * (8 + 8) + static_cast<size_t>(B + 1) * 8;
+  return static_cast<size_t>(kChunkRows) * D * 2 * (SPLIT ? 2 : 1) + kChunkRows * (8 + 8) +
+         static_cast<size_t>(kWarps) * kStages * kKvBlock * D + static_cast<size_t>(B + 1) * 8;
 }
 
 // SPLIT: queries in two fp16 terms.
@@ -116,10 +119,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
   uint32_t* s_q = reinterpret_cast<uint32_t*>(smem_raw);                   // [tile][step][lane][kWords]
   float2* s_row = reinterpret_cast<float2*>(s_q + kChunkRows * D / 2 * (SPLIT ? 2 : 1));   // score of a unit product, -lse: base 2
   int2* s_see = reinterpret_cast<int2*>(s_row + kChunkRows);               // positions a row sees: (x, y]
-  long long* s_cum = reinterpret_cast<long long*>(s_see + kChunkRows);     // [B + 1] first unit of each sequence
+  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_see + kChunkRows);        // [warp][stage] a block's codes
+  long long* s_cum = reinterpret_cast<long long*>(s_ring + kWarps * kStages * kKvBlock * D);   // [B + 1] first unit of each sequence
   __shared__ long long s_warp[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
   const int g = lane >> 2, c = lane & 3;
+  // a lane copies every 32nd 16 bytes of a block; of D = 128 every other token's halves change places: no bank twice
+  constexpr uint32_t kBlockBytes = kKvBlock * D, kOdd = D == 128 ? 64 : 0;
+  const uint32_t ring = smem_u32(s_ring + warp * kStages * kBlockBytes);
+  const uint32_t put = (lane * 16) ^ (D == 128 && (lane >> 3 & 1) ? kOdd : 0);
+  const uint32_t take = (g * D + c * 16) ^ (g & 1 ? kOdd : 0);   // of token g; g + 8 is as odd
   pdl_launch_dependents();
   pdl_wait();
 
@@ -257,18 +266,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
             if (seen) my_scale = __ldg(a.c.ks + my_at);
           }
         }
-        // keys of the block that lane n looked up
-        auto load = [&](int n, uint4 (&k)[2][kParts]) {
-          const int at = __shfl_sync(0xffffffffu, my_at, n);
-          if (n >= count || at < 0 || !(__shfl_sync(0xffffffffu, my_kind, n) & 1u)) return;
-          const int8_t* from_k = a.c.k + static_cast<long long>(at) * (kKvBlock * D) + g * D + c * 16;
+        // keys of the block that lane n looked up; always closes a group, so that groups count blocks
+        auto copy = [&](int n, uint32_t to) {
+          const int at = __shfl_sync(0xffffffffu, my_at, n & 31);
+          const unsigned kind = __shfl_sync(0xffffffffu, my_kind, n & 31);
+          if (n < count && at >= 0 && (kind & 1u)) {
+            const int8_t* from_k = a.c.k + static_cast<long long>(at) * kBlockBytes + lane * 16;
 #pragma unroll
-          for (int x = 0; x < kParts; ++x) {
-            k[0][x] = __ldg(reinterpret_cast<const uint4*>(from_k + x * 64));
-            k[1][x] = __ldg(reinterpret_cast<const uint4*>(from_k + 8 * D + x * 64));
+            for (uint32_t x = 0; x < kBlockBytes / 512; ++x)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + put + x * 512), "l"(from_k + x * 512) : "memory");
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto work = [&](int n, const uint4 (&k)[2][kParts]) {
+        auto work = [&](int n, uint32_t block) {
           const int at = __shfl_sync(0xffffffffu, my_at, n);
           const unsigned kind = __shfl_sync(0xffffffffu, my_kind, n);
           if (at < 0) return;
@@ -281,6 +291,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
           float sum[2] = {0.f, 0.f};
           if (kind & 1u) {
             const float ks = __shfl_sync(0xffffffffu, my_scale, n);
+            uint4 k[2][kParts];
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) {
+              const uint32_t from_k = block + (take ^ (64 * x));
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(k[0][x].x), "=r"(k[0][x].y), "=r"(k[0][x].z), "=r"(k[0][x].w) : "r"(from_k));
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(k[1][x].x), "=r"(k[1][x].y), "=r"(k[1][x].z), "=r"(k[1][x].w) : "r"(from_k + 8 * D));
+            }
             for (int t8 = 0; t8 < tiles; ++t8) {
               float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
               const uint32_t* q = s_q + (t8 * KT * 32 + lane) * kWords;
@@ -324,17 +341,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
           }
           if (mine && (kind & 1u || pos >= s.held)) *w = had + sum[0];
         };
-        // two sets of registers take turns: a block is on its way while the other is in work
-        uint4 k[2][2][kParts];
+        uint32_t stage = ring;
+        auto next = [&](uint32_t at) { return at + kBlockBytes == ring + kStages * kBlockBytes ? ring : at + kBlockBytes; };
 #pragma unroll
-        for (int x = 0; x < 2 * 2 * kParts; ++x) (&k[0][0][0])[x] = make_uint4(0, 0, 0, 0);
-        load(0, k[0]);
-        for (int n = 0; n < count; n += 2) {
-          load(n + 1, k[1]);
-          work(n, k[0]);
-          load(n + 2, k[0]);
-          if (n + 1 < count) work(n + 1, k[1]);
+        for (int n = 0; n < kStages; ++n) copy(n, ring + n * kBlockBytes);
+        for (int n = 0; n < count; ++n) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+          __syncwarp();
+          work(n, stage);
+          __syncwarp();
+          copy(n + kStages, stage);
+          stage = next(stage);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
       }
     }
   }
