@@ -140,13 +140,13 @@ constexpr size_t smem_bytes(int B) {
 
 // Range of blocks [lo, hi) the queries of a sequence may see, at least one block where there are queries.  MORE: the
 // blocks of the sinks that lie before the window's (from `front` on) are counted right before these, from lo on.
-template <bool MORE>
+template <bool MORE, bool TREE>
 __device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len, int& lo, int& hi, int& front) {
   hi = max(1, (len + kKvBlock - 1) / kKvBlock);
   lo = 0;
   if (a.window > 0) {
     // a drafted token that sees no new one has the position before the first
-    const long long first = a.causal ? static_cast<long long>(len) - nq - a.window + (MORE && a.tree ? 0 : 1) : 0;
+    const long long first = a.causal ? static_cast<long long>(len) - nq - a.window + (TREE ? 0 : 1) : 0;
     lo = first > 0 ? min(static_cast<int>(first / kKvBlock), hi - 1) : 0;
   }
   front = lo;
@@ -276,9 +276,9 @@ __device__ __forceinline__ void join(const AttnParams& p, const Segment& s, int 
 }
 
 // SPLIT: the 16 rows of an MMA tile are 8 query rows in two fp16 terms each; else 16 in one term.
-// TEAM: warps that take a range of units together.  MORE: with sinks, drafted tokens' bits or sums of exponentials
-// (each may be absent); a form of its own, so that calls without them keep their code.
-template <int D, bool SPLIT, int TEAM, bool MORE>
+// TEAM: warps that take a range of units together.  MORE: with sinks or sums of exponentials (each may be absent), TREE:
+// with drafted tokens' bits too; forms of their own, so that calls without them keep their registers.
+template <int D, bool SPLIT, int TEAM, bool MORE, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = SPLIT ? 1 : 2;             // query rows of a thread
   // what starting and ending a (sequence, tile, head) costs, in units: more where all of a CTA's warps wait for it
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       if (b < B) {
         const int nq = a.b.cu[b + 1] - a.b.cu[b];
         int lo, hi, front;
-        seq_blocks<MORE>(a, nq, a.b.kv_len[b], lo, hi, front);
+        seq_blocks<MORE, TREE>(a, nq, a.b.kv_len[b], lo, hi, front);
         const long long rows = static_cast<long long>(nq) * p.group;
         const long long tiles = nq > 0 && rows <= p.max_rows ? (rows + kTileRows - 1) / kTileRows : 0;
         const long long n = tiles * a.c.heads * (hi - lo + kSegCost);
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     s.nq = a.b.cu[lo + 1] - s.c0;
     s.len = a.b.kv_len[lo];
     int b0, b1;
-    seq_blocks<MORE>(a, s.nq, s.len, b0, b1, s.front);
+    seq_blocks<MORE, TREE>(a, s.nq, s.len, b0, b1, s.front);
     s.shift = b0;
     const int nb = b1 - b0 + kSegCost;
     const long long in = u - s_cum[lo], pair = in / nb;
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
         const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
         const float rowf = __uint_as_float(static_cast<uint32_t>(127 - up) << 23) * a.scale * kLog2e;
         if (c == 0) {
-          if (MORE && a.tree) {                 // as many new tokens as its path has; they are seen by their bits alone
+          if (TREE) {                           // as many new tokens as its path has; they are seen by their bits alone
             int path = 0;
             if (have[e]) {
               const long long at = static_cast<long long>(s.c0) + (row0 + g + 8 * e) / p.group;
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
           const long long from = a.window > 0 && a.causal ? static_cast<long long>(qpos[e]) - a.window : -1LL;
           s_rowf[team][g + 8 * e] = rowf;
           s_see[team][g + 8 * e] = make_int2(from < -1 ? -1 : static_cast<int>(from),
-                                             !have[e] ? -1 : MORE && a.tree ? s.len - s.nq - 1 : a.causal ? qpos[e] : s.len - 1);
+                                             !have[e] ? -1 : TREE ? s.len - s.nq - 1 : a.causal ? qpos[e] : s.len - 1);
         }
 #pragma unroll
         for (int t = 0; t < KT; ++t)
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     int inner_lo, inner_hi;
     {
       int p0 = s.len - s.nq + row0 / p.group, p1 = s.len - s.nq + (row0 + rows - 1) / p.group;
-      if (MORE && a.tree) p0 = s.len - s.nq - 1, p1 = s.len - 1;   // the shortest and the longest path there may be
+      if (TREE) p0 = s.len - s.nq - 1, p1 = s.len - 1;   // the shortest and the longest path there may be
       inner_hi = max(0, a.causal ? p0 + 1 : s.len) / kKvBlock;
       inner_lo = a.window > 0 && p1 >= a.window ? static_cast<int>((p1 - a.window + kKvBlock) / kKvBlock) : 0;
     }
@@ -620,10 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             bool seen = pos + i > see.x && pos + i <= see.y;
-            if (MORE) {
-              seen |= pos + i < a.sinks && pos + i <= see.y;
+            if (MORE) seen |= pos + i < a.sinks && pos + i <= see.y;
+            if (TREE) {
               const int k = pos + i - (s.len - s.nq);   // place among the new tokens
-              if (a.tree && have[e] && k >= 0 && k < s.nq) {
+              if (have[e] && k >= 0 && k < s.nq) {
                 const long long at = static_cast<long long>(s.c0) + (row0 + g + 8 * e) / p.group;
                 seen = tree_word(a, at, k >> 5) >> (k & 31) & 1u;
               }
@@ -802,11 +802,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
       a.lse[i] = -INFINITY;
 }
 
-template <int D, bool SPLIT, int TEAM, bool MORE>
+template <int D, bool SPLIT, int TEAM, bool MORE, bool TREE>
 cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   const size_t smem = smem_bytes<D>(p.a.b.B);
   static std::atomic<unsigned long long> allowed;
-  cudaError_t e = allow_smem(q4_kv_attn_split_kernel<D, SPLIT, TEAM, MORE>, smem_bytes<D>(kKvMaxSeqs), allowed);
+  cudaError_t e = allow_smem(q4_kv_attn_split_kernel<D, SPLIT, TEAM, MORE, TREE>, smem_bytes<D>(kKvMaxSeqs), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -818,18 +818,18 @@ cudaError_t launch(const AttnParams& p, int grid, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q4_kv_attn_split_kernel<D, SPLIT, TEAM, MORE>, p);
+  return cudaLaunchKernelEx(&cfg, q4_kv_attn_split_kernel<D, SPLIT, TEAM, MORE, TREE>, p);
 }
 
-template <int D, bool SPLIT, bool MORE>
+template <int D, bool SPLIT, bool MORE, bool TREE>
 cudaError_t launch(const AttnParams& p, int rows, int grid, cudaStream_t st) {
   // Teams of four while there are more (sequence, tile, head)s than SMs: a team's start and end then fall into the
   // others' streams (quarters / whole CTAs: 64 sequences of 50 to 8191 tokens, 8 heads, 96 / 141 us; of 4096 tokens
   // 96 / 115 us).  With fewer, whole CTAs, which leave a quarter of the shares to join (one sequence of 131,071
   // tokens 62 / 54 us, 8 of 1024 17 / 16 us).
   const long long tiles = (rows + (SPLIT ? 7 : 15)) / (SPLIT ? 8 : 16);
-  return p.a.b.B * tiles * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams, MORE>(p, grid, st)
-                                              : launch<D, SPLIT, kWarps, MORE>(p, grid, st);
+  return p.a.b.B * tiles * p.a.c.heads > grid ? launch<D, SPLIT, kWarps / kTeams, MORE, TREE>(p, grid, st)
+                                              : launch<D, SPLIT, kWarps, MORE, TREE>(p, grid, st);
 }
 
 }  // namespace
@@ -852,12 +852,15 @@ cudaError_t launch_kv_attn_split(const KvAttnCall& a, int max_q, int max_rows, v
   // softmax instead of two (64 sequences of 50 to 8191 tokens 96 us, 106 us with rows in both halves)
   const int rows = static_cast<int>(std::min<long long>(static_cast<long long>(max_q) * p.group, max_rows));
   const bool split = !a.q_bf16 || !a.out_bf16 || rows <= 8;
-  const auto by_form = [&](auto more) {
-    constexpr bool kMore = decltype(more)::value;
-    if (a.c.dim == 128) return split ? launch<128, true, kMore>(p, rows, sms, st) : launch<128, false, kMore>(p, rows, sms, st);
-    return split ? launch<64, true, kMore>(p, rows, sms, st) : launch<64, false, kMore>(p, rows, sms, st);
+  const auto by_form = [&](auto more, auto tree) {
+    constexpr bool kMore = decltype(more)::value, kTree = decltype(tree)::value;
+    if (a.c.dim == 128)
+      return split ? launch<128, true, kMore, kTree>(p, rows, sms, st) : launch<128, false, kMore, kTree>(p, rows, sms, st);
+    return split ? launch<64, true, kMore, kTree>(p, rows, sms, st) : launch<64, false, kMore, kTree>(p, rows, sms, st);
   };
-  return kv_attn_more(a) ? by_form(std::true_type{}) : by_form(std::false_type{});
+  const std::true_type yes;
+  const std::false_type no;
+  return a.tree ? by_form(yes, yes) : kv_attn_more(a) ? by_form(yes, no) : by_form(no, no);
 }
 
 }  // namespace q4
