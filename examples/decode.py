@@ -95,8 +95,10 @@ class Decoder:
             x = x + self.project(torch.nn.functional.silu(g) * u, w["down"], self.hidden, workspace=mm_ws)
         return x
 
-    def choose(self, x, u, settings, out, workspace=None):
+    def choose(self, x, u, settings, out, workspace=None, penalties=None):
         logits = self.project(rms(x), self.head, self.vocab, dtype=torch.float32, workspace=workspace)
+        if penalties is not None:       # in place: a history on the device, and how much of it there is
+            q4.q4_adjust_logits(logits, logits, **penalties)
         q4.q4_sample(out, logits, u, **settings)
         return logits
 
@@ -111,23 +113,33 @@ class Decoder:
         logits = self.choose(x[(cu[1:] - 1).cuda().long()], u, settings, tokens)
         return tokens, logits
 
-    def capture_step(self, tokens, u, settings):
-        """A graph of one step for the whole batch: reads `tokens` and `u`, writes the next ones into `tokens`."""
+    def capture_step(self, tokens, u, settings, penalties=None):
+        """A graph of one step for the whole batch: reads `tokens` and `u`, writes the next ones into `tokens`.
+        penalties: arguments of q4_adjust_logits; the chosen tokens are put behind the history that they name."""
         self.step_cu = cu = torch.arange(self.seqs + 1, dtype=torch.int32, device="cuda")   # the graph reads it
 
         def step():
             self.kv_len += 1
             x = self.forward(tokens, cu, 1, self.mm_ws, self.attn_ws)
-            return self.choose(x, u, settings, tokens, self.mm_ws)
+            logits = self.choose(x, u, settings, tokens, self.mm_ws, penalties)
+            if penalties is not None:
+                length = penalties["history_len"]
+                penalties["history"].scatter_(1, length.long()[:, None], tokens[:, None])
+                length += 1
+            return logits
 
         stream = torch.cuda.Stream()
         keep = self.kv_len.clone(), tokens.clone()
+        if penalties is not None:
+            keep += penalties["history_len"].clone(),
         stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(stream):     # once outside the capture, on positions that are written again
             step()
         torch.cuda.current_stream().wait_stream(stream)
         self.kv_len.copy_(keep[0])
         tokens.copy_(keep[1])
+        if penalties is not None:
+            penalties["history_len"].copy_(keep[2])
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=stream):
             logits = step()
@@ -139,6 +151,7 @@ def main():
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--batch", type=int, default=4)
+    ap.add_argument("--repetition", type=float, default=1.0, help="penalty of tokens that a sequence has already")
     a = ap.parse_args()
     gen = torch.Generator("cuda").manual_seed(1)
     m = Decoder(layers=a.layers, seqs=a.batch)
@@ -149,7 +162,17 @@ def main():
                for i in range(a.batch)]
     u = torch.rand(a.batch, generator=gen, device="cuda")
     tokens, _ = m.prompts(prompts, u, settings)
-    graph, _ = m.capture_step(tokens, u, settings)
+    penalties = None
+    if a.repetition != 1:
+        history = torch.full((a.batch, m.max_tokens), -1, dtype=torch.int32, device="cuda")
+        lens = [p.numel() for p in prompts]
+        for row, p in zip(history, prompts):
+            row[:p.numel()] = p
+        prompt_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        history.scatter_(1, prompt_len.long()[:, None], tokens[:, None])
+        penalties = dict(history=history, history_len=prompt_len + 1, prompt_len=prompt_len,
+                         repetition=torch.full((a.batch,), a.repetition, device="cuda"))
+    graph, _ = m.capture_step(tokens, u, settings, penalties)
     out = [tokens.clone()]
     torch.cuda.synchronize()
     t = time.perf_counter()
