@@ -690,7 +690,8 @@ Q4_API int q4_kv_weigh(float *weight, const void *q, int q_dtype, int64_t q_stri
  * q4_kv_select -- which tokens of a sequence to keep, for each kv head.
  *   kept    int32 [B][heads][width] (out): positions, ascending; entries past
  *           count[b] are not written
- *   count   int32 [B] (out): min(kv_len[b], budget[b], width), at least 0
+ *   count   int32 [B] (out): min(kv_len[b], budget[b], width), at least 0 (a
+ *           kv_len past the page table records Q4_DEVERR_INDEX and counts as what it has)
  *   weight  as for q4_kv_weigh; max_kv: at least the largest kv_len
  * Kept are the first `sinks` tokens, the last `recent` ones (where these are
  * more than count allows: first the sinks, in order, then the newest), and of

@@ -54,6 +54,13 @@ __device__ __forceinline__ int warp_count_le(int n, int i, F f) {
   return lo;
 }
 
+// Tokens that the page table has room for, of a sequence said to have `len`: lengths on the device may be anything, and
+// work goes by what there is.
+__device__ __forceinline__ int kv_tokens(const KvView& c, long long table_stride, int len) {
+  const long long room = table_stride << c.page_log2;
+  return static_cast<int>(min(static_cast<long long>(max(len, 0)), room));
+}
+
 // Row of codes (token `pos`, head h) in units of rows of `dim`, or -1 where
 // the page table has no valid page for it.
 __device__ __forceinline__ long long kv_row(const KvView& c, const int32_t* table,

@@ -110,7 +110,7 @@ __device__ __forceinline__ bool pair_any(int pair, bool x) {
 __device__ __forceinline__ void seq_tiles(const KvAttnCall& a, int nq, int len, int& start, int& first, int& stay, int& n) {
   const long long f = a.window > 0 ? static_cast<long long>(len) - nq - a.window + (a.tree ? 0 : 1) : 0;
   start = f > 0 ? static_cast<int>(f) : 0;
-  const int hi = max(1, (max(len, 0) + kTile - 1) / kTile);
+  const int hi = max(1, static_cast<int>((kv_tokens(a.c, a.b.table_stride, len) + kTile - 1LL) / kTile));
   first = min(start / kTile, hi - 1);
   stay = static_cast<int>(min(static_cast<long long>(first), (a.sinks + kTile - 1) / kTile));
   n = stay + hi - first;
@@ -164,10 +164,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b < B) {
-        const int nq = a.b.cu[b + 1] - a.b.cu[b];
-        const long long rows = static_cast<long long>(nq) * p.group;
+        const int nq = a.b.cu[b + 1] - a.b.cu[b], len = a.b.kv_len[b];
+        const long long rows = static_cast<long long>(min(nq, a.b.T)) * p.group;
+        if (nq > 0 && kv_tokens(a.c, a.b.table_stride, len) < len) atomicOr(a.err, kDevErrIndex);
         int start, first, stay, n;
-        seq_tiles(a, nq, a.b.kv_len[b], start, first, stay, n);
+        seq_tiles(a, nq, len, start, first, stay, n);
         if (nq > 0 && rows <= p.max_rows) sum += (rows + kTile - 1) / kTile * a.c.heads * (n + kSegCost);
         s_cum[b + 1] = sum;
       }

@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) q4_kv_select_kernel(const __gr
   pdl_launch_dependents();
   pdl_wait();
   const int pair = blockIdx.x / cluster, b = pair / p.c.heads, h = pair - b * p.c.heads;
-  const int len = max(0, p.kv_len[b]);
+  const int len = kv_tokens(p.c, p.table_stride, p.kv_len[b]);
+  if (len < p.kv_len[b] && tid == 0) atomicOr(p.err, kDevErrIndex);
   const int count = static_cast<int>(min(static_cast<long long>(max(0, min(len, p.budget[b]))), p.width));
   const int head = static_cast<int>(min(static_cast<long long>(count), p.sinks));
   const int tail = static_cast<int>(min(static_cast<long long>(count - head), p.recent));

@@ -89,7 +89,7 @@ __device__ __forceinline__ Seq sequence(const KvWeighCall& a, int group, int max
   s.held = a.held ? max(0, min(a.held[b], s.len)) : max(0, s.len - s.nq);
   s.rows = static_cast<long long>(s.nq) * group;
   s.cost = max(1LL, min((s.rows + kTileRows - 1) / kTileRows, kMostCost));
-  const int hi = (s.len + kKvBlock - 1) / kKvBlock;
+  const int hi = (kv_tokens(a.c, a.b.table_stride, s.len) + kKvBlock - 1) / kKvBlock;
   int lo = s.nq > 0 ? 0 : hi;
   if (a.window > 0 && s.nq > 0) {
     const long long first = static_cast<long long>(s.len) - s.nq - a.window + 1;
@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
       const int b = tid * per + i;
       if (b < B) {
         const Seq s = sequence(a, group, max_rows, b);
+        if (kv_tokens(a.c, a.b.table_stride, s.len) < s.len) atomicOr(a.err, kDevErrIndex);
         const int n = s.blocks.count();
         sum += n > 0 ? static_cast<long long>(n + kSegCost) * s.cost * a.c.heads : 0;
         s_cum[b + 1] = sum;

@@ -70,7 +70,8 @@ __device__ __forceinline__ void widen4_bf16(uint32_t w, uint32_t& lo, uint32_t& 
 }
 
 __device__ __forceinline__ int pieces_of(const WeighPromptParams& p, int b) {
-  const int nq = max(0, p.a.b.cu[b + 1] - p.a.b.cu[b]), len = p.a.b.kv_len[b];
+  const int nq = max(0, p.a.b.cu[b + 1] - p.a.b.cu[b]), len = kv_tokens(p.a.c, p.a.b.table_stride, p.a.b.kv_len[b]);
+  if (len < p.a.b.kv_len[b]) atomicOr(p.a.err, kDevErrIndex);
   if ((p.split_rows > 0 && static_cast<long long>(nq) * p.group <= p.split_rows) || len <= 0) return 0;
   return static_cast<int>(min((len + kTokens - 1LL) / kTokens * p.a.c.heads, static_cast<long long>(kMostItems)));
 }

@@ -122,6 +122,29 @@ def test_select_pages_outside_the_cache():
         assert np.array_equal(kept[0, h, :60], select(v, 60, 2, 3))
 
 
+def test_lengths_past_the_table():
+    """Work goes by what the table has, whatever the lengths say."""
+    c = Cache([64], 2, 64, 16, 15)
+    w = weights(c, 15)
+    table = c.table[:, :4].copy()
+    kept, count = run_select(c, w, [1 << 30], 0, 3, table=table, lens=[2 ** 31 - 1], width=70, max_kv=64)
+    assert q4.q4_get_device_status() == q4.Q4_ERR_DEVICE and q4.q4_last_device_flags() == q4.Q4_DEVERR_INDEX
+    assert count.tolist() == [64] and np.array_equal(kept[0, :, :64], np.tile(np.arange(64), (2, 1)))
+    cache, _ = c.to_device()
+    q, lse = torch.zeros(40, 8, 64, dtype=torch.bfloat16, device=device()), torch.zeros(40, 8, device=device())
+    tree = torch.zeros(40, 2, dtype=torch.int32, device=device())
+    out = torch.empty_like(q)
+    for n in (1, 40):
+        q4.q4_kv_attention(out[:n], q[:n], cache, dev(table), i32([2 ** 31 - 1]), i32([0, n]), n, 64, tree=tree[:n].contiguous(),
+                           lse=lse[:n]) if n > 2 else None
+        weight = torch.ones(c.pages, 2, 16, device=device())
+        q4.q4_kv_weigh(weight, q[:n], torch.zeros_like(lse[:n]), cache, dev(table), i32([2 ** 31 - 1]), i32([0, n]), n, 64)
+        torch.cuda.synchronize()
+        assert q4.q4_get_device_status() == q4.Q4_ERR_DEVICE and q4.q4_last_device_flags() == q4.Q4_DEVERR_INDEX
+        got = weight.cpu().numpy()[c.table[0, :4]]
+        assert np.all(got == 1 + 4 * n)          # all queries see all that is there, four heads of them: exp(0) each
+
+
 # ------------------------------------------------------------------ moving
 def check_move(c, kept, first, seed, to=False, head_lists=True, ragged=0):
     """kept[b][h]: positions.  All of the cache is compared: what is not to change, too."""
