@@ -13,6 +13,14 @@
 // beside their neighbours they would hold up whole warps, one after another.
 // A CTA is bound by the latency of what it looks up; so all that can be is on
 // its way at once, and the first part of the history before its length is known.
+//
+// Measured: 200 rows of 128,007 bf16 logits, histories of 2,667 to 8,000 tokens,
+// 100 biases a row, grammars on half of the rows 48 us (2.2 TB/s of logits); the
+// same without any of these 17 us, with histories alone 41.  What is looked up
+// comes first and leaves HBM idle: notes are cleared and searched, and every
+// slice reads the whole history.  Slices of 8192 logits take 52 us, of 4096 61;
+// a cluster that shares the history by reductions in each other's shared memory
+// 65 to 81; a persistent form that holds the history in registers 79.
 #include <algorithm>
 
 #include "q4_kernels.h"

@@ -35,7 +35,8 @@
 // by the 16 warps that 128 registers a thread leave room for.  Short ones wait
 // for a chain of page lookup, copy, product and join.
 // Two blocks a step, under one softmax, need more registers than there are
-// (an earlier step: 136 us for 127).
+// (an earlier step: 136 us for 127).  With a window of 4096 and 4 first tokens,
+// 64 sequences of 900 to 16,001 tokens take 100 us, 4.8 TB/s.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>

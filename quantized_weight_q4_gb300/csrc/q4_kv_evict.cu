@@ -1,5 +1,12 @@
 // Leaving tokens out of the paged 8-bit cache (sm_103a): choosing those to keep
 // by their weight, and moving kept tokens together.
+//
+// Measured (8 kv heads of 128): 48 sequences of 1500 to 8191 tokens to 2048 each,
+// choice 24 us, moving 70 us (95,931 tokens, 394 MB read and written, 5.6 TB/s);
+// one of 100,003 tokens to 32,768, choice 37 us, moving 27 us (4.9 TB/s).  The
+// choice reads 4 bytes a token and head: it is bound by its passes over shared
+// memory and the barriers between them.  Moving is bound by HBM, with a chain of
+// list, page and scale before a run's first codes.
 #include <algorithm>
 #include <cfloat>
 
@@ -18,7 +25,8 @@ namespace {
 // 10 bits): each CTA counts its tokens by digit among those that agree in the
 // digits before, and every CTA adds the counts of all.  The list is then
 // written in the tokens' order: warps count what they keep in runs of their
-// own, and write it behind the counts of those before.
+// own, and write it behind the counts of those before.  A thread takes four
+// tokens side by side (one at a time: 35 us for the batch above).
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMostCluster = 8;        // one sequence of 100,003 tokens, 8 heads, four / eight / sixteen: 35 / 37 / 64 us
