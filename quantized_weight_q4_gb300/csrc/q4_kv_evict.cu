@@ -253,23 +253,20 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveTokens = 128;
 
 // Four codes times `ratio` (at most 1), each rounded: rint(code * ratio), one fp32 operation a step.  Codes become
-// floats, and floats codes, by an addition that leaves the whole number in the low bits.
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 y;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
-  return y;
-}
-__device__ __forceinline__ uint32_t scale4(uint32_t w, f32x2 ratio) {
+// floats, and floats codes, by an addition that leaves the whole number in the low bits.  The product and the addition
+// that rounds it are operations of one number each: those of two numbers are fused, which rounds once and moves a code
+// whose product lies within half a unit of the last place of a half (one of 400,000).
+__device__ __forceinline__ uint32_t scale4(uint32_t w, float ratio) {
   const uint32_t u = w ^ 0x80808080u;             // code + 128: the low byte of 2^23 + code + 128
-  const f32x2 less = dup2(-8388736.f), whole = dup2(12582912.f);   // -(2^23 + 128); 2^23 + 2^22: no fraction is left
+  const f32x2 less = dup2(-8388736.f);            // -(2^23 + 128)
   uint32_t y[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const f32x2 x = pack2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + 2 * i)),
-                          __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 + 2 * i)));
     float a, b;
-    unpack2(add2(mul2(add2(x, less), ratio), whole), a, b);
-    y[2 * i] = __float_as_uint(a), y[2 * i + 1] = __float_as_uint(b);
+    unpack2(add2(pack2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + 2 * i)),
+                       __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 + 2 * i))), less), a, b);
+    y[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(a, ratio), 12582912.f));   // 2^23 + 2^22: no fraction is left
+    y[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(b, ratio), 12582912.f));
   }
   return __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
 }
@@ -353,10 +350,8 @@ __global__ void __launch_bounds__(kMoveThreads) q4_kv_compact_kernel(const __gri
         const float ratio = s_ratio[x][t];
         if (dst == kNone || ratio < 0.f) continue;
         uint4 y = w[x][i];
-        if (ratio != 1.f) {
-          const f32x2 two = dup2(ratio);
-          y.x = scale4(y.x, two), y.y = scale4(y.y, two), y.z = scale4(y.z, two), y.w = scale4(y.w, two);
-        }
+        if (ratio != 1.f)
+          y.x = scale4(y.x, ratio), y.y = scale4(y.y, ratio), y.z = scale4(y.z, ratio), y.w = scale4(y.w, ratio);
         *reinterpret_cast<uint4*>((x ? p.c.v : p.c.k) + at) = y;
       }
     }

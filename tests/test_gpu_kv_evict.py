@@ -240,6 +240,19 @@ def test_move_nothing_changes():
     check_move(c, [[np.r_[0:200, 210:300]] * 2], [0], 9)
 
 
+@pytest.mark.parametrize("to", [False, True])
+def test_move_rounds_products_first(to):
+    """Millions of codes: some products lie so near a half that rounding them to fp32 first, or not, decides the code."""
+    n = 30_000
+    c = Cache.__new__(Cache)
+    g = rng(17, 1)
+    c.lens, c.heads, c.dim, c.page, c.pages = [n], 1, 128, 256, -(-n // 256)
+    c.table = g.permutation(c.pages).astype(np.int32)[None]
+    c.k, c.v = (g.integers(-127, 128, (c.pages, 1, 256, 128)).astype(np.int8) for _ in range(2))
+    c.ks, c.vs = ((0.02 + 0.03 * g.random((c.pages, 1, 16))).astype(f32) for _ in range(2))
+    check_move(c, random_kept(c, [0], [20_000], 17), [0], 17, to=to)
+
+
 def test_move_zero_scales():
     c = Cache([200], 2, 64, 64, 10)
     c.ks[c.table[0, 0]] = 0
