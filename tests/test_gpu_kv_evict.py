@@ -60,6 +60,22 @@ def test_select_batches(heads, page):
     check_select(c, weights(c, heads, ties=True), [300, 0, 2, 1000, 63, 600], 2, 8)
 
 
+@pytest.mark.parametrize("seqs,heads,n", [(1, 1, 9003), (2, 2, 2049), (3, 8, 5001), (10, 8, 2500), (5, 32, 8190), (1, 2, 16385)])
+def test_select_launch_shapes(seqs, heads, n):
+    """One CTA a (sequence, head), clusters with an SM for each CTA, and clusters that share SMs."""
+    c = Cache([n - 37 * b for b in range(seqs)], heads, 64, 64, seqs + heads)
+    check_select(c, weights(c, seqs), [n // 3 + b for b in range(seqs)], 5, 17)
+    check_select(c, weights(c, n, ties=True), [n // 7] * seqs, 1, 130)
+
+
+@pytest.mark.parametrize("many", [1.0, 0.5])
+def test_select_mostly_equal_weights(many):
+    """Many tokens at the cut, in every CTA of a cluster: the first of them stay."""
+    c = Cache([7003, 6000], 4, 64, 64, 5)
+    w = np.where(rng(17, 4).random((c.pages, c.heads, c.page)) < many, f32(0.25), weights(c, 3))
+    check_select(c, w, [3001, 4500], 3, 9)
+
+
 @pytest.mark.parametrize("sinks,recent", [(0, 0), (10, 0), (0, 10), (10, 20), (30, 30), (100, 5), (5, 100), (1000, 1000)])
 def test_select_first_and_last(sinks, recent):
     """Also where the budget is less than both together."""
