@@ -22,10 +22,14 @@
 //
 // Measured (32 query heads on 8 kv heads of 128): a prompt of 8192 tokens 228 us,
 // 1206 TFLOP/s of visible products.  The tensor pipe is busy in 54% of the
-// cycles, the exponentials' pipe in 55%.  Without copies and exponentials the
-// MMAs alone would take 180 us: reading both operands from shared memory takes
-// 96 of its 128 bytes a cycle, and the copies of queries 32.  Eight more warps
-// for the exponentials change nothing (241 us).
+// cycles, the exponentials' pipe in 55%, and neither alone is the bound: without
+// exponentials it takes 209 us, with an eighth of the MMAs 229, without copies of
+// queries 223, without all three 171.  A tile of 256 queries and 256 tokens takes
+// 1.7 us, 1.1 of either pipe; uneven pieces add 6%, starts and ends 20 us.
+// Tried, slower: keys as the operand in tensor memory (192 queries a tile) 233,
+// that with scores in two halves 256, with eight more warps 237; eight more warps
+// here 241; queries as the scores' rows, with the sums of 64 or 128 tokens in a
+// thread's registers, 280 and more, as they spill.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
