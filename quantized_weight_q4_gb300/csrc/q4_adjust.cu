@@ -15,12 +15,14 @@
 // its way at once, and the first part of the history before its length is known.
 //
 // Measured: 200 rows of 128,007 bf16 logits, histories of 2,667 to 8,000 tokens,
-// 100 biases a row, grammars on half of the rows 48 us (2.2 TB/s of logits); the
-// same without any of these 17 us, with histories alone 41.  What is looked up
-// comes first and leaves HBM idle: notes are cleared and searched, and every
-// slice reads the whole history.  Slices of 8192 logits take 52 us, of 4096 61;
-// a cluster that shares the history by reductions in each other's shared memory
-// 65 to 81; a persistent form that holds the history in registers 79.
+// 100 biases a row, grammars on half of the rows 45 us (2.3 TB/s of logits); the
+// same without any of these 17 us.  What is looked up comes first and leaves HBM
+// idle: of a CTA's 6.5 us, 1.8 pass until history and lengths are there and notes
+// are cleared, 1.6 noting, 1.3 searching for notes, 0.9 storing, 0.7 with the list.
+// Room in the list taken a quad of words at a time: 48 us; a warp at a time, by
+// ballots 53.  Then (48 us) slices of 8192 logits took 52, of 4096 61; a cluster
+// that shares the history by reductions in each other's shared memory 65 to 81; a
+// persistent form that holds the history in registers 79.
 #include <algorithm>
 
 #include "q4_kernels.h"
@@ -206,14 +208,22 @@ __global__ void __launch_bounds__(kThreads) q4_adjust_kernel(const __grid_consta
       if (rest < p.history_width) note(__ldg(history + rest), rest);   // three at most
     }
     __syncthreads();
-    for (int i = tid; i < slice / 4; i += kThreads) {
-      const uint4 x = reinterpret_cast<const uint4*>(s_note)[i];
-      if ((x.x | x.y | x.z | x.w) == 0) continue;
-      int to_list = atomicAdd(&s_listed, (x.x != 0) + (x.y != 0) + (x.z != 0) + (x.w != 0));
-      if (x.x) s_list[to_list++] = static_cast<uint16_t>(4 * i);
-      if (x.y) s_list[to_list++] = static_cast<uint16_t>(4 * i + 1);
-      if (x.z) s_list[to_list++] = static_cast<uint16_t>(4 * i + 2);
-      if (x.w) s_list[to_list] = static_cast<uint16_t>(4 * i + 3);
+    // a thread takes room in the list once, for all that it finds
+    constexpr int kFours = kMostSlice / 4 / kThreads;
+    static_assert(4 * kFours <= 32, "a bit each");
+    unsigned found = 0;
+#pragma unroll
+    for (int k = 0; k < kFours; ++k)
+      if (k * kThreads + tid < slice / 4) {
+        const uint4 x = reinterpret_cast<const uint4*>(s_note)[k * kThreads + tid];
+        found |= ((x.x ? 1u : 0u) | (x.y ? 2u : 0u) | (x.z ? 4u : 0u) | (x.w ? 8u : 0u)) << 4 * k;
+      }
+    if (found) {
+      int to_list = atomicAdd(&s_listed, __popc(found));
+      for (; found; found &= found - 1) {
+        const int bit = __ffs(found) - 1;
+        s_list[to_list++] = static_cast<uint16_t>(4 * ((bit >> 2) * kThreads + tid) + (bit & 3));
+      }
     }
   }
 #pragma unroll
