@@ -24,7 +24,7 @@
 //   to fp16, relative to a power of two above the scales that the row has seen.
 //
 // Measured (bf16, 32 query heads on 8 kv heads of 128): 16 drafts of 7 to 61
-// tokens on 492 to 6062 cached ones 84 us (both other forms, one after another:
+// tokens on 492 to 6062 cached ones 82 us (both other forms, one after another:
 // 237 us); 19 drafts of 32 tokens on 4000 67 us.  A tile takes 1.6 us, of which
 // the softmax's chain is 1.2 (scores from tensor memory, 64 exponentials a
 // thread, the pair's vote, weights back) and 0.8 what the codes' way takes of
@@ -53,7 +53,7 @@ constexpr int kStages = 2;                // of keys, and of values, as fp16
 constexpr int kRaw = 4;                   // of codes: keys and values of a tile in turn
 constexpr int kRecs = 8;                  // records of tiles: copies are six tiles at most before the softmax
 constexpr int kBlocks = kTile / kKvBlock;
-constexpr int kSegCost = 6;               // what starting a (sequence, rows, head) costs, in tiles (3 / 4 / 6 / 8: 92 / 85 / 85 / 86 us)
+constexpr int kSegCost = 6;               // what starting a (sequence, rows, head) costs, in tiles (3 / 4 / 6 / 8: 92 / 85 / 85 / 86 us when it was chosen)
 constexpr int kLeastTiles = 6;            // of a CTA, about: a share to join costs as much as several
 constexpr float kLazy = 8.0f;             // the reference moves once a score exceeds it by 2^kLazy
 constexpr float kUnit = 7.0f;             // weights are 2^7 at the reference: up to 2^15, below fp16's 65504
@@ -153,7 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
   __shared__ int s_fail, s_last, s_go;
 
   const KvAttnCall& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
+  // numbers that warps branch on come from one lane, so that they are known to be the same in all: exchanges and votes
+  // behind a branch that may part lanes take much longer (the batch above 84 us)
+  auto same = [](auto x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int tid = threadIdx.x, lane = tid & 31, warp = same(tid >> 5), B = a.b.B;
   if (tid == 0) {
     for (int i = 0; i < kRaw; ++i) mbar_init(&raw_full[i], 1 + kBlocks), mbar_init(&raw_empty[i], kWiden);
     for (int i = 0; i < kStages; ++i)
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     return into <= kSegCost ? u - into : u;
   };
   const long long range = blockIdx.x;
-  const long long u0 = range < ranges ? range_of(range) : units, u1 = range < ranges ? range_of(range + 1) : units;
+  const long long u0 = same(range < ranges ? range_of(range) : units), u1 = same(range < ranges ? range_of(range + 1) : units);
 
   auto locate = [&](long long u, Segment& s) {
     int lo = 0, hi = B - 1;                     // the last b with s_cum[b] <= u
@@ -452,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
     // after a failed wait, of whichever warp, these go on without results: they meet in barriers
     for (long long u = u0; u < u1; u = s.to) {
       locate(u, s);
-      const int n = s.hi - s.lo, row = s.rows0 + r, j = row / p.group, head = s.h * p.group + row % p.group;
+      s.to = same(s.to);
+      const int n = same(s.hi - s.lo), row = s.rows0 + r, j = row / p.group, head = s.h * p.group + row % p.group;
       const long long t = static_cast<long long>(s.c0) + j;
       const bool have = j < s.nq && s.c0 >= 0 && t < a.b.T;
       const int base = s.len - s.nq;

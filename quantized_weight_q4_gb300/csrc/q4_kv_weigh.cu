@@ -25,7 +25,7 @@
 // With few queries HBM bounds it at best: D + 4 bytes a token and head, against
 // 2 D flops and an exponential for each query.  Measured (bf16, 32 query heads on
 // 8 kv heads of 128): one or two queries of 64 sequences of 50 to 8192 tokens
-// 71 us, 4.3 TB/s; instructions are issued in 66% of the cycles, a third of them
+// 64 us, 4.8 TB/s; instructions are issued in 66% of the cycles, a third of them
 // widening codes.  One query over 390 tokens of 32 heads takes 10 us.
 #include <algorithm>
 #include <cfloat>
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtas = 3;                  // of an SM; with 2 / 3 blocks of a ring, 64 sequences of 50 to 8191 tokens: 71 / 77 us (two CTAs, 4: 72)
+constexpr int kCtas = 3;                  // of an SM; with 2 / 3 blocks of a ring, 64 sequences of 50 to 8191 tokens: 64 / 65 us (two CTAs, 4: 70; four, 2: 63)
 constexpr int kStages = 2;                // blocks of a warp's ring
 constexpr int kTileRows = 8;              // query rows of an MMA's columns
 constexpr int kChunkTiles = 8;            // of them in shared memory at a time
@@ -125,7 +125,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
   uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_see + kChunkRows);        // [warp][stage] a block's codes
   long long* s_cum = reinterpret_cast<long long*>(s_ring + kWarps * kStages * kKvBlock * D);   // [B + 1] first unit of each sequence
   __shared__ long long s_warp[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.b.B;
+  // the warp's number from one lane, so that what depends on it is known to be the same in all: exchanges of lanes behind
+  // a branch that may part them take much longer (the batch above 71 us)
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), B = a.b.B;
   const int g = lane >> 2, c = lane & 3;
   // a lane copies every 32nd 16 bytes of a block; of D = 128 every other token's halves change places: no bank twice
   constexpr uint32_t kBlockBytes = kKvBlock * D, kOdd = D == 128 ? 64 : 0;
