@@ -25,7 +25,7 @@
 // With few queries HBM bounds it at best: D + 4 bytes a token and head, against
 // 2 D flops and an exponential for each query.  Measured (bf16, 32 query heads on
 // 8 kv heads of 128): one or two queries of 64 sequences of 50 to 8192 tokens
-// 64 us, 4.8 TB/s; instructions are issued in 66% of the cycles, a third of them
+// 56 us, 5.4 TB/s; instructions are issued in 67% of the cycles, over a quarter of them
 // widening codes.  One query over 390 tokens of 32 heads takes 10 us.
 #include <algorithm>
 #include <cfloat>
@@ -38,12 +38,12 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtas = 3;                  // of an SM; with 2 / 3 blocks of a ring, 64 sequences of 50 to 8191 tokens: 64 / 65 us (two CTAs, 4: 70; four, 2: 63)
+constexpr int kCtas = 3;                  // of an SM; with 2 / 3 blocks of a ring, 64 sequences of 50 to 8191 tokens, with 2 kWarps below: 64 / 65 us (two CTAs, 4: 70; four, 2: 63)
 constexpr int kStages = 2;                // blocks of a warp's ring
 constexpr int kTileRows = 8;              // query rows of an MMA's columns
 constexpr int kChunkTiles = 8;            // of them in shared memory at a time
 constexpr int kChunkRows = kTileRows * kChunkTiles;
-constexpr int kSegCost = 2 * kWarps;      // what starting a (sequence, head) costs, in blocks of one tile of rows
+constexpr int kSegCost = 5 * kWarps;      // what starting a (sequence, head) costs, in blocks of one tile of rows (2 / 3 / 5 / 8 a warp: 64 / 62 / 56 / 57 us)
 constexpr long long kMostCost = 4096;     // of a block, so that no line, whatever the lengths, is too long for 64 bits
 constexpr int kSplitRows = 64;            // query rows of a head up to which a sequence of bf16 queries takes this form
 constexpr float kLog2e = 1.4426950408889634f;
