@@ -139,11 +139,12 @@ constexpr size_t smem_bytes(int B) {
          static_cast<size_t>(B + 1) * 8 + 64;
 }
 
-// Range of blocks [lo, hi) the queries of a sequence may see, at least one block where there are queries.  MORE: the
-// blocks of the sinks that lie before the window's (from `front` on) are counted right before these, from lo on.
+// Range of blocks [lo, hi) the queries of a sequence may see, at least one block where there are queries, of those that
+// the page table has.  MORE: the blocks of the sinks that lie before the window's (from `front` on) are counted right
+// before these, from lo on.
 template <bool MORE, bool TREE>
 __device__ __forceinline__ void seq_blocks(const KvAttnCall& a, int nq, int len, int& lo, int& hi, int& front) {
-  hi = max(1, (len + kKvBlock - 1) / kKvBlock);
+  hi = max(1, static_cast<int>((kv_tokens(a.c, a.b.table_stride, len) + kKvBlock - 1LL) / kKvBlock));
   lo = 0;
   if (a.window > 0) {
     // a drafted token that sees no new one has the position before the first
@@ -331,9 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_attn_split_kernel(const __g
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b < B) {
-        const int nq = a.b.cu[b + 1] - a.b.cu[b];
+        const int nq = a.b.cu[b + 1] - a.b.cu[b], len = a.b.kv_len[b];
         int lo, hi, front;
-        seq_blocks<MORE, TREE>(a, nq, a.b.kv_len[b], lo, hi, front);
+        seq_blocks<MORE, TREE>(a, nq, len, lo, hi, front);
+        if (nq > 0 && kv_tokens(a.c, a.b.table_stride, len) < len) atomicOr(a.err, kDevErrIndex);
         const long long rows = static_cast<long long>(nq) * p.group;
         const long long tiles = nq > 0 && rows <= p.max_rows ? (rows + kTileRows - 1) / kTileRows : 0;
         const long long n = tiles * a.c.heads * (hi - lo + kSegCost);
