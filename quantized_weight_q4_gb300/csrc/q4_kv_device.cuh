@@ -55,9 +55,9 @@ __device__ __forceinline__ int warp_count_le(int n, int i, F f) {
 }
 
 // Tokens that the page table has room for, of a sequence said to have `len`: lengths on the device may be anything, and
-// work goes by what there is.
+// work goes by what there is.  At most 2^30, the largest bound of a call: positions rounded up to tiles fit an int.
 __device__ __forceinline__ int kv_tokens(const KvView& c, long long table_stride, int len) {
-  const long long room = table_stride << c.page_log2;
+  const long long room = min(table_stride << c.page_log2, 1LL << 30);
   return static_cast<int>(min(static_cast<long long>(max(len, 0)), room));
 }
 

@@ -70,3 +70,27 @@ def test_attention_goes_by_what_the_table_has(kind, n, extra, D):
                 assert np.all(np.abs(got[i, h] - want) <= tol), (length, i, h)
                 if extra != "none":      # a logarithm below 8, to a few units of 2^-22
                     assert abs(sums[i, h] - np.log(f32(m))) <= 2.0 ** -20, (length, i, h)
+
+
+@pytest.mark.parametrize("kind,n", [("f32", 1), ("bf16", 2), ("bf16", 40)])
+def test_a_table_of_two_billion_tokens(kind, n):
+    """Positions next to 2^31: counted up to 2^30, the bound of every call, whatever the table has room for."""
+    td, page, D = torch.float32 if kind == "f32" else torch.bfloat16, 256, 64
+    c = Cache([page], 1, D, page, 16)
+    cache, _ = c.to_device()
+    table = torch.full((1, (1 << 31) // page), -1, dtype=torch.int32, device=device())
+    table[0, 0] = int(c.table[0, 0])
+    q, lse = torch.zeros(n, 4, D, dtype=td, device=device()), torch.zeros(n, 4, device=device())
+    weight = torch.ones(c.pages, 1, page, device=device())
+    assert q4.q4_get_device_status() == q4.Q4_OK
+    for length in (1 << 30, 2 ** 31 - 200, 2 ** 31 - 1):
+        args = cache, table, i32([length]), i32([0, n]), n, 1 << 30
+        weight.fill_(1)
+        q4.q4_kv_weigh(weight, q, torch.zeros_like(lse), *args)
+        assert q4.q4_get_device_status() == q4.Q4_ERR_DEVICE and q4.q4_last_device_flags() == q4.Q4_DEVERR_INDEX
+        got = weight.cpu().numpy()      # all that is there gets an exp(0) of every row; other slots stay
+        assert np.all(got[c.table[0, 0]] == 1 + 4 * n) and np.all(np.delete(got, c.table[0, 0], 0) == 1)
+        out = torch.empty_like(q)
+        q4.q4_kv_attention(out, q, *args, lse=lse)
+        assert q4.q4_get_device_status() == q4.Q4_ERR_DEVICE and q4.q4_last_device_flags() == q4.Q4_DEVERR_INDEX
+        assert np.all(np.abs(lse.cpu().numpy() - np.log(f32(page))) <= 2.0 ** -20)
