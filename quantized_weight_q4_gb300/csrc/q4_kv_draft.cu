@@ -414,12 +414,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
             uint64_t* bar = &raw_full[stage];
             if (copied >= kRaw) ok = __all_sync(0xffffffffu, quick_wait(&raw_empty[stage], phase, &s_fail, a.err));
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
             Rec& r = s_rec[it % kRecs];
             if (v == 0 && mine) {
               r.seen[lane] = static_cast<uint16_t>(have);
               if (blk < 0) r.ks[lane] = r.vs[lane] = 0.f;
             }
+            // lane 0's arrival comes behind the lanes' stores, and so publishes them: the other arrivals of this phase
+            // follow the lanes' asynchronous copies alone
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
             __syncwarp();
             if (copies)
               asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
