@@ -617,7 +617,8 @@ Q4_API int q4_kv_gather(void *k_out, void *v_out, int dtype, const q4_kv_cache *
  * scale is smaller than that by more loses bits of its share.
  *   workspace  q4_kv_attention_workspace_size bytes (for these bounds or
  *              larger ones), 16-byte aligned, the first 4 KB zero
- *              before its first use; every completed call leaves them zero.
+ *              before its first use; every completed call leaves them zero, one
+ *              that records Q4_DEVERR_TIMEOUT (its results are undefined) too.
  *              Calls that share it must not overlap.  NULL: scratch the
  *              library owns per stream (allocated by an eager call; one
  *              that needs more waits for the stream and replaces it; a call

@@ -618,9 +618,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       if (tid == 0) s_go = !s_fail;
       l = s_far[0][r] + s_far[1][r];
       rows_sync();
-      if (!s_go) continue;        // the same for all of them
-      tc_fence_after();
       const bool whole = s.from >= u0 && s.to <= u1;
+      // the ranges that share what is cut, with the cuts before its tiles at its start
+      const long long o0 = whole ? 0 : owner_of(s.from + kSegCost), o1 = whole ? 0 : owner_of(s.to - 1);
+      // by one thread: whether this CTA is the last of them, which leaves the counter at zero
+      auto take_ticket = [&]() {
+        const bool last = atom_add_acq_rel_gpu(p.tickets + o0, 1u) == static_cast<unsigned>(o1 - o0);
+        if (last) p.tickets[o0] = 0;
+        return last;
+      };
+      if (!s_go) {                // the same for all of them
+        if (!whole && tid == 0) take_ticket();   // without a share: the next call finds all counters at zero
+        continue;
+      }
+      tc_fence_after();
       constexpr int kShare = kTile * (D / 4 + 1);
       if (whole) {
         const float k = l > 0.f ? power_of_two(e) / l : l == 0.f ? 0.f : l;   // a row that sees nothing: zeros; a NaN stays
@@ -664,12 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       tc_fence_before();
       if (have && half == 0) slot[D / 4 * kTile] = make_float4(m, l, __int_as_float(e), 0.f);
       rows_sync();
-      const long long o0 = owner_of(s.from + kSegCost), o1 = owner_of(s.to - 1);   // with the cuts before its tiles at its start
-      if (tid == 0) {
-        const unsigned old = atom_add_acq_rel_gpu(p.tickets + o0, 1u);
-        s_last = old == static_cast<unsigned>(o1 - o0);
-        if (s_last) p.tickets[o0] = 0;
-      }
+      if (tid == 0) s_last = take_ticket();
       rows_sync();
       if (s_last && have) {
         const int shares = static_cast<int>(o1 - o0) + 1;
