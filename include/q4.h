@@ -513,8 +513,9 @@ Q4_API size_t q4_moe_block_workspace_size(int64_t T, int64_t topk, int64_t E, in
  *   page_table  int32 [B][table_stride]: the page that holds tokens
  *               i * page_tokens .. of a sequence.  A page outside [0, pages)
  *               records Q4_DEVERR_INDEX; its tokens are not written, and not
- *               seen.  Pages may be shared for reading; a page that is
- *               appended to belongs to one sequence.
+ *               seen.  Pages may be shared for reading; a page whose
+ *               tokens a call writes (appends, moves, weighs) belongs to one
+ *               sequence of that call.
  *   kv_len      int32 [B]: tokens each sequence has, new ones included
  *   cu_q        int32 [B + 1], cu_q[0] = 0: sequence b's new tokens are rows
  *               cu_q[b] .. cu_q[b + 1] - 1, at positions kv_len[b] - n .. kv_len[b] - 1.
@@ -680,6 +681,12 @@ Q4_API int q4_kv_attention_ex(void *out, int out_dtype, const void *q, int q_dty
  * the same call gives the same bits.  With fp32 queries scores are those of
  * fp32 arithmetic; bf16 queries and all codes are exact.  Slots of no token
  * keep what they hold.  A page outside the cache records Q4_DEVERR_INDEX.
+ * A slot has one weight, and a call gives it from one sequence: where two
+ * sequences of a call list one page, both writing its tokens (those that a query
+ * sees, and those from held[b] on), its weights are undefined, one
+ * sequence's or another's.  Sequences that share a prefix are weighed by
+ * calls of their own, one after another on a stream; with held at the
+ * prefix's end or behind it, its slots add up over them, in the calls' order.
  */
 Q4_API int q4_kv_weigh(float *weight, const void *q, int q_dtype, int64_t q_stride, int64_t Hq,
                        const float *lse, const q4_kv_cache *cache, const int32_t *page_table,
@@ -715,8 +722,10 @@ Q4_API int q4_kv_select(int32_t *kept, int64_t width, int32_t *count, const floa
  *   first   int32 [B] or NULL (0)
  *   weight  as for q4_kv_weigh, moved along, or NULL
  *   to_table, to_stride   the page table of the tokens' new places; NULL: they
- *           move within page_table.  Pages that to_table lists from token first
- *           on belong to one sequence and hold no token that the call reads.
+ *           move within page_table, whose pages from token first's block on
+ *           then belong to one sequence (a shared prefix before it stays as it
+ *           is).  Pages that to_table lists from token first on belong to one
+ *           sequence and hold no token that the call reads.
  * A block of 16 tokens takes the largest scale s of those that its tokens come
  * with (tokens before first, in a block that they share: their block's), and
  * codes become rint(code * (s0 / s)), each step one fp32 operation.  kv_len is

@@ -224,7 +224,9 @@ def q4_kv_weigh(weight, q, lse, cache: KVCache, page_table, kv_len, cu_q, max_q:
     """Adds to weight (fp32 [pages, heads, page_tokens], the cache's slots) the
     attention weight that each cached token gets from the queries q [T, Hq, dim],
     with lse [T, Hq] of q4_kv_attention over the same queries.  held: int32 [B],
-    tokens whose weight is kept; the others begin at 0 (default: the new ones)."""
+    tokens whose weight is kept; the others begin at 0 (default: the new ones).
+    Sequences that share pages are weighed by calls of their own: a slot's weight
+    comes from one sequence of a call (include/q4.h)."""
     T, Hq, dim = q.shape
     B = kv_len.shape[0]
     qp, qs = _rows(q, Hq, cache.dim)
@@ -267,8 +269,9 @@ def q4_kv_compact(cache: KVCache, page_table, kv_len, kept, count, weight=None, 
                   stream=None) -> None:
     """Moves the tokens kept (int32 [B, 1 or heads, width], ascending; count [B] of
     them) to places first[b] .. (default 0) of their sequences, with their weights,
-    within page_table or into the pages of to_table.  Each sequence then has
-    first + count tokens: kv_len is the caller's to set."""
+    within page_table or into the pages of to_table (pages that other sequences
+    read stay whole there).  Each sequence then has first + count tokens: kv_len is
+    the caller's to set."""
     B, heads, width = kept.shape
     if heads not in (1, cache.heads):
         raise ValueError(f"kept has {heads} heads, neither 1 nor {cache.heads}")
