@@ -123,8 +123,9 @@ class Decoder:
             x = self.forward(tokens, cu, 1, self.mm_ws, self.attn_ws)
             logits = self.choose(x, u, settings, tokens, self.mm_ws, penalties)
             if penalties is not None:
-                length = penalties["history_len"]
-                penalties["history"].scatter_(1, length.long()[:, None], tokens[:, None])
+                history, length = penalties["history"], penalties["history_len"]
+                # a full history keeps its last place for the newest token
+                history.scatter_(1, length.clamp(max=history.shape[1] - 1).long()[:, None], tokens[:, None])
                 length += 1
             return logits
 
@@ -153,19 +154,22 @@ def main():
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--repetition", type=float, default=1.0, help="penalty of tokens that a sequence has already")
     a = ap.parse_args()
+    lens, most = [37 + 61 * i for i in range(a.batch)], 1024
+    if a.batch < 1 or a.steps < 1 or lens[-1] + a.steps > most:
+        ap.error(f"{a.batch} prompts, the longest of {lens[-1] if lens else 0} tokens, and {a.steps} steps: the cache has "
+                 f"room for {most} tokens a sequence")
     gen = torch.Generator("cuda").manual_seed(1)
-    m = Decoder(layers=a.layers, seqs=a.batch)
+    m = Decoder(layers=a.layers, seqs=a.batch, max_tokens=most)
     settings = dict(temperature=torch.full((a.batch,), 0.8, device="cuda"),
                     top_k=torch.full((a.batch,), 50, dtype=torch.int32, device="cuda"),
                     top_p=torch.full((a.batch,), 0.95, device="cuda"))
-    prompts = [torch.randint(0, m.vocab, (37 + 61 * i,), generator=gen, device="cuda", dtype=torch.int32)
-               for i in range(a.batch)]
+    prompts = [torch.randint(0, m.vocab, (n,), generator=gen, device="cuda", dtype=torch.int32) for n in lens]
     u = torch.rand(a.batch, generator=gen, device="cuda")
     tokens, _ = m.prompts(prompts, u, settings)
     penalties = None
     if a.repetition != 1:
-        history = torch.full((a.batch, m.max_tokens), -1, dtype=torch.int32, device="cuda")
-        lens = [p.numel() for p in prompts]
+        # the cached tokens, and the newest one, which is not cached yet
+        history = torch.full((a.batch, m.max_tokens + 1), -1, dtype=torch.int32, device="cuda")
         for row, p in zip(history, prompts):
             row[:p.numel()] = p
         prompt_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
