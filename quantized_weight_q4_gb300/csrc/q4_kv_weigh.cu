@@ -26,7 +26,7 @@
 // 2 D flops and an exponential for each query.  Measured (bf16, 32 query heads on
 // 8 kv heads of 128): one or two queries of 64 sequences of 50 to 8192 tokens
 // 56 us, 5.4 TB/s; instructions are issued in 67% of the cycles, over a quarter of them
-// widening codes.  One query over 390 tokens of 32 heads takes 10 us.
+// widening codes.  One query over 390 tokens of 32 heads takes 8 us in a graph, over 3000 of 8 heads too.
 #include <algorithm>
 #include <cfloat>
 
@@ -44,6 +44,7 @@ constexpr int kTileRows = 8;              // query rows of an MMA's columns
 constexpr int kChunkTiles = 8;            // of them in shared memory at a time
 constexpr int kChunkRows = kTileRows * kChunkTiles;
 constexpr int kSegCost = 5 * kWarps;      // what starting a (sequence, head) costs, in blocks of one tile of rows (2 / 3 / 5 / 8 a warp: 64 / 62 / 56 / 57 us)
+constexpr int kLeastUnits = 3 * kWarps;   // of a CTA, with starts: kSegCost + kWarps gave short calls too few CTAs (one query on 3000 tokens, 8 heads, 10.3 us against 7.9; on 4 x 4000 12.9 against 10.2; 64 x 50 to 8191 the same)
 constexpr long long kMostCost = 4096;     // of a block, so that no line, whatever the lengths, is too long for 64 bits
 constexpr int kSplitRows = 64;            // query rows of a head up to which a sequence of bf16 queries takes this form
 constexpr float kLog2e = 1.4426950408889634f;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) q4_kv_weigh_kernel(const __gr
     __syncthreads();
   }
   const long long units = s_cum[B];
-  const long long ranges = max(1LL, min(static_cast<long long>(gridDim.x), units / (kSegCost + kWarps)));
+  const long long ranges = max(1LL, min(static_cast<long long>(gridDim.x), units / kLeastUnits));
   if (blockIdx.x >= ranges) return;
   auto range_of = [&](long long i) { return units / ranges * i + min(i, units % ranges); };
   const long long u0 = range_of(blockIdx.x), u1 = range_of(blockIdx.x + 1);
