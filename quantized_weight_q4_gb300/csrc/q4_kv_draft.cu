@@ -620,15 +620,16 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       rows_sync();
       const bool whole = s.from >= u0 && s.to <= u1;
       // the ranges that share what is cut, with the cuts before its tiles at its start
-      const long long o0 = whole ? 0 : owner_of(s.from + kSegCost), o1 = whole ? 0 : owner_of(s.to - 1);
+      auto first_owner = [&]() { return owner_of(s.from + kSegCost); };
+      auto last_owner = [&]() { return owner_of(s.to - 1); };
       // by one thread: whether this CTA is the last of them, which leaves the counter at zero
-      auto take_ticket = [&]() {
+      auto take_ticket = [&](long long o0, long long o1) {
         const bool last = atom_add_acq_rel_gpu(p.tickets + o0, 1u) == static_cast<unsigned>(o1 - o0);
         if (last) p.tickets[o0] = 0;
         return last;
       };
       if (!s_go) {                // the same for all of them
-        if (!whole && tid == 0) take_ticket();   // without a share: the next call finds all counters at zero
+        if (!whole && tid == 0) take_ticket(first_owner(), last_owner());   // without a share: the next call finds all counters at zero
         continue;
       }
       tc_fence_after();
@@ -675,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_kv_draft_kernel(const __grid_c
       tc_fence_before();
       if (have && half == 0) slot[D / 4 * kTile] = make_float4(m, l, __int_as_float(e), 0.f);
       rows_sync();
-      if (tid == 0) s_last = take_ticket();
+      const long long o0 = first_owner(), o1 = last_owner();
+      if (tid == 0) s_last = take_ticket(o0, o1);
       rows_sync();
       if (s_last && have) {
         const int shares = static_cast<int>(o1 - o0) + 1;
