@@ -728,7 +728,11 @@ Q4_API int q4_kv_select(int32_t *kept, int64_t width, int32_t *count, const floa
  *           sequence and hold no token that the call reads.
  * A block of 16 tokens takes the largest scale s of those that its tokens come
  * with (tokens before first, in a block that they share: their block's), and
- * codes become rint(code * (s0 / s)), each step one fp32 operation.  kv_len is
+ * codes become rint(code * (s0 / s)), each step one fp32 operation.  So scales
+ * only grow, and every call that moves a block rounds its codes once more: drop
+ * many tokens at a time, not one a step (512 Gaussian tokens of uneven size,
+ * a row is 1.1% off at first; after 256 have left, one at a time, 4.9%,
+ * 64 at a time 1.4%).  kv_len is
  * not written: afterwards a sequence has first + count tokens, and what the
  * cache holds behind them is undefined.  An entry of kept out of its bounds,
  * or a page outside the cache, records Q4_DEVERR_INDEX, and the token becomes

@@ -2,8 +2,9 @@
 // by their weight, and moving kept tokens together.
 //
 // Measured (8 kv heads of 128): 48 sequences of 1500 to 8191 tokens to 2048 each,
-// choice 19 us, moving 70 us (95,931 tokens, 394 MB read and written, 5.6 TB/s);
-// one of 100,003 tokens to 32,768, choice 20 us, moving 27 us (4.9 TB/s).  The
+// choice 19 us, moving into other pages 74 us (95,931 tokens, 394 MB read and
+// written, 5.3 TB/s), in place 97; one of 100,003 tokens to 32,768, choice 18 us,
+// moving 31 us (4.4 TB/s), in place 916: one CTA a (sequence, head) there.  The
 // choice reads 4 bytes a token and head: it is bound by its passes over shared
 // memory (three of 2.7 us) and what lies before and between them (length, page
 // and weight one after another 5 us, five meetings of the cluster 1 us each).  Moving is bound by HBM, with a chain of
@@ -270,7 +271,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1) q4_kv_select_
 // earlier one (never of a later one: kept[i] >= first + i), so there a CTA takes
 // all the places of a (sequence, head), in order, and writes some after all of
 // their sources are in registers; into other pages every run of places has a
-// CTA.
+// CTA.  So a long sequence is cut fastest into other pages; in place is for many
+// sequences, and for a few tokens each (accepted paths of 16 drafts: 3.4 us in a
+// graph).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTokens = 128;
 

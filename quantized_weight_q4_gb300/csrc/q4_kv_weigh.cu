@@ -27,6 +27,8 @@
 // 8 kv heads of 128): one or two queries of 64 sequences of 50 to 8192 tokens
 // 56 us, 5.4 TB/s; instructions are issued in 67% of the cycles, over a quarter of them
 // widening codes.  One query over 390 tokens of 32 heads takes 8 us in a graph, over 3000 of 8 heads too.
+// Many fp32 queries have no other form: keys are read, and their codes widened, again for every 64 rows, and two
+// products a pair: a prompt of 8192 takes 6.3 ms.
 #include <algorithm>
 #include <cfloat>
 
@@ -38,7 +40,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtas = 3;                  // of an SM; with 2 / 3 blocks of a ring, 64 sequences of 50 to 8191 tokens, with 2 kWarps below: 64 / 65 us (two CTAs, 4: 70; four, 2: 63)
+// CTAs of an SM (with rings of 4 blocks for two of them).  One query each over 64 sequences of 50 to 8191 tokens two / three
+// / four: 74 / 63 / 58 us; over 4 of 4000 9 / 10 / 12; 16 queries each over 16 of 1000 to 4000 35 / 34 / 37
+constexpr int kCtas = 3;
 constexpr int kStages = 2;                // blocks of a warp's ring
 constexpr int kTileRows = 8;              // query rows of an MMA's columns
 constexpr int kChunkTiles = 8;            // of them in shared memory at a time

@@ -20,8 +20,8 @@
 //   there and back, the largest (the first tokens, which most queries see)
 //   first, so that their sums of work are nearly alike.
 //
-// Measured (32 query heads on 8 kv heads of 128): a prompt of 8192 tokens 228 us,
-// 1206 TFLOP/s of visible products.  The tensor pipe is busy in 54% of the
+// Measured (32 query heads on 8 kv heads of 128): a prompt of 8192 tokens 231 us,
+// 1190 TFLOP/s of visible products.  The tensor pipe is busy in 54% of the
 // cycles, the exponentials' pipe in 55%, and neither alone is the bound: without
 // exponentials it takes 209 us, with an eighth of the MMAs 229, without copies of
 // queries 223, without all three 171.  A tile of 256 queries and 256 tokens takes

@@ -187,7 +187,19 @@ struct AttnPlan {
 };
 
 // Query rows up to which a sequence of a call with sinks, drafts or sums to give takes the draft form, where more than
-// kRowTile may come.
+// kRowTile may come.  Measured with sums to give, 8 kv heads of 4 query heads each (draft form / the form that a call
+// without them would take, us), rows 32, 64, 128, 256, 512, 1024:
+//   heads of 128    1 x 500     26/15   30/16   34/16   35/17   35/32   22/30
+//                   1 x 16000   38/29   39/41   44/63   47/101  63/273  102/223
+//                   16 x 500    29/30   33/32   37/45   46/49   72/72   132/119
+//                   16 x 4000   66/99   67/152  72/156  120/160 224/219 435/341
+//                   64 x 2000   131/187 133/349 139/305 268/334 509/448 1029/726
+//   heads of 64     1 x 500     20/10   22/10   24/10   25/10   24/18   17/19
+//                   16 x 500    23/18   25/17   27/30   32/30   50/44   92/76
+//                   16 x 4000   51/42   52/63   53/107  94/109  176/162 344/259
+//                   64 x 2000   99/72   100/129 103/205 195/223 375/318 771/538
+// So it is the right one from 64 to 256 rows on long sequences or many; alone on short ones, below 64 rows of heads of
+// 64, and from 512 rows of many sequences on, the others are faster by what stands there, and this bound does not know.
 constexpr int kMostDraftRows = 1024;
 
 // more: with sinks, a tree or sums to give.  sized: with room for every form that a call of these bounds, or of smaller
